@@ -86,14 +86,22 @@ enum {
                                  work was abandoned; report it as a bug)       */
 };
 
-enum { SSA_KV_BF16 = 0, SSA_KV_FP8_E4M3 = 1 };
+/* KV formats.  FP8_E4M3: e4m3 codes, one fp32 scale per token (over all KV
+ * heads) for K and one for V.  The PAGE_HEAD formats: e4m3 or int8 codes, one
+ * fp32 scale per page and KV head for K and one for V. */
+enum {
+  SSA_KV_BF16 = 0,
+  SSA_KV_FP8_E4M3 = 1,
+  SSA_KV_E4M3_PAGE_HEAD = 2,
+  SSA_KV_INT8_PAGE_HEAD = 3
+};
 
 /*
  * Shapes.  Validated by every call.
  *   page_size   P, tokens per page: 16, 32, 64 or 128
  *   n_q_heads   Hq;  n_kv_heads Hkv;  G = Hq / Hkv must be an integer, 1..8
  *   head_dim    D, must be 128
- *   kv_dtype    SSA_KV_BF16 or SSA_KV_FP8_E4M3
+ *   kv_dtype    one of SSA_KV_*
  *   n_layers    layers held by the cache arrays
  *   logical_pages  Lp, logical page ids per layer (0 .. Lp-1)
  *   pool_slots  S, physical GPU slots per layer
@@ -111,11 +119,13 @@ typedef struct ssa_layout {
 /*
  * The paged KV cache and its residency state (all per layer, layer-major).
  *
- *   k_pool   [Lyr][S][Hkv][P][D]   bf16 values, or e4m3 codes
- *   v_pool   bf16: [Lyr][S][Hkv][P][D];  fp8: [Lyr][S][Hkv][D][P] (each KV
+ *   k_pool   [Lyr][S][Hkv][P][D]   bf16 values, or 8-bit codes
+ *   v_pool   bf16: [Lyr][S][Hkv][P][D];  8-bit: [Lyr][S][Hkv][D][P] (each KV
  *            head's page stored d-major, tokens contiguous, so the attention
  *            kernel reads 8-bit V with tokens along the reduction)
- *   k_scale, v_scale   [Lyr][S][P] fp32 per-token scales (fp8 only; else NULL)
+ *   k_scale, v_scale   [Lyr][S][P] fp32 per-token scales (FP8_E4M3), or
+ *            [Lyr][S][Hkv] fp32 scales of each page and KV head (PAGE_HEAD
+ *            formats); NULL for bf16
  *   k_mirror, v_mirror, k_scale_mirror, v_scale_mirror: the same per-page
  *            blocks indexed by logical page, [Lyr][Lp][...], in pinned host
  *            memory; all four NULL means no host tier.  Mirror bytes equal
@@ -183,6 +193,19 @@ int ssa_lru_init(const ssa_layout *lay, const ssa_cache *c, int identity,
  * in token order, counts them, and re-quantises the touched pages:
  * mean = sum / count, s = max|mean| / 127, code = clamp(rint(mean/s), +-127)
  * (all zero when max|mean| = 0).  Out-of-range pages: SSA_ST_BAD_ID.
+ *
+ * PAGE_HEAD formats: per page, KV head and tensor, with amax the largest
+ * finite |x| of the call's tokens of that page and qmax = 448 (e4m3) or 127
+ * (int8):
+ *   need = amax / qmax;  s' = need on a page without tokens (slab_cnt 0),
+ *   else max(s, need);
+ *   when s' > s on a page with tokens, every code of the block becomes
+ *   Q(code * (s / s'));
+ *   the new codes are Q(x / s'), all zero when s' = 0,
+ * with Q rounding to nearest even (int8 clamped to +-127, NaN -> 0; e4m3
+ * saturating).  So a page's scale only grows, and pages filled over several
+ * calls can hold codes that were rounded more than once (at most half a code
+ * step each time the scale grew).  k and v must be 16-byte aligned.
  */
 int ssa_store_kv_mirror(const ssa_layout *lay, const ssa_cache *c, int layer0, int n_layers,
                         const void *k, const void *v, const int64_t *pos, int T,

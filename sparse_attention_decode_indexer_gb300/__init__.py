@@ -27,6 +27,10 @@ LIB_PATH = os.path.join(_HERE, "libssa_gb300.so")
 
 SSA_KV_BF16 = 0
 SSA_KV_FP8_E4M3 = 1
+SSA_KV_E4M3_PAGE_HEAD = 2
+SSA_KV_INT8_PAGE_HEAD = 3
+KV_FORMATS = {"bf16": SSA_KV_BF16, "fp8": SSA_KV_FP8_E4M3,
+              "e4m3_page_head": SSA_KV_E4M3_PAGE_HEAD, "int8_page_head": SSA_KV_INT8_PAGE_HEAD}
 
 ST_DROP, ST_BAD_ID, ST_MISS_NO_MIRROR, ST_UNRESOLVED, ST_BAD_POS, ST_TIMEOUT = 1, 2, 4, 8, 16, 32
 ST_INTERNAL = 64
@@ -152,6 +156,11 @@ def max_sel_pages(block_topk: int) -> int:
 
 @dataclass
 class Layout:
+    """Shapes of a cache and its calls.  ``kv_format`` names the KV format:
+    "bf16", "fp8" (e4m3, one scale per token), "e4m3_page_head" or
+    "int8_page_head" (8-bit codes, one K and one V scale per page and KV
+    head); None takes bf16 or fp8 by ``fp8``.  ``fp8`` ends up saying whether
+    the codes are 8 bits wide (V d-major in the pool, with scales)."""
     page_size: int
     n_q_heads: int
     n_kv_heads: int
@@ -163,6 +172,21 @@ class Layout:
     batch: int
     max_pages: int
     block_topk: int
+    kv_format: str | None = None
+
+    def __post_init__(self):
+        if self.kv_format is None:
+            self.kv_format = "fp8" if self.fp8 else "bf16"
+        if self.kv_format not in KV_FORMATS:
+            raise ValueError(f"kv_format {self.kv_format!r}: one of {sorted(KV_FORMATS)}")
+        self.fp8 = self.kv_format != "bf16"
+
+    @property
+    def scale_floats(self) -> int:
+        """fp32 K scales (and as many V scales) of one page."""
+        if self.kv_format.endswith("_page_head"):
+            return self.n_kv_heads
+        return self.page_size if self.fp8 else 0
 
     @property
     def max_sel(self) -> int:
@@ -170,7 +194,7 @@ class Layout:
 
     def c(self) -> SsaLayout:
         return SsaLayout(self.page_size, self.n_q_heads, self.n_kv_heads, self.head_dim,
-                         SSA_KV_FP8_E4M3 if self.fp8 else SSA_KV_BF16, self.n_layers,
+                         KV_FORMATS[self.kv_format], self.n_layers,
                          self.logical_pages, self.pool_slots, self.batch, self.max_pages,
                          self.block_topk, self.max_sel)
 
@@ -191,21 +215,22 @@ class KVCache:
         L, Lp, S = layout.n_layers, layout.logical_pages, layout.pool_slots
         H, P, D = layout.n_kv_heads, layout.page_size, layout.head_dim
         esz = 1 if layout.fp8 else 2
+        ns = layout.scale_floats
         pb = H * P * D * esz
         u8 = torch.uint8
         self.k_pool = torch.zeros((L, S, pb), dtype=u8, device=device)
         self.v_pool = torch.zeros((L, S, pb), dtype=u8, device=device)
         if layout.fp8:
-            self.k_scale = torch.zeros((L, S, P), dtype=torch.float32, device=device)
-            self.v_scale = torch.zeros((L, S, P), dtype=torch.float32, device=device)
+            self.k_scale = torch.zeros((L, S, ns), dtype=torch.float32, device=device)
+            self.v_scale = torch.zeros((L, S, ns), dtype=torch.float32, device=device)
         else:
             self.k_scale = self.v_scale = None
         if host_tier:
             self.k_mirror = torch.zeros((L, Lp, pb), dtype=u8, pin_memory=True)
             self.v_mirror = torch.zeros((L, Lp, pb), dtype=u8, pin_memory=True)
             if layout.fp8:
-                self.k_scale_mirror = torch.zeros((L, Lp, P), dtype=torch.float32, pin_memory=True)
-                self.v_scale_mirror = torch.zeros((L, Lp, P), dtype=torch.float32, pin_memory=True)
+                self.k_scale_mirror = torch.zeros((L, Lp, ns), dtype=torch.float32, pin_memory=True)
+                self.v_scale_mirror = torch.zeros((L, Lp, ns), dtype=torch.float32, pin_memory=True)
             else:
                 self.k_scale_mirror = self.v_scale_mirror = None
         else:

@@ -27,14 +27,16 @@ bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 int check_layout(const ssa_layout* lay, Dims& d) {
   if (!lay) return SSA_ERR_INVALID_ARG;
   d.P = lay->page_size; d.Hq = lay->n_q_heads; d.Hkv = lay->n_kv_heads; d.D = lay->head_dim;
-  d.fp8 = lay->kv_dtype == SSA_KV_FP8_E4M3;
+  d.kind = lay->kv_dtype;
+  d.fp8 = lay->kv_dtype != SSA_KV_BF16;
   d.Lyr = lay->n_layers; d.Lp = lay->logical_pages; d.S = lay->pool_slots;
   d.B = lay->batch; d.nmax = lay->max_pages; d.k = lay->block_topk; d.W = lay->max_sel;
   if (d.Lyr < 1 || d.Lp < 1 || d.S < 1 || d.B < 1 || d.nmax < 1 || d.k < 1 || d.Hq < 1 ||
       d.Hkv < 1)
     return SSA_ERR_INVALID_ARG;
   if (d.W != 2 * d.k + 8) return SSA_ERR_INVALID_ARG;
-  if (lay->kv_dtype != SSA_KV_BF16 && lay->kv_dtype != SSA_KV_FP8_E4M3) return SSA_ERR_UNSUPPORTED;
+  if (lay->kv_dtype < SSA_KV_BF16 || lay->kv_dtype > SSA_KV_INT8_PAGE_HEAD)
+    return SSA_ERR_UNSUPPORTED;
   if (d.D != 128) return SSA_ERR_UNSUPPORTED;
   if (!(d.P == 16 || d.P == 32 || d.P == 64 || d.P == 128)) return SSA_ERR_UNSUPPORTED;
   if (d.Hq % d.Hkv != 0) return SSA_ERR_UNSUPPORTED;
@@ -190,6 +192,8 @@ int ssa_store_kv_mirror(const ssa_layout* lay, const ssa_cache* c, int layer0, i
   if (T < 0 || (T > 0 && (!k || !v || !pos))) return SSA_ERR_INVALID_ARG;
   if (!c->slab_scale || !c->slab_sum || !c->slab_cnt) return SSA_ERR_INVALID_ARG;
   if (T > 2147483647 / 2) return SSA_ERR_INVALID_ARG;
+  // the page_head store reads its input in 16-byte units
+  if (d.page_head() && (((uintptr_t)k | (uintptr_t)v) & 15)) return SSA_ERR_INVALID_ARG;
   cudaError_t e = launch_store(d, *c, layer0, n_layers, k, v, pos, T, status,
                                (cudaStream_t)stream);
   return e == cudaSuccess ? SSA_OK : fail_cuda(e);

@@ -204,6 +204,18 @@ __device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t w, uint32_t& lo, uint
       : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
+// Four int8 codes (one 32-bit word) -> two f16x2: lo = bytes 0,1; hi = bytes
+// 2,3.  Exact: a byte biased by 128 under the exponent byte 0x64 is the f16
+// 1024 + 128 + code.
+__device__ __forceinline__ void s8x4_to_f16x2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const uint32_t bias = 0x64806480u;                   // 1152, 1152
+  lo = __byte_perm(u, 0x64646464u, 0x4140);
+  hi = __byte_perm(u, 0x64646464u, 0x4342);
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(bias));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(bias));
+}
+
 // Four e4m3 codes -> their four values as floats (exact).
 __device__ __forceinline__ void e4m3x4_to_f32x4(uint32_t w, float& x0, float& x1, float& x2,
                                                 float& x3) {

@@ -418,7 +418,7 @@ struct CopyParams {
   uint8_t *k_pool, *v_pool;
   float *k_scale, *v_scale;
   const int32_t *miss_page, *miss_slot, *n_miss;
-  int layer0, Lp, S, BW, P, fp8;
+  int layer0, Lp, S, BW, n_scale, page_head;
   int shared;             // one miss list (the first layer's) for every layer
   long long page_bytes;   // one page, all KV heads
 };
@@ -433,7 +433,9 @@ __global__ void __launch_bounds__(kCopyThreads) miss_copy_kernel(CopyParams p) {
   const int slot = p.miss_slot[(size_t)lst * p.BW + entry];
   if (pg < 0 || pg >= p.Lp || slot < 0 || slot >= p.S) return;
   const long long pb16 = p.page_bytes / 16;
-  const long long sc16 = p.fp8 ? (long long)p.P * 4 / 16 : 0;
+  // per-token scales: 16-byte units (P >= 16); page_head scales: n_scale = Hkv
+  // words, copied apart below
+  const long long sc16 = p.page_head ? 0 : (long long)p.n_scale * 4 / 16;
   const long long total = 2 * pb16 + 2 * sc16;
   const size_t mp = (size_t)layer * p.Lp + pg, ps = (size_t)layer * p.S + slot;
   // 16-byte unit idx of the concatenation [K page | V page | K scales | V scales]
@@ -447,14 +449,19 @@ __global__ void __launch_bounds__(kCopyThreads) miss_copy_kernel(CopyParams p) {
       dst = reinterpret_cast<uint4*>(p.v_pool + ps * p.page_bytes) + idx;
     } else if (idx < 2 * pb16 + sc16) {
       idx -= 2 * pb16;
-      src = reinterpret_cast<const uint4*>(p.ks_mir + mp * p.P) + idx;
-      dst = reinterpret_cast<uint4*>(p.k_scale + ps * p.P) + idx;
+      src = reinterpret_cast<const uint4*>(p.ks_mir + mp * p.n_scale) + idx;
+      dst = reinterpret_cast<uint4*>(p.k_scale + ps * p.n_scale) + idx;
     } else {
       idx -= 2 * pb16 + sc16;
-      src = reinterpret_cast<const uint4*>(p.vs_mir + mp * p.P) + idx;
-      dst = reinterpret_cast<uint4*>(p.v_scale + ps * p.P) + idx;
+      src = reinterpret_cast<const uint4*>(p.vs_mir + mp * p.n_scale) + idx;
+      dst = reinterpret_cast<uint4*>(p.v_scale + ps * p.n_scale) + idx;
     }
   };
+  if (p.page_head && blockIdx.x == 0 && threadIdx.x < 2 * p.n_scale) {
+    const int which = threadIdx.x >= p.n_scale, h = threadIdx.x - which * p.n_scale;
+    (which ? p.v_scale : p.k_scale)[ps * p.n_scale + h] =
+        (which ? p.vs_mir : p.ks_mir)[mp * p.n_scale + h];
+  }
   uint4 buf[kCopyUnroll];
   uint4* dst[kCopyUnroll];
 #pragma unroll
@@ -592,11 +599,14 @@ cudaError_t launch_miss_copy(const Dims& d, const ssa_cache& c, int layer0, int 
   p.k_pool = static_cast<uint8_t*>(c.k_pool); p.v_pool = static_cast<uint8_t*>(c.v_pool);
   p.k_scale = c.k_scale; p.v_scale = c.v_scale;
   p.miss_page = miss_page; p.miss_slot = miss_slot; p.n_miss = n_miss;
-  p.layer0 = layer0; p.Lp = d.Lp; p.S = d.S; p.P = d.P; p.fp8 = d.fp8;
+  p.layer0 = layer0; p.Lp = d.Lp; p.S = d.S;
+  p.n_scale = d.scale_floats();
+  p.page_head = d.page_head();
   p.shared = shared ? 1 : 0;
   p.BW = d.B * d.W * (shared ? n_layers : 1);   // list stride and entries per list
   p.page_bytes = (long long)d.page_bytes();
-  const long long total16 = 2 * p.page_bytes / 16 + (d.fp8 ? 2LL * d.P * 4 / 16 : 0);
+  const long long total16 =
+      2 * p.page_bytes / 16 + (p.page_head ? 0 : 2LL * p.n_scale * 4 / 16);
   dim3 grid((unsigned)((total16 + kCopyChunk - 1) / kCopyChunk), p.BW, n_layers);
   cudaError_t e = launch_pdl(miss_copy_kernel, grid, dim3(kCopyThreads), 0, s, p);
   count_launch();

@@ -12,11 +12,18 @@ namespace ssa {
 
 // Validated, derived view of an ssa_layout.
 struct Dims {
-  int P, Hq, Hkv, D, G, fp8, Lyr, Lp, S, B, nmax, k, W;
+  // kind: SSA_KV_*; fp8: the codes are 8 bits wide (every kind but bf16)
+  int P, Hq, Hkv, D, G, kind, fp8, Lyr, Lp, S, B, nmax, k, W;
   size_t esz() const { return fp8 ? 1 : 2; }
   // bytes of one KV head of one page (K or V), and of a whole page (all heads)
   size_t head_page_bytes() const { return (size_t)P * D * esz(); }
   size_t page_bytes() const { return (size_t)Hkv * head_page_bytes(); }
+  // one K and one V scale per page and KV head (else one per token, or none)
+  bool page_head() const {
+    return kind == SSA_KV_E4M3_PAGE_HEAD || kind == SSA_KV_INT8_PAGE_HEAD;
+  }
+  // fp32 K scales (and as many V scales) of one page
+  int scale_floats() const { return page_head() ? Hkv : (fp8 ? P : 0); }
   int max_selected() const { return k + 1 < nmax ? k + 1 : nmax; }
 };
 
@@ -29,6 +36,11 @@ cudaError_t launch_lru_init(const Dims& d, const ssa_cache& c, int identity, cud
 cudaError_t launch_store(const Dims& d, const ssa_cache& c, int layer0, int n_layers,
                          const void* k, const void* v, const int64_t* pos, int T,
                          int32_t* status, cudaStream_t s);
+
+// -- store_page_head.cu -----------------------------------------------------
+cudaError_t launch_store_page_head(const Dims& d, const ssa_cache& c, int layer0, int n_layers,
+                                   const void* k, const void* v, const int64_t* pos, int T,
+                                   int32_t* status, cudaStream_t s);
 
 // -- index.cu ---------------------------------------------------------------
 cudaError_t launch_index_scores(const Dims& d, const ssa_cache& c, int layer0, int n_layers,
@@ -102,6 +114,9 @@ struct DecodeArgs {
   const int32_t* bt;  // [B][nmax]
 };
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
+// -- decode_page_head.cu ----------------------------------------------------
+int decode_max_ctas_page_head(const Dims& d, int num_sms);
+cudaError_t launch_decode_page_head(const DecodeArgs& a, cudaStream_t s);
 
 // Properties of the current device, queried once per device ordinal and
 // cached (SM count; the most dynamic shared memory one CTA may opt in to).

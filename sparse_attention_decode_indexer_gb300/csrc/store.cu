@@ -296,6 +296,8 @@ cudaError_t launch_store(const Dims& d, const ssa_cache& c, int layer0, int n_la
                          const void* k, const void* v, const int64_t* pos, int T,
                          int32_t* status, cudaStream_t s) {
   if (T == 0) return cudaSuccess;
+  if (d.page_head())
+    return launch_store_page_head(d, c, layer0, n_layers, k, v, pos, T, status, s);
   StoreParams p{};
   p.k_pool = static_cast<uint8_t*>(c.k_pool);
   p.v_pool = static_cast<uint8_t*>(c.v_pool);

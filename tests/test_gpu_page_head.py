@@ -1,0 +1,294 @@
+"""The page_head KV formats (e4m3 or int8 codes, one fp32 scale per page and KV head): the write path
+bit for bit against the definition, the attention against 64 bits, and the whole step with a host
+tier in each of its forms (copy, deferred fetch, host tail, preload, shared residency)."""
+import numpy as np
+import pytest
+import torch
+
+from tests.page_head_ref import RefPages, attend, sm_scale
+
+pytestmark = pytest.mark.gpu
+FORMATS = ["int8_page_head", "e4m3_page_head"]
+D = 128
+
+
+def _layout(fmt, P=64, Hq=8, Hkv=2, L=2, Lp=12, S=None, B=2, nmax=6, k=2):
+    import sparse_attention_decode_indexer_gb300 as ssa
+    return ssa.Layout(P, Hq, Hkv, D, True, L, Lp, Lp if S is None else S, B, nmax, k, kv_format=fmt)
+
+
+def _bf16(rng, *shape, scale=1.0):
+    t = torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).bfloat16()
+    return t, t.float().numpy()
+
+
+def _cache(lay, host_tier=False, identity=True):
+    import sparse_attention_decode_indexer_gb300 as ssa
+    c = ssa.KVCache(lay, host_tier)
+    ssa.ssa_lru_init(c, identity)
+    return c, torch.zeros((1,), dtype=torch.int32, device="cuda")
+
+
+def _pages(c, l, where="pool"):
+    """(k, v, ks, vs) blocks of one layer: by slot for the pool, by page for the mirror."""
+    lay = c.layout
+    H, P = lay.n_kv_heads, lay.page_size
+    n = lambda t: t[l].cpu().numpy()  # noqa: E731
+    k = n(getattr(c, "k_" + where)).reshape(-1, H, P, D)
+    v = n(getattr(c, "v_" + where)).reshape(-1, H, D, P).transpose(0, 1, 3, 2)
+    tail = "" if where == "pool" else "_mirror"
+    return k, v, n(getattr(c, "k_scale" + tail)), n(getattr(c, "v_scale" + tail))
+
+
+def _same_pages(ref, got, ids, at):
+    for name, r, g in zip(("k", "v", "k_scale", "v_scale"), (ref.k, ref.v, ref.ks, ref.vs), got):
+        np.testing.assert_array_equal(r[ids], g[at], err_msg=name)
+
+
+def _same_slab(ref, c, l):
+    for name, r in (("slab_sum", ref.sums), ("slab_cnt", ref.cnt), ("slab_scale", ref.slab_scale),
+                    ("slab", ref.slab)):
+        np.testing.assert_array_equal(r, getattr(c, name)[l].cpu().numpy(), err_msg=name)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("P,Hkv", [(16, 1), (32, 8), (64, 2), (128, 4)])
+@pytest.mark.parametrize("host", [False, True])
+def test_store_in_pieces_equals_the_definition(fmt, P, Hkv, host):
+    """Prefill, ragged pieces and single tokens, growing magnitudes (so that scales grow and old codes
+    are rounded again), gaps inside a page, resident and not."""
+    import sparse_attention_decode_indexer_gb300 as ssa
+    L, Lp = 2, 7
+    lay = _layout(fmt, P=P, Hq=Hkv, Hkv=Hkv, L=L, Lp=Lp, B=1, nmax=Lp, k=1)
+    c, status = _cache(lay, host_tier=host, identity=not host)
+    if host:                                     # every other page holds a slot
+        for l in range(L):
+            c.slot_of[l, ::2] = torch.arange(0, (Lp + 1) // 2, dtype=torch.int32, device="cuda")
+            c.page_of[l, :(Lp + 1) // 2] = torch.arange(0, Lp, 2, dtype=torch.int32, device="cuda")
+    refs = [RefPages(fmt, Lp, Hkv, P) for _ in range(L)]
+    rng = np.random.default_rng([P, Hkv, host])
+    total = Lp * P
+    cuts = [0, 1, 2, P // 2 + 1, P, 3 * P, 3 * P + 5, 4 * P - 1, total - 3]
+    pieces = [np.arange(a, b) for a, b in zip(cuts, cuts[1:])]
+    pieces.append(np.array([total - 3, total - 1]))          # a gap
+    for i, pos in enumerate(pieces):
+        k, kf = _bf16(rng, L, len(pos), Hkv, D, scale=1.5 ** i)
+        v, vf = _bf16(rng, L, len(pos), Hkv, D, scale=0.6 ** i)
+        ssa.ssa_store_kv_mirror(c, 0, L, k.cuda(), v.cuda(), torch.from_numpy(pos).cuda(), status)
+        for l in range(L):
+            refs[l].store(kf[l], vf[l], pos)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    for l in range(L):
+        slots = c.slot_of[l].cpu().numpy()
+        ids = np.flatnonzero(slots >= 0)
+        _same_pages(refs[l], _pages(c, l), ids, slots[ids])
+        if host:
+            _same_pages(refs[l], _pages(c, l, "mirror"), np.arange(Lp), np.arange(Lp))
+        _same_slab(refs[l], c, l)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_store_long_call_and_odd_values(fmt):
+    """A call of over 4,096 tokens (page-sized chunks) that starts inside a page and skips pages; zero
+    pages, values of very different size, infinities and NaN (which leave the scale alone)."""
+    import sparse_attention_decode_indexer_gb300 as ssa
+    P, H, Lp = 64, 2, 90
+    lay = _layout(fmt, P=P, Hq=H, Hkv=H, L=1, Lp=Lp, B=1, nmax=Lp, k=1)
+    c, status = _cache(lay)
+    rng = np.random.default_rng(5)
+    pos = np.arange(17, Lp * P - 30)
+    pos = pos[(pos // P) % 9 != 4]
+    assert len(pos) >= 4096
+    k, _ = _bf16(rng, 1, len(pos), H, D)
+    v, _ = _bf16(rng, 1, len(pos), H, D)
+    k *= torch.from_numpy(2.0 ** rng.integers(-20, 20, (1, len(pos), 1, 1))).bfloat16()
+    k[0, :P] = 0
+    v[0, 100:400, 1] = 0
+    v[0, 1000, 0, 3] = float("inf")
+    v[0, 1001, 1, 4] = float("nan")
+    v[0, 1002, 1, 5] = -float("inf")
+    ssa.ssa_store_kv_mirror(c, 0, 1, k.cuda(), v.cuda(), torch.from_numpy(pos).cuda(), status)
+    ref = RefPages(fmt, Lp, H, P)
+    with np.errstate(invalid="ignore"):
+        ref.store(k.float().numpy()[0], v.float().numpy()[0], pos)
+    assert int(status.item()) == 0
+    kr, vr, ks, vs = _pages(c, 0)
+    if fmt == "e4m3_page_head":                  # NaN: either sign's code
+        vr, ref.v = np.where(vr == 0xFF, 0x7F, vr), np.where(ref.v == 0xFF, 0x7F, ref.v)
+    _same_pages(ref, (kr, vr, ks, vs), np.arange(Lp), np.arange(Lp))
+    _same_slab(ref, c, 0)
+
+
+def test_store_flags_bad_positions():
+    import sparse_attention_decode_indexer_gb300 as ssa
+    lay = _layout("int8_page_head", P=16, Hq=1, Hkv=1, L=1, Lp=3, B=1, nmax=3, k=1)
+    x = torch.ones((1, 2, 1, D), dtype=torch.bfloat16, device="cuda")
+    for pos, bits in (([48, 49], ssa.ST_BAD_ID), ([-1, 0], ssa.ST_BAD_ID), ([5, 5], ssa.ST_BAD_POS),
+                      ([5, 4], ssa.ST_BAD_POS)):
+        c, status = _cache(lay)
+        ssa.ssa_store_kv_mirror(c, 0, 1, x, x, torch.tensor(pos, device="cuda"), status)
+        assert int(status.item()) & bits, pos
+
+
+def _filled(fmt, lay, rng, host_tier=False, identity=True, lens=None, spread=3.0):
+    """A cache with every logical page stored, and the reference states."""
+    import sparse_attention_decode_indexer_gb300 as ssa
+    c, status = _cache(lay, host_tier, identity)
+    L, H, P, Lp = lay.n_layers, lay.n_kv_heads, lay.page_size, lay.logical_pages
+    refs = [RefPages(fmt, Lp, H, P) for _ in range(L)]
+    pos = np.arange(Lp * P)
+    for l in range(L):
+        mag = torch.from_numpy(2.0 ** rng.uniform(-spread, spread, (1, Lp, 1, H, 1))).bfloat16()
+        k, _ = _bf16(rng, 1, Lp * P, H, D)
+        v = (_bf16(rng, 1, Lp, P, H, D)[0] * mag).reshape(1, Lp * P, H, D)
+        ssa.ssa_store_kv_mirror(c, l, 1, k.cuda(), v.cuda(), torch.from_numpy(pos).cuda(), status)
+        refs[l].store(k.float().numpy()[0], v.float().numpy()[0], pos)
+    assert int(status.item()) == 0
+    return c, status, refs
+
+
+def _check_attention(lay, refs, q, sel, bt, lens, out, fmt):
+    P, H, G = lay.page_size, lay.n_kv_heads, lay.n_q_heads // lay.n_kv_heads
+    out = out.float().cpu().numpy()
+    qn = q.float().cpu().numpy()
+    for l in range(sel.shape[0]):
+        for b in range(sel.shape[1]):
+            s = sel[l, b]
+            s = s[s >= 0]
+            ids = bt[b, s]
+            live = (s[:, None] * P + np.arange(P)) < lens[b]
+            for h in range(H):
+                want, bound = attend(fmt, refs[l].k[ids, h], refs[l].v[ids, h], refs[l].ks[ids, h],
+                                     refs[l].vs[ids, h], qn[l, b, h * G:(h + 1) * G], sm_scale(), live)
+                got = out[l, b, h * G:(h + 1) * G]
+                assert np.all(np.abs(got - want) <= bound), (l, b, h, np.max(np.abs(got - want) / bound))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("P,Hq,Hkv,k,lens", [
+    (16, 8, 1, 3, (1, 95, 0)),                   # one token; a request without any
+    (32, 5, 1, 5, (192, 33, 32)),                # an odd group
+    (64, 16, 2, 2, (384, 65, 300)),
+    (128, 64, 8, 1, (257, 640, 129)),
+    (64, 4, 4, 47, (384, 384, 7)),               # every page selected
+])
+def test_attention_against_64_bits(fmt, P, Hq, Hkv, k, lens):
+    import sparse_attention_decode_indexer_gb300 as ssa
+    B, L = len(lens), 2
+    nmax = max(-(-n // P) for n in lens)
+    lay = _layout(fmt, P=P, Hq=Hq, Hkv=Hkv, L=L, Lp=B * nmax, B=B, nmax=nmax, k=k)
+    rng = np.random.default_rng([P, Hq, k])
+    c, status, refs = _filled(fmt, lay, rng)
+    bt = np.arange(B * nmax, dtype=np.int32).reshape(B, nmax)
+    W = lay.max_sel
+    sel = np.full((L, B, W), -1, np.int32)
+    for l in range(L):
+        for b in range(B):
+            n = -(-lens[b] // P)
+            pick = rng.permutation(max(n - 1, 0))[:k]
+            s = np.sort(np.append(pick, n - 1)) if n else np.empty(0, np.int64)
+            sel[l, b, :len(s)] = s
+    phys = np.where(sel >= 0, np.take_along_axis(np.broadcast_to(bt, (L, B, nmax)), np.maximum(sel, 0), -1), -1)
+    q, _ = _bf16(rng, L, B, Hq, D, scale=2.0)
+    q = q.cuda()
+    out = torch.full((L, B, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros((ssa.ssa_workspace_size(lay),), dtype=torch.uint8, device="cuda")
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x.astype(np.int32))).cuda()  # noqa: E731
+    args = (dev(sel), dev(phys), dev(np.asarray(lens)), sm_scale())
+    ssa.ssa_sparse_paged_decode(c, 0, L, q, *args, out, status, ws)
+    first = out.clone()
+    ssa.ssa_sparse_paged_decode(c, 0, L, q, *args, out, status, ws)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert torch.equal(first, out)               # the same bits twice
+    _check_attention(lay, refs, q, sel, bt, lens, out, fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_attention_unselected_bytes_do_not_matter(fmt):
+    """Codes behind a request's last token (NaN codes and large ones) leave the output as it is."""
+    import sparse_attention_decode_indexer_gb300 as ssa
+    lay = _layout(fmt, P=64, Hq=8, Hkv=1, L=1, Lp=2, B=1, nmax=2, k=1)
+    rng = np.random.default_rng(3)
+    c, status, refs = _filled(fmt, lay, rng)
+    lens = torch.tensor([64 + 21], dtype=torch.int32, device="cuda")
+    sel = torch.full((1, 1, lay.max_sel), -1, dtype=torch.int32, device="cuda")
+    sel[..., :2] = torch.tensor([0, 1])
+    q = _bf16(rng, 1, 1, 8, D)[0].cuda()
+    ws = torch.zeros((ssa.ssa_workspace_size(lay),), dtype=torch.uint8, device="cuda")
+    outs = []
+    for byte in (0x00, 0x7F, 0xFF, 0x80):
+        c.k_pool.view(1, 2, 64, D)[0, 1, 21:] = byte
+        c.v_pool.view(1, 2, D, 64)[0, 1, :, 21:] = byte
+        out = torch.empty((1, 1, 8, D), dtype=torch.bfloat16, device="cuda")
+        ssa.ssa_sparse_paged_decode(c, 0, 1, q, sel, sel, lens, sm_scale(), out, status, ws)
+        outs.append(out)
+    assert all(torch.equal(outs[0], o) for o in outs)
+    assert bool(outs[0].isfinite().all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("form", ["copy", "fetch", "overlap", "preload", "shared", "per_layer", "graphs"])
+def test_decode_steps_with_a_host_tier(fmt, form):
+    """Runner steps over an evicting pool: after each step every bound slot holds its page's mirror bytes
+    and scales, and the attention over the selection is that of 64 bits."""
+    import sparse_attention_decode_indexer_gb300 as ssa
+    from sparse_attention_decode_indexer_gb300.runner import DecodeRunner
+    P, Hq, Hkv, L, B, nmax, k = 32, 16, 4, 3, 2, 14, 3
+    lens = (14 * P, 9 * P + 5)
+    # 28 pages in use; 28 slots a layer (fewer than the 60 logical pages), or all of them shared
+    lay = _layout(fmt, P=P, Hq=Hq, Hkv=Hkv, L=L, Lp=B * nmax if form == "shared" else 60, S=28, B=B,
+                  nmax=nmax, k=k)
+    rng = np.random.default_rng(11)
+    bt = np.arange(B * nmax, dtype=np.int32).reshape(B, nmax)
+    run = DecodeRunner(lay, host_tier=True, identity=False, block_table=bt, seq_lens=np.asarray(lens),
+                       preload_width=5 if form == "preload" else 0, shared_residency=form == "shared",
+                       fetch_in_attention=form == "fetch", graphs=form == "graphs",
+                       overlap_groups=2 if form == "overlap" else 0)
+    c = run.cache
+    refs = [RefPages(fmt, lay.logical_pages, Hkv, P) for _ in range(L)]
+    pos = np.arange(B * nmax * P)
+    k_, _ = _bf16(rng, L, len(pos), Hkv, D)
+    v_, _ = _bf16(rng, L, len(pos), Hkv, D)
+    run.store(0, L, k_.cuda(), v_.cuda(), torch.from_numpy(pos).cuda())
+    for l in range(L):
+        refs[l].store(k_.float().numpy()[l], v_.float().numpy()[l], pos)
+    q = torch.empty((L, B, Hq, D), dtype=torch.bfloat16, device="cuda")
+    missed = 0
+    for step in range(6):
+        q.copy_(_bf16(rng, L, B, Hq, D)[0])
+        run.step(q, per_layer=form == "per_layer")
+        torch.cuda.synchronize()
+        assert int(run.status.item()) == 0
+        missed += int(run.n_miss[:1 if form == "shared" else L].sum())
+        sel = run.sel.cpu().numpy()
+        _check_attention(lay, refs, q, sel, bt, lens, run.out, fmt)
+        for l in range(L):
+            own = c.page_of[0 if form == "shared" else l].cpu().numpy()
+            slots = np.flatnonzero(own >= 0)
+            _same_pages(refs[l], _pages(c, l), own[slots], slots)
+    assert missed > 0
+    # zero-copy host tail over the same selection: same pages, same arithmetic
+    if form == "copy":
+        out = torch.empty_like(run.out)
+        ssa.ssa_sparse_paged_decode_host_tail(c, 0, L, q, run.sel, run.block_table, run.seq_lens,
+                                              sm_scale(), out, run.status, run.ws)
+        c.slot_of.fill_(-1)
+        out2 = torch.empty_like(run.out)
+        ssa.ssa_sparse_paged_decode_host_tail(c, 0, L, q, run.sel, run.block_table, run.seq_lens,
+                                              sm_scale(), out2, run.status, run.ws)
+        torch.cuda.synchronize()
+        assert int(run.status.item()) == 0
+        assert torch.equal(out, run.out) and torch.equal(out2, run.out)
+
+
+def test_layout_formats_and_refusals():
+    import sparse_attention_decode_indexer_gb300 as ssa
+    with pytest.raises(ValueError):
+        _layout("int4")
+    lay = _layout("int8_page_head")
+    c, status = _cache(lay)
+    x = torch.zeros((2 * 2 * 2 * D + 4,), dtype=torch.bfloat16, device="cuda")[1:1 + 2 * 2 * 2 * D]
+    with pytest.raises(ssa.SsaError):            # not 16-byte aligned
+        ssa.ssa_store_kv_mirror(c, 0, 2, x, x, torch.zeros((2,), dtype=torch.int64, device="cuda"), status)
