@@ -455,6 +455,62 @@ int ssa_sparse_paged_decode_host_tail(const ssa_layout *lay, const ssa_cache *c,
                                       ssa_stream_t stream);
 
 /*
+ * Rotary positions of queries and keys, before ssa_store_kv_mirror (keys) and
+ * ssa_index_topk / ssa_sparse_paged_decode (queries).  (The pages take q and
+ * k as given; every model that fills such a cache rotates them first.)  Pair
+ * i < rotary_dim / 2 of a head is (x[i], x[i + rotary_dim / 2]), or (x[2i],
+ * x[2i + 1]) with `interleaved`; dimensions from rotary_dim on are copied.
+ *   angle = (pos[t] + pos_offset) * theta_i,  (c, s) = factor (cos, sin)(angle)
+ *   a' = a c - b s,  b' = b c + a s     (inverse: s -> -s, which is also the
+ *                                        gradient of the rotation)
+ *   dtype     SSA_BF16, SSA_F16 or SSA_F32; computed in fp32, rounded once
+ *   freq      [rotary_dim / 2] device: theta_i / (2 pi) as a 64-bit fraction
+ *             of a turn (ssa_rope_frequencies), so that the angle is exact
+ *             modulo a turn at any position
+ *   pos       [n_tokens] device, int32 or (pos_is_64) int64; may be negative
+ *   q, k      at most one NULL: heads, and element strides of layer, token and
+ *             head (elements of a head are contiguous), so that a slice of a
+ *             fused projection needs no copy.  out == in (same strides) rotates
+ *             in place; otherwise the two must not overlap.
+ * 16-byte accesses where pointers, strides and dimensions allow, single
+ * elements otherwise; same values either way.
+ */
+enum { SSA_BF16 = 0, SSA_F16 = 1, SSA_F32 = 2 };
+#define SSA_ROPE_MAX_DIM 1024
+typedef struct ssa_rope_tensor {
+  const void *in;
+  void *out;
+  int heads;
+  int64_t in_stride[3], out_stride[3];   /* layer, token, head */
+} ssa_rope_tensor;
+int ssa_rope(int dtype, int head_dim, int rotary_dim, int interleaved, int inverse,
+             const uint64_t *freq, float factor, int n_layers, int n_tokens, const void *pos,
+             int pos_is_64, int64_t pos_offset, const ssa_rope_tensor *q,
+             const ssa_rope_tensor *k, ssa_stream_t stream);
+
+/*
+ * The frequency table of ssa_rope, on the host: theta_i = base^(-2i /
+ * rotary_dim), changed for contexts longer than the model was trained on:
+ *   PLAIN   as it is
+ *   LINEAR  theta / factor
+ *   NTK     base * factor^(rotary_dim / (rotary_dim - 2)) in place of base
+ *   BANDS   by the turns n = original_len * theta / (2 pi) a pair makes over
+ *           the original length: theta / factor for n <= low, theta for
+ *           n >= high, and linear in n between the two
+ *   YARN    theta / factor and theta blended along the pair index, from the
+ *           pair that makes `high` turns over original_len (theta) to the one
+ *           that makes `low` (theta / factor), both rounded outwards; the
+ *           attention factor is 0.1 ln(factor) + 1 (1 for the others)
+ *   freq         [rotary_dim / 2] out, host
+ *   attn_factor  out or NULL: the `factor` argument of ssa_rope
+ */
+enum { SSA_ROPE_PLAIN = 0, SSA_ROPE_LINEAR = 1, SSA_ROPE_NTK = 2, SSA_ROPE_BANDS = 3,
+       SSA_ROPE_YARN = 4 };
+int ssa_rope_frequencies(int rotary_dim, double base, int scaling, double factor,
+                         double original_len, double low, double high, uint64_t *freq,
+                         double *attn_factor);
+
+/*
  * ssa_index_topk without a workspace: the same indexer and top-k selection
  * (same arguments and results as ssa_index_topk, without scores_opt and ws),
  * for callers that cannot allocate device memory -- a plugin inside a host

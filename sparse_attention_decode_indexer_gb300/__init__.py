@@ -12,6 +12,7 @@ library is missing or no GPU is present the calls raise.
     ssa_remap_block_table    logical -> physical block table
     ssa_sparse_paged_decode  attention over the selected pages
     ssa_prefetch_pages       top-k preload of the next step's likely pages
+    ssa_rope                 rotary positions of queries and new keys
 """
 from __future__ import annotations
 
@@ -41,7 +42,8 @@ EXPORTS = ("ssa_workspace_size", "ssa_lru_init", "ssa_store_kv_mirror", "ssa_ind
            "ssa_index_topk_static_scratch", "ssa_selftest_bounded_wait", "ssa_host_read_probe",
            "ssa_prefetch_pages", "ssa_ensure_remap", "ssa_sparse_paged_decode_host_tail",
            "ssa_ensure_remap_shared", "ssa_ensure_remap_deferred",
-           "ssa_sparse_paged_decode_fetch", "ssa_ensure_remap_bind", "ssa_fetch_misses")
+           "ssa_sparse_paged_decode_fetch", "ssa_ensure_remap_bind", "ssa_fetch_misses",
+           "ssa_rope", "ssa_rope_frequencies")
 
 
 class SsaError(RuntimeError):
@@ -61,6 +63,11 @@ class SsaCache(ctypes.Structure):
         "k_pool", "v_pool", "k_scale", "v_scale", "k_mirror", "v_mirror", "k_scale_mirror",
         "v_scale_mirror", "slab", "slab_scale", "slab_sum", "slab_cnt", "slot_of", "page_of",
         "last_use", "clock")]
+
+
+class SsaRopeTensor(ctypes.Structure):
+    _fields_ = [("inp", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("in_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3)]
 
 
 _lib = None
@@ -120,6 +127,13 @@ def lib():
                                          + [vp] * 6)
         L.ssa_host_read_probe.restype = i32
         L.ssa_host_read_probe.argtypes = [vp, vp, vp, i32, i32, i32, vp]
+        f64 = ctypes.c_double
+        L.ssa_rope.restype = i32
+        L.ssa_rope.argtypes = [i32, i32, i32, i32, i32, vp, ctypes.c_float, i32, i32, vp, i32,
+                               ctypes.c_int64, P(SsaRopeTensor), P(SsaRopeTensor), vp]
+        L.ssa_rope_frequencies.restype = i32
+        L.ssa_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64,
+                                           P(ctypes.c_uint64), P(f64)]
         _lib = L
     return _lib
 
@@ -383,6 +397,116 @@ def ssa_sparse_paged_decode_host_tail(cache: KVCache, layer0: int, n_layers: int
         ctypes.byref(cache._lay), ctypes.byref(cache.c), layer0, n_layers, _ptr(q), _ptr(sel),
         _ptr(block_table), _ptr(seq_lens), float(sm_scale), _ptr(out), _ptr(status), _ptr(ws),
         _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------
+
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+_ROPE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+@dataclass
+class RopeScaling:
+    """How the frequencies change for contexts longer than ``original_len``:
+    "linear" and "ntk" take ``factor``; "bands" and "yarn" also
+    ``original_len`` and the turns over it, ``low`` and ``high``, between
+    which pairs go from stretched to kept (include/ssa.h has the formulas)."""
+    kind: str
+    factor: float = 1.0
+    original_len: float = 0.0
+    low: float = 1.0
+    high: float = 32.0
+
+
+class RopePlan:
+    """Frequencies of ssa_rope on the device.
+
+    head_dim, rotary_dim (default: the whole head), interleaved: the layout of
+    a head's pairs.  base and scaling give the frequencies, or ``theta``
+    (radians per position of each pair) gives them outright.  factor: the
+    factor on cos and sin (default: the scaling's)."""
+
+    def __init__(self, head_dim: int, rotary_dim: int | None = None, base: float = 10000.0,
+                 interleaved: bool = False, scaling: RopeScaling | None = None, theta=None,
+                 factor: float | None = None, device="cuda"):
+        rd = head_dim if rotary_dim is None else rotary_dim
+        if rd < 2 or rd % 2 or rd > head_dim:
+            raise ValueError(f"rotary_dim {rd}: an even number from 2 to head_dim {head_dim}")
+        self.head_dim, self.rotary_dim, self.interleaved = head_dim, rd, bool(interleaved)
+        own = ctypes.c_double(1.0)
+        if theta is not None:
+            theta = [float(x) for x in theta]
+            if len(theta) != rd // 2 or not all(math.isfinite(x) for x in theta):
+                raise ValueError(f"theta: {rd // 2} finite numbers")
+            freq = [round(math.ldexp(math.fmod(x / (2 * math.pi), 1.0), 64)) % (1 << 64)
+                    for x in theta]
+        else:
+            sc = scaling or RopeScaling("plain")
+            if sc.kind not in ROPE_SCALINGS:
+                raise ValueError(f"scaling {sc.kind!r}: one of {sorted(ROPE_SCALINGS)}")
+            buf = (ctypes.c_uint64 * (rd // 2))()
+            _check(lib().ssa_rope_frequencies(rd, float(base), ROPE_SCALINGS[sc.kind],
+                                              float(sc.factor), float(sc.original_len),
+                                              float(sc.low), float(sc.high), buf,
+                                              ctypes.byref(own)))
+            freq = list(buf)
+        self.factor = float(own.value if factor is None else factor)
+        # two's complement: the same 64 bits
+        self.freq = torch.tensor([f - (1 << 64) if f >= 1 << 63 else f for f in freq],
+                                 dtype=torch.int64, device=device)
+
+
+def _rope_tensor(plan, name, x, out, T):
+    """The C view of one tensor: [n_layers][T][H][D] or [T][H][D], any strides
+    but the last."""
+    if out is None:
+        out = x
+    if x.dim() not in (3, 4) or x.shape[-3] != T or x.shape[-1] != plan.head_dim:
+        raise ValueError(f"{name}: [n_layers][{T}][heads][{plan.head_dim}], got {tuple(x.shape)}")
+    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
+        raise ValueError(f"{name}_out: shape, type or device other than {name}'s")
+    st, so = x.stride(), out.stride()
+    if x.numel() and (st[-1] != 1 or so[-1] != 1):
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    lead = x.dim() == 4
+    return SsaRopeTensor(x.data_ptr(), out.data_ptr(), x.shape[-2],
+                         (ctypes.c_int64 * 3)(st[0] if lead else 0, st[-3], st[-2]),
+                         (ctypes.c_int64 * 3)(so[0] if lead else 0, so[-3], so[-2]))
+
+
+def ssa_rope(plan: RopePlan, positions, q=None, k=None, q_out=None, k_out=None, offset: int = 0,
+             inverse: bool = False, stream=None):
+    """Rotate q and k ([n_layers][T][heads][D] or [T][heads][D], strided views
+    allowed) by positions + offset ([T] int32 or int64), in place or into
+    q_out / k_out; one launch for both.  ``inverse`` turns back (the gradient
+    of the rotation)."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k")
+    if x.dtype not in _ROPE_DTYPES:
+        raise ValueError(f"dtype {x.dtype}: bfloat16, float16 or float32")
+    if positions.dim() != 1 or positions.dtype not in (torch.int32, torch.int64) or \
+            not positions.is_contiguous():
+        raise ValueError("positions: a contiguous [T] int32 or int64 tensor")
+    T = positions.shape[0]
+    n_layers = x.shape[0] if x.dim() == 4 else 1
+    for t in (q, k):
+        if t is not None and (t.dtype != x.dtype or t.dim() != x.dim() or
+                              (t.dim() == 4 and t.shape[0] != n_layers)):
+            raise ValueError("q and k: the same type and layers")
+    for t in (q, k, positions):
+        if t is not None and t.device != plan.freq.device:
+            raise ValueError(f"tensors on {t.device}, the plan on {plan.freq.device}")
+    cq = _rope_tensor(plan, "q", q, q_out, T) if q is not None else None
+    ck = _rope_tensor(plan, "k", k, k_out, T) if k is not None else None
+    if x.numel() == 0:
+        return
+    _check(lib().ssa_rope(_ROPE_DTYPES[x.dtype], plan.head_dim, plan.rotary_dim,
+                          plan.interleaved, inverse, plan.freq.data_ptr(), plan.factor, n_layers,
+                          T, positions.data_ptr(), positions.dtype == torch.int64, offset,
+                          cq, ck, _stream(stream)))
 
 
 def ssa_selftest_bounded_wait(status, stream=None):

@@ -463,6 +463,60 @@ int ssa_sparse_paged_decode_host_tail(const ssa_layout* lay, const ssa_cache* c,
                      out, status, ws, stream, 1);
 }
 
+int ssa_rope_frequencies(int rotary_dim, double base, int scaling, double factor,
+                         double original_len, double low, double high, uint64_t* freq,
+                         double* attn_factor) {
+  return rope_frequencies(rotary_dim, base, scaling, factor, original_len, low, high, freq,
+                          attn_factor);
+}
+
+int ssa_rope(int dtype, int head_dim, int rotary_dim, int interleaved, int inverse,
+             const uint64_t* freq, float factor, int n_layers, int n_tokens, const void* pos,
+             int pos_is_64, int64_t pos_offset, const ssa_rope_tensor* q,
+             const ssa_rope_tensor* k, ssa_stream_t stream) {
+  if (dtype < SSA_BF16 || dtype > SSA_F32) return SSA_ERR_UNSUPPORTED;
+  if (rotary_dim < 2 || rotary_dim % 2 || rotary_dim > head_dim) return SSA_ERR_INVALID_ARG;
+  if (rotary_dim > SSA_ROPE_MAX_DIM || head_dim > 16384) return SSA_ERR_UNSUPPORTED;
+  if (n_layers < 1 || n_tokens < 0 || (!q && !k)) return SSA_ERR_INVALID_ARG;
+  if (!freq || (n_tokens > 0 && !pos)) return SSA_ERR_INVALID_ARG;
+  const size_t esz = dtype == SSA_F32 ? 4 : 2;
+  RopeArgs a{};
+  for (const ssa_rope_tensor* t : {q, k}) {
+    if (!t) continue;
+    if (t->heads < 1 || t->heads > 65536) return SSA_ERR_INVALID_ARG;
+    if (n_tokens > 0 && (!t->in || !t->out)) return SSA_ERR_INVALID_ARG;
+    if ((((uintptr_t)t->in | (uintptr_t)t->out) & (esz - 1))) return SSA_ERR_INVALID_ARG;
+    RopeTensor& r = a.x[a.n_x++];
+    r.in = t->in;
+    r.out = t->out;
+    r.heads = t->heads;
+    for (int i = 0; i < 3; ++i) {
+      r.is[i] = t->in_stride[i];
+      r.os[i] = t->out_stride[i];
+      const int n = i == 0 ? n_layers : i == 1 ? n_tokens : t->heads;
+      // in place: the same element for input and output, so the same strides
+      if (t->in == t->out && n > 1 && r.is[i] != r.os[i]) return SSA_ERR_INVALID_ARG;
+      if (n > 1 && r.os[i] == 0) return SSA_ERR_INVALID_ARG;   // several results, one place
+    }
+  }
+  if (n_tokens == 0) return SSA_OK;
+  a.dtype = dtype;
+  a.D = head_dim;
+  a.rd = rotary_dim;
+  a.interleaved = interleaved ? 1 : 0;
+  a.inverse = inverse ? 1 : 0;
+  a.n_layers = n_layers;
+  a.n_tokens = n_tokens;
+  a.pos64 = pos_is_64 ? 1 : 0;
+  a.num_sms = num_sms();
+  a.freq = freq;
+  a.pos = pos;
+  a.offset = pos_offset;
+  a.factor = factor;
+  cudaError_t e = launch_rope(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? SSA_OK : fail_cuda(e);
+}
+
 const char* ssa_status_str(int code) {
   switch (code) {
     case SSA_OK: return "ok";

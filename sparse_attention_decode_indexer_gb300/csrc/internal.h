@@ -118,6 +118,25 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 int decode_max_ctas_page_head(const Dims& d, int num_sms);
 cudaError_t launch_decode_page_head(const DecodeArgs& a, cudaStream_t s);
 
+// -- rope.cu -----------------------------------------------------------------
+struct RopeTensor {
+  const void* in;
+  void* out;
+  int heads;
+  int64_t is[3], os[3];      // layer, token, head strides in elements
+};
+struct RopeArgs {
+  RopeTensor x[2];
+  int n_x, dtype, D, rd, interleaved, inverse, n_layers, n_tokens, pos64, num_sms;
+  const uint64_t* freq;
+  const void* pos;
+  int64_t offset;
+  float factor;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+int rope_frequencies(int rd, double base, int scaling, double factor, double original_len,
+                     double low, double high, uint64_t* freq, double* attn_factor);
+
 // Properties of the current device, queried once per device ordinal and
 // cached (SM count; the most dynamic shared memory one CTA may opt in to).
 constexpr int kMaxDevices = 64;

@@ -24,6 +24,11 @@ the next step's likely pages are fetched while this step's attention and the
 next step's indexer run, and the next step's ensure waits for it.  The
 step's scores alternate between two buffers so that the preload reads one
 while the next indexer writes the other.
+
+With ``rope`` (a RopePlan), queries and keys come without their positions:
+``store`` rotates the keys by the ``positions`` it is given, ``step`` the
+queries by each request's last position (seq_lens - 1), both into buffers of
+the runner's own, in front of the calls that read them.
 """
 from __future__ import annotations
 
@@ -34,8 +39,8 @@ import torch
 from . import (KVCache, Layout, ssa_ensure_remap, ssa_ensure_remap_bind,
                ssa_ensure_remap_deferred, ssa_ensure_remap_shared, ssa_ensure_resident,
                ssa_fetch_misses, ssa_index_topk, ssa_lru_init, ssa_prefetch_pages,
-               ssa_remap_block_table, ssa_sparse_paged_decode, ssa_sparse_paged_decode_fetch,
-               ssa_store_kv_mirror, ssa_workspace_size)
+               ssa_remap_block_table, ssa_rope, ssa_sparse_paged_decode,
+               ssa_sparse_paged_decode_fetch, ssa_store_kv_mirror, ssa_workspace_size)
 
 
 def split_layers(n_layers: int, groups: int):
@@ -51,7 +56,7 @@ class DecodeRunner:
     def __init__(self, layout: Layout, host_tier: bool, identity: bool, block_table, seq_lens,
                  device="cuda", preload_width: int = 0, shared_residency: bool = False,
                  fetch_in_attention: bool = False, graphs: bool = False,
-                 overlap_groups: int = 0):
+                 overlap_groups: int = 0, rope=None):
         self.layout = layout
         self.cache = KVCache(layout, host_tier, device)
         L, B, W = layout.n_layers, layout.batch, layout.max_sel
@@ -87,6 +92,11 @@ class DecodeRunner:
         self._graphs = {}
         self.host_tier = bool(host_tier)
         self.overlap_groups = int(overlap_groups)
+        if rope is not None and rope.head_dim != layout.head_dim:
+            raise ValueError(f"rope: head_dim {rope.head_dim}, the cache's is {layout.head_dim}")
+        self.rope = rope
+        if rope is not None:
+            self.q_rot = torch.zeros_like(self.out)
 
     def enable_preload(self, width: int):
         """Issue the top-k preload of `width` pages per request with every
@@ -106,14 +116,30 @@ class DecodeRunner:
         self.n_steps = 0
 
     # write path ---------------------------------------------------------------
-    def store(self, layer0: int, n_layers: int, k, v, pos):
-        """k, v: bf16 [n_layers][T][Hkv][D] on the device; pos: int64 [T]."""
+    def store(self, layer0: int, n_layers: int, k, v, pos, positions=None):
+        """k, v: bf16 [n_layers][T][Hkv][D] on the device; pos: int64 [T]
+        logical token ids.  With ``rope``, positions [T] (int32 or int64) are
+        the tokens' positions in their requests; k itself stays as it is."""
+        if self.rope is not None:
+            if positions is None:
+                raise ValueError("store with rope: positions of the tokens")
+            k_rot = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            ssa_rope(self.rope, positions, k=k, k_out=k_rot)
+            k = k_rot
         ssa_store_kv_mirror(self.cache, layer0, n_layers, k, v, pos, self.status)
 
     # one decode step ------------------------------------------------------------
+    def _rotated(self, q, sl=slice(None)):
+        """The queries of the layers `sl` at their requests' last positions."""
+        if self.rope is None:
+            return q
+        ssa_rope(self.rope, self.seq_lens, q=q, q_out=self.q_rot[sl], offset=-1)
+        return self.q_rot[sl]
+
     def _calls(self, q, layer0: int, n_layers: int, keep_scores: bool, fused: bool):
         sl = slice(layer0, layer0 + n_layers)
         c = self.cache
+        q = self._rotated(q, sl)
         ssa_index_topk(c, layer0, n_layers, q, self.block_table, self.seq_lens, self.sel[sl],
                        self.n_sel[sl], self.scores[sl] if keep_scores else None, self.status,
                        self.ws)
@@ -153,6 +179,7 @@ class DecodeRunner:
             self.ev_fetched = [torch.cuda.Event() for _ in range(L)]
             self.ev_attended = torch.cuda.Event()
         main, att = torch.cuda.current_stream(), self.att_stream
+        q = self._rotated(q)
         ssa_index_topk(c, 0, L, q, self.block_table, self.seq_lens, self.sel, self.n_sel,
                        self.scores if keep_scores else None, self.status, self.ws)
         ssa_ensure_remap_bind(c, 0, L, self.sel, self.block_table, self.phys, self.miss_page,
@@ -182,6 +209,7 @@ class DecodeRunner:
         L, c = self.layout.n_layers, self.cache
         scores = self.scores if self.n_steps % 2 == 0 else self.scores_alt
         main = torch.cuda.current_stream()
+        q = self._rotated(q)
         ssa_index_topk(c, 0, L, q, self.block_table, self.seq_lens, self.sel, self.n_sel, scores,
                        self.status, self.ws)
         main.wait_event(self.ev_preload)          # the previous step's preload is done
