@@ -82,8 +82,9 @@ enum {
   SSA_ST_UNRESOLVED = 8,      /* a selected page had no slot at remap/decode */
   SSA_ST_BAD_POS = 16,        /* store positions not strictly increasing     */
   SSA_ST_TIMEOUT = 32,        /* a bounded device wait gave up               */
-  SSA_ST_INTERNAL = 64        /* a kernel's own consistency check failed (its
+  SSA_ST_INTERNAL = 64,       /* a kernel's own consistency check failed (its
                                  work was abandoned; report it as a bug)       */
+  SSA_ST_NO_PAGES = 128       /* ssa_fork_requests found too few free pages    */
 };
 
 /* KV formats.  FP8_E4M3: e4m3 codes, one fp32 scale per token (over all KV
@@ -453,6 +454,88 @@ int ssa_sparse_paged_decode_host_tail(const ssa_layout *lay, const ssa_cache *c,
                                       const int32_t *block_table, const int32_t *seq_lens,
                                       float sm_scale, void *out, int32_t *status, void *ws,
                                       ssa_stream_t stream);
+
+/*
+ * Owners of the pages: copying pages, forking, growing and freeing requests,
+ * compacting the logical page space.  (FreeToken PR #499, "What", has logical
+ * pages that outlive the requests that filled them; the pages leave handing
+ * them out to the engine around the cache.)
+ *   block_table [B][n_max], seq_lens [B]: as for ssa_index_topk, here updated
+ *   ref [Lp]  references of each logical page, device: one per row and entry
+ *             below ceil(seq_len / P), plus any the caller adds to pin a page
+ *             (a cached prefix, say).  ref <= 0: the page is free.
+ * The calls work on every layer of the cache.  They order like every other
+ * call; between ssa_ensure_remap_bind / _deferred and the call that completes
+ * it none of them may run, and work on other streams (a preload) must have
+ * been waited for.  ws: ssa_workspace_size bytes, zeroed once, not used by
+ * another call at the same time.  With residency shared by the layers
+ * (ssa_ensure_remap_shared) the other layers' state arrays must be unbound, as
+ * ssa_lru_init leaves them, and a page that holds a slot is no dst of
+ * ssa_copy_pages (only layer0's pool block would be written).  Lengths outside [0, n_max * P] set
+ * SSA_ST_BAD_POS and count as the nearest bound; ids out of range set
+ * SSA_ST_BAD_ID and are carried along, never followed.
+ */
+typedef struct ssa_requests {
+  int32_t *block_table, *seq_lens, *ref;
+} ssa_requests;
+
+/* ref := the references of the table's rows (any pins are forgotten). */
+int ssa_page_refs(const ssa_layout *lay, const ssa_requests *r, int32_t *status,
+                  ssa_stream_t stream);
+
+/*
+ * Page dst[i] := page src[i], in every layer: K, V and scales, in the mirror
+ * (where there is one) and in the slot that dst[i] holds (if any), and the
+ * slab row.  The source is src[i]'s slot, or its mirror block.
+ *   src, dst  [n] int32 device; n <= 16384 (SSA_ERR_UNSUPPORTED above);
+ *             a pair with a negative id is padding
+ * Pairs with an id out of range, whose dst is the dst of an earlier pair, or
+ * the src of another pair, are skipped: SSA_ST_BAD_ID.  Without a mirror, a
+ * page without a slot has no K and V to copy (SSA_ST_UNRESOLVED; the slab row
+ * is copied).  Reference counts and residency stay as they are.
+ */
+int ssa_copy_pages(const ssa_layout *lay, const ssa_cache *c, const int32_t *src,
+                   const int32_t *dst, int n, int32_t *status, void *ws, ssa_stream_t stream);
+
+/*
+ * Fork, grow and free requests: row i becomes a continuation of what row
+ * parent[i] held before the call, max(its length, new_lens[i]) tokens long.
+ *   parent[i] = i    the row goes on (and may grow)
+ *   parent[i] = j    the row's own pages are let go; it shares j's context
+ *   parent[i] = -1   the row is freed (new_lens[i] > 0: and admitted anew,
+ *                    with new_lens[i] tokens' worth of empty pages)
+ *   parent [B] int32, new_lens_opt [B] int32 or NULL (no growth); device
+ * Full pages are shared.  A partly filled last page is kept by the lowest row
+ * that continues it, unless a reference from elsewhere stays (a row that holds
+ * it as a full page, a pin); every other row gets a copy (as ssa_copy_pages).
+ * New pages are the lowest free ids, in row order (the copy, then growth);
+ * pages let go in this call count as free.  New pages start with an empty slab
+ * row.  With a mirror, new pages and pages that became free give their slots
+ * back; without one every page keeps the slot it has.  Entries past a row's
+ * pages become -1.
+ * Too few free pages: SSA_ST_NO_PAGES, and the rows that got none are cut to
+ * the tokens their pages hold (a missing copy cuts the partly filled page).
+ * A parent below -1 or at B and above: SSA_ST_BAD_ID, the row goes on; a
+ * new_lens above n_max * P: SSA_ST_BAD_POS, clipped.
+ */
+int ssa_fork_requests(const ssa_layout *lay, const ssa_cache *c, const ssa_requests *r,
+                      const int32_t *parent, const int32_t *new_lens_opt, int32_t *status,
+                      void *ws, ssa_stream_t stream);
+
+/*
+ * Compaction: with n live pages (ref > 0), every live page gets an id below n,
+ * so that the ids from n on (and their mirror blocks) are free.  The k-th live
+ * page at or above n moves to the k-th free id below n, both ascending: slab
+ * row, mirror block and count move, the two pages trade their slots (pool
+ * bytes stay), and the rows name the new id.
+ *   moved_from_opt, moved_to_opt [Lp] int32 out or NULL: the first n_moved
+ *   entries are the moves (for references that the caller keeps itself)
+ *   n_moved_opt [1] int32 out or NULL
+ * Row entries whose page nothing counts set SSA_ST_BAD_ID.
+ */
+int ssa_compact_pages(const ssa_layout *lay, const ssa_cache *c, const ssa_requests *r,
+                      int32_t *moved_from_opt, int32_t *moved_to_opt, int32_t *n_moved_opt,
+                      int32_t *status, void *ws, ssa_stream_t stream);
 
 /*
  * Rotary positions of queries and keys, before ssa_store_kv_mirror (keys) and

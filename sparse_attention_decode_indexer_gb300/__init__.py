@@ -13,6 +13,8 @@ library is missing or no GPU is present the calls raise.
     ssa_sparse_paged_decode  attention over the selected pages
     ssa_prefetch_pages       top-k preload of the next step's likely pages
     ssa_rope                 rotary positions of queries and new keys
+    ssa_copy_pages, ssa_fork_requests, ssa_compact_pages
+                             owners of the pages: copy, fork / grow / free, compact
 """
 from __future__ import annotations
 
@@ -34,7 +36,7 @@ KV_FORMATS = {"bf16": SSA_KV_BF16, "fp8": SSA_KV_FP8_E4M3,
               "e4m3_page_head": SSA_KV_E4M3_PAGE_HEAD, "int8_page_head": SSA_KV_INT8_PAGE_HEAD}
 
 ST_DROP, ST_BAD_ID, ST_MISS_NO_MIRROR, ST_UNRESOLVED, ST_BAD_POS, ST_TIMEOUT = 1, 2, 4, 8, 16, 32
-ST_INTERNAL = 64
+ST_INTERNAL, ST_NO_PAGES = 64, 128
 
 EXPORTS = ("ssa_workspace_size", "ssa_lru_init", "ssa_store_kv_mirror", "ssa_index_topk",
            "ssa_ensure_resident", "ssa_remap_block_table", "ssa_sparse_paged_decode",
@@ -43,7 +45,8 @@ EXPORTS = ("ssa_workspace_size", "ssa_lru_init", "ssa_store_kv_mirror", "ssa_ind
            "ssa_prefetch_pages", "ssa_ensure_remap", "ssa_sparse_paged_decode_host_tail",
            "ssa_ensure_remap_shared", "ssa_ensure_remap_deferred",
            "ssa_sparse_paged_decode_fetch", "ssa_ensure_remap_bind", "ssa_fetch_misses",
-           "ssa_rope", "ssa_rope_frequencies")
+           "ssa_rope", "ssa_rope_frequencies", "ssa_page_refs", "ssa_copy_pages",
+           "ssa_fork_requests", "ssa_compact_pages")
 
 
 class SsaError(RuntimeError):
@@ -63,6 +66,11 @@ class SsaCache(ctypes.Structure):
         "k_pool", "v_pool", "k_scale", "v_scale", "k_mirror", "v_mirror", "k_scale_mirror",
         "v_scale_mirror", "slab", "slab_scale", "slab_sum", "slab_cnt", "slot_of", "page_of",
         "last_use", "clock")]
+
+
+class SsaRequests(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("ref", ctypes.c_void_p)]
 
 
 class SsaRopeTensor(ctypes.Structure):
@@ -134,6 +142,15 @@ def lib():
         L.ssa_rope_frequencies.restype = i32
         L.ssa_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64,
                                            P(ctypes.c_uint64), P(f64)]
+        R = P(SsaRequests)
+        L.ssa_page_refs.restype = i32
+        L.ssa_page_refs.argtypes = [P(SsaLayout), R, vp, vp]
+        L.ssa_copy_pages.restype = i32
+        L.ssa_copy_pages.argtypes = [P(SsaLayout), P(SsaCache), vp, vp, i32, vp, vp, vp]
+        L.ssa_fork_requests.restype = i32
+        L.ssa_fork_requests.argtypes = [P(SsaLayout), P(SsaCache), R, vp, vp, vp, vp, vp]
+        L.ssa_compact_pages.restype = i32
+        L.ssa_compact_pages.argtypes = [P(SsaLayout), P(SsaCache), R, vp, vp, vp, vp, vp, vp]
         _lib = L
     return _lib
 
@@ -397,6 +414,93 @@ def ssa_sparse_paged_decode_host_tail(cache: KVCache, layer0: int, n_layers: int
         ctypes.byref(cache._lay), ctypes.byref(cache.c), layer0, n_layers, _ptr(q), _ptr(sel),
         _ptr(block_table), _ptr(seq_lens), float(sm_scale), _ptr(out), _ptr(status), _ptr(ws),
         _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# owners of the pages
+# ---------------------------------------------------------------------------
+
+def _ints(name, t, n, device):
+    """A contiguous int32 device tensor of n entries, or an error."""
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name}: {n} contiguous int32 on {device}, got {tuple(t.shape)} "
+                         f"{t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+class RequestTable:
+    """The requests' pages: block_table [B][max_pages], seq_lens [B] and the
+    references of every logical page, ref [logical_pages], all int32 on the
+    device.  int32 tensors already there are taken as they are, so that a
+    runner's tables change in place.  Without ``ref`` the rows are counted
+    (ssa_page_refs); add to ref[p] to pin page p."""
+
+    def __init__(self, layout: Layout, block_table, seq_lens, ref=None, device="cuda"):
+        i32 = torch.int32
+        self.layout = layout
+        self.block_table = torch.as_tensor(block_table).to(device=device, dtype=i32).contiguous()
+        self.seq_lens = torch.as_tensor(seq_lens).to(device=device, dtype=i32).contiguous()
+        dev = self.block_table.device
+        _ints("block_table", self.block_table, layout.batch * layout.max_pages, dev)
+        _ints("seq_lens", self.seq_lens, layout.batch, dev)
+        if ref is None:
+            self.ref = torch.zeros((layout.logical_pages,), dtype=i32, device=dev)
+        else:
+            self.ref = torch.as_tensor(ref).to(device=dev, dtype=i32).contiguous()
+        _ints("ref", self.ref, layout.logical_pages, dev)
+        self._c = SsaRequests(self.block_table.data_ptr(), self.seq_lens.data_ptr(),
+                              self.ref.data_ptr())
+        self._lay = layout.c()
+        if ref is None:
+            ssa_page_refs(self)
+
+
+def _same_pages(cache: KVCache, table: RequestTable):
+    a, b = cache.layout, table.layout
+    if (a.batch, a.max_pages, a.logical_pages, a.page_size) != \
+            (b.batch, b.max_pages, b.logical_pages, b.page_size):
+        raise ValueError("the cache and the request table have different layouts")
+    if cache.slot_of.device != table.ref.device:
+        raise ValueError("the cache and the request table are on different devices")
+
+
+def ssa_page_refs(table: RequestTable, status=None, stream=None):
+    """Count the rows' references anew (any pins are forgotten)."""
+    _check(lib().ssa_page_refs(table._lay, table._c, _ptr(status), _stream(stream)))
+
+
+def ssa_copy_pages(cache: KVCache, src, dst, status, ws, stream=None):
+    """Page dst[i] := page src[i] in every layer; int32 device lists, negative
+    ids are padding."""
+    n, dev = src.numel(), cache.slot_of.device
+    _check(lib().ssa_copy_pages(cache._lay, cache._c, _ints("src", src, n, dev),
+                                _ints("dst", dst, n, dev), n, _ptr(status), _ptr(ws),
+                                _stream(stream)))
+
+
+def ssa_fork_requests(cache: KVCache, table: RequestTable, parent, new_lens, status, ws,
+                      stream=None):
+    """Row i continues what row parent[i] held (-1: nothing, the row is freed),
+    grown to new_lens[i] tokens (None: no growth): full pages shared, partly
+    filled ones copied, new ones taken, unused ones freed."""
+    _same_pages(cache, table)
+    B, dev = cache.layout.batch, cache.slot_of.device
+    _check(lib().ssa_fork_requests(cache._lay, cache._c, table._c, _ints("parent", parent, B, dev),
+                                   None if new_lens is None else
+                                   _ints("new_lens", new_lens, B, dev),
+                                   _ptr(status), _ptr(ws), _stream(stream)))
+
+
+def ssa_compact_pages(cache: KVCache, table: RequestTable, status, ws, moved_from=None,
+                      moved_to=None, n_moved=None, stream=None):
+    """Move the live pages to the lowest ids; the moves go to moved_from /
+    moved_to ([logical_pages]) and their number to n_moved ([1])."""
+    _same_pages(cache, table)
+    Lp, dev = cache.layout.logical_pages, cache.slot_of.device
+    outs = [None if t is None else _ints(name, t, n, dev) for name, t, n in (
+        ("moved_from", moved_from, Lp), ("moved_to", moved_to, Lp), ("n_moved", n_moved, 1))]
+    _check(lib().ssa_compact_pages(cache._lay, cache._c, table._c, *outs, _ptr(status), _ptr(ws),
+                                   _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

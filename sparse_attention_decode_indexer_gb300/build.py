@@ -17,7 +17,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 OUT = os.path.join(HERE, "libssa_gb300.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "store.cu", "store_page_head.cu", "index.cu", "ensure.cu", "decode.cu",
-           "decode_page_head.cu", "rope.cu", "noalloc.cu", "selftest.cu", "probe.cu"]
+           "decode_page_head.cu", "pages.cu", "rope.cu", "noalloc.cu", "selftest.cu", "probe.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", INCLUDE]

@@ -87,6 +87,9 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 struct WsLayout {
   size_t scores, miss_page, miss_slot, n_miss, part_o, part_ml, tickets, idx_tickets;
   size_t pf_cand, pf_ncand, pf_miss_page, pf_miss_slot, pf_n_miss;   // ssa_prefetch_pages
+  // the page calls
+  size_t pg_bt, pg_len, pg_bits, pg_list, pg_to, pg_map, pg_plan, pg_copy, pg_count, pg_ok,
+      pg_ticket;
   size_t total;
 };
 
@@ -111,6 +114,17 @@ WsLayout ws_layout(const Dims& d) {
   w.pf_miss_page = off; off += align256((size_t)d.Lyr * d.B * d.W * 4);
   w.pf_miss_slot = off; off += align256((size_t)d.Lyr * d.B * d.W * 4);
   w.pf_n_miss = off; off += align256((size_t)d.Lyr * 4);
+  w.pg_bt = off;     off += align256((size_t)d.B * d.nmax * 4);
+  w.pg_len = off;    off += align256((size_t)d.B * 4);
+  w.pg_bits = off;   off += align256(((size_t)d.Lp + 31) / 32 * 4);
+  w.pg_list = off;   off += align256((size_t)d.Lp * 4);
+  w.pg_to = off;     off += align256((size_t)d.Lp * 4);
+  w.pg_map = off;    off += align256((size_t)d.Lp * 4);
+  w.pg_plan = off;   off += align256((size_t)d.B * 16);
+  w.pg_copy = off;   off += align256((size_t)d.B * 8);
+  w.pg_count = off;  off += 256;
+  w.pg_ok = off;     off += align256((size_t)kMaxCopyPairs * 4);
+  w.pg_ticket = off; off += 256;
   w.total = off;
   return w;
 }
@@ -118,6 +132,30 @@ WsLayout ws_layout(const Dims& d) {
 template <typename T>
 T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
+}
+
+PageWs page_ws(const Dims& d, void* ws) {
+  const WsLayout w = ws_layout(d);
+  return PageWs{at<int32_t>(ws, w.pg_bt),   at<int32_t>(ws, w.pg_len),
+                at<uint32_t>(ws, w.pg_bits), at<int32_t>(ws, w.pg_list),
+                at<int32_t>(ws, w.pg_to),   at<int32_t>(ws, w.pg_map),
+                at<char>(ws, w.pg_plan),    at<char>(ws, w.pg_copy),
+                at<int32_t>(ws, w.pg_count), at<int32_t>(ws, w.pg_ok),
+                at<int32_t>(ws, w.pg_ticket)};
+}
+
+// The page calls write every array of a cache.
+int check_page_cache(const Dims& d, const ssa_cache* c) {
+  const int r = check_cache(d, c);
+  if (r) return r;
+  if (!c->slab_scale || !c->slab_sum || !c->slab_cnt) return SSA_ERR_INVALID_ARG;
+  // grid dimensions: requests and layers
+  if (d.B > 65535 || d.Lyr > 65534) return SSA_ERR_UNSUPPORTED;
+  return SSA_OK;
+}
+
+int check_requests(const ssa_requests* r) {
+  return r && r->block_table && r->seq_lens && r->ref ? SSA_OK : SSA_ERR_INVALID_ARG;
 }
 
 }  // namespace
@@ -463,6 +501,57 @@ int ssa_sparse_paged_decode_host_tail(const ssa_layout* lay, const ssa_cache* c,
                      out, status, ws, stream, 1);
 }
 
+int ssa_page_refs(const ssa_layout* lay, const ssa_requests* req, int32_t* status,
+                  ssa_stream_t stream) {
+  Dims d;
+  int r = check_layout(lay, d);
+  if (r) return r;
+  if ((r = check_requests(req))) return r;
+  cudaError_t e = launch_page_refs(d, *req, status, (cudaStream_t)stream);
+  return e == cudaSuccess ? SSA_OK : fail_cuda(e);
+}
+
+int ssa_copy_pages(const ssa_layout* lay, const ssa_cache* c, const int32_t* src,
+                   const int32_t* dst, int n, int32_t* status, void* ws, ssa_stream_t stream) {
+  Dims d;
+  int r = check_layout(lay, d);
+  if (r) return r;
+  if ((r = check_page_cache(d, c))) return r;
+  if (n < 0 || !ws || (n > 0 && (!src || !dst))) return SSA_ERR_INVALID_ARG;
+  if (n > kMaxCopyPairs) return SSA_ERR_UNSUPPORTED;
+  cudaError_t e = launch_copy_pages(d, *c, src, dst, n, status, page_ws(d, ws),
+                                    (cudaStream_t)stream);
+  return e == cudaSuccess ? SSA_OK : fail_cuda(e);
+}
+
+int ssa_fork_requests(const ssa_layout* lay, const ssa_cache* c, const ssa_requests* req,
+                      const int32_t* parent, const int32_t* new_lens_opt, int32_t* status,
+                      void* ws, ssa_stream_t stream) {
+  Dims d;
+  int r = check_layout(lay, d);
+  if (r) return r;
+  if ((r = check_page_cache(d, c))) return r;
+  if ((r = check_requests(req))) return r;
+  if (!parent || !ws) return SSA_ERR_INVALID_ARG;
+  cudaError_t e = launch_fork(d, *c, *req, parent, new_lens_opt, status, page_ws(d, ws),
+                              (cudaStream_t)stream);
+  return e == cudaSuccess ? SSA_OK : fail_cuda(e);
+}
+
+int ssa_compact_pages(const ssa_layout* lay, const ssa_cache* c, const ssa_requests* req,
+                      int32_t* moved_from_opt, int32_t* moved_to_opt, int32_t* n_moved_opt,
+                      int32_t* status, void* ws, ssa_stream_t stream) {
+  Dims d;
+  int r = check_layout(lay, d);
+  if (r) return r;
+  if ((r = check_page_cache(d, c))) return r;
+  if ((r = check_requests(req))) return r;
+  if (!ws) return SSA_ERR_INVALID_ARG;
+  cudaError_t e = launch_compact(d, *c, *req, moved_from_opt, moved_to_opt, n_moved_opt, status,
+                                 page_ws(d, ws), num_sms(), (cudaStream_t)stream);
+  return e == cudaSuccess ? SSA_OK : fail_cuda(e);
+}
+
 int ssa_rope_frequencies(int rotary_dim, double base, int scaling, double factor,
                          double original_len, double low, double high, uint64_t* freq,
                          double* attn_factor) {
@@ -533,8 +622,8 @@ const char* ssa_status_str(int code) {
     static thread_local char buf[256];
     buf[0] = 0;
     const char* names[] = {"drop", "bad_id", "miss_no_mirror", "unresolved", "bad_pos",
-                           "timeout", "internal"};
-    for (int i = 0; i < 7; ++i)
+                           "timeout", "internal", "no_pages"};
+    for (int i = 0; i < 8; ++i)
       if (code & (1 << i)) {
         if (buf[0]) strncat(buf, "|", sizeof(buf) - strlen(buf) - 1);
         strncat(buf, names[i], sizeof(buf) - strlen(buf) - 1);

@@ -118,6 +118,34 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 int decode_max_ctas_page_head(const Dims& d, int num_sms);
 cudaError_t launch_decode_page_head(const DecodeArgs& a, cudaStream_t s);
 
+// -- pages.cu ----------------------------------------------------------------
+// Scratch of the page calls, all in the caller's workspace.
+struct PageWs {
+  int32_t* old_bt;     // [B][n_max]
+  int32_t* old_len;    // [B]
+  uint32_t* bits;      // [ceil(Lp / 32)]
+  int32_t* list;       // [Lp] new pages (fork), moved pages (compaction)
+  int32_t* to;         // [Lp]
+  int32_t* map;        // [Lp]
+  void* plan;          // [B] int4
+  void* copy;          // [B] int2
+  int32_t* count;      // [2]
+  int32_t* ok;         // [kMaxCopyPairs]
+  int32_t* ticket;     // zero between calls
+};
+constexpr int kMaxCopyPairs = 16384;
+cudaError_t launch_page_refs(const Dims& d, const ssa_requests& r, int32_t* status,
+                             cudaStream_t s);
+cudaError_t launch_copy_pages(const Dims& d, const ssa_cache& c, const int32_t* src,
+                              const int32_t* dst, int n, int32_t* status, const PageWs& w,
+                              cudaStream_t s);
+cudaError_t launch_fork(const Dims& d, const ssa_cache& c, const ssa_requests& r,
+                        const int32_t* parent, const int32_t* new_lens, int32_t* status,
+                        const PageWs& w, cudaStream_t s);
+cudaError_t launch_compact(const Dims& d, const ssa_cache& c, const ssa_requests& r,
+                           int32_t* moved_from, int32_t* moved_to, int32_t* n_moved,
+                           int32_t* status, const PageWs& w, int num_sms, cudaStream_t s);
+
 // -- rope.cu -----------------------------------------------------------------
 struct RopeTensor {
   const void* in;

@@ -36,9 +36,9 @@ import math
 
 import torch
 
-from . import (KVCache, Layout, ssa_ensure_remap, ssa_ensure_remap_bind,
+from . import (KVCache, Layout, RequestTable, ssa_compact_pages, ssa_ensure_remap, ssa_ensure_remap_bind,
                ssa_ensure_remap_deferred, ssa_ensure_remap_shared, ssa_ensure_resident,
-               ssa_fetch_misses, ssa_index_topk, ssa_lru_init, ssa_prefetch_pages,
+               ssa_fetch_misses, ssa_fork_requests, ssa_index_topk, ssa_lru_init, ssa_prefetch_pages,
                ssa_remap_block_table, ssa_rope, ssa_sparse_paged_decode,
                ssa_sparse_paged_decode_fetch, ssa_store_kv_mirror, ssa_workspace_size)
 
@@ -127,6 +127,35 @@ class DecodeRunner:
             ssa_rope(self.rope, positions, k=k, k_out=k_rot)
             k = k_rot
         ssa_store_kv_mirror(self.cache, layer0, n_layers, k, v, pos, self.status)
+
+    # owners of the pages ----------------------------------------------------------
+    @property
+    def table(self) -> RequestTable:
+        """The runner's block table and lengths with the pages' reference
+        counts, counted on first use."""
+        if not hasattr(self, "_table"):
+            self._table = RequestTable(self.layout, self.block_table, self.seq_lens,
+                                       device=self.block_table.device)
+        return self._table
+
+    def _wait_preload(self):
+        # the last step's preload may still bind slots on its own stream
+        if hasattr(self, "side"):
+            torch.cuda.current_stream().wait_event(self.ev_preload)
+
+    def fork(self, parent, new_lens=None):
+        """Row i goes on with what row parent[i] held (-1: freed), grown to
+        new_lens[i] tokens; int32 [B] on the device.  The block table and the
+        lengths change in place, so captured steps see them."""
+        table = self.table
+        self._wait_preload()
+        ssa_fork_requests(self.cache, table, parent, new_lens, self.status, self.ws)
+
+    def compact(self, moved_from=None, moved_to=None, n_moved=None):
+        """Move the live pages to the lowest logical ids."""
+        table = self.table
+        self._wait_preload()
+        ssa_compact_pages(self.cache, table, self.status, self.ws, moved_from, moved_to, n_moved)
 
     # one decode step ------------------------------------------------------------
     def _rotated(self, q, sl=slice(None)):
