@@ -289,7 +289,6 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(Table t, const 
                                                                  PageCache c) {
   extern __shared__ int32_t dyn[];
   __shared__ int s_tmp[33];
-  __shared__ int s_got;
   pdl_trigger();
   pdl_wait();
   if (!page_bits(t.ref, c.Lp, w.bits, false, w.ticket)) return;

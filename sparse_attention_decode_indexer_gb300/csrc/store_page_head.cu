@@ -14,16 +14,28 @@
 //
 // What bounds it: bf16 K and V in (4 Hkv D bytes a token) and codes out
 // (2 Hkv D, and as many again to the mirror over the host link), so HBM or the
-// host link; each input is read once, into shared memory, because the scale
-// has to be known before the first code.
+// host link; an append of one token per request is latency, a chain of
+// dependent reads (position, slot, scale).
 //
-// Split: one CTA per (run of consecutive tokens of one page, layer, KV head),
-// so that a decode append (one token per request) spreads over requests x
-// layers x heads, and a page's tokens of one head fit in shared memory as they
-// came.  The heads of a page meet only in the slab's scale (max over all
-// heads): they form a cluster of Hkv CTAs and read each other's maximum
-// through distributed shared memory.  Runs are found per chunk of tokens as in
-// store.cu: chunks of one token for short calls, of one page for long ones.
+// Two kernels, by the length of the call as in store.cu: a call of 4,096
+// tokens or more is a prefill, whose runs (consecutive tokens of one page) are
+// mostly whole pages; a shorter one is mostly an append, whose runs are one or
+// a few tokens.
+//
+// Prefill: one CTA per (run, layer, KV head), which keeps the run's rows of
+// its head in registers while the scale becomes known, so that each input is
+// read once.  A thread holds 8 dimensions of 4 consecutive tokens, so V leaves
+// as whole words of its d-major block through a swizzled tile.  The heads of a
+// page meet only in the slab's scale (max over all heads): they form a cluster
+// and read each other's maximum through distributed shared memory.
+// Its arithmetic is the division x / s'.  s' is the block's, so the reciprocal
+// is computed once and each quotient is corrected from its exact residual
+// twice (Markstein 1990: a faithful quotient plus its fused residual times the
+// correctly rounded reciprocal is the correctly rounded quotient), two
+// elements per f32x2 instruction: 5 instead of about 20 per pair.
+//
+// Append: one CTA per (run, layer) with a thread per slab element, so that the
+// heads meet in shared memory and a run costs three dependent reads.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -33,10 +45,9 @@ namespace ssa {
 namespace {
 
 constexpr int kHD = 128;                 // head_dim
-constexpr int kThreads = 128;            // one per head dimension
 constexpr int kMaxP = 128;
-constexpr int kUnitsPerRow = kHD * 2 / 16;     // 16-byte units of a bf16 token row
-constexpr int kLoads = 8;                // input loads in flight per thread and tensor
+constexpr int kRowUnits = kHD * 2 / 16;  // 16-byte units of a bf16 token row
+constexpr int kTokBatch = 8;             // append: tokens in flight per thread
 
 struct StorePHParams {
   uint8_t *k_pool, *v_pool;
@@ -51,7 +62,7 @@ struct StorePHParams {
   const __nv_bfloat16 *k, *v;            // [n_layers][T][Hkv][D]
   const int64_t* pos;
   int32_t* status;
-  int T, chunk, layer0, Lp, S, Hkv;
+  int T, layer0, Lp, S, Hkv;
 };
 
 __device__ __forceinline__ void cluster_sync() {
@@ -84,7 +95,270 @@ __device__ __forceinline__ float value(uint8_t c) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
 }
 
-// |x| of the finite ones of 8 bf16 values, maximum
+// The codes already in a block of one tensor, again at the scale that grew by
+// 1 / ratio: from the pool's copy where there is one (the mirror's bytes are
+// the same), to both.
+template <bool I8>
+__device__ __forceinline__ void rescale_block(uint8_t* mir, uint8_t* pool, int bytes, float ratio,
+                                              int tid, int nthreads) {
+  const uint8_t* from = pool ? pool : mir;
+  for (int u = tid; u < bytes / 16; u += nthreads) {
+    uint4 w = reinterpret_cast<const uint4*>(from)[u];
+    uint8_t* b = reinterpret_cast<uint8_t*>(&w);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) b[i] = quant<I8>(value<I8>(b[i]) * ratio);
+    if (mir) reinterpret_cast<uint4*>(mir)[u] = w;
+    if (pool) reinterpret_cast<uint4*>(pool)[u] = w;
+  }
+}
+
+// One tensor's block of one page and head: where it is held, and its scale.
+struct Block {
+  uint8_t *mir, *pool;
+  float *sc_m, *sc_p;
+  __device__ __forceinline__ Block(const StorePHParams& p, bool v, int layer, int pg, int slot,
+                                   int h, size_t pe) {
+    const size_t m = ((size_t)layer * p.Lp + pg) * p.Hkv + h;
+    const size_t s = ((size_t)layer * p.S + (slot < 0 ? 0 : slot)) * p.Hkv + h;
+    mir = v ? p.v_mir : p.k_mir;
+    sc_m = v ? p.v_scale_m : p.k_scale_m;
+    if (mir) { mir += m * pe; sc_m += m; }
+    pool = slot >= 0 ? (v ? p.v_pool : p.k_pool) + s * pe : nullptr;
+    sc_p = slot >= 0 ? (v ? p.v_scale : p.k_scale) + s : nullptr;
+  }
+  __device__ __forceinline__ float scale() const { return sc_p ? *sc_p : (mir ? *sc_m : 0.0f); }
+  __device__ __forceinline__ void set_scale(float s) const {
+    if (mir) *sc_m = s;
+    if (sc_p) *sc_p = s;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// append
+// ---------------------------------------------------------------------------
+// block: a thread per slab element (h, d); grid (tokens, layers): the CTA of a
+// run's first token stores the run, the others return.
+template <bool I8, int P>
+__global__ void __launch_bounds__(1024) append_page_head_kernel(StorePHParams p) {
+  __shared__ int s_row[P];
+  __shared__ int s_run;
+  __shared__ float s_max[2][32];
+  __shared__ __align__(16) uint8_t s_code[1024];
+  constexpr float kQmax = I8 ? 127.0f : 448.0f;
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int Hkv = p.Hkv, HD = Hkv * kHD, h = tid >> 7, d = tid & 127;
+  const int t0 = blockIdx.x, li = blockIdx.y, layer = p.layer0 + li;
+  // this token's position and the ones around it, in one round trip
+  const int64_t pos0 = p.pos[t0];
+  const int64_t prev = t0 > 0 ? p.pos[t0 - 1] : -1;
+  static_assert(P <= kHD, "the run's scan has a thread per token");
+  int64_t x0 = -1, x1 = -1;              // of tokens t0 + tid - 1 and t0 + tid
+  if (tid < P && t0 + tid < p.T) {
+    x1 = p.pos[t0 + tid];
+    if (tid > 0) x0 = p.pos[t0 + tid - 1];
+  }
+  if (pos0 < 0 || pos0 / P >= p.Lp) {
+    if (tid == 0) set_status(p.status, SSA_ST_BAD_ID);
+    return;
+  }
+  const int pg = (int)(pos0 / P);
+  if (t0 > 0) {
+    if (tid == 0 && prev >= pos0) set_status(p.status, SSA_ST_BAD_POS);
+    if (prev >= 0 && prev / P == pg) return;                 // inside a run
+  }
+  const size_t lp = (size_t)layer * p.Lp + pg;
+  const size_t so = lp * HD + tid;
+  float sum = p.slab_sum[so];
+  const int cnt0 = p.slab_cnt[lp];
+  int slot = p.slot_of[lp];
+  // the run's first token, while its length is found
+  const __nv_bfloat16* kin = p.k + ((size_t)li * p.T + t0) * HD + tid;
+  const __nv_bfloat16* vin = p.v + ((size_t)li * p.T + t0) * HD + tid;
+  __nv_bfloat16 k0 = kin[0], v0 = vin[0];
+  if (tid == 0) s_run = P;
+  __syncthreads();
+  if (tid < P) {
+    bool ends = t0 + tid >= p.T || x1 < 0 || x1 / P != pg;
+    if (!ends) {
+      s_row[tid] = (int)(x1 % P);
+      if (tid > 0 && x1 <= x0) set_status(p.status, SSA_ST_BAD_POS);
+    } else {
+      atomicMin(&s_run, tid);
+    }
+  }
+  if (slot >= p.S) {                       // corrupt state: never write through it
+    if (tid == 0) set_status(p.status, SSA_ST_BAD_ID);
+    slot = -1;
+  }
+  const size_t pe = (size_t)P * kHD;       // codes of one head of one page
+  const Block bk(p, false, layer, pg, slot, h, pe), bv(p, true, layer, pg, slot, h, pe);
+  const float old_k = cnt0 > 0 ? bk.scale() : 0.0f, old_v = cnt0 > 0 ? bv.scale() : 0.0f;
+  __syncthreads();
+  const int R = s_run;
+
+  // finite maxima of the run per head
+  float ak = 0.0f, av = 0.0f;
+  auto take = [](float& m, __nv_bfloat16 x) {
+    const float a = fabsf(__bfloat162float(x));
+    if (a < INFINITY) m = fmaxf(m, a);
+  };
+  take(ak, k0);
+  take(av, v0);
+  for (int r0 = 1; r0 < R; r0 += kTokBatch) {
+    __nv_bfloat16 xk[kTokBatch], xv[kTokBatch];
+#pragma unroll
+    for (int i = 0; i < kTokBatch; ++i)
+      if (r0 + i < R) {
+        xk[i] = kin[(size_t)(r0 + i) * HD];
+        xv[i] = vin[(size_t)(r0 + i) * HD];
+      }
+#pragma unroll
+    for (int i = 0; i < kTokBatch; ++i)
+      if (r0 + i < R) {
+        take(ak, xk[i]);
+        take(av, xv[i]);
+      }
+  }
+  ak = warp_max(ak);
+  av = warp_max(av);
+  if (lane == 0) {
+    s_max[0][warp] = ak;
+    s_max[1][warp] = av;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    ak = fmaxf(ak, s_max[0][(warp & ~3) + w]);
+    av = fmaxf(av, s_max[1][(warp & ~3) + w]);
+  }
+  const float need_k = ak / kQmax, need_v = av / kQmax;
+  const float sk = cnt0 > 0 ? fmaxf(old_k, need_k) : need_k;
+  const float sv = cnt0 > 0 ? fmaxf(old_v, need_v) : need_v;
+  if (d == 0) {
+    bk.set_scale(sk);
+    bv.set_scale(sv);
+  }
+  const bool gk = cnt0 > 0 && sk > old_k, gv = cnt0 > 0 && sv > old_v;
+  if (gk) rescale_block<I8>(bk.mir, bk.pool, (int)pe, old_k / sk, d, kHD);
+  if (gv) rescale_block<I8>(bv.mir, bv.pool, (int)pe, old_v / sv, d, kHD);
+  __syncthreads();                         // the new codes go on top
+
+  for (int r = 0; r < R; ++r) {
+    const __nv_bfloat16 xk = r == 0 ? k0 : kin[(size_t)r * HD], xv = r == 0 ? v0 : vin[(size_t)r * HD];
+    const float fk = __bfloat162float(xk), fv = __bfloat162float(xv);
+    const int j = s_row[r];
+    // K row j: the warp's 32 codes as two 16-byte stores
+    s_code[tid] = sk > 0.0f ? quant<I8>(fk / sk) : 0;
+    __syncwarp();
+    if (lane < 2) {
+      const uint4 w = *reinterpret_cast<const uint4*>(s_code + (tid & ~31) + 16 * lane);
+      const size_t off = (size_t)j * kHD + (d & ~31) + 16 * lane;
+      if (bk.mir) *reinterpret_cast<uint4*>(bk.mir + off) = w;
+      if (bk.pool) *reinterpret_cast<uint4*>(bk.pool + off) = w;
+    }
+    __syncwarp();
+    const uint8_t c = sv > 0.0f ? quant<I8>(fv / sv) : 0;
+    const size_t off = (size_t)d * P + j;
+    if (bv.mir) bv.mir[off] = c;
+    if (bv.pool) bv.pool[off] = c;
+    sum = sum + fk;                        // the slab: fp32, token order
+  }
+  p.slab_sum[so] = sum;
+  const int cnt = cnt0 + R;
+  const float mean = sum / (float)cnt;
+  const float a = warp_max(fabsf(mean));
+  if (lane == 0) s_max[0][warp] = a;       // the scales' maxima were read before the last barrier
+  __syncthreads();
+  float amax = 0.0f;
+  for (int w = 0; w < 4 * Hkv; ++w) amax = fmaxf(amax, s_max[0][w]);
+  const float s = amax / 127.0f;
+  int c = 0;
+  if (amax > 0.0f) c = (int)fminf(fmaxf(rintf(mean / s), -127.0f), 127.0f);
+  p.slab[so] = (int8_t)c;
+  if (tid == 0) {
+    p.slab_cnt[lp] = cnt;
+    p.slab_scale[lp] = s;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// prefill
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Divides by one block's scale.  With ny = -RN(1 / s) and nx = -x, each step
+// corrects the quotient by its residual q s - x (exact in one fma); the signs
+// are such that a zero keeps its own.  exact: s in [2^-90, 2^100] and x
+// finite, so that nothing on the way over- or underflows unless the quotient
+// is below 2^-12 (every code 0).
+struct Divider {
+  float s;
+  uint64_t s2, ny2;
+  bool exact;
+  __device__ __forceinline__ Divider(float s_, bool finite) : s(s_) {
+    exact = finite && s >= 0x1p-90f && s <= 0x1p100f;
+    const float ny = exact ? -(1.0f / s) : 0.0f;
+    s2 = pack2(s, s);
+    ny2 = pack2(ny, ny);
+  }
+  // two negated elements -> the two quotients
+  __device__ __forceinline__ uint64_t operator()(float nx0, float nx1) const {
+    const uint64_t nx = pack2(nx0, nx1);
+    uint64_t q = mul2(nx, ny2);
+    q = fma2(fma2(q, s2, nx), ny2, q);
+    q = fma2(fma2(q, s2, nx), ny2, q);
+    return q;
+  }
+};
+
+// Four quotients -> four codes, the first in byte 0.
+template <bool I8>
+__device__ __forceinline__ uint32_t codes4(uint64_t a, uint64_t b) {
+  float x0, x1, x2, x3;
+  unpack2(a, x0, x1);
+  unpack2(b, x2, x3);
+  if (I8) {
+    // |x| <= 127 (1 + 2^-24): adding 1.5 * 2^23 rounds to nearest even and
+    // leaves the code in the low byte
+    const float m = 12582912.0f;
+    const uint32_t lo = __byte_perm(__float_as_uint(x0 + m), __float_as_uint(x1 + m), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(x2 + m), __float_as_uint(x3 + m), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
+  }
+  return f32x4_to_e4m3x4(x0, x1, x2, x3);
+}
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Bit patterns of 8 |bf16|, maximum so far per 16-bit half (as integers, which
+// orders them; infinities and NaN from 0x7F80 on)
+__device__ __forceinline__ uint32_t absmax_bits(uint32_t m, uint4 v) {
+  m = __vmaxu2(m, v.x & 0x7FFF7FFFu);
+  m = __vmaxu2(m, v.y & 0x7FFF7FFFu);
+  m = __vmaxu2(m, v.z & 0x7FFF7FFFu);
+  return __vmaxu2(m, v.w & 0x7FFF7FFFu);
+}
+
 __device__ __forceinline__ float finite_absmax(uint4 v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   float m = 0.0f;
@@ -97,32 +371,39 @@ __device__ __forceinline__ float finite_absmax(uint4 v) {
   return m;
 }
 
-// dynamic shared memory: the run's K and V rows of one head as they came
-// (2 * P * 256 B), then the codes of one tensor on their way out (P * 128 B)
-inline size_t smem_bytes(int P) { return (size_t)P * (2 * kHD * 2 + kHD); }
+// Threads of a CTA and 16-byte units of K (and of V) a thread holds: 4 tokens
+// at a time, at most 8 units.
+constexpr int prefill_threads(int P) { return P == 16 ? 64 : (P == 128 ? 256 : 128); }
+constexpr int prefill_units(int P) { return P * kRowUnits / prefill_threads(P); }
+// dynamic shared memory: K rows as they came (for the slab's sums) and V's
+// codes on their way out
+inline size_t prefill_smem(int P) { return (size_t)P * kHD * 3; }
 
 template <bool I8, int P>
-__global__ void __launch_bounds__(kThreads) store_page_head_kernel(StorePHParams p) {
+__global__ void __launch_bounds__(prefill_threads(P), P == 128 ? 2 : 4)
+prefill_page_head_kernel(StorePHParams p) {
+  constexpr int NT = prefill_threads(P), NU = prefill_units(P), NW = NT / 32;
+  constexpr int G = NT / kRowUnits;      // groups of 4 tokens side by side
   extern __shared__ __align__(16) uint8_t dsm[];
-  __nv_bfloat16* kx = reinterpret_cast<__nv_bfloat16*>(dsm);       // [R][D]
-  __nv_bfloat16* vx = kx + P * kHD;
-  uint8_t* codes = reinterpret_cast<uint8_t*>(vx + P * kHD);       // K: [j][D]; V: [D][j]
+  uint4* kx = reinterpret_cast<uint4*>(dsm);                       // [r][16 units]
+  uint32_t* vt = reinterpret_cast<uint32_t*>(dsm + P * kHD * 2);   // [d][P / 4 words], swizzled
   __shared__ int s_start[P];
   __shared__ int s_row[P];               // the run's tokens' rows j, ascending
-  __shared__ int s_at[P];                // the token of row j in this run, or -1
   __shared__ int s_nstart, s_run;
-  __shared__ float s_red[2][kThreads / 32];
+  __shared__ uint32_t s_bits[2][NW];
+  __shared__ float s_red[2][NW], s_slab[2];
   __shared__ float s_head_amax;          // read by the other heads of the cluster
   constexpr float kQmax = I8 ? 127.0f : 448.0f;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int c = tid % kRowUnits, g = tid / kRowUnits;              // dims 8c.., tokens 4g..
   const int h = blockIdx.x % p.Hkv, Hkv = p.Hkv;                   // the cluster's rank
   const int li = blockIdx.y, layer = p.layer0 + li;
 
   // the runs that start in this cluster's chunk (each head finds the same)
-  const int c0 = (int)(blockIdx.x / p.Hkv) * p.chunk, nc = min(p.chunk, p.T - c0);
-  for (int i = tid; i < nc; i += kThreads) {
+  const int c0 = (int)(blockIdx.x / p.Hkv) * P, nc = min(P, p.T - c0);
+  for (int i = tid; i < nc; i += NT) {
     const int t = c0 + i;
     const int64_t x = p.pos[t];
     bool start = true;
@@ -151,8 +432,9 @@ __global__ void __launch_bounds__(kThreads) store_page_head_kernel(StorePHParams
     const int pg = (int)(p.pos[t0] / P);
     const size_t lp = (size_t)layer * p.Lp + pg;
     // the page's state, loaded now: its latency overlaps the run's scan
-    const size_t so = (lp * Hkv + h) * kHD + tid;
-    float sum = p.slab_sum[so];
+    const size_t so = (lp * Hkv + h) * kHD;
+    float2 sum = make_float2(0.0f, 0.0f);
+    if (tid < kHD / 2) sum = reinterpret_cast<const float2*>(p.slab_sum + so)[tid];
     const int cnt0 = p.slab_cnt[lp];
     int slot = p.slot_of[lp];
     if (slot >= p.S) {                     // corrupt state: never write through it
@@ -161,179 +443,240 @@ __global__ void __launch_bounds__(kThreads) store_page_head_kernel(StorePHParams
     }
     // run length: consecutive tokens of the same page (at most P)
     if (tid == 0) s_run = P;
-    if (tid < P) s_at[tid] = -1;
     __syncthreads();
-    if (tid < P) {
-      const int t = t0 + tid;
+    bool in_place = true;                  // token r in row r
+    for (int r = tid; r < P; r += NT) {
+      const int t = t0 + r;
       bool ends = t >= p.T;
       if (!ends) {
         const int64_t x = p.pos[t];
         ends = x < 0 || x / P != pg;
-        if (!ends) s_row[tid] = (int)(x % P);
-        if (!ends && tid > 0 && x <= p.pos[t - 1] && h == 0) set_status(p.status, SSA_ST_BAD_POS);
+        if (!ends) {
+          s_row[r] = (int)(x % P);
+          in_place = in_place && x % P == r;
+          if (r > 0 && x <= p.pos[t - 1] && h == 0) set_status(p.status, SSA_ST_BAD_POS);
+        }
       }
-      if (ends) atomicMin(&s_run, tid);
+      if (ends) {
+        atomicMin(&s_run, r);
+        in_place = false;
+      }
     }
-    __syncthreads();
+    const bool full = __syncthreads_and(in_place);     // the run is the whole page
     const int R = s_run;
-    if (tid < R) s_at[s_row[tid]] = tid;
 
-    // the run's rows of this head, into shared memory; their finite maxima
-    float ak = 0.0f, av = 0.0f;
+    // the run's rows of this head, in registers; the largest magnitudes
+    uint4 kr[NU], vr[NU];
+    auto token = [&](int i) { return (i >> 2) * (4 * G) + 4 * g + (i & 3); };
     {
-      const size_t row0 = ((size_t)li * p.T + t0) * Hkv + h;       // token r: row0 + r * Hkv
       const uint4* kg = reinterpret_cast<const uint4*>(p.k);
       const uint4* vg = reinterpret_cast<const uint4*>(p.v);
-      const int n = R * kUnitsPerRow;
-      for (int u0 = tid; u0 < n; u0 += kThreads * kLoads) {
-        uint4 bk[kLoads], bv[kLoads];
+      const size_t row0 = (((size_t)li * p.T + t0) * Hkv + h) * kRowUnits + c;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int u = u0 + i * kThreads;
-          if (u < n) {
-            const size_t g = (row0 + (size_t)(u / kUnitsPerRow) * Hkv) * kUnitsPerRow + u % kUnitsPerRow;
-            bk[i] = kg[g];
-            bv[i] = vg[g];
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int u = u0 + i * kThreads;
-          if (u < n) {
-            reinterpret_cast<uint4*>(kx)[u] = bk[i];
-            reinterpret_cast<uint4*>(vx)[u] = bv[i];
-            ak = fmaxf(ak, finite_absmax(bk[i]));
-            av = fmaxf(av, finite_absmax(bv[i]));
-          }
+      for (int i = 0; i < NU; ++i) {
+        const int r = token(i);
+        kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+        if (r < R) {
+          kr[i] = __ldcs(kg + row0 + (size_t)r * Hkv * kRowUnits);
+          vr[i] = __ldcs(vg + row0 + (size_t)r * Hkv * kRowUnits);
         }
       }
     }
-    ak = warp_max(ak);
-    av = warp_max(av);
-    if (lane == 0) {
-      s_red[0][warp] = ak;
-      s_red[1][warp] = av;
-    }
-    __syncthreads();                       // rows, s_at and the maxima are in place
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      ak = fmaxf(ak, s_red[0][w]);
-      av = fmaxf(av, s_red[1][w]);
-    }
-
-    // K, then V: scale, the codes already there, the new codes
     const size_t pe = (size_t)P * kHD;     // codes of one head of one page
-#pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-      float* sc_m = which ? p.v_scale_m : p.k_scale_m;
-      float* sc_p = which ? p.v_scale : p.k_scale;
-      uint8_t* mir = which ? p.v_mir : p.k_mir;
-      uint8_t* pool = which ? p.v_pool : p.k_pool;
-      const __nv_bfloat16* xs = which ? vx : kx;
-      if (mir) mir += (lp * Hkv + h) * pe;
-      pool = slot >= 0 ? pool + (((size_t)layer * p.S + slot) * Hkv + h) * pe : nullptr;
-      sc_m = sc_m ? sc_m + lp * Hkv + h : nullptr;
-      sc_p = slot >= 0 ? sc_p + ((size_t)layer * p.S + slot) * Hkv + h : nullptr;
-      if (!mir && !pool) continue;         // the page is held nowhere
-      // the pool's copy where there is one (the mirror's bytes are the same)
-      const float need = (which ? av : ak) / kQmax;
-      const float old = cnt0 > 0 ? (sc_p ? *sc_p : *sc_m) : 0.0f;
-      const float s = cnt0 > 0 ? fmaxf(old, need) : need;
-      const bool grow = cnt0 > 0 && s > old;
-      const float ratio = grow ? old / s : 1.0f;
-      __syncthreads();                     // every thread has read the old scale
-      if (tid == 0) {
-        if (sc_m) *sc_m = s;
-        if (sc_p) *sc_p = s;
-      }
-      const uint8_t* from = pool ? pool : mir;
-      if (grow) {                          // the whole block at its new scale
-        for (int u = tid; u < (int)pe / 16; u += kThreads) {
-          uint4 w = reinterpret_cast<const uint4*>(from)[u];
-          uint8_t* b = reinterpret_cast<uint8_t*>(&w);
+    const Block bk(p, false, layer, pg, slot, h, pe), bv(p, true, layer, pg, slot, h, pe);
+    const float old_k = cnt0 > 0 ? bk.scale() : 0.0f, old_v = cnt0 > 0 ? bv.scale() : 0.0f;
+    uint32_t mk = 0, mv = 0;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) b[i] = quant<I8>(value<I8>(b[i]) * ratio);
-          reinterpret_cast<uint4*>(codes)[u] = w;
-        }
-        __syncthreads();
+    for (int i = 0; i < NU; ++i) {
+      mk = absmax_bits(mk, kr[i]);
+      mv = absmax_bits(mv, vr[i]);
+      kx[token(i) * kRowUnits + c] = kr[i];
+    }
+    mk = __reduce_max_sync(0xffffffffu, max(mk >> 16, mk & 0xFFFFu));
+    mv = __reduce_max_sync(0xffffffffu, max(mv >> 16, mv & 0xFFFFu));
+    if (lane == 0) {
+      s_bits[0][warp] = mk;
+      s_bits[1][warp] = mv;
+    }
+    __syncthreads();                       // (every thread has read the old scales)
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      mk = max(mk, s_bits[0][w]);
+      mv = max(mv, s_bits[1][w]);
+    }
+    const bool fin_k = mk < 0x7F80u, fin_v = mv < 0x7F80u;
+    float ak = __uint_as_float(mk << 16), av = __uint_as_float(mv << 16);
+    if (!fin_k || !fin_v) {                // infinities and NaN leave the scale alone
+      ak = av = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        ak = fmaxf(ak, finite_absmax(kr[i]));
+        av = fmaxf(av, finite_absmax(vr[i]));
       }
-      // new codes: K rows [j][D]; V transposed to [D][j]
-      for (int r = 0; r < R; ++r) {
-        const float x = __bfloat162float(xs[r * kHD + tid]);
-        const uint8_t c = s > 0.0f ? quant<I8>(x / s) : 0;
-        codes[which ? tid * P + s_row[r] : s_row[r] * kHD + tid] = c;
+      ak = warp_max(ak);
+      av = warp_max(av);
+      if (lane == 0) {
+        s_red[0][warp] = ak;
+        s_red[1][warp] = av;
       }
       __syncthreads();
-      // out: 16-byte units whose codes are all known, single codes otherwise
-      for (int u = tid; u < (int)pe / 16; u += kThreads) {
-        const uint4 w = reinterpret_cast<const uint4*>(codes)[u];
-        if (!which) {
-          if (grow || s_at[u / (kHD / 16)] >= 0) {
-            if (mir) reinterpret_cast<uint4*>(mir)[u] = w;
-            if (pool) reinterpret_cast<uint4*>(pool)[u] = w;
-          }
-          continue;
-        }
-        const int j0 = u * 16 % P;
-        uint32_t known = 0;
+      for (int w = 0; w < NW; ++w) {
+        ak = fmaxf(ak, s_red[0][w]);
+        av = fmaxf(av, s_red[1][w]);
+      }
+    }
+    const float need_k = ak / kQmax, need_v = av / kQmax;
+    const float sk = cnt0 > 0 ? fmaxf(old_k, need_k) : need_k;
+    const float sv = cnt0 > 0 ? fmaxf(old_v, need_v) : need_v;
+    if (tid == 0) {
+      bk.set_scale(sk);
+      bv.set_scale(sv);
+    }
+    if (!full && cnt0 > 0) {               // a whole page leaves no code of before
+      if (sk > old_k) rescale_block<I8>(bk.mir, bk.pool, (int)pe, old_k / sk, tid, NT);
+      if (sv > old_v) rescale_block<I8>(bv.mir, bv.pool, (int)pe, old_v / sv, tid, NT);
+      __syncthreads();                     // the new codes go on top
+    }
+
+    const Divider dk(sk, fin_k), dv(sv, fin_v);
+    constexpr uint32_t kNeg = 0x80008000u;
+    // K: 8 codes of a row per unit
 #pragma unroll
-        for (int i = 0; i < 16; ++i) known |= (grow || s_at[j0 + i] >= 0 ? 1u : 0u) << i;
-        if (known == 0xFFFFu) {
-          if (mir) reinterpret_cast<uint4*>(mir)[u] = w;
-          if (pool) reinterpret_cast<uint4*>(pool)[u] = w;
+    for (int i = 0; i < NU; ++i) {
+      const int r = token(i);
+      const uint32_t w[4] = {kr[i].x, kr[i].y, kr[i].z, kr[i].w};
+      uint2 out;
+      if (dk.exact) {
+        uint64_t q[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q[k] = dk(lo_f(w[k] ^ kNeg), hi_f(w[k] ^ kNeg));
+        out = make_uint2(codes4<I8>(q[0], q[1]), codes4<I8>(q[2], q[3]));
+      } else {
+        uint8_t* b = reinterpret_cast<uint8_t*>(&out);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          b[k] = sk > 0.0f ? quant<I8>((k & 1 ? hi_f(w[k >> 1]) : lo_f(w[k >> 1])) / sk) : 0;
+      }
+      if (r < R) {
+        const size_t off = (size_t)(full ? r : s_row[r]) * kHD + 8 * c;
+        if (bk.mir) *reinterpret_cast<uint2*>(bk.mir + off) = out;
+        if (bk.pool) *reinterpret_cast<uint2*>(bk.pool + off) = out;
+      }
+    }
+    // V: words of 4 tokens per dimension
+#pragma unroll
+    for (int i = 0; i < NU; i += 4) {
+      const int r = token(i);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        auto word = [&](const uint4& v) { return k < 2 ? v.x : (k < 4 ? v.y : (k < 6 ? v.z : v.w)); };
+        const uint32_t w[4] = {word(vr[i]), word(vr[i + 1]), word(vr[i + 2]), word(vr[i + 3])};
+        uint32_t out;
+        if (dv.exact) {
+          float nx[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) nx[m] = k & 1 ? hi_f(w[m] ^ kNeg) : lo_f(w[m] ^ kNeg);
+          out = codes4<I8>(dv(nx[0], nx[1]), dv(nx[2], nx[3]));
         } else {
-          for (; known; known &= known - 1) {
-            const int i = __ffs(known) - 1;
-            const uint8_t c = codes[u * 16 + i];
-            if (mir) mir[u * 16 + i] = c;
-            if (pool) pool[u * 16 + i] = c;
+          uint8_t* b = reinterpret_cast<uint8_t*>(&out);
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            b[m] = sv > 0.0f ? quant<I8>((k & 1 ? hi_f(w[m]) : lo_f(w[m])) / sv) : 0;
+        }
+        const int d = 8 * c + k;
+        if (full) {
+          // word r / 4 of row d, at a place that spreads the 16 dimension
+          // groups over the banks
+          constexpr int kWords = P / 4;
+          vt[d * kWords + ((r >> 2) ^ (c & (kWords - 1)))] = out;
+        } else {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            if (r + m >= R) continue;
+            const uint8_t b = (uint8_t)(out >> (8 * m));
+            const size_t off = (size_t)d * P + s_row[r + m];
+            if (bv.mir) bv.mir[off] = b;
+            if (bv.pool) bv.pool[off] = b;
           }
         }
       }
-      __syncthreads();                     // codes are rewritten for V, and by the next run
+    }
+    if (full) {
+      __syncthreads();
+      constexpr int kWords = P / 4, kVec = P / 16;       // words, 16-byte units of a row
+      for (int u = tid; u < kHD * kVec; u += NT) {
+        const int d = u / kVec, x = u % kVec, sw = (d >> 3) & (kWords - 1);
+        // the unit's words lie together, in another order
+        const uint4 q = *reinterpret_cast<const uint4*>(vt + d * kWords + ((4 * x) ^ (sw & ~3)));
+        const bool b0 = sw & 1, b1 = sw & 2;
+        const uint2 e = b1 ? make_uint2(q.z, q.w) : make_uint2(q.x, q.y);
+        const uint2 f = b1 ? make_uint2(q.x, q.y) : make_uint2(q.z, q.w);
+        const uint4 out = b0 ? make_uint4(e.y, e.x, f.y, f.x) : make_uint4(e.x, e.y, f.x, f.y);
+        if (bv.mir) reinterpret_cast<uint4*>(bv.mir)[u] = out;
+        if (bv.pool) reinterpret_cast<uint4*>(bv.pool)[u] = out;
+      }
     }
 
-    // the slab: fp32 running sum in token order, the page's row again
-    for (int r = 0; r < R; ++r) sum = sum + __bfloat162float(kx[r * kHD + tid]);
-    p.slab_sum[so] = sum;
+    // the slab: fp32 running sums in token order, two dimensions per thread
     const int cnt = cnt0 + R;
-    const float mean = sum / (float)cnt;
-    float a = warp_max(fabsf(mean));
-    if (lane == 0) s_red[0][warp] = a;
-    __syncthreads();
-    if (tid == 0) {
-      a = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) a = fmaxf(a, s_red[0][w]);
-      s_head_amax = a;
+    float2 mean = make_float2(0.0f, 0.0f);
+    float a = 0.0f;
+    if (tid < kHD / 2) {
+      const uint32_t* col = reinterpret_cast<const uint32_t*>(kx) + tid;
+#pragma unroll 8
+      for (int r = 0; r < R; ++r) {
+        const uint32_t w = col[r * (kHD / 2)];
+        sum.x = sum.x + lo_f(w);
+        sum.y = sum.y + hi_f(w);
+      }
+      reinterpret_cast<float2*>(p.slab_sum + so)[tid] = sum;
+      mean = make_float2(sum.x / (float)cnt, sum.y / (float)cnt);
+      a = warp_max(fmaxf(fabsf(mean.x), fabsf(mean.y)));
+      if (lane == 0) s_slab[warp] = a;
     }
+    __syncthreads();
+    if (tid == 0) s_head_amax = fmaxf(s_slab[0], s_slab[1]);
     cluster_sync();
     float amax = 0.0f;
     for (int r = 0; r < Hkv; ++r) amax = fmaxf(amax, cluster_read(&s_head_amax, r));
     cluster_sync();                        // read before it is rewritten, or the CTA ends
     const float s = amax / 127.0f;
-    int c = 0;
-    if (amax > 0.0f) c = (int)fminf(fmaxf(rintf(mean / s), -127.0f), 127.0f);
-    p.slab[so] = (int8_t)c;
+    if (tid < kHD / 2) {
+      auto code = [&](float m) -> int {
+        return amax > 0.0f ? (int)fminf(fmaxf(rintf(m / s), -127.0f), 127.0f) : 0;
+      };
+      reinterpret_cast<char2*>(p.slab + so)[tid] =
+          make_char2((signed char)code(mean.x), (signed char)code(mean.y));
+    }
     if (tid == 0 && h == 0) {              // every head has read the count by now
       p.slab_cnt[lp] = cnt;
       p.slab_scale[lp] = s;
     }
-    __syncthreads();                       // s_row, s_at, s_run, the rows: the next run's
+    __syncthreads();                       // s_row, s_run, the tiles: the next run's
   }
 }
 
+// Calls of at least this many tokens take the prefill kernel.
+constexpr int kPrefillTokens = 4096;
+
 template <bool I8, int P>
 cudaError_t launch_t(const StorePHParams& p, int n_layers, cudaStream_t s) {
-  const size_t smem = smem_bytes(P);
-  cudaError_t e = cudaFuncSetAttribute(store_page_head_kernel<I8, P>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e;
+  if (p.T < kPrefillTokens) {
+    e = launch_pdl(append_page_head_kernel<I8, P>, dim3((unsigned)p.T, (unsigned)n_layers),
+                   dim3((unsigned)(p.Hkv * kHD)), 0, s, p);
+    count_launch();
+    return e;
+  }
+  const size_t smem = prefill_smem(P);
+  e = cudaFuncSetAttribute(prefill_page_head_kernel<I8, P>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const long long nchunk = (p.T + (long long)p.chunk - 1) / p.chunk;
+  const long long nchunk = (p.T + (long long)P - 1) / P;
   if (nchunk * p.Hkv > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(nchunk * p.Hkv), (unsigned)n_layers);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(prefill_threads(P));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -345,7 +688,7 @@ cudaError_t launch_t(const StorePHParams& p, int n_layers, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, store_page_head_kernel<I8, P>, p);
+  e = cudaLaunchKernelEx(&cfg, prefill_page_head_kernel<I8, P>, p);
   count_launch();
   return e;
 }
@@ -387,7 +730,6 @@ cudaError_t launch_store_page_head(const Dims& d, const ssa_cache& c, int layer0
   p.pos = pos;
   p.status = status;
   p.T = T;
-  p.chunk = T >= 4096 ? d.P : 1;
   p.layer0 = layer0; p.Lp = d.Lp; p.S = d.S; p.Hkv = d.Hkv;
   return d.kind == SSA_KV_INT8_PAGE_HEAD ? launch_p<true>(p, d.P, n_layers, s)
                                          : launch_p<false>(p, d.P, n_layers, s);
