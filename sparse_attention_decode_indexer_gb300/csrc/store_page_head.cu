@@ -65,9 +65,11 @@ struct StorePHParams {
   int T, layer0, Lp, S, Hkv;
 };
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // a float of the same shared variable in CTA `rank` of the cluster
@@ -350,31 +352,50 @@ __device__ __forceinline__ uint32_t codes4(uint64_t a, uint64_t b) {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// Bit patterns of 8 |bf16|, maximum so far per 16-bit half (as integers, which
-// orders them; infinities and NaN from 0x7F80 on)
-__device__ __forceinline__ uint32_t absmax_bits(uint32_t m, uint4 v) {
-  m = __vmaxu2(m, v.x & 0x7FFF7FFFu);
-  m = __vmaxu2(m, v.y & 0x7FFF7FFFu);
-  m = __vmaxu2(m, v.z & 0x7FFF7FFFu);
-  return __vmaxu2(m, v.w & 0x7FFF7FFFu);
+// Largest |bf16| so far per half, NaN if there is one (so: bits from 0x7F80 on
+// where a value is not finite)
+__device__ __forceinline__ void absmax(__nv_bfloat162& m, uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
 }
 
-__device__ __forceinline__ float finite_absmax(uint4 v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float m = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = (w[i] << 16) & 0x7FFF0000u, hi = w[i] & 0x7FFF0000u;
-    if (lo < 0x7F800000u) m = fmaxf(m, __uint_as_float(lo));
-    if (hi < 0x7F800000u) m = fmaxf(m, __uint_as_float(hi));
+__device__ __forceinline__ uint32_t max_bits(__nv_bfloat162 m) {
+  const uint32_t w = *reinterpret_cast<uint32_t*>(&m);
+  return __reduce_max_sync(0xffffffffu, max(w >> 16, w & 0xFFFFu));
+}
+
+// A run's codes one by one, by plain division: scales outside the Divider's
+// range, and blocks with values that are not finite.  x: the run's first row
+// of this head, rows HD apart.
+template <bool I8, int P>
+__device__ __noinline__ void store_plain(const __nv_bfloat16* x, int HD, int R, const int* s_row,
+                                         float s, bool v, uint8_t* mir, uint8_t* pool,
+                                         int nthreads) {
+  for (int e = threadIdx.x; e < R * kHD; e += nthreads) {
+    const int r = e / kHD, d = e % kHD, j = s_row[r];
+    const uint8_t c = s > 0.0f ? quant<I8>(__bfloat162float(x[(size_t)r * HD + d]) / s) : 0;
+    const int off = v ? d * P + j : j * kHD + d;
+    if (mir) mir[off] = c;
+    if (pool) pool[off] = c;
   }
-  return m;
+}
+
+// The largest finite magnitude of a run's rows of one head (a thread's share).
+__device__ __noinline__ float finite_max(const __nv_bfloat16* x, int HD, int R, int nthreads) {
+  float m = 0.0f;
+  for (int e = threadIdx.x; e < R * kHD; e += nthreads) {
+    const float a = fabsf(__bfloat162float(x[(size_t)(e / kHD) * HD + e % kHD]));
+    if (a < INFINITY) m = fmaxf(m, a);
+  }
+  return warp_max(m);
 }
 
 // Threads of a CTA and 16-byte units of K (and of V) a thread holds: 4 tokens
 // at a time, at most 8 units.
-constexpr int prefill_threads(int P) { return P == 16 ? 64 : (P == 128 ? 256 : 128); }
-constexpr int prefill_units(int P) { return P * kRowUnits / prefill_threads(P); }
+constexpr int prefill_threads(int P) { return P == 128 ? 256 : 128; }
+constexpr int prefill_units(int P) { return P <= 32 ? 4 : 8; }
 // dynamic shared memory: K rows as they came (for the slab's sums) and V's
 // codes on their way out
 inline size_t prefill_smem(int P) { return (size_t)P * kHD * 3; }
@@ -387,78 +408,75 @@ prefill_page_head_kernel(StorePHParams p) {
   extern __shared__ __align__(16) uint8_t dsm[];
   uint4* kx = reinterpret_cast<uint4*>(dsm);                       // [r][16 units]
   uint32_t* vt = reinterpret_cast<uint32_t*>(dsm + P * kHD * 2);   // [d][P / 4 words], swizzled
-  __shared__ int s_start[P];
+  __shared__ int64_t s_pos[2 * P];       // positions of the chunk and of the run it may end in
+  __shared__ uint32_t s_start[(P + 31) / 32];
   __shared__ int s_row[P];               // the run's tokens' rows j, ascending
-  __shared__ int s_nstart, s_run;
+  __shared__ int s_run;
   __shared__ uint32_t s_bits[2][NW];
-  __shared__ float s_red[2][NW], s_slab[2];
+  __shared__ float s_red[2][NW], s_slab[4];
   __shared__ float s_head_amax;          // read by the other heads of the cluster
   constexpr float kQmax = I8 ? 127.0f : 448.0f;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c = tid % kRowUnits, g = tid / kRowUnits;              // dims 8c.., tokens 4g..
-  const int h = blockIdx.x % p.Hkv, Hkv = p.Hkv;                   // the cluster's rank
+  const int h = blockIdx.x % p.Hkv, Hkv = p.Hkv, HD = Hkv * kHD;   // h: the cluster's rank
   const int li = blockIdx.y, layer = p.layer0 + li;
 
-  // the runs that start in this cluster's chunk (each head finds the same)
+  // the chunk's positions, and the runs that start in it (each head finds the same)
   const int c0 = (int)(blockIdx.x / p.Hkv) * P, nc = min(P, p.T - c0);
-  for (int i = tid; i < nc; i += NT) {
-    const int t = c0 + i;
-    const int64_t x = p.pos[t];
-    bool start = true;
-    if (x < 0 || x / P >= p.Lp) {
-      if (h == 0) set_status(p.status, SSA_ST_BAD_ID);
-      start = false;
-    } else if (t > 0) {
-      const int64_t prev = p.pos[t - 1];
-      if (prev >= x && h == 0) set_status(p.status, SSA_ST_BAD_POS);
-      if (prev >= 0 && prev / P == x / P) start = false;           // inside a run
+  const int64_t before = c0 > 0 ? p.pos[c0 - 1] : -1;
+#pragma unroll
+  for (int i = tid; i < 2 * P; i += NT)
+    if (c0 + i < p.T) s_pos[i] = p.pos[c0 + i];
+  __syncthreads();
+  if (tid < (P + 31) / 32 * 32) {
+    bool start = false;
+    if (tid < nc) {
+      const int64_t x = s_pos[tid], prev = tid > 0 ? s_pos[tid - 1] : before;
+      start = x >= 0 && x / P < p.Lp;
+      if (!start && h == 0) set_status(p.status, SSA_ST_BAD_ID);
+      if (start && c0 + tid > 0) {
+        if (prev >= x && h == 0) set_status(p.status, SSA_ST_BAD_POS);
+        if (prev >= 0 && prev / P == x / P) start = false;         // inside a run
+      }
     }
-    s_start[i] = start ? t : -1;
+    const uint32_t m = __ballot_sync(0xffffffffu, start);
+    if (lane == 0) s_start[warp] = m;
   }
   __syncthreads();
-  if (tid == 0) {
-    int n = 0;
-    for (int i = 0; i < nc; ++i)
-      if (s_start[i] >= 0) s_start[n++] = s_start[i];
-    s_nstart = n;
-  }
-  __syncthreads();
-  const int nstart = s_nstart;
 
-  for (int ri = 0; ri < nstart; ++ri) {
-    const int t0 = s_start[ri];
-    const int pg = (int)(p.pos[t0] / P);
+#pragma unroll 1
+  for (int at = 0; at < P; ++at) {
+    const uint32_t ahead = s_start[at >> 5] >> (at & 31);
+    if (!ahead) { at |= 31; continue; }
+    at += __ffs(ahead) - 1;
+    const int t0 = c0 + at;
+    const int64_t page = s_pos[at] / P;
+    const int pg = (int)page;
     const size_t lp = (size_t)layer * p.Lp + pg;
     // the page's state, loaded now: its latency overlaps the run's scan
-    const size_t so = (lp * Hkv + h) * kHD;
-    float2 sum = make_float2(0.0f, 0.0f);
-    if (tid < kHD / 2) sum = reinterpret_cast<const float2*>(p.slab_sum + so)[tid];
+    const size_t so = (lp * Hkv + h) * kHD + tid;
+    float sum = tid < kHD ? p.slab_sum[so] : 0.0f;
     const int cnt0 = p.slab_cnt[lp];
     int slot = p.slot_of[lp];
-    if (slot >= p.S) {                     // corrupt state: never write through it
-      if (tid == 0 && h == 0) set_status(p.status, SSA_ST_BAD_ID);
-      slot = -1;
-    }
     // run length: consecutive tokens of the same page (at most P)
     if (tid == 0) s_run = P;
     __syncthreads();
     bool in_place = true;                  // token r in row r
-    for (int r = tid; r < P; r += NT) {
-      const int t = t0 + r;
-      bool ends = t >= p.T;
+    if (tid < P) {
+      bool ends = t0 + tid >= p.T;
       if (!ends) {
-        const int64_t x = p.pos[t];
-        ends = x < 0 || x / P != pg;
+        const int64_t x = s_pos[at + tid];
+        ends = x < 0 || x / P != page;
         if (!ends) {
-          s_row[r] = (int)(x % P);
-          in_place = in_place && x % P == r;
-          if (r > 0 && x <= p.pos[t - 1] && h == 0) set_status(p.status, SSA_ST_BAD_POS);
+          s_row[tid] = (int)(x % P);
+          in_place = x % P == tid;
+          if (tid > 0 && x <= s_pos[at + tid - 1] && h == 0) set_status(p.status, SSA_ST_BAD_POS);
         }
       }
       if (ends) {
-        atomicMin(&s_run, r);
+        atomicMin(&s_run, tid);
         in_place = false;
       }
     }
@@ -468,63 +486,77 @@ prefill_page_head_kernel(StorePHParams p) {
     // the run's rows of this head, in registers; the largest magnitudes
     uint4 kr[NU], vr[NU];
     auto token = [&](int i) { return (i >> 2) * (4 * G) + 4 * g + (i & 3); };
+    const size_t row0 = ((size_t)li * p.T + t0) * HD + h * kHD;
     {
-      const uint4* kg = reinterpret_cast<const uint4*>(p.k);
-      const uint4* vg = reinterpret_cast<const uint4*>(p.v);
-      const size_t row0 = (((size_t)li * p.T + t0) * Hkv + h) * kRowUnits + c;
+      const uint4* kg = reinterpret_cast<const uint4*>(p.k + row0) + c;
+      const uint4* vg = reinterpret_cast<const uint4*>(p.v + row0) + c;
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         const int r = token(i);
         kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
         if (r < R) {
-          kr[i] = __ldcs(kg + row0 + (size_t)r * Hkv * kRowUnits);
-          vr[i] = __ldcs(vg + row0 + (size_t)r * Hkv * kRowUnits);
+          kr[i] = __ldcs(kg + r * (HD / 8));
+          vr[i] = __ldcs(vg + r * (HD / 8));
         }
       }
     }
-    const size_t pe = (size_t)P * kHD;     // codes of one head of one page
+    if (slot >= p.S) {                     // corrupt state: never write through it
+      if (tid == 0 && h == 0) set_status(p.status, SSA_ST_BAD_ID);
+      slot = -1;
+    }
+    constexpr int pe = P * kHD;            // codes of one head of one page
     const Block bk(p, false, layer, pg, slot, h, pe), bv(p, true, layer, pg, slot, h, pe);
     const float old_k = cnt0 > 0 ? bk.scale() : 0.0f, old_v = cnt0 > 0 ? bv.scale() : 0.0f;
-    uint32_t mk = 0, mv = 0;
+    __nv_bfloat162 mk2 = __floats2bfloat162_rn(0.0f, 0.0f), mv2 = mk2;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      mk = absmax_bits(mk, kr[i]);
-      mv = absmax_bits(mv, vr[i]);
-      kx[token(i) * kRowUnits + c] = kr[i];
+      if (token(i) < P) kx[token(i) * kRowUnits + c] = kr[i];
+      absmax(mk2, kr[i]);
+      absmax(mv2, vr[i]);
     }
-    mk = __reduce_max_sync(0xffffffffu, max(mk >> 16, mk & 0xFFFFu));
-    mv = __reduce_max_sync(0xffffffffu, max(mv >> 16, mv & 0xFFFFu));
+    uint32_t mk = max_bits(mk2), mv = max_bits(mv2);
     if (lane == 0) {
       s_bits[0][warp] = mk;
       s_bits[1][warp] = mv;
     }
     __syncthreads();                       // (every thread has read the old scales)
+
+    // the slab: fp32 running sums in token order; the heads' maxima meet while
+    // the codes are made
+    const int cnt = cnt0 + R;
+    float mean = 0.0f;
+    if (tid < kHD) {
+      const __nv_bfloat16* col = reinterpret_cast<const __nv_bfloat16*>(kx) + tid;
+#pragma unroll 16
+      for (int r = 0; r < R; ++r) sum = sum + __bfloat162float(col[r * kHD]);
+      p.slab_sum[so] = sum;
+      mean = sum / (float)cnt;
+      const float a = warp_max(fabsf(mean));
+      if (lane == 0) s_slab[warp] = a;
+    }
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       mk = max(mk, s_bits[0][w]);
       mv = max(mv, s_bits[1][w]);
     }
-    const bool fin_k = mk < 0x7F80u, fin_v = mv < 0x7F80u;
+    const bool finite = mk < 0x7F80u && mv < 0x7F80u;
     float ak = __uint_as_float(mk << 16), av = __uint_as_float(mv << 16);
-    if (!fin_k || !fin_v) {                // infinities and NaN leave the scale alone
-      ak = av = 0.0f;
-#pragma unroll
-      for (int i = 0; i < NU; ++i) {
-        ak = fmaxf(ak, finite_absmax(kr[i]));
-        av = fmaxf(av, finite_absmax(vr[i]));
-      }
-      ak = warp_max(ak);
-      av = warp_max(av);
+    if (!finite) {                         // infinities and NaN leave the scale alone
+      ak = finite_max(p.k + row0, HD, R, NT);
+      av = finite_max(p.v + row0, HD, R, NT);
       if (lane == 0) {
         s_red[0][warp] = ak;
         s_red[1][warp] = av;
       }
-      __syncthreads();
+    }
+    __syncthreads();                       // s_slab, s_red
+    if (tid == 0) s_head_amax = fmaxf(fmaxf(s_slab[0], s_slab[1]), fmaxf(s_slab[2], s_slab[3]));
+    cluster_arrive();
+    if (!finite)
       for (int w = 0; w < NW; ++w) {
         ak = fmaxf(ak, s_red[0][w]);
         av = fmaxf(av, s_red[1][w]);
       }
-    }
     const float need_k = ak / kQmax, need_v = av / kQmax;
     const float sk = cnt0 > 0 ? fmaxf(old_k, need_k) : need_k;
     const float sv = cnt0 > 0 ? fmaxf(old_v, need_v) : need_v;
@@ -533,126 +565,105 @@ prefill_page_head_kernel(StorePHParams p) {
       bv.set_scale(sv);
     }
     if (!full && cnt0 > 0) {               // a whole page leaves no code of before
-      if (sk > old_k) rescale_block<I8>(bk.mir, bk.pool, (int)pe, old_k / sk, tid, NT);
-      if (sv > old_v) rescale_block<I8>(bv.mir, bv.pool, (int)pe, old_v / sv, tid, NT);
+      if (sk > old_k) rescale_block<I8>(bk.mir, bk.pool, pe, old_k / sk, tid, NT);
+      if (sv > old_v) rescale_block<I8>(bv.mir, bv.pool, pe, old_v / sv, tid, NT);
       __syncthreads();                     // the new codes go on top
     }
 
-    const Divider dk(sk, fin_k), dv(sv, fin_v);
     constexpr uint32_t kNeg = 0x80008000u;
+    const Divider dk(sk, finite), dv(sv, finite);
     // K: 8 codes of a row per unit
+    if (dk.exact) {
+      uint2 out[NU];
 #pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      const int r = token(i);
-      const uint32_t w[4] = {kr[i].x, kr[i].y, kr[i].z, kr[i].w};
-      uint2 out;
-      if (dk.exact) {
+      for (int i = 0; i < NU; ++i) {
+        const uint32_t w[4] = {kr[i].x ^ kNeg, kr[i].y ^ kNeg, kr[i].z ^ kNeg, kr[i].w ^ kNeg};
         uint64_t q[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) q[k] = dk(lo_f(w[k] ^ kNeg), hi_f(w[k] ^ kNeg));
-        out = make_uint2(codes4<I8>(q[0], q[1]), codes4<I8>(q[2], q[3]));
-      } else {
-        uint8_t* b = reinterpret_cast<uint8_t*>(&out);
+        for (int k = 0; k < 4; ++k) q[k] = dk(lo_f(w[k]), hi_f(w[k]));
+        out[i] = make_uint2(codes4<I8>(q[0], q[1]), codes4<I8>(q[2], q[3]));
+      }
+      auto put = [&](uint8_t* to) {
+        if (!to) return;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          b[k] = sk > 0.0f ? quant<I8>((k & 1 ? hi_f(w[k >> 1]) : lo_f(w[k >> 1])) / sk) : 0;
-      }
-      if (r < R) {
-        const size_t off = (size_t)(full ? r : s_row[r]) * kHD + 8 * c;
-        if (bk.mir) *reinterpret_cast<uint2*>(bk.mir + off) = out;
-        if (bk.pool) *reinterpret_cast<uint2*>(bk.pool + off) = out;
-      }
+        for (int i = 0; i < NU; ++i) {
+          const int r = token(i);
+          if (r < R) *reinterpret_cast<uint2*>(to + (full ? r : s_row[r]) * kHD + 8 * c) = out[i];
+        }
+      };
+      put(bk.mir);
+      put(bk.pool);
+    } else {
+      store_plain<I8, P>(p.k + row0, HD, R, s_row, sk, false, bk.mir, bk.pool, NT);
     }
     // V: words of 4 tokens per dimension
+    if (dv.exact) {
 #pragma unroll
-    for (int i = 0; i < NU; i += 4) {
-      const int r = token(i);
+      for (int i = 0; i < NU; i += 4) {
+        const int r = token(i);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        auto word = [&](const uint4& v) { return k < 2 ? v.x : (k < 4 ? v.y : (k < 6 ? v.z : v.w)); };
-        const uint32_t w[4] = {word(vr[i]), word(vr[i + 1]), word(vr[i + 2]), word(vr[i + 3])};
-        uint32_t out;
-        if (dv.exact) {
-          float nx[4];
+        for (int k = 0; k < 8; k += 2) {
+          auto word = [&](const uint4& v) {
+            return (k < 2 ? v.x : (k < 4 ? v.y : (k < 6 ? v.z : v.w))) ^ kNeg;
+          };
+          const uint32_t w[4] = {word(vr[i]), word(vr[i + 1]), word(vr[i + 2]), word(vr[i + 3])};
+          const uint32_t o[2] = {
+              codes4<I8>(dv(lo_f(w[0]), lo_f(w[1])), dv(lo_f(w[2]), lo_f(w[3]))),
+              codes4<I8>(dv(hi_f(w[0]), hi_f(w[1])), dv(hi_f(w[2]), hi_f(w[3])))};
 #pragma unroll
-          for (int m = 0; m < 4; ++m) nx[m] = k & 1 ? hi_f(w[m] ^ kNeg) : lo_f(w[m] ^ kNeg);
-          out = codes4<I8>(dv(nx[0], nx[1]), dv(nx[2], nx[3]));
-        } else {
-          uint8_t* b = reinterpret_cast<uint8_t*>(&out);
-#pragma unroll
-          for (int m = 0; m < 4; ++m)
-            b[m] = sv > 0.0f ? quant<I8>((k & 1 ? hi_f(w[m]) : lo_f(w[m])) / sv) : 0;
-        }
-        const int d = 8 * c + k;
-        if (full) {
-          // word r / 4 of row d, at a place that spreads the 16 dimension
-          // groups over the banks
-          constexpr int kWords = P / 4;
-          vt[d * kWords + ((r >> 2) ^ (c & (kWords - 1)))] = out;
-        } else {
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            if (r + m >= R) continue;
-            const uint8_t b = (uint8_t)(out >> (8 * m));
-            const size_t off = (size_t)d * P + s_row[r + m];
-            if (bv.mir) bv.mir[off] = b;
-            if (bv.pool) bv.pool[off] = b;
+          for (int e = 0; e < 2; ++e) {
+            const int d = 8 * c + k + e;
+            if (full) {
+              // word r / 4 of row d, at a place that spreads the 16 dimension
+              // groups over the banks
+              constexpr int kWords = P / 4;
+              if (r < P) vt[d * kWords + ((r >> 2) ^ (c & (kWords - 1)))] = o[e];
+            } else {
+#pragma unroll 1
+              for (int m = 0; m < 4 && r + m < R; ++m) {
+                const uint8_t b = (uint8_t)(o[e] >> (8 * m));
+                const int off = d * P + s_row[r + m];
+                if (bv.mir) bv.mir[off] = b;
+                if (bv.pool) bv.pool[off] = b;
+              }
+            }
           }
         }
       }
-    }
-    if (full) {
-      __syncthreads();
-      constexpr int kWords = P / 4, kVec = P / 16;       // words, 16-byte units of a row
-      for (int u = tid; u < kHD * kVec; u += NT) {
-        const int d = u / kVec, x = u % kVec, sw = (d >> 3) & (kWords - 1);
-        // the unit's words lie together, in another order
-        const uint4 q = *reinterpret_cast<const uint4*>(vt + d * kWords + ((4 * x) ^ (sw & ~3)));
-        const bool b0 = sw & 1, b1 = sw & 2;
-        const uint2 e = b1 ? make_uint2(q.z, q.w) : make_uint2(q.x, q.y);
-        const uint2 f = b1 ? make_uint2(q.x, q.y) : make_uint2(q.z, q.w);
-        const uint4 out = b0 ? make_uint4(e.y, e.x, f.y, f.x) : make_uint4(e.x, e.y, f.x, f.y);
-        if (bv.mir) reinterpret_cast<uint4*>(bv.mir)[u] = out;
-        if (bv.pool) reinterpret_cast<uint4*>(bv.pool)[u] = out;
+      if (full) {
+        __syncthreads();
+        constexpr int kWords = P / 4, kVec = P / 16;     // words, 16-byte units of a row
+#pragma unroll
+        for (int u0 = 0; u0 < kHD * kVec; u0 += NT) {
+          const int u = u0 + tid;
+          const int d = u / kVec, x = u % kVec, sw = (d >> 3) & (kWords - 1);
+          // the unit's words lie together, in another order
+          const uint4 q = *reinterpret_cast<const uint4*>(vt + d * kWords + ((4 * x) ^ (sw & ~3)));
+          const bool b0 = sw & 1, b1 = sw & 2;
+          const uint2 e = b1 ? make_uint2(q.z, q.w) : make_uint2(q.x, q.y);
+          const uint2 f = b1 ? make_uint2(q.x, q.y) : make_uint2(q.z, q.w);
+          const uint4 out = b0 ? make_uint4(e.y, e.x, f.y, f.x) : make_uint4(e.x, e.y, f.x, f.y);
+          if (bv.mir) reinterpret_cast<uint4*>(bv.mir)[u] = out;
+          if (bv.pool) reinterpret_cast<uint4*>(bv.pool)[u] = out;
+        }
       }
+    } else {
+      store_plain<I8, P>(p.v + row0, HD, R, s_row, sv, true, bv.mir, bv.pool, NT);
     }
 
-    // the slab: fp32 running sums in token order, two dimensions per thread
-    const int cnt = cnt0 + R;
-    float2 mean = make_float2(0.0f, 0.0f);
-    float a = 0.0f;
-    if (tid < kHD / 2) {
-      const uint32_t* col = reinterpret_cast<const uint32_t*>(kx) + tid;
-#pragma unroll 8
-      for (int r = 0; r < R; ++r) {
-        const uint32_t w = col[r * (kHD / 2)];
-        sum.x = sum.x + lo_f(w);
-        sum.y = sum.y + hi_f(w);
-      }
-      reinterpret_cast<float2*>(p.slab_sum + so)[tid] = sum;
-      mean = make_float2(sum.x / (float)cnt, sum.y / (float)cnt);
-      a = warp_max(fmaxf(fabsf(mean.x), fabsf(mean.y)));
-      if (lane == 0) s_slab[warp] = a;
-    }
-    __syncthreads();
-    if (tid == 0) s_head_amax = fmaxf(s_slab[0], s_slab[1]);
-    cluster_sync();
+    // the page's slab row, now that every head's maximum is there
+    cluster_wait();
     float amax = 0.0f;
     for (int r = 0; r < Hkv; ++r) amax = fmaxf(amax, cluster_read(&s_head_amax, r));
-    cluster_sync();                        // read before it is rewritten, or the CTA ends
+    cluster_arrive();
     const float s = amax / 127.0f;
-    if (tid < kHD / 2) {
-      auto code = [&](float m) -> int {
-        return amax > 0.0f ? (int)fminf(fmaxf(rintf(m / s), -127.0f), 127.0f) : 0;
-      };
-      reinterpret_cast<char2*>(p.slab + so)[tid] =
-          make_char2((signed char)code(mean.x), (signed char)code(mean.y));
-    }
+    if (tid < kHD)
+      p.slab[so] = (int8_t)(amax > 0.0f ? (int)fminf(fmaxf(rintf(mean / s), -127.0f), 127.0f) : 0);
     if (tid == 0 && h == 0) {              // every head has read the count by now
       p.slab_cnt[lp] = cnt;
       p.slab_scale[lp] = s;
     }
-    __syncthreads();                       // s_row, s_run, the tiles: the next run's
+    cluster_wait();                        // all have read s_head_amax; (the tiles may go)
   }
 }
 
