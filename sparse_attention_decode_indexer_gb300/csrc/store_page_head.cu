@@ -65,20 +65,14 @@ struct StorePHParams {
   int T, layer0, Lp, S, Hkv;
 };
 
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// a float of the same shared variable in CTA `rank` of the cluster
-__device__ __forceinline__ float cluster_read(const float* p, int rank) {
-  uint32_t a;
-  float v;
+// A 4-byte word into the same shared variable of CTA `rank` of the cluster,
+// counted by that CTA's barrier.
+__device__ __forceinline__ void push_f32(const float* p, uint64_t* bar, int rank, float v) {
+  uint32_t a, m;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(m) : "r"(smem_u32(bar)), "r"(rank));
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];"
+               ::"r"(a), "r"(__float_as_uint(v)), "r"(m) : "memory");
 }
 
 template <bool I8>
@@ -114,26 +108,127 @@ __device__ __forceinline__ void rescale_block(uint8_t* mir, uint8_t* pool, int b
   }
 }
 
-// One tensor's block of one page and head: where it is held, and its scale.
+// Where one page's block of one head is held: block number in the mirror and
+// in the pool, -1 where it is not (K's and V's blocks and scales are alike).
 struct Block {
-  uint8_t *mir, *pool;
-  float *sc_m, *sc_p;
-  __device__ __forceinline__ Block(const StorePHParams& p, bool v, int layer, int pg, int slot,
-                                   int h, size_t pe) {
-    const size_t m = ((size_t)layer * p.Lp + pg) * p.Hkv + h;
-    const size_t s = ((size_t)layer * p.S + (slot < 0 ? 0 : slot)) * p.Hkv + h;
-    mir = v ? p.v_mir : p.k_mir;
-    sc_m = v ? p.v_scale_m : p.k_scale_m;
-    if (mir) { mir += m * pe; sc_m += m; }
-    pool = slot >= 0 ? (v ? p.v_pool : p.k_pool) + s * pe : nullptr;
-    sc_p = slot >= 0 ? (v ? p.v_scale : p.k_scale) + s : nullptr;
+  long long m, s;
+  __device__ __forceinline__ Block(const StorePHParams& p, int layer, int pg, int slot, int h) {
+    m = p.k_mir ? ((long long)layer * p.Lp + pg) * p.Hkv + h : -1;
+    s = slot >= 0 ? ((long long)layer * p.S + slot) * p.Hkv + h : -1;
   }
-  __device__ __forceinline__ float scale() const { return sc_p ? *sc_p : (mir ? *sc_m : 0.0f); }
-  __device__ __forceinline__ void set_scale(float s) const {
-    if (mir) *sc_m = s;
-    if (sc_p) *sc_p = s;
+  // the scale, from the pool where it is there (the mirror's is the same)
+  __device__ __forceinline__ float scale(const float* mir, const float* pool) const {
+    return s >= 0 ? pool[s] : (m >= 0 ? mir[m] : 0.0f);
+  }
+  __device__ __forceinline__ void set_scale(float* mir, float* pool, float v) const {
+    if (m >= 0) mir[m] = v;
+    if (s >= 0) pool[s] = v;
+  }
+  __device__ __forceinline__ uint8_t* mirror(uint8_t* base, int pe) const {
+    return m >= 0 ? base + m * pe : nullptr;
+  }
+  __device__ __forceinline__ uint8_t* slot(uint8_t* base, int pe) const {
+    return s >= 0 ? base + s * pe : nullptr;
   }
 };
+
+// Stores a run with a thread per dimension, whatever its tokens and values;
+// 128 threads per head, every thread of the CTA calls it (`active`: those with
+// a column).  kin, vin: the column's first token, rows HD apart; k0, v0: that
+// token's values.  Returns the column's slab sum, `sum` on entry.  Scratch:
+// s_max [2][warps], s_code [threads].
+template <bool I8, int P>
+__device__ __forceinline__ float store_columns(const StorePHParams& p, const Block& blk, bool active,
+                                               int d, const __nv_bfloat16* kin,
+                                               const __nv_bfloat16* vin, __nv_bfloat16 k0,
+                                               __nv_bfloat16 v0, int HD, int R, const int* s_row,
+                                               int cnt0, float sum, float (*s_max)[32],
+                                               uint8_t* s_code) {
+  constexpr float kQmax = I8 ? 127.0f : 448.0f;
+  constexpr int pe = P * kHD;              // codes of one head of one page
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float old_k = cnt0 > 0 ? blk.scale(p.k_scale_m, p.k_scale) : 0.0f;
+  const float old_v = cnt0 > 0 ? blk.scale(p.v_scale_m, p.v_scale) : 0.0f;
+  // finite maxima of the run
+  float ak = 0.0f, av = 0.0f;
+  auto take = [](float& m, __nv_bfloat16 x) {
+    const float a = fabsf(__bfloat162float(x));
+    if (a < INFINITY) m = fmaxf(m, a);
+  };
+  if (active) {
+    take(ak, k0);
+    take(av, v0);
+    for (int r0 = 1; r0 < R; r0 += kTokBatch) {
+      __nv_bfloat16 xk[kTokBatch], xv[kTokBatch];
+#pragma unroll
+      for (int i = 0; i < kTokBatch; ++i)
+        if (r0 + i < R) {
+          xk[i] = kin[(size_t)(r0 + i) * HD];
+          xv[i] = vin[(size_t)(r0 + i) * HD];
+        }
+#pragma unroll
+      for (int i = 0; i < kTokBatch; ++i)
+        if (r0 + i < R) {
+          take(ak, xk[i]);
+          take(av, xv[i]);
+        }
+    }
+  }
+  ak = warp_max(ak);
+  av = warp_max(av);
+  if (lane == 0) {
+    s_max[0][warp] = ak;
+    s_max[1][warp] = av;
+  }
+  __syncthreads();                         // (every thread has read the old scales)
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    ak = fmaxf(ak, s_max[0][(warp & ~3) + w]);
+    av = fmaxf(av, s_max[1][(warp & ~3) + w]);
+  }
+  const float need_k = ak / kQmax, need_v = av / kQmax;
+  const float sk = cnt0 > 0 ? fmaxf(old_k, need_k) : need_k;
+  const float sv = cnt0 > 0 ? fmaxf(old_v, need_v) : need_v;
+  uint8_t *km = blk.mirror(p.k_mir, pe), *kp = blk.slot(p.k_pool, pe);
+  uint8_t *vm = blk.mirror(p.v_mir, pe), *vp = blk.slot(p.v_pool, pe);
+  if (active) {
+    if (d == 0) {
+      blk.set_scale(p.k_scale_m, p.k_scale, sk);
+      blk.set_scale(p.v_scale_m, p.v_scale, sv);
+    }
+    if (km || kp) {
+      if (cnt0 > 0 && sk > old_k) rescale_block<I8>(km, kp, pe, old_k / sk, d, kHD);
+      if (cnt0 > 0 && sv > old_v) rescale_block<I8>(vm, vp, pe, old_v / sv, d, kHD);
+    }
+  }
+  __syncthreads();                         // the new codes go on top
+  if (!active) return sum;
+  for (int r = 0; r < R; ++r) {
+    const __nv_bfloat16 xk = r == 0 ? k0 : kin[(size_t)r * HD];
+    const __nv_bfloat16 xv = r == 0 ? v0 : vin[(size_t)r * HD];
+    const float fk = __bfloat162float(xk), fv = __bfloat162float(xv);
+    const int j = s_row[r];
+    // K row j: the warp's 32 codes as two 16-byte stores
+    s_code[tid] = sk > 0.0f ? quant<I8>(fk / sk) : 0;
+    __syncwarp();
+    if (lane < 2) {
+      const uint4 w = *reinterpret_cast<const uint4*>(s_code + (tid & ~31) + 16 * lane);
+      const int off = j * kHD + (d & ~31) + 16 * lane;
+      if (km) *reinterpret_cast<uint4*>(km + off) = w;
+      if (kp) *reinterpret_cast<uint4*>(kp + off) = w;
+    }
+    __syncwarp();
+    const uint8_t c = sv > 0.0f ? quant<I8>(fv / sv) : 0;
+    if (vm) vm[d * P + j] = c;
+    if (vp) vp[d * P + j] = c;
+    sum = sum + fk;                        // the slab: fp32, token order
+  }
+  return sum;
+}
+
+__device__ __forceinline__ int slab_code(float mean, float amax, float s) {
+  return amax > 0.0f ? (int)fminf(fmaxf(rintf(mean / s), -127.0f), 127.0f) : 0;
+}
 
 // ---------------------------------------------------------------------------
 // append
@@ -146,7 +241,6 @@ __global__ void __launch_bounds__(1024) append_page_head_kernel(StorePHParams p)
   __shared__ int s_run;
   __shared__ float s_max[2][32];
   __shared__ __align__(16) uint8_t s_code[1024];
-  constexpr float kQmax = I8 ? 127.0f : 448.0f;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -178,11 +272,11 @@ __global__ void __launch_bounds__(1024) append_page_head_kernel(StorePHParams p)
   // the run's first token, while its length is found
   const __nv_bfloat16* kin = p.k + ((size_t)li * p.T + t0) * HD + tid;
   const __nv_bfloat16* vin = p.v + ((size_t)li * p.T + t0) * HD + tid;
-  __nv_bfloat16 k0 = kin[0], v0 = vin[0];
+  const __nv_bfloat16 k0 = kin[0], v0 = vin[0];
   if (tid == 0) s_run = P;
   __syncthreads();
   if (tid < P) {
-    bool ends = t0 + tid >= p.T || x1 < 0 || x1 / P != pg;
+    const bool ends = t0 + tid >= p.T || x1 < 0 || x1 / P != pg;
     if (!ends) {
       s_row[tid] = (int)(x1 % P);
       if (tid > 0 && x1 <= x0) set_status(p.status, SSA_ST_BAD_POS);
@@ -194,91 +288,21 @@ __global__ void __launch_bounds__(1024) append_page_head_kernel(StorePHParams p)
     if (tid == 0) set_status(p.status, SSA_ST_BAD_ID);
     slot = -1;
   }
-  const size_t pe = (size_t)P * kHD;       // codes of one head of one page
-  const Block bk(p, false, layer, pg, slot, h, pe), bv(p, true, layer, pg, slot, h, pe);
-  const float old_k = cnt0 > 0 ? bk.scale() : 0.0f, old_v = cnt0 > 0 ? bv.scale() : 0.0f;
+  const Block blk(p, layer, pg, slot, h);
   __syncthreads();
   const int R = s_run;
-
-  // finite maxima of the run per head
-  float ak = 0.0f, av = 0.0f;
-  auto take = [](float& m, __nv_bfloat16 x) {
-    const float a = fabsf(__bfloat162float(x));
-    if (a < INFINITY) m = fmaxf(m, a);
-  };
-  take(ak, k0);
-  take(av, v0);
-  for (int r0 = 1; r0 < R; r0 += kTokBatch) {
-    __nv_bfloat16 xk[kTokBatch], xv[kTokBatch];
-#pragma unroll
-    for (int i = 0; i < kTokBatch; ++i)
-      if (r0 + i < R) {
-        xk[i] = kin[(size_t)(r0 + i) * HD];
-        xv[i] = vin[(size_t)(r0 + i) * HD];
-      }
-#pragma unroll
-    for (int i = 0; i < kTokBatch; ++i)
-      if (r0 + i < R) {
-        take(ak, xk[i]);
-        take(av, xv[i]);
-      }
-  }
-  ak = warp_max(ak);
-  av = warp_max(av);
-  if (lane == 0) {
-    s_max[0][warp] = ak;
-    s_max[1][warp] = av;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    ak = fmaxf(ak, s_max[0][(warp & ~3) + w]);
-    av = fmaxf(av, s_max[1][(warp & ~3) + w]);
-  }
-  const float need_k = ak / kQmax, need_v = av / kQmax;
-  const float sk = cnt0 > 0 ? fmaxf(old_k, need_k) : need_k;
-  const float sv = cnt0 > 0 ? fmaxf(old_v, need_v) : need_v;
-  if (d == 0) {
-    bk.set_scale(sk);
-    bv.set_scale(sv);
-  }
-  const bool gk = cnt0 > 0 && sk > old_k, gv = cnt0 > 0 && sv > old_v;
-  if (gk) rescale_block<I8>(bk.mir, bk.pool, (int)pe, old_k / sk, d, kHD);
-  if (gv) rescale_block<I8>(bv.mir, bv.pool, (int)pe, old_v / sv, d, kHD);
-  __syncthreads();                         // the new codes go on top
-
-  for (int r = 0; r < R; ++r) {
-    const __nv_bfloat16 xk = r == 0 ? k0 : kin[(size_t)r * HD], xv = r == 0 ? v0 : vin[(size_t)r * HD];
-    const float fk = __bfloat162float(xk), fv = __bfloat162float(xv);
-    const int j = s_row[r];
-    // K row j: the warp's 32 codes as two 16-byte stores
-    s_code[tid] = sk > 0.0f ? quant<I8>(fk / sk) : 0;
-    __syncwarp();
-    if (lane < 2) {
-      const uint4 w = *reinterpret_cast<const uint4*>(s_code + (tid & ~31) + 16 * lane);
-      const size_t off = (size_t)j * kHD + (d & ~31) + 16 * lane;
-      if (bk.mir) *reinterpret_cast<uint4*>(bk.mir + off) = w;
-      if (bk.pool) *reinterpret_cast<uint4*>(bk.pool + off) = w;
-    }
-    __syncwarp();
-    const uint8_t c = sv > 0.0f ? quant<I8>(fv / sv) : 0;
-    const size_t off = (size_t)d * P + j;
-    if (bv.mir) bv.mir[off] = c;
-    if (bv.pool) bv.pool[off] = c;
-    sum = sum + fk;                        // the slab: fp32, token order
-  }
+  sum = store_columns<I8, P>(p, blk, true, d, kin, vin, k0, v0, HD, R, s_row, cnt0, sum, s_max,
+                             s_code);
   p.slab_sum[so] = sum;
   const int cnt = cnt0 + R;
   const float mean = sum / (float)cnt;
   const float a = warp_max(fabsf(mean));
-  if (lane == 0) s_max[0][warp] = a;       // the scales' maxima were read before the last barrier
+  if (lane == 0) s_max[0][warp] = a;       // (its last readers are a barrier back)
   __syncthreads();
   float amax = 0.0f;
   for (int w = 0; w < 4 * Hkv; ++w) amax = fmaxf(amax, s_max[0][w]);
   const float s = amax / 127.0f;
-  int c = 0;
-  if (amax > 0.0f) c = (int)fminf(fmaxf(rintf(mean / s), -127.0f), 127.0f);
-  p.slab[so] = (int8_t)c;
+  p.slab[so] = (int8_t)slab_code(mean, amax, s);
   if (tid == 0) {
     p.slab_cnt[lp] = cnt;
     p.slab_scale[lp] = s;
@@ -301,6 +325,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -309,19 +338,12 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 
 // Divides by one block's scale.  With ny = -RN(1 / s) and nx = -x, each step
 // corrects the quotient by its residual q s - x (exact in one fma); the signs
-// are such that a zero keeps its own.  exact: s in [2^-90, 2^100] and x
-// finite, so that nothing on the way over- or underflows unless the quotient
-// is below 2^-12 (every code 0).
+// are such that a zero keeps its own.  For s in [2^-90, 2^100] and x finite:
+// nothing on the way over- or underflows then unless the quotient is below
+// 2^-12 (every code 0).
 struct Divider {
-  float s;
   uint64_t s2, ny2;
-  bool exact;
-  __device__ __forceinline__ Divider(float s_, bool finite) : s(s_) {
-    exact = finite && s >= 0x1p-90f && s <= 0x1p100f;
-    const float ny = exact ? -(1.0f / s) : 0.0f;
-    s2 = pack2(s, s);
-    ny2 = pack2(ny, ny);
-  }
+  __device__ __forceinline__ Divider(float2 s) : s2(pack2(s.x, s.x)), ny2(pack2(s.y, s.y)) {}
   // two negated elements -> the two quotients
   __device__ __forceinline__ uint64_t operator()(float nx0, float nx1) const {
     const uint64_t nx = pack2(nx0, nx1);
@@ -366,32 +388,6 @@ __device__ __forceinline__ uint32_t max_bits(__nv_bfloat162 m) {
   return __reduce_max_sync(0xffffffffu, max(w >> 16, w & 0xFFFFu));
 }
 
-// A run's codes one by one, by plain division: scales outside the Divider's
-// range, and blocks with values that are not finite.  x: the run's first row
-// of this head, rows HD apart.
-template <bool I8, int P>
-__device__ __noinline__ void store_plain(const __nv_bfloat16* x, int HD, int R, const int* s_row,
-                                         float s, bool v, uint8_t* mir, uint8_t* pool,
-                                         int nthreads) {
-  for (int e = threadIdx.x; e < R * kHD; e += nthreads) {
-    const int r = e / kHD, d = e % kHD, j = s_row[r];
-    const uint8_t c = s > 0.0f ? quant<I8>(__bfloat162float(x[(size_t)r * HD + d]) / s) : 0;
-    const int off = v ? d * P + j : j * kHD + d;
-    if (mir) mir[off] = c;
-    if (pool) pool[off] = c;
-  }
-}
-
-// The largest finite magnitude of a run's rows of one head (a thread's share).
-__device__ __noinline__ float finite_max(const __nv_bfloat16* x, int HD, int R, int nthreads) {
-  float m = 0.0f;
-  for (int e = threadIdx.x; e < R * kHD; e += nthreads) {
-    const float a = fabsf(__bfloat162float(x[(size_t)(e / kHD) * HD + e % kHD]));
-    if (a < INFINITY) m = fmaxf(m, a);
-  }
-  return warp_max(m);
-}
-
 // Threads of a CTA and 16-byte units of K (and of V) a thread holds: 4 tokens
 // at a time, at most 8 units.
 constexpr int prefill_threads(int P) { return P == 128 ? 256 : 128; }
@@ -400,7 +396,8 @@ constexpr int prefill_units(int P) { return P <= 32 ? 4 : 8; }
 // codes on their way out
 inline size_t prefill_smem(int P) { return (size_t)P * kHD * 3; }
 
-template <bool I8, int P>
+// MIR: the cache has a host mirror.
+template <bool I8, int P, bool MIR>
 __global__ void __launch_bounds__(prefill_threads(P), P == 128 ? 2 : 4)
 prefill_page_head_kernel(StorePHParams p) {
   constexpr int NT = prefill_threads(P), NU = prefill_units(P), NW = NT / 32;
@@ -413,12 +410,24 @@ prefill_page_head_kernel(StorePHParams p) {
   __shared__ int s_row[P];               // the run's tokens' rows j, ascending
   __shared__ int s_run;
   __shared__ uint32_t s_bits[2][NW];
-  __shared__ float s_red[2][NW], s_slab[4];
-  __shared__ float s_head_amax;          // read by the other heads of the cluster
+  __shared__ float s_max[2][32], s_slab[4];
+  __shared__ __align__(16) uint8_t s_code[NT];
+  __shared__ float2 s_scale[2];          // K's, V's: (scale, -1 / scale, 0 outside the exact range)
+  // the heads' maxima of two runs, and their barriers: head r of the cluster
+  // writes entry r of every head.  (Two of each: a head can be one run ahead.)
+  __shared__ float s_heads[2][8];
+  __shared__ uint64_t s_bar[2];
   constexpr float kQmax = I8 ? 127.0f : 448.0f;
-  pdl_trigger();
-  pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    mbar_init(&s_bar[0], 1);
+    mbar_init(&s_bar[1], 1);
+    fence_barrier_init();
+  }
+  pdl_trigger();
+  // every head's barriers are there before the first push (waited for below)
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  pdl_wait();
   const int c = tid % kRowUnits, g = tid / kRowUnits;              // dims 8c.., tokens 4g..
   const int h = blockIdx.x % p.Hkv, Hkv = p.Hkv, HD = Hkv * kHD;   // h: the cluster's rank
   const int li = blockIdx.y, layer = p.layer0 + li;
@@ -445,7 +454,9 @@ prefill_page_head_kernel(StorePHParams p) {
     if (lane == 0) s_start[warp] = m;
   }
   __syncthreads();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 
+  int run = 0;
 #pragma unroll 1
   for (int at = 0; at < P; ++at) {
     const uint32_t ahead = s_start[at >> 5] >> (at & 31);
@@ -456,8 +467,7 @@ prefill_page_head_kernel(StorePHParams p) {
     const int pg = (int)page;
     const size_t lp = (size_t)layer * p.Lp + pg;
     // the page's state, loaded now: its latency overlaps the run's scan
-    const size_t so = (lp * Hkv + h) * kHD + tid;
-    float sum = tid < kHD ? p.slab_sum[so] : 0.0f;
+    const size_t so = (lp * Hkv + h) * kHD;
     const int cnt0 = p.slab_cnt[lp];
     int slot = p.slot_of[lp];
     // run length: consecutive tokens of the same page (at most P)
@@ -482,206 +492,198 @@ prefill_page_head_kernel(StorePHParams p) {
     }
     const bool full = __syncthreads_and(in_place);     // the run is the whole page
     const int R = s_run;
-
-    // the run's rows of this head, in registers; the largest magnitudes
-    uint4 kr[NU], vr[NU];
-    auto token = [&](int i) { return (i >> 2) * (4 * G) + 4 * g + (i & 3); };
     const size_t row0 = ((size_t)li * p.T + t0) * HD + h * kHD;
-    {
-      const uint4* kg = reinterpret_cast<const uint4*>(p.k + row0) + c;
-      const uint4* vg = reinterpret_cast<const uint4*>(p.v + row0) + c;
-#pragma unroll
-      for (int i = 0; i < NU; ++i) {
-        const int r = token(i);
-        kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-        if (r < R) {
-          kr[i] = __ldcs(kg + r * (HD / 8));
-          vr[i] = __ldcs(vg + r * (HD / 8));
-        }
-      }
-    }
     if (slot >= p.S) {                     // corrupt state: never write through it
       if (tid == 0 && h == 0) set_status(p.status, SSA_ST_BAD_ID);
       slot = -1;
     }
-    constexpr int pe = P * kHD;            // codes of one head of one page
-    const Block bk(p, false, layer, pg, slot, h, pe), bv(p, true, layer, pg, slot, h, pe);
-    const float old_k = cnt0 > 0 ? bk.scale() : 0.0f, old_v = cnt0 > 0 ? bv.scale() : 0.0f;
-    __nv_bfloat162 mk2 = __floats2bfloat162_rn(0.0f, 0.0f), mv2 = mk2;
-#pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      if (token(i) < P) kx[token(i) * kRowUnits + c] = kr[i];
-      absmax(mk2, kr[i]);
-      absmax(mv2, vr[i]);
-    }
-    uint32_t mk = max_bits(mk2), mv = max_bits(mv2);
-    if (lane == 0) {
-      s_bits[0][warp] = mk;
-      s_bits[1][warp] = mv;
-    }
-    __syncthreads();                       // (every thread has read the old scales)
-
-    // the slab: fp32 running sums in token order; the heads' maxima meet while
-    // the codes are made
+    const Block blk(p, layer, pg, slot, h);
     const int cnt = cnt0 + R;
-    float mean = 0.0f;
-    if (tid < kHD) {
-      const __nv_bfloat16* col = reinterpret_cast<const __nv_bfloat16*>(kx) + tid;
-#pragma unroll 16
-      for (int r = 0; r < R; ++r) sum = sum + __bfloat162float(col[r * kHD]);
-      p.slab_sum[so] = sum;
-      mean = sum / (float)cnt;
-      const float a = warp_max(fabsf(mean));
-      if (lane == 0) s_slab[warp] = a;
-    }
+    const float fcnt = (float)cnt;
+
+    // a whole page: its rows of this head in registers; the largest magnitudes
+    uint4 kr[NU], vr[NU];
+    auto token = [&](int i) { return (i >> 2) * (4 * G) + 4 * g + (i & 3); };
+    constexpr bool kIdle = NT * NU > P * kRowUnits;    // threads without tokens (P = 16)
+    const bool mine = !kIdle || token(0) < P;
+    float2 mean = make_float2(0.0f, 0.0f);             // of dims 2 tid, 2 tid + 1
+    if (full) {
+      const uint4* kg = reinterpret_cast<const uint4*>(p.k + row0) + c;
+      const uint4* vg = reinterpret_cast<const uint4*>(p.v + row0) + c;
+      const int rs = HD / 8;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      mk = max(mk, s_bits[0][w]);
-      mv = max(mv, s_bits[1][w]);
-    }
-    const bool finite = mk < 0x7F80u && mv < 0x7F80u;
-    float ak = __uint_as_float(mk << 16), av = __uint_as_float(mv << 16);
-    if (!finite) {                         // infinities and NaN leave the scale alone
-      ak = finite_max(p.k + row0, HD, R, NT);
-      av = finite_max(p.v + row0, HD, R, NT);
+      for (int i = 0; i < NU; ++i) {
+        kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+        if (mine) {
+          kr[i] = __ldcs(kg + token(i) * rs);
+          vr[i] = __ldcs(vg + token(i) * rs);
+        }
+      }
+      // warps 0 and 1 have the slab's sums to make, warp 2 (3) K's (V's) scale
+      float2 sum = make_float2(0.0f, 0.0f);
+      float old = 0.0f;
+      if (tid < kHD / 2) sum = reinterpret_cast<const float2*>(p.slab_sum + so)[tid];
+      if (tid == 64 && cnt0 > 0) old = blk.scale(p.k_scale_m, p.k_scale);
+      if (tid == 96 && cnt0 > 0) old = blk.scale(p.v_scale_m, p.v_scale);
+      __nv_bfloat162 mk2 = __floats2bfloat162_rn(0.0f, 0.0f), mv2 = mk2;
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        if (mine) kx[token(i) * kRowUnits + c] = kr[i];
+        absmax(mk2, kr[i]);
+        absmax(mv2, vr[i]);
+      }
+      const uint32_t mk = max_bits(mk2), mv = max_bits(mv2);
       if (lane == 0) {
-        s_red[0][warp] = ak;
-        s_red[1][warp] = av;
+        s_bits[0][warp] = mk;
+        s_bits[1][warp] = mv;
       }
-    }
-    __syncthreads();                       // s_slab, s_red
-    if (tid == 0) s_head_amax = fmaxf(fmaxf(s_slab[0], s_slab[1]), fmaxf(s_slab[2], s_slab[3]));
-    cluster_arrive();
-    if (!finite)
-      for (int w = 0; w < NW; ++w) {
-        ak = fmaxf(ak, s_red[0][w]);
-        av = fmaxf(av, s_red[1][w]);
+      __syncthreads();
+      if (tid < kHD / 2) {
+        // fp32 running sums in token order, two dimensions per thread
+        const uint32_t* col = reinterpret_cast<const uint32_t*>(kx) + tid;
+        uint64_t acc = pack2(sum.x, sum.y);
+#pragma unroll 16
+        for (int r = 0; r < P; ++r) {
+          const uint32_t w = col[r * (kHD / 2)];
+          acc = add2(acc, pack2(lo_f(w), hi_f(w)));
+        }
+        unpack2(acc, sum.x, sum.y);
+        reinterpret_cast<float2*>(p.slab_sum + so)[tid] = sum;
+        mean = make_float2(sum.x / fcnt, sum.y / fcnt);
+        const float a = warp_max(fmaxf(fabsf(mean.x), fabsf(mean.y)));
+        if (lane == 0) s_slab[warp] = a;
+      } else if (tid == 64 || tid == 96) {
+        uint32_t m = 0;
+        for (int w = 0; w < NW; ++w) m = max(m, s_bits[warp - 2][w]);
+        const float need = __uint_as_float(m << 16) / kQmax;
+        const float s = cnt0 > 0 ? fmaxf(old, need) : need;
+        // finite values, and a scale that keeps the quotients exact (see Divider)
+        const bool exact = m < 0x7F80u && s >= 0x1p-90f && s <= 0x1p100f;
+        s_scale[warp - 2] = make_float2(s, exact ? -(1.0f / s) : 0.0f);
       }
-    const float need_k = ak / kQmax, need_v = av / kQmax;
-    const float sk = cnt0 > 0 ? fmaxf(old_k, need_k) : need_k;
-    const float sv = cnt0 > 0 ? fmaxf(old_v, need_v) : need_v;
-    if (tid == 0) {
-      bk.set_scale(sk);
-      bv.set_scale(sv);
+      __syncthreads();
     }
-    if (!full && cnt0 > 0) {               // a whole page leaves no code of before
-      if (sk > old_k) rescale_block<I8>(bk.mir, bk.pool, pe, old_k / sk, tid, NT);
-      if (sv > old_v) rescale_block<I8>(bv.mir, bv.pool, pe, old_v / sv, tid, NT);
-      __syncthreads();                     // the new codes go on top
+    const float2 sck = s_scale[0], scv = s_scale[1];
+    const bool fast = full && sck.y != 0.0f && scv.y != 0.0f;
+    if (fast) {
+      if (tid == 0) {
+        blk.set_scale(p.k_scale_m, p.k_scale, sck.x);
+        blk.set_scale(p.v_scale_m, p.v_scale, scv.x);
+      }
+    } else {
+      // part of a page, or values or scales out of the ordinary
+      const int d = tid & (kHD - 1);
+      const bool active = tid < kHD;
+      const __nv_bfloat16 *kin = p.k + row0 + d, *vin = p.v + row0 + d;
+      // (a whole page has its sums already)
+      float sum = active && !full ? p.slab_sum[so + d] : 0.0f;
+      sum = store_columns<I8, P>(p, blk, active, d, kin, vin, kin[0], vin[0], HD, R, s_row, cnt0,
+                                 sum, s_max, s_code);
+      if (!full && active) {
+        p.slab_sum[so + d] = sum;
+        mean.x = sum / fcnt;
+        const float a = warp_max(fabsf(mean.x));
+        if (lane == 0) s_slab[warp] = a;
+      }
+      __syncthreads();
+    }
+    // the page's heads exchange their maxima while the codes are made
+    const int par = run & 1;
+    if (tid == 0) mbar_arrive_expect_tx(&s_bar[par], 4 * Hkv);
+    if (tid < Hkv) {
+      float a = fmaxf(s_slab[0], s_slab[1]);
+      if (!full) a = fmaxf(a, fmaxf(s_slab[2], s_slab[3]));
+      push_f32(&s_heads[par][h], &s_bar[par], tid, a);
     }
 
-    constexpr uint32_t kNeg = 0x80008000u;
-    const Divider dk(sk, finite), dv(sv, finite);
-    // K: 8 codes of a row per unit
-    if (dk.exact) {
-      uint2 out[NU];
+    if (fast) {
+      constexpr int pe = P * kHD;          // codes of one head of one page
+      constexpr uint32_t kNeg = 0x80008000u;
+      // K: 8 codes of a row per unit
+      const Divider dk(sck), dv(scv);
+      uint8_t* kp = blk.slot(p.k_pool, pe);
+      uint8_t* km = MIR ? blk.mirror(p.k_mir, pe) : nullptr;
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         const uint32_t w[4] = {kr[i].x ^ kNeg, kr[i].y ^ kNeg, kr[i].z ^ kNeg, kr[i].w ^ kNeg};
         uint64_t q[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) q[k] = dk(lo_f(w[k]), hi_f(w[k]));
-        out[i] = make_uint2(codes4<I8>(q[0], q[1]), codes4<I8>(q[2], q[3]));
+        const uint2 out = make_uint2(codes4<I8>(q[0], q[1]), codes4<I8>(q[2], q[3]));
+        const int off = token(i) * kHD + 8 * c;
+        if (MIR && mine) *reinterpret_cast<uint2*>(km + off) = out;
+        if (mine && kp) *reinterpret_cast<uint2*>(kp + off) = out;
       }
-      auto put = [&](uint8_t* to) {
-        if (!to) return;
-#pragma unroll
-        for (int i = 0; i < NU; ++i) {
-          const int r = token(i);
-          if (r < R) *reinterpret_cast<uint2*>(to + (full ? r : s_row[r]) * kHD + 8 * c) = out[i];
-        }
-      };
-      put(bk.mir);
-      put(bk.pool);
-    } else {
-      store_plain<I8, P>(p.k + row0, HD, R, s_row, sk, false, bk.mir, bk.pool, NT);
-    }
-    // V: words of 4 tokens per dimension
-    if (dv.exact) {
+      // V: words of 4 tokens per dimension; word r / 4 of row d goes to a place
+      // that spreads the 16 dimension groups over the banks
+      constexpr int kWords = P / 4, kVec = P / 16;       // words, 16-byte units of a row
 #pragma unroll
       for (int i = 0; i < NU; i += 4) {
-        const int r = token(i);
+        const int at_w = (token(i) >> 2) ^ (c & (kWords - 1));
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
           auto word = [&](const uint4& v) {
             return (k < 2 ? v.x : (k < 4 ? v.y : (k < 6 ? v.z : v.w))) ^ kNeg;
           };
           const uint32_t w[4] = {word(vr[i]), word(vr[i + 1]), word(vr[i + 2]), word(vr[i + 3])};
-          const uint32_t o[2] = {
-              codes4<I8>(dv(lo_f(w[0]), lo_f(w[1])), dv(lo_f(w[2]), lo_f(w[3]))),
-              codes4<I8>(dv(hi_f(w[0]), hi_f(w[1])), dv(hi_f(w[2]), hi_f(w[3])))};
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int d = 8 * c + k + e;
-            if (full) {
-              // word r / 4 of row d, at a place that spreads the 16 dimension
-              // groups over the banks
-              constexpr int kWords = P / 4;
-              if (r < P) vt[d * kWords + ((r >> 2) ^ (c & (kWords - 1)))] = o[e];
-            } else {
-#pragma unroll 1
-              for (int m = 0; m < 4 && r + m < R; ++m) {
-                const uint8_t b = (uint8_t)(o[e] >> (8 * m));
-                const int off = d * P + s_row[r + m];
-                if (bv.mir) bv.mir[off] = b;
-                if (bv.pool) bv.pool[off] = b;
-              }
-            }
+          const uint32_t o0 = codes4<I8>(dv(lo_f(w[0]), lo_f(w[1])), dv(lo_f(w[2]), lo_f(w[3])));
+          const uint32_t o1 = codes4<I8>(dv(hi_f(w[0]), hi_f(w[1])), dv(hi_f(w[2]), hi_f(w[3])));
+          if (mine) {
+            vt[(8 * c + k) * kWords + at_w] = o0;
+            vt[(8 * c + k + 1) * kWords + at_w] = o1;
           }
         }
       }
-      if (full) {
-        __syncthreads();
-        constexpr int kWords = P / 4, kVec = P / 16;     // words, 16-byte units of a row
+      __syncthreads();
+      uint8_t* vp = blk.slot(p.v_pool, pe);
+      uint8_t* vm = MIR ? blk.mirror(p.v_mir, pe) : nullptr;
 #pragma unroll
-        for (int u0 = 0; u0 < kHD * kVec; u0 += NT) {
-          const int u = u0 + tid;
-          const int d = u / kVec, x = u % kVec, sw = (d >> 3) & (kWords - 1);
-          // the unit's words lie together, in another order
-          const uint4 q = *reinterpret_cast<const uint4*>(vt + d * kWords + ((4 * x) ^ (sw & ~3)));
-          const bool b0 = sw & 1, b1 = sw & 2;
-          const uint2 e = b1 ? make_uint2(q.z, q.w) : make_uint2(q.x, q.y);
-          const uint2 f = b1 ? make_uint2(q.x, q.y) : make_uint2(q.z, q.w);
-          const uint4 out = b0 ? make_uint4(e.y, e.x, f.y, f.x) : make_uint4(e.x, e.y, f.x, f.y);
-          if (bv.mir) reinterpret_cast<uint4*>(bv.mir)[u] = out;
-          if (bv.pool) reinterpret_cast<uint4*>(bv.pool)[u] = out;
-        }
+      for (int u0 = 0; u0 < kHD * kVec; u0 += NT) {
+        const int u = u0 + tid;
+        const int d = u / kVec, x = u % kVec, sw = (d >> 3) & (kWords - 1);
+        // the unit's words lie together, in another order
+        const uint4 q = *reinterpret_cast<const uint4*>(vt + d * kWords + ((4 * x) ^ (sw & ~3)));
+        const bool b0 = sw & 1, b1 = sw & 2;
+        const uint2 e = b1 ? make_uint2(q.z, q.w) : make_uint2(q.x, q.y);
+        const uint2 f = b1 ? make_uint2(q.x, q.y) : make_uint2(q.z, q.w);
+        const uint4 out = b0 ? make_uint4(e.y, e.x, f.y, f.x) : make_uint4(e.x, e.y, f.x, f.y);
+        if (MIR) reinterpret_cast<uint4*>(vm)[u] = out;
+        if (vp) reinterpret_cast<uint4*>(vp)[u] = out;
       }
-    } else {
-      store_plain<I8, P>(p.v + row0, HD, R, s_row, sv, true, bv.mir, bv.pool, NT);
     }
 
     // the page's slab row, now that every head's maximum is there
-    cluster_wait();
+    if (!mbar_wait(&s_bar[par], (run >> 1) & 1, nullptr)) {
+      set_status(p.status, SSA_ST_TIMEOUT);
+      return;
+    }
     float amax = 0.0f;
-    for (int r = 0; r < Hkv; ++r) amax = fmaxf(amax, cluster_read(&s_head_amax, r));
-    cluster_arrive();
+    for (int r = 0; r < Hkv; ++r) amax = fmaxf(amax, s_heads[par][r]);
     const float s = amax / 127.0f;
-    if (tid < kHD)
-      p.slab[so] = (int8_t)(amax > 0.0f ? (int)fminf(fmaxf(rintf(mean / s), -127.0f), 127.0f) : 0);
+    if (full) {
+      if (tid < kHD / 2)
+        reinterpret_cast<char2*>(p.slab + so)[tid] = make_char2(
+            (signed char)slab_code(mean.x, amax, s), (signed char)slab_code(mean.y, amax, s));
+    } else if (tid < kHD) {
+      p.slab[so + tid] = (int8_t)slab_code(mean.x, amax, s);
+    }
     if (tid == 0 && h == 0) {              // every head has read the count by now
       p.slab_cnt[lp] = cnt;
       p.slab_scale[lp] = s;
     }
-    cluster_wait();                        // all have read s_head_amax; (the tiles may go)
+    ++run;
+    __syncthreads();                       // the tiles and s_row: the next run's
   }
 }
 
 // Calls of at least this many tokens take the prefill kernel.
 constexpr int kPrefillTokens = 4096;
 
-template <bool I8, int P>
-cudaError_t launch_t(const StorePHParams& p, int n_layers, cudaStream_t s) {
-  cudaError_t e;
-  if (p.T < kPrefillTokens) {
-    e = launch_pdl(append_page_head_kernel<I8, P>, dim3((unsigned)p.T, (unsigned)n_layers),
-                   dim3((unsigned)(p.Hkv * kHD)), 0, s, p);
-    count_launch();
-    return e;
-  }
+template <bool I8, int P, bool MIR>
+cudaError_t launch_prefill(const StorePHParams& p, int n_layers, cudaStream_t s) {
   const size_t smem = prefill_smem(P);
-  e = cudaFuncSetAttribute(prefill_page_head_kernel<I8, P>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(prefill_page_head_kernel<I8, P, MIR>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const long long nchunk = (p.T + (long long)P - 1) / P;
   if (nchunk * p.Hkv > 0x7FFFFFFFll) return cudaErrorInvalidValue;
@@ -699,7 +701,19 @@ cudaError_t launch_t(const StorePHParams& p, int n_layers, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, prefill_page_head_kernel<I8, P>, p);
+  e = cudaLaunchKernelEx(&cfg, prefill_page_head_kernel<I8, P, MIR>, p);
+  count_launch();
+  return e;
+}
+
+template <bool I8, int P>
+cudaError_t launch_t(const StorePHParams& p, int n_layers, cudaStream_t s) {
+  if (p.T >= kPrefillTokens)
+    return p.k_mir ? launch_prefill<I8, P, true>(p, n_layers, s)
+                   : launch_prefill<I8, P, false>(p, n_layers, s);
+  cudaError_t e = launch_pdl(append_page_head_kernel<I8, P>,
+                             dim3((unsigned)p.T, (unsigned)n_layers),
+                             dim3((unsigned)(p.Hkv * kHD)), 0, s, p);
   count_launch();
   return e;
 }
