@@ -23,8 +23,8 @@
 // a few tokens.
 //
 // Prefill: one CTA per (run, layer, KV head), which keeps the run's rows of
-// its head in registers while the scale becomes known, so that each input is
-// read once.  A thread holds 8 dimensions of 4 consecutive tokens, so V leaves
+// its head in shared memory while the scale becomes known, so that each input
+// is read once.  A thread holds 8 dimensions of 4 consecutive tokens, so V leaves
 // as whole words of its d-major block through a swizzled tile.  The heads of a
 // page meet only in the slab's scale (max over all heads): they form a cluster
 // and read each other's maximum through distributed shared memory.
@@ -374,6 +374,11 @@ __device__ __forceinline__ uint32_t codes4(uint64_t a, uint64_t b) {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+__device__ __forceinline__ void copy_async16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
+               : "memory");
+}
+
 // Largest |bf16| so far per half, NaN if there is one (so: bits from 0x7F80 on
 // where a value is not finite)
 __device__ __forceinline__ void absmax(__nv_bfloat162& m, uint4 v) {
@@ -392,19 +397,20 @@ __device__ __forceinline__ uint32_t max_bits(__nv_bfloat162 m) {
 // at a time, at most 8 units.
 constexpr int prefill_threads(int P) { return P == 128 ? 256 : 128; }
 constexpr int prefill_units(int P) { return P <= 32 ? 4 : 8; }
-// dynamic shared memory: K rows as they came (for the slab's sums) and V's
-// codes on their way out
-inline size_t prefill_smem(int P) { return (size_t)P * kHD * 3; }
+// dynamic shared memory: K and V rows as they came; V's codes on their way out
+// take the place of K's
+inline size_t prefill_smem(int P) { return (size_t)P * kHD * 4; }
 
 // MIR: the cache has a host mirror.
 template <bool I8, int P, bool MIR>
-__global__ void __launch_bounds__(prefill_threads(P), P == 128 ? 2 : 4)
+__global__ void __launch_bounds__(prefill_threads(P), P == 128 ? 3 : 6)
 prefill_page_head_kernel(StorePHParams p) {
   constexpr int NT = prefill_threads(P), NU = prefill_units(P), NW = NT / 32;
   constexpr int G = NT / kRowUnits;      // groups of 4 tokens side by side
   extern __shared__ __align__(16) uint8_t dsm[];
   uint4* kx = reinterpret_cast<uint4*>(dsm);                       // [r][16 units]
-  uint32_t* vt = reinterpret_cast<uint32_t*>(dsm + P * kHD * 2);   // [d][P / 4 words], swizzled
+  uint4* vx = kx + P * kRowUnits;
+  uint32_t* vt = reinterpret_cast<uint32_t*>(dsm);                 // [d][P / 4 words], swizzled
   __shared__ int64_t s_pos[2 * P];       // positions of the chunk and of the run it may end in
   __shared__ uint32_t s_start[(P + 31) / 32];
   __shared__ int s_row[P];               // the run's tokens' rows j, ascending
@@ -501,8 +507,9 @@ prefill_page_head_kernel(StorePHParams p) {
     const int cnt = cnt0 + R;
     const float fcnt = (float)cnt;
 
-    // a whole page: its rows of this head in registers; the largest magnitudes
-    uint4 kr[NU], vr[NU];
+    // a whole page: its rows of this head into shared memory (asynchronous
+    // copies, so that no register waits for them); the largest magnitudes.  A
+    // thread copies the units that it works on itself.
     auto token = [&](int i) { return (i >> 2) * (4 * G) + 4 * g + (i & 3); };
     constexpr bool kIdle = NT * NU > P * kRowUnits;    // threads without tokens (P = 16)
     const bool mine = !kIdle || token(0) < P;
@@ -511,14 +518,14 @@ prefill_page_head_kernel(StorePHParams p) {
       const uint4* kg = reinterpret_cast<const uint4*>(p.k + row0) + c;
       const uint4* vg = reinterpret_cast<const uint4*>(p.v + row0) + c;
       const int rs = HD / 8;
+      if (mine) {
 #pragma unroll
-      for (int i = 0; i < NU; ++i) {
-        kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-        if (mine) {
-          kr[i] = __ldcs(kg + token(i) * rs);
-          vr[i] = __ldcs(vg + token(i) * rs);
+        for (int i = 0; i < NU; ++i) {
+          copy_async16(&kx[token(i) * kRowUnits + c], kg + token(i) * rs);
+          copy_async16(&vx[token(i) * kRowUnits + c], vg + token(i) * rs);
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       // warps 0 and 1 have the slab's sums to make, warp 2 (3) K's (V's) scale
       float2 sum = make_float2(0.0f, 0.0f);
       float old = 0.0f;
@@ -526,11 +533,12 @@ prefill_page_head_kernel(StorePHParams p) {
       if (tid == 64 && cnt0 > 0) old = blk.scale(p.k_scale_m, p.k_scale);
       if (tid == 96 && cnt0 > 0) old = blk.scale(p.v_scale_m, p.v_scale);
       __nv_bfloat162 mk2 = __floats2bfloat162_rn(0.0f, 0.0f), mv2 = mk2;
+      if (mine) {
 #pragma unroll
-      for (int i = 0; i < NU; ++i) {
-        if (mine) kx[token(i) * kRowUnits + c] = kr[i];
-        absmax(mk2, kr[i]);
-        absmax(mv2, vr[i]);
+        for (int i = 0; i < NU; ++i) {
+          absmax(mk2, kx[token(i) * kRowUnits + c]);
+          absmax(mv2, vx[token(i) * kRowUnits + c]);
+        }
       }
       const uint32_t mk = max_bits(mk2), mv = max_bits(mv2);
       if (lane == 0) {
@@ -605,33 +613,38 @@ prefill_page_head_kernel(StorePHParams p) {
       uint8_t* km = MIR ? blk.mirror(p.k_mir, pe) : nullptr;
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
-        const uint32_t w[4] = {kr[i].x ^ kNeg, kr[i].y ^ kNeg, kr[i].z ^ kNeg, kr[i].w ^ kNeg};
+        if (!mine) break;
+        const uint4 x = kx[token(i) * kRowUnits + c];
+        const uint32_t w[4] = {x.x ^ kNeg, x.y ^ kNeg, x.z ^ kNeg, x.w ^ kNeg};
         uint64_t q[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) q[k] = dk(lo_f(w[k]), hi_f(w[k]));
         const uint2 out = make_uint2(codes4<I8>(q[0], q[1]), codes4<I8>(q[2], q[3]));
         const int off = token(i) * kHD + 8 * c;
-        if (MIR && mine) *reinterpret_cast<uint2*>(km + off) = out;
-        if (mine && kp) *reinterpret_cast<uint2*>(kp + off) = out;
+        if (MIR) *reinterpret_cast<uint2*>(km + off) = out;
+        if (kp) *reinterpret_cast<uint2*>(kp + off) = out;
       }
+      __syncthreads();                     // K's rows make room for V's codes
       // V: words of 4 tokens per dimension; word r / 4 of row d goes to a place
       // that spreads the 16 dimension groups over the banks
       constexpr int kWords = P / 4, kVec = P / 16;       // words, 16-byte units of a row
 #pragma unroll
       for (int i = 0; i < NU; i += 4) {
+        if (!mine) break;
         const int at_w = (token(i) >> 2) ^ (c & (kWords - 1));
+        uint4 vr[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) vr[m] = vx[token(i + m) * kRowUnits + c];
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
           auto word = [&](const uint4& v) {
             return (k < 2 ? v.x : (k < 4 ? v.y : (k < 6 ? v.z : v.w))) ^ kNeg;
           };
-          const uint32_t w[4] = {word(vr[i]), word(vr[i + 1]), word(vr[i + 2]), word(vr[i + 3])};
+          const uint32_t w[4] = {word(vr[0]), word(vr[1]), word(vr[2]), word(vr[3])};
           const uint32_t o0 = codes4<I8>(dv(lo_f(w[0]), lo_f(w[1])), dv(lo_f(w[2]), lo_f(w[3])));
           const uint32_t o1 = codes4<I8>(dv(hi_f(w[0]), hi_f(w[1])), dv(hi_f(w[2]), hi_f(w[3])));
-          if (mine) {
-            vt[(8 * c + k) * kWords + at_w] = o0;
-            vt[(8 * c + k + 1) * kWords + at_w] = o1;
-          }
+          vt[(8 * c + k) * kWords + at_w] = o0;
+          vt[(8 * c + k + 1) * kWords + at_w] = o1;
         }
       }
       __syncthreads();
