@@ -13,8 +13,8 @@
 //
 // What bounds it: each element read and written once, HBM (3 flop per 4
 // bytes).  The angles are shared by all layers and heads of a token, so a CTA
-// serves one token: its threads start their first loads, rd/2 of them put the
-// token's cos and sin into shared memory, and all rotate with 16-byte
+// serves whole tokens: its threads start their first loads, then put the
+// tokens' cos and sin into shared memory, and all rotate with 16-byte
 // accesses.  Few tokens (a decode step) split a token's layers and heads over
 // more CTAs, each of which computes the rd/2 pairs again.
 #include <cmath>
@@ -27,7 +27,7 @@ namespace ssa {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 4;           // units in flight per thread
+constexpr int kRopeUnroll = 4;           // rows in flight per thread
 
 template <typename T> struct Conv;
 template <> struct Conv<float> {
@@ -60,102 +60,100 @@ __device__ __forceinline__ float2 turn(uint64_t pos, uint64_t f) {
 
 struct RopeParams {
   RopeTensor x[2];
-  int n_x;
   const uint64_t* freq;
   const void* pos;
   int64_t offset;
   float factor;
   int pos64, inverse, D, rd, L, T;
-  int u_rot, units, rows_x0, rows;       // units of a row: rotated, with the tail; rows of q, of both
-  int per_cta;                           // units of one CTA
+  int heads0, heads;                     // of q, of both
+  int u_rot, units;                      // units of a row that turn, and with the tail
+  int lanes_row, rows_pass;              // threads on a row, rows side by side in a CTA
+  int tokens, rows;                      // of one CTA's group: tokens, (token, layer, head) rows
+  int per_cta;                           // rows of one CTA
+  int dt, dl, dh;                        // rows_pass rows on, as tokens, layers, heads
 };
 
-// INTER: V elements hold V / 2 pairs.  Else a unit is V elements of each half.
-// V counts elements per access; with INTER a scalar unit is one pair in two
-// accesses (V = 1, NA = 2).
+// A unit is what a thread moves at once: V elements of each half of a head
+// (or one pair), INTER: V elements that hold V / 2 pairs (or one pair, V = 1).
+// A thread keeps its unit of the head and walks over (token, layer, head)
+// rows, so that an access costs a few additions.
 template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
-  extern __shared__ float2 s_cs[];
+  extern __shared__ float2 s_cs[];       // [tokens][rd / 2]
   using A = Vec<T, V>;
-  // accesses of a unit and the pairs in it
-  constexpr int NA = (INTER && V > 1) ? 1 : 2;
-  constexpr int NP = (INTER && V > 1) ? V / 2 : V;
+  constexpr int NA = (INTER && V > 1) ? 1 : 2;      // accesses of a unit
+  constexpr int NP = (INTER && V > 1) ? V / 2 : V;  // pairs of a unit
   pdl_trigger();
   pdl_wait();
-  const int t = blockIdx.x, tid = threadIdx.x;
-  const int half = p.rd / 2;
-  const int u0 = blockIdx.y * p.per_cta;
-  const int u1 = min(u0 + p.per_cta, p.rows * p.units);
-
-  // unit u of the token: which row, where its accesses are
-  struct Place { const T* in; T* out; int64_t step; int pair; int n; };
-  auto place = [&](int u) -> Place {
-    int row = u / p.units;
-    const int w = u - row * p.units;
-    const RopeTensor& x = p.x[row >= p.rows_x0];
-    if (row >= p.rows_x0) row -= p.rows_x0;
-    const int l = row / x.heads, h = row - l * x.heads;
-    Place r;
-    r.in = static_cast<const T*>(x.in) + l * x.is[0] + t * x.is[1] + h * x.is[2];
-    r.out = static_cast<T*>(x.out) + l * x.os[0] + t * x.os[1] + h * x.os[2];
-    int e;
-    if (w < p.u_rot) {
-      r.pair = w * NP;
-      e = INTER ? w * NP * 2 : w * V;
-      r.step = INTER ? V : half;
-      r.n = NA;
-    } else {                              // the dimensions that stay
-      r.pair = -1;
-      e = p.rd + (w - p.u_rot) * V;
-      r.step = 0;
-      r.n = 1;
-    }
-    r.in += e;
-    r.out += e;
-    return r;
-  };
+  const int tid = threadIdx.x, half = p.rd / 2;
+  const int token0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - token0);
+  const int r1 = min((int)(blockIdx.y + 1) * p.per_cta, nt * p.L * p.heads);
+  const int lane = tid % p.lanes_row, first = tid / p.lanes_row;
+  const int rows_pass = first < p.rows_pass ? p.rows_pass : 0;     // the threads left over idle
 
   bool have_table = false;
-  for (int base = u0; base < u1; base += kRopeThreads * kRopeUnroll) {
-    A a[kRopeUnroll][NA];
+  for (int w0 = 0; w0 < p.units; w0 += p.lanes_row) {
+    const int w = w0 + lane;
+    const bool turns = w < p.u_rot, on = w < p.units && rows_pass;
+    // this unit's first element, and the distance to its second access
+    const int e = turns ? (INTER ? w * NP * 2 : w * V) : p.rd + (w - p.u_rot) * V;
+    const int step = INTER ? V : half;
+    int r = blockIdx.y * p.per_cta + first;
+    int t = r / (p.L * p.heads), l = (r - t * p.L * p.heads) / p.heads;
+    int h = r - (t * p.L + l) * p.heads;
+    const int rounds = (p.per_cta + p.rows_pass * kRopeUnroll - 1) / (p.rows_pass * kRopeUnroll);
+    for (int round = 0; round < rounds; ++round) {
+      A a[kRopeUnroll][NA];
+      T* out[kRopeUnroll];
+      int tt[kRopeUnroll];
 #pragma unroll
-    for (int i = 0; i < kRopeUnroll; ++i) {
-      const int u = base + i * kRopeThreads + tid;
-      if (u < u1) {
-        const Place r = place(u);
-        a[i][0] = *reinterpret_cast<const A*>(r.in);
-        if (NA > 1 && r.n > 1) a[i][NA - 1] = *reinterpret_cast<const A*>(r.in + r.step);
+      for (int i = 0; i < kRopeUnroll; ++i) {
+        out[i] = nullptr;
+        tt[i] = t;
+        if (on && r < r1) {
+          const bool second = h >= p.heads0;
+          const RopeTensor& x = p.x[second];
+          const int hh = second ? h - p.heads0 : h;
+          const int64_t tok = token0 + t;
+          const T* in = static_cast<const T*>(x.in) + l * x.is[0] + tok * x.is[1] + hh * x.is[2] + e;
+          out[i] = static_cast<T*>(x.out) + l * x.os[0] + tok * x.os[1] + hh * x.os[2] + e;
+          a[i][0] = *reinterpret_cast<const A*>(in);
+          if (NA > 1 && turns) a[i][NA - 1] = *reinterpret_cast<const A*>(in + step);
+        }
+        r += p.rows_pass;
+        h += p.dh;
+        l += p.dl;
+        t += p.dt;
+        if (h >= p.heads) { h -= p.heads; ++l; }
+        if (l >= p.L) { l -= p.L; ++t; }
       }
-    }
-    if (!have_table) {                    // while the first loads are in flight
-      const int64_t raw = p.pos64 ? static_cast<const int64_t*>(p.pos)[t]
-                                  : (int64_t) static_cast<const int32_t*>(p.pos)[t];
-      const uint64_t pos = (uint64_t)raw + (uint64_t)p.offset;
-      for (int i = tid; i < half; i += kRopeThreads) {
-        const float2 cs = turn(pos, p.freq[i]);
-        s_cs[i] = make_float2(cs.x * p.factor, (p.inverse ? -cs.y : cs.y) * p.factor);
+      if (!have_table) {                  // while the first loads are in flight
+        for (int i = tid; i < nt * half; i += kRopeThreads) {
+          const int k = i / half, j = i - k * half;
+          const int64_t raw = p.pos64 ? static_cast<const int64_t*>(p.pos)[token0 + k]
+                                      : (int64_t) static_cast<const int32_t*>(p.pos)[token0 + k];
+          const float2 cs = turn((uint64_t)raw + (uint64_t)p.offset, p.freq[j]);
+          s_cs[i] = make_float2(cs.x * p.factor, (p.inverse ? -cs.y : cs.y) * p.factor);
+        }
+        __syncthreads();
+        have_table = true;
       }
-      __syncthreads();
-      have_table = true;
-    }
 #pragma unroll
-    for (int i = 0; i < kRopeUnroll; ++i) {
-      const int u = base + i * kRopeThreads + tid;
-      if (u < u1) {
-        const Place r = place(u);
-        if (r.pair >= 0) {
+      for (int i = 0; i < kRopeUnroll; ++i) {
+        if (!out[i]) continue;
+        if (turns) {
+          const float2* cs = s_cs + tt[i] * half + w * NP;
 #pragma unroll
           for (int k = 0; k < NP; ++k) {
-            const float2 cs = s_cs[r.pair + k];
             T& ea = NA == 1 ? a[i][0].x[2 * k % V] : a[i][0].x[k % V];
             T& eb = NA == 1 ? a[i][0].x[(2 * k + 1) % V] : a[i][NA - 1].x[k % V];
             const float x = Conv<T>::in(ea), y = Conv<T>::in(eb);
-            ea = Conv<T>::out(x * cs.x - y * cs.y);
-            eb = Conv<T>::out(y * cs.x + x * cs.y);
+            ea = Conv<T>::out(x * cs[k].x - y * cs[k].y);
+            eb = Conv<T>::out(y * cs[k].x + x * cs[k].y);
           }
+          if (NA > 1) *reinterpret_cast<A*>(out[i] + step) = a[i][NA - 1];
         }
-        *reinterpret_cast<A*>(r.out) = a[i][0];
-        if (NA > 1 && r.n > 1) *reinterpret_cast<A*>(r.out + r.step) = a[i][NA - 1];
+        *reinterpret_cast<A*>(out[i]) = a[i][0];
       }
     }
   }
@@ -177,20 +175,35 @@ cudaError_t launch_rope_t(RopeParams p, bool copy_tail, int num_sms, cudaStream_
   const int np = (INTER && V > 1) ? V / 2 : V;                 // pairs per unit
   p.u_rot = p.rd / 2 / np;
   p.units = p.u_rot + (copy_tail ? (p.D - p.rd) / V : 0);
-  const long long total = (long long)p.rows * p.units;         // of one token
-  if (total > 0x3FFFFFFF) return cudaErrorInvalidValue;
-  // one CTA per token where there are enough tokens to fill the machine
-  // (8 CTAs of 256 threads per SM), else a token's units over several CTAs,
-  // down to one unit per thread
-  const long long full = 8LL * num_sms;
-  long long split = (full + p.T - 1) / p.T;
-  const long long most = (total + kRopeThreads - 1) / kRopeThreads;
+  p.lanes_row = p.units < kRopeThreads ? p.units : kRopeThreads;
+  p.rows_pass = kRopeThreads / p.lanes_row;
+  const long long row_tok = (long long)p.L * p.heads;          // rows of one token
+  const long long round = (long long)p.rows_pass * kRopeUnroll;
+  // Tokens of a CTA: as many as give every thread one round of loads (at most
+  // 8, and 16 KB of table), as long as the grid still holds 4 CTAs per SM; one
+  // token's rows are split over CTAs, down to one pass, where the tokens alone
+  // give fewer than that.
+  const long long want = 4LL * num_sms;
+  long long tokens = (round + row_tok - 1) / row_tok;
+  if (tokens > 8) tokens = 8;
+  while (tokens > 1 && tokens * p.rd / 2 * (long long)sizeof(float2) > 16384) --tokens;
+  if (tokens > p.T / want) tokens = p.T / want;
+  if (tokens < 1) tokens = 1;
+  p.tokens = (int)tokens;
+  p.rows = (int)(tokens * row_tok);
+  const long long groups = (p.T + tokens - 1) / tokens;
+  long long split = (want + groups - 1) / groups;
+  const long long most = (p.rows + p.rows_pass - 1) / p.rows_pass;
   if (split > most) split = most;
   if (split > 65535) split = 65535;
-  p.per_cta = (int)((total + split - 1) / split);
-  const unsigned gy = (unsigned)((total + p.per_cta - 1) / p.per_cta);
-  cudaError_t e = launch_pdl(rope_kernel<T, V, INTER>, dim3((unsigned)p.T, gy), dim3(kRopeThreads),
-                             (size_t)p.rd / 2 * sizeof(float2), s, p);
+  p.per_cta = (int)((p.rows + split - 1) / split);
+  const unsigned gy = (unsigned)((p.rows + p.per_cta - 1) / p.per_cta);
+  p.dt = (int)(p.rows_pass / row_tok);
+  const int rest = (int)(p.rows_pass % row_tok);
+  p.dl = rest / p.heads;
+  p.dh = rest % p.heads;
+  cudaError_t e = launch_pdl(rope_kernel<T, V, INTER>, dim3((unsigned)groups, gy),
+                             dim3(kRopeThreads), (size_t)tokens * p.rd / 2 * sizeof(float2), s, p);
   count_launch();
   return e;
 }
@@ -200,7 +213,8 @@ cudaError_t launch_rope_d(const RopeParams& p, bool inter, bool copy_tail, int n
                           cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   bool vec = p.D % V == 0 && (inter ? p.rd : p.rd / 2) % V == 0;
-  for (int i = 0; i < p.n_x; ++i) vec = vec && aligned(p.x[i], V, sizeof(T), p.L, p.T);
+  for (int i = 0; i < (p.heads > p.heads0 ? 2 : 1); ++i)
+    vec = vec && aligned(p.x[i], V, sizeof(T), p.L, p.T);
   if (vec)
     return inter ? launch_rope_t<T, V, true>(p, copy_tail, num_sms, s)
                  : launch_rope_t<T, V, false>(p, copy_tail, num_sms, s);
@@ -212,7 +226,6 @@ cudaError_t launch_rope_d(const RopeParams& p, bool inter, bool copy_tail, int n
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
   RopeParams p{};
-  p.n_x = a.n_x;
   bool copy_tail = false;
   for (int i = 0; i < a.n_x; ++i) {
     p.x[i] = a.x[i];
@@ -226,8 +239,9 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
   p.factor = a.factor;
   p.inverse = a.inverse;
   p.D = a.D; p.rd = a.rd; p.L = a.n_layers; p.T = a.n_tokens;
-  p.rows_x0 = a.n_layers * a.x[0].heads;
-  p.rows = p.rows_x0 + (a.n_x > 1 ? a.n_layers * a.x[1].heads : 0);
+  p.heads0 = a.x[0].heads;
+  p.heads = p.heads0 + (a.n_x > 1 ? a.x[1].heads : 0);
+  if ((long long)p.L * p.heads > 0x0FFFFFFF) return cudaErrorInvalidValue;
   switch (a.dtype) {
     case SSA_BF16: return launch_rope_d<__nv_bfloat16>(p, a.interleaved, copy_tail, a.num_sms, s);
     case SSA_F16: return launch_rope_d<__half>(p, a.interleaved, copy_tail, a.num_sms, s);
