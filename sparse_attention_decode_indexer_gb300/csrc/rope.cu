@@ -12,11 +12,12 @@
 // of a turn, goes to sincospif.
 //
 // What bounds it: each element read and written once, HBM (3 flop per 4
-// bytes).  The angles are shared by all layers and heads of a token, so a CTA
-// serves whole tokens: its threads start their first loads, then put the
-// tokens' cos and sin into shared memory, and all rotate with 16-byte
-// accesses.  Few tokens (a decode step) split a token's layers and heads over
-// more CTAs, each of which computes the rd/2 pairs again.
+// bytes).  The angles are shared by all layers and heads of a token, so a warp
+// serves one token: its lanes start their first loads, compute the token's cos
+// and sin once (a pair or more per lane, exchanged through shared memory), and
+// then only move and rotate 16-byte pieces.  Few tokens (a decode step) split
+// a token's layers and heads over more warps, each of which computes the rd/2
+// pairs again.
 #include <cmath>
 #include <cuda_fp16.h>
 
@@ -27,7 +28,6 @@ namespace ssa {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 4;           // rows in flight per thread
 
 template <typename T> struct Conv;
 template <> struct Conv<float> {
@@ -67,54 +67,57 @@ struct RopeParams {
   int pos64, inverse, D, rd, L, T;
   int heads0, heads;                     // of q, of both
   int u_rot, units;                      // units of a row that turn, and with the tail
-  int lanes_row, rows_pass;              // threads on a row, rows side by side in a CTA
-  int tokens, rows;                      // of one CTA's group: tokens, (token, layer, head) rows
-  int per_cta;                           // rows of one CTA
-  int dt, dl, dh;                        // rows_pass rows on, as tokens, layers, heads
+  int lanes_row, rows_pass;              // lanes on a row, rows side by side in a warp
+  int split, per_warp;                   // warps on one token, rows of one of them
+  int dl, dh;                            // rows_pass rows on, as layers and heads
 };
 
-// A unit is what a thread moves at once: V elements of each half of a head
-// (or one pair), INTER: V elements that hold V / 2 pairs (or one pair, V = 1).
-// A thread keeps its unit of the head and walks over (token, layer, head)
-// rows, so that an access costs a few additions.
+// Rows in flight per lane: four 16-byte loads.
+template <int NA> constexpr int rope_unroll() { return NA == 1 ? 4 : 2; }
+
+// A unit is what a lane moves at once: V elements of each half of a head (or
+// one pair), INTER: V elements that hold V / 2 pairs (or one pair, V = 1).  A
+// lane keeps its unit, and its cos and sin, and walks over the token's
+// (layer, head) rows.
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
-  extern __shared__ float2 s_cs[];       // [tokens][rd / 2]
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams p) {
+  extern __shared__ float2 s_cs[];       // [warps][rd / 2]
   using A = Vec<T, V>;
   constexpr int NA = (INTER && V > 1) ? 1 : 2;      // accesses of a unit
   constexpr int NP = (INTER && V > 1) ? V / 2 : V;  // pairs of a unit
+  constexpr int NR = rope_unroll<NA>();
   pdl_trigger();
   pdl_wait();
-  const int tid = threadIdx.x, half = p.rd / 2;
-  const int token0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - token0);
-  const int r1 = min((int)(blockIdx.y + 1) * p.per_cta, nt * p.L * p.heads);
-  const int lane = tid % p.lanes_row, first = tid / p.lanes_row;
-  const int rows_pass = first < p.rows_pass ? p.rows_pass : 0;     // the threads left over idle
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = p.rd / 2;
+  const long long gw = (long long)blockIdx.x * (kRopeThreads / 32) + warp;
+  const long long tok = gw / p.split;
+  if (tok >= p.T) return;
+  const int part = (int)(gw - tok * p.split);
+  float2* cs_w = s_cs + warp * half;
+  const int col = lane % p.lanes_row, first = lane / p.lanes_row;
+  const int r1 = min((part + 1) * p.per_warp, p.L * p.heads);
 
   bool have_table = false;
   for (int w0 = 0; w0 < p.units; w0 += p.lanes_row) {
-    const int w = w0 + lane;
-    const bool turns = w < p.u_rot, on = w < p.units && rows_pass;
+    const int w = w0 + col;
+    const bool turns = w < p.u_rot;
     // this unit's first element, and the distance to its second access
     const int e = turns ? (INTER ? w * NP * 2 : w * V) : p.rd + (w - p.u_rot) * V;
     const int step = INTER ? V : half;
-    int r = blockIdx.y * p.per_cta + first;
-    int t = r / (p.L * p.heads), l = (r - t * p.L * p.heads) / p.heads;
-    int h = r - (t * p.L + l) * p.heads;
-    const int rounds = (p.per_cta + p.rows_pass * kRopeUnroll - 1) / (p.rows_pass * kRopeUnroll);
-    for (int round = 0; round < rounds; ++round) {
-      A a[kRopeUnroll][NA];
-      T* out[kRopeUnroll];
-      int tt[kRopeUnroll];
+    // the lanes left over idle
+    int r = w < p.units && first < p.rows_pass ? part * p.per_warp + first : r1;
+    int l = r / p.heads, h = r - l * p.heads;
+    float2 cs[NP];
+    for (int base = part * p.per_warp; base < r1; base += p.rows_pass * NR) {
+      A a[NR][NA];
+      T* out[NR];
 #pragma unroll
-      for (int i = 0; i < kRopeUnroll; ++i) {
+      for (int i = 0; i < NR; ++i) {
         out[i] = nullptr;
-        tt[i] = t;
-        if (on && r < r1) {
+        if (r < r1) {
           const bool second = h >= p.heads0;
           const RopeTensor& x = p.x[second];
           const int hh = second ? h - p.heads0 : h;
-          const int64_t tok = token0 + t;
           const T* in = static_cast<const T*>(x.in) + l * x.is[0] + tok * x.is[1] + hh * x.is[2] + e;
           out[i] = static_cast<T*>(x.out) + l * x.os[0] + tok * x.os[1] + hh * x.os[2] + e;
           a[i][0] = *reinterpret_cast<const A*>(in);
@@ -123,26 +126,26 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
         r += p.rows_pass;
         h += p.dh;
         l += p.dl;
-        t += p.dt;
         if (h >= p.heads) { h -= p.heads; ++l; }
-        if (l >= p.L) { l -= p.L; ++t; }
       }
       if (!have_table) {                  // while the first loads are in flight
-        for (int i = tid; i < nt * half; i += kRopeThreads) {
-          const int k = i / half, j = i - k * half;
-          const int64_t raw = p.pos64 ? static_cast<const int64_t*>(p.pos)[token0 + k]
-                                      : (int64_t) static_cast<const int32_t*>(p.pos)[token0 + k];
-          const float2 cs = turn((uint64_t)raw + (uint64_t)p.offset, p.freq[j]);
-          s_cs[i] = make_float2(cs.x * p.factor, (p.inverse ? -cs.y : cs.y) * p.factor);
+        const int64_t raw = p.pos64 ? static_cast<const int64_t*>(p.pos)[tok]
+                                    : (int64_t) static_cast<const int32_t*>(p.pos)[tok];
+        for (int i = lane; i < half; i += 32) {
+          const float2 t = turn((uint64_t)raw + (uint64_t)p.offset, p.freq[i]);
+          cs_w[i] = make_float2(t.x * p.factor, (p.inverse ? -t.y : t.y) * p.factor);
         }
-        __syncthreads();
+        __syncwarp();
         have_table = true;
       }
+      if (base == part * p.per_warp && turns) {
 #pragma unroll
-      for (int i = 0; i < kRopeUnroll; ++i) {
+        for (int k = 0; k < NP; ++k) cs[k] = cs_w[w * NP + k];
+      }
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
         if (!out[i]) continue;
         if (turns) {
-          const float2* cs = s_cs + tt[i] * half + w * NP;
 #pragma unroll
           for (int k = 0; k < NP; ++k) {
             T& ea = NA == 1 ? a[i][0].x[2 * k % V] : a[i][0].x[k % V];
@@ -175,35 +178,24 @@ cudaError_t launch_rope_t(RopeParams p, bool copy_tail, int num_sms, cudaStream_
   const int np = (INTER && V > 1) ? V / 2 : V;                 // pairs per unit
   p.u_rot = p.rd / 2 / np;
   p.units = p.u_rot + (copy_tail ? (p.D - p.rd) / V : 0);
-  p.lanes_row = p.units < kRopeThreads ? p.units : kRopeThreads;
-  p.rows_pass = kRopeThreads / p.lanes_row;
-  const long long row_tok = (long long)p.L * p.heads;          // rows of one token
-  const long long round = (long long)p.rows_pass * kRopeUnroll;
-  // Tokens of a CTA: as many as give every thread one round of loads (at most
-  // 8, and 16 KB of table), as long as the grid still holds 4 CTAs per SM; one
-  // token's rows are split over CTAs, down to one pass, where the tokens alone
-  // give fewer than that.
-  const long long want = 4LL * num_sms;
-  long long tokens = (round + row_tok - 1) / row_tok;
-  if (tokens > 8) tokens = 8;
-  while (tokens > 1 && tokens * p.rd / 2 * (long long)sizeof(float2) > 16384) --tokens;
-  if (tokens > p.T / want) tokens = p.T / want;
-  if (tokens < 1) tokens = 1;
-  p.tokens = (int)tokens;
-  p.rows = (int)(tokens * row_tok);
-  const long long groups = (p.T + tokens - 1) / tokens;
-  long long split = (want + groups - 1) / groups;
-  const long long most = (p.rows + p.rows_pass - 1) / p.rows_pass;
+  p.lanes_row = p.units < 32 ? p.units : 32;
+  p.rows_pass = 32 / p.lanes_row;
+  const int rows = p.L * p.heads;                              // of one token
+  // a warp per token where the tokens fill the machine (32 warps per SM), else
+  // a token's rows over several warps, down to one pass each
+  const long long want = 32LL * num_sms;
+  long long split = (want + p.T - 1) / p.T;
+  const long long most = (rows + p.rows_pass - 1) / p.rows_pass;
   if (split > most) split = most;
-  if (split > 65535) split = 65535;
-  p.per_cta = (int)((p.rows + split - 1) / split);
-  const unsigned gy = (unsigned)((p.rows + p.per_cta - 1) / p.per_cta);
-  p.dt = (int)(p.rows_pass / row_tok);
-  const int rest = (int)(p.rows_pass % row_tok);
-  p.dl = rest / p.heads;
-  p.dh = rest % p.heads;
-  cudaError_t e = launch_pdl(rope_kernel<T, V, INTER>, dim3((unsigned)groups, gy),
-                             dim3(kRopeThreads), (size_t)tokens * p.rd / 2 * sizeof(float2), s, p);
+  p.per_warp = (int)(((rows + split - 1) / split + p.rows_pass - 1) / p.rows_pass * p.rows_pass);
+  p.split = (rows + p.per_warp - 1) / p.per_warp;
+  p.dl = p.rows_pass / p.heads;
+  p.dh = p.rows_pass % p.heads;
+  const long long warps = (long long)p.T * p.split;
+  const long long ctas = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  cudaError_t e = launch_pdl(rope_kernel<T, V, INTER>, dim3((unsigned)ctas), dim3(kRopeThreads),
+                             (size_t)(kRopeThreads / 32) * p.rd / 2 * sizeof(float2), s, p);
   count_launch();
   return e;
 }
