@@ -19,6 +19,7 @@
 // a token's layers and heads over more warps, each of which computes the rd/2
 // pairs again.
 #include <cmath>
+#include <type_traits>
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -28,23 +29,129 @@ namespace ssa {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeCtas = 4;             // per SM
+constexpr int kRopeRows = 4;             // accesses in flight per lane
 
-template <typename T> struct Conv;
-template <> struct Conv<float> {
-  static __device__ __forceinline__ float in(float x) { return x; }
-  static __device__ __forceinline__ float out(float x) { return x; }
-};
-template <> struct Conv<__half> {
-  static __device__ __forceinline__ float in(__half x) { return __half2float(x); }
-  static __device__ __forceinline__ __half out(float x) { return __float2half_rn(x); }
-};
-template <> struct Conv<__nv_bfloat16> {
-  static __device__ __forceinline__ float in(__nv_bfloat16 x) { return __bfloat162float(x); }
-  static __device__ __forceinline__ __nv_bfloat16 out(float x) { return __float2bfloat16_rn(x); }
+// Two 16-bit elements of a word as floats, and back (one rounding each).
+template <typename T> __device__ __forceinline__ float2 unpack(uint32_t w);
+template <> __device__ __forceinline__ float2 unpack<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <> __device__ __forceinline__ float2 unpack<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<__half2*>(&w));
+}
+template <typename T> __device__ __forceinline__ uint32_t pack(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float lo, float hi) {
+  return pack_bf16(lo, hi);
+}
+template <> __device__ __forceinline__ uint32_t pack<__half>(float lo, float hi) {
+  return pack_f16(lo, hi);
+}
+
+__device__ __forceinline__ void rotate(float& a, float& b, float2 cs) {
+  const float x = a, y = b;
+  a = x * cs.x - y * cs.y;
+  b = y * cs.x + x * cs.y;
+}
+
+// What a lane moves at once (a unit): with V > 1 16 bytes of each half of a
+// head, or 16 bytes of interleaved pairs; with V = 1 one pair.
+template <typename T, int V, bool INTER> struct Unit {
+  static constexpr int NP = V;                      // pairs
+  static constexpr int NA = 2;                      // accesses
+  uint4 a, b;
+  __device__ __forceinline__ void load(const T* p, int step, bool two) {
+    a = *reinterpret_cast<const uint4*>(p);
+    if (two) b = *reinterpret_cast<const uint4*>(p + step);
+  }
+  __device__ __forceinline__ void store(T* p, int step, bool two) const {
+    *reinterpret_cast<uint4*>(p) = a;
+    if (two) *reinterpret_cast<uint4*>(p + step) = b;
+  }
+  __device__ __forceinline__ void turn(const float2* cs) {
+    uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        float u = __uint_as_float(x[i]), v = __uint_as_float(y[i]);
+        rotate(u, v, cs[i]);
+        x[i] = __float_as_uint(u);
+        y[i] = __float_as_uint(v);
+      } else {
+        float2 u = unpack<T>(x[i]), v = unpack<T>(y[i]);
+        rotate(u.x, v.x, cs[2 * i]);
+        rotate(u.y, v.y, cs[2 * i + 1]);
+        x[i] = pack<T>(u.x, u.y);
+        y[i] = pack<T>(v.x, v.y);
+      }
+    }
+    a = make_uint4(x[0], x[1], x[2], x[3]);
+    b = make_uint4(y[0], y[1], y[2], y[3]);
+  }
 };
 
-// V elements moved as one access (16 bytes, or one element)
-template <typename T, int V> struct alignas(sizeof(T) * V) Vec { T x[V]; };
+template <typename T, int V> struct Unit<T, V, true> {
+  static constexpr int NP = V / 2;
+  static constexpr int NA = 1;
+  uint4 a;
+  __device__ __forceinline__ void load(const T* p, int, bool) {
+    a = *reinterpret_cast<const uint4*>(p);
+  }
+  __device__ __forceinline__ void store(T* p, int, bool) const { *reinterpret_cast<uint4*>(p) = a; }
+  __device__ __forceinline__ void turn(const float2* cs) {
+    uint32_t x[4] = {a.x, a.y, a.z, a.w};
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float u = __uint_as_float(x[2 * i]), v = __uint_as_float(x[2 * i + 1]);
+        rotate(u, v, cs[i]);
+        x[2 * i] = __float_as_uint(u);
+        x[2 * i + 1] = __float_as_uint(v);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float2 u = unpack<T>(x[i]);
+        rotate(u.x, u.y, cs[i]);
+        x[i] = pack<T>(u.x, u.y);
+      }
+    }
+    a = make_uint4(x[0], x[1], x[2], x[3]);
+  }
+};
+
+template <typename T> __device__ __forceinline__ float one_in(T x) {
+  if constexpr (sizeof(T) == 4) return x;
+  else if constexpr (std::is_same_v<T, __half>) return __half2float(x);
+  else return __bfloat162float(x);
+}
+template <typename T> __device__ __forceinline__ T one_out(float x) {
+  if constexpr (sizeof(T) == 4) return x;
+  else if constexpr (std::is_same_v<T, __half>) return __float2half_rn(x);
+  else return __float2bfloat16_rn(x);
+}
+
+template <typename T> struct Pair {
+  static constexpr int NP = 1;
+  static constexpr int NA = 2;
+  T a, b;
+  __device__ __forceinline__ void load(const T* p, int step, bool two) {
+    a = p[0];
+    if (two) b = p[step];
+  }
+  __device__ __forceinline__ void store(T* p, int step, bool two) const {
+    p[0] = a;
+    if (two) p[step] = b;
+  }
+  __device__ __forceinline__ void turn(const float2* cs) {
+    float u = one_in(a), v = one_in(b);
+    rotate(u, v, *cs);
+    a = one_out<T>(u);
+    b = one_out<T>(v);
+  }
+};
+template <typename T> struct Unit<T, 1, false> : Pair<T> {};
+template <typename T> struct Unit<T, 1, true> : Pair<T> {};
 
 // (cos, sin) of pos * f turns, f a 64-bit fraction
 __device__ __forceinline__ float2 turn(uint64_t pos, uint64_t f) {
@@ -58,34 +165,35 @@ __device__ __forceinline__ float2 turn(uint64_t pos, uint64_t f) {
   return make_float2(c, s);
 }
 
+// One of q and k, as the lanes of a warp walk over its (layer, head) rows.
+struct RopeRows {
+  RopeTensor x;
+  int per_warp;                          // rows of one warp
+  int dh;                                // heads of a step of rows_pass rows, modulo x.heads
+  int64_t in_step, out_step;             // elements of such a step ...
+  int64_t in_wrap, out_wrap;             // ... and more where it runs past the last head
+};
+
 struct RopeParams {
-  RopeTensor x[2];
+  RopeRows x[2];
+  int n_x;
   const uint64_t* freq;
   const void* pos;
   int64_t offset;
   float factor;
   int pos64, inverse, D, rd, L, T;
-  int heads0, heads;                     // of q, of both
   int u_rot, units;                      // units of a row that turn, and with the tail
   int lanes_row, rows_pass;              // lanes on a row, rows side by side in a warp
-  int split, per_warp;                   // warps on one token, rows of one of them
-  int dl, dh;                            // rows_pass rows on, as layers and heads
+  int split;                             // warps on one token
 };
 
-// Rows in flight per lane: four 16-byte loads.
-template <int NA> constexpr int rope_unroll() { return NA == 1 ? 4 : 2; }
-
-// A unit is what a lane moves at once: V elements of each half of a head (or
-// one pair), INTER: V elements that hold V / 2 pairs (or one pair, V = 1).  A
-// lane keeps its unit, and its cos and sin, and walks over the token's
-// (layer, head) rows.
+// A lane keeps its unit of the head, and its cos and sin, and walks over the
+// token's (layer, head) rows, a few of them in flight: up to 64 bytes.
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const RopeParams p) {
   extern __shared__ float2 s_cs[];       // [warps][rd / 2]
-  using A = Vec<T, V>;
-  constexpr int NA = (INTER && V > 1) ? 1 : 2;      // accesses of a unit
-  constexpr int NP = (INTER && V > 1) ? V / 2 : V;  // pairs of a unit
-  constexpr int NR = rope_unroll<NA>();
+  using U = Unit<T, V, INTER>;
+  constexpr int NP = U::NP, NR = kRopeRows / U::NA;
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = p.rd / 2;
@@ -95,68 +203,65 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
   const int part = (int)(gw - tok * p.split);
   float2* cs_w = s_cs + warp * half;
   const int col = lane % p.lanes_row, first = lane / p.lanes_row;
-  const int r1 = min((part + 1) * p.per_warp, p.L * p.heads);
 
   bool have_table = false;
   for (int w0 = 0; w0 < p.units; w0 += p.lanes_row) {
     const int w = w0 + col;
     const bool turns = w < p.u_rot;
     // this unit's first element, and the distance to its second access
-    const int e = turns ? (INTER ? w * NP * 2 : w * V) : p.rd + (w - p.u_rot) * V;
-    const int step = INTER ? V : half;
-    // the lanes left over idle
-    int r = w < p.units && first < p.rows_pass ? part * p.per_warp + first : r1;
-    int l = r / p.heads, h = r - l * p.heads;
+    const int e = turns ? (INTER ? w * NP * 2 : w * NP) : p.rd + (w - p.u_rot) * V;
+    const int step = INTER ? 1 : half;
+    const bool on = w < p.units && first < p.rows_pass;           // the lanes left over idle
     float2 cs[NP];
-    for (int base = part * p.per_warp; base < r1; base += p.rows_pass * NR) {
-      A a[NR][NA];
-      T* out[NR];
+    bool have_cs = false;
+    for (int xi = 0; xi < p.n_x; ++xi) {
+      const RopeRows& x = p.x[xi];
+      const int heads = x.x.heads, rows = p.L * heads;
+      const int base = part * x.per_warp, r1 = min(base + x.per_warp, rows);
+      int left = on ? r1 - base - first : 0;                      // rows from this lane's on
+      const int l = (base + first) / heads;
+      int h = base + first - l * heads;
+      const T* in = static_cast<const T*>(x.x.in) + l * x.x.is[0] + tok * x.x.is[1] + h * x.x.is[2] + e;
+      T* out = static_cast<T*>(x.x.out) + l * x.x.os[0] + tok * x.x.os[1] + h * x.x.os[2] + e;
+      for (int r = base; r < r1; r += p.rows_pass * NR) {
+        U u[NR];
+        uint32_t wraps = 0;
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        out[i] = nullptr;
-        if (r < r1) {
-          const bool second = h >= p.heads0;
-          const RopeTensor& x = p.x[second];
-          const int hh = second ? h - p.heads0 : h;
-          const T* in = static_cast<const T*>(x.in) + l * x.is[0] + tok * x.is[1] + hh * x.is[2] + e;
-          out[i] = static_cast<T*>(x.out) + l * x.os[0] + tok * x.os[1] + hh * x.os[2] + e;
-          a[i][0] = *reinterpret_cast<const A*>(in);
-          if (NA > 1 && turns) a[i][NA - 1] = *reinterpret_cast<const A*>(in + step);
-        }
-        r += p.rows_pass;
-        h += p.dh;
-        l += p.dl;
-        if (h >= p.heads) { h -= p.heads; ++l; }
-      }
-      if (!have_table) {                  // while the first loads are in flight
-        const int64_t raw = p.pos64 ? static_cast<const int64_t*>(p.pos)[tok]
-                                    : (int64_t) static_cast<const int32_t*>(p.pos)[tok];
-        for (int i = lane; i < half; i += 32) {
-          const float2 t = turn((uint64_t)raw + (uint64_t)p.offset, p.freq[i]);
-          cs_w[i] = make_float2(t.x * p.factor, (p.inverse ? -t.y : t.y) * p.factor);
-        }
-        __syncwarp();
-        have_table = true;
-      }
-      if (base == part * p.per_warp && turns) {
-#pragma unroll
-        for (int k = 0; k < NP; ++k) cs[k] = cs_w[w * NP + k];
-      }
-#pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        if (!out[i]) continue;
-        if (turns) {
-#pragma unroll
-          for (int k = 0; k < NP; ++k) {
-            T& ea = NA == 1 ? a[i][0].x[2 * k % V] : a[i][0].x[k % V];
-            T& eb = NA == 1 ? a[i][0].x[(2 * k + 1) % V] : a[i][NA - 1].x[k % V];
-            const float x = Conv<T>::in(ea), y = Conv<T>::in(eb);
-            ea = Conv<T>::out(x * cs[k].x - y * cs[k].y);
-            eb = Conv<T>::out(y * cs[k].x + x * cs[k].y);
+        for (int i = 0; i < NR; ++i) {
+          if (left > i * p.rows_pass) u[i].load(in, step, turns);
+          in += x.in_step;
+          h += x.dh;
+          if (h >= heads) {
+            h -= heads;
+            in += x.in_wrap;
+            wraps |= 1u << i;
           }
-          if (NA > 1) *reinterpret_cast<A*>(out[i] + step) = a[i][NA - 1];
         }
-        *reinterpret_cast<A*>(out[i]) = a[i][0];
+        if (!have_table) {                // while the first loads are in flight
+          const int64_t raw = p.pos64 ? static_cast<const int64_t*>(p.pos)[tok]
+                                      : (int64_t) static_cast<const int32_t*>(p.pos)[tok];
+          for (int i = lane; i < half; i += 32) {
+            const float2 t = turn((uint64_t)raw + (uint64_t)p.offset, p.freq[i]);
+            cs_w[i] = make_float2(t.x * p.factor, (p.inverse ? -t.y : t.y) * p.factor);
+          }
+          __syncwarp();
+          have_table = true;
+        }
+        if (!have_cs) {
+          have_cs = true;
+#pragma unroll
+          for (int k = 0; k < NP; ++k) cs[k] = turns ? cs_w[w * NP + k] : make_float2(1.0f, 0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          if (left > i * p.rows_pass) {
+            if (turns) u[i].turn(cs);
+            u[i].store(out, step, turns);
+          }
+          out += x.out_step;
+          if (wraps >> i & 1) out += x.out_wrap;
+        }
+        left -= NR * p.rows_pass;
       }
     }
   }
@@ -180,17 +285,27 @@ cudaError_t launch_rope_t(RopeParams p, bool copy_tail, int num_sms, cudaStream_
   p.units = p.u_rot + (copy_tail ? (p.D - p.rd) / V : 0);
   p.lanes_row = p.units < 32 ? p.units : 32;
   p.rows_pass = 32 / p.lanes_row;
-  const int rows = p.L * p.heads;                              // of one token
   // a warp per token where the tokens fill the machine (32 warps per SM), else
   // a token's rows over several warps, down to one pass each
+  long long rows = 0;                                          // of one token
+  for (int i = 0; i < p.n_x; ++i) rows += (long long)p.L * p.x[i].x.heads;
   const long long want = 32LL * num_sms;
   long long split = (want + p.T - 1) / p.T;
   const long long most = (rows + p.rows_pass - 1) / p.rows_pass;
   if (split > most) split = most;
-  p.per_warp = (int)(((rows + split - 1) / split + p.rows_pass - 1) / p.rows_pass * p.rows_pass);
-  p.split = (rows + p.per_warp - 1) / p.per_warp;
-  p.dl = p.rows_pass / p.heads;
-  p.dh = p.rows_pass % p.heads;
+  p.split = (int)split;
+  for (int i = 0; i < p.n_x; ++i) {
+    RopeRows& x = p.x[i];
+    const long long n = (long long)p.L * x.x.heads;
+    const long long per = (n + split - 1) / split;
+    x.per_warp = (int)((per + p.rows_pass - 1) / p.rows_pass * p.rows_pass);
+    const int dl = p.rows_pass / x.x.heads;
+    x.dh = p.rows_pass % x.x.heads;
+    x.in_step = dl * x.x.is[0] + x.dh * x.x.is[2];
+    x.out_step = dl * x.x.os[0] + x.dh * x.x.os[2];
+    x.in_wrap = x.x.is[0] - x.x.heads * x.x.is[2];
+    x.out_wrap = x.x.os[0] - x.x.heads * x.x.os[2];
+  }
   const long long warps = (long long)p.T * p.split;
   const long long ctas = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
@@ -205,8 +320,7 @@ cudaError_t launch_rope_d(const RopeParams& p, bool inter, bool copy_tail, int n
                           cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   bool vec = p.D % V == 0 && (inter ? p.rd : p.rd / 2) % V == 0;
-  for (int i = 0; i < (p.heads > p.heads0 ? 2 : 1); ++i)
-    vec = vec && aligned(p.x[i], V, sizeof(T), p.L, p.T);
+  for (int i = 0; i < p.n_x; ++i) vec = vec && aligned(p.x[i].x, V, sizeof(T), p.L, p.T);
   if (vec)
     return inter ? launch_rope_t<T, V, true>(p, copy_tail, num_sms, s)
                  : launch_rope_t<T, V, false>(p, copy_tail, num_sms, s);
@@ -220,7 +334,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
   RopeParams p{};
   bool copy_tail = false;
   for (int i = 0; i < a.n_x; ++i) {
-    p.x[i] = a.x[i];
+    p.x[i].x = a.x[i];
     copy_tail = copy_tail || (a.x[i].in != a.x[i].out);
   }
   copy_tail = copy_tail && a.rd < a.D;
@@ -231,9 +345,9 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
   p.factor = a.factor;
   p.inverse = a.inverse;
   p.D = a.D; p.rd = a.rd; p.L = a.n_layers; p.T = a.n_tokens;
-  p.heads0 = a.x[0].heads;
-  p.heads = p.heads0 + (a.n_x > 1 ? a.x[1].heads : 0);
-  if ((long long)p.L * p.heads > 0x0FFFFFFF) return cudaErrorInvalidValue;
+  p.n_x = a.n_x;
+  for (int i = 0; i < a.n_x; ++i)
+    if ((long long)a.n_layers * a.x[i].heads > 0x0FFFFFFF) return cudaErrorInvalidValue;
   switch (a.dtype) {
     case SSA_BF16: return launch_rope_d<__nv_bfloat16>(p, a.interleaved, copy_tail, a.num_sms, s);
     case SSA_F16: return launch_rope_d<__half>(p, a.interleaved, copy_tail, a.num_sms, s);
