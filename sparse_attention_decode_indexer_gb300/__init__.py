@@ -21,6 +21,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -76,6 +77,9 @@ class SsaRequests(ctypes.Structure):
 class SsaRopeTensor(ctypes.Structure):
     _fields_ = [("inp", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int),
                 ("in_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3)]
+
+
+_pack_rope = struct.Struct("@PPi4x6q").pack     # an SsaRopeTensor's bytes
 
 
 _lib = None
@@ -138,7 +142,7 @@ def lib():
         f64 = ctypes.c_double
         L.ssa_rope.restype = i32
         L.ssa_rope.argtypes = [i32, i32, i32, i32, i32, vp, ctypes.c_float, i32, i32, vp, i32,
-                               ctypes.c_int64, P(SsaRopeTensor), P(SsaRopeTensor), vp]
+                               ctypes.c_int64, vp, vp, vp]
         L.ssa_rope_frequencies.restype = i32
         L.ssa_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64,
                                            P(ctypes.c_uint64), P(f64)]
@@ -165,15 +169,15 @@ def _check(code: int):
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    return ctypes.c_void_p(t.data_ptr())
+    """A tensor's address (None for a null pointer)."""
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
+    """A stream's handle; the current stream's without building a Stream."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def max_sel_pages(block_topk: int) -> int:
@@ -560,24 +564,26 @@ class RopePlan:
         # two's complement: the same 64 bits
         self.freq = torch.tensor([f - (1 << 64) if f >= 1 << 63 else f for f in freq],
                                  dtype=torch.int64, device=device)
+        self._freq = self.freq.data_ptr()
 
 
-def _rope_tensor(plan, name, x, out, T):
-    """The C view of one tensor: [n_layers][T][H][D] or [T][H][D], any strides
-    but the last."""
+def _rope_tensor(plan, name, x, out, shape):
+    """The C view of one tensor, whose shape but for the heads is `shape`:
+    any strides but the last."""
     if out is None:
         out = x
-    if x.dim() not in (3, 4) or x.shape[-3] != T or x.shape[-1] != plan.head_dim:
-        raise ValueError(f"{name}: [n_layers][{T}][heads][{plan.head_dim}], got {tuple(x.shape)}")
-    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
-        raise ValueError(f"{name}_out: shape, type or device other than {name}'s")
+    got, lead = x.shape, len(shape) == 4
+    if len(got) != len(shape) or got[:-2] != shape[:-2] or got[-1] != shape[-1]:
+        raise ValueError(f"{name}: [n_layers][T][heads][D] or [T][heads][D] with (T, D) of the "
+                         f"positions and the plan and the same layers for q and k, got "
+                         f"{tuple(got)}")
     st, so = x.stride(), out.stride()
-    if x.numel() and (st[-1] != 1 or so[-1] != 1):
+    if out is not x and (out.shape != got or out.dtype != x.dtype or out.device != x.device):
+        raise ValueError(f"{name}_out: shape, type or device other than {name}'s")
+    if st[-1] != 1 or so[-1] != 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
-    lead = x.dim() == 4
-    return SsaRopeTensor(x.data_ptr(), out.data_ptr(), x.shape[-2],
-                         (ctypes.c_int64 * 3)(st[0] if lead else 0, st[-3], st[-2]),
-                         (ctypes.c_int64 * 3)(so[0] if lead else 0, so[-3], so[-2]))
+    return _pack_rope(x.data_ptr(), out.data_ptr(), got[-2], st[0] if lead else 0, st[-3], st[-2],
+                      so[0] if lead else 0, so[-3], so[-2])
 
 
 def ssa_rope(plan: RopePlan, positions, q=None, k=None, q_out=None, k_out=None, offset: int = 0,
@@ -589,28 +595,26 @@ def ssa_rope(plan: RopePlan, positions, q=None, k=None, q_out=None, k_out=None, 
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k")
-    if x.dtype not in _ROPE_DTYPES:
-        raise ValueError(f"dtype {x.dtype}: bfloat16, float16 or float32")
-    if positions.dim() != 1 or positions.dtype not in (torch.int32, torch.int64) or \
+    dtype = _ROPE_DTYPES.get(x.dtype)
+    if dtype is None or (k is not None and k.dtype != x.dtype):
+        raise ValueError("q and k: bfloat16, float16 or float32, the same")
+    wide = positions.dtype == torch.int64
+    if positions.dim() != 1 or not (wide or positions.dtype == torch.int32) or \
             not positions.is_contiguous():
         raise ValueError("positions: a contiguous [T] int32 or int64 tensor")
+    dev = plan.freq.device
+    if x.device != dev or positions.device != dev or (k is not None and k.device != dev):
+        raise ValueError(f"q, k and positions: on the plan's device, {dev}")
     T = positions.shape[0]
-    n_layers = x.shape[0] if x.dim() == 4 else 1
-    for t in (q, k):
-        if t is not None and (t.dtype != x.dtype or t.dim() != x.dim() or
-                              (t.dim() == 4 and t.shape[0] != n_layers)):
-            raise ValueError("q and k: the same type and layers")
-    for t in (q, k, positions):
-        if t is not None and t.device != plan.freq.device:
-            raise ValueError(f"tensors on {t.device}, the plan on {plan.freq.device}")
-    cq = _rope_tensor(plan, "q", q, q_out, T) if q is not None else None
-    ck = _rope_tensor(plan, "k", k, k_out, T) if k is not None else None
-    if x.numel() == 0:
+    shape = (x.shape[0], T, 0, plan.head_dim) if x.dim() == 4 else (T, 0, plan.head_dim)
+    cq = _rope_tensor(plan, "q", q, q_out, shape) if q is not None else None
+    ck = _rope_tensor(plan, "k", k, k_out, shape) if k is not None else None
+    n_layers = shape[0] if len(shape) == 4 else 1
+    if T == 0 or n_layers == 0:
         return
-    _check(lib().ssa_rope(_ROPE_DTYPES[x.dtype], plan.head_dim, plan.rotary_dim,
-                          plan.interleaved, inverse, plan.freq.data_ptr(), plan.factor, n_layers,
-                          T, positions.data_ptr(), positions.dtype == torch.int64, offset,
-                          cq, ck, _stream(stream)))
+    _check(lib().ssa_rope(dtype, plan.head_dim, plan.rotary_dim, plan.interleaved, inverse,
+                          plan._freq, plan.factor, n_layers, T, positions.data_ptr(), wide,
+                          offset, cq, ck, _stream(stream)))
 
 
 def ssa_selftest_bounded_wait(status, stream=None):

@@ -81,8 +81,9 @@ def test_refusals(ssa):
     p = 0x10000
     t = lambda i=p, o=p, h=2, ist=(0, 256, 128), ost=(0, 256, 128): ssa.SsaRopeTensor(  # noqa: E731
         i, o, h, (ctypes.c_int64 * 3)(*ist), (ctypes.c_int64 * 3)(*ost))
+    ref = lambda x: None if x is None else ctypes.byref(x)  # noqa: E731
     call = lambda dtype=0, D=128, rd=128, freq=p, L=1, T=4, pos=p, q=t(), k=None: lib.ssa_rope(  # noqa: E731
-        dtype, D, rd, 0, 0, freq, 1.0, L, T, pos, 0, 0, q, k, None)
+        dtype, D, rd, 0, 0, freq, 1.0, L, T, pos, 0, 0, ref(q), k, None)
     assert call(dtype=3) == UNSUPPORTED and call(D=4096, rd=2048) == UNSUPPORTED
     for bad in (dict(rd=130), dict(rd=5), dict(rd=0), dict(freq=None), dict(pos=None), dict(L=0), dict(T=-1),
                 dict(q=None), dict(q=t(h=0)), dict(q=t(i=None)), dict(q=t(o=None)), dict(q=t(i=p + 1)),
