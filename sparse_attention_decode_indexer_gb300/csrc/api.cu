@@ -88,8 +88,8 @@ struct WsLayout {
   size_t scores, miss_page, miss_slot, n_miss, part_o, part_ml, tickets, idx_tickets;
   size_t pf_cand, pf_ncand, pf_miss_page, pf_miss_slot, pf_n_miss;   // ssa_prefetch_pages
   // the page calls
-  size_t pg_bt, pg_len, pg_bits, pg_list, pg_to, pg_map, pg_plan, pg_copy, pg_count, pg_ok,
-      pg_ticket;
+  size_t pg_bt, pg_len, pg_bits, pg_list, pg_to, pg_map, pg_from, pg_plan, pg_copy, pg_count,
+      pg_ok, pg_ticket;
   size_t total;
 };
 
@@ -120,6 +120,7 @@ WsLayout ws_layout(const Dims& d) {
   w.pg_list = off;   off += align256((size_t)d.Lp * 4);
   w.pg_to = off;     off += align256((size_t)d.Lp * 4);
   w.pg_map = off;    off += align256((size_t)d.Lp * 4);
+  w.pg_from = off;   off += align256((size_t)d.B * 8);
   w.pg_plan = off;   off += align256((size_t)d.B * 16);
   w.pg_copy = off;   off += align256((size_t)d.B * 8);
   w.pg_count = off;  off += 256;
@@ -139,7 +140,8 @@ PageWs page_ws(const Dims& d, void* ws) {
   return PageWs{at<int32_t>(ws, w.pg_bt),   at<int32_t>(ws, w.pg_len),
                 at<uint32_t>(ws, w.pg_bits), at<int32_t>(ws, w.pg_list),
                 at<int32_t>(ws, w.pg_to),   at<int32_t>(ws, w.pg_map),
-                at<char>(ws, w.pg_plan),    at<char>(ws, w.pg_copy),
+                at<char>(ws, w.pg_from),    at<char>(ws, w.pg_plan),
+                at<char>(ws, w.pg_copy),
                 at<int32_t>(ws, w.pg_count), at<int32_t>(ws, w.pg_ok),
                 at<int32_t>(ws, w.pg_ticket)};
 }
@@ -534,7 +536,7 @@ int ssa_fork_requests(const ssa_layout* lay, const ssa_cache* c, const ssa_reque
   if ((r = check_requests(req))) return r;
   if (!parent || !ws) return SSA_ERR_INVALID_ARG;
   cudaError_t e = launch_fork(d, *c, *req, parent, new_lens_opt, status, page_ws(d, ws),
-                              (cudaStream_t)stream);
+                              num_sms(), (cudaStream_t)stream);
   return e == cudaSuccess ? SSA_OK : fail_cuda(e);
 }
 

@@ -127,6 +127,7 @@ struct PageWs {
   int32_t* list;       // [Lp] new pages (fork), moved pages (compaction)
   int32_t* to;         // [Lp]
   int32_t* map;        // [Lp]
+  void* from;          // [B] int2
   void* plan;          // [B] int4
   void* copy;          // [B] int2
   int32_t* count;      // [2]
@@ -141,7 +142,7 @@ cudaError_t launch_copy_pages(const Dims& d, const ssa_cache& c, const int32_t* 
                               cudaStream_t s);
 cudaError_t launch_fork(const Dims& d, const ssa_cache& c, const ssa_requests& r,
                         const int32_t* parent, const int32_t* new_lens, int32_t* status,
-                        const PageWs& w, cudaStream_t s);
+                        const PageWs& w, int num_sms, cudaStream_t s);
 cudaError_t launch_compact(const Dims& d, const ssa_cache& c, const ssa_requests& r,
                            int32_t* moved_from, int32_t* moved_to, int32_t* n_moved,
                            int32_t* status, const PageWs& w, int num_sms, cudaStream_t s);

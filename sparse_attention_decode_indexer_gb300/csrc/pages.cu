@@ -11,12 +11,12 @@
 // it: with n_g rows continuing g and ref[g] - n_g other references left, the
 // lowest of those rows keeps g if no other reference is left, and every other
 // one gets a copy of it in a new page.  New pages are the lowest free ids, in
-// row order (a row's copy first, then its growth).  Three launches:
-//   count  each row's old references off, its new ones on (g counts once per
+// row order (a row's copy first, then its growth).  Two launches:
+//   plan   each row's old references off, its new ones on (g counts once per
 //          row that continues it, so a page is free exactly when its count is
-//          0); the old table kept aside;
-//   plan   one bit per free page; the last CTA to finish resolves the claims,
-//          scans the rows' needs and lists that many free pages;
+//          0), the old table kept aside; then the last CTA to finish marks the
+//          free pages, resolves the claims, scans the rows' needs and lists
+//          that many free pages;
 //   apply  the rows, and per layer the copies, the cleared slab rows of new
 //          pages and the slots of freed ones.
 //
@@ -37,7 +37,9 @@ namespace {
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 4;
 constexpr int kCopyChunk = kCopyThreads * kCopyUnroll;     // 16-byte units per CTA
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWords = 4096;         // words of page bits kept in shared memory
+constexpr int kPlanList = 1024;          // new pages kept there
 
 // The cache as the page calls see it.
 struct PageCache {
@@ -61,69 +63,101 @@ __device__ __forceinline__ int slot_at(const PageCache& c, int layer, int id) {
   return s >= 0 && s < c.S ? s : -1;
 }
 
-// One CTA's share of dst := src in one layer: chunk `x` of the concatenation
-// [K | V | slab sums | slab codes], with chunk 0 the scales and counts.
-// DST_SLOT: a pool slot that dst holds is written too.  POOL: pool and scale
-// blocks move (else only the mirror's and the slab).
+// dst := src in one layer: where the pages are, and their 16-byte units, the
+// concatenation [K | V | slab sums | slab codes] (the scales and counts apart).
+// DST_SLOT: a pool slot that dst holds is written too.  POOL: K and V move in
+// the pool as well (else only in the mirror).
 template <bool DST_SLOT, bool POOL>
-__device__ __forceinline__ void copy_page(const PageCache& c, int layer, int src, int dst, int x) {
-  const size_t ls = (size_t)layer * c.Lp + src, ld = (size_t)layer * c.Lp + dst;
-  const bool mir = c.k_mir != nullptr;
-  const bool kv = POOL || mir;
-  const int ss = kv ? slot_at(c, layer, src) : -1;
-  const int sd = DST_SLOT ? slot_at(c, layer, dst) : -1;
-  const size_t ps = (size_t)layer * c.S + max(ss, 0), pd = (size_t)layer * c.S + max(sd, 0);
-  const bool can = kv && (ss >= 0 || mir) && (mir || sd >= 0);
-  if (kv && !can && x == 0 && threadIdx.x == 0) set_status(c.status, SSA_ST_UNRESOLVED);
-  const long long kv16 = can ? 2 * c.pb16 : 0;
-  const long long total = kv16 + c.HD / 4 + c.HD / 16;
+struct PageCopy {
+  size_t ls, ld, ps, pd;
+  int ss, sd;
+  bool mir, can;
+  long long kv16;
+  __device__ __forceinline__ PageCopy(const PageCache& c, int layer, int src, int dst) {
+    ls = (size_t)layer * c.Lp + src;
+    ld = (size_t)layer * c.Lp + dst;
+    mir = c.k_mir != nullptr;
+    const bool kv = POOL || mir;
+    ss = kv ? slot_at(c, layer, src) : -1;
+    sd = DST_SLOT ? slot_at(c, layer, dst) : -1;
+    ps = (size_t)layer * c.S + max(ss, 0);
+    pd = (size_t)layer * c.S + max(sd, 0);
+    can = kv && (ss >= 0 || mir) && (mir || sd >= 0);
+    kv16 = can ? 2 * c.pb16 : 0;
+  }
+  __device__ __forceinline__ long long units(const PageCache& c) const {
+    return kv16 + c.HD / 4 + c.HD / 16;
+  }
+  // unit u: read from `from`, written to d0 and d1 (null: nowhere)
+  __device__ __forceinline__ void unit(const PageCache& c, long long u, const uint4*& from,
+                                       uint4*& d0, uint4*& d1) const {
+    d1 = nullptr;
+    if (u < kv16) {
+      const bool v = u >= c.pb16;
+      if (v) u -= c.pb16;
+      uint4* pool = reinterpret_cast<uint4*>(v ? c.v_pool : c.k_pool);
+      uint4* m = reinterpret_cast<uint4*>(v ? c.v_mir : c.k_mir);
+      from = ss >= 0 ? pool + ps * c.pb16 + u : m + ls * c.pb16 + u;
+      d0 = mir ? m + ld * c.pb16 + u : nullptr;
+      if (sd >= 0) d1 = pool + pd * c.pb16 + u;
+    } else if ((u -= kv16) < c.HD / 4) {
+      uint4* sum = reinterpret_cast<uint4*>(c.slab_sum);
+      from = sum + ls * (c.HD / 4) + u;
+      d0 = sum + ld * (c.HD / 4) + u;
+    } else {
+      u -= c.HD / 4;
+      uint4* code = reinterpret_cast<uint4*>(c.slab);
+      from = code + ls * (c.HD / 16) + u;
+      d0 = code + ld * (c.HD / 16) + u;
+    }
+  }
+  // the scales, and the slab row's scale and count: threads i of n
+  __device__ __forceinline__ void small(const PageCache& c, int i0, int n) const {
+    if (i0 == 0) {
+      c.slab_scale[ld] = c.slab_scale[ls];
+      c.slab_cnt[ld] = c.slab_cnt[ls];
+    }
+    if (!can) return;
+    for (int i = i0; i < 2 * c.n_scale; i += n) {
+      const bool v = i >= c.n_scale;
+      const int j = v ? i - c.n_scale : i;
+      float* pool = v ? c.v_scale : c.k_scale;
+      float* m = v ? c.vs_mir : c.ks_mir;
+      const float s = ss >= 0 ? pool[ps * c.n_scale + j] : m[ls * c.n_scale + j];
+      if (mir) m[ld * c.n_scale + j] = s;
+      if (sd >= 0) pool[pd * c.n_scale + j] = s;
+    }
+  }
+};
+
+// One CTA's share, chunk `x` (chunk 0 with the scales and counts).  `go` is
+// asked, by every thread, once the loads are on their way: false leaves dst as
+// it is.
+template <bool DST_SLOT, bool POOL, typename Go>
+__device__ __forceinline__ void copy_page(const PageCache& c, int layer, int src, int dst, int x,
+                                          Go go) {
+  const PageCopy<DST_SLOT, POOL> pc(c, layer, src, dst);
+  const long long total = pc.units(c);
   uint4 buf[kCopyUnroll];
   uint4 *d0[kCopyUnroll], *d1[kCopyUnroll];
 #pragma unroll
   for (int i = 0; i < kCopyUnroll; ++i) {
-    long long u = (long long)x * kCopyChunk + i * kCopyThreads + threadIdx.x;
+    const long long u = (long long)x * kCopyChunk + i * kCopyThreads + threadIdx.x;
     d0[i] = d1[i] = nullptr;
-    if (u >= total) continue;
-    const uint4* from;
-    if (u < kv16) {
-      const bool v = u >= c.pb16;
-      if (v) u -= c.pb16;
-      const uint8_t* pool = v ? c.v_pool : c.k_pool;
-      const uint8_t* m = v ? c.v_mir : c.k_mir;
-      from = ss >= 0 ? reinterpret_cast<const uint4*>(pool) + ps * c.pb16 + u
-                     : reinterpret_cast<const uint4*>(m) + ls * c.pb16 + u;
-      if (mir) d0[i] = reinterpret_cast<uint4*>(v ? c.v_mir : c.k_mir) + ld * c.pb16 + u;
-      if (sd >= 0) d1[i] = reinterpret_cast<uint4*>(v ? c.v_pool : c.k_pool) + pd * c.pb16 + u;
-    } else if ((u -= kv16) < c.HD / 4) {
-      from = reinterpret_cast<const uint4*>(c.slab_sum + ls * c.HD) + u;
-      d0[i] = reinterpret_cast<uint4*>(c.slab_sum + ld * c.HD) + u;
-    } else {
-      u -= c.HD / 4;
-      from = reinterpret_cast<const uint4*>(c.slab + ls * c.HD) + u;
-      d0[i] = reinterpret_cast<uint4*>(c.slab + ld * c.HD) + u;
+    if (u < total) {
+      const uint4* from;
+      pc.unit(c, u, from, d0[i], d1[i]);
+      buf[i] = *from;
     }
-    buf[i] = *from;
   }
+  if (!go()) return;
+  if (!pc.can && x == 0 && threadIdx.x == 0) set_status(c.status, SSA_ST_UNRESOLVED);
 #pragma unroll
   for (int i = 0; i < kCopyUnroll; ++i) {
     if (d0[i]) *d0[i] = buf[i];
     if (d1[i]) *d1[i] = buf[i];
   }
-  if (x != 0) return;
-  if (threadIdx.x == 0) {
-    c.slab_scale[ld] = c.slab_scale[ls];
-    c.slab_cnt[ld] = c.slab_cnt[ls];
-  }
-  if (!can) return;
-  for (int i = threadIdx.x; i < 2 * c.n_scale; i += kCopyThreads) {
-    const bool v = i >= c.n_scale;
-    const int j = v ? i - c.n_scale : i;
-    const float* pool = v ? c.v_scale : c.k_scale;
-    const float* m = v ? c.vs_mir : c.ks_mir;
-    const float s = ss >= 0 ? pool[ps * c.n_scale + j] : m[ls * c.n_scale + j];
-    if (mir) (v ? c.vs_mir : c.ks_mir)[ld * c.n_scale + j] = s;
-    if (sd >= 0) (v ? c.v_scale : c.k_scale)[pd * c.n_scale + j] = s;
-  }
+  if (x == 0) pc.small(c, threadIdx.x, kCopyThreads);
 }
 
 // The slot a page holds becomes free (host tier: the mirror holds the page).
@@ -142,47 +176,64 @@ __device__ __forceinline__ void release_slot(const PageCache& c, int layer, int 
 // copy
 // ---------------------------------------------------------------------------
 
-// ok[i] = pair i is copied: both ids in range and different, dst[i] not the
-// dst of an earlier pair nor the src of any (so no copy reads what another
-// writes and the result does not depend on their order).
-__global__ void copy_check_kernel(const int32_t* src, const int32_t* dst, int n, int32_t* ok,
-                                  PageCache c) {
-  __shared__ int2 tile[kCopyThreads];
-  pdl_trigger();
-  pdl_wait();
-  const int i = blockIdx.x * kCopyThreads + threadIdx.x;
-  const int s = i < n ? src[i] : -1, d = i < n ? dst[i] : -1;
+// Pair i is copied: both ids in range and different, dst[i] not the dst of an
+// earlier pair nor the src of any (so no copy reads what another writes and
+// the result does not depend on their order).
+
+// This lane's share of the search for a pair that clashes with pair i.
+__device__ __forceinline__ bool pair_clash(const int32_t* src, const int32_t* dst, int n, int i,
+                                           int d, int first, int step) {
   bool clash = false;
-  for (int base = 0; base < n; base += kCopyThreads) {
-    const int j = base + threadIdx.x;
-    __syncthreads();
-    tile[threadIdx.x] = j < n ? make_int2(src[j], dst[j]) : make_int2(-1, -1);
-    __syncthreads();
-    const int m = min(kCopyThreads, n - base);
-    for (int k = 0; k < m; ++k) {
-      const int2 o = tile[k];
-      if (o.x < 0 || o.y < 0) continue;                     // padding
-      if (base + k != i && o.x == d) clash = true;
-      if (base + k < i && o.y == d) clash = true;
-    }
+  for (int j = first; j < n; j += step) {
+    const int a = src[j], b = dst[j];
+    if (a < 0 || b < 0 || j == i) continue;                 // padding, itself
+    clash = clash || a == d || (j < i && b == d);
   }
-  if (i >= n) return;
-  int good = 0;
-  if (s >= 0 && d >= 0) {
-    if (!valid_page(c, s) || !valid_page(c, d) || clash) set_status(c.status, SSA_ST_BAD_ID);
-    else good = s != d;
-  }
-  ok[i] = good;
+  return clash;
 }
 
+// ok[i], a warp per pair
+__global__ void copy_check_kernel(const int32_t* src, const int32_t* dst, int n, int32_t* ok,
+                                  PageCache c) {
+  pdl_trigger();
+  pdl_wait();
+  const int i = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (i >= n) return;
+  const int s = src[i], d = dst[i];
+  bool good = false;
+  if (s >= 0 && d >= 0) {
+    const bool in = valid_page(c, s) && valid_page(c, d);
+    good = in && !__any_sync(0xffffffffu, pair_clash(src, dst, n, i, d, lane, 32));
+    if (!good && lane == 0) set_status(c.status, SSA_ST_BAD_ID);
+  }
+  if (lane == 0) ok[i] = good && s != d;
+}
+
+// FUSED: a few pairs, each CTA looks for clashes itself while its loads are on
+// their way (one launch fewer: 1 pair of 2 layers 4.1 -> FUSED_1 us, 400 of 12
+// layers 122 -> FUSED_400); else ok has the answer.
+template <bool FUSED>
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const int32_t* src,
-                                                                  const int32_t* dst,
+                                                                  const int32_t* dst, int n,
                                                                   const int32_t* ok, PageCache c) {
   pdl_trigger();
   pdl_wait();
-  const int i = blockIdx.y;
-  if (!ok[i]) return;
-  copy_page<true, true>(c, blockIdx.z, src[i], dst[i], blockIdx.x);
+  const int i = blockIdx.y, layer = blockIdx.z;
+  if (!FUSED && !ok[i]) return;
+  const int s = src[i], d = dst[i];
+  if (FUSED) {
+    if (s < 0 || d < 0) return;
+    if (!valid_page(c, s) || !valid_page(c, d)) {
+      if (threadIdx.x == 0) set_status(c.status, SSA_ST_BAD_ID);
+      return;
+    }
+  }
+  copy_page<true, true>(c, layer, s, d, blockIdx.x, [&]() -> bool {
+    if (!FUSED) return true;
+    const bool clash = __syncthreads_or(pair_clash(src, dst, n, i, d, threadIdx.x, kCopyThreads));
+    if (clash && threadIdx.x == 0) set_status(c.status, SSA_ST_BAD_ID);
+    return !clash && s != d;
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -224,8 +275,11 @@ struct ForkWs {
   int32_t *old_bt, *old_len;     // [B][nmax], [B]
   uint32_t* bits;                // [ceil(Lp / 32)] free pages
   int32_t* list;                 // the new pages, in rank order
-  int4* plan;                    // [B] {parent, base, new length, 1 copy | 2 keep}
-  int2* copy;                    // [B] {src, dst} of the row's copy, or -1
+  int2* from;                    // [B] {the partly filled page the row continues or -1, the
+                                 // parent's length}
+  int4* plan;                    // [B] {parent, its length, new length, rank of its growth}
+  int2* copy;                    // [B] {src, dst} of the row's copy; src -1: the last page is
+                                 // kept, -2: it should have been copied
   int32_t* ticket;
 };
 
@@ -236,52 +290,24 @@ __device__ __forceinline__ int parent_of(const int32_t* parent, int i, int B, in
   return i;
 }
 
-__global__ void fork_count_kernel(Table t, const int32_t* parent, ForkWs w, PageCache c) {
-  pdl_trigger();
-  pdl_wait();
-  const long long n = (long long)t.B * t.nmax;
-  auto add = [&](int id, int v) {
-    if (valid_page(c, id)) atomicAdd(&t.ref[id], v);
-    else set_status(c.status, SSA_ST_BAD_ID);
-  };
-  for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < n;
-       x += (long long)gridDim.x * blockDim.x) {
-    const int i = (int)(x / t.nmax), p = (int)(x - (long long)i * t.nmax);
-    const int id = t.bt[x], len = row_len(t, i, c.status);
-    w.old_bt[x] = id;
-    if (p == 0) w.old_len[i] = len;
-    const int j = parent_of(parent, i, t.B, c.status);
-    if (j == i) continue;
-    if (p < (len + t.P - 1) / t.P) add(id, -1);
-    if (j >= 0 && p < (row_len(t, j, c.status) + t.P - 1) / t.P) add(t.bt[(long long)j * t.nmax + p], 1);
-  }
-}
-
-// One bit per page: ref > 0 (live) or not, by the whole grid; the last CTA to
-// finish gets true.
-__device__ __forceinline__ bool page_bits(const int32_t* ref, int Lp, uint32_t* bits, bool live,
-                                          int32_t* ticket) {
-  __shared__ int s_last;
-  const int lane = threadIdx.x & 31;
+// One bit per page, ref > 0 (live) or not, by one CTA; into the workspace and,
+// where it fits, shared memory, which is what the CTA goes on with.
+__device__ __forceinline__ const uint32_t* page_bits(const int32_t* ref, int Lp, uint32_t* bits,
+                                                     uint32_t* s_bits, bool live) {
+  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   const int words = (Lp + 31) / 32;
-  const int warps = gridDim.x * (blockDim.x >> 5);
-  for (int w = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < words; w += warps) {
+  const bool fits = words <= kPlanWords;
+#pragma unroll 8
+  for (int w = threadIdx.x >> 5; w < words; w += nw) {
     const int id = w * 32 + lane;
     const bool bit = id < Lp && (__ldcg(&ref[id]) > 0) == live;
     const uint32_t m = __ballot_sync(0xffffffffu, bit);
-    if (lane == 0) bits[w] = m;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    s_last = atomicAdd(ticket, 1) == (int)gridDim.x - 1;
-    if (s_last) {
-      *ticket = 0;                        // ready for the next call
-      __threadfence();
+    if (lane == 0) {
+      bits[w] = m;
+      if (fits) s_bits[w] = m;
     }
   }
-  __syncthreads();
-  return s_last;
+  return fits ? s_bits : bits;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(Table t, const int32_t* parent,
@@ -289,65 +315,90 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(Table t, const 
                                                                  PageCache c) {
   extern __shared__ int32_t dyn[];
   __shared__ int s_tmp[33];
+  __shared__ int s_last;
+  __shared__ int32_t s_list[kPlanList];
   pdl_trigger();
   pdl_wait();
-  if (!page_bits(t.ref, c.Lp, w.bits, false, w.ticket)) return;
   const int tid = threadIdx.x, B = t.B, P = t.P;
-  int32_t* gs = dyn;                      // [B] the partly filled page a row continues, or -1
-  int32_t* others = gs + B;               // [B] its other references, -1 where another row settles them
-  int32_t* need = others + B;             // [B] new pages
-  for (int i = tid; i < B; i += kPlanThreads) {
-    const int j = parent_of(parent, i, B, nullptr);
-    const int plen = j >= 0 ? w.old_len[j] : 0;
-    int g = -1;
-    if (plen % P) {
-      g = w.old_bt[(long long)j * t.nmax + plen / P];
-      if (!valid_page(c, g)) g = -1;      // flagged by the count; carried as it is
+  // the references, and what each row continues
+  {
+    const int n = B * t.nmax;             // at most 1638 x 49152
+    auto add = [&](int id, int v) {
+      if (valid_page(c, id)) atomicAdd(&t.ref[id], v);
+      else set_status(c.status, SSA_ST_BAD_ID);
+    };
+    for (int x = blockIdx.x * kPlanThreads + tid; x < n; x += gridDim.x * kPlanThreads) {
+      const int i = x / t.nmax, p = x - i * t.nmax;
+      const int id = t.bt[x], len = row_len(t, i, c.status);
+      const int j = parent_of(parent, i, B, c.status);
+      const int jid = j >= 0 ? t.bt[j * t.nmax + p] : -1;
+      const int jlen = j >= 0 ? row_len(t, j, c.status) : 0;
+      w.old_bt[x] = id;
+      if (p == 0) w.old_len[i] = len;
+      if (p == (jlen % P ? jlen / P : 0))
+        w.from[i] = make_int2(jlen % P && valid_page(c, jid) ? jid : -1, jlen);
+      if (j == i) continue;
+      if (p < (len + P - 1) / P) add(id, -1);
+      if (p < (jlen + P - 1) / P) add(jid, 1);
     }
-    gs[i] = g;
   }
   __syncthreads();
+  if (gridDim.x > 1) {
+    if (tid == 0) {
+      __threadfence();
+      s_last = atomicAdd(w.ticket, 1) == (int)gridDim.x - 1;
+      if (s_last) {
+        *w.ticket = 0;                    // ready for the next call
+        __threadfence();
+      }
+    }
+    __syncthreads();
+    if (!s_last) return;
+  }
+
+  // the last CTA: which pages are free, what each row needs
+  int32_t* gs = dyn;                      // [B] the partly filled page a row continues, or -1
+  int32_t* refg = gs + B;                 // [B] references of it
+  int32_t* plens = refg + B;              // [B] the parent's length
+  int32_t* nlens = plens + B;             // [B] the new length
+  int32_t* copies = nlens + B;            // [B] 1: the row needs a copy of that page
+  int32_t* need = copies + B;             // [B] new pages
+  int32_t* ranks = need + B;              // [B] the first of them in the list
+  uint32_t* s_bits = reinterpret_cast<uint32_t*>(ranks + B);       // [kPlanWords] or none
   for (int i = tid; i < B; i += kPlanThreads) {
-    const int j = parent_of(parent, i, B, nullptr);
-    const int plen = j >= 0 ? w.old_len[j] : 0;
+    const int2 f = __ldcg(&w.from[i]);
+    const int want = new_lens ? new_lens[i] : 0;
+    gs[i] = f.x;
+    plens[i] = f.y;
+    refg[i] = f.x >= 0 ? __ldcg(&t.ref[f.x]) : 0;
+    const int most = t.nmax * P;
+    if (want > most) set_status(c.status, SSA_ST_BAD_POS);
+    nlens[i] = max(f.y, min(want, most));
+  }
+  const uint32_t* bits = page_bits(t.ref, c.Lp, w.bits, s_bits, false);
+  __syncthreads();
+  for (int i = tid; i < B; i += kPlanThreads) {
     const int g = gs[i];
-    int n = 0, first = i, left = 0, flags = 2;
+    int n = 0, first = i, left = 0;
     if (g >= 0) {
       for (int k = 0; k < B; ++k)
         if (gs[k] == g) {
           ++n;
           first = min(first, k);
         }
-      left = __ldcg(&t.ref[g]) - n;
-      flags = first == i && left <= 0 ? 2 : 1;
-      if (first != i) left = -1;          // only the first row settles the count
-      else left = max(left, 0);
+      left = max(refg[i] - n, 0);
+      if (first == i) t.ref[g] = max(left, 1);               // the first row settles the count
     }
-    others[i] = left;
-    int nlen = plen;
-    if (new_lens) {
-      int want = new_lens[i];
-      const long long most = (long long)t.nmax * P;
-      if (want > most) {
-        set_status(c.status, SSA_ST_BAD_POS);
-        want = (int)most;
-      }
-      nlen = max(plen, want);
-    }
-    need[i] = (flags == 1) + (nlen + P - 1) / P - (plen + P - 1) / P;
-    w.plan[i] = make_int4(j, 0, nlen, flags);
+    copies[i] = first != i || left > 0;
+    need[i] = copies[i] + (nlens[i] + P - 1) / P - (plens[i] + P - 1) / P;
   }
   __syncthreads();
   int total = 0;
   for (int base = 0; base < B; base += kPlanThreads) {
     const int i = base + tid;
     int sum;
-    const int v = i < B ? need[i] : 0;
-    const int e = block_exclusive_scan(v, s_tmp, sum);
-    if (i < B) {
-      w.plan[i].y = total + e;
-      if (gs[i] >= 0 && others[i] >= 0) t.ref[gs[i]] = max(others[i], 1);
-    }
+    const int e = block_exclusive_scan(i < B ? need[i] : 0, s_tmp, sum);
+    if (i < B) ranks[i] = total + e;
     total += sum;
   }
   // the lowest `total` free pages
@@ -355,12 +406,13 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(Table t, const 
   int got = 0;
   for (int base = 0; base < words && got < total; base += kPlanThreads) {
     const int x = base + tid;
-    uint32_t m = x < words ? __ldcg(&w.bits[x]) : 0u;
+    uint32_t m = x < words ? bits[x] : 0u;
     int sum;
     int r = got + block_exclusive_scan(__popc(m), s_tmp, sum);
     for (; m && r < total; m &= m - 1, ++r) {
       const int id = x * 32 + __ffs(m) - 1;
       w.list[r] = id;
+      if (r < kPlanList) s_list[r] = id;
       t.ref[id] = 1;
     }
     got += sum;
@@ -368,16 +420,17 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(Table t, const 
   if (got > total) got = total;
   __syncthreads();                        // the list is written
   for (int i = tid; i < B; i += kPlanThreads) {
-    int4 pl = w.plan[i];
-    const int plen = pl.x >= 0 ? w.old_len[pl.x] : 0;
-    const int avail = min(max(got - pl.y, 0), need[i]);
+    const int plen = plens[i], base = ranks[i], copy = copies[i];
+    int nlen = nlens[i];
+    const int avail = min(max(got - base, 0), need[i]);
     if (avail < need[i]) {                // too few free pages: the row is cut to what it has
       set_status(c.status, SSA_ST_NO_PAGES);
-      if (pl.w == 1 && avail == 0) pl.z = plen / P * P;
-      else pl.z = min(pl.z, ((plen + P - 1) / P + avail - (pl.w == 1)) * P);
+      if (copy && avail == 0) nlen = plen / P * P;
+      else nlen = min(nlen, ((plen + P - 1) / P + avail - copy) * P);
     }
-    w.copy[i] = pl.w == 1 && avail > 0 ? make_int2(gs[i], w.list[pl.y]) : make_int2(-1, -1);
-    w.plan[i] = pl;
+    w.copy[i] = copy ? (avail > 0 ? make_int2(gs[i], base < kPlanList ? s_list[base] : w.list[base]) : make_int2(-2, -1))
+                     : make_int2(-1, -1);
+    w.plan[i] = make_int4(parent_of(parent, i, B, nullptr), plen, nlen, base + copy);
   }
 }
 
@@ -388,16 +441,14 @@ __global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(Table t, ForkW
   const int i = blockIdx.y, P = t.P, layer = blockIdx.z;
   const int4 pl = w.plan[i];
   const int2 cp = w.copy[i];
-  const int j = pl.x;
-  const int plen = j >= 0 ? w.old_len[j] : 0;
+  const int j = pl.x, plen = pl.y, growth = pl.w;
   const int full = plen / P, pn = (plen + P - 1) / P, nn = (pl.z + P - 1) / P;
   const int first = blockIdx.x * kCopyThreads + threadIdx.x, step = gridDim.x * kCopyThreads;
-  const int growth = pl.y + (pl.w == 1);             // rank of the row's first growth page
   if (layer == (int)gridDim.z - 1) {
     for (int p = first; p < t.nmax; p += step) {
       int id = -1;
       if (p < nn) {
-        if (p < full || (p < pn && pl.w == 2)) id = w.old_bt[(long long)j * t.nmax + p];
+        if (p < full || (p < pn && cp.x == -1)) id = w.old_bt[(long long)j * t.nmax + p];
         else if (p < pn) id = cp.y;
         else id = w.list[growth + p - pn];
       }
@@ -409,11 +460,12 @@ __global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(Table t, ForkW
   const bool mir = c.k_mir != nullptr;
   if (cp.x >= 0) {
     // a new page of a host-tier cache holds no slot: its copy goes to the mirror
+    auto yes = []() { return true; };
     if (mir) {
       if (first == 0) release_slot(c, layer, cp.y);
-      copy_page<false, true>(c, layer, cp.x, cp.y, blockIdx.x);
+      copy_page<false, true>(c, layer, cp.x, cp.y, blockIdx.x, yes);
     } else {
-      copy_page<true, true>(c, layer, cp.x, cp.y, blockIdx.x);
+      copy_page<true, true>(c, layer, cp.x, cp.y, blockIdx.x, yes);
     }
   }
   // pages the row grew by: empty slab rows, no slot
@@ -450,7 +502,6 @@ struct CompactWs {
   uint32_t* bits;                // live pages
   int32_t *from, *to, *map;      // the moves, ascending; map[from] = to
   int32_t* count;                // {live pages, moves}
-  int32_t* ticket;
 };
 
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(Table t, CompactWs w, int Lp,
@@ -458,25 +509,27 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(Table t, Com
                                                                     int32_t* to_opt,
                                                                     int32_t* n_opt) {
   __shared__ int s_tmp[33];
+  __shared__ uint32_t s_bits[kPlanWords];
   pdl_trigger();
   pdl_wait();
-  if (!page_bits(t.ref, Lp, w.bits, true, w.ticket)) return;
+  const uint32_t* bits = page_bits(t.ref, Lp, w.bits, s_bits, true);
+  __syncthreads();
   const int tid = threadIdx.x, words = (Lp + 31) / 32;
   // live pages in all, then those below that number
   int mine = 0, n_live, below;
-  for (int x = tid; x < words; x += kPlanThreads) mine += __popc(__ldcg(&w.bits[x]));
+  for (int x = tid; x < words; x += kPlanThreads) mine += __popc(bits[x]);
   block_exclusive_scan(mine, s_tmp, n_live);
   mine = 0;
   for (int x = tid; x * 32 < n_live; x += kPlanThreads) {
     const int k = n_live - x * 32;
-    mine += __popc(__ldcg(&w.bits[x]) & (k >= 32 ? 0xffffffffu : (1u << k) - 1u));
+    mine += __popc(bits[x] & (k >= 32 ? 0xffffffffu : (1u << k) - 1u));
   }
   block_exclusive_scan(mine, s_tmp, below);
   const int moves = n_live - below;
   int seen = 0;                           // live pages before this round's words
   for (int base = 0; base < words && moves > 0; base += kPlanThreads) {
     const int x = base + tid;
-    const uint32_t m = x < words ? __ldcg(&w.bits[x]) : 0u;
+    const uint32_t m = x < words ? bits[x] : 0u;
     int sum;
     const int pre = seen + block_exclusive_scan(__popc(m), s_tmp, sum);
     const int k = n_live - x * 32;        // ids of this word below n_live
@@ -503,16 +556,38 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(Table t, Com
   }
 }
 
+// The moves: a warp per (page, layer, 128 of its 16-byte units), four of them
+// in flight per lane.
 __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(CompactWs w, PageCache c,
                                                                     int layers, int chunks) {
   pdl_trigger();
   pdl_wait();
+  const int lane = threadIdx.x & 31;
   const long long items = (long long)w.count[1] * layers * chunks;
-  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-    const int x = (int)(it % chunks);
+  const long long step = (long long)gridDim.x * (kCopyThreads / 32);
+  for (long long it = (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); it < items;
+       it += step) {
     const long long rest = it / chunks;
-    const int layer = (int)(rest % layers), r = (int)(rest / layers);
-    copy_page<false, false>(c, layer, w.from[r], w.to[r], x);
+    const int x = (int)(it - rest * chunks), r = (int)(rest / layers);
+    const PageCopy<false, false> pc(c, (int)(rest - (long long)r * layers), w.from[r], w.to[r]);
+    const int units = (int)pc.units(c);
+    uint4 buf[kCopyUnroll];
+    uint4* to[kCopyUnroll];
+#pragma unroll
+    for (int i = 0; i < kCopyUnroll; ++i) {
+      const int u = (x * kCopyUnroll + i) * 32 + lane;
+      to[i] = nullptr;
+      if (u < units) {
+        const uint4* from;
+        uint4* none;
+        pc.unit(c, u, from, to[i], none);
+        buf[i] = *from;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kCopyUnroll; ++i)
+      if (to[i]) *to[i] = buf[i];
+    if (x == 0) pc.small(c, lane, 32);
   }
 }
 
@@ -584,12 +659,8 @@ unsigned table_blocks(const Dims& d) {
   return (unsigned)(n < 1024 ? n : 1024);
 }
 
-// CTAs of the bit pass: a few words per warp
-unsigned bit_blocks(const Dims& d) {
-  const long long words = (d.Lp + 31) / 32, per = 8 * (kPlanThreads / 32);
-  const long long n = (words + per - 1) / per;
-  return (unsigned)(n < 1 ? 1 : n > 256 ? 256 : n);
-}
+// Pairs up to which a copy looks for clashes itself.
+constexpr int kFusedPairs = 64;
 
 }  // namespace
 
@@ -608,32 +679,54 @@ cudaError_t launch_copy_pages(const Dims& d, const ssa_cache& c, const int32_t* 
                               cudaStream_t s) {
   if (n == 0) return cudaSuccess;
   const PageCache pc = page_cache(d, c, status);
-  cudaError_t e = launch_pdl(copy_check_kernel, dim3((n + kCopyThreads - 1) / kCopyThreads),
-                             dim3(kCopyThreads), 0, s, src, dst, n, w.ok, pc);
+  const dim3 grid(page_chunks(pc, true), n, d.Lyr);
+  cudaError_t e;
+  if (n <= kFusedPairs) {
+    e = launch_pdl(copy_pages_kernel<true>, grid, dim3(kCopyThreads), 0, s, src, dst, n,
+                   (const int32_t*)nullptr, pc);
+    count_launch();
+    return e;
+  }
+  constexpr int kWarps = kCopyThreads / 32;
+  e = launch_pdl(copy_check_kernel, dim3((n + kWarps - 1) / kWarps), dim3(kCopyThreads), 0, s, src,
+                 dst, n, w.ok, pc);
   count_launch();
   if (e != cudaSuccess) return e;
-  e = launch_pdl(copy_pages_kernel, dim3(page_chunks(pc, true), n, d.Lyr), dim3(kCopyThreads), 0, s,
-                 src, dst, (const int32_t*)w.ok, pc);
+  e = launch_pdl(copy_pages_kernel<false>, grid, dim3(kCopyThreads), 0, s, src, dst, n,
+                 (const int32_t*)w.ok, pc);
   count_launch();
   return e;
 }
 
 cudaError_t launch_fork(const Dims& d, const ssa_cache& c, const ssa_requests& r,
                         const int32_t* parent, const int32_t* new_lens, int32_t* status,
-                        const PageWs& w, cudaStream_t s) {
+                        const PageWs& w, int num_sms, cudaStream_t s) {
   const PageCache pc = page_cache(d, c, status);
   const Table t = table_of(d, r);
-  const ForkWs fw{w.old_bt, w.old_len, w.bits, w.list, (int4*)w.plan, (int2*)w.copy, w.ticket};
-  cudaError_t e = launch_pdl(fork_count_kernel, dim3(table_blocks(d)), dim3(256), 0, s, t, parent,
-                             fw, pc);
+  const ForkWs fw{w.old_bt,       w.old_len,      w.bits,         w.list,
+                  (int2*)w.from,  (int4*)w.plan,  (int2*)w.copy,  w.ticket};
+  // one CTA up to four entries a thread (it then needs no ticket), else up to
+  // two per SM
+  const long long entries = (long long)d.B * d.nmax;
+  long long ctas = entries <= 4 * kPlanThreads ? 1 : (entries + kPlanThreads - 1) / kPlanThreads;
+  if (ctas > 2 * num_sms) ctas = 2 * num_sms;
+  const int words = (d.Lp + 31) / 32;
+  const size_t smem = ((size_t)7 * d.B + (words <= kPlanWords ? words : 0)) * sizeof(int32_t);
+  cudaError_t e;
+  if (smem + 8192 > 48 * 1024) {
+    e = cudaFuncSetAttribute(fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  e = launch_pdl(fork_plan_kernel, dim3((unsigned)ctas), dim3(kPlanThreads), smem, s, t, parent,
+                 new_lens, fw, pc);
   count_launch();
   if (e != cudaSuccess) return e;
-  e = launch_pdl(fork_plan_kernel, dim3(bit_blocks(d)), dim3(kPlanThreads),
-                 (size_t)3 * d.B * sizeof(int32_t), s, t, parent, new_lens, fw, pc);
-  count_launch();
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(fork_apply_kernel, dim3(page_chunks(pc, true), d.B, d.Lyr + 1), dim3(kCopyThreads),
-                 0, s, t, fw, pc);
+  // growth can be many pages of few rows: eight CTAs a row and layer at least
+  unsigned chunks = page_chunks(pc, true);
+  if (new_lens && chunks < 8) chunks = 8;
+  e = launch_pdl(fork_apply_kernel, dim3(chunks, d.B, d.Lyr + 1), dim3(kCopyThreads), 0, s, t, fw,
+                 pc);
   count_launch();
   return e;
 }
@@ -643,13 +736,15 @@ cudaError_t launch_compact(const Dims& d, const ssa_cache& c, const ssa_requests
                            int32_t* status, const PageWs& w, int num_sms, cudaStream_t s) {
   const PageCache pc = page_cache(d, c, status);
   const Table t = table_of(d, r);
-  const CompactWs cw{w.bits, w.list, w.to, w.map, w.count, w.ticket};
-  cudaError_t e = launch_pdl(compact_plan_kernel, dim3(bit_blocks(d)), dim3(kPlanThreads), 0, s, t,
+  const CompactWs cw{w.bits, w.list, w.to, w.map, w.count};
+  cudaError_t e = launch_pdl(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, t,
                              cw, d.Lp, moved_from, moved_to, n_moved);
   count_launch();
   if (e != cudaSuccess) return e;
+  const long long per = (pc.mirror() ? 2 * pc.pb16 : 0) + pc.HD / 4 + pc.HD / 16;
+  constexpr int kWarpUnits = 32 * kCopyUnroll;
   e = launch_pdl(compact_move_kernel, dim3(8 * num_sms), dim3(kCopyThreads), 0, s, cw, pc, d.Lyr,
-                 (int)page_chunks(pc, pc.mirror()));
+                 (int)((per + kWarpUnits - 1) / kWarpUnits));
   count_launch();
   if (e != cudaSuccess) return e;
   e = launch_pdl(compact_tables_kernel, dim3(2 * num_sms), dim3(256), 0, s, t, cw, pc, d.Lyr);
