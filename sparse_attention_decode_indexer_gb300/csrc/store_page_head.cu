@@ -34,8 +34,10 @@
 // correctly rounded reciprocal is the correctly rounded quotient), two
 // elements per f32x2 instruction: 5 instead of about 20 per pair.
 //
-// Append: one CTA per (run, layer) with a thread per slab element, so that the
-// heads meet in shared memory and a run costs three dependent reads.
+// Append: one CTA per (run, layer) with a warp per head, so that a head's
+// maxima are a warp's and only the slab's scale meets in shared memory; a run
+// costs three dependent reads (position, state, scale), and 64 requests of 12
+// layers are all resident at once.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -132,39 +134,55 @@ struct Block {
   }
 };
 
-// Stores a run with a thread per dimension, whatever its tokens and values;
-// 128 threads per head, every thread of the CTA calls it (`active`: those with
-// a column).  kin, vin: the column's first token, rows HD apart; k0, v0: that
-// token's values.  Returns the column's slab sum, `sum` on entry.  Scratch:
-// s_max [2][warps], s_code [threads].
-template <bool I8, int P>
-__device__ __forceinline__ float store_columns(const StorePHParams& p, const Block& blk, bool active,
-                                               int d, const __nv_bfloat16* kin,
-                                               const __nv_bfloat16* vin, __nv_bfloat16 k0,
-                                               __nv_bfloat16 v0, int HD, int R, const int* s_row,
-                                               int cnt0, float sum, float (*s_max)[32],
-                                               uint8_t* s_code) {
+// E consecutive bf16 of a row, as they lie in memory.
+template <int E> struct Row;
+template <> struct Row<1> {
+  __nv_bfloat16 v;
+  __device__ __forceinline__ float at(int) const { return __bfloat162float(v); }
+};
+template <> struct Row<4> {
+  uint2 v;
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t w = i < 2 ? v.x : v.y;
+    return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+  }
+};
+
+// Stores a run of one head, whatever its tokens and values, with 128 / E
+// threads that have E dimensions each: a warp (E = 4), or four (E = 1; then
+// every thread of the CTA calls it, `active` those with a dimension, and s_max
+// [2][4] is their scratch).  kin, vin: the thread's elements of the first
+// token, rows HD apart; k0, v0: their values.  sum: the slab's sums, updated.
+template <bool I8, int P, int E>
+__device__ __forceinline__ void store_run(const StorePHParams& p, const Block& blk, bool active,
+                                          int d, const Row<E>* kin, const Row<E>* vin, Row<E> k0,
+                                          Row<E> v0, int HD, int R, const int* s_row, int cnt0,
+                                          float (&sum)[E], float (*s_max)[4]) {
   constexpr float kQmax = I8 ? 127.0f : 448.0f;
   constexpr int pe = P * kHD;              // codes of one head of one page
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int NT = kHD / E;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rs = HD / E;
   const float old_k = cnt0 > 0 ? blk.scale(p.k_scale_m, p.k_scale) : 0.0f;
   const float old_v = cnt0 > 0 ? blk.scale(p.v_scale_m, p.v_scale) : 0.0f;
   // finite maxima of the run
   float ak = 0.0f, av = 0.0f;
-  auto take = [](float& m, __nv_bfloat16 x) {
-    const float a = fabsf(__bfloat162float(x));
-    if (a < INFINITY) m = fmaxf(m, a);
+  auto take = [](float& m, const Row<E>& x) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float a = fabsf(x.at(e));
+      if (a < INFINITY) m = fmaxf(m, a);
+    }
   };
   if (active) {
     take(ak, k0);
     take(av, v0);
     for (int r0 = 1; r0 < R; r0 += kTokBatch) {
-      __nv_bfloat16 xk[kTokBatch], xv[kTokBatch];
+      Row<E> xk[kTokBatch], xv[kTokBatch];
 #pragma unroll
       for (int i = 0; i < kTokBatch; ++i)
         if (r0 + i < R) {
-          xk[i] = kin[(size_t)(r0 + i) * HD];
-          xv[i] = vin[(size_t)(r0 + i) * HD];
+          xk[i] = kin[(size_t)(r0 + i) * rs];
+          xv[i] = vin[(size_t)(r0 + i) * rs];
         }
 #pragma unroll
       for (int i = 0; i < kTokBatch; ++i)
@@ -176,15 +194,17 @@ __device__ __forceinline__ float store_columns(const StorePHParams& p, const Blo
   }
   ak = warp_max(ak);
   av = warp_max(av);
-  if (lane == 0) {
-    s_max[0][warp] = ak;
-    s_max[1][warp] = av;
-  }
-  __syncthreads();                         // (every thread has read the old scales)
+  if (E == 1) {
+    if (active && lane == 0) {
+      s_max[0][warp] = ak;
+      s_max[1][warp] = av;
+    }
+    __syncthreads();                       // (every thread has read the old scales)
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    ak = fmaxf(ak, s_max[0][(warp & ~3) + w]);
-    av = fmaxf(av, s_max[1][(warp & ~3) + w]);
+    for (int w = 0; w < 4; ++w) {
+      ak = fmaxf(ak, s_max[0][w]);
+      av = fmaxf(av, s_max[1][w]);
+    }
   }
   const float need_k = ak / kQmax, need_v = av / kQmax;
   const float sk = cnt0 > 0 ? fmaxf(old_k, need_k) : need_k;
@@ -196,34 +216,35 @@ __device__ __forceinline__ float store_columns(const StorePHParams& p, const Blo
       blk.set_scale(p.k_scale_m, p.k_scale, sk);
       blk.set_scale(p.v_scale_m, p.v_scale, sv);
     }
-    if (km || kp) {
-      if (cnt0 > 0 && sk > old_k) rescale_block<I8>(km, kp, pe, old_k / sk, d, kHD);
-      if (cnt0 > 0 && sv > old_v) rescale_block<I8>(vm, vp, pe, old_v / sv, d, kHD);
-    }
+    const bool gk = cnt0 > 0 && sk > old_k, gv = cnt0 > 0 && sv > old_v;
+    if ((km || kp) && gk) rescale_block<I8>(km, kp, pe, old_k / sk, d / E, NT);
+    if ((km || kp) && gv) rescale_block<I8>(vm, vp, pe, old_v / sv, d / E, NT);
   }
-  __syncthreads();                         // the new codes go on top
-  if (!active) return sum;
+  // the new codes go on top
+  if (E == 1) __syncthreads();
+  else __syncwarp();
+  if (!active) return;
   for (int r = 0; r < R; ++r) {
-    const __nv_bfloat16 xk = r == 0 ? k0 : kin[(size_t)r * HD];
-    const __nv_bfloat16 xv = r == 0 ? v0 : vin[(size_t)r * HD];
-    const float fk = __bfloat162float(xk), fv = __bfloat162float(xv);
+    const Row<E> xk = r == 0 ? k0 : kin[(size_t)r * rs], xv = r == 0 ? v0 : vin[(size_t)r * rs];
     const int j = s_row[r];
-    // K row j: the warp's 32 codes as two 16-byte stores
-    s_code[tid] = sk > 0.0f ? quant<I8>(fk / sk) : 0;
-    __syncwarp();
-    if (lane < 2) {
-      const uint4 w = *reinterpret_cast<const uint4*>(s_code + (tid & ~31) + 16 * lane);
-      const int off = j * kHD + (d & ~31) + 16 * lane;
-      if (km) *reinterpret_cast<uint4*>(km + off) = w;
-      if (kp) *reinterpret_cast<uint4*>(kp + off) = w;
+    uint32_t ck = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float fk = xk.at(e), fv = xv.at(e);
+      ck |= (uint32_t)(sk > 0.0f ? quant<I8>(fk / sk) : 0) << (8 * e);
+      const uint8_t c = sv > 0.0f ? quant<I8>(fv / sv) : 0;
+      if (vm) vm[(d + e) * P + j] = c;
+      if (vp) vp[(d + e) * P + j] = c;
+      sum[e] = sum[e] + fk;                // the slab: fp32, token order
     }
-    __syncwarp();
-    const uint8_t c = sv > 0.0f ? quant<I8>(fv / sv) : 0;
-    if (vm) vm[d * P + j] = c;
-    if (vp) vp[d * P + j] = c;
-    sum = sum + fk;                        // the slab: fp32, token order
+    if (E == 1) {
+      if (km) km[j * kHD + d] = (uint8_t)ck;
+      if (kp) kp[j * kHD + d] = (uint8_t)ck;
+    } else {
+      if (km) *reinterpret_cast<uint32_t*>(km + j * kHD + d) = ck;
+      if (kp) *reinterpret_cast<uint32_t*>(kp + j * kHD + d) = ck;
+    }
   }
-  return sum;
 }
 
 __device__ __forceinline__ int slab_code(float mean, float amax, float s) {
@@ -233,28 +254,26 @@ __device__ __forceinline__ int slab_code(float mean, float amax, float s) {
 // ---------------------------------------------------------------------------
 // append
 // ---------------------------------------------------------------------------
-// block: a thread per slab element (h, d); grid (tokens, layers): the CTA of a
-// run's first token stores the run, the others return.
+// A warp per KV head, four dimensions a lane; grid (tokens, layers): the CTA
+// of a run's first token stores the run, the others return.
 template <bool I8, int P>
-__global__ void __launch_bounds__(1024) append_page_head_kernel(StorePHParams p) {
+__global__ void __launch_bounds__(256) append_page_head_kernel(StorePHParams p) {
   __shared__ int s_row[P];
   __shared__ int s_run;
-  __shared__ float s_max[2][32];
-  __shared__ __align__(16) uint8_t s_code[1024];
+  __shared__ float s_head[8];
   pdl_trigger();
   pdl_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int Hkv = p.Hkv, HD = Hkv * kHD, h = tid >> 7, d = tid & 127;
+  const int tid = threadIdx.x, lane = tid & 31, h = tid >> 5;
+  const int Hkv = p.Hkv, HD = Hkv * kHD, d = 4 * lane;
   const int t0 = blockIdx.x, li = blockIdx.y, layer = p.layer0 + li;
-  // this token's position and the ones around it, in one round trip
+  // this token's position and the ones around it, in one round trip with the
+  // run's first token
   const int64_t pos0 = p.pos[t0];
   const int64_t prev = t0 > 0 ? p.pos[t0 - 1] : -1;
-  static_assert(P <= kHD, "the run's scan has a thread per token");
-  int64_t x0 = -1, x1 = -1;              // of tokens t0 + tid - 1 and t0 + tid
-  if (tid < P && t0 + tid < p.T) {
-    x1 = p.pos[t0 + tid];
-    if (tid > 0) x0 = p.pos[t0 + tid - 1];
-  }
+  const size_t in0 = (((size_t)li * p.T + t0) * HD + h * kHD + d) / 4;
+  const Row<4>* kin = reinterpret_cast<const Row<4>*>(p.k) + in0;
+  const Row<4>* vin = reinterpret_cast<const Row<4>*>(p.v) + in0;
+  const Row<4> k0 = *kin, v0 = *vin;
   if (pos0 < 0 || pos0 / P >= p.Lp) {
     if (tid == 0) set_status(p.status, SSA_ST_BAD_ID);
     return;
@@ -265,23 +284,21 @@ __global__ void __launch_bounds__(1024) append_page_head_kernel(StorePHParams p)
     if (prev >= 0 && prev / P == pg) return;                 // inside a run
   }
   const size_t lp = (size_t)layer * p.Lp + pg;
-  const size_t so = lp * HD + tid;
-  float sum = p.slab_sum[so];
+  const size_t so = lp * HD + h * kHD + d;
+  const float4 old_sum = *reinterpret_cast<const float4*>(p.slab_sum + so);
   const int cnt0 = p.slab_cnt[lp];
   int slot = p.slot_of[lp];
-  // the run's first token, while its length is found
-  const __nv_bfloat16* kin = p.k + ((size_t)li * p.T + t0) * HD + tid;
-  const __nv_bfloat16* vin = p.v + ((size_t)li * p.T + t0) * HD + tid;
-  const __nv_bfloat16 k0 = kin[0], v0 = vin[0];
+  // the run's length
   if (tid == 0) s_run = P;
   __syncthreads();
-  if (tid < P) {
-    const bool ends = t0 + tid >= p.T || x1 < 0 || x1 / P != pg;
-    if (!ends) {
-      s_row[tid] = (int)(x1 % P);
-      if (tid > 0 && x1 <= x0) set_status(p.status, SSA_ST_BAD_POS);
+  for (int r = tid; r < P; r += blockDim.x) {
+    const int t = t0 + r;
+    const int64_t x = t < p.T ? p.pos[t] : -1;
+    if (x < 0 || x / P != pg) {
+      atomicMin(&s_run, r);
     } else {
-      atomicMin(&s_run, tid);
+      s_row[r] = (int)(x % P);
+      if (r > 0 && x <= p.pos[t - 1]) set_status(p.status, SSA_ST_BAD_POS);
     }
   }
   if (slot >= p.S) {                       // corrupt state: never write through it
@@ -291,18 +308,28 @@ __global__ void __launch_bounds__(1024) append_page_head_kernel(StorePHParams p)
   const Block blk(p, layer, pg, slot, h);
   __syncthreads();
   const int R = s_run;
-  sum = store_columns<I8, P>(p, blk, true, d, kin, vin, k0, v0, HD, R, s_row, cnt0, sum, s_max,
-                             s_code);
-  p.slab_sum[so] = sum;
+  float sum[4] = {old_sum.x, old_sum.y, old_sum.z, old_sum.w};
+  store_run<I8, P, 4>(p, blk, true, d, kin, vin, k0, v0, HD, R, s_row, cnt0, sum, nullptr);
+  *reinterpret_cast<float4*>(p.slab_sum + so) = make_float4(sum[0], sum[1], sum[2], sum[3]);
   const int cnt = cnt0 + R;
-  const float mean = sum / (float)cnt;
-  const float a = warp_max(fabsf(mean));
-  if (lane == 0) s_max[0][warp] = a;       // (its last readers are a barrier back)
+  float mean[4], a = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    mean[e] = sum[e] / (float)cnt;
+    a = fmaxf(a, fabsf(mean[e]));
+  }
+  a = warp_max(a);
+  if (lane == 0) s_head[h] = a;
   __syncthreads();
   float amax = 0.0f;
-  for (int w = 0; w < 4 * Hkv; ++w) amax = fmaxf(amax, s_max[0][w]);
+  for (int w = 0; w < Hkv; ++w) amax = fmaxf(amax, s_head[w]);
   const float s = amax / 127.0f;
-  p.slab[so] = (int8_t)slab_code(mean, amax, s);
+  char4 code;
+  code.x = (signed char)slab_code(mean[0], amax, s);
+  code.y = (signed char)slab_code(mean[1], amax, s);
+  code.z = (signed char)slab_code(mean[2], amax, s);
+  code.w = (signed char)slab_code(mean[3], amax, s);
+  *reinterpret_cast<char4*>(p.slab + so) = code;
   if (tid == 0) {
     p.slab_cnt[lp] = cnt;
     p.slab_scale[lp] = s;
@@ -416,8 +443,7 @@ prefill_page_head_kernel(StorePHParams p) {
   __shared__ int s_row[P];               // the run's tokens' rows j, ascending
   __shared__ int s_run;
   __shared__ uint32_t s_bits[2][NW];
-  __shared__ float s_max[2][32], s_slab[4];
-  __shared__ __align__(16) uint8_t s_code[NT];
+  __shared__ float s_max[2][4], s_slab[4];
   __shared__ float2 s_scale[2];          // K's, V's: (scale, -1 / scale, 0 outside the exact range)
   // the heads' maxima of two runs, and their barriers: head r of the cluster
   // writes entry r of every head.  (Two of each: a head can be one run ahead.)
@@ -582,14 +608,14 @@ prefill_page_head_kernel(StorePHParams p) {
       // part of a page, or values or scales out of the ordinary
       const int d = tid & (kHD - 1);
       const bool active = tid < kHD;
-      const __nv_bfloat16 *kin = p.k + row0 + d, *vin = p.v + row0 + d;
+      const Row<1>* kin = reinterpret_cast<const Row<1>*>(p.k + row0 + d);
+      const Row<1>* vin = reinterpret_cast<const Row<1>*>(p.v + row0 + d);
       // (a whole page has its sums already)
-      float sum = active && !full ? p.slab_sum[so + d] : 0.0f;
-      sum = store_columns<I8, P>(p, blk, active, d, kin, vin, kin[0], vin[0], HD, R, s_row, cnt0,
-                                 sum, s_max, s_code);
+      float sum[1] = {active && !full ? p.slab_sum[so + d] : 0.0f};
+      store_run<I8, P, 1>(p, blk, active, d, kin, vin, *kin, *vin, HD, R, s_row, cnt0, sum, s_max);
       if (!full && active) {
-        p.slab_sum[so + d] = sum;
-        mean.x = sum / fcnt;
+        p.slab_sum[so + d] = sum[0];
+        mean.x = sum[0] / fcnt;
         const float a = warp_max(fabsf(mean.x));
         if (lane == 0) s_slab[warp] = a;
       }
@@ -726,7 +752,7 @@ cudaError_t launch_t(const StorePHParams& p, int n_layers, cudaStream_t s) {
                    : launch_prefill<I8, P, false>(p, n_layers, s);
   cudaError_t e = launch_pdl(append_page_head_kernel<I8, P>,
                              dim3((unsigned)p.T, (unsigned)n_layers),
-                             dim3((unsigned)(p.Hkv * kHD)), 0, s, p);
+                             dim3((unsigned)(p.Hkv * 32)), 0, s, p);
   count_launch();
   return e;
 }
