@@ -120,6 +120,37 @@ def test_store_long_call_and_odd_values(fmt):
     _same_slab(ref, c, 0)
 
 
+@pytest.mark.parametrize("P,H", [(16, 8), (64, 4), (128, 1)])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T", [511, 512, 700, 4095])
+def test_store_of_short_and_long_runs_in_one_call(fmt, P, H, T):
+    """Calls between an append and a prefill: single tokens, short runs, the longest short run and the
+    shortest long one, and whole pages side by side, on pages with and without earlier tokens."""
+    import sparse_attention_decode_indexer_gb300 as ssa
+    rng = np.random.default_rng([P, T])
+    lengths, page = [], 0
+    pos = []
+    while len(pos) < T:
+        n = int(rng.choice([1, 1, 2, 8, 9, P, P, P - 1]))
+        n = min(n, P, T - len(pos))
+        j = int(rng.integers(0, P - n + 1)) if n < P else 0
+        pos += [page * P + j + i for i in range(n)]
+        lengths.append(n)
+        page += int(rng.integers(1, 3))
+    pos, Lp = np.array(pos), page + 1
+    lay = _layout(fmt, P=P, Hq=H, Hkv=H, L=1, Lp=Lp, B=1, nmax=1, k=1)
+    c, status = _cache(lay)
+    ref = RefPages(fmt, Lp, H, P)
+    for i in range(2):                            # the second call writes over the first's rows
+        k, kf = _bf16(rng, 1, T, H, D, scale=3.0 ** i)
+        v, vf = _bf16(rng, 1, T, H, D)
+        ssa.ssa_store_kv_mirror(c, 0, 1, k.cuda(), v.cuda(), torch.from_numpy(pos).cuda(), status)
+        ref.store(kf[0], vf[0], pos)
+    assert int(status.item()) == 0
+    _same_pages(ref, _pages(c, 0), np.arange(Lp), np.arange(Lp))
+    _same_slab(ref, c, 0)
+
+
 def test_store_flags_bad_positions():
     import sparse_attention_decode_indexer_gb300 as ssa
     lay = _layout("int8_page_head", P=16, Hq=1, Hkv=1, L=1, Lp=3, B=1, nmax=3, k=1)
