@@ -511,8 +511,9 @@ int ssa_copy_pages(const ssa_layout *lay, const ssa_cache *c, const int32_t *src
  * New pages are the lowest free ids, in row order (the copy, then growth);
  * pages let go in this call count as free.  New pages start with an empty slab
  * row.  With a mirror, new pages and pages that became free give their slots
- * back; without one every page keeps the slot it has.  Entries past a row's
- * pages become -1.
+ * back; without one every page keeps the slot it has (so a cache without a
+ * mirror wants pool_slots >= logical_pages: a new page without a slot holds no
+ * K and V).  Entries past a row's pages become -1.
  * Too few free pages: SSA_ST_NO_PAGES, and the rows that got none are cut to
  * the tokens their pages hold (a missing copy cuts the partly filled page).
  * A parent below -1 or at B and above: SSA_ST_BAD_ID, the row goes on; a

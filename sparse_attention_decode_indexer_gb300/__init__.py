@@ -424,6 +424,12 @@ def ssa_sparse_paged_decode_host_tail(cache: KVCache, layer0: int, n_layers: int
 # owners of the pages
 # ---------------------------------------------------------------------------
 
+def _on_current_device(device):
+    """The calls launch on the current device: refuse tensors of another."""
+    if device.type != "cuda" or device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on {device}, which is not the current CUDA device")
+
+
 def _ints(name, t, n, device):
     """A contiguous int32 device tensor of n entries, or an error."""
     if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != device:
@@ -470,6 +476,7 @@ def _same_pages(cache: KVCache, table: RequestTable):
 
 def ssa_page_refs(table: RequestTable, status=None, stream=None):
     """Count the rows' references anew (any pins are forgotten)."""
+    _on_current_device(table.ref.device)
     _check(lib().ssa_page_refs(table._lay, table._c, _ptr(status), _stream(stream)))
 
 
@@ -477,8 +484,9 @@ def ssa_copy_pages(cache: KVCache, src, dst, status, ws, stream=None):
     """Page dst[i] := page src[i] in every layer; int32 device lists, negative
     ids are padding."""
     n, dev = src.numel(), cache.slot_of.device
-    _check(lib().ssa_copy_pages(cache._lay, cache._c, _ints("src", src, n, dev),
-                                _ints("dst", dst, n, dev), n, _ptr(status), _ptr(ws),
+    src, dst = _ints("src", src, n, dev), _ints("dst", dst, n, dev)
+    _on_current_device(dev)
+    _check(lib().ssa_copy_pages(cache._lay, cache._c, src, dst, n, _ptr(status), _ptr(ws),
                                 _stream(stream)))
 
 
@@ -489,10 +497,11 @@ def ssa_fork_requests(cache: KVCache, table: RequestTable, parent, new_lens, sta
     filled ones copied, new ones taken, unused ones freed."""
     _same_pages(cache, table)
     B, dev = cache.layout.batch, cache.slot_of.device
-    _check(lib().ssa_fork_requests(cache._lay, cache._c, table._c, _ints("parent", parent, B, dev),
-                                   None if new_lens is None else
-                                   _ints("new_lens", new_lens, B, dev),
-                                   _ptr(status), _ptr(ws), _stream(stream)))
+    parent = _ints("parent", parent, B, dev)
+    new_lens = None if new_lens is None else _ints("new_lens", new_lens, B, dev)
+    _on_current_device(dev)
+    _check(lib().ssa_fork_requests(cache._lay, cache._c, table._c, parent, new_lens, _ptr(status),
+                                   _ptr(ws), _stream(stream)))
 
 
 def ssa_compact_pages(cache: KVCache, table: RequestTable, status, ws, moved_from=None,
@@ -503,6 +512,7 @@ def ssa_compact_pages(cache: KVCache, table: RequestTable, status, ws, moved_fro
     Lp, dev = cache.layout.logical_pages, cache.slot_of.device
     outs = [None if t is None else _ints(name, t, n, dev) for name, t, n in (
         ("moved_from", moved_from, Lp), ("moved_to", moved_to, Lp), ("n_moved", n_moved, 1))]
+    _on_current_device(dev)
     _check(lib().ssa_compact_pages(cache._lay, cache._c, table._c, *outs, _ptr(status), _ptr(ws),
                                    _stream(stream)))
 
@@ -612,6 +622,7 @@ def ssa_rope(plan: RopePlan, positions, q=None, k=None, q_out=None, k_out=None, 
     n_layers = shape[0] if len(shape) == 4 else 1
     if T == 0 or n_layers == 0:
         return
+    _on_current_device(dev)
     _check(lib().ssa_rope(dtype, plan.head_dim, plan.rotary_dim, plan.interleaved, inverse,
                           plan._freq, plan.factor, n_layers, T, positions.data_ptr(), wide,
                           offset, cq, ck, _stream(stream)))

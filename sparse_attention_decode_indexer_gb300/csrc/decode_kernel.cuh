@@ -693,13 +693,15 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
   // softmax state of heads 2c, 2c+1 (the lanes that own those O^T columns);
   // fp8: probabilities carry v_scale / vref, vref a power of two above every
   // V scale seen so far (0 before the first block)
-  float m_run0, m_run1, l_run0, l_run1, vref;
+  // page_head: vref follows the page's scale down as well (vtop: its highest)
+  float m_run0, m_run1, l_run0, l_run1, vref, vtop;
   auto reset = [&]() {
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.0f;
     m_run0 = m_run1 = -INFINITY;
     l_run0 = l_run1 = 0.0f;
     vref = FP8 ? 0.0f : 1.0f;
+    vtop = 0.0f;
   };
   reset();
   // token of MMA row r4 and r4+8 within a 16-token block.  fp8: rows 2j, 2j+1
@@ -1161,7 +1163,25 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
         const float mu0 = mn0 == -INFINITY ? 0.0f : mn0, mu1 = mn1 == -INFINITY ? 0.0f : mn1;
         float oc0 = corr0, oc1 = corr1;
         float vinv = 1.0f;
-        if (FP8) {
+        if (PH) {
+          // one scale for the block's tokens, the same in every lane: the
+          // reference is the power of two above it, moved only when a page's
+          // scale leaves [2^-9, 1) of it, so that small pages keep their
+          // precision in f16 beside large ones; at most 2^60 below the largest
+          // so far, which keeps the fp32 sums in range
+          const float pv = page_sc.y;
+          const float low = fmaxf(vtop * 0x1p-60f, 0x1p-126f);
+          if (pv >= vref || (pv > 0.0f && pv < vref * 0x1p-9f && vref > low)) {
+            const float nref =
+                fmaxf(__uint_as_float(((__float_as_uint(pv) >> 23) + 1) << 23), low);
+            const float ratio = vref * pow2_rcp(nref);
+            oc0 *= ratio;
+            oc1 *= ratio;
+            vref = nref;
+            vtop = fmaxf(vtop, nref);
+          }
+          vinv = pow2_rcp(vref);
+        } else if (FP8) {
           float vmax = fmaxf(vsA[0], vsB[0]);
 #pragma unroll
           for (int j = 1; j < NB; ++j) vmax = fmaxf(vmax, fmaxf(vsA[j], vsB[j]));

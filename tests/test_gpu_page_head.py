@@ -237,6 +237,84 @@ def test_attention_against_64_bits(fmt, P, Hq, Hkv, k, lens):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("heavy", [0, 1, 2, 3])
+def test_attention_over_pages_of_very_different_scale(fmt, heavy):
+    """V of 2^-28, 2^-14, 1 and 2^26 by page, an all-zero page, and nearly all weight on one page: a
+    small page beside large ones keeps its precision."""
+    import sparse_attention_decode_indexer_gb300 as ssa
+    P, Hq, n = 32, 4, 5
+    lay = _layout(fmt, P=P, Hq=Hq, Hkv=1, L=1, Lp=n, B=1, nmax=n, k=n)
+    rng = np.random.default_rng(heavy)
+    c, status = _cache(lay)
+    ref = RefPages(fmt, n, 1, P)
+    k, _ = _bf16(rng, 1, n * P, 1, D, scale=0.05)
+    v, _ = _bf16(rng, 1, n * P, 1, D)
+    order = np.array([2.0 ** -14, 2.0 ** 26, 2.0 ** -28, 1.0, 0.0], np.float32)
+    v = (v.view(1, n, P, 1, D) * torch.from_numpy(order).view(1, n, 1, 1, 1).bfloat16()).view(1, n * P, 1, D)
+    q, _ = _bf16(rng, 1, 1, Hq, D)
+    # the heavy page's keys lie along q: its scores are about 90 above the others'
+    k.view(n, P, D)[heavy] += (q[0, 0].float().mean(0) * 16).bfloat16()
+    ssa.ssa_store_kv_mirror(c, 0, 1, k.cuda(), v.cuda(), torch.arange(n * P, device="cuda"), status)
+    ref.store(k.float().numpy()[0], v.float().numpy()[0], np.arange(n * P))
+    sel = torch.full((1, 1, lay.max_sel), -1, dtype=torch.int32, device="cuda")
+    sel[..., :n] = torch.arange(n)
+    lens = torch.tensor([n * P], dtype=torch.int32, device="cuda")
+    out = torch.empty((1, 1, Hq, D), dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros((ssa.ssa_workspace_size(lay),), dtype=torch.uint8, device="cuda")
+    ssa.ssa_sparse_paged_decode(c, 0, 1, q.cuda(), sel, sel, lens, sm_scale(), out, status, ws)
+    assert int(status.item()) == 0
+    _check_attention(lay, [ref], q, sel.cpu().numpy(), np.arange(n)[None], [n * P], out, fmt)
+
+
+def test_captured_store_and_attention_replay():
+    """A store and an attention captured on a stream of their own: the replay stores what k, v and pos
+    hold then, into pages that were cleared, and attends over it."""
+    import sparse_attention_decode_indexer_gb300 as ssa
+    fmt, P = "int8_page_head", 64
+    lay = _layout(fmt, P=P, Hq=8, Hkv=2, L=1, Lp=6, B=1, nmax=6, k=5)
+    rng = np.random.default_rng(8)
+    for T in (1, 300):
+        c, status = _cache(lay)
+        k, v = (torch.zeros((1, T, 2, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        pos = torch.arange(T, device="cuda")
+        q = _bf16(rng, 1, 1, 8, D)[0]
+        qd = q.cuda()
+        sel = torch.full((1, 1, lay.max_sel), -1, dtype=torch.int32, device="cuda")
+        n = -(-T // P)
+        sel[..., :n] = torch.arange(n)
+        lens = torch.tensor([T], dtype=torch.int32, device="cuda")
+        out = torch.empty((1, 1, 8, D), dtype=torch.bfloat16, device="cuda")
+        ws = torch.zeros((ssa.ssa_workspace_size(lay),), dtype=torch.uint8, device="cuda")
+
+        def calls():
+            c.slab_cnt.zero_()
+            c.slab_sum.zero_()
+            ssa.ssa_store_kv_mirror(c, 0, 1, k, v, pos, status)
+            ssa.ssa_sparse_paged_decode(c, 0, 1, qd, sel, sel, lens, sm_scale(), out, status, ws)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            calls()
+            s.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                calls()
+        for scale in (4.0, 0.5):
+            kk, kf = _bf16(rng, 1, T, 2, D, scale=scale)
+            vv, vf = _bf16(rng, 1, T, 2, D, scale=scale)
+            k.copy_(kk)
+            v.copy_(vv)
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            ref = RefPages(fmt, 6, 2, P)
+            ref.store(kf[0], vf[0], np.arange(T))
+            assert int(status.item()) == 0
+            _same_slab(ref, c, 0)
+            _check_attention(lay, [ref], q, sel.cpu().numpy(), np.arange(6)[None], [T], out, fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_attention_unselected_bytes_do_not_matter(fmt):
     """Codes behind a request's last token (NaN codes and large ones) leave the output as it is."""
     import sparse_attention_decode_indexer_gb300 as ssa
