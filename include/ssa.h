@@ -13,9 +13,16 @@
  *
  * and the write path that fills the cache:
  *
- *   ssa_store_kv_mirror     quantise (fp8) or pass through (bf16) new K/V,
- *                           write the pinned host mirror and, when resident,
- *                           the GPU slot; update the indexer slab
+ *   ssa_store_kv_mirror     quantise (8-bit formats) or pass through (bf16)
+ *                           new K/V, write the pinned host mirror and, when
+ *                           resident, the GPU slot; update the indexer slab
+ *
+ * and what a serving loop does around them:
+ *
+ *   ssa_rope                rotary positions of queries and new keys
+ *   ssa_copy_pages, ssa_fork_requests, ssa_compact_pages
+ *                           who owns the pages: copies, forks, growth, freed
+ *                           requests, a compact page space
  *
  * Sources (web pages, cited by title and section):
  *   FreeToken PR #499 "host-RAM KV tier for sparse-attention models
@@ -344,7 +351,7 @@ int ssa_sparse_paged_decode_fetch(const ssa_layout *lay, const ssa_cache *c, int
  *   1. U = distinct logical ids selected by any layer of the range, ascending;
  *   2-5. as ssa_ensure_resident, on that one state: hits touched, misses take
  *      free slots then untouched slots by (last_use, slot), rebind, clock + 1;
- *      each miss's K, V (and fp8 scales) are copied into the same slot of
+ *      each miss's K, V (and scales) are copied into the same slot of
  *      EVERY layer's pool (one launch for all layers);
  *   then phys [n_layers][B][W] = slot_of[layer0][bt[b][sel]] for every layer.
  *   miss_page_opt, miss_slot_opt [n_layers * B * W] int32 out or NULL
