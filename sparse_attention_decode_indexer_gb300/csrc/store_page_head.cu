@@ -20,10 +20,8 @@
 // A run is the consecutive tokens of one page in a call.  Three ways to store
 // one, the division x / s' being most of their arithmetic.  s' is the block's,
 // so its reciprocal is computed once and each quotient is corrected from its
-// exact residual twice (Markstein 1990: a faithful quotient plus its fused
-// residual times the correctly rounded reciprocal is the correctly rounded
-// quotient), two elements per f32x2 instruction: 5 instead of about 20 per
-// pair.
+// fused residual (after Markstein 1990), two elements per f32x2 instruction: 3
+// instead of about 20 per pair.
 //   * a whole page (prefill): a CTA per head.  Its rows wait in shared memory
 //     while the scale becomes known, so that each input is read once.  A thread
 //     has 8 dimensions of 4 consecutive tokens at a time, so V leaves as whole
@@ -159,25 +157,31 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// Divides by one block's scale.  With ny = -RN(1 / s) and nx = -x, each step
-// corrects the quotient by its residual q s - x (exact in one fma); the signs
-// are such that a zero keeps its own.  For s in [2^-90, 2^100] and x finite:
-// nothing on the way over- or underflows then unless the quotient is below
-// 2^-12 (every code 0).
+// Divides by one block's scale, to quotients whose codes are those of the IEEE
+// quotients.  With ny = -RN(1 / s) and nx = -x, one step corrects the quotient
+// by its residual q s - x; the signs are such that a zero keeps its own.  The
+// result is RN(x / s + e) with |e| < 2^-45 x / s, so it can differ from
+// RN(x / s), and then by one unit, only where x / s lies that close to the
+// middle between two floats; and a code can differ only where one of the two
+// is a border between codes (at most 9 significant bits).  x has 8 significant
+// bits and s 24, and the only such s has all of them set (with x a power of
+// two): the search over every border is a test.  So: any s in [2^-90, 2^100]
+// but those, x finite; nothing on the way over- or underflows then unless the
+// quotient is below 2^-12 (every code 0).
 struct Divider {
   uint64_t s2, ny2;
   __device__ __forceinline__ Divider(float2 s) : s2(pack2(s.x, s.x)), ny2(pack2(s.y, s.y)) {}
   // two negated elements -> the two quotients
   __device__ __forceinline__ uint64_t operator()(float nx0, float nx1) const {
     const uint64_t nx = pack2(nx0, nx1);
-    uint64_t q = mul2(nx, ny2);
-    q = fma2(fma2(q, s2, nx), ny2, q);
-    q = fma2(fma2(q, s2, nx), ny2, q);
-    return q;
+    const uint64_t q = mul2(nx, ny2);
+    return fma2(fma2(q, s2, nx), ny2, q);
   }
 };
 
-__device__ __forceinline__ bool divides(float s) { return s >= 0x1p-90f && s <= 0x1p100f; }
+__device__ __forceinline__ bool divides(float s) {
+  return s >= 0x1p-90f && s <= 0x1p100f && (__float_as_uint(s) & 0x7FFFFFu) != 0x7FFFFFu;
+}
 
 // Four quotients -> four codes, the first in byte 0.
 template <bool I8>
@@ -410,8 +414,8 @@ __device__ __forceinline__ bool whole_page(const StorePHParams& p, int t, int64_
 
 // Runs of any kind, but for whole pages where the other kernel stores those
 // (p.whole).  A warp per KV head, four dimensions a lane; grid (pieces of
-// p.chunk tokens, 1 or, MANY, up to 32, layers): a CTA stores the runs that
-// start in its piece.
+// p.chunk tokens, 1 or, MANY, more, layers): a CTA stores the runs that start
+// in its piece.
 template <bool I8, int P, bool MANY>
 __global__ void __launch_bounds__(256) append_page_head_kernel(
     const __grid_constant__ StorePHParams p) {
@@ -426,91 +430,100 @@ __global__ void __launch_bounds__(256) append_page_head_kernel(
   // the piece's positions, a lane each (every warp finds the same runs), in one
   // round trip with the first token's K and V
   const int chunk = MANY ? p.chunk : 1;
-  const int c0 = blockIdx.x * chunk, t_mine = c0 + lane;
-  bool start = false;
-  int64_t pos_mine = -1;
-  if (lane < chunk && t_mine < p.T) {
-    pos_mine = p.pos[t_mine];
-    const int64_t prev = t_mine > 0 ? p.pos[t_mine - 1] : -1;
-    start = pos_mine >= 0 && pos_mine / P < p.Lp;
-    if (!start && h == 0) set_status(p.status, SSA_ST_BAD_ID);
-    if (t_mine > 0) {
-      if (start && h == 0 && prev >= pos_mine) set_status(p.status, SSA_ST_BAD_POS);
-      if (prev >= 0 && prev / P == pos_mine / P) start = false;    // inside a run
-    }
-    if (MANY && p.whole && start && whole_page<P>(p, t_mine, pos_mine)) start = false;
-  }
-  const size_t in_c = (((size_t)li * p.T + c0) * HD + h * kHD + d) / 4;
-  const Row<4>* kin = reinterpret_cast<const Row<4>*>(p.k) + in_c;
-  const Row<4>* vin = reinterpret_cast<const Row<4>*>(p.v) + in_c;
-  Row<4> k0 = *kin, v0 = *vin;
-  int at = 0;                              // the token that kin, vin, k0 and v0 are of
+  const int first = blockIdx.x * chunk, end = min(first + chunk, p.T);
 #pragma unroll 1
-  for (uint32_t runs = __ballot_sync(0xffffffffu, start); runs; runs &= runs - 1) {
-    const int next = __ffs(runs) - 1;
-    if (MANY && next > at) {
-      kin += (size_t)(next - at) * (HD / 4);
-      vin += (size_t)(next - at) * (HD / 4);
+  for (int c0 = first; c0 < end; c0 += 32) {
+    const int t_mine = c0 + lane;
+    bool start = false;
+    int64_t pos_mine = -1;
+    if (t_mine < end) {
+      pos_mine = p.pos[t_mine];
+      const int64_t prev = t_mine > 0 ? p.pos[t_mine - 1] : -1;
+      start = pos_mine >= 0 && pos_mine / P < p.Lp;
+      if (!start && h == 0) set_status(p.status, SSA_ST_BAD_ID);
+      if (t_mine > 0) {
+        if (start && h == 0 && prev >= pos_mine) set_status(p.status, SSA_ST_BAD_POS);
+        if (prev >= 0 && prev / P == pos_mine / P) start = false;    // inside a run
+      }
+      if (MANY && p.whole && start && whole_page<P>(p, t_mine, pos_mine)) start = false;
+    }
+    const size_t in_c = (((size_t)li * p.T + c0) * HD + h * kHD + d) / 4;
+    const Row<4>* kin = reinterpret_cast<const Row<4>*>(p.k) + in_c;
+    const Row<4>* vin = reinterpret_cast<const Row<4>*>(p.v) + in_c;
+    Row<4> k0, v0;
+    if (!MANY) {
       k0 = *kin;
       v0 = *vin;
-      at = next;
     }
-    const int t0 = c0 + at;
-    const int pg = (int)(__shfl_sync(0xffffffffu, pos_mine, at) / P);
-    const size_t lp = (size_t)layer * p.Lp + pg;
-    const size_t so = lp * HD + h * kHD + d;
-    const float4 old_sum = *reinterpret_cast<const float4*>(p.slab_sum + so);
-    const int cnt0 = p.slab_cnt[lp];
-    int slot = p.slot_of[lp];
-    // the run's length
-    if (tid == 0) s_run = P;
-    __syncthreads();
-    for (int r = tid; r < P; r += blockDim.x) {
-      const int t = t0 + r;
-      const int64_t x = t < p.T ? p.pos[t] : -1;
-      if (x < 0 || x / P != pg) {
-        atomicMin(&s_run, r);
-      } else {
-        s_row[r] = (int)(x % P);
-        if (r > 0 && x <= p.pos[t - 1]) set_status(p.status, SSA_ST_BAD_POS);
+    int at = 0;                              // the token that kin and vin are of
+#pragma unroll 1
+    for (uint32_t runs = __ballot_sync(0xffffffffu, start); runs; runs &= runs - 1) {
+      const int next = __ffs(runs) - 1;
+      if (MANY) {
+        kin += (size_t)(next - at) * (HD / 4);
+        vin += (size_t)(next - at) * (HD / 4);
+        k0 = *kin;
+        v0 = *vin;
+        at = next;
       }
-    }
-    if (slot >= p.S) {                     // corrupt state: never write through it
-      if (tid == 0) set_status(p.status, SSA_ST_BAD_ID);
-      slot = -1;
-    }
-    const Block blk(p, layer, pg, slot, h);
-    __syncthreads();
-    const int R = s_run;
-    float sum[4] = {old_sum.x, old_sum.y, old_sum.z, old_sum.w};
-    store_run<I8, P, 4>(p, blk, true, d, kin, vin, k0, v0, HD, R, [&](int r) { return s_row[r]; },
-                        cnt0, sum, nullptr);
-    *reinterpret_cast<float4*>(p.slab_sum + so) = make_float4(sum[0], sum[1], sum[2], sum[3]);
-    const int cnt = cnt0 + R;
-    float mean[4], a = 0.0f;
+      const int t0 = c0 + at;
+      const int pg = (int)(__shfl_sync(0xffffffffu, pos_mine, at) / P);
+      const size_t lp = (size_t)layer * p.Lp + pg;
+      const size_t so = lp * HD + h * kHD + d;
+      const float4 old_sum = *reinterpret_cast<const float4*>(p.slab_sum + so);
+      const int cnt0 = p.slab_cnt[lp];
+      int slot = p.slot_of[lp];
+      // the run's length
+      if (tid == 0) s_run = P;
+      __syncthreads();
+      for (int r = tid; r < P; r += blockDim.x) {
+        const int t = t0 + r;
+        const int64_t x = t < p.T ? p.pos[t] : -1;
+        if (x < 0 || x / P != pg) {
+          atomicMin(&s_run, r);
+        } else {
+          s_row[r] = (int)(x % P);
+          if (r > 0 && x <= p.pos[t - 1]) set_status(p.status, SSA_ST_BAD_POS);
+        }
+      }
+      if (slot >= p.S) {                     // corrupt state: never write through it
+        if (tid == 0) set_status(p.status, SSA_ST_BAD_ID);
+        slot = -1;
+      }
+      const Block blk(p, layer, pg, slot, h);
+      __syncthreads();
+      const int R = s_run;
+      float sum[4] = {old_sum.x, old_sum.y, old_sum.z, old_sum.w};
+      store_run<I8, P, 4>(p, blk, true, d, kin, vin, k0, v0, HD, R, [&](int r) { return s_row[r]; },
+                          cnt0, sum, nullptr);
+      *reinterpret_cast<float4*>(p.slab_sum + so) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+      const int cnt = cnt0 + R;
+      float mean[4], a = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      mean[e] = sum[e] / (float)cnt;
-      a = fmaxf(a, fabsf(mean[e]));
-    }
-    a = warp_max(a);
-    if (lane == 0) s_head[h] = a;
-    __syncthreads();
-    float amax = 0.0f;
-    for (int w = 0; w < Hkv; ++w) amax = fmaxf(amax, s_head[w]);
-    const float s = amax / 127.0f;
-    char4 code;
-    code.x = (signed char)slab_code(mean[0], amax, s);
-    code.y = (signed char)slab_code(mean[1], amax, s);
-    code.z = (signed char)slab_code(mean[2], amax, s);
-    code.w = (signed char)slab_code(mean[3], amax, s);
-    *reinterpret_cast<char4*>(p.slab + so) = code;
-    if (tid == 0) {
-      p.slab_cnt[lp] = cnt;
-      p.slab_scale[lp] = s;
+      for (int e = 0; e < 4; ++e) {
+        mean[e] = sum[e] / (float)cnt;
+        a = fmaxf(a, fabsf(mean[e]));
+      }
+      a = warp_max(a);
+      if (lane == 0) s_head[h] = a;
+      __syncthreads();
+      float amax = 0.0f;
+      for (int w = 0; w < Hkv; ++w) amax = fmaxf(amax, s_head[w]);
+      const float s = amax / 127.0f;
+      char4 code;
+      code.x = (signed char)slab_code(mean[0], amax, s);
+      code.y = (signed char)slab_code(mean[1], amax, s);
+      code.z = (signed char)slab_code(mean[2], amax, s);
+      code.w = (signed char)slab_code(mean[3], amax, s);
+      *reinterpret_cast<char4*>(p.slab + so) = code;
+      if (tid == 0) {
+        p.slab_cnt[lp] = cnt;
+        p.slab_scale[lp] = s;
+      }
+      if (!MANY) return;
+      __syncthreads();                       // s_run, s_row, s_head: the next run's
     }
     if (!MANY) return;
-    __syncthreads();                       // s_run, s_row, s_head: the next run's
   }
 }
 
@@ -535,10 +548,8 @@ store_page_head_kernel(const __grid_constant__ StorePHParams p) {
   uint4* vx = kx + P * kRowUnits;
   uint32_t* vt = reinterpret_cast<uint32_t*>(dsm);                 // [d][P / 4 words], swizzled
   __shared__ int s_first;                // the page's first token
-  __shared__ int64_t s_pos;              // and its position
   __shared__ uint32_t s_bits[2][NW];
   __shared__ float s_max[2][4], s_slab[2];
-  __shared__ float2 s_scale[2];          // K's, V's: (scale, -1 / scale, 0 outside the exact range)
   __shared__ float s_heads[8];           // the heads' maxima, pushed by each of them
   __shared__ uint64_t s_bar;             // counts their bytes
   constexpr float kQmax = I8 ? 127.0f : 448.0f;
@@ -550,7 +561,7 @@ store_page_head_kernel(const __grid_constant__ StorePHParams p) {
   }
   pdl_trigger();
   // every head's barrier is there before the first push (waited for below)
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
   const int c = tid % kRowUnits, g = tid / kRowUnits;              // dims 8c.., tokens 4g..
   const int h = blockIdx.x % p.Hkv, Hkv = p.Hkv, HD = Hkv * kHD;   // h: the cluster's rank
@@ -567,14 +578,14 @@ store_page_head_kernel(const __grid_constant__ StorePHParams p) {
       atomicMax(&s_first, t);
     }
   }
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
   const int t0 = s_first;
-  if (t0 < 0) return;
-  if (t == t0) s_pos = p.pos[t];
-  __syncthreads();
+  if (t0 < 0) {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    return;
+  }
 
-  const int pg = (int)(s_pos / P);
+  const int pg = (int)(p.pos[t0] / P);
   const size_t lp = (size_t)layer * p.Lp + pg;
   const size_t so = (lp * Hkv + h) * kHD;
   const size_t row0 = ((size_t)li * p.T + t0) * HD + h * kHD;
@@ -599,12 +610,10 @@ store_page_head_kernel(const __grid_constant__ StorePHParams p) {
     slot = -1;
   }
   const Block blk(p, layer, pg, slot, h);
-  // warps 0 and 1 have the slab's sums to make, warp 2 (3) K's (V's) scale
   float2 sum = make_float2(0.0f, 0.0f), mean = sum;      // of dims 2 tid, 2 tid + 1
-  float old = 0.0f;
   if (tid < kHD / 2) sum = reinterpret_cast<const float2*>(p.slab_sum + so)[tid];
-  if (tid == 64 && cnt0 > 0) old = blk.scale(p.k_scale_m, p.k_scale);
-  if (tid == 96 && cnt0 > 0) old = blk.scale(p.v_scale_m, p.v_scale);
+  const float old_k = cnt0 > 0 ? blk.scale(p.k_scale_m, p.k_scale) : 0.0f;
+  const float old_v = cnt0 > 0 ? blk.scale(p.v_scale_m, p.v_scale) : 0.0f;
   asm volatile("cp.async.wait_all;" ::: "memory");
   // the largest magnitudes
   {
@@ -620,7 +629,17 @@ store_page_head_kernel(const __grid_constant__ StorePHParams p) {
       s_bits[1][warp] = mv;
     }
   }
-  __syncthreads();
+  __syncthreads();                         // (every thread has read the old scales)
+  // (scale, -1 / scale, or 0 where values are not finite or the Divider's range ends)
+  auto scale_of = [&](const uint32_t* bits, float old) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) m = max(m, bits[w]);
+    const float need = __uint_as_float(m << 16) / kQmax;
+    const float s = cnt0 > 0 ? fmaxf(old, need) : need;
+    return make_float2(s, m < 0x7F80u && divides(s) ? -(1.0f / s) : 0.0f);
+  };
+  const float2 sck = scale_of(s_bits[0], old_k), scv = scale_of(s_bits[1], old_v);
   if (tid < kHD / 2) {
     // fp32 running sums in token order, two dimensions per thread
     const uint32_t* col = reinterpret_cast<const uint32_t*>(kx) + tid;
@@ -635,20 +654,13 @@ store_page_head_kernel(const __grid_constant__ StorePHParams p) {
     mean = make_float2(sum.x / fcnt, sum.y / fcnt);
     const float a = warp_max(fmaxf(fabsf(mean.x), fabsf(mean.y)));
     if (lane == 0) s_slab[warp] = a;
-  } else if (tid == 64 || tid == 96) {
-    uint32_t m = 0;
-    for (int w = 0; w < NW; ++w) m = max(m, s_bits[warp - 2][w]);
-    const float need = __uint_as_float(m << 16) / kQmax;
-    const float s = cnt0 > 0 ? fmaxf(old, need) : need;
-    // finite values, and a scale that keeps the quotients exact (see Divider)
-    const bool exact = m < 0x7F80u && divides(s);
-    s_scale[warp - 2] = make_float2(s, exact ? -(1.0f / s) : 0.0f);
   }
-  __syncthreads();
-  // the page's heads exchange their maxima while the codes are made
-  if (tid == 0) mbar_arrive_expect_tx(&s_bar, 4 * Hkv);
-  if (tid < Hkv) push_f32(&s_heads[h], &s_bar, tid, fmaxf(s_slab[0], s_slab[1]));
-  const float2 sck = s_scale[0], scv = s_scale[1];
+  // the page's heads exchange their maxima while V's codes are made
+  auto exchange = [&]() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (tid == 0) mbar_arrive_expect_tx(&s_bar, 4 * Hkv);
+    if (tid < Hkv) push_f32(&s_heads[h], &s_bar, tid, fmaxf(s_slab[0], s_slab[1]));
+  };
   if (sck.y != 0.0f && scv.y != 0.0f) {
     if (tid == 0) {
       blk.set_scale(p.k_scale_m, p.k_scale, sck.x);
@@ -673,6 +685,7 @@ store_page_head_kernel(const __grid_constant__ StorePHParams p) {
       if (kp) *reinterpret_cast<uint2*>(kp + off) = out;
     }
     __syncthreads();                       // K's rows make room for V's codes
+    exchange();
     // V: words of 4 tokens per dimension; word r / 4 of row d goes to a place
     // that spreads the 16 dimension groups over the banks
     constexpr int kWords = P / 4, kVec = P / 16;         // words, 16-byte units of a row
@@ -718,6 +731,8 @@ store_page_head_kernel(const __grid_constant__ StorePHParams p) {
     float unused[1] = {0.0f};
     store_run<I8, P, 1>(p, blk, tid < kHD, d, kin, vin, *kin, *vin, HD, P, [](int r) { return r; },
                         cnt0, unused, s_max);
+    __syncthreads();
+    exchange();
   }
 
   // the page's slab row, now that every head's maximum is there
@@ -781,7 +796,7 @@ cudaError_t launch_t(StorePHParams p, int n_layers, cudaStream_t s) {
     return e;
   }
   // pieces: single tokens of many requests want many CTAs, a prefill few
-  p.chunk = p.T < 4096 ? 4 : (P == 16 ? 16 : 32);
+  p.chunk = p.T < 4096 ? 4 : (P == 16 ? 16 : 64);
   p.whole = P > 16;
   e = launch_pdl(append_page_head_kernel<I8, P, true>,
                  dim3((unsigned)((p.T + (long long)p.chunk - 1) / p.chunk), (unsigned)n_layers),
