@@ -796,7 +796,7 @@ cudaError_t launch_t(StorePHParams p, int n_layers, cudaStream_t s) {
     return e;
   }
   // pieces: single tokens of many requests want many CTAs, a prefill few
-  p.chunk = p.T < 4096 ? 4 : (P == 16 ? 16 : 64);
+  p.chunk = p.T < 1024 ? 4 : (P == 16 ? 16 : (p.T < 4096 ? 8 : 64));
   p.whole = P > 16;
   e = launch_pdl(append_page_head_kernel<I8, P, true>,
                  dim3((unsigned)((p.T + (long long)p.chunk - 1) / p.chunk), (unsigned)n_layers),
