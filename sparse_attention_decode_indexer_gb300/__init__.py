@@ -424,17 +424,20 @@ def ssa_sparse_paged_decode_host_tail(cache: KVCache, layer0: int, n_layers: int
 # owners of the pages
 # ---------------------------------------------------------------------------
 
-def _on_current_device(device):
-    """The calls launch on the current device: refuse tensors of another."""
-    if device.type != "cuda" or device.index != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors on {device}, which is not the current CUDA device")
+def _on_current_device(device: int):
+    """The calls launch on the current device: refuse tensors of another (by
+    ordinal, -1 for the host)."""
+    if device < 0 or device != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on device {device}, which is not the current CUDA device")
 
 
-def _ints(name, t, n, device):
-    """A contiguous int32 device tensor of n entries, or an error."""
-    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name}: {n} contiguous int32 on {device}, got {tuple(t.shape)} "
-                         f"{t.dtype} on {t.device}")
+def _ints(name, t, n, device: int):
+    """The address of a contiguous int32 tensor of n entries on a device
+    (ordinal), or an error."""
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or \
+            t.get_device() != device:
+        raise ValueError(f"{name}: {n} contiguous int32 on device {device}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
 
 
@@ -450,13 +453,13 @@ class RequestTable:
         self.layout = layout
         self.block_table = torch.as_tensor(block_table).to(device=device, dtype=i32).contiguous()
         self.seq_lens = torch.as_tensor(seq_lens).to(device=device, dtype=i32).contiguous()
-        dev = self.block_table.device
+        dev = self.block_table.get_device()
         _ints("block_table", self.block_table, layout.batch * layout.max_pages, dev)
         _ints("seq_lens", self.seq_lens, layout.batch, dev)
         if ref is None:
-            self.ref = torch.zeros((layout.logical_pages,), dtype=i32, device=dev)
+            self.ref = torch.zeros((layout.logical_pages,), dtype=i32, device=device)
         else:
-            self.ref = torch.as_tensor(ref).to(device=dev, dtype=i32).contiguous()
+            self.ref = torch.as_tensor(ref).to(device=device, dtype=i32).contiguous()
         _ints("ref", self.ref, layout.logical_pages, dev)
         self._c = SsaRequests(self.block_table.data_ptr(), self.seq_lens.data_ptr(),
                               self.ref.data_ptr())
@@ -470,20 +473,20 @@ def _same_pages(cache: KVCache, table: RequestTable):
     if (a.batch, a.max_pages, a.logical_pages, a.page_size) != \
             (b.batch, b.max_pages, b.logical_pages, b.page_size):
         raise ValueError("the cache and the request table have different layouts")
-    if cache.slot_of.device != table.ref.device:
+    if cache.slot_of.get_device() != table.ref.get_device():
         raise ValueError("the cache and the request table are on different devices")
 
 
 def ssa_page_refs(table: RequestTable, status=None, stream=None):
     """Count the rows' references anew (any pins are forgotten)."""
-    _on_current_device(table.ref.device)
+    _on_current_device(table.ref.get_device())
     _check(lib().ssa_page_refs(table._lay, table._c, _ptr(status), _stream(stream)))
 
 
 def ssa_copy_pages(cache: KVCache, src, dst, status, ws, stream=None):
     """Page dst[i] := page src[i] in every layer; int32 device lists, negative
     ids are padding."""
-    n, dev = src.numel(), cache.slot_of.device
+    n, dev = src.numel(), cache.slot_of.get_device()
     src, dst = _ints("src", src, n, dev), _ints("dst", dst, n, dev)
     _on_current_device(dev)
     _check(lib().ssa_copy_pages(cache._lay, cache._c, src, dst, n, _ptr(status), _ptr(ws),
@@ -496,7 +499,7 @@ def ssa_fork_requests(cache: KVCache, table: RequestTable, parent, new_lens, sta
     grown to new_lens[i] tokens (None: no growth): full pages shared, partly
     filled ones copied, new ones taken, unused ones freed."""
     _same_pages(cache, table)
-    B, dev = cache.layout.batch, cache.slot_of.device
+    B, dev = cache.layout.batch, cache.slot_of.get_device()
     parent = _ints("parent", parent, B, dev)
     new_lens = None if new_lens is None else _ints("new_lens", new_lens, B, dev)
     _on_current_device(dev)
@@ -509,7 +512,7 @@ def ssa_compact_pages(cache: KVCache, table: RequestTable, status, ws, moved_fro
     """Move the live pages to the lowest ids; the moves go to moved_from /
     moved_to ([logical_pages]) and their number to n_moved ([1])."""
     _same_pages(cache, table)
-    Lp, dev = cache.layout.logical_pages, cache.slot_of.device
+    Lp, dev = cache.layout.logical_pages, cache.slot_of.get_device()
     outs = [None if t is None else _ints(name, t, n, dev) for name, t, n in (
         ("moved_from", moved_from, Lp), ("moved_to", moved_to, Lp), ("n_moved", n_moved, 1))]
     _on_current_device(dev)
@@ -574,7 +577,7 @@ class RopePlan:
         # two's complement: the same 64 bits
         self.freq = torch.tensor([f - (1 << 64) if f >= 1 << 63 else f for f in freq],
                                  dtype=torch.int64, device=device)
-        self._freq = self.freq.data_ptr()
+        self._freq, self._dev = self.freq.data_ptr(), self.freq.get_device()
 
 
 def _rope_tensor(plan, name, x, out, shape):
@@ -587,8 +590,10 @@ def _rope_tensor(plan, name, x, out, shape):
         raise ValueError(f"{name}: [n_layers][T][heads][D] or [T][heads][D] with (T, D) of the "
                          f"positions and the plan and the same layers for q and k, got "
                          f"{tuple(got)}")
-    st, so = x.stride(), out.stride()
-    if out is not x and (out.shape != got or out.dtype != x.dtype or out.device != x.device):
+    st = x.stride()
+    so = st if out is x else out.stride()
+    if out is not x and (out.shape != got or out.dtype != x.dtype or
+                         out.get_device() != plan._dev):
         raise ValueError(f"{name}_out: shape, type or device other than {name}'s")
     if st[-1] != 1 or so[-1] != 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
@@ -612,9 +617,10 @@ def ssa_rope(plan: RopePlan, positions, q=None, k=None, q_out=None, k_out=None, 
     if positions.dim() != 1 or not (wide or positions.dtype == torch.int32) or \
             not positions.is_contiguous():
         raise ValueError("positions: a contiguous [T] int32 or int64 tensor")
-    dev = plan.freq.device
-    if x.device != dev or positions.device != dev or (k is not None and k.device != dev):
-        raise ValueError(f"q, k and positions: on the plan's device, {dev}")
+    dev = plan._dev
+    if x.get_device() != dev or positions.get_device() != dev or \
+            (k is not None and k.get_device() != dev):
+        raise ValueError(f"q, k and positions: on the plan's device, {plan.freq.device}")
     T = positions.shape[0]
     shape = (x.shape[0], T, 0, plan.head_dim) if x.dim() == 4 else (T, 0, plan.head_dim)
     cq = _rope_tensor(plan, "q", q, q_out, shape) if q is not None else None

@@ -26,8 +26,9 @@
 //
 // What bounds them: the copies move each byte once in and once out (HBM; the
 // mirror's over the host link); the tables are latency, a few dependent
-// passes over B n_max and Lp words.  Copies: one CTA per 16 KB of a page and
-// layer, four 16-byte loads in flight per thread.
+// passes over B n_max and Lp words.  Copies: one CTA per 32 KB of a page's K or
+// V and layer, eight 16-byte loads in flight per thread (with 16 KB and four,
+// 400 pages of 12 layers took 118 us, now 101).
 #include "common.cuh"
 #include "internal.h"
 
@@ -35,8 +36,9 @@ namespace ssa {
 namespace {
 
 constexpr int kCopyThreads = 256;
-constexpr int kCopyUnroll = 4;
+constexpr int kCopyUnroll = 8;
 constexpr int kCopyChunk = kCopyThreads * kCopyUnroll;     // 16-byte units per CTA
+constexpr int kMoveUnroll = 4;                             // compaction: units per lane
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWords = 4096;         // words of page bits kept in shared memory
 constexpr int kPlanList = 1024;          // new pages kept there
@@ -130,34 +132,56 @@ struct PageCopy {
   }
 };
 
-// One CTA's share, chunk `x` (chunk 0 with the scales and counts).  `go` is
-// asked, by every thread, once the loads are on their way: false leaves dst as
-// it is.
+// One CTA's share, chunk `x`: 32 KB of K or V, or (the last chunk) the slab
+// row, scales and counts.  `go` is asked, by every thread, once the loads are
+// on their way: false leaves dst as it is.
 template <bool DST_SLOT, bool POOL, typename Go>
 __device__ __forceinline__ void copy_page(const PageCache& c, int layer, int src, int dst, int x,
                                           Go go) {
   const PageCopy<DST_SLOT, POOL> pc(c, layer, src, dst);
-  const long long total = pc.units(c);
-  uint4 buf[kCopyUnroll];
-  uint4 *d0[kCopyUnroll], *d1[kCopyUnroll];
+  const int pb16 = (int)c.pb16;
+  const int nk = (pb16 + kCopyChunk - 1) / kCopyChunk;      // chunks of K, and of V
+  const int tid = threadIdx.x;
+  if (x < 2 * nk) {
+    const bool v = x >= nk;
+    const int u0 = (v ? x - nk : x) * kCopyChunk + tid;
+    uint4* pool = reinterpret_cast<uint4*>(v ? c.v_pool : c.k_pool);
+    uint4* m = reinterpret_cast<uint4*>(v ? c.v_mir : c.k_mir);
+    const uint4* from = (pc.ss >= 0 ? pool + pc.ps * c.pb16 : m + pc.ls * c.pb16) + u0;
+    uint4 buf[kCopyUnroll];
+    if (pc.can) {
 #pragma unroll
-  for (int i = 0; i < kCopyUnroll; ++i) {
-    const long long u = (long long)x * kCopyChunk + i * kCopyThreads + threadIdx.x;
-    d0[i] = d1[i] = nullptr;
-    if (u < total) {
-      const uint4* from;
-      pc.unit(c, u, from, d0[i], d1[i]);
+      for (int i = 0; i < kCopyUnroll; ++i)
+        if (u0 + i * kCopyThreads < pb16) buf[i] = from[i * kCopyThreads];
+    }
+    if (!go() || !pc.can) return;
+    auto put = [&](uint4* to) {
+#pragma unroll
+      for (int i = 0; i < kCopyUnroll; ++i)
+        if (u0 + i * kCopyThreads < pb16) to[i * kCopyThreads] = buf[i];
+    };
+    if (pc.mir) put(m + pc.ld * c.pb16 + u0);
+    if (pc.sd >= 0) put(pool + pc.pd * c.pb16 + u0);
+    return;
+  }
+  uint4 buf[2];                            // HD <= 1024: at most 320 units of slab row
+  const int units = c.HD / 4 + c.HD / 16;
+  const uint4* from;
+  uint4 *to[2], *none;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    to[i] = nullptr;
+    if (tid + i * kCopyThreads < units) {
+      pc.unit(c, pc.kv16 + tid + i * kCopyThreads, from, to[i], none);
       buf[i] = *from;
     }
   }
   if (!go()) return;
-  if (!pc.can && x == 0 && threadIdx.x == 0) set_status(c.status, SSA_ST_UNRESOLVED);
+  if (!pc.can && tid == 0) set_status(c.status, SSA_ST_UNRESOLVED);
 #pragma unroll
-  for (int i = 0; i < kCopyUnroll; ++i) {
-    if (d0[i]) *d0[i] = buf[i];
-    if (d1[i]) *d1[i] = buf[i];
-  }
-  if (x == 0) pc.small(c, threadIdx.x, kCopyThreads);
+  for (int i = 0; i < 2; ++i)
+    if (to[i]) *to[i] = buf[i];
+  pc.small(c, tid, kCopyThreads);
 }
 
 // The slot a page holds becomes free (host tier: the mirror holds the page).
@@ -210,8 +234,8 @@ __global__ void copy_check_kernel(const int32_t* src, const int32_t* dst, int n,
 }
 
 // FUSED: a few pairs, each CTA looks for clashes itself while its loads are on
-// their way (1 pair of 2 layers 3.1 us, 4.1 with a launch that checks; 400 of
-// 12 layers 130 us against 118); else ok has the answer.
+// their way (1 pair of 2 layers: a microsecond less than with a launch that
+// checks; 400 of 12 layers: a tenth more); else ok has the answer.
 template <bool FUSED>
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const int32_t* src,
                                                                   const int32_t* dst, int n,
@@ -571,11 +595,11 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(CompactWs w,
     const int x = (int)(it - rest * chunks), r = (int)(rest / layers);
     const PageCopy<false, false> pc(c, (int)(rest - (long long)r * layers), w.from[r], w.to[r]);
     const int units = (int)pc.units(c);
-    uint4 buf[kCopyUnroll];
-    uint4* to[kCopyUnroll];
+    uint4 buf[kMoveUnroll];
+    uint4* to[kMoveUnroll];
 #pragma unroll
-    for (int i = 0; i < kCopyUnroll; ++i) {
-      const int u = (x * kCopyUnroll + i) * 32 + lane;
+    for (int i = 0; i < kMoveUnroll; ++i) {
+      const int u = (x * kMoveUnroll + i) * 32 + lane;
       to[i] = nullptr;
       if (u < units) {
         const uint4* from;
@@ -585,7 +609,7 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(CompactWs w,
       }
     }
 #pragma unroll
-    for (int i = 0; i < kCopyUnroll; ++i)
+    for (int i = 0; i < kMoveUnroll; ++i)
       if (to[i]) *to[i] = buf[i];
     if (x == 0) pc.small(c, lane, 32);
   }
@@ -645,9 +669,9 @@ PageCache page_cache(const Dims& d, const ssa_cache& c, int32_t* status) {
   return p;
 }
 
-unsigned page_chunks(const PageCache& c, bool kv) {
-  const long long total = (kv ? 2 * c.pb16 : 0) + c.HD / 4 + c.HD / 16;
-  return (unsigned)((total + kCopyChunk - 1) / kCopyChunk);
+// CTAs of copy_page for one page and layer.
+unsigned page_chunks(const PageCache& c) {
+  return (unsigned)(2 * ((c.pb16 + kCopyChunk - 1) / kCopyChunk) + 1);
 }
 
 Table table_of(const Dims& d, const ssa_requests& r) {
@@ -679,7 +703,7 @@ cudaError_t launch_copy_pages(const Dims& d, const ssa_cache& c, const int32_t* 
                               cudaStream_t s) {
   if (n == 0) return cudaSuccess;
   const PageCache pc = page_cache(d, c, status);
-  const dim3 grid(page_chunks(pc, true), n, d.Lyr);
+  const dim3 grid(page_chunks(pc), n, d.Lyr);
   cudaError_t e;
   if (n <= kFusedPairs) {
     e = launch_pdl(copy_pages_kernel<true>, grid, dim3(kCopyThreads), 0, s, src, dst, n,
@@ -723,7 +747,7 @@ cudaError_t launch_fork(const Dims& d, const ssa_cache& c, const ssa_requests& r
   count_launch();
   if (e != cudaSuccess) return e;
   // growth can be many pages of few rows: eight CTAs a row and layer at least
-  unsigned chunks = page_chunks(pc, true);
+  unsigned chunks = page_chunks(pc);
   if (new_lens && chunks < 8) chunks = 8;
   e = launch_pdl(fork_apply_kernel, dim3(chunks, d.B, d.Lyr + 1), dim3(kCopyThreads), 0, s, t, fw,
                  pc);
@@ -742,7 +766,7 @@ cudaError_t launch_compact(const Dims& d, const ssa_cache& c, const ssa_requests
   count_launch();
   if (e != cudaSuccess) return e;
   const long long per = (pc.mirror() ? 2 * pc.pb16 : 0) + pc.HD / 4 + pc.HD / 16;
-  constexpr int kWarpUnits = 32 * kCopyUnroll;
+  constexpr int kWarpUnits = 32 * kMoveUnroll;
   e = launch_pdl(compact_move_kernel, dim3(8 * num_sms), dim3(kCopyThreads), 0, s, cw, pc, d.Lyr,
                  (int)((per + kWarpUnits - 1) / kWarpUnits));
   count_launch();
