@@ -239,8 +239,9 @@ template <> struct Row<4> {
 // Stores a run of one head, whatever its tokens and values, with 128 / E
 // threads that have E dimensions each: a warp (E = 4), or four (E = 1; then
 // every thread of the CTA calls it, `active` those with a dimension, and s_max
-// [2][4] is their scratch).  row_of(r): the page's row of token r.  kin, vin: the thread's elements of the first
-// token, rows HD apart; k0, v0: their values.  sum: the slab's sums, updated.
+// [2][4] is their scratch).  row_of(r): the page's row of token r.  kin, vin:
+// the thread's elements of the first token, rows HD apart; k0, v0: their
+// values.  sum: the slab's sums, updated.
 template <bool I8, int P, int E, typename RowOf>
 __device__ __forceinline__ void store_run(const StorePHParams& p, const Block& blk, bool active,
                                           int d, const Row<E>* kin, const Row<E>* vin, Row<E> k0,
@@ -284,7 +285,7 @@ __device__ __forceinline__ void store_run(const StorePHParams& p, const Block& b
   }
   ak = warp_max(ak);
   av = warp_max(av);
-  if (E == 1) {
+  if constexpr (E == 1) {
     if (active && lane == 0) {
       s_max[0][warp] = ak;
       s_max[1][warp] = av;
@@ -295,6 +296,8 @@ __device__ __forceinline__ void store_run(const StorePHParams& p, const Block& b
       ak = fmaxf(ak, s_max[0][w]);
       av = fmaxf(av, s_max[1][w]);
     }
+  } else {
+    __syncwarp();                          // (every lane has read the old scales)
   }
   const float need_k = ak / kQmax, need_v = av / kQmax;
   const float sk = cnt0 > 0 ? fmaxf(old_k, need_k) : need_k;
