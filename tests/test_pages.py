@@ -1,5 +1,6 @@
 """Owners of the pages (copy; fork, grow and free; compaction) against a plain model of the definitions
 in include/ssa.h: every table, count, slot, slab row, pool and mirror byte equal after each call."""
+import collections
 import ctypes
 
 import numpy as np
@@ -124,7 +125,9 @@ class Model:
             refs[g] = max(left, 1)
         free = [p for p in range(self.Lp) if refs[p] <= 0]
         freed = [old_bt[i, p] for i, j in enumerate(par) if j != i for p in range(self.pages(old_len[i]))]
-        freed = [p for p in freed if p in set(free)]
+        free_now = set(free)
+        freed = [p for p in freed if p in free_now]
+        free = collections.deque(free)
         copies = []
         for i, j in enumerate(par):
             n = int(old_len[j]) if j >= 0 else 0
@@ -138,7 +141,7 @@ class Model:
             if not keep[i]:
                 g = row.pop()
                 if free:
-                    row.append(free.pop(0))
+                    row.append(free.popleft())
                     refs[row[-1]] = 1
                     copies.append((g, row[-1]))
                 else:
@@ -147,7 +150,7 @@ class Model:
                 if not free:
                     short = True
                     break
-                row.append(free.pop(0))
+                row.append(free.popleft())
                 refs[row[-1]] = 1
                 for n_ in self.SLAB:
                     self.a[n_][:, row[-1]] = 0
@@ -367,6 +370,34 @@ def test_fork_grow_free_and_compact_in_turn(ssa, kw, seed):
             assert bool((frm[len(src):] == -9).all())
             if pin is not None:
                 pin = dict(zip(src.tolist(), dst.tolist())).get(pin, pin)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", [
+    # more pages than the plan keeps bits of on chip, more new pages than its list holds there, and
+    # tables that take several blocks to count (pages without a slot: their copies are flagged)
+    dict(Lp=135000, B=60, nmax=2100, S=50, L=1, Hkv=1),
+    # more requests than a block has threads
+    dict(Lp=4000, B=1300, nmax=3, L=1, Hkv=1),
+], ids=["pages", "requests"])
+def test_large_tables(ssa, kw):
+    c, table, ws, status, rng = _setup(ssa, seed=9, **kw)
+    B, nmax, P = kw["B"], kw["nmax"], 16
+    m = Model(c, table)
+    everyone = np.arange(B, dtype=np.int32)
+    beams = rng.integers(0, B, B).astype(np.int32)
+    steps = [(np.where(rng.random(B) < 0.4, -1, everyone), None), "compact",
+             (everyone, rng.integers(0, nmax * P + 1, B)), (beams, None), "compact",
+             (np.where(rng.random(B) < 0.2, -1, beams), rng.integers(0, nmax * P + 1, B))]
+    for step in steps:
+        if step == "compact":
+            m.compact()
+            ssa.ssa_compact_pages(c, table, status, ws)
+        else:
+            parent, new = step
+            m.fork(parent, new)
+            ssa.ssa_fork_requests(c, table, _dev(parent), None if new is None else _dev(new), status, ws)
+        m.check(status)
 
 
 @pytest.mark.gpu
