@@ -266,6 +266,53 @@ def test_attention_over_pages_of_very_different_scale(fmt, heavy):
     _check_attention(lay, [ref], q, sel.cpu().numpy(), np.arange(n)[None], [n * P], out, fmt)
 
 
+def test_pool_beyond_4_gib():
+    """Store, attention and page copy at slots whose byte offsets pass 2^32 (two pools of 9.2 GB)."""
+    import sparse_attention_decode_indexer_gb300 as ssa
+    fmt, P, H, S, L = "int8_page_head", 64, 8, 70000, 2
+    lay = _layout(fmt, P=P, Hq=H, Hkv=H, L=L, Lp=S, S=S, B=1, nmax=4, k=3)
+    c, status = _cache(lay)
+    ws = torch.zeros((ssa.ssa_workspace_size(lay),), dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(2)
+    ids = np.array([3, S - 9, S - 2, S - 1])
+    T = 3 * P + 9
+    order = np.concatenate([i * P + np.arange(P) for i in ids])[:T]
+    for step in (300, 0):                         # enough tokens for the whole-page kernel, or not
+        k, kf = _bf16(rng, L, T + step, H, D)
+        v, vf = _bf16(rng, L, T + step, H, D)
+        pos = np.concatenate([order[:P], 10 * P + np.arange(step), order[P:]])
+        c.slab_cnt.zero_()
+        c.slab_sum.zero_()
+        ssa.ssa_store_kv_mirror(c, 0, L, k.cuda(), v.cuda(), torch.from_numpy(pos).cuda(), status)
+        keep = np.concatenate([np.arange(P), P + step + np.arange(T - P)])
+        refs = []
+        for l in range(L):
+            ref = RefPages(fmt, 4, H, P)
+            ref.store(kf[l][keep], vf[l][keep], np.arange(T))
+            refs.append(ref)
+            got = [getattr(c, n)[l, torch.from_numpy(ids).cuda()].cpu().numpy()
+                   for n in ("k_pool", "v_pool", "k_scale", "v_scale")]
+            got[0] = got[0].reshape(4, H, P, D)
+            got[1] = got[1].reshape(4, H, D, P).transpose(0, 1, 3, 2)
+            _same_pages(ref, got, np.arange(4), np.arange(4))
+    sel = torch.full((L, 1, lay.max_sel), -1, dtype=torch.int32, device="cuda")
+    phys = sel.clone()
+    sel[..., :4] = torch.arange(4)
+    phys[..., :4] = torch.from_numpy(ids.astype(np.int32))
+    q, _ = _bf16(rng, L, 1, H, D)
+    out = torch.empty((L, 1, H, D), dtype=torch.bfloat16, device="cuda")
+    lens = torch.tensor([T], dtype=torch.int32, device="cuda")
+    ssa.ssa_sparse_paged_decode(c, 0, L, q.cuda(), sel, phys, lens, sm_scale(), out, status, ws)
+    _check_attention(lay, refs, q, sel.cpu().numpy(), np.arange(4)[None], [T], out, fmt)
+    ssa.ssa_copy_pages(c, torch.tensor([S - 1, 3], dtype=torch.int32, device="cuda"),
+                       torch.tensor([7, S - 5], dtype=torch.int32, device="cuda"), status, ws)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    for n in ("k_pool", "v_pool", "k_scale", "v_scale", "slab", "slab_sum", "slab_cnt"):
+        t = getattr(c, n)
+        assert torch.equal(t[:, 7], t[:, S - 1]) and torch.equal(t[:, S - 5], t[:, 3]), n
+
+
 def test_captured_store_and_attention_replay():
     """A store and an attention captured on a stream of their own: the replay stores what k, v and pos
     hold then, into pages that were cleared, and attends over it."""
