@@ -163,8 +163,9 @@ typedef struct ssa_cache {
 } ssa_cache;
 
 /* Bytes of scratch (device memory, 256-byte aligned) that ssa_index_topk,
- * ssa_ensure_resident and ssa_sparse_paged_decode need for any layer range
- * of this layout.  The calls use disjoint parts of it.  Zero the workspace
+ * ssa_ensure_resident, ssa_sparse_paged_decode and the page calls need for any
+ * layer range of this layout.  The calls use disjoint parts of it (the page
+ * calls one part together).  Zero the workspace
  * once before its first use: ssa_sparse_paged_decode keeps per-unit split
  * counters in it, and every call that completes leaves them zero again (a
  * call that reported SSA_ST_TIMEOUT may not: zero the workspace again).
@@ -422,7 +423,8 @@ int ssa_remap_block_table(const ssa_layout *lay, const ssa_cache *c, int layer0,
  * remapped table).  For request b and query head hq (KV head h = hq / G):
  *   out[b][hq] = sum_t softmax_t(sm_scale * q[b][hq] . K[t]) V[t]
  * over tokens t = p*P + j of the pages p = sel[b][i] with phys[b][i] >= 0
- * and t < seq_lens[b]; K[t] = code * k_scale[t] for fp8 (V likewise).
+ * and t < seq_lens[b]; K[t] = code * k_scale[t] for fp8, code *
+ * k_scale[slot][h] for the PAGE_HEAD formats (V likewise).
  * Entries with sel < 0 are padding; sel >= 0 with phys < 0 are skipped and
  * flagged SSA_ST_UNRESOLVED.  A request with no token gets zeros.
  *   q    [n_layers][B][Hq][D] bf16;  out [n_layers][B][Hq][D] bf16
