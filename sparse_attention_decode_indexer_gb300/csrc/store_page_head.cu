@@ -46,6 +46,7 @@ namespace {
 constexpr int kHD = 128;                 // head_dim
 constexpr int kMaxP = 128;
 constexpr int kRowUnits = kHD * 2 / 16;  // 16-byte units of a bf16 token row
+constexpr int kMaxPiece = 128;           // tokens whose runs one CTA of the append kernel stores
 constexpr int kTokBatch = 4;             // tokens of a run in flight, for their maxima
 
 struct StorePHParams {
@@ -425,52 +426,59 @@ __global__ void __launch_bounds__(256) append_page_head_kernel(
   __shared__ int s_row[P];
   __shared__ int s_run;
   __shared__ float s_head[8];
+  __shared__ uint32_t s_starts[kMaxPiece / 32];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, h = tid >> 5;
   const int Hkv = p.Hkv, HD = Hkv * kHD, d = 4 * lane;
   const int li = blockIdx.y, layer = p.layer0 + li;
-  // the piece's positions, a lane each (every warp finds the same runs), in one
-  // round trip with the first token's K and V
+  // the runs that start in the piece: a lane per token, MANY: 32 of them per
+  // warp; alone, in one round trip with the token's K and V
   const int chunk = MANY ? p.chunk : 1;
   const int first = blockIdx.x * chunk, end = min(first + chunk, p.T);
-#pragma unroll 1
-  for (int c0 = first; c0 < end; c0 += 32) {
-    const int t_mine = c0 + lane;
-    bool start = false;
-    int64_t pos_mine = -1;
-    if (t_mine < end) {
-      pos_mine = p.pos[t_mine];
-      const int64_t prev = t_mine > 0 ? p.pos[t_mine - 1] : -1;
-      start = pos_mine >= 0 && pos_mine / P < p.Lp;
-      if (!start && h == 0) set_status(p.status, SSA_ST_BAD_ID);
-      if (t_mine > 0) {
-        if (start && h == 0 && prev >= pos_mine) set_status(p.status, SSA_ST_BAD_POS);
-        if (prev >= 0 && prev / P == pos_mine / P) start = false;    // inside a run
-      }
-      if (MANY && p.whole && start && whole_page<P>(p, t_mine, pos_mine)) start = false;
+  auto run_starts = [&](int t) -> bool {
+    if (t >= end) return false;
+    const int64_t x = p.pos[t], prev = t > 0 ? p.pos[t - 1] : -1;
+    if (x < 0 || x / P >= p.Lp) {
+      set_status(p.status, SSA_ST_BAD_ID);
+      return false;
     }
-    const size_t in_c = (((size_t)li * p.T + c0) * HD + h * kHD + d) / 4;
-    const Row<4>* kin = reinterpret_cast<const Row<4>*>(p.k) + in_c;
-    const Row<4>* vin = reinterpret_cast<const Row<4>*>(p.v) + in_c;
-    Row<4> k0, v0;
-    if (!MANY) {
-      k0 = *kin;
-      v0 = *vin;
+    if (t > 0) {
+      if (prev >= x) set_status(p.status, SSA_ST_BAD_POS);
+      if (prev >= 0 && prev / P == x / P) return false;              // inside a run
     }
-    int at = 0;                              // the token that kin and vin are of
+    return !(MANY && p.whole && whole_page<P>(p, t, x));
+  };
+  int words = 1;
+  uint32_t runs = 0;
+  Row<4> k0, v0;
+  if (MANY) {
+    words = (chunk + 31) / 32;
+    for (int w = h; w < words; w += Hkv) {
+      const uint32_t m = __ballot_sync(0xffffffffu, run_starts(first + 32 * w + lane));
+      if (lane == 0) s_starts[w] = m;
+    }
+    __syncthreads();
+  } else {
+    const size_t in_c = (((size_t)li * p.T + first) * HD + h * kHD + d) / 4;
+    k0 = reinterpret_cast<const Row<4>*>(p.k)[in_c];
+    v0 = reinterpret_cast<const Row<4>*>(p.v)[in_c];
+    runs = run_starts(first) ? 1u : 0u;    // (the same in every thread)
+  }
 #pragma unroll 1
-    for (uint32_t runs = __ballot_sync(0xffffffffu, start); runs; runs &= runs - 1) {
-      const int next = __ffs(runs) - 1;
+  for (int w = 0; w < words; ++w) {
+    if (MANY) runs = s_starts[w];
+#pragma unroll 1
+    for (; runs; runs &= runs - 1) {
+      const int t0 = first + 32 * w + __ffs(runs) - 1;
+      const size_t in_c = (((size_t)li * p.T + t0) * HD + h * kHD + d) / 4;
+      const Row<4>* kin = reinterpret_cast<const Row<4>*>(p.k) + in_c;
+      const Row<4>* vin = reinterpret_cast<const Row<4>*>(p.v) + in_c;
       if (MANY) {
-        kin += (size_t)(next - at) * (HD / 4);
-        vin += (size_t)(next - at) * (HD / 4);
         k0 = *kin;
         v0 = *vin;
-        at = next;
       }
-      const int t0 = c0 + at;
-      const int pg = (int)(__shfl_sync(0xffffffffu, pos_mine, at) / P);
+      const int pg = (int)(p.pos[t0] / P);
       const size_t lp = (size_t)layer * p.Lp + pg;
       const size_t so = lp * HD + h * kHD + d;
       const float4 old_sum = *reinterpret_cast<const float4*>(p.slab_sum + so);
@@ -799,7 +807,7 @@ cudaError_t launch_t(StorePHParams p, int n_layers, cudaStream_t s) {
     return e;
   }
   // pieces: single tokens of many requests want many CTAs, a prefill few
-  p.chunk = p.T < 1024 ? 4 : (P == 16 ? 16 : (p.T < 4096 ? 8 : 64));
+  p.chunk = p.T < 1024 ? 4 : (P == 16 ? 16 : (p.T < 4096 ? 8 : kMaxPiece));
   p.whole = P > 16;
   e = launch_pdl(append_page_head_kernel<I8, P, true>,
                  dim3((unsigned)((p.T + (long long)p.chunk - 1) / p.chunk), (unsigned)n_layers),
