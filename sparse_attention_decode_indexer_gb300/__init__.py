@@ -194,8 +194,9 @@ class Layout:
     """Shapes of a cache and its calls.  ``kv_format`` names the KV format:
     "bf16", "fp8" (e4m3, one scale per token), "e4m3_page_head" or
     "int8_page_head" (8-bit codes, one K and one V scale per page and KV
-    head); None takes bf16 or fp8 by ``fp8``.  ``fp8`` ends up saying whether
-    the codes are 8 bits wide (V d-major in the pool, with scales)."""
+    head); None takes bf16 or fp8 by ``fp8``.  Where it is given, ``fp8`` ends
+    up saying whether the codes are 8 bits wide (V d-major in the pool, with
+    scales)."""
     page_size: int
     n_q_heads: int
     n_kv_heads: int
@@ -210,8 +211,8 @@ class Layout:
     kv_format: str | None = None
 
     def __post_init__(self):
-        if self.kv_format is None:
-            self.kv_format = "fp8" if self.fp8 else "bf16"
+        if self.kv_format is None:        # stays so: a copy with another fp8 takes that one's
+            return
         if self.kv_format not in KV_FORMATS:
             raise ValueError(f"kv_format {self.kv_format!r}: one of {sorted(KV_FORMATS)}")
         self.fp8 = self.kv_format != "bf16"
@@ -219,7 +220,7 @@ class Layout:
     @property
     def scale_floats(self) -> int:
         """fp32 K scales (and as many V scales) of one page."""
-        if self.kv_format.endswith("_page_head"):
+        if self.kv_format in ("e4m3_page_head", "int8_page_head"):
             return self.n_kv_heads
         return self.page_size if self.fp8 else 0
 
@@ -229,7 +230,8 @@ class Layout:
 
     def c(self) -> SsaLayout:
         return SsaLayout(self.page_size, self.n_q_heads, self.n_kv_heads, self.head_dim,
-                         KV_FORMATS[self.kv_format], self.n_layers,
+                         KV_FORMATS[self.kv_format or ("fp8" if self.fp8 else "bf16")],
+                         self.n_layers,
                          self.logical_pages, self.pool_slots, self.batch, self.max_pages,
                          self.block_topk, self.max_sel)
 
