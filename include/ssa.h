@@ -564,7 +564,8 @@ int ssa_compact_pages(const ssa_layout *lay, const ssa_cache *c, const ssa_reque
  *   q, k      at most one NULL: heads, and element strides of layer, token and
  *             head (elements of a head are contiguous), so that a slice of a
  *             fused projection needs no copy.  out == in (same strides) rotates
- *             in place; otherwise the two must not overlap.
+ *             in place; otherwise the two must not overlap.  What one of q
+ *             and k writes must not overlap what the other reads or writes.
  * 16-byte accesses where pointers, strides and dimensions allow, single
  * elements otherwise; same values either way.
  */

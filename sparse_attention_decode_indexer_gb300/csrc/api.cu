@@ -591,6 +591,9 @@ int ssa_rope(int dtype, int head_dim, int rotary_dim, int interleaved, int inver
     }
   }
   if (n_tokens == 0) return SSA_OK;
+  // both would turn, or write, the same elements, in no order
+  if (q && k && (q->out == k->out || q->out == k->in || k->out == q->in))
+    return SSA_ERR_INVALID_ARG;
   a.dtype = dtype;
   a.D = head_dim;
   a.rd = rotary_dim;

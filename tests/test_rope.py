@@ -100,6 +100,14 @@ def test_refusals(ssa):
             ssa.ssa_rope(plan, *a, **kw)
 
 
+def test_q_and_k_on_the_same_elements_are_refused(ssa):
+    P = 0x10000
+    t = lambda i, o: ctypes.byref(ssa.SsaRopeTensor(  # noqa: E731
+        i * P, o * P, 2, (ctypes.c_int64 * 3)(0, 256, 128), (ctypes.c_int64 * 3)(0, 256, 128)))
+    for q, k in (((1, 1), (1, 1)), ((1, 2), (3, 2)), ((1, 2), (2, 3)), ((3, 2), (4, 3))):
+        assert ssa.lib().ssa_rope(0, 128, 128, 0, 0, P, 1.0, 1, 4, P, 0, 0, t(*q), t(*k), None) == -1
+
+
 def _exact(x, pos, theta, m, rd, inter, inverse):
     ang = pos.double()[:, None] * torch.tensor(theta, dtype=torch.float64)
     c, s = m * ang.cos()[:, None], m * ang.sin()[:, None]
