@@ -446,8 +446,8 @@ def _ints(name, t, n, device: int):
 class RequestTable:
     """The requests' pages: block_table [B][max_pages], seq_lens [B] and the
     references of every logical page, ref [logical_pages], all int32 on the
-    device.  int32 tensors already there are taken as they are, so that a
-    runner's tables change in place.  Without ``ref`` the rows are counted
+    device.  Contiguous int32 tensors already there are taken as they are, so
+    that a runner's tables change in place.  Without ``ref`` the rows are counted
     (ssa_page_refs); add to ref[p] to pin page p."""
 
     def __init__(self, layout: Layout, block_table, seq_lens, ref=None, device="cuda"):

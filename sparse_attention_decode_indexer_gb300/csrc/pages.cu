@@ -42,6 +42,9 @@ constexpr int kMoveUnroll = 4;                             // compaction: units 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWords = 4096;         // words of page bits kept in shared memory
 constexpr int kPlanList = 1024;          // new pages kept there
+// most dynamic shared memory of a fork's plan: batch * max_sel <= 16384 and
+// max_sel >= 10 leave 1638 rows, of seven words each
+constexpr size_t kForkSmem = (7 * 1638 + kPlanWords) * sizeof(int32_t);
 
 // The cache as the page calls see it.
 struct PageCache {
@@ -736,12 +739,11 @@ cudaError_t launch_fork(const Dims& d, const ssa_cache& c, const ssa_requests& r
   if (ctas > 2 * num_sms) ctas = 2 * num_sms;
   const int words = (d.Lp + 31) / 32;
   const size_t smem = ((size_t)7 * d.B + (words <= kPlanWords ? words : 0)) * sizeof(int32_t);
-  cudaError_t e;
-  if (smem + 8192 > 48 * 1024) {
-    e = cudaFuncSetAttribute(fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  if (smem > kForkSmem) return cudaErrorInvalidValue;
+  // every call sets the same limit, so none lowers another's before its launch
+  cudaError_t e = cudaFuncSetAttribute(
+      fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kForkSmem);
+  if (e != cudaSuccess) return e;
   e = launch_pdl(fork_plan_kernel, dim3((unsigned)ctas), dim3(kPlanThreads), smem, s, t, parent,
                  new_lens, fw, pc);
   count_launch();

@@ -132,8 +132,11 @@ class DecodeRunner:
     @property
     def table(self) -> RequestTable:
         """The runner's block table and lengths with the pages' reference
-        counts, counted on first use."""
+        counts, counted on first use (outside a capture: a replay would count
+        anew and forget pins)."""
         if not hasattr(self, "_table"):
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("use the runner's table once before a capture")
             self._table = RequestTable(self.layout, self.block_table, self.seq_lens,
                                        device=self.block_table.device)
         return self._table

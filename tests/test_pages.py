@@ -563,6 +563,29 @@ def test_forked_requests_decode_alike(ssa, fmt, host):
     assert int(run.status.item()) == 0
 
 
+@pytest.mark.gpu
+def test_a_runner_counts_its_table_outside_captures(ssa):
+    from sparse_attention_decode_indexer_gb300.runner import DecodeRunner
+    lay = ssa.Layout(16, 2, 2, 128, False, 1, 8, 8, 2, 3, 1)
+    bt = torch.tensor([[0, 1, -1], [2, -1, -1]])
+    run = DecodeRunner(lay, host_tier=False, identity=True, block_table=bt, seq_lens=torch.tensor([20, 16]))
+    parent, x = torch.tensor([1, 1], dtype=torch.int32, device="cuda"), torch.zeros(4, device="cuda")
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        x.add_(1)
+        with pytest.raises(RuntimeError):
+            run.fork(parent)
+    assert run.table.ref.tolist() == [1, 1, 1, 0, 0, 0, 0, 0]
+    run.table.ref[0] += 1
+    run.fork(torch.arange(2, dtype=torch.int32, device="cuda"))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run.fork(parent)
+    g.replay()
+    g.replay()
+    assert run.table.ref.tolist() == [1, 0, 2, 0, 0, 0, 0, 0]
+    assert run.block_table.tolist() == [[2, -1, -1], [2, -1, -1]] and int(run.status.item()) == 0
+
+
 def test_refusals(ssa):
     """On the host, before anything is enqueued."""
     lib, p, INVALID, UNSUPPORTED = ssa.lib(), 0x10000, -1, -3
