@@ -46,7 +46,7 @@ namespace {
 constexpr int kHD = 128;                 // head_dim
 constexpr int kMaxP = 128;
 constexpr int kRowUnits = kHD * 2 / 16;  // 16-byte units of a bf16 token row
-constexpr int kMaxPiece = 128;           // tokens whose runs one CTA of the append kernel stores
+constexpr int kMaxPiece = 128;           // most tokens whose runs one CTA of the append kernel stores
 constexpr int kTokBatch = 4;             // tokens of a run in flight, for their maxima
 
 struct StorePHParams {
@@ -417,11 +417,12 @@ __device__ __forceinline__ bool whole_page(const StorePHParams& p, int t, int64_
 }
 
 // Runs of any kind, but for whole pages where the other kernel stores those
-// (p.whole).  A warp per KV head, four dimensions a lane; grid (pieces of
-// p.chunk tokens, 1 or, MANY, more, layers): a CTA stores the runs that start
-// in its piece.
+// (p.whole).  A warp per KV head, four dimensions a lane; grid (CTAs, layers):
+// a CTA stores the runs that start at its tokens, one or, MANY, up to p.chunk,
+// as far apart as there are CTAs, so that a few single tokens behind a prefill
+// are not left to a few CTAs.
 template <bool I8, int P, bool MANY>
-__global__ void __launch_bounds__(256) append_page_head_kernel(
+__global__ void __launch_bounds__(256, MANY ? 3 : 0) append_page_head_kernel(
     const __grid_constant__ StorePHParams p) {
   __shared__ int s_row[P];
   __shared__ int s_run;
@@ -432,12 +433,13 @@ __global__ void __launch_bounds__(256) append_page_head_kernel(
   const int tid = threadIdx.x, lane = tid & 31, h = tid >> 5;
   const int Hkv = p.Hkv, HD = Hkv * kHD, d = 4 * lane;
   const int li = blockIdx.y, layer = p.layer0 + li;
-  // the runs that start in the piece: a lane per token, MANY: 32 of them per
+  // the runs that start at its tokens: a lane per token, MANY: 32 of them per
   // warp; alone, in one round trip with the token's K and V
-  const int chunk = MANY ? p.chunk : 1;
-  const int first = blockIdx.x * chunk, end = min(first + chunk, p.T);
-  auto run_starts = [&](int t) -> bool {
-    if (t >= end) return false;
+  const int first = blockIdx.x, step = gridDim.x;
+  auto run_starts = [&](int i) -> bool {
+    const long long at = first + (long long)i * step;
+    if (at >= p.T) return false;
+    const int t = (int)at;
     const int64_t x = p.pos[t], prev = t > 0 ? p.pos[t - 1] : -1;
     if (x < 0 || x / P >= p.Lp) {
       set_status(p.status, SSA_ST_BAD_ID);
@@ -453,9 +455,9 @@ __global__ void __launch_bounds__(256) append_page_head_kernel(
   uint32_t runs = 0;
   Row<4> k0, v0;
   if (MANY) {
-    words = (chunk + 31) / 32;
+    words = (p.chunk + 31) / 32;
     for (int w = h; w < words; w += Hkv) {
-      const uint32_t m = __ballot_sync(0xffffffffu, run_starts(first + 32 * w + lane));
+      const uint32_t m = __ballot_sync(0xffffffffu, run_starts(32 * w + lane));
       if (lane == 0) s_starts[w] = m;
     }
     __syncthreads();
@@ -463,14 +465,14 @@ __global__ void __launch_bounds__(256) append_page_head_kernel(
     const size_t in_c = (((size_t)li * p.T + first) * HD + h * kHD + d) / 4;
     k0 = reinterpret_cast<const Row<4>*>(p.k)[in_c];
     v0 = reinterpret_cast<const Row<4>*>(p.v)[in_c];
-    runs = run_starts(first) ? 1u : 0u;    // (the same in every thread)
+    runs = run_starts(0) ? 1u : 0u;    // (the same in every thread)
   }
 #pragma unroll 1
   for (int w = 0; w < words; ++w) {
     if (MANY) runs = s_starts[w];
 #pragma unroll 1
     for (; runs; runs &= runs - 1) {
-      const int t0 = first + 32 * w + __ffs(runs) - 1;
+      const int t0 = first + (32 * w + __ffs(runs) - 1) * step;
       const size_t in_c = (((size_t)li * p.T + t0) * HD + h * kHD + d) / 4;
       const Row<4>* kin = reinterpret_cast<const Row<4>*>(p.k) + in_c;
       const Row<4>* vin = reinterpret_cast<const Row<4>*>(p.v) + in_c;
@@ -768,6 +770,12 @@ store_page_head_kernel(const __grid_constant__ StorePHParams p) {
 // pages to the other kernel.  (Pages of 16 tokens are one step of a warp, and
 // stay there.)
 constexpr int kWholeTokens = 256;
+// CTAs of the append kernel in such a call: single tokens want many, but a
+// prefill's find nothing to do at 1 us a thousand.  (12 layers: 4,096 tokens of
+// whole pages, then 256 single ones behind them and 1,000 single ones alone:
+// 1,024 CTAs 36.6, 72.7 and 144 us, 2,048 37.3, 66.6 and 118 us, 8,192 43.2,
+// 64.0 and 112 us.)
+constexpr int kAppendCtas = 2048;
 
 template <bool I8, int P, bool MIR>
 cudaError_t launch_m(const StorePHParams& p, int n_layers, cudaStream_t s) {
@@ -806,12 +814,16 @@ cudaError_t launch_t(StorePHParams p, int n_layers, cudaStream_t s) {
     count_launch();
     return e;
   }
-  // pieces: single tokens of many requests want many CTAs, a prefill few
-  p.chunk = p.T < 1024 ? 4 : (P == 16 ? 16 : (p.T < 4096 ? 8 : kMaxPiece));
+  // (pages of 16: a prefill's CTAs store every page; 32,768 tokens of 3 layers
+  // and 2 heads 74.0 us with one times as many, 60.8 with four, 72.9 with 16)
+  constexpr int kCtas = P == 16 ? 4 * kAppendCtas : kAppendCtas;
+  const long long per = ((long long)p.T * n_layers + kCtas - 1) / kCtas;
+  p.chunk = per < 4 ? 4 : (per > kMaxPiece ? kMaxPiece : (int)per);
+  // odd, so that runs that start 16 or 32 tokens apart reach all CTAs
+  const unsigned ctas = (unsigned)(((long long)p.T + p.chunk - 1) / p.chunk) | 1u;
   p.whole = P > 16;
   e = launch_pdl(append_page_head_kernel<I8, P, true>,
-                 dim3((unsigned)((p.T + (long long)p.chunk - 1) / p.chunk), (unsigned)n_layers),
-                 block, 0, s, p);
+                 dim3(ctas, (unsigned)n_layers), block, 0, s, p);
   count_launch();
   if (e != cudaSuccess) return e;
   if constexpr (P > 16)

@@ -151,6 +151,31 @@ def test_store_of_short_and_long_runs_in_one_call(fmt, P, H, T):
     _same_slab(ref, c, 0)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("P", [16, 32])
+def test_store_of_a_prefill_and_single_tokens_in_many_layers(fmt, P):
+    """Whole pages, single tokens of other requests behind them and a run of a page and a half, in so
+    many layers that one CTA looks after more than 32 tokens."""
+    import sparse_attention_decode_indexer_gb300 as ssa
+    L, whole, single = 36, 2560 // P, 900
+    Lp = whole + single + 2
+    lay = _layout(fmt, P=P, Hq=1, Hkv=1, L=L, Lp=Lp, B=1, nmax=Lp, k=1)
+    c, status = _cache(lay)
+    rng = np.random.default_rng(P)
+    ones = (whole + np.arange(single)) * P + rng.integers(0, P, single)
+    pos = np.concatenate([np.arange(whole * P), ones, np.arange((Lp - 2) * P, (Lp - 2) * P + P + P // 2)])
+    assert len(pos) * L > 2048 * 48
+    k, kf = _bf16(rng, L, len(pos), 1, D)
+    v, vf = _bf16(rng, L, len(pos), 1, D)
+    ssa.ssa_store_kv_mirror(c, 0, L, k.cuda(), v.cuda(), torch.from_numpy(pos).cuda(), status)
+    assert int(status.item()) == 0
+    for l in (0, 17, L - 1):
+        ref = RefPages(fmt, Lp, 1, P)
+        ref.store(kf[l], vf[l], pos)
+        _same_pages(ref, _pages(c, l), np.arange(Lp), c.slot_of[l].cpu().numpy())
+        _same_slab(ref, c, l)
+
+
 def test_store_flags_bad_positions():
     import sparse_attention_decode_indexer_gb300 as ssa
     lay = _layout("int8_page_head", P=16, Hq=1, Hkv=1, L=1, Lp=3, B=1, nmax=3, k=1)
