@@ -64,8 +64,9 @@
 //     warps) run the same online recurrence in piece order, so the output
 //     does not depend on which piece finishes last.
 //   * page_head formats: one K and one V scale per (page, KV head), read by
-//     the producer's two 4-byte asynchronous copies per page into the stage's
-//     descriptor, so the score takes one factor per page.  e4m3 codes run the
+//     the producer's two 4-byte asynchronous copies per page beside the stage's
+//     descriptor, so the score takes one factor per page.  Pages of 16 and 32
+//     tokens share stages of 64.  e4m3 codes run the
 //     fp8 path above; int8 codes become f16 exactly (a byte permute into
 //     1024 + code + 128 and one subtraction per pair), QK and PV as m16n8k16
 //     f16 MMAs against q * 2^e in f16 (no hi/lo split: half the QK MMAs);
@@ -113,7 +114,9 @@ constexpr int kLast = 2;    // last page of a piece: flush after it
 constexpr int kEmpty = 4;   // a piece without pages (no data in the stage)
 constexpr int kDone = 8;    // end of the CTA's range
 constexpr int kFinal = 16;  // with kLast / kEmpty: the CTA's last piece
-constexpr int kWriteBack = 32;  // fetch mode: the stage's page goes to its slot too
+constexpr int kWriteBack = 32;  // fetch mode: the stage's page goes to its slot too (pages
+                                // that share a stage: shifted by the page's place in it)
+constexpr int kCountShift = 12; // the stage's number of pages, where it can be several
 
 __host__ __device__ constexpr int round_up(int x, int a) { return (x + a - 1) / a * a; }
 
@@ -127,17 +130,23 @@ __host__ __device__ constexpr bool is_page_head(int kind) {
 template <int KIND, int P>
 struct Cfg {
   static constexpr int kTileBytes = P * kD * (is_8bit(KIND) ? 1 : 2);   // one KV head of one page
+  // pages of a stage: page_head pages below 64 tokens share one, since a stage
+  // costs the producer and every consumer warp a wait, a descriptor and an
+  // arrival whatever it holds, and a lane per page issues them side by side.
+  // (288 rows of 8 KV heads, 48 pages each: pages of 16 164 -> 96 us, of 32
+  // 207 -> 166 us; of 16 with the producer's lane 0 issuing each, 163 us.)
+  static constexpr int kPages = is_page_head(KIND) && P < 64 ? 64 / P : 1;
   // per-token scales travel in the stage; the two page_head scales beside the
   // descriptors, which leaves the stage at 18 KB for 64-token pages instead of
   // 19 and so room for a fifth one
   static constexpr int kScaleBytes = KIND == SSA_KV_FP8_E4M3 ? 2 * P * 4 : 0;
-  static constexpr int kPairBytes = is_page_head(KIND) ? 8 : 0;
-  static constexpr int kQOff = 2 * kTileBytes + kScaleBytes;
+  static constexpr int kPairBytes = is_page_head(KIND) ? 8 * kPages : 0;
+  static constexpr int kQOff = kPages * 2 * kTileBytes + kScaleBytes;
   static constexpr int kQBytes = kMaxG * kD * 2;
   static constexpr int kStageBytes = round_up(kQOff + kQBytes, 1024);
   static constexpr int kCombineBytes = kConsumerWarps * kMaxG * kD * 4 + 2 * kConsumerWarps * kMaxG * 4;
   // alignment slack, combine area, producer window, descriptors and barriers
-  static constexpr int kFixed = 1024 + kCombineBytes + kWindow * 12 + kMaxStages * (36 + kPairBytes) + 64;
+  static constexpr int kFixed = 1024 + kCombineBytes + kWindow * 12 + kMaxStages * (32 + 4 * kPages + kPairBytes) + 64;
   // two CTAs per SM when at least two stages fit beside the second CTA
   static constexpr int kStages2 = (kSmemPerSm / 2 - kSmemReservedPerCta - kFixed) / kStageBytes;
   static constexpr int kCtasPerSm = kStages2 >= 2 ? 2 : 1;
@@ -262,7 +271,7 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
   constexpr bool PH = is_page_head(KIND);    // one K and one V scale per page and KV head
   constexpr bool I8 = KIND == SSA_KV_INT8_PAGE_HEAD;
   using C = Cfg<KIND, P>;
-  constexpr int NST = C::kStages;
+  constexpr int NST = C::kStages, NPG = C::kPages;
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte aligned (the TMA swizzle atom) by pointer arithmetic on the
   // shared array itself, so that every access below stays a shared-memory
@@ -273,13 +282,13 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
   int2* plist = reinterpret_cast<int2*>(smem + NST * C::kStageBytes + C::kCombineBytes);
   int* pid = reinterpret_cast<int*>(plist + kWindow);                      // [kWindow] ids
   int4* meta = reinterpret_cast<int4*>(pid + kWindow);                     // [NST]
-  float2* psc = reinterpret_cast<float2*>(meta + NST);     // page_head: [NST] (K, V) scales
-  uint64_t* full = reinterpret_cast<uint64_t*>(meta + NST) + (PH ? NST : 0);
+  float2* psc = reinterpret_cast<float2*>(meta + NST);     // page_head: [NST][NPG] (K, V) scales
+  uint64_t* full = reinterpret_cast<uint64_t*>(meta + NST) + (PH ? NST * NPG : 0);
   uint64_t* empty = full + NST;
   uint64_t* cfull = empty + NST;           // the consumers' states are in comb
   uint64_t* cfree = cfull + 1;             // the merge warp is done reading comb
   uint64_t* cbar = cfree + 1;              // the consumer warps' barrier (last piece)
-  int* wslot = reinterpret_cast<int*>(cbar + 1);                         // [NST] fetch mode
+  int* wslot = reinterpret_cast<int*>(cbar + 1);                         // [NST][NPG] fetch mode
   __shared__ int s_abort;
   __shared__ int s_last;
 
@@ -466,17 +475,23 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
     // logical id mid) by 16-byte cp.async copies from the pinned mirror, every
     // lane a share, into the same swizzled stage layout, and in fetch mode
     // marked for the consumers to write into the slot.  The whole warp in
-    // the host-tail and fetch modes, lane 0 alone in the resident mode.
+    // the host-tail and fetch modes, lane 0 alone in the resident mode.  The
+    // page is the `sub`-th of its stage, `end`: the last.
+    int stage_flags = 0, stage_valid = 0;    // of the stage's pages so far
     auto issue_page = [&](int2 ent, int mid, int flags, int unit, int h, int layer,
-                          int seq_len) -> bool {
-      if (!(WARP_ISSUE ? acquire_warp() : acquire(st))) return false;
-      const int sb = st % NST;
-      uint8_t* stage = ring + sb * C::kStageBytes;
+                          int seq_len, int sub, bool end) -> bool {
+      if (sub == 0) {
+        if (!(WARP_ISSUE ? acquire_warp() : acquire(st))) return false;
+        stage_flags = stage_valid = 0;
+      }
+      const int sb = st % NST, ps = sb * NPG + sub;
+      uint8_t* const first_page = ring + sb * C::kStageBytes;
+      uint8_t* const stage = first_page + sub * 2 * C::kTileBytes;
       const uint32_t qbytes = (flags & kFirst) ? (uint32_t)p.G * kD * 2 : 0u;
       const bool host = WARP_ISSUE && ent.y < 0;
       if (FT && host) {
-        flags |= kWriteBack;
-        if (lane == 0) wslot[sb] = -2 - ent.y;
+        flags |= kWriteBack << sub;
+        if (lane == 0) wslot[ps] = -2 - ent.y;
       }
       if constexpr (WARP_ISSUE) if (host) {
         const size_t id = (size_t)(FT ? mid : -2 - ent.y);
@@ -499,7 +514,7 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
           }
           if (PH) {
             const size_t so = ((size_t)layer * p.Lp + id) * p.Hkv + h;
-            if (lane < 2) cp_async4(smem_u32(&psc[sb]) + 4 * lane, (lane ? p.vs_mir : p.ks_mir) + so);
+            if (lane < 2) cp_async4(smem_u32(&psc[ps]) + 4 * lane, (lane ? p.vs_mir : p.ks_mir) + so);
           } else {
             const size_t so = ((size_t)layer * p.Lp + id) * P;
             for (int i = lane; i < 2 * (P / 4); i += 32) {
@@ -522,15 +537,22 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
       }
       if (lane == 0) {
         const int nvalid = max(0, min(P, seq_len - ent.x * P));
-        meta[sb] = make_int4(flags, nvalid, unit, st);
+        stage_flags |= flags;
+        stage_valid |= nvalid << (8 * sub);
+        if (end) {
+          if (NPG > 1) stage_flags |= (sub + 1) << kCountShift;
+          meta[sb] = make_int4(stage_flags, stage_valid, unit, st);
+        }
         if (PH && !host) {       // in flight with the page, tracked by its barrier
           const size_t so = ((size_t)layer * p.S + ent.y) * p.Hkv + h;
-          cp_async4(smem_u32(&psc[sb]), p.k_scale + so);
-          cp_async4(smem_u32(&psc[sb]) + 4, p.v_scale + so);
+          cp_async4(smem_u32(&psc[ps]), p.k_scale + so);
+          cp_async4(smem_u32(&psc[ps]) + 4, p.v_scale + so);
           cp_async_mbar_arrive(&full[sb]);
         }
-        mbar_arrive_expect_tx(&full[sb],
-                              (host ? 0u : (uint32_t)(2 * C::kTileBytes + C::kScaleBytes)) + qbytes);
+        const uint32_t bytes =
+            (host ? 0u : (uint32_t)(2 * C::kTileBytes + C::kScaleBytes)) + qbytes;
+        if (end) mbar_arrive_expect_tx(&full[sb], bytes);
+        else mbar_expect_tx(&full[sb], bytes);
         if (!host) {
           const int row_k = ((layer * p.S + ent.y) * p.Hkv + h) * P;
           if (FP8) {
@@ -549,9 +571,50 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
             tma_load_2d(stage + C::kTileBytes + P * 128, &tmV, &full[sb], 64, row_k);
           }
         }
-        if (qbytes) bulk_load(stage + C::kQOff, p.q + (size_t)unit * p.G * kD, qbytes, &full[sb]);
+        if (qbytes) bulk_load(first_page + C::kQOff, p.q + (size_t)unit * p.G * kD, qbytes, &full[sb]);
       }
-      ++st;
+      if (end) ++st;
+      return true;
+    };
+
+    // pages that share a stage, all resident: `n` entries of the window as its
+    // pages from the sub0-th on, a lane each
+    auto issue_group = [&](const int2* ents, int n, int flags, int unit, int h, int layer,
+                           int seq_len, int sub0, bool end) -> bool {
+      if (sub0 == 0) {
+        if (!acquire_warp()) return false;
+        stage_flags = stage_valid = 0;
+      }
+      const int sb = st % NST, sub = sub0 + lane;
+      uint8_t* const first_page = ring + sb * C::kStageBytes;
+      const uint32_t qbytes = (flags & kFirst) ? (uint32_t)p.G * kD * 2 : 0u;
+      int valid = 0;
+      if (lane < n) {
+        const int2 ent = ents[lane];
+        valid = max(0, min(P, seq_len - ent.x * P)) << (8 * sub);
+        const int head = (layer * p.S + ent.y) * p.Hkv + h;
+        uint8_t* const stage = first_page + sub * 2 * C::kTileBytes;
+        const uint32_t sc = smem_u32(&psc[sb * NPG + sub]);
+        cp_async4(sc, p.k_scale + head);
+        cp_async4(sc + 4, p.v_scale + head);
+        cp_async_mbar_arrive(&full[sb]);
+        tma_load_2d(stage, &tmK, &full[sb], 0, head * P);
+        tma_load_2d(stage + C::kTileBytes, &tmV, &full[sb], 0, head * kD);
+      }
+      stage_flags |= flags;
+      stage_valid |= __reduce_or_sync(0xffffffffu, valid);   // (and every lane has arrived)
+      if (lane == 0) {
+        const uint32_t bytes = (uint32_t)(n * 2 * C::kTileBytes) + qbytes;
+        if (end) {
+          meta[sb] = make_int4(stage_flags | (sub0 + n) << kCountShift, stage_valid, unit, st);
+          mbar_arrive_expect_tx(&full[sb], bytes);
+        } else {
+          mbar_expect_tx(&full[sb], bytes);
+        }
+        if (qbytes)
+          bulk_load(first_page + C::kQOff, p.q + (size_t)unit * p.G * kD, qbytes, &full[sb]);
+      }
+      if (end) ++st;
       return true;
     };
 
@@ -656,11 +719,25 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
           }
           __syncwarp();
           const int nw = __popc(mi);
-          if (WARP_ISSUE || lane == 0) {       // the resident path issues from lane 0 alone
-            for (int x = 0; x < nw && ok; ++x, ++issued) {
+          if constexpr (NPG > 1 && !WARP_ISSUE) {
+            for (int x = 0; x < nw && ok;) {
+              const int sub = issued % NPG, n = min(NPG - sub, nw - x);
+              const bool last = issued + n == j1 - j0;
               const int flags = (issued == 0 ? kFirst : 0) |
-                                (issued == j1 - j0 - 1 ? (u == u_last ? kLast | kFinal : kLast) : 0);
-              ok = issue_page(plist[x], pid[x], flags, u, h, layer, seq_len);
+                                (last ? (u == u_last ? kLast | kFinal : kLast) : 0);
+              ok = issue_group(plist + x, n, flags, u, h, layer, seq_len, sub,
+                               last || sub + n == NPG);
+              x += n;
+              issued += n;
+            }
+          } else if (WARP_ISSUE || lane == 0) {       // the resident path issues from lane 0 alone
+            for (int x = 0; x < nw && ok; ++x, ++issued) {
+              const bool last = issued == j1 - j0 - 1;
+              const int flags = (issued == 0 ? kFirst : 0) |
+                                (last ? (u == u_last ? kLast | kFinal : kLast) : 0);
+              const int sub = issued % NPG;
+              ok = issue_page(plist[x], pid[x], flags, u, h, layer, seq_len, sub,
+                              last || sub == NPG - 1);
             }
           }
           if (!WARP_ISSUE) ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -925,13 +1002,8 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
         funit = dsc.z;
         goto flushes;
       }
-      const int nvalid = dsc.y;
-      uint8_t* stage = ring + sb * C::kStageBytes;
-      const uint32_t kb = smem_u32(stage);
-      const uint32_t vb = kb + C::kTileBytes;
-      const float* ksc = reinterpret_cast<const float*>(stage + 2 * C::kTileBytes);
-      const float* vsc = ksc + P;
-      const float2 page_sc = PH ? psc[sb] : make_float2(1.0f, 1.0f);
+      uint8_t* const first_page = ring + sb * C::kStageBytes;
+      const int n_pages = NPG == 1 ? 1 : dsc.x >> kCountShift;
 
       if (dsc.x & kFirst) {
         // the unit's G query rows as the B operand (rows >= G are zero).
@@ -941,7 +1013,7 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
         // ~2^-18 of |q|max), so QK runs as e4m3 MMAs on the raw K codes;
         // per k32 step b0 = d 32ks + 4c..+3, b1 = d + 16; qb[ks] = hi,
         // qb[4 + ks] = lo
-        const __nv_bfloat16* qs = reinterpret_cast<const __nv_bfloat16*>(stage + C::kQOff);
+        const __nv_bfloat16* qs = reinterpret_cast<const __nv_bfloat16*>(first_page + C::kQOff);
         const bool row_ok = r4 < p.G;
         if (FP8) {
           float amax = 0.0f;
@@ -1000,16 +1072,24 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
       // than two CTAs per SM leave, so one.
       constexpr int NB = 1;
       constexpr int kSteps = C::kBlocks / NB;
-      // this warp's blocks of the page: the stream's block index
+      // this warp's blocks of the stage: the stream's block index
       // pc * kSteps + bs taken round-robin, block bs == warp - pc*kSteps mod 4
 #pragma unroll 1
-      for (int bs = (warp - pc * kSteps) & (kConsumerWarps - 1); bs < kSteps;
+      for (int bs = (warp - pc * kSteps) & (kConsumerWarps - 1); bs < n_pages * kSteps;
            bs += kConsumerWarps) {
-        const int tb0 = bs * NB * 16;
-        if (FT && (dsc.x & kWriteBack)) {
+        const int sub = NPG == 1 ? 0 : bs / kSteps;
+        const int tb0 = (bs - sub * kSteps) * NB * 16;
+        const int nvalid = NPG == 1 ? dsc.y : dsc.y >> (8 * sub) & 0xFF;
+        uint8_t* const stage = first_page + sub * 2 * C::kTileBytes;
+        const uint32_t kb = smem_u32(stage);
+        const uint32_t vb = kb + C::kTileBytes;
+        const float* ksc = reinterpret_cast<const float*>(stage + 2 * C::kTileBytes);
+        const float* vsc = ksc + P;
+        const float2 page_sc = PH ? psc[sb * NPG + sub] : make_float2(1.0f, 1.0f);
+        if (FT && (dsc.x & kWriteBack << sub)) {
           // fetch mode: this block's rows of the fetched page go to its slot
           // (before any zeroing below), K, V and, from KV head 0, the scales
-          const int slot = wslot[sb];
+          const int slot = wslot[sb * NPG + sub];
           const int row = dsc.z / p.Hkv, hh = dsc.z - row * p.Hkv;
           const int layer = p.layer0 + row / p.B;
           const size_t hp = ((size_t)layer * p.S + slot) * p.Hkv + hh;      // head-page index
@@ -1280,7 +1360,7 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[sb]);
-      ++pc;
+      pc += n_pages;
       if (dsc.x & kLast) {
         fkind = (dsc.x & kFinal) ? 2 : 1;
         funit = dsc.z;
@@ -1324,7 +1404,8 @@ template <int KIND, int P>
 size_t decode_smem() {
   using C = Cfg<KIND, P>;
   return 1024 + (size_t)C::kStages * C::kStageBytes + C::kCombineBytes + kWindow * 12 +
-         (size_t)C::kStages * (16 + C::kPairBytes) + 2 * C::kStages * 8 + 4 * 8 + (size_t)C::kStages * 4;
+         (size_t)C::kStages * (16 + C::kPairBytes) + 2 * C::kStages * 8 + 4 * 8 +
+         (size_t)C::kStages * C::kPages * 4;
 }
 
 // CTAs of one wave: resident CTAs per SM (the configuration's target, or
