@@ -262,6 +262,52 @@ def test_attention_against_64_bits(fmt, P, Hq, Hkv, k, lens):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("P,B", [(16, 3), (32, 3), (16, 40), (32, 40)])
+def test_attention_over_small_pages_with_holes(fmt, P, B):
+    """Rows of more entries than the kernel compacts at a time, padding and unresolved pages anywhere in
+    them, requests that end inside a page, one selected page, none; then the same pages from the host."""
+    import sparse_attention_decode_indexer_gb300 as ssa
+    L, Hkv, Hq, nmax, k = 2, 2, 6, 61, 47
+    rng = np.random.default_rng([P, B])
+    lay = _layout(fmt, P=P, Hq=Hq, Hkv=Hkv, L=L, Lp=nmax, B=B, nmax=nmax, k=k)
+    c, status, refs = _filled(fmt, lay, rng, host_tier=True)
+    bt = np.broadcast_to(np.arange(nmax, dtype=np.int32), (B, nmax))      # the requests share their pages
+    lens = rng.integers(1, nmax * P + 1, B)
+    lens[:2] = nmax * P - 3, 1
+    W = lay.max_sel
+    sel, phys = np.full((L, B, W), -1, np.int32), np.full((L, B, W), -1, np.int32)
+    slot_of = c.slot_of.cpu().numpy()
+    for l in range(L):
+        for b in range(B):
+            n = -(-int(lens[b]) // P)
+            s = np.sort(rng.permutation(n)[:k + 1])
+            at = np.sort(rng.permutation(W)[:len(s)])                     # padding between the entries
+            sel[l, b, at] = s
+            phys[l, b, at] = slot_of[l, s]
+    holes = (sel >= 0) & (rng.random(sel.shape) < 0.2)
+    holes[:, 2] = sel[:, 2] >= 0                                          # a row without any page
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x.astype(np.int32))).cuda()  # noqa: E731
+    q = _bf16(rng, L, B, Hq, D)[0].cuda()
+    ws = torch.zeros((ssa.ssa_workspace_size(lay),), dtype=torch.uint8, device="cuda")
+    out = torch.full((L, B, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    ssa.ssa_sparse_paged_decode(c, 0, L, q, dev(sel), dev(np.where(holes, -1, phys)), dev(lens), sm_scale(),
+                                out, status, ws)
+    assert int(status.item()) == ssa.ST_UNRESOLVED
+    assert not bool(out[:, 2].any())
+    left = np.where(holes, -1, sel)
+    some = [0, 1, 3] if B > 3 else [0, 1]
+    _check_attention(lay, refs, q[:, some], left[:, some], bt, lens[some], out[:, some], fmt)
+    status.zero_()
+    tail = torch.empty_like(out)
+    ssa.ssa_sparse_paged_decode(c, 0, L, q, dev(sel), dev(phys), dev(lens), sm_scale(), out, status, ws)
+    c.slot_of[:, 1::3] = -1
+    ssa.ssa_sparse_paged_decode_host_tail(c, 0, L, q, dev(sel), dev(bt), dev(lens), sm_scale(), tail, status, ws)
+    assert int(status.item()) == 0
+    assert torch.equal(out, tail)
+    _check_attention(lay, refs, q[:, some], sel[:, some], bt, lens[some], out[:, some], fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("heavy", [0, 1, 2, 3])
 def test_attention_over_pages_of_very_different_scale(fmt, heavy):
     """V of 2^-28, 2^-14, 1 and 2^26 by page, an all-zero page, and nearly all weight on one page: a
