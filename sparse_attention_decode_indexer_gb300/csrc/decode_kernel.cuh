@@ -439,12 +439,13 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
 
   if (warp == kProducerWarp) {
     // ---------------- producer warp ----------------------------------------
-    // The warp reads and compacts the rows; lane 0 issues the TMA loads (the
-    // resident path issues pages from lane 0 alone; the host-tail path from
-    // the whole warp, every lane its share of 16-byte copies for a page
-    // without a slot).  Lane 0's st counts the stages.  A stage's descriptor
-    // carries it, and the consumers check it against the stage they waited
-    // for.
+    // The warp reads and compacts the rows.  Who issues a page's loads: in the
+    // resident path lane 0 alone where a stage holds one page, a lane per page
+    // where pages share a stage (NPG > 1); in the host-tail and fetch modes
+    // the whole warp, every lane its share of 16-byte copies of a page
+    // without a slot.  st counts the stages: lane 0's, and where several lanes
+    // issue every lane's, all alike.  A stage's descriptor carries it, and the
+    // consumers check it against the stage they waited for.
     int st = 0;
     bool ok = true;
     int cur_row = -1, cnt = 0, seq_len = 0;
@@ -474,9 +475,10 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
     // host-tail mode logical id -2 - ent.y; in fetch mode slot -2 - ent.y,
     // logical id mid) by 16-byte cp.async copies from the pinned mirror, every
     // lane a share, into the same swizzled stage layout, and in fetch mode
-    // marked for the consumers to write into the slot.  The whole warp in
-    // the host-tail and fetch modes, lane 0 alone in the resident mode.  The
-    // page is the `sub`-th of its stage, `end`: the last.
+    // marked for the consumers to write into the slot.  Called by the whole
+    // warp in the host-tail and fetch modes, by lane 0 alone in the resident
+    // mode with one page per stage.  The page is the `sub`-th of its stage,
+    // `end`: the last.
     int stage_flags = 0, stage_valid = 0;    // of the stage's pages so far
     auto issue_page = [&](int2 ent, int mid, int flags, int unit, int h, int layer,
                           int seq_len, int sub, bool end) -> bool {
@@ -602,7 +604,8 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
         tma_load_2d(stage + C::kTileBytes, &tmV, &full[sb], 0, head * kD);
       }
       stage_flags |= flags;
-      stage_valid |= __reduce_or_sync(0xffffffffu, valid);   // (and every lane has arrived)
+      stage_valid |= __reduce_or_sync(0xffffffffu, valid);
+      __syncwarp();                            // every lane's copies are tracked first
       if (lane == 0) {
         const uint32_t bytes = (uint32_t)(n * 2 * C::kTileBytes) + qbytes;
         if (end) {
@@ -730,7 +733,7 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
               x += n;
               issued += n;
             }
-          } else if (WARP_ISSUE || lane == 0) {       // the resident path issues from lane 0 alone
+          } else if (WARP_ISSUE || lane == 0) {       // one resident page per stage: lane 0 alone
             for (int x = 0; x < nw && ok; ++x, ++issued) {
               const bool last = issued == j1 - j0 - 1;
               const int flags = (issued == 0 ? kFirst : 0) |
