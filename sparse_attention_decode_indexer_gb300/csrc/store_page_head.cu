@@ -749,7 +749,7 @@ store_page_head_kernel(const __grid_constant__ StorePHParams p) {
   }
 
   // the page's slab row, now that every head's maximum is there
-  if (!mbar_wait(&s_bar, 0, nullptr)) {
+  if (!mbar_wait<true>(&s_bar, 0, nullptr)) {
     set_status(p.status, SSA_ST_TIMEOUT);
     return;
   }

@@ -21,3 +21,12 @@ def test_lanes_copies_are_tracked_before_the_stage_may_complete(start):
     body = _source("decode_kernel.cuh").split(start)[1].split("return true;")[0]
     tracked, arrive = body.index("cp_async_mbar_arrive(&full[sb])"), body.index("mbar_arrive_expect_tx(&full[sb]")
     assert tracked < body.index("__syncwarp()") < arrive
+
+
+def test_words_pushed_by_other_ctas_are_acquired_at_cluster_scope():
+    """The heads' maxima of a whole page come from other CTAs by st.async, released at cluster scope."""
+    store, common = _source("store_page_head.cu"), _source("common.cuh")
+    assert "st.async.shared::cluster" in store
+    assert re.findall(r"mbar_wait\S*\(&s_bar", store) == ["mbar_wait<true>(&s_bar"]
+    cluster = common.split("if constexpr (CLUSTER)")[1].split("else")[0]
+    assert "mbarrier.try_wait.parity.acquire.cluster.shared::cta" in cluster
