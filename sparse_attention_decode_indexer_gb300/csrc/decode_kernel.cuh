@@ -40,7 +40,8 @@
 //     m16n8k16 f16 MMAs on the V codes converted exactly to f16; fragments
 //     by ldmatrix.  The K scale multiplies the fp32 score, and the V scale
 //     folds into the probabilities (relative to a running power-of-two
-//     reference, so the f16 operand never overflows).  V is stored d-major
+//     reference, so the f16 operand never overflows; the page_head formats
+//     keep it within a window of the reference, see kVWindow).  V is stored d-major
 //     in the pool ([Hkv][D][P]) so that the 8-bit reads run along tokens, the
 //     reduction axis of PV;
 //   * at the end of a piece each consumer warp leaves its softmax state in
@@ -98,6 +99,17 @@ constexpr int kMaxG = 8;
 constexpr int kWindow = 32;          // producer compaction window (entries)
 constexpr int kMaxStages = 12;
 constexpr float kSlack = 8.0f;     // log2 headroom of the running softmax reference
+// page_head: the weights p * v_scale / vref enter f16 raised by kRaise = 2^7
+// (p <= 2^kSlack and v_scale < vref, so at most 2^15), and vref moves when a
+// page's scale leaves [kVWindow, 1) of it.  So a weight keeps f16's 11 bits
+// down to 2^-17 of the row's largest whatever the pages' scales are, and
+// below that has steps of 2^-27: tokens far below an attention sink that has
+// no V of its own are what the output is made of.  A move rescales the
+// accumulators; over pages whose scales spread by an octave (standard
+// deviation), 32 requests x 12 layers: a window of 1/2 142.6 us, 1/4 141.4,
+// 1/16 139.7, 1/512 139.2.
+constexpr float kRaise = 128.0f;
+constexpr float kVWindow = 0.0625f;
 constexpr int kSmemPerSm = 228 * 1024;
 constexpr int kSmemPerCtaMax = 227 * 1024;
 constexpr int kSmemReservedPerCta = 1024;
@@ -819,6 +831,7 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
   // warps never wait for one another.
   int n_flush = 0;
   auto flush = [&]() -> bool {
+    const float vout = vref * (PH ? 1.0f / kRaise : 1.0f);   // exact
     float l0 = l_run0, l1 = l_run1;
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
@@ -834,10 +847,10 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) {
       const int d = (16 * mt + r4) ^ (8 * c);
-      cO[(warp * kMaxG + 2 * c) * kD + d] = o[mt][0] * vref;
-      cO[(warp * kMaxG + 2 * c + 1) * kD + d] = o[mt][1] * vref;
-      cO[(warp * kMaxG + 2 * c) * kD + (d ^ 8)] = o[mt][2] * vref;
-      cO[(warp * kMaxG + 2 * c + 1) * kD + (d ^ 8)] = o[mt][3] * vref;
+      cO[(warp * kMaxG + 2 * c) * kD + d] = o[mt][0] * vout;
+      cO[(warp * kMaxG + 2 * c + 1) * kD + d] = o[mt][1] * vout;
+      cO[(warp * kMaxG + 2 * c) * kD + (d ^ 8)] = o[mt][2] * vout;
+      cO[(warp * kMaxG + 2 * c + 1) * kD + (d ^ 8)] = o[mt][3] * vout;
     }
     if (r4 == 0) {
       cM[warp * kMaxG + 2 * c] = m_run0;
@@ -864,6 +877,7 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
     return ok;
   };
   auto final_flush = [&](int unit) -> bool {
+    const float vout = vref * (PH ? 1.0f / kRaise : 1.0f);   // exact
     float l0 = l_run0, l1 = l_run1;
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
@@ -877,10 +891,10 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) {
       const int d = (16 * mt + r4) ^ (8 * c);
-      cO[(warp * kMaxG + 2 * c) * kD + d] = o[mt][0] * vref;
-      cO[(warp * kMaxG + 2 * c + 1) * kD + d] = o[mt][1] * vref;
-      cO[(warp * kMaxG + 2 * c) * kD + (d ^ 8)] = o[mt][2] * vref;
-      cO[(warp * kMaxG + 2 * c + 1) * kD + (d ^ 8)] = o[mt][3] * vref;
+      cO[(warp * kMaxG + 2 * c) * kD + d] = o[mt][0] * vout;
+      cO[(warp * kMaxG + 2 * c + 1) * kD + d] = o[mt][1] * vout;
+      cO[(warp * kMaxG + 2 * c) * kD + (d ^ 8)] = o[mt][2] * vout;
+      cO[(warp * kMaxG + 2 * c + 1) * kD + (d ^ 8)] = o[mt][3] * vout;
     }
     if (r4 == 0) {
       cM[warp * kMaxG + 2 * c] = m_run0;
@@ -1248,13 +1262,13 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
         float vinv = 1.0f;
         if (PH) {
           // one scale for the block's tokens, the same in every lane: the
-          // reference is the power of two above it, moved only when a page's
-          // scale leaves [2^-9, 1) of it, so that small pages keep their
-          // precision in f16 beside large ones; at most 2^60 below the largest
-          // so far, which keeps the fp32 sums in range
+          // reference is the power of two above it, moved when a page's scale
+          // leaves the window, so that small pages keep their precision in f16
+          // beside large ones; at most 2^60 below the largest so far, which
+          // keeps the fp32 sums in range
           const float pv = page_sc.y;
           const float low = fmaxf(vtop * 0x1p-60f, 0x1p-126f);
-          if (pv >= vref || (pv > 0.0f && pv < vref * 0x1p-9f && vref > low)) {
+          if (pv >= vref || (pv > 0.0f && pv < vref * kVWindow && vref > low)) {
             const float nref =
                 fmaxf(__uint_as_float(((__float_as_uint(pv) >> 23) + 1) << 23), low);
             const float ratio = vref * pow2_rcp(nref);
@@ -1291,7 +1305,8 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
           if (FP8) {
             ls0 += p0 + p2;
             ls1 += p1 + p3;
-            const float wA = vsA[j] * vinv, wB = vsB[j] * vinv;
+            float wA = vsA[j] * vinv, wB = vsB[j] * vinv;
+            if (PH) { wA *= kRaise; wB *= kRaise; }
             P0 = pack_f16(p0 * wA, p1 * wA);
             P1 = pack_f16(p2 * wB, p3 * wB);
           } else {
