@@ -194,9 +194,9 @@ class Layout:
     """Shapes of a cache and its calls.  ``kv_format`` names the KV format:
     "bf16", "fp8" (e4m3, one scale per token), "e4m3_page_head" or
     "int8_page_head" (8-bit codes, one K and one V scale per page and KV
-    head); None takes bf16 or fp8 by ``fp8``.  Where it is given, ``fp8`` ends
-    up saying whether the codes are 8 bits wide (V d-major in the pool, with
-    scales)."""
+    head); None takes bf16 or fp8 by ``fp8``.  Where it is given, ``fp8`` says
+    whether the codes are 8 bits wide (V d-major in the pool, with scales),
+    and follows it."""
     page_size: int
     n_q_heads: int
     n_kv_heads: int
@@ -210,12 +210,15 @@ class Layout:
     block_topk: int
     kv_format: str | None = None
 
-    def __post_init__(self):
-        if self.kv_format is None:        # stays so: a copy with another fp8 takes that one's
-            return
-        if self.kv_format not in KV_FORMATS:
-            raise ValueError(f"kv_format {self.kv_format!r}: one of {sorted(KV_FORMATS)}")
-        self.fp8 = self.kv_format != "bf16"
+    def __setattr__(self, name, value):
+        # the two never contradict each other: a cache's buffers go by both
+        if name == "kv_format" and value is not None:
+            if value not in KV_FORMATS:
+                raise ValueError(f"kv_format {value!r}: one of {sorted(KV_FORMATS)}")
+            object.__setattr__(self, "fp8", value != "bf16")
+        elif name == "fp8" and self.kv_format is not None and bool(value) != (self.kv_format != "bf16"):
+            raise ValueError(f"fp8 {value!r}: kv_format is {self.kv_format!r}")
+        object.__setattr__(self, name, value)
 
     @property
     def scale_floats(self) -> int:
