@@ -167,8 +167,9 @@ typedef struct ssa_cache {
  * layer range of this layout.  The calls use disjoint parts of it (the page
  * calls one part together).  Zero the workspace
  * once before its first use: ssa_sparse_paged_decode keeps per-unit split
- * counters in it, and every call that completes leaves them zero again (a
- * call that reported SSA_ST_TIMEOUT may not: zero the workspace again).
+ * counters in it, ssa_fork_requests a ticket and marks, and every call that
+ * completes leaves them zero again (a call that reported SSA_ST_TIMEOUT may
+ * not: zero the workspace again).
  * 0 on a bad layout. */
 size_t ssa_workspace_size(const ssa_layout *lay);
 
@@ -519,7 +520,10 @@ int ssa_copy_pages(const ssa_layout *lay, const ssa_cache *c, const int32_t *src
  * it as a full page, a pin); every other row gets a copy (as ssa_copy_pages).
  * New pages are the lowest free ids, in row order (the copy, then growth);
  * pages let go in this call count as free.  New pages start with an empty slab
- * row.  With a mirror, new pages and pages that became free give their slots
+ * row.  A page that a row goes on holding is never a new one: if nothing counts
+ * it (the row's length grew past the page by other means than this call, after
+ * the counting), it gets a count of one and SSA_ST_BAD_ID is set.
+ * With a mirror, new pages and pages that became free give their slots
  * back; without one every page keeps the slot it has (so a cache without a
  * mirror wants pool_slots >= logical_pages: a new page without a slot holds no
  * K and V).  Entries past a row's pages become -1.
@@ -541,7 +545,8 @@ int ssa_fork_requests(const ssa_layout *lay, const ssa_cache *c, const ssa_reque
  *   moved_from_opt, moved_to_opt [Lp] int32 out or NULL: the first n_moved
  *   entries are the moves (for references that the caller keeps itself)
  *   n_moved_opt [1] int32 out or NULL
- * Row entries whose page nothing counts set SSA_ST_BAD_ID.
+ * Row entries whose page nothing counts set SSA_ST_BAD_ID; their pages are free
+ * to be moved onto, so count first (ssa_page_refs, ssa_fork_requests).
  */
 int ssa_compact_pages(const ssa_layout *lay, const ssa_cache *c, const ssa_requests *r,
                       int32_t *moved_from_opt, int32_t *moved_to_opt, int32_t *n_moved_opt,

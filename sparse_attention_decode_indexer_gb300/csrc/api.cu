@@ -82,14 +82,14 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Workspace: [scores | miss_page | miss_slot | n_miss | part_o | part_ml |
 // tickets | idx_tickets], each sized for the whole layer range of the
-// layout.  Only the tickets need a defined start (zero); every call leaves
-// them zero.
+// layout.  Only the tickets and pg_held need a defined start (zero); every
+// call leaves them zero.
 struct WsLayout {
   size_t scores, miss_page, miss_slot, n_miss, part_o, part_ml, tickets, idx_tickets;
   size_t pf_cand, pf_ncand, pf_miss_page, pf_miss_slot, pf_n_miss;   // ssa_prefetch_pages
   // the page calls
   size_t pg_bt, pg_len, pg_bits, pg_list, pg_to, pg_map, pg_from, pg_plan, pg_copy, pg_count,
-      pg_ok, pg_ticket;
+      pg_ok, pg_ticket, pg_held;
   size_t total;
 };
 
@@ -126,6 +126,7 @@ WsLayout ws_layout(const Dims& d) {
   w.pg_count = off;  off += 256;
   w.pg_ok = off;     off += align256((size_t)kMaxCopyPairs * 4);
   w.pg_ticket = off; off += 256;
+  w.pg_held = off;   off += align256((size_t)d.Lp);
   w.total = off;
   return w;
 }
@@ -143,7 +144,7 @@ PageWs page_ws(const Dims& d, void* ws) {
                 at<char>(ws, w.pg_from),    at<char>(ws, w.pg_plan),
                 at<char>(ws, w.pg_copy),
                 at<int32_t>(ws, w.pg_count), at<int32_t>(ws, w.pg_ok),
-                at<int32_t>(ws, w.pg_ticket)};
+                at<int32_t>(ws, w.pg_ticket), at<uint8_t>(ws, w.pg_held)};
 }
 
 // The page calls write every array of a cache.

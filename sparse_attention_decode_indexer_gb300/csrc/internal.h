@@ -133,6 +133,7 @@ struct PageWs {
   int32_t* count;      // [2]
   int32_t* ok;         // [kMaxCopyPairs]
   int32_t* ticket;     // zero between calls
+  uint8_t* held;       // [Lp], zero between calls
 };
 constexpr int kMaxCopyPairs = 16384;
 cudaError_t launch_page_refs(const Dims& d, const ssa_requests& r, int32_t* status,

@@ -13,10 +13,11 @@
 // one gets a copy of it in a new page.  New pages are the lowest free ids, in
 // row order (a row's copy first, then its growth).  Two launches:
 //   plan   each row's old references off, its new ones on (g counts once per
-//          row that continues it, so a page is free exactly when its count is
-//          0), the old table kept aside; then the last CTA to finish marks the
-//          free pages, resolves the claims, scans the rows' needs and lists
-//          that many free pages;
+//          row that continues it), the old table kept aside and the pages that
+//          rows go on holding marked; then the last CTA to finish finds the free
+//          pages (count 0 and not held: a held page that nothing counts is
+//          flagged and counted), resolves the claims, scans the rows' needs and
+//          lists that many free pages;
 //   apply  the rows, and per layer the copies, the cleared slab rows of new
 //          pages and the slots of freed ones.
 //
@@ -301,6 +302,7 @@ __global__ void count_refs_kernel(Table t, int Lp, int32_t* status) {
 struct ForkWs {
   int32_t *old_bt, *old_len;     // [B][nmax], [B]
   uint32_t* bits;                // [ceil(Lp / 32)] free pages
+  uint8_t* held;                 // [Lp] 1: a row holds the page after the call; zero between calls
   int32_t* list;                 // the new pages, in rank order
   int2* from;                    // [B] {the partly filled page the row continues or -1, the
                                  // parent's length}
@@ -317,21 +319,43 @@ __device__ __forceinline__ int parent_of(const int32_t* parent, int i, int B, in
   return i;
 }
 
-// One bit per page, ref > 0 (live) or not, by one CTA; into the workspace and,
-// where it fits, shared memory, which is what the CTA goes on with.
-__device__ __forceinline__ const uint32_t* page_bits(const int32_t* ref, int Lp, uint32_t* bits,
-                                                     uint32_t* s_bits, bool live) {
+// One bit per page by one CTA: ref > 0 (live), or, FREE, neither counted nor
+// held; into the workspace and, where it fits, shared memory, which is what
+// the CTA goes on with.  FREE clears the marks for the next call, and a held
+// page that nothing counts gets a count of one.
+template <bool FREE>
+__device__ __forceinline__ const uint32_t* page_bits(int32_t* ref, uint8_t* held, int Lp,
+                                                     uint32_t* bits, uint32_t* s_bits,
+                                                     int32_t* status) {
+  constexpr int kBatch = 8;               // words a warp loads before it writes any
   const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   const int words = (Lp + 31) / 32;
   const bool fits = words <= kPlanWords;
-#pragma unroll 8
-  for (int w = threadIdx.x >> 5; w < words; w += nw) {
-    const int id = w * 32 + lane;
-    const bool bit = id < Lp && (__ldcg(&ref[id]) > 0) == live;
-    const uint32_t m = __ballot_sync(0xffffffffu, bit);
-    if (lane == 0) {
-      bits[w] = m;
-      if (fits) s_bits[w] = m;
+  for (int w0 = threadIdx.x >> 5; w0 < words; w0 += kBatch * nw) {
+    int n[kBatch];
+    uint8_t h[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int id = (w0 + k * nw) * 32 + lane;
+      n[k] = id < Lp ? __ldcg(&ref[id]) : (FREE ? 1 : 0);
+      h[k] = FREE && id < Lp ? __ldcg(&held[id]) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int w = w0 + k * nw, id = w * 32 + lane;
+      if (w >= words) break;
+      if (FREE && h[k]) {
+        held[id] = 0;
+        if (n[k] <= 0) {
+          ref[id] = 1;
+          set_status(status, SSA_ST_BAD_ID);
+        }
+      }
+      const uint32_t m = __ballot_sync(0xffffffffu, FREE ? n[k] <= 0 && !h[k] : n[k] > 0);
+      if (lane == 0) {
+        bits[w] = m;
+        if (fits) s_bits[w] = m;
+      }
     }
   }
   return fits ? s_bits : bits;
@@ -350,10 +374,6 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(Table t, const 
   // the references, and what each row continues
   {
     const int n = B * t.nmax;             // at most 1638 x 49152
-    auto add = [&](int id, int v) {
-      if (valid_page(c, id)) atomicAdd(&t.ref[id], v);
-      else set_status(c.status, SSA_ST_BAD_ID);
-    };
     for (int x = blockIdx.x * kPlanThreads + tid; x < n; x += gridDim.x * kPlanThreads) {
       const int i = x / t.nmax, p = x - i * t.nmax;
       const int id = t.bt[x], len = row_len(t, i, c.status);
@@ -364,9 +384,14 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(Table t, const 
       if (p == 0) w.old_len[i] = len;
       if (p == (jlen % P ? jlen / P : 0))
         w.from[i] = make_int2(jlen % P && valid_page(c, jid) ? jid : -1, jlen);
-      if (j == i) continue;
-      if (p < (len + P - 1) / P) add(id, -1);
-      if (p < (jlen + P - 1) / P) add(jid, 1);
+      const bool out = j != i && p < (len + P - 1) / P, in = p < (jlen + P - 1) / P;
+      if ((out && !valid_page(c, id)) || (in && !valid_page(c, jid)))
+        set_status(c.status, SSA_ST_BAD_ID);
+      if (out && valid_page(c, id)) atomicAdd(&t.ref[id], -1);
+      if (in && valid_page(c, jid)) {
+        w.held[jid] = 1;
+        if (j != i) atomicAdd(&t.ref[jid], 1);
+      }
     }
   }
   __syncthreads();
@@ -402,7 +427,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(Table t, const 
     if (want > most) set_status(c.status, SSA_ST_BAD_POS);
     nlens[i] = max(f.y, min(want, most));
   }
-  const uint32_t* bits = page_bits(t.ref, c.Lp, w.bits, s_bits, false);
+  const uint32_t* bits = page_bits<true>(t.ref, w.held, c.Lp, w.bits, s_bits, c.status);
   __syncthreads();
   for (int i = tid; i < B; i += kPlanThreads) {
     const int g = gs[i];
@@ -539,7 +564,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(Table t, Com
   __shared__ uint32_t s_bits[kPlanWords];
   pdl_trigger();
   pdl_wait();
-  const uint32_t* bits = page_bits(t.ref, Lp, w.bits, s_bits, true);
+  const uint32_t* bits = page_bits<false>(t.ref, nullptr, Lp, w.bits, s_bits, nullptr);
   __syncthreads();
   const int tid = threadIdx.x, words = (Lp + 31) / 32;
   // live pages in all, then those below that number
@@ -730,8 +755,8 @@ cudaError_t launch_fork(const Dims& d, const ssa_cache& c, const ssa_requests& r
                         const PageWs& w, int num_sms, cudaStream_t s) {
   const PageCache pc = page_cache(d, c, status);
   const Table t = table_of(d, r);
-  const ForkWs fw{w.old_bt,       w.old_len,      w.bits,         w.list,
-                  (int2*)w.from,  (int4*)w.plan,  (int2*)w.copy,  w.ticket};
+  const ForkWs fw{w.old_bt,       w.old_len,      w.bits,        w.held,  w.list,
+                  (int2*)w.from,  (int4*)w.plan,  (int2*)w.copy, w.ticket};
   // one CTA up to four entries a thread (it then needs no ticket), else up to
   // two per SM
   const long long entries = (long long)d.B * d.nmax;

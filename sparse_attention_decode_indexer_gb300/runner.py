@@ -149,7 +149,10 @@ class DecodeRunner:
     def fork(self, parent, new_lens=None):
         """Row i goes on with what row parent[i] held (-1: freed), grown to
         new_lens[i] tokens; int32 [B] on the device.  The block table and the
-        lengths change in place, so captured steps see them."""
+        lengths change in place, so captured steps see them.  From the first
+        use of the table on, lengths grow past a page by this call only: a
+        page that nothing counts sets ST_BAD_ID (here it is kept and counted;
+        a compaction takes it for free)."""
         table = self.table
         self._wait_preload()
         ssa_fork_requests(self.cache, table, parent, new_lens, self.status, self.ws)
