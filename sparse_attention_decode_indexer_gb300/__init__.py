@@ -288,6 +288,7 @@ class KVCache:
             self.k_scale_mirror, self.v_scale_mirror, self.slab, self.slab_scale, self.slab_sum,
             self.slab_cnt, self.slot_of, self.page_of, self.last_use, self.clock)])
         self._lay = layout.c()
+        self._row = H * D                # elements of a token's K, and of its V
 
     @property
     def c(self) -> SsaCache:
@@ -303,12 +304,25 @@ def ssa_lru_init(cache: KVCache, identity: bool, stream=None):
                               _stream(stream)))
 
 
+_BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
+_INT64 = torch.int64
+
+
 def ssa_store_kv_mirror(cache: KVCache, layer0: int, n_layers: int, k, v, pos, status,
                         stream=None):
-    """k, v: bf16 [n_layers][T][Hkv][D]; pos: int64 [T] logical token ids."""
-    T = int(pos.shape[0])
-    _check(lib().ssa_store_kv_mirror(ctypes.byref(cache._lay), ctypes.byref(cache.c), layer0,
-                                     n_layers, _ptr(k), _ptr(v), _ptr(pos), T, _ptr(status),
+    """k, v: bf16 (or its bits) [n_layers][T][Hkv][D]; pos: int64 [T] logical
+    token ids; all contiguous."""
+    T = pos.shape[0]
+    n = n_layers * T * cache._row
+    if not (k.is_contiguous() and v.is_contiguous() and pos.is_contiguous() and
+            k.dtype in _BF16_BITS and v.dtype in _BF16_BITS and pos.dtype is _INT64 and
+            k.numel() >= n and v.numel() >= n):
+        got = ", ".join(f"{name} {tuple(x.shape)} {x.dtype} strides {x.stride()}"
+                        for name, x in (("k", k), ("v", v), ("pos", pos)))
+        raise ValueError("k, v: contiguous bfloat16 [n_layers][T][Hkv][D], pos: contiguous int64 "
+                         f"[T]; got {got}")
+    _check(lib().ssa_store_kv_mirror(cache._lay, cache._c, layer0, n_layers, k.data_ptr(),
+                                     v.data_ptr(), pos.data_ptr(), T, _ptr(status),
                                      _stream(stream)))
 
 

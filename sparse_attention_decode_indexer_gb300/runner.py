@@ -117,16 +117,18 @@ class DecodeRunner:
 
     # write path ---------------------------------------------------------------
     def store(self, layer0: int, n_layers: int, k, v, pos, positions=None):
-        """k, v: bf16 [n_layers][T][Hkv][D] on the device; pos: int64 [T]
-        logical token ids.  With ``rope``, positions [T] (int32 or int64) are
-        the tokens' positions in their requests; k itself stays as it is."""
+        """k, v: bf16 [n_layers][T][Hkv][D] on the device, strided views (of a
+        fused projection, say) among them; pos: int64 [T] logical token ids.
+        With ``rope``, positions [T] (int32 or int64) are the tokens' positions
+        in their requests; k itself stays as it is."""
         if self.rope is not None:
             if positions is None:
                 raise ValueError("store with rope: positions of the tokens")
             k_rot = torch.empty(k.shape, dtype=k.dtype, device=k.device)
             ssa_rope(self.rope, positions, k=k, k_out=k_rot)
             k = k_rot
-        ssa_store_kv_mirror(self.cache, layer0, n_layers, k, v, pos, self.status)
+        ssa_store_kv_mirror(self.cache, layer0, n_layers, k.contiguous(), v.contiguous(), pos,
+                            self.status)
 
     # owners of the pages ----------------------------------------------------------
     @property
