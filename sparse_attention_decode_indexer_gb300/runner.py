@@ -280,7 +280,8 @@ class DecodeRunner:
             for l in range(L):
                 self._calls(q[l:l + 1], l, 1, keep_scores, fused=False)
         elif self.graphs:
-            key = (q.data_ptr(), tuple(q.shape), keep_scores)
+            # with rope q may be a strided view, and views share their addresses
+            key = (q.data_ptr(), tuple(q.shape), q.stride(), keep_scores)
             g = self._graphs.get(key)
             if g is None:
                 # this call's step runs eagerly (and sets the kernels'
