@@ -101,6 +101,7 @@ class DecodeRunner:
     def enable_preload(self, width: int):
         """Issue the top-k preload of `width` pages per request with every
         later layer-batched step (0 turns it off)."""
+        self._wait_preload()
         self.preload_width = int(width)
         if not self.preload_width or hasattr(self, "side"):
             return
@@ -120,7 +121,9 @@ class DecodeRunner:
         """k, v: bf16 [n_layers][T][Hkv][D] on the device, strided views (of a
         fused projection, say) among them; pos: int64 [T] logical token ids.
         With ``rope``, positions [T] (int32 or int64) are the tokens' positions
-        in their requests; k itself stays as it is."""
+        in their requests; k itself stays as it is.  Waits for the last step's
+        preload, but in a capture, whose replays are the caller's to order."""
+        self._wait_preload()
         if self.rope is not None:
             if positions is None:
                 raise ValueError("store with rope: positions of the tokens")
@@ -144,9 +147,15 @@ class DecodeRunner:
         return self._table
 
     def _wait_preload(self):
-        # the last step's preload may still bind slots on its own stream
-        if hasattr(self, "side"):
+        # the last step's preload may still bind and fill slots on its own stream
+        if hasattr(self, "side") and not torch.cuda.is_current_stream_capturing():
             torch.cuda.current_stream().wait_event(self.ev_preload)
+
+    def _wait_preload_or_refuse(self):
+        if self.preload_width and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("no capture of page calls while steps preload: a replay would not "
+                               "wait for the last step's preload (enable_preload(0) first)")
+        self._wait_preload()
 
     def fork(self, parent, new_lens=None):
         """Row i goes on with what row parent[i] held (-1: freed), grown to
@@ -156,13 +165,13 @@ class DecodeRunner:
         page that nothing counts sets ST_BAD_ID (here it is kept and counted;
         a compaction takes it for free)."""
         table = self.table
-        self._wait_preload()
+        self._wait_preload_or_refuse()
         ssa_fork_requests(self.cache, table, parent, new_lens, self.status, self.ws)
 
     def compact(self, moved_from=None, moved_to=None, n_moved=None):
         """Move the live pages to the lowest logical ids."""
         table = self.table
-        self._wait_preload()
+        self._wait_preload_or_refuse()
         ssa_compact_pages(self.cache, table, self.status, self.ws, moved_from, moved_to, n_moved)
 
     # one decode step ------------------------------------------------------------
