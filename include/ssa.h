@@ -361,7 +361,9 @@ int ssa_sparse_paged_decode_fetch(const ssa_layout *lay, const ssa_cache *c, int
  * Requires n_layers * B * W <= 16384 (SSA_ERR_UNSUPPORTED) and pool_slots >=
  * min(n_layers * B * W, logical_pages) (SSA_ERR_POOL_TOO_SMALL).  Use one
  * residency mode per cache: this call and ssa_ensure_resident / ssa_ensure_remap
- * keep different state.
+ * keep different state.  ssa_store_kv_mirror goes by each layer's own slot_of:
+ * for a store that may touch pages that hold a slot, copy layer0's row over the
+ * other layers' and set those back to -1 after the call.
  */
 int ssa_ensure_remap_shared(const ssa_layout *lay, const ssa_cache *c, int layer0,
                             int n_layers, const int32_t *sel, const int32_t *block_table,

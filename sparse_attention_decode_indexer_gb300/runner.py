@@ -81,6 +81,10 @@ class DecodeRunner:
         # one LRU state for all layers (the first layer's), each miss copied
         # for every layer; layer-batched steps only
         self.shared_residency = bool(shared_residency)
+        if shared_residency and host_tier:
+            # the other layers' state stays unbound (what the page calls go by)
+            for t in (self.cache.slot_of, self.cache.page_of):
+                t[1:].fill_(-1)
         # misses fetched inside the attention (ssa_ensure_remap_deferred +
         # ssa_sparse_paged_decode_fetch) instead of by a copy before it
         self.fetch_in_attention = bool(fetch_in_attention) and host_tier
@@ -130,8 +134,16 @@ class DecodeRunner:
             k_rot = torch.empty(k.shape, dtype=k.dtype, device=k.device)
             ssa_rope(self.rope, positions, k=k, k_out=k_rot)
             k = k_rot
+        # with shared residency a page's slot is that of layer 0 in every layer:
+        # the other layers' rows say so while the store reads them
+        rows = None
+        if self.shared_residency and self.host_tier:
+            rows = self.cache.slot_of[max(layer0, 1):layer0 + n_layers]
+            rows.copy_(self.cache.slot_of[:1].expand_as(rows))
         ssa_store_kv_mirror(self.cache, layer0, n_layers, k.contiguous(), v.contiguous(), pos,
                             self.status)
+        if rows is not None:
+            rows.fill_(-1)
 
     # owners of the pages ----------------------------------------------------------
     @property
