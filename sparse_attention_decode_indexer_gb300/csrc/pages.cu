@@ -94,27 +94,26 @@ struct PageCopy {
   __device__ __forceinline__ long long units(const PageCache& c) const {
     return kv16 + c.HD / 4 + c.HD / 16;
   }
-  // unit u: read from `from`, written to d0 and d1 (null: nowhere)
+  // unit u: read from `from`, written to `to`; K's and V's only where they
+  // move in the mirror alone (compaction: !DST_SLOT, !POOL)
   __device__ __forceinline__ void unit(const PageCache& c, long long u, const uint4*& from,
-                                       uint4*& d0, uint4*& d1) const {
-    d1 = nullptr;
-    if (u < kv16) {
+                                       uint4*& to) const {
+    if (!POOL && u < kv16) {
       const bool v = u >= c.pb16;
       if (v) u -= c.pb16;
-      uint4* pool = reinterpret_cast<uint4*>(v ? c.v_pool : c.k_pool);
+      const uint4* pool = reinterpret_cast<const uint4*>(v ? c.v_pool : c.k_pool);
       uint4* m = reinterpret_cast<uint4*>(v ? c.v_mir : c.k_mir);
       from = ss >= 0 ? pool + ps * c.pb16 + u : m + ls * c.pb16 + u;
-      d0 = mir ? m + ld * c.pb16 + u : nullptr;
-      if (sd >= 0) d1 = pool + pd * c.pb16 + u;
+      to = m + ld * c.pb16 + u;
     } else if ((u -= kv16) < c.HD / 4) {
       uint4* sum = reinterpret_cast<uint4*>(c.slab_sum);
       from = sum + ls * (c.HD / 4) + u;
-      d0 = sum + ld * (c.HD / 4) + u;
+      to = sum + ld * (c.HD / 4) + u;
     } else {
       u -= c.HD / 4;
       uint4* code = reinterpret_cast<uint4*>(c.slab);
       from = code + ls * (c.HD / 16) + u;
-      d0 = code + ld * (c.HD / 16) + u;
+      to = code + ld * (c.HD / 16) + u;
     }
   }
   // the scales, and the slab row's scale and count: threads i of n
@@ -171,12 +170,12 @@ __device__ __forceinline__ void copy_page(const PageCache& c, int layer, int src
   uint4 buf[2];                            // HD <= 1024: at most 320 units of slab row
   const int units = c.HD / 4 + c.HD / 16;
   const uint4* from;
-  uint4 *to[2], *none;
+  uint4* to[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     to[i] = nullptr;
     if (tid + i * kCopyThreads < units) {
-      pc.unit(c, pc.kv16 + tid + i * kCopyThreads, from, to[i], none);
+      pc.unit(c, pc.kv16 + tid + i * kCopyThreads, from, to[i]);
       buf[i] = *from;
     }
   }
@@ -631,8 +630,7 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(CompactWs w,
       to[i] = nullptr;
       if (u < units) {
         const uint4* from;
-        uint4* none;
-        pc.unit(c, u, from, to[i], none);
+        pc.unit(c, u, from, to[i]);
         buf[i] = *from;
       }
     }
