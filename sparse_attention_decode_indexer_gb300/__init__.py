@@ -1,8 +1,9 @@
 """GB300 (sm_103a) sparse-attention decode step: Python binding of libssa_gb300.so.
 
-The five calls of the decode step keep their C names and only marshal
-arguments (torch tensors -> raw pointers, the current CUDA stream); every step
-of the path runs in the library's CUDA kernels.  PyTorch provides device
+The calls keep their C names, check what a pointer cannot show (strides, types,
+devices, where a wrong one would be misread) and marshal arguments (torch
+tensors -> raw pointers, the current CUDA stream); every step of the path runs
+in the library's CUDA kernels.  PyTorch provides device
 memory, pinned host memory and streams.  There is no CPU fallback: if the
 library is missing or no GPU is present the calls raise.
 
