@@ -81,10 +81,7 @@ class DecodeRunner:
         # one LRU state for all layers (the first layer's), each miss copied
         # for every layer; layer-batched steps only
         self.shared_residency = bool(shared_residency)
-        if shared_residency and host_tier:
-            # the other layers' state stays unbound (what the page calls go by)
-            for t in (self.cache.slot_of, self.cache.page_of):
-                t[1:].fill_(-1)
+        self._shared_state = False       # a step has taken that state into use
         # misses fetched inside the attention (ssa_ensure_remap_deferred +
         # ssa_sparse_paged_decode_fetch) instead of by a copy before it
         self.fetch_in_attention = bool(fetch_in_attention) and host_tier
@@ -137,7 +134,7 @@ class DecodeRunner:
         # with shared residency a page's slot is that of layer 0 in every layer:
         # the other layers' rows say so while the store reads them
         rows = None
-        if self.shared_residency and self.host_tier:
+        if self._shared_state:
             rows = self.cache.slot_of[max(layer0, 1):layer0 + n_layers]
             rows.copy_(self.cache.slot_of[:1].expand_as(rows))
         ssa_store_kv_mirror(self.cache, layer0, n_layers, k.contiguous(), v.contiguous(), pos,
@@ -202,6 +199,12 @@ class DecodeRunner:
                        self.n_sel[sl], self.scores[sl] if keep_scores else None, self.status,
                        self.ws)
         if fused and self.shared_residency:
+            if self.host_tier and not self._shared_state:
+                # from here on the other layers' state is unbound (what the page
+                # calls go by); with steps that go by each layer's it stays
+                for t in (c.slot_of, c.page_of):
+                    t[1:].fill_(-1)
+                self._shared_state = True
             ssa_ensure_remap_shared(c, layer0, n_layers, self.sel[sl], self.block_table,
                                     self.phys[sl], self.miss_page[sl], self.miss_slot[sl],
                                     self.n_miss[sl], self.status, self.ws)

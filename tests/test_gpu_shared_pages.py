@@ -85,3 +85,40 @@ def test_shared_residency_in_a_serving_loop(fmt, identity, by_layer):
     step()
     ref = runs[0].table.ref
     assert torch.equal(ref, runs[1].table.ref) and int(ref.sum()) > 0
+
+
+@pytest.mark.parametrize("form", ["per_layer", "preload"])
+@pytest.mark.parametrize("identity", [False, True])
+def test_steps_by_each_layers_state_keep_it(form, identity):
+    """A runner made for shared residency whose steps go by each layer's own state (per-layer steps, preload):
+    its stores do too, over an evicting pool."""
+    import sparse_attention_decode_indexer_gb300 as ssa
+    from sparse_attention_decode_indexer_gb300.runner import DecodeRunner
+    P, Hq, Hkv, L, B, nmax, k = 16, 4, 2, 3, 2, 16, 1
+    lay = ssa.Layout(P, Hq, Hkv, 128, True, L, B * nmax, 20, B, nmax, k, kv_format="int8_page_head")
+    bt = np.arange(B * nmax, dtype=np.int32).reshape(B, nmax)
+    lens = np.array([nmax * P - 9, 7 * P + 5], np.int32)
+    runs = [DecodeRunner(lay, host_tier=True, identity=identity, block_table=bt, seq_lens=lens,
+                         shared_residency=shared, preload_width=3 if form == "preload" else 0)
+            for shared in (True, False)]
+    g = torch.Generator().manual_seed(4)
+
+    def store(pos):
+        x = torch.randn((2, L, len(pos), Hkv, 128), generator=g).bfloat16().cuda()
+        for run in runs:
+            run.store(0, L, x[0], x[1], torch.tensor(pos, device="cuda"))
+    store([r * nmax * P + i for r in range(B) for i in range(lens[r])])
+    for t in range(8):
+        q = torch.randn((L, B, Hq, 128), generator=g).bfloat16().cuda()
+        for run in runs:
+            run.step(q, per_layer=form == "per_layer")
+        torch.cuda.synchronize()
+        a, b = runs
+        assert int(a.status.item()) == int(b.status.item()) == 0
+        assert torch.equal(a.out, b.out)
+        for n in ("slot_of", "page_of", "last_use", "k_pool", "v_pool", "k_scale", "v_scale"):
+            assert torch.equal(getattr(a.cache, n), getattr(b.cache, n)), n
+        for run in runs:
+            run.seq_lens += 1
+        store([int(r * nmax * P + n) for r, n in enumerate(lens)])
+        lens += 1
