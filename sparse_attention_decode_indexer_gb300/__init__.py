@@ -305,19 +305,19 @@ def ssa_lru_init(cache: KVCache, identity: bool, stream=None):
                               _stream(stream)))
 
 
-_BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
-_INT64 = torch.int64
+_BF16, _INT64 = torch.bfloat16, torch.int64
 
 
 def ssa_store_kv_mirror(cache: KVCache, layer0: int, n_layers: int, k, v, pos, status,
                         stream=None):
-    """k, v: bf16 (or its bits) [n_layers][T][Hkv][D]; pos: int64 [T] logical
-    token ids; all contiguous."""
+    """k, v: bf16 [n_layers][T][Hkv][D] (or its bits in an integer type); pos:
+    int64 [T] logical token ids; all contiguous."""
     T = pos.shape[0]
     n = n_layers * T * cache._row
     if not (k.is_contiguous() and v.is_contiguous() and pos.is_contiguous() and
-            k.dtype in _BF16_BITS and v.dtype in _BF16_BITS and pos.dtype is _INT64 and
-            k.numel() >= n and v.numel() >= n):
+            (k.dtype is _BF16 or not k.is_floating_point()) and
+            (v.dtype is _BF16 or not v.is_floating_point()) and pos.dtype is _INT64 and
+            k.nbytes >= 2 * n and v.nbytes >= 2 * n):
         got = ", ".join(f"{name} {tuple(x.shape)} {x.dtype} strides {x.stride()}"
                         for name, x in (("k", k), ("v", v), ("pos", pos)))
         raise ValueError("k, v: contiguous bfloat16 [n_layers][T][Hkv][D], pos: contiguous int64 "

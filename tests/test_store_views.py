@@ -45,3 +45,18 @@ def test_a_runner_stores_views(fmt, rope):
     for n in ("k_pool", "v_pool", "k_scale", "v_scale", "slab", "slab_sum", "slab_cnt"):
         if getattr(a, n) is not None:
             assert torch.equal(getattr(a, n), getattr(b, n)), n
+
+
+@pytest.mark.gpu
+def test_bits_of_another_type_are_the_same_input():
+    k, v = (torch.randn((L, T, H, D), generator=torch.Generator().manual_seed(i)).bfloat16().cuda() for i in (1, 2))
+    pos = torch.arange(T, device="cuda")
+    caches = []
+    for bits in (torch.bfloat16, torch.int16, torch.uint8, torch.int32):
+        c, status = ssa.KVCache(_layout("int8_page_head"), False), torch.zeros((1,), dtype=torch.int32, device="cuda")
+        ssa.ssa_lru_init(c, True)
+        ssa.ssa_store_kv_mirror(c, 0, L, k.view(bits), v.view(bits), pos, status)
+        assert int(status.item()) == 0
+        caches.append(c)
+    for c in caches[1:]:
+        assert torch.equal(c.k_pool, caches[0].k_pool) and torch.equal(c.v_pool, caches[0].v_pool)
