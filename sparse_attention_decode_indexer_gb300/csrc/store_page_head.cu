@@ -31,8 +31,9 @@
 //   * other runs, a decode step's single tokens above all: a warp per head,
 //     four dimensions a lane, the heads of a run in one CTA, so that a run costs
 //     three dependent reads (position, state, scale).  16 rows of one 16-byte
-//     unit of V leave as units; single tokens touch every row of their block,
-//     so a large append is bound by the sectors it touches;
+//     unit of V leave as units; a single token writes one byte in every row of
+//     its block, 32-byte sectors that come to about half of a large append's
+//     time (1,000 tokens of 12 layers and 4 heads, 118 us);
 //   * whole pages with values that are not finite, or scales near the ends of
 //     fp32: 128 threads, one per dimension, plain division.
 #include <cuda_fp8.h>
@@ -95,7 +96,9 @@ __device__ __forceinline__ float value(uint8_t c) {
 
 // The codes already in a block of one tensor, again at the scale that grew by
 // 1 / ratio: from the pool's copy where there is one (the mirror's bytes are
-// the same), to both.
+// the same), to both.  (One unit in flight per thread: an append of 64 tokens,
+// 12 layers and 4 heads takes 25 us where 6 % of the blocks' scales grow and 48
+// where all do, against 7.7 without.)
 template <bool I8>
 __device__ __forceinline__ void rescale_block(uint8_t* mir, uint8_t* pool, int bytes, float ratio,
                                               int tid, int nthreads) {
