@@ -612,6 +612,51 @@ int ssa_rope_frequencies(int rotary_dim, double base, int scaling, double factor
                          double *attn_factor);
 
 /*
+ * Attention over whole prompts, on the way into the cache (the pages start from a
+ * filled cache; a model's prompt attends over itself first).  Sequences of
+ * different lengths lie one behind the other: sequence s has the query tokens
+ * [cu_q[s], cu_q[s + 1]) of q and the keys [cu_kv[s], cu_kv[s + 1]) of k and v.
+ * With Lq query tokens and Lk keys, query token i of a sequence and its head
+ * hq = h * G + g, G = Hq / Hkv:
+ *   out = sum_j w_j v_j[h],  w = softmax_j(sm_scale * q . k_j[h]),
+ *   over j <= i + Lk - Lq (causal: the query tokens are the last ones of the
+ *   keys' sequence, so keys that came before need not be passed as queries) or
+ *   over all j < Lk
+ *   lse = ln sum_j exp(sm_scale * q . k_j[h])
+ * A query token that sees no key gets zeros and lse -inf; tokens outside every
+ * sequence are left as they were.  What a row does not see has no part in it,
+ * infinities and NaN among it.
+ *   dtype     SSA_BF16 or SSA_F16, of q, k, v and out; scores, softmax and sums
+ *             in fp32, weights rounded to dtype
+ *   head_dim  128;  G at most 128
+ *   q, out    [n_q][Hq][128];  k, v [n_kv][Hkv][128], 16-byte aligned; element
+ *             strides of token and head, positive multiples of 8, so that
+ *             slices of a fused projection need no copy.  out must not overlap
+ *             the others.
+ *   cu_q, cu_kv  [n_seqs + 1] int32, device, ascending, within the tensors
+ *             (SSA_ST_BAD_POS otherwise; nothing outside the tensors is read
+ *             or written).  The same array where queries and keys are the same
+ *             tokens.
+ *   sm_scale  finite, not negative
+ *   lse_opt   [n_q][Hq] fp32 out, or NULL
+ *   ws        ssa_prompt_workspace_size() bytes, 16-byte aligned, not used by
+ *             another call at the same time; needs no clearing
+ * Where a call has few rows and many keys the keys are split over the machine
+ * and the parts joined in a fixed order: the same inputs give the same bits.
+ */
+typedef struct ssa_prompt_tensor {
+  void *data;
+  int heads;
+  int64_t stride[2];                     /* token, head */
+} ssa_prompt_tensor;
+size_t ssa_prompt_workspace_size(void);
+int ssa_prompt_attention(int dtype, int head_dim, int n_seqs, int n_q, int n_kv,
+                         const ssa_prompt_tensor *q, const ssa_prompt_tensor *k,
+                         const ssa_prompt_tensor *v, const ssa_prompt_tensor *out,
+                         const int32_t *cu_q, const int32_t *cu_kv, int causal, float sm_scale,
+                         float *lse_opt, int32_t *status, void *ws, ssa_stream_t stream);
+
+/*
  * ssa_index_topk without a workspace: the same indexer and top-k selection
  * (same arguments and results as ssa_index_topk, without scores_opt and ws),
  * for callers that cannot allocate device memory -- a plugin inside a host

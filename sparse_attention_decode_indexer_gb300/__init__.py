@@ -14,6 +14,7 @@ library is missing or no GPU is present the calls raise.
     ssa_sparse_paged_decode  attention over the selected pages
     ssa_prefetch_pages       top-k preload of the next step's likely pages
     ssa_rope                 rotary positions of queries and new keys
+    ssa_prompt_attention     attention over whole prompts, packed sequences
     ssa_copy_pages, ssa_fork_requests, ssa_compact_pages
                              owners of the pages: copy, fork / grow / free, compact
 """
@@ -48,7 +49,8 @@ EXPORTS = ("ssa_workspace_size", "ssa_lru_init", "ssa_store_kv_mirror", "ssa_ind
            "ssa_ensure_remap_shared", "ssa_ensure_remap_deferred",
            "ssa_sparse_paged_decode_fetch", "ssa_ensure_remap_bind", "ssa_fetch_misses",
            "ssa_rope", "ssa_rope_frequencies", "ssa_page_refs", "ssa_copy_pages",
-           "ssa_fork_requests", "ssa_compact_pages")
+           "ssa_fork_requests", "ssa_compact_pages", "ssa_prompt_workspace_size",
+           "ssa_prompt_attention")
 
 
 class SsaError(RuntimeError):
@@ -80,6 +82,12 @@ class SsaRopeTensor(ctypes.Structure):
                 ("in_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3)]
 
 
+class SsaPromptTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("stride", ctypes.c_int64 * 2)]
+
+
+_pack_prompt = struct.Struct("@Pi4x2q").pack    # an SsaPromptTensor's bytes
 _pack_rope = struct.Struct("@PPi4x6q").pack     # an SsaRopeTensor's bytes
 
 
@@ -156,6 +164,10 @@ def lib():
         L.ssa_fork_requests.argtypes = [P(SsaLayout), P(SsaCache), R, vp, vp, vp, vp, vp]
         L.ssa_compact_pages.restype = i32
         L.ssa_compact_pages.argtypes = [P(SsaLayout), P(SsaCache), R, vp, vp, vp, vp, vp, vp]
+        L.ssa_prompt_workspace_size.restype = ctypes.c_size_t
+        L.ssa_prompt_workspace_size.argtypes = []
+        L.ssa_prompt_attention.restype = i32
+        L.ssa_prompt_attention.argtypes = ([i32] * 5 + [vp] * 6 + [i32, ctypes.c_float] + [vp] * 4)
         _lib = L
     return _lib
 
@@ -652,6 +664,71 @@ def ssa_rope(plan: RopePlan, positions, q=None, k=None, q_out=None, k_out=None, 
     _check(lib().ssa_rope(dtype, plan.head_dim, plan.rotary_dim, plan.interleaved, inverse,
                           plan._freq, plan.factor, n_layers, T, positions.data_ptr(), wide,
                           offset, cq, ck, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# attention over whole prompts
+# ---------------------------------------------------------------------------
+
+_PROMPT_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def ssa_prompt_workspace_size() -> int:
+    """Bytes of scratch of ssa_prompt_attention, whatever the call's sizes."""
+    return int(lib().ssa_prompt_workspace_size())
+
+
+def _prompt_tensor(name, x, n, dtype, dev):
+    """The C view of q, k, v or out: [n][heads][D], any strides but the last."""
+    got = x.shape
+    if len(got) != 3 or (n is not None and got[0] != n) or x.dtype != dtype or x.get_device() != dev:
+        raise ValueError(f"{name}: [tokens][heads][D] of q's type and device, k's tokens as v's and "
+                         f"q's as out's, got {tuple(got)} {x.dtype} on {x.device}")
+    st = x.stride()
+    if st[2] != 1 and x.numel():
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    return _pack_prompt(x.data_ptr(), got[1], st[0], st[1])
+
+
+def ssa_prompt_attention(q, k, v, cu_q, out, status, ws, cu_k=None, causal: bool = True,
+                         sm_scale: float | None = None, lse=None, stream=None):
+    """Attention over packed sequences of different lengths: q [Tq][Hq][D] over
+    k, v [Tk][Hkv][D] into out [Tq][Hq][D], strided views allowed.  Sequence s
+    has the query tokens cu_q[s] .. cu_q[s + 1] and the keys cu_k[s] ..
+    cu_k[s + 1] (default: cu_q), int32 on the device; with ``causal`` its query
+    tokens are the last ones of its keys.  sm_scale: default 1 / sqrt(D).  lse:
+    fp32 [Tq][Hq], the logarithm of each row's sum.  ws: at least
+    ssa_prompt_workspace_size() bytes."""
+    dtype, dev = _PROMPT_DTYPES.get(q.dtype), q.get_device()
+    if dtype is None:
+        raise ValueError(f"q, k, v: bfloat16 or float16, got {q.dtype}")
+    tq = _prompt_tensor("q", q, None, q.dtype, dev)
+    tk = _prompt_tensor("k", k, None, q.dtype, dev)
+    tv = _prompt_tensor("v", v, k.shape[0], q.dtype, dev)
+    to = _prompt_tensor("out", out, q.shape[0], q.dtype, dev)
+    n_q, heads, D = q.shape
+    if k.shape[2] != D or v.shape[1:] != k.shape[1:] or out.shape != q.shape:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, out "
+                         f"{tuple(out.shape)}: one head size, k and v alike, q and out alike")
+    if cu_k is None:
+        cu_k = cu_q
+    n = cu_q.numel()
+    pq, pk = _ints("cu_q", cu_q, n, dev), _ints("cu_k", cu_k, n, dev)
+    if n < 1:
+        raise ValueError("cu_q: the first token of each sequence, and the end of the last")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n_q, heads) or
+                            not lse.is_contiguous() or lse.get_device() != dev):
+        raise ValueError(f"lse: contiguous float32 [{n_q}][{heads}] on q's device")
+    if status is not None:
+        _ints("status", status, 1, dev)
+    if ws.get_device() != dev or ws.nbytes < lib().ssa_prompt_workspace_size() or not ws.is_contiguous():
+        raise ValueError("ws: ssa_prompt_workspace_size() contiguous bytes on q's device")
+    _on_current_device(dev)
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(D)
+    _check(lib().ssa_prompt_attention(dtype, D, n - 1, n_q, k.shape[0], tq, tk, tv, to, pq, pk,
+                                      causal, sm_scale, _ptr(lse), _ptr(status), ws.data_ptr(),
+                                      _stream(stream)))
 
 
 def ssa_selftest_bounded_wait(status, stream=None):

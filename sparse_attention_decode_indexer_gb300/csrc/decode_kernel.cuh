@@ -76,8 +76,6 @@
 // enough; the fp8 consumers' issue and ALU work limit the rest.
 #pragma once
 
-#include <cudaTypedefs.h>
-#include <cuda.h>
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -85,6 +83,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "tmap.cuh"
 
 namespace ssa {
 namespace {
@@ -1393,19 +1392,6 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    cudaDriverEntryPointQueryResult q;
-    void* ptr = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                         cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
-
 bool make_tmap(CUtensorMap* tm, void* base, CUtensorMapDataType dt, int esz, uint64_t inner,
                uint64_t rows, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw) {
   auto fn = encode_fn();

@@ -1,0 +1,597 @@
+// prompt.cu -- attention over whole prompts: packed sequences, grouped heads.
+//
+// For query token i of a sequence of Lq query tokens and Lk keys, and query
+// head hq = h * G + g,
+//   out = sum_j w_j v_j,  w = softmax_j(scale q . k_j),  j <= i + Lk - Lq
+// (causal) or all j < Lk; zeros where no key is seen.
+//
+// What bounds it: the two products, 4 * 128 flop per pair of query row and
+// key, on the tensor cores; the exponentials (one per pair) come next.  Work:
+//   * A row is a (token, head of the group) pair, so that the G heads that
+//     share K and V share every byte of them that is loaded.  A CTA owns two
+//     tiles of up to 128 rows (128 / G tokens each) and walks over the keys in
+//     blocks of 128.
+//   * The packed token axis is cut into tiles wherever sequences begin or end;
+//     each row knows the range [lo, hi) of packed keys that it sees (one
+//     binary search in the sequence table).  The keys that a tile's rows see
+//     lie next to one another, so a tile walks from the least lo to the
+//     greatest hi; scores outside a row's range are set to -inf.
+//   * S = Q K^T and O += P V are tcgen05 MMAs of 128 x 128 with accumulators
+//     in tensor memory: S0, S1, O0, O1, 128 columns each; P, rounded to the
+//     type of V, lies over its S.  The MMAs of one tile run while the other
+//     tile's warps (a thread per row, 128 scores in registers) take its
+//     exponentials.
+//   * Softmax in one pass against a lazy reference: the maximum that p is taken
+//     against moves only when a score exceeds it by 8 octaves; then the row's O
+//     is rescaled in tensor memory.  Sums and references are fp32; P in 16 bits
+//     is off by half a step of its type, as the inputs are.
+//   * Masked scores give p = 0, and 0 times an infinite or NaN v would still
+//     be NaN.  Two spare warps look through the V of those blocks that some
+//     row does not see all of, and set what is not finite to zero; the epilogue
+//     then adds it for the rows that do see it.
+//   * Few rows and many keys: the key blocks of a tile are split over several
+//     CTAs; their unnormalised outputs are joined by a second kernel.
+#include <algorithm>
+#include <cfloat>
+#include <climits>
+#include <type_traits>
+
+#include "internal.h"
+#include "tc5.cuh"
+#include "tmap.cuh"
+
+namespace ssa {
+namespace {
+
+constexpr int kD = 128;                   // head size
+constexpr int kRows = 128;                // rows of a tile
+constexpr int kBlk = 128;                 // keys of a block
+constexpr int kThreads = 384;             // 8 softmax warps, TMA, MMA, 2 that look over V
+constexpr int kStages = 5;                // K and V blocks in flight
+constexpr int kHalf = kRows * 128;        // bytes of 64 of the 128 dimensions
+constexpr int kTile = 2 * kHalf;
+constexpr float kLazy = 8.0f;             // octaves
+
+struct Shared {                           // behind the tiles
+  uint64_t full[kStages], empty[kStages];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t go, clean, drain;
+  uint32_t tmem;
+  int abort, dirty;
+  int lo_min, hi_max;                     // keys that any row sees
+  int lo_max, hi_min;                     // keys that every row sees
+  int t_lo[2], t_hi[2];                   // keys that any row of a tile sees
+};
+constexpr size_t kSmem = 1024 + (size_t)(2 + kStages) * kTile + sizeof(Shared);
+
+struct Params {
+  const int32_t *cu_q, *cu_k;
+  int n_seqs, Tq, Tk, Hq, Hkv, G, tpt;    // tpt: tokens of a tile
+  int n_pairs, n_split, causal;
+  float scale_log2;
+  int64_t v_tok, v_head, o_tok, o_head;   // strides in elements
+  const void* v;
+  void* out;
+  float* lse;
+  float *part_o, *part_ml;                // [pair][head][split][2 * kRows][kD], [..][2]
+  int32_t* status;
+};
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tm, uint64_t* bar, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+               " [%0], [%1, {%2, %3, %4}], [%5];"
+               ::"r"(smem_u32(dst)), "l"(tm), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tm, uint64_t* bar, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+               " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+               ::"r"(smem_u32(dst)), "l"(tm), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)) : "memory");
+}
+
+template <typename T> __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (std::is_same_v<T, __half>) return pack_f16(lo, hi);
+  else return pack_bf16(lo, hi);
+}
+template <typename T> __device__ __forceinline__ float to_f32(T x) {
+  if constexpr (std::is_same_v<T, __half>) return __half2float(x);
+  else return __bfloat162float(x);
+}
+
+// The range of packed keys that query token `tok` sees.  False where no
+// sequence holds it.
+__device__ __forceinline__ bool row_keys(const Params& p, int tok, int& lo, int& hi) {
+  lo = hi = 0;
+  int a = 0, b = p.n_seqs + 1;            // cu_q[a - 1] <= tok < cu_q[b]
+  while (a < b) {
+    const int m = (a + b) >> 1;
+    if (p.cu_q[m] <= tok) a = m + 1;
+    else b = m;
+  }
+  if (a == 0 || a > p.n_seqs) return false;
+  const int q0 = p.cu_q[a - 1], q1 = p.cu_q[a];
+  lo = min(max(p.cu_k[a - 1], 0), p.Tk);
+  hi = min(max(p.cu_k[a], lo), p.Tk);
+  if (p.causal) hi = (int)max((long long)lo, (long long)hi - (q1 - 1 - tok));
+  return true;
+}
+
+// True where one of a word's two elements is infinite or NaN.
+template <typename T> __device__ __forceinline__ uint32_t finite_part(uint32_t w) {
+  constexpr uint32_t e = std::is_same_v<T, __half> ? 0x7C00u : 0x7F80u;
+  if ((w & e) == e) w &= 0xFFFF0000u;
+  if ((w & e << 16) == e << 16) w &= 0x0000FFFFu;
+  return w;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+              const __grid_constant__ CUtensorMap tm_v) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* s_q = base;
+  uint8_t* s_kv = base + 2 * kTile;
+  Shared& sh = *reinterpret_cast<Shared*>(base + (2 + kStages) * kTile);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr bool BF = !std::is_same_v<T, __half>;
+
+  const int id = blockIdx.x, split = id % p.n_split, rest = id / p.n_split;
+  const int head = rest % p.Hkv, pair = p.n_pairs - 1 - rest / p.Hkv;   // the longest rows first
+  const int tok0 = pair * 2 * p.tpt;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 1); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 1); mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], kRows); mbar_init(&sh.o_full[i], 1);
+      sh.t_lo[i] = INT_MAX; sh.t_hi[i] = 0;
+    }
+    mbar_init(&sh.go, 1); mbar_init(&sh.clean, 64); mbar_init(&sh.drain, 1);
+    sh.abort = sh.dirty = 0;
+    sh.lo_min = sh.hi_min = INT_MAX;
+    sh.hi_max = sh.lo_max = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) tmem_alloc_all(&sh.tmem);
+  if (threadIdx.x == 256) { prefetch_tmap(&tm_q); prefetch_tmap(&tm_k); prefetch_tmap(&tm_v); }
+  pdl_trigger();
+  pdl_wait();
+  __syncthreads();
+
+  // rows: threads 0..127 tile 0, 128..255 tile 1
+  const int tile = (threadIdx.x >> 7) & 1, r = threadIdx.x & 127;
+  const int tok = tok0 + tile * p.tpt + r / p.G;
+  int lo = 0, hi = 0;
+  bool in_seq = false;
+  if (threadIdx.x < 256) {
+    in_seq = r < p.tpt * p.G && tok < p.Tq && row_keys(p, tok, lo, hi);
+    if (lo < hi) {
+      atomicMin(&sh.lo_min, lo); atomicMax(&sh.hi_max, hi);
+      atomicMax(&sh.lo_max, lo); atomicMin(&sh.hi_min, hi);
+      atomicMin(&sh.t_lo[tile], lo); atomicMax(&sh.t_hi[tile], hi);
+    }
+  } else if (id == 0) {                   // the tables themselves: ascending, inside the tensors
+    bool bad = false;
+    for (int i = threadIdx.x - 256; i <= p.n_seqs; i += 128) {
+      const int a = p.cu_q[i], b = p.cu_k[i];
+      bad = bad || a < (i ? p.cu_q[i - 1] : 0) || b < (i ? p.cu_k[i - 1] : 0) || a > p.Tq || b > p.Tk;
+    }
+    if (bad) set_status(p.status, SSA_ST_BAD_POS);
+  }
+  tc5_fence_before();
+  __syncthreads();
+  tc5_fence_after();
+
+  // blocks of this CTA, and of each tile in it
+  const int x0 = sh.lo_min;
+  const int nb = sh.hi_max > 0 ? (sh.hi_max - x0 + kBlk - 1) / kBlk : 0;
+  const int b0 = (int)((long long)nb * split / p.n_split), b1 = (int)((long long)nb * (split + 1) / p.n_split);
+  int tb0[2], tb1[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    tb0[t] = tb1[t] = b1;
+    if (sh.t_hi[t] > 0) {
+      tb0[t] = max(b0, (sh.t_lo[t] - x0) / kBlk);
+      tb1[t] = min(b1, (sh.t_hi[t] - x0 + kBlk - 1) / kBlk);
+      if (tb1[t] < tb0[t]) tb1[t] = tb0[t];
+    }
+  }
+  // some row does not see all of block i
+  const auto ragged = [&](int i) { return x0 + i * kBlk < sh.lo_max || x0 + (i + 1) * kBlk > sh.hi_min; };
+  const uint32_t tmem = sh.tmem;
+  volatile int* abort = &sh.abort;
+  const auto give_up = [&](int bits) { sh.abort = 1; set_status(p.status, bits); };
+
+  if (warp == 8 && lane == 0) {
+    // ---- loads ----
+    const uint32_t q_bytes = 2u * 128u * p.G * p.tpt;
+    for (int t = 0; t < 2; ++t)
+      if (tb0[t] < tb1[t]) {
+        mbar_arrive_expect_tx(&sh.q_full[t], q_bytes);
+        for (int h = 0; h < 2; ++h)
+          tma_load_4d(s_q + t * kTile + h * kHalf, &tm_q, &sh.q_full[t], h * 64, 0, head, tok0 + t * p.tpt);
+      }
+    int it = 0;
+    bool ok = true;
+    for (int i = b0; ok && i < b1; ++i)
+      for (int v = 0; ok && v < 2; ++v, ++it) {
+        const int st = it % kStages, use = it / kStages;
+        if (use > 0 && !mbar_wait(&sh.empty[st], (use - 1) & 1, abort)) { give_up(SSA_ST_TIMEOUT); ok = false; break; }
+        mbar_arrive_expect_tx(&sh.full[st], kTile);
+        for (int h = 0; h < 2; ++h)
+          tma_load_3d(s_kv + st * kTile + h * kHalf, v ? (const void*)&tm_v : (const void*)&tm_k, &sh.full[st],
+                      h * 64, head, x0 + i * kBlk);
+      }
+    if (*abort) {                         // copies in flight land before the CTA goes
+      for (int t = 0; t < 2; ++t)
+        if (tb0[t] < tb1[t]) mbar_wait(&sh.q_full[t], 0, nullptr);
+      for (int j = max(0, it - kStages); j < it; ++j)
+        mbar_wait(&sh.full[j % kStages], (j / kStages) & 1, nullptr);
+    }
+  } else if (warp == 9 && lane == 0) {
+    // ---- MMAs ----
+    constexpr uint32_t id_qk = tc5_idesc(BF, kBlk, false), id_pv = tc5_idesc(BF, kD, true);
+    const uint32_t a_q = smem_u32(s_q), a_kv = smem_u32(s_kv);
+    bool ok = true;
+    int n_ragged = 0;
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok && !mbar_wait(bar, parity, abort)) { give_up(SSA_ST_TIMEOUT); ok = false; }
+    };
+    for (int t = 0; t < 2; ++t)
+      if (tb0[t] < tb1[t]) wait(&sh.q_full[t], 0);
+    for (int i = b0; ok && i <= b1; ++i) {
+      const int kk = 2 * (i - b0), vv = kk - 1;         // uses of the ring: K of i, V of i - 1
+      if (i < b1) wait(&sh.full[kk % kStages], (kk / kStages) & 1);
+      if (i > b0) {
+        wait(&sh.full[vv % kStages], (vv / kStages) & 1);
+        if (ragged(i - 1)) { wait(&sh.clean, n_ragged & 1); ++n_ragged; }
+      }
+      for (int t = 0; ok && t < 2; ++t) {
+        const uint32_t S = tmem + t * 128, O = tmem + 256 + t * 128;
+        if (i - 1 >= tb0[t] && i - 1 < tb1[t]) {
+          wait(&sh.p_full[t], (i - 1 - tb0[t]) & 1);
+          if (!ok) break;
+          tc5_fence_after();
+          const uint32_t v = a_kv + (vv % kStages) * kTile;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc5_mma_ta(O, S + k * 8, tc5_desc(v + k * 2048, kHalf, 1024), id_pv, i - 1 > tb0[t] || k > 0);
+          tc5_commit(&sh.o_full[t]);
+        }
+        if (i >= tb0[t] && i < tb1[t]) {
+          const uint32_t q = a_q + t * kTile, kb = a_kv + (kk % kStages) * kTile;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
+            tc5_mma(S, tc5_desc(q + off, 16, 1024), tc5_desc(kb + off, 16, 1024), id_qk, k > 0);
+          }
+          tc5_commit(&sh.s_full[t]);
+        }
+      }
+      if (!ok) break;
+      if (i > b0) tc5_commit(&sh.empty[vv % kStages]);
+      if (i < b1) {
+        tc5_commit(&sh.empty[kk % kStages]);
+        if (ragged(i)) {
+          wait(&sh.full[(kk + 1) % kStages], ((kk + 1) / kStages) & 1);
+          mbar_arrive(&sh.go);
+        }
+      }
+    }
+    tc5_commit(&sh.drain);                // no MMA is in flight when the CTA goes
+    mbar_wait(&sh.drain, 0, nullptr);
+  } else if (warp >= 10) {
+    // ---- V of the blocks that some row does not see all of ----
+    int n = 0;
+    for (int i = b0; i < b1; ++i) {
+      if (!ragged(i)) continue;
+      if (!mbar_wait(&sh.go, n & 1, abort)) { give_up(SSA_ST_TIMEOUT); break; }
+      // (the barrier has this phase until `clean` lets the block go)
+      const int use = 2 * (i - b0) + 1;
+      if (!mbar_wait(&sh.full[use % kStages], (use / kStages) & 1, abort)) { give_up(SSA_ST_TIMEOUT); break; }
+      ++n;
+      uint4* v = reinterpret_cast<uint4*>(s_kv + use % kStages * kTile);
+      bool found = false;
+      for (int j = threadIdx.x - 320; j < kTile / 16; j += 64) {
+        const uint4 w = v[j];
+        const uint4 f = make_uint4(finite_part<T>(w.x), finite_part<T>(w.y), finite_part<T>(w.z), finite_part<T>(w.w));
+        if (f.x != w.x || f.y != w.y || f.z != w.z || f.w != w.w) {
+          v[j] = f;
+          found = true;
+        }
+      }
+      if (found) {
+        sh.dirty = 1;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      mbar_arrive(&sh.clean);
+    }
+  } else if (warp < 8) {
+    // ---- softmax: a thread per row ----
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t S = tmem + tile * 128 + lanes, O = tmem + 256 + tile * 128 + lanes;
+    const bool live = lo < hi;
+    // a warp goes on together or not at all
+    const auto all = [&](bool got) {
+      const bool ok = __all_sync(~0u, got);
+      if (!ok) give_up(SSA_ST_TIMEOUT);
+      return ok;
+    };
+    float m = -INFINITY, l = 0.0f;
+    int n = 0;
+    bool ok = true;
+    for (int i = tb0[tile]; i < tb1[tile]; ++i, ++n) {
+      if (!all(mbar_wait(&sh.s_full[tile], n & 1, abort))) { ok = false; break; }
+      tc5_fence_after();
+      uint32_t s[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(s + 32 * c, S + 32 * c);
+      tmem_wait_ld();
+      const int x = x0 + i * kBlk;
+      if (__any_sync(~0u, live && (x < lo || x + kBlk > hi))) {
+        const uint32_t from = lo - x, len = hi - lo;
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if ((uint32_t)c - from >= len) s[c] = 0xFF800000u;
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+      const bool move = live && top > m + kLazy;
+      if (__any_sync(~0u, move)) {
+        const float a = move ? fast_exp2(m - top) : 1.0f;
+        if (move) m = top;
+        l *= a;
+        if (n > 0) {
+          if (!all(mbar_wait(&sh.o_full[tile], (n - 1) & 1, abort))) { ok = false; break; }
+          tc5_fence_after();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o, O + 32 * c);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
+            tmem_st32(O + 32 * c, o);
+          }
+        }
+      }
+      const float ref = m == -INFINITY ? 0.0f : m;
+      float sum[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float e0 = fast_exp2(fmaf(__uint_as_float(s[64 * c + 2 * j]), p.scale_log2, -ref));
+          const float e1 = fast_exp2(fmaf(__uint_as_float(s[64 * c + 2 * j + 1]), p.scale_log2, -ref));
+          sum[j & 3] += e0 + e1;
+          w[j] = pack16<T>(e0, e1);
+        }
+        tmem_st32(S + 32 * c, w);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      tc5_fence_before();
+      mbar_arrive(&sh.p_full[tile]);
+    }
+    // ---- epilogue ----
+    if (ok && n > 0) ok = all(mbar_wait(&sh.o_full[tile], (n - 1) & 1, abort));
+    if (ok) {
+      tc5_fence_after();
+      const bool seen = live && n > 0;
+      if (!live) { m = -INFINITY; l = 0.0f; }          // (a row without keys ran along)
+      const float inv = 1.0f / l;
+      const size_t row = (((size_t)pair * p.Hkv + head) * p.n_split + split) * (2 * kRows) + threadIdx.x;
+      const int hq = head * p.G + r % p.G;
+      if (p.n_split > 1) {
+        if (r < p.tpt * p.G && tok < p.Tq)
+          *reinterpret_cast<float2*>(p.part_ml + 2 * row) = make_float2(m, in_seq ? l : -1.0f);
+      } else if (in_seq && p.lse) {
+        p.lse[(size_t)tok * p.Hq + hq] = l != 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      }
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32(o, O + 32 * c);
+          tmem_wait_ld();
+        }
+        if (in_seq) {
+          if (!seen) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0;
+          }
+          if (seen && sh.dirty) {         // what was set to zero, for the rows that see it
+            const T* v = static_cast<const T*>(p.v) + head * p.v_head + 32 * c;
+            for (int x = max(lo, x0 + b0 * kBlk); x < min(hi, x0 + b1 * kBlk); ++x) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float e = to_f32<T>(v[(int64_t)x * p.v_tok + j]);
+                if (!isfinite(e)) o[j] = __float_as_uint(__uint_as_float(o[j]) + e);
+              }
+            }
+          }
+          if (p.n_split > 1) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + row * kD + 32 * c);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              dst[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                                   __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+          } else {
+            const float f = seen && l != 0.0f ? inv : 0.0f;
+            T* dst = static_cast<T*>(p.out) + tok * p.o_tok + hq * p.o_head + 32 * c;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack16<T>(__uint_as_float(o[8 * j + 2 * e]) * f, __uint_as_float(o[8 * j + 2 * e + 1]) * f);
+              reinterpret_cast<uint4*>(dst)[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+    tc5_fence_before();
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 9) {
+    tc5_fence_after();
+    tmem_free_all(tmem);
+  }
+}
+
+// out = sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - max m): a warp per row,
+// four dimensions a lane, the splits in order.
+template <typename T>
+__global__ void __launch_bounds__(256) prompt_join_kernel(const Params p) {
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int tok = (int)(i / p.Hq), hq = (int)(i % p.Hq);
+  if (tok >= p.Tq) return;
+  const int head = hq / p.G, pair = tok / (2 * p.tpt), in = tok % (2 * p.tpt);
+  const int r = in / p.tpt * kRows + in % p.tpt * p.G + hq % p.G;
+  const size_t row0 = ((size_t)pair * p.Hkv + head) * p.n_split * (2 * kRows) + r;
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  if (ml[row0].y < 0.0f) return;          // not a token of any sequence
+  float m = -INFINITY;
+  for (int s = lane; s < p.n_split; s += 32) m = fmaxf(m, ml[row0 + (size_t)s * 2 * kRows].x);
+  m = warp_max(m);
+  float l = 0.0f;
+  float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+  for (int s = 0; s < p.n_split; ++s) {
+    const size_t row = row0 + (size_t)s * 2 * kRows;
+    const float2 x = ml[row];
+    const float4 y = reinterpret_cast<const float4*>(p.part_o + row * kD)[lane];
+    if (x.y == 0.0f) continue;            // saw no key
+    const float w = fast_exp2(x.x - m);
+    l += w * x.y;
+    o.x += w * y.x; o.y += w * y.y; o.z += w * y.z; o.w += w * y.w;
+  }
+  const float f = l != 0.0f ? 1.0f / l : 0.0f;
+  T* dst = static_cast<T*>(p.out) + tok * p.o_tok + hq * p.o_head + 4 * lane;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<T>(o.x * f, o.y * f), pack16<T>(o.z * f, o.w * f));
+  if (p.lse && lane == 0)
+    p.lse[(size_t)tok * p.Hq + hq] = l != 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// One of k and v, [tokens][heads][128] with any strides: 128 tokens of one head.
+bool map_kv(CUtensorMap* tm, const ssa_prompt_tensor& x, int n, bool bf) {
+  cuuint64_t dims[3] = {kD, (cuuint64_t)x.heads, (cuuint64_t)n};
+  cuuint64_t str[2] = {(cuuint64_t)(x.heads > 1 ? x.stride[1] : kD) * 2, (cuuint64_t)(n > 1 ? x.stride[0] : kD) * 2};
+  cuuint32_t box[3] = {64, 1, kBlk}, one[3] = {1, 1, 1};
+  auto fn = encode_fn();
+  return fn && fn(tm, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, x.data, dims, str,
+                  box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// q as [tokens][KV heads][G][128]: a tile's tokens of one KV head.
+bool map_q(CUtensorMap* tm, const ssa_prompt_tensor& x, int n, int Hkv, int tpt, bool bf) {
+  const int G = x.heads / Hkv;
+  const cuuint64_t hs = (cuuint64_t)(x.heads > 1 ? x.stride[1] : kD) * 2;
+  cuuint64_t dims[4] = {kD, (cuuint64_t)G, (cuuint64_t)Hkv, (cuuint64_t)n};
+  cuuint64_t str[3] = {hs, hs * G, (cuuint64_t)(n > 1 ? x.stride[0] : kD) * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)tpt}, one[4] = {1, 1, 1, 1};
+  auto fn = encode_fn();
+  return fn && fn(tm, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, x.data, dims, str,
+                  box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T>
+cudaError_t launch_prompt(const Params& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                          cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  const long long n = (long long)p.n_pairs * p.Hkv * p.n_split;
+  if (n > INT_MAX) return cudaErrorInvalidValue;
+  e = launch_pdl(prompt_kernel<T>, dim3((unsigned)n), dim3(kThreads), kSmem, s, p, q, k, v);
+  count_launch();
+  if (e != cudaSuccess || p.n_split == 1) return e;
+  const long long rows = (long long)p.Tq * p.Hq;
+  e = launch_pdl(prompt_join_kernel<T>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, p);
+  count_launch();
+  return e;
+}
+
+// Partial rows of one launch: a split launch has no more CTAs than SMs.
+size_t part_rows(int sms) { return (size_t)sms * 2 * kRows; }
+
+int check_tensor(const ssa_prompt_tensor* x, int n) {
+  if (!x || x->heads < 1) return SSA_ERR_INVALID_ARG;
+  if (n > 0 && (!x->data || ((uintptr_t)x->data & 15))) return SSA_ERR_INVALID_ARG;
+  const int size[2] = {n, x->heads};
+  for (int i = 0; i < 2; ++i)
+    if (size[i] > 1 && (x->stride[i] <= 0 || x->stride[i] % 8 || x->stride[i] >= 1ll << 38)) return SSA_ERR_INVALID_ARG;
+  return SSA_OK;
+}
+
+}  // namespace
+}  // namespace ssa
+
+extern "C" {
+
+size_t ssa_prompt_workspace_size(void) {
+  return ssa::part_rows(ssa::current_device_info().sms) * (ssa::kD + 2) * sizeof(float);
+}
+
+int ssa_prompt_attention(int dtype, int head_dim, int n_seqs, int n_q, int n_kv, const ssa_prompt_tensor* q,
+                         const ssa_prompt_tensor* k, const ssa_prompt_tensor* v, const ssa_prompt_tensor* out,
+                         const int32_t* cu_q, const int32_t* cu_kv, int causal, float sm_scale, float* lse_opt,
+                         int32_t* status, void* ws, ssa_stream_t stream) {
+  using namespace ssa;
+  if (dtype != SSA_BF16 && dtype != SSA_F16) return SSA_ERR_UNSUPPORTED;
+  if (head_dim != kD) return SSA_ERR_UNSUPPORTED;
+  if (n_seqs < 0 || n_q < 0 || n_kv < 0 || !cu_q || !cu_kv || !ws) return SSA_ERR_INVALID_ARG;
+  if (!(sm_scale >= 0.0f) || !(sm_scale < INFINITY)) return SSA_ERR_INVALID_ARG;
+  for (const ssa_prompt_tensor* x : {q, k, v, out})
+    if (int e = check_tensor(x, x == q || x == out ? n_q : n_kv)) return e;
+  if (k->heads != v->heads || q->heads != out->heads) return SSA_ERR_INVALID_ARG;
+  if (q->heads % k->heads || q->heads / k->heads > kRows) return SSA_ERR_UNSUPPORTED;
+  if ((uintptr_t)ws & 15) return SSA_ERR_INVALID_ARG;
+  if (n_q > INT_MAX / 2 || n_kv > INT_MAX / 2) return SSA_ERR_UNSUPPORTED;
+  if (n_q == 0 || n_seqs == 0) return SSA_OK;
+
+  Params p{};
+  p.cu_q = cu_q; p.cu_k = cu_kv;
+  p.n_seqs = n_seqs; p.Tq = n_q; p.Tk = n_kv;
+  p.Hq = q->heads; p.Hkv = k->heads; p.G = p.Hq / p.Hkv;
+  p.tpt = kRows / p.G;
+  p.n_pairs = (n_q + 2 * p.tpt - 1) / (2 * p.tpt);
+  p.causal = causal ? 1 : 0;
+  // not zero: masked scores are -inf, and stay so when scaled
+  p.scale_log2 = std::max(sm_scale * 1.4426950408889634f, FLT_MIN);
+  p.v = v->data; p.v_tok = v->stride[0]; p.v_head = v->stride[1];
+  p.out = out->data; p.o_tok = out->stride[0]; p.o_head = out->stride[1];
+  p.lse = lse_opt;
+  p.status = status;
+  const int sms = current_device_info().sms;
+  const long long units = (long long)p.n_pairs * p.Hkv;
+  // at least four blocks of keys to a split
+  const long long most = std::max(1, (n_kv + 4 * kBlk - 1) / (4 * kBlk));
+  p.n_split = (int)std::max(1ll, std::min(sms / units, most));
+  p.part_o = static_cast<float*>(ws);
+  p.part_ml = p.part_o + part_rows(sms) * kD;
+
+  const bool bf = dtype == SSA_BF16;
+  CUtensorMap mq, mk, mv;
+  // without keys nothing is loaded through these two
+  ssa_prompt_tensor none = *q;
+  none.heads = k->heads;
+  if (!map_q(&mq, *q, n_q, p.Hkv, p.tpt, bf) || !map_kv(&mk, n_kv ? *k : none, n_kv ? n_kv : 1, bf) ||
+      !map_kv(&mv, n_kv ? *v : none, n_kv ? n_kv : 1, bf))
+    return record_cuda_error(cudaErrorInvalidValue);
+  const cudaError_t e = bf ? launch_prompt<__nv_bfloat16>(p, mq, mk, mv, (cudaStream_t)stream)
+                           : launch_prompt<__half>(p, mq, mk, mv, (cudaStream_t)stream);
+  return e == cudaSuccess ? SSA_OK : record_cuda_error(e);
+}
+
+}  // extern "C"

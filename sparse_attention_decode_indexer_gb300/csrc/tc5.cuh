@@ -1,0 +1,82 @@
+// tc5.cuh -- the fifth-generation tensor cores (tcgen05) and their memory.
+//
+// One thread issues a 128-row MMA whose operands lie in shared memory (A may
+// lie in tensor memory) and whose fp32 accumulators lie in tensor memory, 128
+// lanes by 512 columns per SM.  Lane r of an accumulator is row r; a warp reads
+// and writes the 32 lanes of its rank modulo four.
+#pragma once
+
+#include "common.cuh"
+
+namespace ssa {
+
+// Takes all 512 columns; the address (0) goes to *dst.  One warp.
+__device__ __forceinline__ void tmem_alloc_all(uint32_t* dst) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
+               ::"r"(smem_u32(dst)) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free_all(uint32_t addr) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(addr));
+}
+
+__device__ __forceinline__ void tc5_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc5_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// The barrier gets one arrival when every MMA issued so far by this thread is done.
+__device__ __forceinline__ void tc5_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+               ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Shared-memory operand with the 128-byte swizzle, both strides in bytes.
+// K-major: rows of 64 16-bit elements, `sbo` between groups of 8 rows.
+// MN-major: `lbo` between groups of 64 elements, `sbo` between groups of 8 k.
+__device__ __forceinline__ uint64_t tc5_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 |
+         1ull << 46 | 2ull << 61;
+}
+// kind::f16, fp32 accumulators, 128 x N; b_mn: B is MN-major
+__host__ __device__ constexpr uint32_t tc5_idesc(bool bf16, int N, bool b_mn) {
+  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_mn ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 |
+         (uint32_t)(128 >> 4) << 24;
+}
+__device__ __forceinline__ void tc5_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
+__device__ __forceinline__ void tc5_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
+
+// 32 columns of this warp's lanes.
+#define SSA_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), \
+                     "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
+#define SSA_W8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), \
+                     "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
+__device__ __forceinline__ void tmem_ld32(uint32_t* x, uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+               "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : SSA_R8(x, 0), SSA_R8(x, 8), SSA_R8(x, 16), SSA_R8(x, 24) : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+               "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+               ::SSA_W8(x, 0), SSA_W8(x, 8), SSA_W8(x, 16), SSA_W8(x, 24), "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+}  // namespace ssa
