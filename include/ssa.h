@@ -590,6 +590,23 @@ int ssa_rope(int dtype, int head_dim, int rotary_dim, int interleaved, int inver
              const ssa_rope_tensor *k, ssa_stream_t stream);
 
 /*
+ * Norms of queries and keys, head by head, and their rotary positions in one
+ * pass (models that norm q and k do so right before the rotation):
+ *   y = x / sqrt(mean(x^2) + eps) * w,  then ssa_rope's rotation of y
+ * over the head_dim elements of every (layer, token, head); in fp32, rounded
+ * once.  Arguments as for ssa_rope (no inverse), and
+ *   q_weight, k_weight  [n_layers][head_dim] fp32, device, weight_step floats
+ *             from one layer's to the next's (0: all layers share them); NULL:
+ *             ones
+ *   eps       finite, not negative
+ */
+int ssa_norm_rope(int dtype, int head_dim, int rotary_dim, int interleaved, const uint64_t *freq,
+                  float factor, int n_layers, int n_tokens, const void *pos, int pos_is_64,
+                  int64_t pos_offset, const ssa_rope_tensor *q, const ssa_rope_tensor *k,
+                  const float *q_weight, const float *k_weight, int64_t weight_step, float eps,
+                  ssa_stream_t stream);
+
+/*
  * The frequency table of ssa_rope, on the host: theta_i = base^(-2i /
  * rotary_dim), changed for contexts longer than the model was trained on:
  *   PLAIN   as it is

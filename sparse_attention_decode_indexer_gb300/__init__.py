@@ -14,6 +14,7 @@ library is missing or no GPU is present the calls raise.
     ssa_sparse_paged_decode  attention over the selected pages
     ssa_prefetch_pages       top-k preload of the next step's likely pages
     ssa_rope                 rotary positions of queries and new keys
+    ssa_norm_rope            the same with the heads' norms in front
     ssa_prompt_attention     attention over whole prompts, packed sequences
     ssa_copy_pages, ssa_fork_requests, ssa_compact_pages
                              owners of the pages: copy, fork / grow / free, compact
@@ -49,7 +50,7 @@ EXPORTS = ("ssa_workspace_size", "ssa_lru_init", "ssa_store_kv_mirror", "ssa_ind
            "ssa_ensure_remap_shared", "ssa_ensure_remap_deferred",
            "ssa_sparse_paged_decode_fetch", "ssa_ensure_remap_bind", "ssa_fetch_misses",
            "ssa_rope", "ssa_rope_frequencies", "ssa_page_refs", "ssa_copy_pages",
-           "ssa_fork_requests", "ssa_compact_pages", "ssa_prompt_workspace_size",
+           "ssa_fork_requests", "ssa_compact_pages", "ssa_norm_rope", "ssa_prompt_workspace_size",
            "ssa_prompt_attention")
 
 
@@ -152,6 +153,10 @@ def lib():
         L.ssa_rope.restype = i32
         L.ssa_rope.argtypes = [i32, i32, i32, i32, i32, vp, ctypes.c_float, i32, i32, vp, i32,
                                ctypes.c_int64, vp, vp, vp]
+        L.ssa_norm_rope.restype = i32
+        L.ssa_norm_rope.argtypes = [i32, i32, i32, i32, vp, ctypes.c_float, i32, i32, vp, i32,
+                                    ctypes.c_int64, vp, vp, vp, vp, ctypes.c_int64,
+                                    ctypes.c_float, vp]
         L.ssa_rope_frequencies.restype = i32
         L.ssa_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64,
                                            P(ctypes.c_uint64), P(f64)]
@@ -633,12 +638,9 @@ def _rope_tensor(plan, name, x, out, shape):
                       so[0] if lead else 0, so[-3], so[-2])
 
 
-def ssa_rope(plan: RopePlan, positions, q=None, k=None, q_out=None, k_out=None, offset: int = 0,
-             inverse: bool = False, stream=None):
-    """Rotate q and k ([n_layers][T][heads][D] or [T][heads][D], strided views
-    allowed) by positions + offset ([T] int32 or int64), in place or into
-    q_out / k_out; one launch for both.  ``inverse`` turns back (the gradient
-    of the rotation)."""
+def _rope_args(plan, positions, q, k, q_out, k_out):
+    """Checked arguments of a call on q and k: type, layers, tokens, 64-bit
+    positions or not, the C views."""
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k")
@@ -657,13 +659,74 @@ def ssa_rope(plan: RopePlan, positions, q=None, k=None, q_out=None, k_out=None, 
     shape = (x.shape[0], T, 0, plan.head_dim) if x.dim() == 4 else (T, 0, plan.head_dim)
     cq = _rope_tensor(plan, "q", q, q_out, shape) if q is not None else None
     ck = _rope_tensor(plan, "k", k, k_out, shape) if k is not None else None
-    n_layers = shape[0] if len(shape) == 4 else 1
+    return dtype, shape[0] if len(shape) == 4 else 1, T, wide, cq, ck
+
+
+def ssa_rope(plan: RopePlan, positions, q=None, k=None, q_out=None, k_out=None, offset: int = 0,
+             inverse: bool = False, stream=None):
+    """Rotate q and k ([n_layers][T][heads][D] or [T][heads][D], strided views
+    allowed) by positions + offset ([T] int32 or int64), in place or into
+    q_out / k_out; one launch for both.  ``inverse`` turns back (the gradient
+    of the rotation)."""
+    dtype, n_layers, T, wide, cq, ck = _rope_args(plan, positions, q, k, q_out, k_out)
     if T == 0 or n_layers == 0:
         return
-    _on_current_device(dev)
+    _on_current_device(plan._dev)
     _check(lib().ssa_rope(dtype, plan.head_dim, plan.rotary_dim, plan.interleaved, inverse,
                           plan._freq, plan.factor, n_layers, T, positions.data_ptr(), wide,
                           offset, cq, ck, _stream(stream)))
+
+
+class HeadNorm:
+    """Norm of every head of q and k: x / sqrt(mean(x^2) + eps) * (weight + offset).
+
+    q_weight, k_weight: [D], or [n_layers][D] for a vector per layer, kept as
+    fp32 on the device; None: ones.  ``offset``: 1 for models whose weights are
+    kept about zero."""
+
+    def __init__(self, q_weight=None, k_weight=None, eps: float = 1e-6, offset: float = 0.0,
+                 device="cuda"):
+        ws = [None if w is None else
+              (torch.as_tensor(w).detach().to(device=device, dtype=torch.float32) + offset).contiguous()
+              for w in (q_weight, k_weight)]
+        shapes = {tuple(w.shape) for w in ws if w is not None}
+        if len(shapes) > 1 or any(len(x) not in (1, 2) for x in shapes):
+            raise ValueError("q_weight, k_weight: [D] or [n_layers][D], the same for both")
+        if not 0.0 <= eps < math.inf:
+            raise ValueError(f"eps {eps!r}: a finite number, not negative")
+        if offset and None in ws and shapes:
+            raise ValueError("offset: of both weights, so both of them or none")
+        self.q_weight, self.k_weight = ws
+        self.eps = float(eps)
+        shape = shapes.pop() if shapes else None
+        self.layers = shape[0] if shape and len(shape) == 2 else None     # None: shared by all
+        self.head_dim = shape[-1] if shape else None
+        self._ptr = [0 if w is None else w.data_ptr() for w in ws]
+        self._dev = next((w.get_device() for w in ws if w is not None), None)
+
+
+def ssa_norm_rope(plan: RopePlan, norm: HeadNorm, positions, q=None, k=None, q_out=None,
+                  k_out=None, offset: int = 0, layer0: int = 0, stream=None):
+    """ssa_rope with the heads' norms in front of the rotation, in the same
+    pass.  layer0: the layer of the first slice of q and k, where the norm has a
+    weight vector per layer."""
+    dtype, n_layers, T, wide, cq, ck = _rope_args(plan, positions, q, k, q_out, k_out)
+    D = plan.head_dim
+    if norm.head_dim not in (None, D) or norm._dev not in (None, plan._dev):
+        raise ValueError(f"norm: weights of {norm.head_dim} on device {norm._dev}, the plan's heads "
+                         f"are {D} on {plan._dev}")
+    step = 0
+    if norm.layers is not None:
+        if layer0 < 0 or layer0 + n_layers > norm.layers:
+            raise ValueError(f"layers {layer0} to {layer0 + n_layers} of a norm of {norm.layers}")
+        step = D
+    if T == 0 or n_layers == 0:
+        return
+    _on_current_device(plan._dev)
+    wq, wk = (w and w + 4 * step * layer0 for w in norm._ptr)
+    _check(lib().ssa_norm_rope(dtype, D, plan.rotary_dim, plan.interleaved, plan._freq,
+                               plan.factor, n_layers, T, positions.data_ptr(), wide, offset, cq,
+                               ck, wq, wk, step, norm.eps, _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

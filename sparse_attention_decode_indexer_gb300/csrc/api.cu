@@ -3,6 +3,7 @@
 // Every entry point validates its arguments on the host, then only enqueues
 // kernels on the caller's stream.  Nothing here synchronises, allocates or
 // keeps a pointer past the call.
+#include <cfloat>
 #include <climits>
 #include <cstdio>
 #include <cstring>
@@ -134,6 +135,55 @@ WsLayout ws_layout(const Dims& d) {
 template <typename T>
 T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
+}
+
+// The arguments that ssa_rope and ssa_norm_rope share, checked into a.
+int rope_args(int dtype, int head_dim, int rotary_dim, int interleaved, int inverse,
+              const uint64_t* freq, float factor, int n_layers, int n_tokens, const void* pos,
+              int pos_is_64, int64_t pos_offset, const ssa_rope_tensor* q, const ssa_rope_tensor* k,
+              RopeArgs& a) {
+  if (dtype < SSA_BF16 || dtype > SSA_F32) return SSA_ERR_UNSUPPORTED;
+  if (rotary_dim < 2 || rotary_dim % 2 || rotary_dim > head_dim) return SSA_ERR_INVALID_ARG;
+  if (rotary_dim > SSA_ROPE_MAX_DIM || head_dim > 16384) return SSA_ERR_UNSUPPORTED;
+  if (n_layers < 1 || n_tokens < 0 || (!q && !k)) return SSA_ERR_INVALID_ARG;
+  if (!freq || (n_tokens > 0 && !pos)) return SSA_ERR_INVALID_ARG;
+  const size_t esz = dtype == SSA_F32 ? 4 : 2;
+  for (const ssa_rope_tensor* t : {q, k}) {
+    if (!t) continue;
+    if (t->heads < 1 || t->heads > 65536) return SSA_ERR_INVALID_ARG;
+    if (n_tokens > 0 && (!t->in || !t->out)) return SSA_ERR_INVALID_ARG;
+    if ((((uintptr_t)t->in | (uintptr_t)t->out) & (esz - 1))) return SSA_ERR_INVALID_ARG;
+    RopeTensor& r = a.x[a.n_x++];
+    r.in = t->in;
+    r.out = t->out;
+    r.heads = t->heads;
+    for (int i = 0; i < 3; ++i) {
+      r.is[i] = t->in_stride[i];
+      r.os[i] = t->out_stride[i];
+      const int n = i == 0 ? n_layers : i == 1 ? n_tokens : t->heads;
+      // in place: the same element for input and output, so the same strides
+      if (t->in == t->out && n > 1 && r.is[i] != r.os[i]) return SSA_ERR_INVALID_ARG;
+      if (n > 1 && r.os[i] == 0) return SSA_ERR_INVALID_ARG;   // several results, one place
+    }
+  }
+  if (n_tokens == 0) return SSA_OK;
+  // both would turn, or write, the same elements, in no order
+  if (q && k && (q->out == k->out || q->out == k->in || k->out == q->in))
+    return SSA_ERR_INVALID_ARG;
+  a.dtype = dtype;
+  a.D = head_dim;
+  a.rd = rotary_dim;
+  a.interleaved = interleaved ? 1 : 0;
+  a.inverse = inverse ? 1 : 0;
+  a.n_layers = n_layers;
+  a.n_tokens = n_tokens;
+  a.pos64 = pos_is_64 ? 1 : 0;
+  a.num_sms = num_sms();
+  a.freq = freq;
+  a.pos = pos;
+  a.offset = pos_offset;
+  a.factor = factor;
+  return SSA_OK;
 }
 
 PageWs page_ws(const Dims& d, void* ws) {
@@ -566,49 +616,28 @@ int ssa_rope(int dtype, int head_dim, int rotary_dim, int interleaved, int inver
              const uint64_t* freq, float factor, int n_layers, int n_tokens, const void* pos,
              int pos_is_64, int64_t pos_offset, const ssa_rope_tensor* q,
              const ssa_rope_tensor* k, ssa_stream_t stream) {
-  if (dtype < SSA_BF16 || dtype > SSA_F32) return SSA_ERR_UNSUPPORTED;
-  if (rotary_dim < 2 || rotary_dim % 2 || rotary_dim > head_dim) return SSA_ERR_INVALID_ARG;
-  if (rotary_dim > SSA_ROPE_MAX_DIM || head_dim > 16384) return SSA_ERR_UNSUPPORTED;
-  if (n_layers < 1 || n_tokens < 0 || (!q && !k)) return SSA_ERR_INVALID_ARG;
-  if (!freq || (n_tokens > 0 && !pos)) return SSA_ERR_INVALID_ARG;
-  const size_t esz = dtype == SSA_F32 ? 4 : 2;
   RopeArgs a{};
-  for (const ssa_rope_tensor* t : {q, k}) {
-    if (!t) continue;
-    if (t->heads < 1 || t->heads > 65536) return SSA_ERR_INVALID_ARG;
-    if (n_tokens > 0 && (!t->in || !t->out)) return SSA_ERR_INVALID_ARG;
-    if ((((uintptr_t)t->in | (uintptr_t)t->out) & (esz - 1))) return SSA_ERR_INVALID_ARG;
-    RopeTensor& r = a.x[a.n_x++];
-    r.in = t->in;
-    r.out = t->out;
-    r.heads = t->heads;
-    for (int i = 0; i < 3; ++i) {
-      r.is[i] = t->in_stride[i];
-      r.os[i] = t->out_stride[i];
-      const int n = i == 0 ? n_layers : i == 1 ? n_tokens : t->heads;
-      // in place: the same element for input and output, so the same strides
-      if (t->in == t->out && n > 1 && r.is[i] != r.os[i]) return SSA_ERR_INVALID_ARG;
-      if (n > 1 && r.os[i] == 0) return SSA_ERR_INVALID_ARG;   // several results, one place
-    }
-  }
-  if (n_tokens == 0) return SSA_OK;
-  // both would turn, or write, the same elements, in no order
-  if (q && k && (q->out == k->out || q->out == k->in || k->out == q->in))
-    return SSA_ERR_INVALID_ARG;
-  a.dtype = dtype;
-  a.D = head_dim;
-  a.rd = rotary_dim;
-  a.interleaved = interleaved ? 1 : 0;
-  a.inverse = inverse ? 1 : 0;
-  a.n_layers = n_layers;
-  a.n_tokens = n_tokens;
-  a.pos64 = pos_is_64 ? 1 : 0;
-  a.num_sms = num_sms();
-  a.freq = freq;
-  a.pos = pos;
-  a.offset = pos_offset;
-  a.factor = factor;
+  const int r = rope_args(dtype, head_dim, rotary_dim, interleaved, inverse, freq, factor, n_layers,
+                          n_tokens, pos, pos_is_64, pos_offset, q, k, a);
+  if (r != SSA_OK || n_tokens == 0) return r;
   cudaError_t e = launch_rope(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? SSA_OK : fail_cuda(e);
+}
+
+int ssa_norm_rope(int dtype, int head_dim, int rotary_dim, int interleaved, const uint64_t* freq,
+                  float factor, int n_layers, int n_tokens, const void* pos, int pos_is_64,
+                  int64_t pos_offset, const ssa_rope_tensor* q, const ssa_rope_tensor* k,
+                  const float* q_weight, const float* k_weight, int64_t weight_step, float eps,
+                  ssa_stream_t stream) {
+  RopeArgs a{};
+  const int r = rope_args(dtype, head_dim, rotary_dim, interleaved, 0, freq, factor, n_layers,
+                          n_tokens, pos, pos_is_64, pos_offset, q, k, a);
+  if (r != SSA_OK) return r;
+  if (!(eps >= 0.0f) || !(eps <= FLT_MAX) || weight_step < 0) return SSA_ERR_INVALID_ARG;
+  if (((uintptr_t)q_weight | (uintptr_t)k_weight) & 3) return SSA_ERR_INVALID_ARG;
+  if (n_tokens == 0) return SSA_OK;
+  const float* w[2] = {q ? q_weight : k_weight, k_weight};
+  cudaError_t e = launch_norm_rope(a, w, weight_step, eps, (cudaStream_t)stream);
   return e == cudaSuccess ? SSA_OK : fail_cuda(e);
 }
 

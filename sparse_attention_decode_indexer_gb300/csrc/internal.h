@@ -164,6 +164,11 @@ struct RopeArgs {
   float factor;
 };
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+// -- norm_rope.cu ------------------------------------------------------------
+// w: the weights of a.x[i] (null: ones), w_step floats from layer to layer
+cudaError_t launch_norm_rope(const RopeArgs& a, const float* const* w, int64_t w_step, float eps,
+                             cudaStream_t s);
+// -- rope.cu -----------------------------------------------------------------
 int rope_frequencies(int rd, double base, int scaling, double factor, double original_len,
                      double low, double high, uint64_t* freq, double* attn_factor);
 

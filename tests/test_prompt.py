@@ -9,7 +9,8 @@ torch.finfo(t).eps / 2):
     above and once below the division; the exponential itself and its argument add less than
     2^-18 (score magnitudes below 2^4);
   * fp16 weights below 2^-14 have steps of 2^-24 beside a sum of at least one: 2^-25 |v| a key;
-  * the result's own rounding: u * |out|.
+  * the result's own rounding: u * |out|, or u times the least normal number where |out| is below
+    it and the steps get no smaller.
 """
 import ctypes
 import math
@@ -70,7 +71,7 @@ def reference(q, k, v, lq, lk, causal, scale=None):
             return o
         o = mix(w, vs)
         vabs = vs.abs().nan_to_num(0.0, 0.0, 0.0)
-        t = (u + 2 * e_s + 2.0 ** -18) * (w @ vabs) + u * o.abs()
+        t = (u + 2 * e_s + 2.0 ** -18) * (w @ vabs) + u * o.abs().clamp(min=torch.finfo(q.dtype).tiny)
         if q.dtype == F16:
             t = t + 2.0 ** -25 * m * vabs.amax()
         out[rows] = o.permute(2, 0, 1, 3).reshape(n, Hq, D)
