@@ -674,6 +674,50 @@ int ssa_prompt_attention(int dtype, int head_dim, int n_seqs, int n_q, int n_kv,
                          float *lse_opt, int32_t *status, void *ws, ssa_stream_t stream);
 
 /*
+ * The next tokens of beams, and what ssa_fork_requests needs to follow them
+ * (which pages a beam goes on with; the pages leave the choice to the engine).
+ * Groups of `beams` rows, rows g * beams .. of a batch, logits x[row][vocab]:
+ *   a candidate (row, t) has the score  scores[row] + x[row][t] - ln sum_t' exp(x[row][t'])
+ *   a finished row has one candidate, (row, eos), at scores[row]
+ *   logits of -infinity and NaN (a mask) are no candidates, nor is anything of a
+ *   row whose score is -infinity or NaN; +infinity counts as the largest float
+ * The `beams` best of each group, best first, equal scores by the lower row and
+ * then the lower token, become the group's rows; the best of several rows may
+ * be of one parent.  Sums and scores in double, one rounding to fp32 at the end.
+ *   dtype     SSA_BF16, SSA_F16 or SSA_F32, of the logits
+ *   logits    [groups * beams] rows, row_stride elements apart
+ *   beams     at most 32, beams * ceil(vocab / 8192) <= 1024 (SSA_ERR_UNSUPPORTED)
+ *   in, out   the rows' state before and after; out may be in:
+ *     scores    [groups * beams] fp32 (a first step: 0 for one row of a group
+ *               and -infinity for the others)
+ *     finished  [groups * beams] bytes, with eos >= 0; NULL without (eos = -1)
+ *     history   [groups * beams][max_len] int32, hist_len [groups] the tokens in
+ *               a row of it; both NULL with max_len = 0.  Rows are reordered
+ *               and the new token appended; where the row is full, or its
+ *               length not in [0, max_len], the token is not kept and
+ *               SSA_ST_BAD_POS set.  Nothing behind the new token is written.
+ *   parent    [groups * beams] int32 out: the row (of the batch) each continues,
+ *             -1 where the group has too few candidates: token -1, score
+ *             -infinity, not finished, its history left as it was
+ *   token     [groups * beams] int32 out
+ *   seq_lens_opt, new_lens_opt  [groups * beams] int32, both or none:
+ *             new_lens[row] = seq_lens[parent] + 1, 0 for parent -1, as
+ *             ssa_fork_requests takes them (may be the same array)
+ *   ws        ssa_beam_workspace_size(groups, beams) bytes, 256-byte aligned,
+ *             zeroed once, not used by another call at the same time
+ */
+typedef struct ssa_beams {
+  float *scores;
+  uint8_t *finished;
+  int32_t *history, *hist_len;
+} ssa_beams;
+size_t ssa_beam_workspace_size(int groups, int beams);
+int ssa_beam_select(int dtype, int groups, int beams, int vocab, const void *logits,
+                    int64_t row_stride, const ssa_beams *in, const ssa_beams *out, int max_len,
+                    int eos, int32_t *parent, int32_t *token, const int32_t *seq_lens_opt,
+                    int32_t *new_lens_opt, int32_t *status, void *ws, ssa_stream_t stream);
+
+/*
  * ssa_index_topk without a workspace: the same indexer and top-k selection
  * (same arguments and results as ssa_index_topk, without scores_opt and ws),
  * for callers that cannot allocate device memory -- a plugin inside a host

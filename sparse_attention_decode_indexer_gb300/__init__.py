@@ -16,6 +16,7 @@ library is missing or no GPU is present the calls raise.
     ssa_rope                 rotary positions of queries and new keys
     ssa_norm_rope            the same with the heads' norms in front
     ssa_prompt_attention     attention over whole prompts, packed sequences
+    ssa_beam_select          the next tokens of beams, their states reordered
     ssa_copy_pages, ssa_fork_requests, ssa_compact_pages
                              owners of the pages: copy, fork / grow / free, compact
 """
@@ -51,7 +52,7 @@ EXPORTS = ("ssa_workspace_size", "ssa_lru_init", "ssa_store_kv_mirror", "ssa_ind
            "ssa_sparse_paged_decode_fetch", "ssa_ensure_remap_bind", "ssa_fetch_misses",
            "ssa_rope", "ssa_rope_frequencies", "ssa_page_refs", "ssa_copy_pages",
            "ssa_fork_requests", "ssa_compact_pages", "ssa_norm_rope", "ssa_prompt_workspace_size",
-           "ssa_prompt_attention")
+           "ssa_prompt_attention", "ssa_beam_workspace_size", "ssa_beam_select")
 
 
 class SsaError(RuntimeError):
@@ -86,6 +87,10 @@ class SsaRopeTensor(ctypes.Structure):
 class SsaPromptTensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int),
                 ("stride", ctypes.c_int64 * 2)]
+
+
+class SsaBeams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("scores", "finished", "history", "hist_len")]
 
 
 _pack_prompt = struct.Struct("@Pi4x2q").pack    # an SsaPromptTensor's bytes
@@ -173,6 +178,11 @@ def lib():
         L.ssa_prompt_workspace_size.argtypes = []
         L.ssa_prompt_attention.restype = i32
         L.ssa_prompt_attention.argtypes = ([i32] * 5 + [vp] * 6 + [i32, ctypes.c_float] + [vp] * 4)
+        L.ssa_beam_workspace_size.restype = ctypes.c_size_t
+        L.ssa_beam_workspace_size.argtypes = [i32, i32]
+        L.ssa_beam_select.restype = i32
+        L.ssa_beam_select.argtypes = [i32, i32, i32, i32, vp, ctypes.c_int64, P(SsaBeams),
+                                      P(SsaBeams), i32, i32] + [vp] * 7
         _lib = L
     return _lib
 
@@ -792,6 +802,79 @@ def ssa_prompt_attention(q, k, v, cu_q, out, status, ws, cu_k=None, causal: bool
     _check(lib().ssa_prompt_attention(dtype, D, n - 1, n_q, k.shape[0], tq, tk, tv, to, pq, pk,
                                       causal, sm_scale, _ptr(lse), _ptr(status), ws.data_ptr(),
                                       _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# the next tokens
+# ---------------------------------------------------------------------------
+
+class BeamState:
+    """What beams carry from token to token, ``groups`` times ``beams`` rows:
+    scores [B] fp32 (sums of log-probabilities), with ``finished`` a byte per row
+    that says it has ended, with ``max_len`` the tokens so far, history
+    [B][max_len] and hist_len [groups], int32.  Starts before the first token:
+    the first row of a group at 0, the others at -infinity, nothing in the
+    histories."""
+
+    def __init__(self, groups: int, beams: int, max_len: int = 0, finished: bool = False,
+                 device="cuda"):
+        B, i32 = groups * beams, torch.int32
+        self.groups, self.beams, self.max_len = groups, beams, max_len
+        self.scores = torch.full((groups, beams), -math.inf, device=device)
+        self.scores[:, 0] = 0.0
+        self.scores = self.scores.view(B)
+        self.finished = torch.zeros((B,), dtype=torch.uint8, device=device) if finished else None
+        self.history = torch.zeros((B, max_len), dtype=i32, device=device) if max_len else None
+        self.hist_len = torch.zeros((groups,), dtype=i32, device=device) if max_len else None
+        self._dev = self.scores.get_device()
+        self._c = SsaBeams(*[_ptr(t) for t in (self.scores, self.finished, self.history,
+                                               self.hist_len)])
+
+    def __setattr__(self, name, value):
+        # calls go by the addresses of the tensors made above
+        if "_c" in self.__dict__:
+            raise AttributeError(f"{name}: change the tensors in place (copy_, fill_)")
+        object.__setattr__(self, name, value)
+
+
+def ssa_beam_workspace_size(groups: int, beams: int) -> int:
+    """Bytes of scratch of ssa_beam_select (zeroed once), for any vocabulary."""
+    return int(lib().ssa_beam_workspace_size(groups, beams))
+
+
+def ssa_beam_select(logits, state: BeamState, parent, token, status, ws, out: BeamState | None = None,
+                    eos: int = -1, seq_lens=None, new_lens=None, stream=None):
+    """The best (row, token) pairs of every group of beams by score plus
+    log-probability: logits [B][V] (rows may be strided), ``state`` before and
+    ``out`` after (default: in place); parent and token [B] int32 out, new_lens
+    [B] = seq_lens[parent] + 1, as ssa_fork_requests takes parent and new_lens.
+    eos: the token that ends a beam (a state with ``finished``), or -1."""
+    out = state if out is None else out
+    B, dev = state.groups * state.beams, state._dev
+    dtype = _ROPE_DTYPES.get(logits.dtype)
+    if dtype is None or logits.dim() != 2 or logits.shape[0] != B or logits.get_device() != dev or \
+            (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError(f"logits: [{B}][V] bfloat16, float16 or float32 on the state's device, a "
+                         f"row's elements contiguous, got {tuple(logits.shape)} {logits.dtype} on "
+                         f"{logits.device}")
+    if (out.groups, out.beams, out.max_len, out._dev) != \
+            (state.groups, state.beams, state.max_len, dev):
+        raise ValueError("state and out: of other sizes, or on other devices")
+    if (eos >= 0) != (state.finished is not None) or (eos >= 0) != (out.finished is not None):
+        raise ValueError(f"eos {eos}: a token for states with finished, -1 for states without")
+    if (seq_lens is None) != (new_lens is None):
+        raise ValueError("seq_lens and new_lens: both or none")
+    ints = [None if t is None else _ints(name, t, n, dev) for name, t, n in (
+        ("parent", parent, B), ("token", token, B), ("seq_lens", seq_lens, B),
+        ("new_lens", new_lens, B), ("status", status, 1))]
+    if ws.get_device() != dev or not ws.is_contiguous() or \
+            ws.nbytes < lib().ssa_beam_workspace_size(state.groups, state.beams):
+        raise ValueError("ws: ssa_beam_workspace_size(groups, beams) contiguous bytes on the "
+                         "state's device")
+    _on_current_device(dev)
+    _check(lib().ssa_beam_select(dtype, state.groups, state.beams, logits.shape[1],
+                                 logits.data_ptr(), logits.stride(0), state._c, out._c,
+                                 state.max_len, eos, *ints, ws.data_ptr(), _stream(stream)))
 
 
 def ssa_selftest_bounded_wait(status, stream=None):
