@@ -680,12 +680,13 @@ int ssa_prompt_attention(int dtype, int head_dim, int n_seqs, int n_q, int n_kv,
  *   a candidate (row, t) has the score  scores[row] + x[row][t] - ln sum_t' exp(x[row][t'])
  *   a finished row has one candidate, (row, eos), at scores[row]
  *   logits of -infinity and NaN (a mask) are no candidates, nor is anything of a
- *   row whose score is -infinity or NaN; +infinity counts as the largest float
+ *   row whose score is -infinity or NaN; logits above 2^126 count as 2^126
  * The `beams` best of each group, best first, equal scores by the lower row and
  * then the lower token, become the group's rows; the best of several rows may
  * be of one parent.  Sums and scores in double, one rounding to fp32 at the end.
  *   dtype     SSA_BF16, SSA_F16 or SSA_F32, of the logits
  *   logits    [groups * beams] rows, row_stride elements apart
+ *   groups    at most 65,535
  *   beams     at most 32, beams * ceil(vocab / 8192) <= 1024 (SSA_ERR_UNSUPPORTED)
  *   in, out   the rows' state before and after; out may be in:
  *     scores    [groups * beams] fp32 (a first step: 0 for one row of a group

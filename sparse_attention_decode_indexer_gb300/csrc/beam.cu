@@ -7,19 +7,26 @@
 // best of a group win, the first beam and then the first token among equals.
 //
 // What bounds it: the logits, read once.  A CTA takes 8,192 of a row's logits
-// into registers and leaves their maximum, the sum of their exponentials and
-// the K best; the last CTA of a group (a ticket) puts these together.
+// into registers and leaves the sum of their exponentials and the K best; the
+// last CTA of a group (a ticket) puts these together.  41 M logits are 270,000
+// to an SM, so every instruction per logit counts: 16-bit logits stay in words,
+// two to a maximum, and the exponential is one product, 2^(x log2e - c).
 //
-// The K best of what the threads of a CTA hold: each thread's own best; the
-// K-th of those bests is a bound that at least K values reach, and values that
-// reach it lie in at most K threads, so they go to a short list, in which each
-// finds its rank by counting.  Values are compared together with their index,
-// so that no two are equal and the order of the list does not matter.
+// The K best of what the threads of a CTA hold: the greatest of each four
+// threads; the K-th of these 64 is a bound that at least K values reach.  The
+// values that reach it, few more than K, go to a list, in which each finds its
+// rank by counting; values are compared together with their index, so no two
+// are equal and the order of the list does not matter.  Where many values
+// equal the bound (a mask of one finite value) the list would overflow: then the
+// bound is taken over (value, index) of each thread, which at most K threads'
+// values reach.
 //
-// Sums: fp32 within a thread (32 values), double above; scores are compared in
-// double, so that candidates of different beams are ordered by what they are
-// and not by a rounding to fp32 (an exponential is off by about 2^-22, an
-// average over many by less).
+// Sums are 64-bit integers in units of 2^-40 beside a largest term above 1/2, so
+// they do not depend on any order.  Double arithmetic (two operations a clock
+// and SM here) makes the logarithms and adds the scores, so that candidates of
+// different beams are ordered by what they are and not by a rounding to fp32:
+// an exponential is off by about 2^-22, an average over many by less.  2^(x L),
+// L = log2e rounded to fp32, in place of e^x is off by 2e-8 of the row's entropy.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -34,10 +41,15 @@ constexpr int kPer = 32;                  // logits of a thread
 constexpr int kSlice = kThreads * kPer;
 constexpr int kMaxBeams = 32;
 constexpr int kMaxLists = 1024;           // (row, slice) lists of a group
+constexpr int kList = 1024;               // values in a CTA's list
+constexpr int kFinal = 512;               // candidates in a group's list
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGreatest = 0x1p126f;     // logits above it count as it: its product with kLog2e is finite
+constexpr float kUnit = 0x1p40f;          // of the sums
 
-struct Part {                             // of a slice
-  double sum;                             // of exp(x - max)
-  float max;
+struct Part {                             // of a slice: sum * 2^(c - 40) is its sum of 2^(x kLog2e)
+  uint64_t sum;
+  float c;                                // -infinity: no logit
   int pad;
 };
 struct Cand {                             // logit and token; token < 0: none
@@ -59,145 +71,235 @@ struct Params {
   Part* part;                             // [row][slice]
   Cand* cand;                             // [row][slice][K]
   int32_t* ticket;                        // [group], zero between calls
+  int32_t* old_len;                       // [group], for the kernel that moves the histories
+  int move_here;                          // histories are moved by the group's last CTA
 };
 
-// Larger keys are better: the logit's order above, the lower token first below.
-__device__ __forceinline__ uint64_t key_of(float x, uint32_t t) {
+// Numbers in their order as integers: the larger, the greater.
+__device__ __forceinline__ uint32_t rank32(float x) {
   const uint32_t b = __float_as_uint(x);
-  return (uint64_t)(b ^ ((int32_t)b < 0 ? 0xFFFFFFFFu : 0x80000000u)) << 32 | (uint32_t)~t;
+  return b ^ ((int32_t)b < 0 ? 0xFFFFFFFFu : 0x80000000u);
 }
-__device__ __forceinline__ float key_x(uint64_t k) {
-  const uint32_t b = (uint32_t)(k >> 32);
+__device__ __forceinline__ float unrank32(uint32_t b) {
   return __uint_as_float(b ^ ((int32_t)b < 0 ? 0x80000000u : 0xFFFFFFFFu));
 }
+__device__ __forceinline__ uint64_t rank64(double x) {
+  const uint64_t b = (uint64_t)__double_as_longlong(x);
+  return b ^ ((int64_t)b < 0 ? ~0ull : 1ull << 63);
+}
+__device__ __forceinline__ double unrank64(uint64_t b) {
+  return __longlong_as_double((int64_t)(b ^ ((int64_t)b < 0 ? 1ull << 63 : ~0ull)));
+}
+// A logit and its token (or another index): the greater logit, then the lower index.
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t t) { return (uint64_t)rank32(x) << 32 | (uint32_t)~t; }
+__device__ __forceinline__ float key_x(uint64_t k) { return unrank32((uint32_t)(k >> 32)); }
 
-__device__ __forceinline__ double warp_sum(double v) {
+__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// A logit as the sums take it: NaN is no candidate, +infinity the greatest number.
-__device__ __forceinline__ float clean(float x) { return x == x ? fminf(x, FLT_MAX) : -INFINITY; }
+// A thread's logits: 32 of them, in 16-byte pieces 16 * kThreads bytes apart.
+template <typename T> struct Logits {
+  static constexpr int N = 16 / sizeof(T);              // of a piece
+  static constexpr int W = kPer * sizeof(T) / 4;        // words
+  uint32_t w[W];
 
-template <typename T>
-__device__ __forceinline__ void load_slice(const T* row, int first, int V, bool vec, float* x) {
-  constexpr int N = 16 / sizeof(T);
+  static __device__ __forceinline__ uint32_t none() {   // a word of -infinity
+    if constexpr (sizeof(T) == 4) return 0xFF800000u;
+    else return std::is_same_v<T, __half> ? 0xFC00FC00u : 0xFF80FF80u;
+  }
+  __device__ __forceinline__ void load(const T* row, int first, int V, bool vec) {
 #pragma unroll
-  for (int j = 0; j < kPer / N; ++j) {
-    const int at = first + (j * kThreads + threadIdx.x) * N;
-    if (vec && at + N <= V) {
-      const uint4 u = *reinterpret_cast<const uint4*>(row + at);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int j = 0; j < kPer / N; ++j) {
+      const int at = first + (j * kThreads + (int)threadIdx.x) * N;
+      if (vec && at + N <= V) {
+        const uint4 u = __ldcs(reinterpret_cast<const uint4*>(row + at));
+        w[4 * j] = u.x; w[4 * j + 1] = u.y; w[4 * j + 2] = u.z; w[4 * j + 3] = u.w;
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 4) {
-          x[j * N + i] = __uint_as_float(w[i]);
-        } else {
-          const float2 f = unpack<T>(w[i]);
-          x[j * N + 2 * i] = f.x;
-          x[j * N + 2 * i + 1] = f.y;
+        for (int i = 0; i < 4; ++i) {
+          w[4 * j + i] = none();
+          if constexpr (sizeof(T) == 4) {
+            if (at + i < V) w[4 * j + i] = __float_as_uint(row[at + i]);
+          } else {
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(row);
+            uint32_t lo = none() & 0xFFFFu, hi = lo;
+            if (at + 2 * i < V) lo = h[at + 2 * i];
+            if (at + 2 * i + 1 < V) hi = h[at + 2 * i + 1];
+            w[4 * j + i] = lo | hi << 16;
+          }
         }
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) x[j * N + i] = at + i < V ? one_in(row[at + i]) : -INFINITY;
     }
   }
-}
-// the token of a thread's i-th logit
-template <typename T> __device__ __forceinline__ int token_of(int first, int i) {
-  constexpr int N = 16 / sizeof(T);
-  return first + ((i / N) * kThreads + (int)threadIdx.x) * N + i % N;
-}
+  // the greatest, NaN aside
+  __device__ __forceinline__ float most() const {
+    if constexpr (sizeof(T) == 4) {
+      float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < W; ++i) m[i & 3] = fmaxf(m[i & 3], __uint_as_float(w[i]));
+      return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    } else {
+      uint32_t m = none();
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        if constexpr (std::is_same_v<T, __half>) asm("max.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+        else asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+      }
+      const float2 f = unpack<T>(m);
+      return fmaxf(f.x, f.y);
+    }
+  }
+  // f(logit, its place in the thread's order)
+  template <typename F> __device__ __forceinline__ void each(F f) const {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        f(__uint_as_float(w[i]), i);
+      } else {
+        const float2 x = unpack<T>(w[i]);
+        f(x.x, 2 * i);
+        f(x.y, 2 * i + 1);
+      }
+    }
+  }
+  static __device__ __forceinline__ int token(int first, int i) {
+    return first + ((i / N) * kThreads + (int)threadIdx.x) * N + i % N;
+  }
+};
 
 struct Score {                            // of a candidate, and its place in the group
-  double s;
+  uint64_t s;                             // rank64 of the score; 0: none
   long long at;                           // row * V + token
 };
 __device__ __forceinline__ bool better(const Score& a, const Score& b) {
   return a.s > b.s || (a.s == b.s && a.at < b.at);
 }
 
+// Scratch of a CTA: its list, or the group's.
+union Scratch {
+  uint64_t list[kList];
+  Score score[kFinal];
+  int32_t move[2048];
+};
+
 // The group's choice and the new states, by the group's last CTA.
-template <typename T>
-__device__ void choose(const Params& p, int g, uint8_t* smem) {
-  const int K = p.K, lists = K * p.slices, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  __shared__ double s_score0[kMaxBeams], s_lse[kMaxBeams];
-  __shared__ Score s_best[kThreads];
-  __shared__ Score s_bound;
-  __shared__ int s_n, s_parent[kMaxBeams], s_token[kMaxBeams];
-  __shared__ uint8_t s_ended[kMaxBeams];
-  __shared__ int s_len[kMaxBeams];
+__device__ __noinline__ void choose(const Params& p, int g, Scratch& sc) {
+  const int K = p.K, lists = K * p.slices, tid = threadIdx.x;
+  __shared__ double s_add[kMaxBeams], s_lse[kMaxBeams];
+  __shared__ uint64_t s_z[kMaxBeams];
+  __shared__ float s_c[kMaxBeams];
+  __shared__ Score s_best[64], s_bound;
+  __shared__ int s_n, s_parent[kMaxBeams], s_token[kMaxBeams], s_len[kMaxBeams];
+  __shared__ uint8_t s_ended[kMaxBeams], s_taken[kMaxLists];
   __shared__ float s_score[kMaxBeams];
   const long long row0 = (long long)g * K;
-  for (int r = warp; r < K; r += kThreads / 32) {
-    const bool ended = p.ended && p.ended[row0 + r];
-    float m = -INFINITY;
-    for (int i = lane; i < p.slices; i += 32) m = fmaxf(m, __ldcg(&p.part[(row0 + r) * p.slices + i].max));
-    m = warp_max(m);
-    double z = 0.0;
-    for (int i = lane; i < p.slices; i += 32) {
-      const Part* q = &p.part[(row0 + r) * p.slices + i];
-      const float qm = __ldcg(&q->max);
-      if (qm > -INFINITY) z += __ldcg(&q->sum) * exp((double)qm - (double)m);
+  for (int r = tid >> 5; r < K; r += kThreads / 32) {
+    const Part* part = p.part + (row0 + r) * p.slices;
+    float c = -INFINITY;
+    for (int i = tid & 31; i < p.slices; i += 32) c = fmaxf(c, __ldcg(&part[i].c));
+    c = warp_max(c);
+    uint64_t z = 0;
+    for (int i = tid & 31; i < p.slices; i += 32) {
+      const float pc = __ldcg(&part[i].c);
+      if (pc > -INFINITY) z += __ldcg(&part[i].sum) >> (int)fminf(c - pc, 63.0f);
     }
     z = warp_sum(z);
-    if (lane == 0) {
-      s_score0[r] = p.scores[row0 + r];
-      s_lse[r] = ended || z == 0.0 ? 0.0 : (double)m + log(z);
-    }
+    if ((tid & 31) == 0) { s_z[r] = z; s_c[r] = c; }
   }
-  if (tid == 0) s_n = 0;
+  if (tid == 0) { s_n = 0; s_bound = Score{0, LLONG_MAX}; }
+  if (tid < K) { s_parent[tid] = s_token[tid] = -1; s_score[tid] = -INFINITY; }
+  __syncthreads();
   if (tid < K) {
-    s_parent[tid] = -1;
-    s_token[tid] = -1;
-    s_score[tid] = -INFINITY;
+    const bool ended = p.ended && p.ended[row0 + tid];
+    s_add[tid] = p.scores[row0 + tid];
+    s_lse[tid] = ended || s_z[tid] == 0 ? 0.0 : ((double)s_c[tid] - 40.0 + log2((double)s_z[tid])) / (double)kLog2e;
   }
   __syncthreads();
 
   const auto score_of = [&](int list, int k) {
     const int r = list / p.slices;
     const int2 c = __ldcg(reinterpret_cast<const int2*>(p.cand + (row0 * p.slices + list) * K + k));
-    Score s{-INFINITY, LLONG_MAX};
+    Score s{0, LLONG_MAX};
     if (c.y >= 0) {
-      const double v = ((double)__int_as_float(c.x) - s_lse[r]) + s_score0[r];
-      if (v > -INFINITY) { s.s = v; s.at = (long long)r * p.V + c.y; }
+      const double v = ((double)__int_as_float(c.x) - s_lse[r]) + s_add[r];
+      if (v > -INFINITY) { s.s = rank64(v); s.at = (long long)r * p.V + c.y; }
     }
     return s;
   };
   // a list is sorted: its first is its best
-  Score best{-INFINITY, LLONG_MAX};
+  Score mine{0, LLONG_MAX};
   for (int i = tid; i < lists; i += kThreads) {
     const Score s = score_of(i, 0);
+    if (better(s, mine)) mine = s;
+  }
+  Score best = mine;
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    const Score s{__shfl_xor_sync(0xffffffffu, best.s, o), __shfl_xor_sync(0xffffffffu, best.at, o)};
     if (better(s, best)) best = s;
   }
-  s_best[tid] = best;
-  if (tid == 0) s_bound = Score{-INFINITY, LLONG_MAX};
+  if ((tid & 3) == 0) s_best[tid >> 2] = best;
   __syncthreads();
-  int rank = 0;
-  for (int j = 0; j < kThreads; ++j) rank += better(s_best[j], best);
-  if (rank == K - 1 && best.s > -INFINITY) s_bound = best;
+  if (tid < 64) {
+    const Score a = s_best[tid];
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < 64; ++j) rank += better(s_best[j], a);
+    if (rank == K - 1 && a.s) s_bound = a;
+  }
   __syncthreads();
   const Score bound = s_bound;
-  Score* list = reinterpret_cast<Score*>(smem);
-  if (best.s > -INFINITY && !better(bound, best))
+  if (mine.s && !better(bound, mine))
     for (int i = tid; i < lists; i += kThreads)
       for (int k = 0; k < K; ++k) {
         const Score s = score_of(i, k);
-        if (s.s == -INFINITY || better(bound, s)) break;
-        list[atomicAdd(&s_n, 1)] = s;
+        if (!s.s || better(bound, s)) break;
+        const int at = atomicAdd(&s_n, 1);
+        if (at < kFinal) sc.score[at] = s;
       }
   __syncthreads();
   const int n = s_n;
-  for (int i = tid; i < n; i += kThreads) {
-    const Score s = list[i];
-    int r = 0;
-    for (int j = 0; j < n; ++j) r += better(list[j], s);
-    if (r < K) {
-      s_parent[r] = (int)(s.at / p.V);
-      s_token[r] = (int)(s.at % p.V);
-      s_score[r] = (float)s.s;
+  const auto place = [&](const Score& s, int r) {
+    s_parent[r] = (int)(s.at / p.V);
+    s_token[r] = (int)(s.at % p.V);
+    s_score[r] = (float)unrank64(s.s);
+  };
+  if (n <= kFinal) {
+    for (int i = tid; i < n; i += kThreads) {
+      const Score s = sc.score[i];
+      int r = 0;
+      for (int j = 0; j < n; ++j) r += better(sc.score[j], s);
+      if (r < K) place(s, r);
+    }
+  } else {
+    // more than the list holds (rows that lie close together): the best of the
+    // lists' next ones, K times
+    for (int i = tid; i < lists; i += kThreads) s_taken[i] = 0;
+    __syncthreads();
+    for (int r = 0; r < K; ++r) {
+      Score top{0, LLONG_MAX};
+      for (int i = tid; i < lists; i += kThreads)
+        if (s_taken[i] < K) {
+          const Score s = score_of(i, s_taken[i]);
+          if (better(s, top)) top = s;
+        }
+      sc.score[tid] = top;
+      __syncthreads();
+      for (int o = kThreads / 2; o; o >>= 1) {
+        if (tid < o && better(sc.score[tid + o], sc.score[tid])) sc.score[tid] = sc.score[tid + o];
+        __syncthreads();
+      }
+      const Score got = sc.score[0];
+      __syncthreads();
+      if (!got.s) break;
+      if (tid == 0) {
+        place(got, r);
+        s_taken[(int)(got.at / p.V) * p.slices + (int)(got.at % p.V) / kSlice] += 1;
+      }
+      __syncthreads();
     }
   }
   __syncthreads();
@@ -223,12 +325,16 @@ __device__ void choose(const Params& p, int g, uint8_t* smem) {
   const bool full = len < 0 || len >= p.max_len;
   if (full && tid == 0) set_status(p.status, SSA_ST_BAD_POS);
   len = min(max(len, 0), p.max_len);
-  int32_t* column = reinterpret_cast<int32_t*>(smem);       // [K][kThreads], a thread its own
-  for (int c = tid; c < len; c += kThreads) {
-    for (int i = 0; i < K; ++i)
-      if (s_parent[i] >= 0) column[i * kThreads + tid] = p.history[(row0 + s_parent[i]) * p.max_len + c];
-    for (int i = 0; i < K; ++i)
-      if (s_parent[i] >= 0) p.history_out[(row0 + i) * p.max_len + c] = column[i * kThreads + tid];
+  if (p.move_here) {                      // K * max_len fit the scratch
+    for (int i = tid; i < K * len; i += kThreads) {
+      const int par = s_parent[i / len];
+      if (par >= 0) sc.move[i] = p.history[(row0 + par) * p.max_len + i % len];
+    }
+    __syncthreads();
+    for (int i = tid; i < K * len; i += kThreads)
+      if (s_parent[i / len] >= 0) p.history_out[(row0 + i / len) * p.max_len + i % len] = sc.move[i];
+  } else if (tid == 0) {
+    p.old_len[g] = len;
   }
   if (!full && tid < K && s_parent[tid] >= 0) p.history_out[(row0 + tid) * p.max_len + len] = s_token[tid];
   if (tid == 0) p.hist_len_out[g] = full ? len : len + 1;
@@ -236,12 +342,11 @@ __device__ void choose(const Params& p, int g, uint8_t* smem) {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ Params p, bool vec) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint64_t s_best[kThreads];
-  __shared__ uint64_t s_bound;
-  __shared__ double s_sum[kThreads / 32];
+  __shared__ Scratch sc;
+  __shared__ uint64_t s_key[kThreads];
+  __shared__ uint64_t s_bound, s_sum[kThreads / 32];
   __shared__ float s_max[kThreads / 32];
-  __shared__ int s_n, s_last;
+  __shared__ int s_n, s_last, s_odd;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, K = p.K;
@@ -252,61 +357,99 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ 
 
   if (p.ended && p.ended[row]) {
     // one candidate, at the beam's score
-    if (tid < K) out[tid] = Cand{0.0f, slice == 0 && tid == 0 ? p.eos : -1};
-    if (tid == 0) *part = Part{0.0, -INFINITY, 0};
+    if (tid < K) out[tid] = Cand{0.0f, slice == p.eos / kSlice && tid == 0 ? p.eos : -1};
+    if (tid == 0) *part = Part{0, -INFINITY, 0};
   } else {
-    float x[kPer];
+    Logits<T> x;
     const int first = slice * kSlice;
-    load_slice<T>(static_cast<const T*>(p.logits) + row * p.stride, first, p.V, vec, x);
-    if (tid == 0) { s_n = 0; s_bound = 0; }
-    float m = -INFINITY;
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      x[i] = clean(x[i]);
-      if (x[i] > m) { m = x[i]; at = i; }
-    }
-    const uint64_t best = key_of(m, (uint32_t)token_of<T>(first, at));
-    s_best[tid] = best;
-    float top = warp_max(m);
-    if (lane == 0) s_max[warp] = top;
+    x.load(static_cast<const T*>(p.logits) + row * p.stride, first, p.V, vec);
+    if (tid == 0) { s_n = 0; s_odd = 0; }
+    const float m = fminf(x.most(), kGreatest);
+    float q = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 2));
+    if ((tid & 3) == 0) s_key[tid >> 2] = key_of(q, tid >> 2);
+    q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 4));
+    q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 8));
+    q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 16));
+    if (lane == 0) s_max[warp] = q;
     __syncthreads();
+    float top = s_max[0];
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, s_max[w]);
-    int rank = 0;
-#pragma unroll 8
-    for (int j = 0; j < kThreads; ++j) rank += s_best[j] > best;
-    if (rank == K - 1) s_bound = best;
+    for (int w = 1; w < kThreads / 32; ++w) top = fmaxf(top, s_max[w]);
+    if (tid < 64) {
+      const uint64_t k = s_key[tid];
+      int rank = 0;
+#pragma unroll 16
+      for (int j = 0; j < 64; ++j) rank += s_key[j] > k;
+      if (rank == K - 1) s_bound = k;
+    }
+    const float c = ceilf(top * kLog2e);  // whole, so that slices add by shifts
     float sum[4] = {0, 0, 0, 0};
-    if (top > -INFINITY) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) sum[i & 3] += fast_exp2((x[i] - top) * 1.4426950408889634f);
-    }
-    const double z = warp_sum((double)((sum[0] + sum[1]) + (sum[2] + sum[3])));
-    if (lane == 0) s_sum[warp] = z;
+    if (top > -INFINITY)
+      x.each([&](float v, int i) { sum[i & 3] += fast_exp2(fmaf(v, kLog2e, -c)); });
+    float z = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    if (!(z <= 64.0f)) s_odd = 1;         // a NaN, or a logit above kGreatest
+    const uint64_t zi = warp_sum((uint64_t)(z * kUnit));
+    if (lane == 0) s_sum[warp] = zi;
     __syncthreads();
-    const uint64_t bound = s_bound;
-    uint64_t* list = reinterpret_cast<uint64_t*>(smem);
-    if (best >= bound) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const uint64_t k = key_of(x[i], (uint32_t)token_of<T>(first, i));
-        if (k >= bound && x[i] > -INFINITY) list[atomicAdd(&s_n, 1)] = k;
-      }
+    if (s_odd) {
+      z = 0.0f;
+      x.each([&](float v, int) {
+        if (v == v) z += fast_exp2(fmaf(fminf(v, kGreatest), kLog2e, -c));
+      });
+      const uint64_t zc = warp_sum((uint64_t)(z * kUnit));
+      if (lane == 0) s_sum[warp] = zc;
     }
+    // the list of what reaches the bound
+    uint64_t bound = s_bound;
+    const float least = key_x(bound);
+    if (m >= least && m > -INFINITY)
+      x.each([&](float v, int i) {
+        if (v >= least && v > -INFINITY) {                 // (never a NaN)
+          const int at = atomicAdd(&s_n, 1);
+          if (at < kList) sc.list[at] = key_of(fminf(v, kGreatest), (uint32_t)x.token(first, i));
+        }
+      });
     __syncthreads();
-    const int n = s_n;
+    int n = s_n;
+    if (n > kList) {
+      // many equal ones: bounded over (value, token) instead
+      uint64_t best = 0;
+      x.each([&](float v, int i) {
+        if (v == v) {
+          const uint64_t k = key_of(fminf(v, kGreatest), (uint32_t)x.token(first, i));
+          if (k > best) best = k;
+        }
+      });
+      s_key[tid] = best;
+      __syncthreads();
+      if (tid == 0) s_n = 0;
+      int rank = 0;
+      for (int j = 0; j < kThreads; ++j) rank += s_key[j] > best || (s_key[j] == best && j < tid);
+      if (rank == K - 1) s_bound = best;
+      __syncthreads();
+      bound = s_bound;
+      if (best >= bound)
+        x.each([&](float v, int i) {
+          if (v == v && v > -INFINITY) {
+            const uint64_t k = key_of(fminf(v, kGreatest), (uint32_t)x.token(first, i));
+            if (k >= bound) sc.list[atomicAdd(&s_n, 1)] = k;
+          }
+        });
+      __syncthreads();
+      n = s_n;
+    }
     if (tid < K && tid >= n) out[tid] = Cand{0.0f, -1};
     for (int i = tid; i < n; i += kThreads) {
-      const uint64_t k = list[i];
+      const uint64_t k = sc.list[i];
       int r = 0;
-      for (int j = 0; j < n; ++j) r += list[j] > k;
+      for (int j = 0; j < n; ++j) r += sc.list[j] > k;
       if (r < K) out[r] = Cand{key_x(k), (int)~(uint32_t)k};
     }
     if (tid == 0) {
-      double s = 0.0;
+      uint64_t s = 0;
       for (int w = 0; w < kThreads / 32; ++w) s += s_sum[w];
-      *part = Part{s, top, 0};
+      *part = Part{s, top > -INFINITY ? c : -INFINITY, 0};
     }
   }
   // the last CTA of the group goes on
@@ -320,26 +463,45 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ 
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  choose<T>(p, g, smem);
+  choose(p, g, sc);
+}
+
+// Histories of a group in their new order: a thread per column, which reads it in
+// every row before it writes one, so in and out may be the same.
+constexpr int kMoveThreads = 128;
+__global__ void __launch_bounds__(kMoveThreads) beam_move_kernel(const __grid_constant__ Params p) {
+  extern __shared__ int32_t s_col[];      // [K][kMoveThreads]
+  pdl_trigger();
+  pdl_wait();
+  const int g = blockIdx.y, K = p.K, tid = threadIdx.x;
+  const int c = blockIdx.x * kMoveThreads + tid;
+  const long long row0 = (long long)g * K;
+  if (c >= p.old_len[g]) return;
+#pragma unroll 8
+  for (int i = 0; i < K; ++i) {
+    const int par = p.parent[row0 + i];
+    if (par >= 0) s_col[i * kMoveThreads + tid] = p.history[(long long)par * p.max_len + c];
+  }
+#pragma unroll 8
+  for (int i = 0; i < K; ++i)
+    if (p.parent[row0 + i] >= 0) p.history_out[(row0 + i) * p.max_len + c] = s_col[i * kMoveThreads + tid];
 }
 
 int slices_of(int V) { return (V + kSlice - 1) / kSlice; }
 
-size_t align16(size_t x) { return (x + 255) & ~(size_t)255; }
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 template <typename T>
 cudaError_t launch(const Params& p, int groups, cudaStream_t s) {
   constexpr int N = 16 / sizeof(T);
   const bool vec = !((uintptr_t)p.logits & 15) && (p.stride % N == 0 || groups * p.K == 1);
-  const int per = (p.K * p.slices + kThreads - 1) / kThreads;        // lists of a thread
-  size_t smem = (size_t)p.K * kPer * sizeof(uint64_t);
-  smem = std::max(smem, (size_t)p.K * per * p.K * sizeof(Score));
-  if (p.history) smem = std::max(smem, (size_t)p.K * kThreads * sizeof(int32_t));
-  cudaError_t e = cudaFuncSetAttribute(beam_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   const long long ctas = (long long)groups * p.K * p.slices;
   if (ctas > INT_MAX) return cudaErrorInvalidValue;
-  e = launch_pdl(beam_kernel<T>, dim3((unsigned)ctas), dim3(kThreads), smem, s, p, vec);
+  cudaError_t e = launch_pdl(beam_kernel<T>, dim3((unsigned)ctas), dim3(kThreads), 0, s, p, vec);
+  count_launch();
+  if (e != cudaSuccess || !p.history || p.move_here) return e;
+  e = launch_pdl(beam_move_kernel, dim3((p.max_len + kMoveThreads - 1) / kMoveThreads, groups), dim3(kMoveThreads),
+                 (size_t)p.K * kMoveThreads * sizeof(int32_t), s, p);
   count_launch();
   return e;
 }
@@ -353,7 +515,7 @@ size_t ssa_beam_workspace_size(int groups, int beams) {
   using namespace ssa;
   if (groups < 1 || beams < 1 || beams > kMaxBeams) return 0;
   const size_t lists = (size_t)groups * kMaxLists;
-  return align16((size_t)groups * 4) + align16(lists * sizeof(Part)) + align16(lists * beams * sizeof(Cand));
+  return 2 * align256((size_t)groups * 4) + align256(lists * sizeof(Part)) + align256(lists * beams * sizeof(Cand));
 }
 
 int ssa_beam_select(int dtype, int groups, int beams, int vocab, const void* logits, int64_t row_stride,
@@ -364,7 +526,7 @@ int ssa_beam_select(int dtype, int groups, int beams, int vocab, const void* log
   if (dtype < SSA_BF16 || dtype > SSA_F32) return SSA_ERR_UNSUPPORTED;
   if (groups < 1 || beams < 1 || vocab < 1 || max_len < 0 || eos < -1 || eos >= vocab) return SSA_ERR_INVALID_ARG;
   if (beams > kMaxBeams || (long long)beams * slices_of(vocab) > kMaxLists) return SSA_ERR_UNSUPPORTED;
-  if ((long long)groups * beams > INT_MAX) return SSA_ERR_UNSUPPORTED;
+  if (groups > 65535) return SSA_ERR_UNSUPPORTED;
   if (!logits || !in || !out || !in->scores || !out->scores || !parent || !token || !ws) return SSA_ERR_INVALID_ARG;
   if ((uintptr_t)logits & (dtype == SSA_F32 ? 3 : 1)) return SSA_ERR_INVALID_ARG;
   if (row_stride < vocab && (long long)groups * beams > 1) return SSA_ERR_INVALID_ARG;
@@ -383,11 +545,14 @@ int ssa_beam_select(int dtype, int groups, int beams, int vocab, const void* log
   p.hist_len_out = out->hist_len;
   p.seq_lens = seq_lens_opt; p.new_lens = new_lens_opt; p.parent = parent; p.token = token;
   p.status = status;
+  p.move_here = (long long)beams * max_len <= (long long)(sizeof(Scratch::move) / 4);
   char* w = static_cast<char*>(ws);
   p.ticket = reinterpret_cast<int32_t*>(w);
-  w += align16((size_t)groups * 4);
+  w += align256((size_t)groups * 4);
+  p.old_len = reinterpret_cast<int32_t*>(w);
+  w += align256((size_t)groups * 4);
   p.part = reinterpret_cast<Part*>(w);
-  w += align16((size_t)groups * kMaxLists * sizeof(Part));
+  w += align256((size_t)groups * kMaxLists * sizeof(Part));
   p.cand = reinterpret_cast<Cand*>(w);
   cudaError_t e;
   switch (dtype) {
