@@ -94,10 +94,41 @@ __device__ __forceinline__ double unrank64(uint64_t b) {
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t t) { return (uint64_t)rank32(x) << 32 | (uint32_t)~t; }
 __device__ __forceinline__ float key_x(uint64_t k) { return unrank32((uint32_t)(k >> 32)); }
 
+__device__ __forceinline__ uint32_t redux_add(uint32_t v) {
+  uint32_t r;
+  asm("redux.sync.add.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(v));
+  return r;
+}
+// The sum of 32 numbers below 2^47, in halves of 21 and 26 bits.
+__device__ __forceinline__ uint64_t warp_sum47(uint64_t v) {
+  const uint32_t lo = redux_add((uint32_t)v & 0x3FFFFFFu), hi = redux_add((uint32_t)(v >> 26));
+  return ((uint64_t)hi << 26) + lo;
+}
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+// Two products and two sums in one instruction each.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // A thread's logits: 32 of them, in 16-byte pieces 16 * kThreads bytes apart.
@@ -106,6 +137,10 @@ template <typename T> struct Logits {
   static constexpr int W = kPer * sizeof(T) / 4;        // words
   uint32_t w[W];
 
+  static __device__ __forceinline__ float lowest() {    // that is finite
+    if constexpr (sizeof(T) == 4) return -FLT_MAX;
+    else return std::is_same_v<T, __half> ? -65504.0f : -0x1.FEp127f;
+  }
   static __device__ __forceinline__ uint32_t none() {   // a word of -infinity
     if constexpr (sizeof(T) == 4) return 0xFF800000u;
     else return std::is_same_v<T, __half> ? 0xFC00FC00u : 0xFF80FF80u;
@@ -165,6 +200,49 @@ template <typename T> struct Logits {
       }
     }
   }
+  // the sum of 2^(x kLog2e - c)
+  __device__ __forceinline__ float sum(float c) const {
+    const uint64_t l2 = pack2(kLog2e, kLog2e), c2 = pack2(-c, -c);
+    uint64_t s[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) {
+      uint64_t x;
+      if constexpr (sizeof(T) == 4) {
+        x = pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+      } else {
+        const float2 f = unpack<T>(w[i]);
+        x = pack2(f.x, f.y);
+      }
+      const float2 t = unpack2(fma2(x, l2, c2));
+      s[i & 1] = add2(s[i & 1], pack2(fast_exp2(t.x), fast_exp2(t.y)));
+    }
+    const float2 r = unpack2(add2(s[0], s[1]));
+    return r.x + r.y;
+  }
+  // which of them are at least `least` (never a NaN): bit i the thread's i-th
+  __device__ __forceinline__ uint32_t reach(float least) const {
+    uint32_t bits = 0;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) bits |= __uint_as_float(w[i]) >= least ? 1u << i : 0u;
+    } else {
+      const uint32_t l = pack<T>(least, least);          // exact, or (fp16) infinity
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        uint32_t m;
+        if constexpr (std::is_same_v<T, __half>)
+          m = __hge2_mask(*reinterpret_cast<const __half2*>(&w[i]), *reinterpret_cast<const __half2*>(&l));
+        else
+          m = __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), *reinterpret_cast<const __nv_bfloat162*>(&l));
+        bits |= m & (1u << i | 0x10000u << i);           // the even ones low, the odd ones high
+      }
+    }
+    return bits;
+  }
+  // the place of a bit of reach()
+  static __device__ __forceinline__ int place(int bit) {
+    return sizeof(T) == 4 ? bit : (bit & 15) * 2 + (bit >> 4);
+  }
   static __device__ __forceinline__ int token(int first, int i) {
     return first + ((i / N) * kThreads + (int)threadIdx.x) * N + i % N;
   }
@@ -172,7 +250,7 @@ template <typename T> struct Logits {
 
 struct Score {                            // of a candidate, and its place in the group
   uint64_t s;                             // rank64 of the score; 0: none
-  long long at;                           // row * V + token
+  uint64_t at;                            // row << 32 | token
 };
 __device__ __forceinline__ bool better(const Score& a, const Score& b) {
   return a.s > b.s || (a.s == b.s && a.at < b.at);
@@ -185,57 +263,79 @@ union Scratch {
   int32_t move[2048];
 };
 
-// The group's choice and the new states, by the group's last CTA.
+// The group's choice and the new states, by the group's last CTA.  What it takes
+// is round trips to L2, one after another, so loads go out together: the parts
+// and the lists' first candidates, then the lists that reach the bound.
 __device__ __noinline__ void choose(const Params& p, int g, Scratch& sc) {
-  const int K = p.K, lists = K * p.slices, tid = threadIdx.x;
+  constexpr int kPerThread = kMaxLists / kThreads;
+  const int K = p.K, lists = K * p.slices, tid = threadIdx.x, lane = tid & 31;
   __shared__ double s_add[kMaxBeams], s_lse[kMaxBeams];
   __shared__ uint64_t s_z[kMaxBeams];
   __shared__ float s_c[kMaxBeams];
   __shared__ Score s_best[64], s_bound;
-  __shared__ int s_n, s_parent[kMaxBeams], s_token[kMaxBeams], s_len[kMaxBeams];
+  __shared__ int s_n, s_lists, s_parent[kMaxBeams], s_token[kMaxBeams], s_len[kMaxBeams];
+  __shared__ uint16_t s_list[kMaxLists];
   __shared__ uint8_t s_ended[kMaxBeams], s_taken[kMaxLists];
   __shared__ float s_score[kMaxBeams];
   const long long row0 = (long long)g * K;
-  for (int r = tid >> 5; r < K; r += kThreads / 32) {
-    const Part* part = p.part + (row0 + r) * p.slices;
-    float c = -INFINITY;
-    for (int i = tid & 31; i < p.slices; i += 32) c = fmaxf(c, __ldcg(&part[i].c));
-    c = warp_max(c);
-    uint64_t z = 0;
-    for (int i = tid & 31; i < p.slices; i += 32) {
-      const float pc = __ldcg(&part[i].c);
-      if (pc > -INFINITY) z += __ldcg(&part[i].sum) >> (int)fminf(c - pc, 63.0f);
-    }
-    z = warp_sum(z);
-    if ((tid & 31) == 0) { s_z[r] = z; s_c[r] = c; }
+  const int2* cand = reinterpret_cast<const int2*>(p.cand + row0 * p.slices * K);
+  int2 head[kPerThread];                  // a list is sorted: its first is its best
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    const int i = tid + j * kThreads;
+    head[j] = i < lists ? __ldcg(cand + (size_t)i * K) : make_int2(0, -1);
   }
-  if (tid == 0) { s_n = 0; s_bound = Score{0, LLONG_MAX}; }
+  float add = 0.0f;
+  bool ended = false;
+  if (tid < K) {
+    add = p.scores[row0 + tid];
+    ended = p.ended && p.ended[row0 + tid];
+  }
+  int len = 0;
+  if (p.history) len = p.hist_len[g];
+  for (int r = tid >> 5; r < K; r += kThreads / 32) {
+    const uint4* part = reinterpret_cast<const uint4*>(p.part + (row0 + r) * p.slices);
+    float c = -INFINITY;
+    uint64_t z = 0;
+    for (int i = lane; i < p.slices; i += 32) {
+      const uint4 u = __ldcg(part + i);
+      const uint64_t s = (uint64_t)u.y << 32 | u.x;
+      const float pc = __uint_as_float(u.z);
+      if (pc > c) {
+        z = (c > -INFINITY ? z >> (int)fminf(pc - c, 63.0f) : 0) + s;
+        c = pc;
+      } else if (pc > -INFINITY) {
+        z += s >> (int)fminf(c - pc, 63.0f);
+      }
+    }
+    const float top = warp_max(c);
+    z = warp_sum(c > -INFINITY ? z >> (int)fminf(top - c, 63.0f) : 0);
+    if (lane == 0) { s_z[r] = z; s_c[r] = top; }
+  }
+  if (tid == 0) { s_n = s_lists = 0; s_bound = Score{0, ~0ull}; }
   if (tid < K) { s_parent[tid] = s_token[tid] = -1; s_score[tid] = -INFINITY; }
   __syncthreads();
   if (tid < K) {
-    const bool ended = p.ended && p.ended[row0 + tid];
-    s_add[tid] = p.scores[row0 + tid];
-    s_lse[tid] = ended || s_z[tid] == 0 ? 0.0 : ((double)s_c[tid] - 40.0 + log2((double)s_z[tid])) / (double)kLog2e;
+    s_add[tid] = add;
+    s_lse[tid] = ended || s_z[tid] == 0 ? 0.0 : ((double)s_c[tid] - 40.0 + log2((double)s_z[tid])) * (1.0 / (double)kLog2e);
   }
   __syncthreads();
 
-  const auto score_of = [&](int list, int k) {
-    const int r = list / p.slices;
-    const int2 c = __ldcg(reinterpret_cast<const int2*>(p.cand + (row0 * p.slices + list) * K + k));
-    Score s{0, LLONG_MAX};
+  const auto score_of = [&](int r, int2 c) {
+    Score s{0, ~0ull};
     if (c.y >= 0) {
       const double v = ((double)__int_as_float(c.x) - s_lse[r]) + s_add[r];
-      if (v > -INFINITY) { s.s = rank64(v); s.at = (long long)r * p.V + c.y; }
+      if (v > -INFINITY) { s.s = rank64(v); s.at = (uint64_t)r << 32 | (uint32_t)c.y; }
     }
     return s;
   };
-  // a list is sorted: its first is its best
-  Score mine{0, LLONG_MAX};
-  for (int i = tid; i < lists; i += kThreads) {
-    const Score s = score_of(i, 0);
-    if (better(s, mine)) mine = s;
+  Score mine[kPerThread], best{0, ~0ull};
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    mine[j] = Score{0, ~0ull};
+    if (tid + j * kThreads < lists) mine[j] = score_of((tid + j * kThreads) / p.slices, head[j]);
+    if (better(mine[j], best)) best = mine[j];
   }
-  Score best = mine;
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
     const Score s{__shfl_xor_sync(0xffffffffu, best.s, o), __shfl_xor_sync(0xffffffffu, best.at, o)};
@@ -246,25 +346,29 @@ __device__ __noinline__ void choose(const Params& p, int g, Scratch& sc) {
   if (tid < 64) {
     const Score a = s_best[tid];
     int rank = 0;
-#pragma unroll 8
+#pragma unroll 16
     for (int j = 0; j < 64; ++j) rank += better(s_best[j], a);
     if (rank == K - 1 && a.s) s_bound = a;
   }
   __syncthreads();
   const Score bound = s_bound;
-  if (mine.s && !better(bound, mine))
-    for (int i = tid; i < lists; i += kThreads)
-      for (int k = 0; k < K; ++k) {
-        const Score s = score_of(i, k);
-        if (!s.s || better(bound, s)) break;
-        const int at = atomicAdd(&s_n, 1);
-        if (at < kFinal) sc.score[at] = s;
-      }
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j)
+    if (mine[j].s && !better(bound, mine[j])) s_list[atomicAdd(&s_lists, 1)] = (uint16_t)(tid + j * kThreads);
+  __syncthreads();
+  for (int i = tid; i < s_lists * K; i += kThreads) {
+    const int list = s_list[i / K];
+    const Score s = score_of(list / p.slices, __ldcg(cand + (size_t)list * K + i % K));
+    if (s.s && !better(bound, s)) {
+      const int at = atomicAdd(&s_n, 1);
+      if (at < kFinal) sc.score[at] = s;
+    }
+  }
   __syncthreads();
   const int n = s_n;
   const auto place = [&](const Score& s, int r) {
-    s_parent[r] = (int)(s.at / p.V);
-    s_token[r] = (int)(s.at % p.V);
+    s_parent[r] = (int)(s.at >> 32);
+    s_token[r] = (int)(uint32_t)s.at;
     s_score[r] = (float)unrank64(s.s);
   };
   if (n <= kFinal) {
@@ -280,10 +384,10 @@ __device__ __noinline__ void choose(const Params& p, int g, Scratch& sc) {
     for (int i = tid; i < lists; i += kThreads) s_taken[i] = 0;
     __syncthreads();
     for (int r = 0; r < K; ++r) {
-      Score top{0, LLONG_MAX};
+      Score top{0, ~0ull};
       for (int i = tid; i < lists; i += kThreads)
         if (s_taken[i] < K) {
-          const Score s = score_of(i, s_taken[i]);
+          const Score s = score_of(i / p.slices, __ldcg(cand + (size_t)i * K + s_taken[i]));
           if (better(s, top)) top = s;
         }
       sc.score[tid] = top;
@@ -297,7 +401,7 @@ __device__ __noinline__ void choose(const Params& p, int g, Scratch& sc) {
       if (!got.s) break;
       if (tid == 0) {
         place(got, r);
-        s_taken[(int)(got.at / p.V) * p.slices + (int)(got.at % p.V) / kSlice] += 1;
+        s_taken[(int)(got.at >> 32) * p.slices + (int)(uint32_t)got.at / kSlice] += 1;
       }
       __syncthreads();
     }
@@ -310,8 +414,6 @@ __device__ __noinline__ void choose(const Params& p, int g, Scratch& sc) {
     s_ended[tid] = par >= 0 && p.ended ? (uint8_t)(p.ended[row0 + par] != 0 || s_token[tid] == p.eos) : (uint8_t)0;
     s_len[tid] = par >= 0 && p.seq_lens ? p.seq_lens[row0 + par] + 1 : 0;
   }
-  int len = 0;
-  if (p.history) len = p.hist_len[g];
   __syncthreads();
   if (tid < K) {
     const int par = s_parent[tid];
@@ -343,17 +445,19 @@ __device__ __noinline__ void choose(const Params& p, int g, Scratch& sc) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ Params p, bool vec) {
   __shared__ Scratch sc;
-  __shared__ uint64_t s_key[kThreads];
+  __shared__ uint64_t s_best[kThreads];
+  __shared__ __align__(16) uint32_t s_key[64];
   __shared__ uint64_t s_bound, s_sum[kThreads / 32];
-  __shared__ float s_max[kThreads / 32];
+  __shared__ uint32_t s_least;
+  __shared__ __align__(16) float s_max[kThreads / 32];
   __shared__ int s_n, s_last, s_odd;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, K = p.K;
-  const long long row = blockIdx.x / p.slices;
-  const int slice = blockIdx.x % p.slices, g = (int)(row / K);
-  Cand* out = p.cand + ((long long)row * p.slices + slice) * K;
-  Part* part = p.part + (long long)row * p.slices + slice;
+  const int row = (int)(blockIdx.x / (unsigned)p.slices), slice = (int)(blockIdx.x % (unsigned)p.slices);
+  const int g = row / K;
+  Cand* out = p.cand + ((size_t)row * p.slices + slice) * K;
+  Part* part = p.part + (size_t)row * p.slices + slice;
 
   if (p.ended && p.ended[row]) {
     // one candidate, at the beam's score
@@ -362,34 +466,40 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ 
   } else {
     Logits<T> x;
     const int first = slice * kSlice;
-    x.load(static_cast<const T*>(p.logits) + row * p.stride, first, p.V, vec);
+    const T* logits = static_cast<const T*>(p.logits) + row * p.stride;
+    x.load(logits, first, p.V, vec);
     if (tid == 0) { s_n = 0; s_odd = 0; }
     const float m = fminf(x.most(), kGreatest);
     float q = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 2));
-    if ((tid & 3) == 0) s_key[tid >> 2] = key_of(q, tid >> 2);
+    // the lowest six bits tell groups apart: a bound rounded down is still one
+    if ((tid & 3) == 0) s_key[tid >> 2] = (rank32(q) & ~63u) | (uint32_t)(tid >> 2);
     q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 4));
     q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 8));
     q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 16));
     if (lane == 0) s_max[warp] = q;
     __syncthreads();
-    float top = s_max[0];
+    float top = -INFINITY;
 #pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) top = fmaxf(top, s_max[w]);
+    for (int w = 0; w < kThreads / 128; ++w) {
+      const float4 f = reinterpret_cast<const float4*>(s_max)[w];
+      top = fmaxf(fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)), top);
+    }
     if (tid < 64) {
-      const uint64_t k = s_key[tid];
+      const uint32_t k = s_key[tid];
       int rank = 0;
-#pragma unroll 16
-      for (int j = 0; j < 64; ++j) rank += s_key[j] > k;
-      if (rank == K - 1) s_bound = k;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const uint4 u = reinterpret_cast<const uint4*>(s_key)[j];
+        rank += (u.x > k) + (u.y > k) + (u.z > k) + (u.w > k);
+      }
+      if (rank == K - 1) s_least = k & ~63u;
     }
     const float c = ceilf(top * kLog2e);  // whole, so that slices add by shifts
-    float sum[4] = {0, 0, 0, 0};
-    if (top > -INFINITY)
-      x.each([&](float v, int i) { sum[i & 3] += fast_exp2(fmaf(v, kLog2e, -c)); });
-    float z = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    float z = 0.0f;
+    if (top > -INFINITY) z = x.sum(c);
     if (!(z <= 64.0f)) s_odd = 1;         // a NaN, or a logit above kGreatest
-    const uint64_t zi = warp_sum((uint64_t)(z * kUnit));
+    const uint64_t zi = warp_sum47((uint64_t)(z * kUnit));
     if (lane == 0) s_sum[warp] = zi;
     __syncthreads();
     if (s_odd) {
@@ -397,19 +507,18 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ 
       x.each([&](float v, int) {
         if (v == v) z += fast_exp2(fmaf(fminf(v, kGreatest), kLog2e, -c));
       });
-      const uint64_t zc = warp_sum((uint64_t)(z * kUnit));
+      const uint64_t zc = warp_sum47((uint64_t)(z * kUnit));
       if (lane == 0) s_sum[warp] = zc;
     }
-    // the list of what reaches the bound
-    uint64_t bound = s_bound;
-    const float least = key_x(bound);
-    if (m >= least && m > -INFINITY)
-      x.each([&](float v, int i) {
-        if (v >= least && v > -INFINITY) {                 // (never a NaN)
-          const int at = atomicAdd(&s_n, 1);
-          if (at < kList) sc.list[at] = key_of(fminf(v, kGreatest), (uint32_t)x.token(first, i));
-        }
-      });
+    // the list of what reaches the bound (read again: registers have no index)
+    const float least = fmaxf(unrank32(s_least), x.lowest());    // (where fewer than K are finite)
+    if (m >= least)
+      for (uint32_t bits = x.reach(least); bits; bits &= bits - 1) {
+        const int at = atomicAdd(&s_n, 1);
+        if (at >= kList) break;
+        const int t = x.token(first, x.place(__ffs(bits) - 1));
+        sc.list[at] = key_of(fminf(one_in(logits[t]), kGreatest), (uint32_t)t);
+      }
     __syncthreads();
     int n = s_n;
     if (n > kList) {
@@ -421,14 +530,14 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ 
           if (k > best) best = k;
         }
       });
-      s_key[tid] = best;
+      s_best[tid] = best;
       __syncthreads();
       if (tid == 0) s_n = 0;
       int rank = 0;
-      for (int j = 0; j < kThreads; ++j) rank += s_key[j] > best || (s_key[j] == best && j < tid);
+      for (int j = 0; j < kThreads; ++j) rank += s_best[j] > best || (s_best[j] == best && j < tid);
       if (rank == K - 1) s_bound = best;
       __syncthreads();
-      bound = s_bound;
+      const uint64_t bound = s_bound;
       if (best >= bound)
         x.each([&](float v, int i) {
           if (v == v && v > -INFINITY) {
