@@ -686,8 +686,7 @@ int ssa_prompt_attention(int dtype, int head_dim, int n_seqs, int n_q, int n_kv,
  * be of one parent.  Sums and scores in double, one rounding to fp32 at the end.
  *   dtype     SSA_BF16, SSA_F16 or SSA_F32, of the logits
  *   logits    [groups * beams] rows, row_stride elements apart
- *   groups    at most 65,535
- *   beams     at most 32, beams * ceil(vocab / 8192) <= 1024 (SSA_ERR_UNSUPPORTED)
+ *   groups at most 65,535, beams at most 32, vocab at most 2^23 (SSA_ERR_UNSUPPORTED)
  *   in, out   the rows' state before and after; out may be in:
  *     scores    [groups * beams] fp32 (a first step: 0 for one row of a group
  *               and -infinity for the others)

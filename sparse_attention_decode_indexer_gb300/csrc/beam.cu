@@ -6,27 +6,31 @@
 // a beam that has ended has one candidate, (r, eos) at score[r].  The K = beams
 // best of a group win, the first beam and then the first token among equals.
 //
-// What bounds it: the logits, read once.  A CTA takes 8,192 of a row's logits
-// into registers and leaves the sum of their exponentials and the K best; the
-// last CTA of a group (a ticket) puts these together.  41 M logits are 270,000
-// to an SM, so every instruction per logit counts: 16-bit logits stay in words,
-// two to a maximum, and the exponential is one product, 2^(x log2e - c).
+// What bounds it: the logits, read once.  A CTA takes a part of a row, 64 bytes a
+// thread at a time with the next 64 in flight, and leaves the sum of their
+// exponentials and the K best; the last CTA of a group (a ticket) puts these
+// together.  41 M logits are 270,000 to an SM, so every instruction per logit
+// counts: 16-bit logits stay in words, two to a maximum, and the exponential is
+// one product, 2^(x log2e - c).
 //
 // The K best of what the threads of a CTA hold: the greatest of each four
-// threads; the K-th of these 64 is a bound that at least K values reach.  The
-// values that reach it, few more than K, go to a list, in which each finds its
-// rank by counting; values are compared together with their index, so no two
-// are equal and the order of the list does not matter.  Where many values
+// threads; the K-th of these 64 is a bound that at least K values reach, and so
+// is the K-th best of the chunks before.  The values that reach it, few more
+// than K, go to a list, in which each finds its rank by counting; values are
+// compared together with their index, so no two are equal and the order of the
+// list does not matter.  Where many values
 // equal the bound (a mask of one finite value) the list would overflow: then the
 // bound is taken over (value, index) of each thread, which at most K threads'
 // values reach.
 //
-// Sums are 64-bit integers in units of 2^-40 beside a largest term above 1/2, so
-// they do not depend on any order.  Double arithmetic (two operations a clock
+// Sums are 64-bit integers in units of 2^-40 beside a largest term above 1/2 (so at
+// most 2^23 terms), which do not depend on any order.  Double arithmetic (two operations a clock
 // and SM here) makes the logarithms and adds the scores, so that candidates of
 // different beams are ordered by what they are and not by a rounding to fp32:
 // an exponential is off by about 2^-22, an average over many by less.  2^(x L),
 // L = log2e rounded to fp32, in place of e^x is off by 2e-8 of the row's entropy.
+// Beyond 2^20 (masks of some large number) c, an fp32 product, would no longer be
+// the logit it stands for: there sums are taken against the logit itself.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -37,20 +41,21 @@ namespace ssa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 32;                  // logits of a thread
-constexpr int kSlice = kThreads * kPer;
+constexpr int kCtas = 4;                  // per SM
+constexpr int kBytes = 64;                // of a chunk of logits, a thread
 constexpr int kMaxBeams = 32;
-constexpr int kMaxLists = 1024;           // (row, slice) lists of a group
-constexpr int kList = 1024;               // values in a CTA's list
+constexpr int kMaxLists = 1024;           // (row, part) lists of a group
+constexpr int kList = kMaxBeams * 33;     // values in a CTA's list: K threads' 32, and K kept
 constexpr int kFinal = 512;               // candidates in a group's list
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGreatest = 0x1p126f;     // logits above it count as it: its product with kLog2e is finite
 constexpr float kUnit = 0x1p40f;          // of the sums
+constexpr float kFar = 0x1p20f;           // references further out are logits, not octaves
 
-struct Part {                             // of a slice: sum * 2^(c - 40) is its sum of 2^(x kLog2e)
+struct Part {                             // of a row: sum * 2^(c - 40) is its sum of 2^(x kLog2e)
   uint64_t sum;
   float c;                                // -infinity: no logit
-  int pad;
+  float ref;                              // the reference as a logit, where it is beyond kFar; else infinity
 };
 struct Cand {                             // logit and token; token < 0: none
   float x;
@@ -60,7 +65,7 @@ struct Cand {                             // logit and token; token < 0: none
 struct Params {
   const void* logits;
   int64_t stride;
-  int K, V, slices, max_len, eos;
+  int K, V, parts, chunks, max_len, eos;  // parts of a row, chunks of a part
   const float* scores;
   const uint8_t* ended;
   const int32_t *history, *hist_len, *seq_lens;
@@ -68,8 +73,8 @@ struct Params {
   uint8_t* ended_out;
   int32_t *history_out, *hist_len_out, *new_lens, *parent, *token;
   int32_t* status;
-  Part* part;                             // [row][slice]
-  Cand* cand;                             // [row][slice][K]
+  Part* part;                             // [row][part]
+  Cand* cand;                             // [row][part][K]
   int32_t* ticket;                        // [group], zero between calls
   int32_t* old_len;                       // [group], for the kernel that moves the histories
   int move_here;                          // histories are moved by the group's last CTA
@@ -131,10 +136,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// A thread's logits: 32 of them, in 16-byte pieces 16 * kThreads bytes apart.
+// A thread's logits of a chunk, in 16-byte pieces 16 * kThreads bytes apart.
 template <typename T> struct Logits {
   static constexpr int N = 16 / sizeof(T);              // of a piece
-  static constexpr int W = kPer * sizeof(T) / 4;        // words
+  static constexpr int W = kBytes / 4;                  // words
+  static constexpr int M = kBytes / sizeof(T);          // logits
+  static constexpr int kChunk = M * kThreads;
   uint32_t w[W];
 
   static __device__ __forceinline__ float lowest() {    // that is finite
@@ -145,10 +152,10 @@ template <typename T> struct Logits {
     if constexpr (sizeof(T) == 4) return 0xFF800000u;
     else return std::is_same_v<T, __half> ? 0xFC00FC00u : 0xFF80FF80u;
   }
-  __device__ __forceinline__ void load(const T* row, int first, int V, bool vec) {
+  __device__ __forceinline__ void load(const T* row, long long first, int V, bool vec) {
 #pragma unroll
-    for (int j = 0; j < kPer / N; ++j) {
-      const int at = first + (j * kThreads + (int)threadIdx.x) * N;
+    for (int j = 0; j < M / N; ++j) {
+      const long long at = first + (j * kThreads + (int)threadIdx.x) * N;
       if (vec && at + N <= V) {
         const uint4 u = __ldcs(reinterpret_cast<const uint4*>(row + at));
         w[4 * j] = u.x; w[4 * j + 1] = u.y; w[4 * j + 2] = u.z; w[4 * j + 3] = u.w;
@@ -205,7 +212,7 @@ template <typename T> struct Logits {
     const uint64_t l2 = pack2(kLog2e, kLog2e), c2 = pack2(-c, -c);
     uint64_t s[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < kPer / 2; ++i) {
+    for (int i = 0; i < M / 2; ++i) {
       uint64_t x;
       if constexpr (sizeof(T) == 4) {
         x = pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
@@ -218,6 +225,22 @@ template <typename T> struct Logits {
     }
     const float2 r = unpack2(add2(s[0], s[1]));
     return r.x + r.y;
+  }
+  // the same, NaN aside
+  __device__ __forceinline__ float sum_clean(float c) const {
+    float s = 0.0f;
+    each([&](float v, int) {
+      if (v == v) s += fast_exp2(fmaf(v, kLog2e, -c));
+    });
+    return s;
+  }
+  // the sum of e^(x - ref), NaN aside: any magnitude
+  __device__ __forceinline__ float sum_from(float ref) const {
+    float s = 0.0f;
+    each([&](float v, int) {
+      if (v == v) s += fast_exp2((fminf(v, kGreatest) - ref) * kLog2e);
+    });
+    return s;
   }
   // which of them are at least `least` (never a NaN): bit i the thread's i-th
   __device__ __forceinline__ uint32_t reach(float least) const {
@@ -263,315 +286,367 @@ union Scratch {
   int32_t move[2048];
 };
 
+// The K-th greatest of the threads' numbers (0: none), or something below it that
+// no more than K reach; N numbers a thread.
+template <int N> __device__ __forceinline__ uint32_t kth(const uint32_t (&x)[N], int K) {
+  uint32_t lo = 0;                        // at least K reach it, or it is 0
+  for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
+    const uint32_t mid = lo | bit;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += __syncthreads_count(x[i] >= mid);
+    if (n >= K) lo = mid;
+    if (n == K) break;
+  }
+  return lo;
+}
+
 // The group's choice and the new states, by the group's last CTA.  What it takes
-// is round trips to L2, one after another, so loads go out together: the parts
-// and the lists' first candidates, then the lists that reach the bound.
+// is round trips to L2, one after another, so loads go out together: the parts,
+// the lists' first candidates and the old states; then the K lists whose first
+// candidates are the best, among which the K best are.
 __device__ __noinline__ void choose(const Params& p, int g, Scratch& sc) {
   constexpr int kPerThread = kMaxLists / kThreads;
-  const int K = p.K, lists = K * p.slices, tid = threadIdx.x, lane = tid & 31;
-  __shared__ double s_add[kMaxBeams], s_lse[kMaxBeams];
+  const int K = p.K, lists = K * p.parts, tid = threadIdx.x, lane = tid & 31;
+  __shared__ double s_add[kMaxBeams], s_ref[kMaxBeams], s_ln[kMaxBeams];
   __shared__ uint64_t s_z[kMaxBeams];
-  __shared__ float s_c[kMaxBeams];
-  __shared__ Score s_best[64], s_bound;
-  __shared__ int s_n, s_lists, s_parent[kMaxBeams], s_token[kMaxBeams], s_len[kMaxBeams];
+  __shared__ float s_c[kMaxBeams], s_far[kMaxBeams];
+  __shared__ int s_n, s_lists, s_parent[kMaxBeams], s_token[kMaxBeams], s_lens[kMaxBeams];
   __shared__ uint16_t s_list[kMaxLists];
-  __shared__ uint8_t s_ended[kMaxBeams], s_taken[kMaxLists];
+  __shared__ uint8_t s_old[kMaxBeams], s_taken[kMaxLists];
   __shared__ float s_score[kMaxBeams];
-  const long long row0 = (long long)g * K;
-  const int2* cand = reinterpret_cast<const int2*>(p.cand + row0 * p.slices * K);
+  const int row0 = g * K;
+  const int2* cand = reinterpret_cast<const int2*>(p.cand + (size_t)row0 * p.parts * K);
   int2 head[kPerThread];                  // a list is sorted: its first is its best
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
     const int i = tid + j * kThreads;
     head[j] = i < lists ? __ldcg(cand + (size_t)i * K) : make_int2(0, -1);
   }
-  float add = 0.0f;
-  bool ended = false;
-  if (tid < K) {
-    add = p.scores[row0 + tid];
-    ended = p.ended && p.ended[row0 + tid];
+  if (tid < K) {                          // everything old: in and out may be the same
+    s_add[tid] = p.scores[row0 + tid];
+    s_old[tid] = p.ended ? p.ended[row0 + tid] : 0;
+    s_lens[tid] = p.seq_lens ? p.seq_lens[row0 + tid] : 0;
+    s_parent[tid] = s_token[tid] = -1;
+    s_score[tid] = -INFINITY;
   }
   int len = 0;
   if (p.history) len = p.hist_len[g];
   for (int r = tid >> 5; r < K; r += kThreads / 32) {
-    const uint4* part = reinterpret_cast<const uint4*>(p.part + (row0 + r) * p.slices);
-    float c = -INFINITY;
+    const uint4* part = reinterpret_cast<const uint4*>(p.part + (size_t)(row0 + r) * p.parts);
+    float c = -INFINITY, far = -INFINITY;
     uint64_t z = 0;
-    for (int i = lane; i < p.slices; i += 32) {
+    for (int i = lane; i < p.parts; i += 32) {
       const uint4 u = __ldcg(part + i);
       const uint64_t s = (uint64_t)u.y << 32 | u.x;
       const float pc = __uint_as_float(u.z);
       if (pc > c) {
         z = (c > -INFINITY ? z >> (int)fminf(pc - c, 63.0f) : 0) + s;
         c = pc;
+        far = __uint_as_float(u.w);
       } else if (pc > -INFINITY) {
         z += s >> (int)fminf(c - pc, 63.0f);
+        if (pc == c) far = fmaxf(far, __uint_as_float(u.w));
       }
     }
     const float top = warp_max(c);
+    far = warp_max(c == top ? far : -INFINITY);
     z = warp_sum(c > -INFINITY ? z >> (int)fminf(top - c, 63.0f) : 0);
-    if (lane == 0) { s_z[r] = z; s_c[r] = top; }
+    if (lane == 0) { s_z[r] = z; s_c[r] = top; s_far[r] = far; }
   }
-  if (tid == 0) { s_n = s_lists = 0; s_bound = Score{0, ~0ull}; }
-  if (tid < K) { s_parent[tid] = s_token[tid] = -1; s_score[tid] = -INFINITY; }
+  if (tid == 0) s_n = s_lists = 0;
   __syncthreads();
   if (tid < K) {
-    s_add[tid] = add;
-    s_lse[tid] = ended || s_z[tid] == 0 ? 0.0 : ((double)s_c[tid] - 40.0 + log2((double)s_z[tid])) * (1.0 / (double)kLog2e);
+    // ln of the sum = ref + ln, apart: beside a far reference ln would be lost
+    const bool none = s_old[tid] || s_z[tid] == 0;
+    s_ref[tid] = none ? 0.0 : s_far[tid] < INFINITY ? (double)s_far[tid] : (double)s_c[tid] * (1.0 / (double)kLog2e);
+    s_ln[tid] = none ? 0.0 : (log2((double)s_z[tid]) - 40.0) * (1.0 / (double)kLog2e);
   }
   __syncthreads();
 
   const auto score_of = [&](int r, int2 c) {
     Score s{0, ~0ull};
     if (c.y >= 0) {
-      const double v = ((double)__int_as_float(c.x) - s_lse[r]) + s_add[r];
+      const double v = ((double)__int_as_float(c.x) - s_ref[r]) - s_ln[r] + s_add[r];
       if (v > -INFINITY) { s.s = rank64(v); s.at = (uint64_t)r << 32 | (uint32_t)c.y; }
     }
     return s;
   };
-  Score mine[kPerThread], best{0, ~0ull};
+  // (the upper half of a score's rank is in its order)
+  uint32_t most[kPerThread];
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
-    mine[j] = Score{0, ~0ull};
-    if (tid + j * kThreads < lists) mine[j] = score_of((tid + j * kThreads) / p.slices, head[j]);
-    if (better(mine[j], best)) best = mine[j];
+    const int i = tid + j * kThreads;
+    most[j] = i < lists ? (uint32_t)(score_of(i / p.parts, head[j]).s >> 32) : 0u;
   }
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    const Score s{__shfl_xor_sync(0xffffffffu, best.s, o), __shfl_xor_sync(0xffffffffu, best.at, o)};
-    if (better(s, best)) best = s;
+  uint32_t bound;
+  if (lists <= kThreads) {
+    const uint32_t one[1] = {most[0]};
+    bound = kth(one, K);
+  } else {
+    bound = kth(most, K);
   }
-  if ((tid & 3) == 0) s_best[tid >> 2] = best;
-  __syncthreads();
-  if (tid < 64) {
-    const Score a = s_best[tid];
-    int rank = 0;
-#pragma unroll 16
-    for (int j = 0; j < 64; ++j) rank += better(s_best[j], a);
-    if (rank == K - 1 && a.s) s_bound = a;
-  }
-  __syncthreads();
-  const Score bound = s_bound;
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j)
-    if (mine[j].s && !better(bound, mine[j])) s_list[atomicAdd(&s_lists, 1)] = (uint16_t)(tid + j * kThreads);
+    if (most[j] && most[j] >= bound) s_list[atomicAdd(&s_lists, 1)] = (uint16_t)(tid + j * kThreads);
   __syncthreads();
-  for (int i = tid; i < s_lists * K; i += kThreads) {
-    const int list = s_list[i / K];
-    const Score s = score_of(list / p.slices, __ldcg(cand + (size_t)list * K + i % K));
-    if (s.s && !better(bound, s)) {
-      const int at = atomicAdd(&s_n, 1);
-      if (at < kFinal) sc.score[at] = s;
-    }
-  }
-  __syncthreads();
-  const int n = s_n;
+  const int some = s_lists * K;           // candidates of those lists
   const auto place = [&](const Score& s, int r) {
     s_parent[r] = (int)(s.at >> 32);
     s_token[r] = (int)(uint32_t)s.at;
     s_score[r] = (float)unrank64(s.s);
   };
+  if (some <= kMaxLists) {
+    Score mine[kPerThread];
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      const int i = tid + j * kThreads;
+      mine[j] = Score{0, ~0ull};
+      if (i < some) {
+        const int list = s_list[i / K];
+        mine[j] = score_of(list / p.parts, __ldcg(cand + (size_t)list * K + i % K));
+      }
+      most[j] = (uint32_t)(mine[j].s >> 32);
+    }
+    if (some <= kThreads) {
+      const uint32_t one[1] = {most[0]};
+      bound = kth(one, K);
+    } else {
+      bound = kth(most, K);
+    }
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j)
+      if (most[j] && most[j] >= bound) {
+        const int at = atomicAdd(&s_n, 1);
+        if (at < kFinal) sc.score[at] = mine[j];
+      }
+  } else if (tid == 0) {
+    s_n = kFinal + 1;
+  }
+  __syncthreads();
+  const int n = s_n;
   if (n <= kFinal) {
     for (int i = tid; i < n; i += kThreads) {
       const Score s = sc.score[i];
       int r = 0;
+#pragma unroll 4
       for (int j = 0; j < n; ++j) r += better(sc.score[j], s);
       if (r < K) place(s, r);
     }
   } else {
-    // more than the list holds (rows that lie close together): the best of the
-    // lists' next ones, K times
+    // more than the list holds (many that are equal): the best of the lists'
+    // next ones, K times
     for (int i = tid; i < lists; i += kThreads) s_taken[i] = 0;
     __syncthreads();
     for (int r = 0; r < K; ++r) {
       Score top{0, ~0ull};
       for (int i = tid; i < lists; i += kThreads)
         if (s_taken[i] < K) {
-          const Score s = score_of(i / p.slices, __ldcg(cand + (size_t)i * K + s_taken[i]));
-          if (better(s, top)) top = s;
+          const Score s = score_of(i / p.parts, __ldcg(cand + (size_t)i * K + s_taken[i]));
+          if (better(s, top)) {
+            top = s;
+            s_list[tid] = (uint16_t)i;    // the list it came from
+          }
         }
       sc.score[tid] = top;
       __syncthreads();
-      for (int o = kThreads / 2; o; o >>= 1) {
-        if (tid < o && better(sc.score[tid + o], sc.score[tid])) sc.score[tid] = sc.score[tid + o];
-        __syncthreads();
-      }
-      const Score got = sc.score[0];
-      __syncthreads();
-      if (!got.s) break;
       if (tid == 0) {
-        place(got, r);
-        s_taken[(int)(got.at >> 32) * p.slices + (int)(uint32_t)got.at / kSlice] += 1;
+        int from = 0;
+        for (int i = 1; i < kThreads; ++i)
+          if (better(sc.score[i], sc.score[from])) from = i;
+        if (sc.score[from].s) {
+          place(sc.score[from], r);
+          s_taken[s_list[from]] += 1;
+        }
       }
       __syncthreads();
     }
   }
   __syncthreads();
 
-  // states: everything old is read before anything new is written, in and out may be the same
   if (tid < K) {
     const int par = s_parent[tid];
-    s_ended[tid] = par >= 0 && p.ended ? (uint8_t)(p.ended[row0 + par] != 0 || s_token[tid] == p.eos) : (uint8_t)0;
-    s_len[tid] = par >= 0 && p.seq_lens ? p.seq_lens[row0 + par] + 1 : 0;
-  }
-  __syncthreads();
-  if (tid < K) {
-    const int par = s_parent[tid];
-    p.parent[row0 + tid] = par < 0 ? -1 : (int)(row0 + par);
+    p.parent[row0 + tid] = par < 0 ? -1 : row0 + par;
     p.token[row0 + tid] = s_token[tid];
     p.scores_out[row0 + tid] = s_score[tid];
-    if (p.ended_out) p.ended_out[row0 + tid] = s_ended[tid];
-    if (p.new_lens) p.new_lens[row0 + tid] = s_len[tid];
+    if (p.ended_out) p.ended_out[row0 + tid] = par >= 0 && (s_old[par] || s_token[tid] == p.eos);
+    if (p.new_lens) p.new_lens[row0 + tid] = par >= 0 ? s_lens[par] + 1 : 0;
   }
   if (!p.history) return;
   const bool full = len < 0 || len >= p.max_len;
   if (full && tid == 0) set_status(p.status, SSA_ST_BAD_POS);
   len = min(max(len, 0), p.max_len);
   if (p.move_here) {                      // K * max_len fit the scratch
-    for (int i = tid; i < K * len; i += kThreads) {
-      const int par = s_parent[i / len];
-      if (par >= 0) sc.move[i] = p.history[(row0 + par) * p.max_len + i % len];
-    }
+    for (int i = 0; i < K; ++i)
+      if (s_parent[i] >= 0)
+        for (int c = tid; c < len; c += kThreads)
+          sc.move[i * len + c] = p.history[(long long)(row0 + s_parent[i]) * p.max_len + c];
     __syncthreads();
-    for (int i = tid; i < K * len; i += kThreads)
-      if (s_parent[i / len] >= 0) p.history_out[(row0 + i / len) * p.max_len + i % len] = sc.move[i];
+    for (int i = 0; i < K; ++i)
+      if (s_parent[i] >= 0)
+        for (int c = tid; c < len; c += kThreads)
+          p.history_out[(long long)(row0 + i) * p.max_len + c] = sc.move[i * len + c];
   } else if (tid == 0) {
     p.old_len[g] = len;
   }
-  if (!full && tid < K && s_parent[tid] >= 0) p.history_out[(row0 + tid) * p.max_len + len] = s_token[tid];
+  if (!full && tid < K && s_parent[tid] >= 0) p.history_out[(long long)(row0 + tid) * p.max_len + len] = s_token[tid];
   if (tid == 0) p.hist_len_out[g] = full ? len : len + 1;
 }
 
+// A CTA takes a part of a row, chunk after chunk, the next one's loads in flight.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ Params p, bool vec) {
+__global__ void __launch_bounds__(kThreads, kCtas) beam_kernel(const __grid_constant__ Params p, bool vec) {
+  using X = Logits<T>;
   __shared__ Scratch sc;
-  __shared__ uint64_t s_best[kThreads];
+  __shared__ uint64_t s_best[kThreads], s_keep[kMaxBeams];
   __shared__ __align__(16) uint32_t s_key[64];
   __shared__ uint64_t s_bound, s_sum[kThreads / 32];
   __shared__ uint32_t s_least;
   __shared__ __align__(16) float s_max[kThreads / 32];
-  __shared__ int s_n, s_last, s_odd;
+  __shared__ int s_n, s_last;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, K = p.K;
-  const int row = (int)(blockIdx.x / (unsigned)p.slices), slice = (int)(blockIdx.x % (unsigned)p.slices);
+  const int row = (int)(blockIdx.x / (unsigned)p.parts), part = (int)(blockIdx.x % (unsigned)p.parts);
   const int g = row / K;
-  Cand* out = p.cand + ((size_t)row * p.slices + slice) * K;
-  Part* part = p.part + (size_t)row * p.slices + slice;
+  Cand* out = p.cand + ((size_t)row * p.parts + part) * K;
+  Part* left = p.part + (size_t)row * p.parts + part;
 
   if (p.ended && p.ended[row]) {
     // one candidate, at the beam's score
-    if (tid < K) out[tid] = Cand{0.0f, slice == p.eos / kSlice && tid == 0 ? p.eos : -1};
-    if (tid == 0) *part = Part{0, -INFINITY, 0};
+    if (tid < K) out[tid] = Cand{0.0f, part == 0 && tid == 0 ? p.eos : -1};
+    if (tid == 0) *left = Part{0, -INFINITY, INFINITY};
   } else {
-    Logits<T> x;
-    const int first = slice * kSlice;
     const T* logits = static_cast<const T*>(p.logits) + row * p.stride;
-    x.load(logits, first, p.V, vec);
-    if (tid == 0) { s_n = 0; s_odd = 0; }
-    const float m = fminf(x.most(), kGreatest);
-    float q = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 2));
-    // the lowest six bits tell groups apart: a bound rounded down is still one
-    if ((tid & 3) == 0) s_key[tid >> 2] = (rank32(q) & ~63u) | (uint32_t)(tid >> 2);
-    q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 4));
-    q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 8));
-    q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 16));
-    if (lane == 0) s_max[warp] = q;
-    __syncthreads();
-    float top = -INFINITY;
+    const long long begin = (long long)part * p.chunks * X::kChunk;
+    const long long end = min((long long)p.V, begin + (long long)p.chunks * X::kChunk);
+    X x;
+    x.load(logits, begin, p.V, vec);
+    if (tid == 0) s_n = 0;
+    int kept = 0;                         // of the list, the best so far
+    float c = -INFINITY;                  // the reference of the sum: whole octaves, so that parts add by shifts,
+    float reached = X::lowest();          // the K-th best so far
+    float far = INFINITY;                 // or this logit, where it is far out
+    uint64_t z = 0;                       // the warp's sum
+    for (long long first = begin; first < end; first += X::kChunk) {
+      X next;
+      if (first + X::kChunk < end) next.load(logits, first + X::kChunk, p.V, vec);
+      const float m = fminf(x.most(), kGreatest);
+      float q = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 2));
+      // the lowest six bits tell groups apart: a bound rounded down is still one
+      if ((tid & 3) == 0) s_key[tid >> 2] = (rank32(q) & ~63u) | (uint32_t)(tid >> 2);
+      q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 4));
+      q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 8));
+      q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 16));
+      if (lane == 0) s_max[warp] = q;
+      __syncthreads();
+      float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kThreads / 128; ++w) {
-      const float4 f = reinterpret_cast<const float4*>(s_max)[w];
-      top = fmaxf(fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)), top);
-    }
-    if (tid < 64) {
-      const uint32_t k = s_key[tid];
-      int rank = 0;
+      for (int w = 0; w < kThreads / 128; ++w) {
+        const float4 f = reinterpret_cast<const float4*>(s_max)[w];
+        top = fmaxf(fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)), top);
+      }
+      if (tid < 64) {
+        const uint32_t k = s_key[tid];
+        int rank = 0;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const uint4 u = reinterpret_cast<const uint4*>(s_key)[j];
-        rank += (u.x > k) + (u.y > k) + (u.z > k) + (u.w > k);
-      }
-      if (rank == K - 1) s_least = k & ~63u;
-    }
-    const float c = ceilf(top * kLog2e);  // whole, so that slices add by shifts
-    float z = 0.0f;
-    if (top > -INFINITY) z = x.sum(c);
-    if (!(z <= 64.0f)) s_odd = 1;         // a NaN, or a logit above kGreatest
-    const uint64_t zi = warp_sum47((uint64_t)(z * kUnit));
-    if (lane == 0) s_sum[warp] = zi;
-    __syncthreads();
-    if (s_odd) {
-      z = 0.0f;
-      x.each([&](float v, int) {
-        if (v == v) z += fast_exp2(fmaf(fminf(v, kGreatest), kLog2e, -c));
-      });
-      const uint64_t zc = warp_sum47((uint64_t)(z * kUnit));
-      if (lane == 0) s_sum[warp] = zc;
-    }
-    // the list of what reaches the bound (read again: registers have no index)
-    const float least = fmaxf(unrank32(s_least), x.lowest());    // (where fewer than K are finite)
-    if (m >= least)
-      for (uint32_t bits = x.reach(least); bits; bits &= bits - 1) {
-        const int at = atomicAdd(&s_n, 1);
-        if (at >= kList) break;
-        const int t = x.token(first, x.place(__ffs(bits) - 1));
-        sc.list[at] = key_of(fminf(one_in(logits[t]), kGreatest), (uint32_t)t);
-      }
-    __syncthreads();
-    int n = s_n;
-    if (n > kList) {
-      // many equal ones: bounded over (value, token) instead
-      uint64_t best = 0;
-      x.each([&](float v, int i) {
-        if (v == v) {
-          const uint64_t k = key_of(fminf(v, kGreatest), (uint32_t)x.token(first, i));
-          if (k > best) best = k;
+        for (int j = 0; j < 16; ++j) {
+          const uint4 u = reinterpret_cast<const uint4*>(s_key)[j];
+          rank += (u.x > k) + (u.y > k) + (u.z > k) + (u.w > k);
         }
-      });
-      s_best[tid] = best;
+        if (rank == K - 1) s_least = k & ~63u;
+      }
+      if (top > -INFINITY) {
+        const bool is_far = fabsf(top) >= kFar;
+        const float tc = is_far ? fmaxf(top, -kGreatest) * kLog2e : ceilf(top * kLog2e);
+        if (tc > c || (tc == c && is_far && top > far)) {
+          if (c > -INFINITY) z >>= (int)fminf(is_far && far < INFINITY ? (top - far) * kLog2e : tc - c, 63.0f);
+          c = tc;
+          far = is_far ? top : INFINITY;
+        }
+      }
+      float sum = 0.0f;
+      if (c > -INFINITY) sum = far < INFINITY ? x.sum_from(far) : x.sum(c);
+      if (!(sum <= 64.0f)) sum = x.sum_clean(c);      // a NaN among them
+      const uint64_t zi = warp_sum47((uint64_t)(sum * kUnit));
+      z += zi;
+      if (lane == 0 && first + X::kChunk >= end) s_sum[warp] = z;
       __syncthreads();
-      if (tid == 0) s_n = 0;
-      int rank = 0;
-      for (int j = 0; j < kThreads; ++j) rank += s_best[j] > best || (s_best[j] == best && j < tid);
-      if (rank == K - 1) s_bound = best;
+      // the list of what reaches the bound (read again: registers have no index)
+      const float least = fmaxf(unrank32(s_least), reached);    // (a NaN where fewer than K are finite)
+      if (m >= least)
+        for (uint32_t bits = x.reach(least); bits; bits &= bits - 1) {
+          const int at = kept + atomicAdd(&s_n, 1);
+          if (at >= kList) break;
+          const int t = x.token(first, x.place(__ffs(bits) - 1));
+          sc.list[at] = key_of(fminf(one_in(logits[t]), kGreatest), (uint32_t)t);
+        }
       __syncthreads();
-      const uint64_t bound = s_bound;
-      if (best >= bound)
+      int n = kept + s_n;
+      if (n > kList) {
+        // many equal ones: bounded over (value, token) instead
+        uint64_t best = 0;
         x.each([&](float v, int i) {
-          if (v == v && v > -INFINITY) {
+          if (v == v) {
             const uint64_t k = key_of(fminf(v, kGreatest), (uint32_t)x.token(first, i));
-            if (k >= bound) sc.list[atomicAdd(&s_n, 1)] = k;
+            if (k > best) best = k;
           }
         });
-      __syncthreads();
-      n = s_n;
+        s_best[tid] = best;
+        __syncthreads();
+        if (tid == 0) s_n = 0;
+        int rank = 0;
+        for (int j = 0; j < kThreads; ++j) rank += s_best[j] > best || (s_best[j] == best && j < tid);
+        if (rank == K - 1) s_bound = best;
+        __syncthreads();
+        const uint64_t bound = s_bound;
+        if (best >= bound)
+          x.each([&](float v, int i) {
+            if (v == v && v > -INFINITY) {
+              const uint64_t k = key_of(fminf(v, kGreatest), (uint32_t)x.token(first, i));
+              if (k >= bound) sc.list[kept + atomicAdd(&s_n, 1)] = k;
+            }
+          });
+        __syncthreads();
+        n = kept + s_n;
+      }
+      if (n > kept) {
+        for (int i = tid; i < n; i += kThreads) {
+          const uint64_t k = sc.list[i];
+          int r = 0;
+#pragma unroll 4
+          for (int j = 0; j < n; ++j) r += sc.list[j] > k;
+          if (r < K) s_keep[r] = k;
+        }
+        __syncthreads();
+        kept = min(n, K);
+        if (tid < kept) sc.list[tid] = s_keep[tid];
+        if (kept == K) reached = key_x(s_keep[K - 1]);
+        if (tid == 0) s_n = 0;
+        // (the next chunk's first barrier comes before either is used again)
+      }
+      x = next;
     }
-    if (tid < K && tid >= n) out[tid] = Cand{0.0f, -1};
-    for (int i = tid; i < n; i += kThreads) {
-      const uint64_t k = sc.list[i];
-      int r = 0;
-      for (int j = 0; j < n; ++j) r += sc.list[j] > k;
-      if (r < K) out[r] = Cand{key_x(k), (int)~(uint32_t)k};
-    }
+    if (tid < K) out[tid] = tid < kept ? Cand{key_x(s_keep[tid]), (int)~(uint32_t)s_keep[tid]} : Cand{0.0f, -1};
     if (tid == 0) {
       uint64_t s = 0;
       for (int w = 0; w < kThreads / 32; ++w) s += s_sum[w];
-      *part = Part{s, top > -INFINITY ? c : -INFINITY, 0};
+      *left = Part{s, c, far};
     }
   }
-  // the last CTA of the group goes on
-  __threadfence();
+  // the last CTA of the group goes on: one thread's release covers what the CTA wrote before the
+  // barrier, its acquire what the others released
   __syncthreads();
   if (tid == 0) {
-    const int last = atomicAdd(p.ticket + g, 1) == K * p.slices - 1;
+    uint32_t before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(p.ticket + g) : "memory");
+    const bool last = before == (uint32_t)(K * p.parts - 1);
     if (last) p.ticket[g] = 0;
     s_last = last;
   }
   __syncthreads();
   if (!s_last) return;
-  __threadfence();
   choose(p, g, sc);
 }
 
@@ -596,17 +671,18 @@ __global__ void __launch_bounds__(kMoveThreads) beam_move_kernel(const __grid_co
     if (p.parent[row0 + i] >= 0) p.history_out[(row0 + i) * p.max_len + c] = s_col[i * kMoveThreads + tid];
 }
 
-int slices_of(int V) { return (V + kSlice - 1) / kSlice; }
-
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 template <typename T>
-cudaError_t launch(const Params& p, int groups, cudaStream_t s) {
+cudaError_t launch(Params p, int groups, cudaStream_t s) {
   constexpr int N = 16 / sizeof(T);
   const bool vec = !((uintptr_t)p.logits & 15) && (p.stride % N == 0 || groups * p.K == 1);
-  const long long ctas = (long long)groups * p.K * p.slices;
-  if (ctas > INT_MAX) return cudaErrorInvalidValue;
-  cudaError_t e = launch_pdl(beam_kernel<T>, dim3((unsigned)ctas), dim3(kThreads), 0, s, p, vec);
+  // parts of a row: as many as one wave of CTAs has room for, whole chunks each
+  const int rows = groups * p.K, all = (int)(((long long)p.V + Logits<T>::kChunk - 1) / Logits<T>::kChunk);
+  const int room = std::max(1, std::min(kMaxLists, current_device_info().sms * kCtas) / rows);
+  p.chunks = (all + room - 1) / room;
+  p.parts = (all + p.chunks - 1) / p.chunks;
+  cudaError_t e = launch_pdl(beam_kernel<T>, dim3((unsigned)(rows * p.parts)), dim3(kThreads), 0, s, p, vec);
   count_launch();
   if (e != cudaSuccess || !p.history || p.move_here) return e;
   e = launch_pdl(beam_move_kernel, dim3((p.max_len + kMoveThreads - 1) / kMoveThreads, groups), dim3(kMoveThreads),
@@ -623,7 +699,7 @@ extern "C" {
 size_t ssa_beam_workspace_size(int groups, int beams) {
   using namespace ssa;
   if (groups < 1 || beams < 1 || beams > kMaxBeams) return 0;
-  const size_t lists = (size_t)groups * kMaxLists;
+  const size_t lists = std::max((size_t)groups * beams, (size_t)kMaxLists);
   return 2 * align256((size_t)groups * 4) + align256(lists * sizeof(Part)) + align256(lists * beams * sizeof(Cand));
 }
 
@@ -634,8 +710,7 @@ int ssa_beam_select(int dtype, int groups, int beams, int vocab, const void* log
   using namespace ssa;
   if (dtype < SSA_BF16 || dtype > SSA_F32) return SSA_ERR_UNSUPPORTED;
   if (groups < 1 || beams < 1 || vocab < 1 || max_len < 0 || eos < -1 || eos >= vocab) return SSA_ERR_INVALID_ARG;
-  if (beams > kMaxBeams || (long long)beams * slices_of(vocab) > kMaxLists) return SSA_ERR_UNSUPPORTED;
-  if (groups > 65535) return SSA_ERR_UNSUPPORTED;
+  if (beams > kMaxBeams || groups > 65535 || vocab > 1 << 23) return SSA_ERR_UNSUPPORTED;
   if (!logits || !in || !out || !in->scores || !out->scores || !parent || !token || !ws) return SSA_ERR_INVALID_ARG;
   if ((uintptr_t)logits & (dtype == SSA_F32 ? 3 : 1)) return SSA_ERR_INVALID_ARG;
   if (row_stride < vocab && (long long)groups * beams > 1) return SSA_ERR_INVALID_ARG;
@@ -648,7 +723,7 @@ int ssa_beam_select(int dtype, int groups, int beams, int vocab, const void* log
 
   Params p{};
   p.logits = logits; p.stride = row_stride;
-  p.K = beams; p.V = vocab; p.slices = slices_of(vocab); p.max_len = max_len; p.eos = eos;
+  p.K = beams; p.V = vocab; p.max_len = max_len; p.eos = eos;
   p.scores = in->scores; p.ended = in->finished; p.history = in->history; p.hist_len = in->hist_len;
   p.scores_out = out->scores; p.ended_out = out->finished; p.history_out = out->history;
   p.hist_len_out = out->hist_len;
@@ -661,7 +736,7 @@ int ssa_beam_select(int dtype, int groups, int beams, int vocab, const void* log
   p.old_len = reinterpret_cast<int32_t*>(w);
   w += align256((size_t)groups * 4);
   p.part = reinterpret_cast<Part*>(w);
-  w += align256((size_t)groups * kMaxLists * sizeof(Part));
+  w += align256(std::max((size_t)groups * beams, (size_t)kMaxLists) * sizeof(Part));
   p.cand = reinterpret_cast<Cand*>(w);
   cudaError_t e;
   switch (dtype) {

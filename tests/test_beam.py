@@ -21,10 +21,13 @@ EPS = 2.0 ** -18
 def candidates(x, scores, finished, eos):
     """[B][V] scores in 64 bits, -inf where there is none."""
     x = x.double()
-    x = torch.where(x.isnan(), -math.inf, x.clamp(max=torch.finfo(F32).max))
+    x = torch.where(x.isnan(), -math.inf, x.clamp(max=2.0 ** 126))
     m = x.amax(-1, keepdim=True)
-    lse = torch.where(m > -math.inf, m + (x - m).exp().sum(-1, keepdim=True).log(), 0.0)
-    c = torch.where(x > -math.inf, x - lse + scores.double()[:, None], -math.inf)
+    m = torch.where(m > -math.inf, m, 0.0)
+    # rows that are alike must have equal sums, whatever order torch adds them in: to 2^-40
+    ln = ((x - m).exp().sum(-1, keepdim=True).log() * 2.0 ** 40).round() * 2.0 ** -40
+    # (x - m first: beside a mask of 1e38 the logarithm would be lost)
+    c = torch.where(x > -math.inf, x - m - ln + scores.double()[:, None], -math.inf)
     if finished is not None:
         stay = torch.full_like(c, -math.inf)
         stay[:, eos] = scores.double()
@@ -248,6 +251,23 @@ def test_same_bits_graph_and_workspace_left_clean():
             assert torch.equal(getattr(live, name), getattr(want, name))
 
 
+@gpu
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("V", [40000, 300000])
+@pytest.mark.parametrize("K", [3, 32])
+def test_rising_equal_and_masked_by_a_number(dtype, V, K):
+    """Every logit better than those before it; all equal; a mask of one finite value."""
+    G = 40 if V == 40000 else 2
+    st = ssa.BeamState(G, K)
+    st.scores.copy_(-torch.arange(G * K, device="cuda") * 0.25)
+    up = torch.linspace(-8, 8, V, device="cuda").to(dtype).expand(G * K, V).contiguous()
+    check(up, copy_of(st))
+    check(torch.full_like(up, -1.5), copy_of(st), exact=True)
+    low = torch.full_like(up, torch.finfo(dtype).min)
+    low[::2, 777::5000] = 3.0
+    check(low, copy_of(st))
+
+
 def _cpu(G=2, K=3, V=10, eos=-1, max_len=0, **kw):
     st = ssa.BeamState(G, K, max_len, eos >= 0, device="cpu")
     i32 = dict(dtype=torch.int32)
@@ -294,7 +314,7 @@ def test_c_refusals():
         o = i if o is None else ssa.SsaBeams(*o)
         return L.ssa_beam_select(dtype, G, K, V, x, stride, ctypes.byref(i), ctypes.byref(o), max_len, eos, par, tok,
                                  lens, new, None, ws, None)
-    assert go(dtype=3) == -3 and go(K=33) == -3 and go(K=32, V=300000, stride=300000) == -3
+    assert go(dtype=3) == -3 and go(K=33) == -3 and go(V=(1 << 23) + 1, stride=1 << 24) == -3 and go(G=70000) == -3
     assert go(G=0) == -1 and go(K=0) == -1 and go(V=0) == -1 and go(max_len=-1) == -1
     assert go(eos=100) == -1 and go(eos=-2) == -1
     assert go(x=None) == -1 and go(x=p + 1) == -1 and go(stride=99) == -1 and go(ws=None) == -1 and go(ws=p + 16) == -1
