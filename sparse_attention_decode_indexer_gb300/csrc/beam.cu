@@ -262,6 +262,19 @@ template <typename T> struct Logits {
     }
     return bits;
   }
+  // the logit at a place (registers have no index: a chain of selects)
+  __device__ __forceinline__ float at(int place) const {
+    const int j = sizeof(T) == 4 ? place : place >> 1;
+    uint32_t v = w[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) v = j == i ? w[i] : v;
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(v);
+    } else {
+      const float2 f = unpack<T>(v);
+      return place & 1 ? f.y : f.x;
+    }
+  }
   // the place of a bit of reach()
   static __device__ __forceinline__ int place(int bit) {
     return sizeof(T) == 4 ? bit : (bit & 15) * 2 + (bit >> 4);
@@ -286,18 +299,60 @@ union Scratch {
   int32_t move[2048];
 };
 
+// ln z, z > 0, to about 2^-35: z = 2^e m with m about one, ln m = 2 atanh(s), s =
+// (m - 1) / (m + 1), |s| < 0.172; the series' first two terms in double.  A
+// double operation takes an SM 16 clocks a warp, so few of them.
+__device__ __forceinline__ double ln_of(uint64_t z) {
+  const int lead = __clzll((long long)z);
+  const uint64_t f = z << lead;           // the leading bit on top
+  const bool high = f >= 0xB504F333F9DE6485ull;           // above sqrt(2)
+  const int e = 63 - lead + (high ? 1 : 0);
+  const double m = __longlong_as_double((long long)(((high ? 1022ull : 1023ull) << 52) | (f << 1 >> 12)));
+  const double d = m + 1.0;
+  double r = (double)(1.0f / (float)d);
+  r = fma(r, fma(-d, r, 1.0), r);
+  const double s = (m - 1.0) * r;
+  const float t = (float)s, t2 = t * t;
+  const float tail = t2 * t2 * t * fmaf(t2, fmaf(t2, fmaf(t2, fmaf(t2, 1.0f / 13, 1.0f / 11), 1.0f / 9), 1.0f / 7), 0.2f);
+  const double sum = s + (s * s * s * (1.0 / 3) + (double)tail);
+  return fma((double)e, 0.69314718055994530942, 2.0 * sum);
+}
+
 // The K-th greatest of the threads' numbers (0: none), or something below it that
 // no more than K reach; N numbers a thread.
 template <int N> __device__ __forceinline__ uint32_t kth(const uint32_t (&x)[N], int K) {
+  __shared__ uint32_t s_and, s_or;
+  if (threadIdx.x == 0) { s_and = ~0u; s_or = 0; }
+  uint32_t all = ~0u, any = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (x[i]) { all &= x[i]; any |= x[i]; }
+  all = __reduce_and_sync(0xffffffffu, all);
+  any = __reduce_or_sync(0xffffffffu, any);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0 && any) { atomicAnd(&s_and, all); atomicOr(&s_or, any); }
+  __syncthreads();
+  // the leading bits that all have in common need no search
+  const uint32_t differ = s_and ^ s_or;
   uint32_t lo = 0;                        // at least K reach it, or it is 0
-  for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
-    const uint32_t mid = lo | bit;
+  if (s_or) {
+    uint32_t bit = differ ? 0x80000000u >> __clz(differ) : 0u;
+    const uint32_t common = bit ? s_and & ~(2 * bit - 1) : s_and;
     int n = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) n += __syncthreads_count(x[i] >= mid);
-    if (n >= K) lo = mid;
-    if (n == K) break;
+    for (int i = 0; i < N; ++i) n += __syncthreads_count(x[i] != 0);
+    if (n > K) {
+      for (lo = common; bit; bit >>= 1) {
+        const uint32_t mid = lo | bit;
+        n = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) n += __syncthreads_count(x[i] >= mid);
+        if (n >= K) lo = mid;
+        if (n == K) break;
+      }
+    }
   }
+  __syncthreads();
   return lo;
 }
 
@@ -360,7 +415,7 @@ __device__ __noinline__ void choose(const Params& p, int g, Scratch& sc) {
     // ln of the sum = ref + ln, apart: beside a far reference ln would be lost
     const bool none = s_old[tid] || s_z[tid] == 0;
     s_ref[tid] = none ? 0.0 : s_far[tid] < INFINITY ? (double)s_far[tid] : (double)s_c[tid] * (1.0 / (double)kLog2e);
-    s_ln[tid] = none ? 0.0 : (log2((double)s_z[tid]) - 40.0) * (1.0 / (double)kLog2e);
+    s_ln[tid] = none ? 0.0 : ln_of(s_z[tid]) - 40.0 * 0.69314718055994530942;
   }
   __syncthreads();
 
@@ -524,39 +579,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) beam_kernel(const __grid_cons
     x.load(logits, begin, p.V, vec);
     if (tid == 0) s_n = 0;
     int kept = 0;                         // of the list, the best so far
-    float c = -INFINITY;                  // the reference of the sum: whole octaves, so that parts add by shifts,
     float reached = X::lowest();          // the K-th best so far
+    float c = -INFINITY;                  // the reference of the sum: whole octaves, so that parts add by shifts,
     float far = INFINITY;                 // or this logit, where it is far out
-    uint64_t z = 0;                       // the warp's sum
-    for (long long first = begin; first < end; first += X::kChunk) {
-      X next;
-      if (first + X::kChunk < end) next.load(logits, first + X::kChunk, p.V, vec);
-      const float m = fminf(x.most(), kGreatest);
-      float q = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 2));
-      // the lowest six bits tell groups apart: a bound rounded down is still one
-      if ((tid & 3) == 0) s_key[tid >> 2] = (rank32(q) & ~63u) | (uint32_t)(tid >> 2);
-      q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 4));
-      q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 8));
-      q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 16));
-      if (lane == 0) s_max[warp] = q;
-      __syncthreads();
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kThreads / 128; ++w) {
-        const float4 f = reinterpret_cast<const float4*>(s_max)[w];
-        top = fmaxf(fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)), top);
-      }
-      if (tid < 64) {
-        const uint32_t k = s_key[tid];
-        int rank = 0;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const uint4 u = reinterpret_cast<const uint4*>(s_key)[j];
-          rank += (u.x > k) + (u.y > k) + (u.z > k) + (u.w > k);
-        }
-        if (rank == K - 1) s_least = k & ~63u;
-      }
+    uint64_t z = 0;                       // the thread's sum
+    // the chunk's greatest becomes the reference where it is above it
+    const auto refer = [&](float top) {
       if (top > -INFINITY) {
         const bool is_far = fabsf(top) >= kFar;
         const float tc = is_far ? fmaxf(top, -kGreatest) * kLog2e : ceilf(top * kLog2e);
@@ -566,52 +594,99 @@ __global__ void __launch_bounds__(kThreads, kCtas) beam_kernel(const __grid_cons
           far = is_far ? top : INFINITY;
         }
       }
-      float sum = 0.0f;
-      if (c > -INFINITY) sum = far < INFINITY ? x.sum_from(far) : x.sum(c);
-      if (!(sum <= 64.0f)) sum = x.sum_clean(c);      // a NaN among them
-      const uint64_t zi = warp_sum47((uint64_t)(sum * kUnit));
-      z += zi;
-      if (lane == 0 && first + X::kChunk >= end) s_sum[warp] = z;
-      __syncthreads();
-      // the list of what reaches the bound (read again: registers have no index)
-      const float least = fmaxf(unrank32(s_least), reached);    // (a NaN where fewer than K are finite)
-      if (m >= least)
+    };
+    const auto block_top = [&]() {
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kThreads / 128; ++w) {
+        const float4 f = reinterpret_cast<const float4*>(s_max)[w];
+        top = fmaxf(fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)), top);
+      }
+      return top;
+    };
+    for (long long first = begin; first < end; first += X::kChunk) {
+      X next;
+      if (first + X::kChunk < end) next.load(logits, first + X::kChunk, p.V, vec);
+      const float m = fminf(x.most(), kGreatest);
+      float least = reached;
+      if (kept < K) {                     // no bound yet: one of this chunk's own
+        float q = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 2));
+        // the lowest six bits tell groups apart: a bound rounded down is still one
+        if ((tid & 3) == 0) s_key[tid >> 2] = (rank32(q) & ~63u) | (uint32_t)(tid >> 2);
+        q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 4));
+        q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 8));
+        q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 16));
+        if (lane == 0) s_max[warp] = q;
+        __syncthreads();
+        refer(block_top());
+        if (tid < 64) {
+          const uint32_t k = s_key[tid];
+          int rank = 0;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint4 u = reinterpret_cast<const uint4*>(s_key)[j];
+            rank += (u.x > k) + (u.y > k) + (u.z > k) + (u.w > k);
+          }
+          if (rank == K - 1) s_least = k & ~63u;
+        }
+        __syncthreads();
+        least = fmaxf(unrank32(s_least), reached);        // (a NaN where fewer than K are finite)
+      }
+      // the list of what reaches the bound
+      int flags = 0;
+      if (m >= least) {
+        flags = 1;
         for (uint32_t bits = x.reach(least); bits; bits &= bits - 1) {
           const int at = kept + atomicAdd(&s_n, 1);
           if (at >= kList) break;
-          const int t = x.token(first, x.place(__ffs(bits) - 1));
-          sc.list[at] = key_of(fminf(one_in(logits[t]), kGreatest), (uint32_t)t);
+          const int i = x.place(__ffs(bits) - 1);
+          sc.list[at] = key_of(fminf(x.at(i), kGreatest), (uint32_t)x.token((int)first, i));
         }
-      __syncthreads();
-      int n = kept + s_n;
-      if (n > kList) {
-        // many equal ones: bounded over (value, token) instead
-        uint64_t best = 0;
-        x.each([&](float v, int i) {
-          if (v == v) {
-            const uint64_t k = key_of(fminf(v, kGreatest), (uint32_t)x.token(first, i));
-            if (k > best) best = k;
-          }
-        });
-        s_best[tid] = best;
+      }
+      float sum = 0.0f;
+      if (c > -INFINITY) sum = far < INFINITY ? x.sum_from(far) : x.sum(c);
+      // above: a NaN, or logits far above the reference of the chunks before
+      if (!(sum <= 64.0f) || (c == -INFINITY && m > -INFINITY)) flags |= 2;
+      const bool some = __syncthreads_or(flags != 0);
+      if (some && __syncthreads_or((flags & 2) != 0)) {
+        const float q = warp_max(m);
+        if (lane == 0) s_max[warp] = q;
         __syncthreads();
-        if (tid == 0) s_n = 0;
-        int rank = 0;
-        for (int j = 0; j < kThreads; ++j) rank += s_best[j] > best || (s_best[j] == best && j < tid);
-        if (rank == K - 1) s_bound = best;
-        __syncthreads();
-        const uint64_t bound = s_bound;
-        if (best >= bound)
+        refer(block_top());
+        sum = 0.0f;
+        if (c > -INFINITY) sum = far < INFINITY ? x.sum_from(far) : x.sum_clean(c);
+      }
+      z += (uint64_t)(sum * kUnit);
+      if (some && s_n > 0) {
+        int n = kept + s_n;
+        if (n > kList) {
+          // many equal ones: bounded over (value, token) instead
+          uint64_t best = 0;
           x.each([&](float v, int i) {
-            if (v == v && v > -INFINITY) {
-              const uint64_t k = key_of(fminf(v, kGreatest), (uint32_t)x.token(first, i));
-              if (k >= bound) sc.list[kept + atomicAdd(&s_n, 1)] = k;
+            if (v == v) {
+              const uint64_t k = key_of(fminf(v, kGreatest), (uint32_t)x.token((int)first, i));
+              if (k > best) best = k;
             }
           });
-        __syncthreads();
-        n = kept + s_n;
-      }
-      if (n > kept) {
+          s_best[tid] = best;
+          __syncthreads();
+          if (tid == 0) s_n = 0;
+          int rank = 0;
+          for (int j = 0; j < kThreads; ++j) rank += s_best[j] > best || (s_best[j] == best && j < tid);
+          if (rank == K - 1) s_bound = best;
+          __syncthreads();
+          const uint64_t bound = s_bound;
+          if (best >= bound)
+            x.each([&](float v, int i) {
+              if (v == v && v > -INFINITY) {
+                const uint64_t k = key_of(fminf(v, kGreatest), (uint32_t)x.token((int)first, i));
+                if (k >= bound) sc.list[kept + atomicAdd(&s_n, 1)] = k;
+              }
+            });
+          __syncthreads();
+          n = kept + s_n;
+        }
         for (int i = tid; i < n; i += kThreads) {
           const uint64_t k = sc.list[i];
           int r = 0;
@@ -622,12 +697,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) beam_kernel(const __grid_cons
         __syncthreads();
         kept = min(n, K);
         if (tid < kept) sc.list[tid] = s_keep[tid];
-        if (kept == K) reached = key_x(s_keep[K - 1]);
+        if (kept == K) reached = fmaxf(key_x(s_keep[K - 1]), reached);
         if (tid == 0) s_n = 0;
-        // (the next chunk's first barrier comes before either is used again)
+        __syncthreads();
       }
       x = next;
     }
+    z = warp_sum(z);
+    if (lane == 0) s_sum[warp] = z;
+    __syncthreads();
     if (tid < K) out[tid] = tid < kept ? Cand{key_x(s_keep[tid]), (int)~(uint32_t)s_keep[tid]} : Cand{0.0f, -1};
     if (tid == 0) {
       uint64_t s = 0;
