@@ -92,6 +92,11 @@ template <typename T> __device__ __forceinline__ uint32_t pack16(float lo, float
   if constexpr (std::is_same_v<T, __half>) return pack_f16(lo, hi);
   else return pack_bf16(lo, hi);
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 template <typename T> __device__ __forceinline__ float to_f32(T x) {
   if constexpr (std::is_same_v<T, __half>) return __half2float(x);
   else return __bfloat162float(x);
@@ -143,7 +148,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
     for (int i = 0; i < kStages; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 1); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 1); mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], kRows); mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.p_full[i], 4); mbar_init(&sh.o_full[i], 1);
       sh.t_lo[i] = INT_MAX; sh.t_hi[i] = 0;
     }
     mbar_init(&sh.go, 1); mbar_init(&sh.clean, 64); mbar_init(&sh.drain, 1);
@@ -323,20 +328,29 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
     for (int i = tb0[tile]; i < tb1[tile]; ++i, ++n) {
       if (!all(mbar_wait(&sh.s_full[tile], n & 1, abort))) { ok = false; break; }
       tc5_fence_after();
-      uint32_t s[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(s + 32 * c, S + 32 * c);
-      tmem_wait_ld();
+      // The scores are read twice, 32 columns at a time with the next on their
+      // way: once for the maximum, once for the weights.
       const int x = x0 + i * kBlk;
-      if (__any_sync(~0u, live && (x < lo || x + kBlk > hi))) {
-        const uint32_t from = lo - x, len = hi - lo;
+      const bool cut = __any_sync(~0u, live && (x < lo || x + kBlk > hi));
+      const uint32_t from = lo - x, len = hi - lo;
+      const auto mask = [&](uint32_t* s, int c) {
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if ((uint32_t)c - from >= len) s[c] = 0xFF800000u;
-      }
+        for (int j = 0; j < 32; ++j)
+          if ((uint32_t)(32 * c + j) - from >= len) s[j] = 0xFF800000u;
+      };
+      uint32_t s[2][32];
+      tmem_ld32(s[0], S);
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+      for (int c = 0; c < 4; ++c) {
+        uint32_t* cur = s[c & 1];
+        tmem_wait_ld(cur);
+        tmem_ld32(s[~c & 1], S + 32 * ((c + 1) & 3));        // (after the last the first again)
+        if (cut) mask(cur, c);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          mx[j & 3] = max3(mx[j & 3], __uint_as_float(cur[2 * j]), __uint_as_float(cur[2 * j + 1]));
+      }
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
       const bool move = live && top > m + kLazy;
       if (__any_sync(~0u, move)) {
@@ -350,7 +364,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
           for (int c = 0; c < 4; ++c) {
             uint32_t o[32];
             tmem_ld32(o, O + 32 * c);
-            tmem_wait_ld();
+            tmem_wait_ld(o);
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
             tmem_st32(O + 32 * c, o);
@@ -358,23 +372,31 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
         }
       }
       const float ref = m == -INFINITY ? 0.0f : m;
-      float sum[4] = {0, 0, 0, 0};
+      const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), ref2 = pack2(-ref, -ref);
+      uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[32];
+      for (int c = 0; c < 4; ++c) {
+        uint32_t* cur = s[c & 1];
+        tmem_wait_ld(cur);
+        if (c < 3) tmem_ld32(s[~c & 1], S + 32 * (c + 1));
+        if (cut) mask(cur, c);
+        uint32_t w[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float e0 = fast_exp2(fmaf(__uint_as_float(s[64 * c + 2 * j]), p.scale_log2, -ref));
-          const float e1 = fast_exp2(fmaf(__uint_as_float(s[64 * c + 2 * j + 1]), p.scale_log2, -ref));
-          sum[j & 3] += e0 + e1;
+        for (int j = 0; j < 16; ++j) {
+          const float2 t = unpack2(fma2(pack2(__uint_as_float(cur[2 * j]), __uint_as_float(cur[2 * j + 1])), scale2, ref2));
+          const float e0 = fast_exp2(t.x), e1 = fast_exp2(t.y);
+          sum[j & 3] = add2(sum[j & 3], pack2(e0, e1));
           w[j] = pack16<T>(e0, e1);
         }
-        tmem_st32(S + 32 * c, w);
+        // (columns that have been read: P's 16 of this piece lie before S's next)
+        tmem_st16(S + 16 * c, w);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      const float2 total = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+      l += total.x + total.y;
       tmem_wait_st();
       tc5_fence_before();
-      mbar_arrive(&sh.p_full[tile]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.p_full[tile]);
     }
     // ---- epilogue ----
     if (ok && n > 0) ok = all(mbar_wait(&sh.o_full[tile], (n - 1) & 1, abort));
@@ -396,7 +418,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
         uint32_t o[32];
         if (n > 0) {
           tmem_ld32(o, O + 32 * c);
-          tmem_wait_ld();
+          tmem_wait_ld(o);
         }
         if (in_seq) {
           if (!seen) {

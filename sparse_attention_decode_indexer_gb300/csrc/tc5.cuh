@@ -72,8 +72,18 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* x) {
                "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
                ::SSA_W8(x, 0), SSA_W8(x, 8), SSA_W8(x, 16), SSA_W8(x, 24), "r"(addr) : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// Waits for the loads so far; x, loaded by the last of them, has its values only now.
+#define SSA_RW8(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3]), "+r"(x[i + 4]), \
+                      "+r"(x[i + 5]), "+r"(x[i + 6]), "+r"(x[i + 7])
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : SSA_RW8(x, 0), SSA_RW8(x, 8), SSA_RW8(x, 16), SSA_RW8(x, 24) :: "memory");
+}
+// 16 columns
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+               "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+               ::SSA_W8(x, 0), SSA_W8(x, 8), "r"(addr) : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
