@@ -233,14 +233,15 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
       for (int j = max(0, it - kStages); j < it; ++j)
         mbar_wait(&sh.full[j % kStages], (j / kStages) & 1, nullptr);
     }
-  } else if (warp == 9 && lane == 0) {
-    // ---- MMAs ----
+  } else if (warp == 9) {
+    // ---- MMAs: the warp together ----
     constexpr uint32_t id_qk = tc5_idesc(BF, kBlk, false), id_pv = tc5_idesc(BF, kD, true);
-    const uint32_t a_q = smem_u32(s_q), a_kv = smem_u32(s_kv);
+    const uint32_t a_q = tc5_desc(smem_u32(s_q), 16), a_k = tc5_desc(smem_u32(s_kv), 16),
+                   a_v = tc5_desc(smem_u32(s_kv), kHalf);
     bool ok = true;
     int n_ragged = 0;
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok && !mbar_wait(bar, parity, abort)) { give_up(SSA_ST_TIMEOUT); ok = false; }
+      if (ok && !__all_sync(~0u, mbar_wait(bar, parity, abort))) { give_up(SSA_ST_TIMEOUT); ok = false; }
     };
     for (int t = 0; t < 2; ++t)
       if (tb0[t] < tb1[t]) wait(&sh.q_full[t], 0);
@@ -257,18 +258,17 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
           wait(&sh.p_full[t], (i - 1 - tb0[t]) & 1);
           if (!ok) break;
           tc5_fence_after();
-          const uint32_t v = a_kv + (vv % kStages) * kTile;
+          const uint32_t v = a_v + (vv % kStages) * (kTile >> 4);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc5_mma_ta(O, S + k * 8, tc5_desc(v + k * 2048, kHalf, 1024), id_pv, i - 1 > tb0[t] || k > 0);
+          for (int k = 0; k < 8; ++k) tc5_mma_ta(O, S + k * 8, v + k * 128, id_pv, i - 1 > tb0[t] || k > 0);
           tc5_commit(&sh.o_full[t]);
         }
         if (i >= tb0[t] && i < tb1[t]) {
-          const uint32_t q = a_q + t * kTile, kb = a_kv + (kk % kStages) * kTile;
+          const uint32_t q = a_q + t * (kTile >> 4), kb = a_k + (kk % kStages) * (kTile >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
-            tc5_mma(S, tc5_desc(q + off, 16, 1024), tc5_desc(kb + off, 16, 1024), id_qk, k > 0);
+            const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+            tc5_mma(S, q + off, kb + off, id_qk, k > 0);
           }
           tc5_commit(&sh.s_full[t]);
         }
@@ -279,7 +279,8 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
         tc5_commit(&sh.empty[kk % kStages]);
         if (ragged(i)) {
           wait(&sh.full[(kk + 1) % kStages], ((kk + 1) / kStages) & 1);
-          mbar_arrive(&sh.go);
+          if (lane == 0) mbar_arrive(&sh.go);
+          __syncwarp();
         }
       }
     }

@@ -26,33 +26,40 @@ __device__ __forceinline__ void tc5_fence_before() {
 __device__ __forceinline__ void tc5_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// The barrier gets one arrival when every MMA issued so far by this thread is done.
+// MMAs and commits are issued by one elected thread of a warp that runs them
+// together: in converged code the operands stay in uniform registers (under an
+// if for one lane every MMA fetched its six words anew, 80 clocks an MMA of 64).
+// The barrier gets one arrival when every MMA issued so far by this warp is done.
 __device__ __forceinline__ void tc5_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+  asm volatile("{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+               "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
                ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Shared-memory operand with the 128-byte swizzle, both strides in bytes.
-// K-major: rows of 64 16-bit elements, `sbo` between groups of 8 rows.
-// MN-major: `lbo` between groups of 64 elements, `sbo` between groups of 8 k.
-__device__ __forceinline__ uint64_t tc5_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 |
-         1ull << 46 | 2ull << 61;
-}
+// Shared-memory operand with the 128-byte swizzle: the words of its descriptor.
+// K-major: rows of 64 16-bit elements, 1024 bytes between groups of 8 rows (kb
+// 16).  MN-major: kb bytes between groups of 64 elements, 1024 between 8 k.
+// Addresses advance by 16 bytes a unit of the low word.
+constexpr uint32_t kTc5DescHigh = 1024u >> 4 | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t tc5_desc(uint32_t addr, uint32_t kb) { return addr >> 4 | kb >> 4 << 16; }
 // kind::f16, fp32 accumulators, 128 x N; b_mn: B is MN-major
 __host__ __device__ constexpr uint32_t tc5_idesc(bool bf16, int N, bool b_mn) {
   return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_mn ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 |
          (uint32_t)(128 >> 4) << 24;
 }
-__device__ __forceinline__ void tc5_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+// d (+)= a b^T, a and b in shared memory
+__device__ __forceinline__ void tc5_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+  asm volatile("{\n.reg .pred p, e;\n.reg .b64 a, b;\nelect.sync _|e, 0xffffffff;\nsetp.ne.u32 p, %4, 0;\n"
+               "mov.b64 a, {%1, %5};\nmov.b64 b, {%2, %5};\n"
+               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}"
+               ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kTc5DescHigh) : "memory");
 }
-__device__ __forceinline__ void tc5_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+// a in tensor memory
+__device__ __forceinline__ void tc5_mma_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+  asm volatile("{\n.reg .pred p, e;\n.reg .b64 b;\nelect.sync _|e, 0xffffffff;\nsetp.ne.u32 p, %4, 0;\n"
+               "mov.b64 b, {%2, %5};\n"
+               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}"
+               ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kTc5DescHigh) : "memory");
 }
 
 // 32 columns of this warp's lanes.
