@@ -26,8 +26,8 @@
 //     is rescaled in tensor memory.  Sums and references are fp32; P in 16 bits
 //     is off by half a step of its type, as the inputs are.
 //   * Masked scores give p = 0, and 0 times an infinite or NaN v would still
-//     be NaN.  Two spare warps look through the V of those blocks that some
-//     row does not see all of, and set what is not finite to zero; the epilogue
+//     be NaN.  A spare warp looks through the V of those blocks that some
+//     row does not see all of, and sets what is not finite to zero; the epilogue
 //     then adds it for the rows that do see it.
 //   * Few rows and many keys: the key blocks of a tile are split over several
 //     CTAs; their unnormalised outputs are joined by a second kernel.
@@ -46,16 +46,17 @@ namespace {
 constexpr int kD = 128;                   // head size
 constexpr int kRows = 128;                // rows of a tile
 constexpr int kBlk = 128;                 // keys of a block
-constexpr int kThreads = 384;             // 8 softmax warps, TMA, MMA, 2 that look over V
+constexpr int kThreads = 384;             // 8 softmax warps; TMA, an MMA warp a tile, one that looks over V
+constexpr int kTma = 8, kMma = 9, kLook = 11;           // these warps
 constexpr int kStages = 5;                // K and V blocks in flight
 constexpr int kHalf = kRows * 128;        // bytes of 64 of the 128 dimensions
 constexpr int kTile = 2 * kHalf;
 constexpr float kLazy = 8.0f;             // octaves
 
 struct Shared {                           // behind the tiles
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kStages], empty[kStages], clean[kStages];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
-  uint64_t go, clean, drain;
+  uint64_t drain;
   uint32_t tmem;
   int abort, dirty;
   int lo_min, hi_max;                     // keys that any row sees
@@ -120,7 +121,14 @@ __device__ __forceinline__ bool row_keys(const Params& p, int tok, int& lo, int&
   return true;
 }
 
-// True where one of a word's two elements is infinite or NaN.
+// Whether one of eight elements is infinite or NaN: its exponent, all ones, and
+// one more carry into the sign's place.
+template <typename T> __device__ __forceinline__ bool any_odd(uint4 u) {
+  constexpr uint32_t e = std::is_same_v<T, __half> ? 0x7C007C00u : 0x7F807F80u;
+  constexpr uint32_t one = std::is_same_v<T, __half> ? 0x04000400u : 0x00800080u;
+  return (((u.x & e) + one) | ((u.y & e) + one) | ((u.z & e) + one) | ((u.w & e) + one)) & 0x80008000u;
+}
+// A word without those.
 template <typename T> __device__ __forceinline__ uint32_t finite_part(uint32_t w) {
   constexpr uint32_t e = std::is_same_v<T, __half> ? 0x7C00u : 0x7F80u;
   if ((w & e) == e) w &= 0xFFFF0000u;
@@ -145,19 +153,19 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
   const int tok0 = pair * 2 * p.tpt;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 1); }
+    for (int i = 0; i < kStages; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 2); mbar_init(&sh.clean[i], 1); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 1); mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i], 4); mbar_init(&sh.o_full[i], 1);
       sh.t_lo[i] = INT_MAX; sh.t_hi[i] = 0;
     }
-    mbar_init(&sh.go, 1); mbar_init(&sh.clean, 64); mbar_init(&sh.drain, 1);
+    mbar_init(&sh.drain, 2);
     sh.abort = sh.dirty = 0;
     sh.lo_min = sh.hi_min = INT_MAX;
     sh.hi_max = sh.lo_max = 0;
     fence_barrier_init();
   }
-  if (warp == 9) tmem_alloc_all(&sh.tmem);
+  if (warp == kMma) tmem_alloc_all(&sh.tmem);
   if (threadIdx.x == 256) { prefetch_tmap(&tm_q); prefetch_tmap(&tm_k); prefetch_tmap(&tm_v); }
   pdl_trigger();
   pdl_wait();
@@ -201,13 +209,11 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
       if (tb1[t] < tb0[t]) tb1[t] = tb0[t];
     }
   }
-  // some row does not see all of block i
-  const auto ragged = [&](int i) { return x0 + i * kBlk < sh.lo_max || x0 + (i + 1) * kBlk > sh.hi_min; };
   const uint32_t tmem = sh.tmem;
   volatile int* abort = &sh.abort;
   const auto give_up = [&](int bits) { sh.abort = 1; set_status(p.status, bits); };
 
-  if (warp == 8 && lane == 0) {
+  if (warp == kTma && lane == 0) {
     // ---- loads ----
     const uint32_t q_bytes = 2u * 128u * p.G * p.tpt;
     for (int t = 0; t < 2; ++t)
@@ -233,38 +239,57 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
       for (int j = max(0, it - kStages); j < it; ++j)
         mbar_wait(&sh.full[j % kStages], (j / kStages) & 1, nullptr);
     }
-  } else if (warp == 9) {
-    // ---- MMAs: the warp together ----
+  } else if (warp == kMma || warp == kMma + 1) {
+    // ---- MMAs: a warp a tile, its lanes together ----
+    // S of block i follows P V of block i - 1, whose P it overwrites; the other
+    // tile's MMAs run while this one's scores are with the softmax.
     constexpr uint32_t id_qk = tc5_idesc(BF, kBlk, false), id_pv = tc5_idesc(BF, kD, true);
-    const uint32_t a_q = tc5_desc(smem_u32(s_q), 16), a_k = tc5_desc(smem_u32(s_kv), 16),
+    const int t = warp - kMma;
+    const uint32_t q = tc5_desc(smem_u32(s_q + t * kTile), 16), a_k = tc5_desc(smem_u32(s_kv), 16),
                    a_v = tc5_desc(smem_u32(s_kv), kHalf);
+    const uint32_t S = tmem + t * 128, O = tmem + 256 + t * 128;
+    const int i0 = tb0[t], i1 = tb1[t];
     bool ok = true;
-    int n_ragged = 0;
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok && !__all_sync(~0u, mbar_wait(bar, parity, abort))) { give_up(SSA_ST_TIMEOUT); ok = false; }
+      ok = __all_sync(~0u, mbar_wait(bar, parity, abort));
+      if (!ok) give_up(SSA_ST_TIMEOUT);
+      return ok;
     };
-    for (int t = 0; t < 2; ++t)
-      if (tb0[t] < tb1[t]) wait(&sh.q_full[t], 0);
+    if (i0 < i1) wait(&sh.q_full[t], 0);
+    // a stage is free when the MMAs that read it are done; a tile that reads
+    // nothing of it lets it go at once
+    const auto release = [&](uint64_t* bar, bool used) {
+      if (used) tc5_commit(bar);
+      else if (lane == 0) mbar_arrive(bar);
+      __syncwarp();
+    };
+    // stages of K of i and V of i - 1, and the phases of their barriers (V comes to a
+    // stage every fifth block, K and V by turns)
+    int ks = 0, vs = 1, v5 = 0;
+    uint32_t kp = 0, vp = 0, turn = 0;
     for (int i = b0; ok && i <= b1; ++i) {
-      const int kk = 2 * (i - b0), vv = kk - 1;         // uses of the ring: K of i, V of i - 1
-      if (i < b1) wait(&sh.full[kk % kStages], (kk / kStages) & 1);
       if (i > b0) {
-        wait(&sh.full[vv % kStages], (vv / kStages) & 1);
-        if (ragged(i - 1)) { wait(&sh.clean, n_ragged & 1); ++n_ragged; }
-      }
-      for (int t = 0; ok && t < 2; ++t) {
-        const uint32_t S = tmem + t * 128, O = tmem + 256 + t * 128;
-        if (i - 1 >= tb0[t] && i - 1 < tb1[t]) {
-          wait(&sh.p_full[t], (i - 1 - tb0[t]) & 1);
-          if (!ok) break;
+        if (!wait(&sh.clean[vs], vp)) break;
+        const bool used = i > i0 && i <= i1;
+        if (used) {
+          if (!wait(&sh.p_full[t], turn)) break;
+          turn ^= 1;
           tc5_fence_after();
-          const uint32_t v = a_v + (vv % kStages) * (kTile >> 4);
+          const uint32_t v = a_v + vs * (kTile >> 4);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) tc5_mma_ta(O, S + k * 8, v + k * 128, id_pv, i - 1 > tb0[t] || k > 0);
+          for (int k = 0; k < 8; ++k) tc5_mma_ta(O, S + k * 8, v + k * 128, id_pv, i - 1 > i0 || k > 0);
           tc5_commit(&sh.o_full[t]);
         }
-        if (i >= tb0[t] && i < tb1[t]) {
-          const uint32_t q = a_q + t * (kTile >> 4), kb = a_k + (kk % kStages) * (kTile >> 4);
+        release(&sh.empty[vs], used);
+        vs += 2;
+        if (vs >= kStages) vs -= kStages;
+        if (++v5 == kStages) { v5 = 0; vp ^= 1; }
+      }
+      if (i < b1) {
+        if (!wait(&sh.full[ks], kp)) break;
+        const bool used = i >= i0 && i < i1;
+        if (used) {
+          const uint32_t kb = a_k + ks * (kTile >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
@@ -272,45 +297,40 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
           }
           tc5_commit(&sh.s_full[t]);
         }
-      }
-      if (!ok) break;
-      if (i > b0) tc5_commit(&sh.empty[vv % kStages]);
-      if (i < b1) {
-        tc5_commit(&sh.empty[kk % kStages]);
-        if (ragged(i)) {
-          wait(&sh.full[(kk + 1) % kStages], ((kk + 1) / kStages) & 1);
-          if (lane == 0) mbar_arrive(&sh.go);
-          __syncwarp();
-        }
+        release(&sh.empty[ks], used);
+        ks += 2;
+        if (ks >= kStages) { ks -= kStages; kp ^= 1; }
       }
     }
-    tc5_commit(&sh.drain);                // no MMA is in flight when the CTA goes
+    release(&sh.drain, i0 < i1);          // no MMA is in flight when the CTA goes
     mbar_wait(&sh.drain, 0, nullptr);
-  } else if (warp >= 10) {
-    // ---- V of the blocks that some row does not see all of ----
-    int n = 0;
+  } else if (warp == kLook) {
+    // ---- V of the blocks that some row does not see all of: what is not finite becomes zero ----
+    const int lo_max = sh.lo_max, hi_min = sh.hi_min;
+    int vs = 1;
+    uint32_t vp = 0;
     for (int i = b0; i < b1; ++i) {
-      if (!ragged(i)) continue;
-      if (!mbar_wait(&sh.go, n & 1, abort)) { give_up(SSA_ST_TIMEOUT); break; }
-      // (the barrier has this phase until `clean` lets the block go)
-      const int use = 2 * (i - b0) + 1;
-      if (!mbar_wait(&sh.full[use % kStages], (use / kStages) & 1, abort)) { give_up(SSA_ST_TIMEOUT); break; }
-      ++n;
-      uint4* v = reinterpret_cast<uint4*>(s_kv + use % kStages * kTile);
-      bool found = false;
-      for (int j = threadIdx.x - 320; j < kTile / 16; j += 64) {
-        const uint4 w = v[j];
-        const uint4 f = make_uint4(finite_part<T>(w.x), finite_part<T>(w.y), finite_part<T>(w.z), finite_part<T>(w.w));
-        if (f.x != w.x || f.y != w.y || f.z != w.z || f.w != w.w) {
-          v[j] = f;
-          found = true;
+      if (!__all_sync(~0u, mbar_wait(&sh.full[vs], vp, abort))) { give_up(SSA_ST_TIMEOUT); break; }
+      if (x0 + i * kBlk < lo_max || x0 + (i + 1) * kBlk > hi_min) {
+        uint4* v = reinterpret_cast<uint4*>(s_kv + vs * kTile);
+        bool found = false;
+#pragma unroll 8
+        for (int j = lane; j < kTile / 16; j += 32) {
+          const uint4 w = v[j];
+          if (any_odd<T>(w)) {
+            v[j] = make_uint4(finite_part<T>(w.x), finite_part<T>(w.y), finite_part<T>(w.z), finite_part<T>(w.w));
+            found = true;
+          }
         }
+        if (found) {
+          sh.dirty = 1;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncwarp();
       }
-      if (found) {
-        sh.dirty = 1;
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      }
-      mbar_arrive(&sh.clean);
+      if (lane == 0) mbar_arrive(&sh.clean[vs]);
+      vs += 2;
+      if (vs >= kStages) { vs -= kStages; vp ^= 1; }
     }
   } else if (warp < 8) {
     // ---- softmax: a thread per row ----
@@ -329,28 +349,24 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
     for (int i = tb0[tile]; i < tb1[tile]; ++i, ++n) {
       if (!all(mbar_wait(&sh.s_full[tile], n & 1, abort))) { ok = false; break; }
       tc5_fence_after();
-      // The scores are read twice, 32 columns at a time with the next on their
-      // way: once for the maximum, once for the weights.
       const int x = x0 + i * kBlk;
       const bool cut = __any_sync(~0u, live && (x < lo || x + kBlk > hi));
       const uint32_t from = lo - x, len = hi - lo;
-      const auto mask = [&](uint32_t* s, int c) {
+      uint32_t s[4][32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if ((uint32_t)(32 * c + j) - from >= len) s[j] = 0xFF800000u;
-      };
-      uint32_t s[2][32];
-      tmem_ld32(s[0], S);
+      for (int c = 0; c < 4; ++c) tmem_ld32(s[c], S + 32 * c);
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t* cur = s[c & 1];
-        tmem_wait_ld(cur);
-        tmem_ld32(s[~c & 1], S + 32 * ((c + 1) & 3));        // (after the last the first again)
-        if (cut) mask(cur, c);
+        tmem_wait_ld(s[c]);
+        if (cut) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if ((uint32_t)(32 * c + j) - from >= len) s[c][j] = 0xFF800000u;
+        }
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          mx[j & 3] = max3(mx[j & 3], __uint_as_float(cur[2 * j]), __uint_as_float(cur[2 * j + 1]));
+          mx[j & 3] = max3(mx[j & 3], __uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1]));
       }
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
       const bool move = live && top > m + kLazy;
@@ -361,14 +377,14 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
         if (n > 0) {
           if (!all(mbar_wait(&sh.o_full[tile], (n - 1) & 1, abort))) { ok = false; break; }
           tc5_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tmem_ld16(o, O + 16 * c);
+            tmem_wait_ld16(o);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32(o, O + 32 * c);
-            tmem_wait_ld(o);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
-            tmem_st32(O + 32 * c, o);
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
+            tmem_st16(O + 16 * c, o);
           }
         }
       }
@@ -377,10 +393,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
       uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t* cur = s[c & 1];
-        tmem_wait_ld(cur);
-        if (c < 3) tmem_ld32(s[~c & 1], S + 32 * (c + 1));
-        if (cut) mask(cur, c);
+        const uint32_t* cur = s[c];
         uint32_t w[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -462,7 +475,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
   }
   __syncwarp();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMma) {
     tc5_fence_after();
     tmem_free_all(tmem);
   }

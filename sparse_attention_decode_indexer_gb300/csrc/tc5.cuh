@@ -87,6 +87,14 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t* x) {
                : SSA_RW8(x, 0), SSA_RW8(x, 8), SSA_RW8(x, 16), SSA_RW8(x, 24) :: "memory");
 }
 // 16 columns
+__device__ __forceinline__ void tmem_ld16(uint32_t* x, uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+               "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : SSA_R8(x, 0), SSA_R8(x, 8) : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t* x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : SSA_RW8(x, 0), SSA_RW8(x, 8) :: "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* x) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
                "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"

@@ -151,7 +151,7 @@ def test_packed(lens, causal):
 @pytest.mark.parametrize("lq,lk", [
     ([1], [1]), ([1], [20000]), ([8], [9000]), ([33], [5000]),               # keys before the queries: split
     ([7, 1, 1], [7, 4000, 600]), ([40, 3], [1, 0]), ([9, 200], [3, 100]),    # rows without keys
-    ([0, 4, 0], [300, 0, 20]), ([500, 20], [900, 6000])])
+    ([0, 4, 0], [300, 0, 20]), ([500, 20], [900, 6000]), ([2, 0, 3], [300, 3000, 20]), ([9, 0, 0, 200], [9, 700, 1500, 200])])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("Hq,Hkv", [(16, 2), (3, 3)])
 def test_other_keys(lq, lk, causal, Hq, Hkv):
