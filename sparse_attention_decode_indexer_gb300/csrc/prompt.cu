@@ -45,7 +45,8 @@ namespace {
 
 constexpr int kD = 128;                   // head size
 constexpr int kRows = 128;                // rows of a tile
-constexpr int kBlk = 128;                 // keys of a block
+constexpr int kBlk = 128;                 // keys of a block, as they are loaded
+constexpr int kSub = 64;                  // and as they are multiplied
 constexpr int kThreads = 384;             // 8 softmax warps; TMA, an MMA warp a tile, one that looks over V
 constexpr int kTma = 8, kMma = 9, kLook = 11;           // these warps
 constexpr int kStages = 5;                // K and V blocks in flight
@@ -55,7 +56,7 @@ constexpr float kLazy = 8.0f;             // octaves
 
 struct Shared {                           // behind the tiles
   uint64_t full[kStages], empty[kStages], clean[kStages];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2];   // [tile][buffer]
   uint64_t drain;
   uint32_t tmem;
   int abort, dirty;
@@ -155,8 +156,8 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 2); mbar_init(&sh.clean[i], 1); }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.q_full[i], 1); mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4); mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.q_full[i], 1); mbar_init(&sh.o_full[i], 1);
+      for (int b = 0; b < 2; ++b) { mbar_init(&sh.s_full[i][b], 1); mbar_init(&sh.p_full[i][b], 4); }
       sh.t_lo[i] = INT_MAX; sh.t_hi[i] = 0;
     }
     mbar_init(&sh.drain, 2);
@@ -199,15 +200,16 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
   const int x0 = sh.lo_min;
   const int nb = sh.hi_max > 0 ? (sh.hi_max - x0 + kBlk - 1) / kBlk : 0;
   const int b0 = (int)((long long)nb * split / p.n_split), b1 = (int)((long long)nb * (split + 1) / p.n_split);
-  int tb0[2], tb1[2];
+  int tb0[2], tb1[2], j1[2];              // j1: the first half block that a tile does not need
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     tb0[t] = tb1[t] = b1;
     if (sh.t_hi[t] > 0) {
       tb0[t] = max(b0, (sh.t_lo[t] - x0) / kBlk);
       tb1[t] = min(b1, (sh.t_hi[t] - x0 + kBlk - 1) / kBlk);
-      if (tb1[t] < tb0[t]) tb1[t] = tb0[t];
+      if (tb1[t] <= tb0[t]) tb0[t] = tb1[t] = b1;         // none in this part
     }
+    j1[t] = tb0[t] < tb1[t] ? min(2 * tb1[t], (sh.t_hi[t] - x0 + kSub - 1) / kSub) : 2 * tb0[t];
   }
   const uint32_t tmem = sh.tmem;
   volatile int* abort = &sh.abort;
@@ -241,21 +243,20 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
     }
   } else if (warp == kMma || warp == kMma + 1) {
     // ---- MMAs: a warp a tile, its lanes together ----
-    // S of block i follows P V of block i - 1, whose P it overwrites; the other
-    // tile's MMAs run while this one's scores are with the softmax.
-    constexpr uint32_t id_qk = tc5_idesc(BF, kBlk, false), id_pv = tc5_idesc(BF, kD, true);
+    // Scores of two half blocks lie in tensor memory: while the softmax has one of
+    // them the other is made, so that it never waits for the products of its own
+    // tile.  S of half block j + 2 follows P V of j, whose P it overwrites.
+    constexpr uint32_t id_qk = tc5_idesc(BF, kSub, false), id_pv = tc5_idesc(BF, kD, true);
     const int t = warp - kMma;
     const uint32_t q = tc5_desc(smem_u32(s_q + t * kTile), 16), a_k = tc5_desc(smem_u32(s_kv), 16),
                    a_v = tc5_desc(smem_u32(s_kv), kHalf);
     const uint32_t S = tmem + t * 128, O = tmem + 256 + t * 128;
-    const int i0 = tb0[t], i1 = tb1[t];
+    const int i0 = tb0[t], i1 = tb1[t], first = 2 * i0, last = j1[t];
     bool ok = true;
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = __all_sync(~0u, mbar_wait(bar, parity, abort));
+      ok = ok && __all_sync(~0u, mbar_wait(bar, parity, abort));
       if (!ok) give_up(SSA_ST_TIMEOUT);
-      return ok;
     };
-    if (i0 < i1) wait(&sh.q_full[t], 0);
     // a stage is free when the MMAs that read it are done; a tile that reads
     // nothing of it lets it go at once
     const auto release = [&](uint64_t* bar, bool used) {
@@ -263,45 +264,59 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
       else if (lane == 0) mbar_arrive(bar);
       __syncwarp();
     };
-    // stages of K of i and V of i - 1, and the phases of their barriers (V comes to a
-    // stage every fifth block, K and V by turns)
+    // stages of the K and of the V at hand, and the phases of their barriers (V comes
+    // to a stage every fifth block, K and V by turns)
     int ks = 0, vs = 1, v5 = 0;
-    uint32_t kp = 0, vp = 0, turn = 0;
-    for (int i = b0; ok && i <= b1; ++i) {
-      if (i > b0) {
-        if (!wait(&sh.clean[vs], vp)) break;
-        const bool used = i > i0 && i <= i1;
-        if (used) {
-          if (!wait(&sh.p_full[t], turn)) break;
-          turn ^= 1;
-          tc5_fence_after();
-          const uint32_t v = a_v + vs * (kTile >> 4);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) tc5_mma_ta(O, S + k * 8, v + k * 128, id_pv, i - 1 > i0 || k > 0);
-          tc5_commit(&sh.o_full[t]);
-        }
-        release(&sh.empty[vs], used);
-        vs += 2;
-        if (vs >= kStages) vs -= kStages;
-        if (++v5 == kStages) { v5 = 0; vp ^= 1; }
+    uint32_t kp = 0, vp = 0;
+    const auto next_k = [&](bool used) {
+      release(&sh.empty[ks], used);
+      ks += 2;
+      if (ks >= kStages) { ks -= kStages; kp ^= 1; }
+    };
+    const auto next_v = [&](bool used) {
+      release(&sh.empty[vs], used);
+      vs += 2;
+      if (vs >= kStages) vs -= kStages;
+      if (++v5 == kStages) { v5 = 0; vp ^= 1; }
+    };
+    const auto skip = [&](int n) {        // blocks that this tile does not need
+      for (int i = 0; ok && i < n; ++i) {
+        wait(&sh.full[ks], kp);
+        if (ok) next_k(false);
+        wait(&sh.clean[vs], vp);
+        if (ok) next_v(false);
       }
-      if (i < b1) {
-        if (!wait(&sh.full[ks], kp)) break;
-        const bool used = i >= i0 && i < i1;
-        if (used) {
-          const uint32_t kb = a_k + ks * (kTile >> 4);
+    };
+    const auto scores = [&](int j) {
+      if (!(j & 1)) wait(&sh.full[ks], kp);
+      if (!ok) return;
+      const uint32_t kb = a_k + ks * (kTile >> 4) + (j & 1) * (kSub * 128 >> 4);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-            tc5_mma(S, q + off, kb + off, id_qk, k > 0);
-          }
-          tc5_commit(&sh.s_full[t]);
-        }
-        release(&sh.empty[ks], used);
-        ks += 2;
-        if (ks >= kStages) { ks -= kStages; kp ^= 1; }
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+        tc5_mma(S + (j & 1) * kSub, q + off, kb + off, id_qk, k > 0);
+      }
+      tc5_commit(&sh.s_full[t][j & 1]);
+      if ((j & 1) || j == last - 1) next_k(true);
+    };
+    skip(i0 - b0);
+    if (i0 < i1) {
+      wait(&sh.q_full[t], 0);
+      for (int j = first; ok && j < min(first + 2, last); ++j) scores(j);
+      for (int j = first; ok && j < last; ++j) {
+        if (!(j & 1)) wait(&sh.clean[vs], vp);
+        wait(&sh.p_full[t][j & 1], ((j - first) >> 1) & 1);
+        if (!ok) break;
+        tc5_fence_after();
+        const uint32_t v = a_v + vs * (kTile >> 4) + (j & 1) * (kSub * 128 >> 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc5_mma_ta(O, S + (j & 1) * kSub + k * 8, v + k * 128, id_pv, j > first || k > 0);
+        tc5_commit(&sh.o_full[t]);
+        if (j + 2 < last) scores(j + 2);
+        if ((j & 1) || j == last - 1) next_v(true);
       }
     }
+    skip(b1 - max(i1, i0));
     release(&sh.drain, i0 < i1);          // no MMA is in flight when the CTA goes
     mbar_wait(&sh.drain, 0, nullptr);
   } else if (warp == kLook) {
@@ -346,27 +361,29 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
     float m = -INFINITY, l = 0.0f;
     int n = 0;
     bool ok = true;
-    for (int i = tb0[tile]; i < tb1[tile]; ++i, ++n) {
-      if (!all(mbar_wait(&sh.s_full[tile], n & 1, abort))) { ok = false; break; }
+    const int first = 2 * tb0[tile];
+    for (int j = first; j < j1[tile]; ++j, ++n) {
+      const uint32_t Sj = S + (j & 1) * kSub;
+      if (!all(mbar_wait(&sh.s_full[tile][j & 1], (n >> 1) & 1, abort))) { ok = false; break; }
       tc5_fence_after();
-      const int x = x0 + i * kBlk;
-      const bool cut = __any_sync(~0u, live && (x < lo || x + kBlk > hi));
+      const int x = x0 + j * kSub;
+      const bool cut = __any_sync(~0u, live && (x < lo || x + kSub > hi));
       const uint32_t from = lo - x, len = hi - lo;
-      uint32_t s[4][32];
+      uint32_t s[2][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(s[c], S + 32 * c);
+      for (int c = 0; c < 2; ++c) tmem_ld32(s[c], Sj + 32 * c);
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         tmem_wait_ld(s[c]);
         if (cut) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if ((uint32_t)(32 * c + j) - from >= len) s[c][j] = 0xFF800000u;
+          for (int e = 0; e < 32; ++e)
+            if ((uint32_t)(32 * c + e) - from >= len) s[c][e] = 0xFF800000u;
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          mx[j & 3] = max3(mx[j & 3], __uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1]));
+        for (int e = 0; e < 16; ++e)
+          mx[e & 3] = max3(mx[e & 3], __uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1]));
       }
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
       const bool move = live && top > m + kLazy;
@@ -392,27 +409,27 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
       const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), ref2 = pack2(-ref, -ref);
       uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t* cur = s[c];
+      for (int c = 0; c < 2; ++c) {
         uint32_t w[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float2 t = unpack2(fma2(pack2(__uint_as_float(cur[2 * j]), __uint_as_float(cur[2 * j + 1])), scale2, ref2));
+        for (int e = 0; e < 16; ++e) {
+          const float2 t = unpack2(fma2(pack2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])), scale2, ref2));
           const float e0 = fast_exp2(t.x), e1 = fast_exp2(t.y);
-          sum[j & 3] = add2(sum[j & 3], pack2(e0, e1));
-          w[j] = pack16<T>(e0, e1);
+          sum[e & 3] = add2(sum[e & 3], pack2(e0, e1));
+          w[e] = pack16<T>(e0, e1);
         }
-        // (columns that have been read: P's 16 of this piece lie before S's next)
-        tmem_st16(S + 16 * c, w);
+        tmem_st16(Sj + 16 * c, w);        // over the scores
       }
       const float2 total = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
       l += total.x + total.y;
       tmem_wait_st();
       tc5_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full[tile]);
+      if (lane == 0) mbar_arrive(&sh.p_full[tile][j & 1]);
     }
     // ---- epilogue ----
+    // (the last scores came behind the last product but two: one phase after the other)
+    if (ok && n > 1) ok = all(mbar_wait(&sh.o_full[tile], n & 1, abort));
     if (ok && n > 0) ok = all(mbar_wait(&sh.o_full[tile], (n - 1) & 1, abort));
     if (ok) {
       tc5_fence_after();
