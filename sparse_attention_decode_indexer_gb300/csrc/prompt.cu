@@ -47,8 +47,9 @@ constexpr int kD = 128;                   // head size
 constexpr int kRows = 128;                // rows of a tile
 constexpr int kBlk = 128;                 // keys of a block, as they are loaded
 constexpr int kSub = 64;                  // and as they are multiplied
-constexpr int kThreads = 384;             // 8 softmax warps; TMA, an MMA warp a tile, one that looks over V
-constexpr int kTma = 8, kMma = 9, kLook = 11;           // these warps
+constexpr int kThreads = 480;             // 8 softmax warps; TMA, an MMA warp a tile, 4 that look over V
+constexpr int kTma = 8, kMma = 9, kLook = 11, kLooks = 4;           // these warps
+constexpr int kTable = 256;               // entries of the sequence tables held on chip
 constexpr int kStages = 5;                // K and V blocks in flight
 constexpr int kHalf = kRows * 128;        // bytes of 64 of the 128 dimensions
 constexpr int kTile = 2 * kHalf;
@@ -56,15 +57,17 @@ constexpr float kLazy = 8.0f;             // octaves
 
 struct Shared {                           // behind the tiles
   uint64_t full[kStages], empty[kStages], clean[kStages];
-  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2];   // [tile][buffer]
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2];   // [tile][buffer]
   uint64_t drain;
   uint32_t tmem;
   int abort, dirty;
   int lo_min, hi_max;                     // keys that any row sees
   int lo_max, hi_min;                     // keys that every row sees
   int t_lo[2], t_hi[2];                   // keys that any row of a tile sees
+  int cu_q[kTable], cu_k[kTable];
 };
-constexpr size_t kSmem = 1024 + (size_t)(2 + kStages) * kTile + sizeof(Shared);
+constexpr size_t kSmem = (size_t)(2 + kStages) * kTile + sizeof(Shared);
+static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 
 struct Params {
   const int32_t *cu_q, *cu_k;
@@ -106,18 +109,19 @@ template <typename T> __device__ __forceinline__ float to_f32(T x) {
 
 // The range of packed keys that query token `tok` sees.  False where no
 // sequence holds it.
-__device__ __forceinline__ bool row_keys(const Params& p, int tok, int& lo, int& hi) {
+__device__ __forceinline__ bool row_keys(const Params& p, const int32_t* cu_q, const int32_t* cu_k, int tok, int& lo,
+                                         int& hi) {
   lo = hi = 0;
   int a = 0, b = p.n_seqs + 1;            // cu_q[a - 1] <= tok < cu_q[b]
   while (a < b) {
     const int m = (a + b) >> 1;
-    if (p.cu_q[m] <= tok) a = m + 1;
+    if (cu_q[m] <= tok) a = m + 1;
     else b = m;
   }
   if (a == 0 || a > p.n_seqs) return false;
-  const int q0 = p.cu_q[a - 1], q1 = p.cu_q[a];
-  lo = min(max(p.cu_k[a - 1], 0), p.Tk);
-  hi = min(max(p.cu_k[a], lo), p.Tk);
+  const int q1 = cu_q[a];
+  lo = min(max(cu_k[a - 1], 0), p.Tk);
+  hi = min(max(cu_k[a], lo), p.Tk);
   if (p.causal) hi = (int)max((long long)lo, (long long)hi - (q1 - 1 - tok));
   return true;
 }
@@ -141,8 +145,11 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) uint8_t base[];
+  if (smem_u32(base) & 1023) {            // the swizzle goes by addresses; there is no room to align here
+    set_status(p.status, SSA_ST_INTERNAL);
+    return;
+  }
   uint8_t* s_q = base;
   uint8_t* s_kv = base + 2 * kTile;
   Shared& sh = *reinterpret_cast<Shared*>(base + (2 + kStages) * kTile);
@@ -154,10 +161,12 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
   const int tok0 = pair * 2 * p.tpt;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 2); mbar_init(&sh.clean[i], 1); }
+    for (int i = 0; i < kStages; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 2); mbar_init(&sh.clean[i], kLooks); }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.q_full[i], 1); mbar_init(&sh.o_full[i], 1);
-      for (int b = 0; b < 2; ++b) { mbar_init(&sh.s_full[i][b], 1); mbar_init(&sh.p_full[i][b], 4); }
+      mbar_init(&sh.q_full[i], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&sh.s_full[i][b], 1); mbar_init(&sh.p_full[i][b], 4); mbar_init(&sh.o_full[i][b], 1);
+      }
       sh.t_lo[i] = INT_MAX; sh.t_hi[i] = 0;
     }
     mbar_init(&sh.drain, 2);
@@ -170,7 +179,14 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
   if (threadIdx.x == 256) { prefetch_tmap(&tm_q); prefetch_tmap(&tm_k); prefetch_tmap(&tm_v); }
   pdl_trigger();
   pdl_wait();
+  const bool on_chip = p.n_seqs < kTable;
+  if (on_chip && threadIdx.x <= p.n_seqs) {
+    sh.cu_q[threadIdx.x] = p.cu_q[threadIdx.x];
+    sh.cu_k[threadIdx.x] = p.cu_k[threadIdx.x];
+  }
+  tc5_fence_before();
   __syncthreads();
+  tc5_fence_after();
 
   // rows: threads 0..127 tile 0, 128..255 tile 1
   const int tile = (threadIdx.x >> 7) & 1, r = threadIdx.x & 127;
@@ -178,23 +194,33 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
   int lo = 0, hi = 0;
   bool in_seq = false;
   if (threadIdx.x < 256) {
-    in_seq = r < p.tpt * p.G && tok < p.Tq && row_keys(p, tok, lo, hi);
-    if (lo < hi) {
-      atomicMin(&sh.lo_min, lo); atomicMax(&sh.hi_max, hi);
-      atomicMax(&sh.lo_max, lo); atomicMin(&sh.hi_min, hi);
-      atomicMin(&sh.t_lo[tile], lo); atomicMax(&sh.t_hi[tile], hi);
+    if (r < p.tpt * p.G && tok < p.Tq)
+      in_seq = on_chip ? row_keys(p, sh.cu_q, sh.cu_k, tok, lo, hi) : row_keys(p, p.cu_q, p.cu_k, tok, lo, hi);
+    const bool any = lo < hi;
+    const int least = __reduce_min_sync(~0u, any ? lo : INT_MAX), most = __reduce_max_sync(~0u, any ? hi : 0);
+    const int lo_max = __reduce_max_sync(~0u, any ? lo : 0), hi_min = __reduce_min_sync(~0u, any ? hi : INT_MAX);
+    if (lane == 0 && most > 0) {
+      atomicMin(&sh.lo_min, least); atomicMax(&sh.hi_max, most);
+      atomicMax(&sh.lo_max, lo_max); atomicMin(&sh.hi_min, hi_min);
+      atomicMin(&sh.t_lo[tile], least); atomicMax(&sh.t_hi[tile], most);
     }
+  } else if (warp == kTma) {
+    // q needs no range
+    for (int t = 0; lane == 0 && t < 2; ++t)
+      if (tok0 + t * p.tpt < p.Tq) {
+        mbar_arrive_expect_tx(&sh.q_full[t], 2u * 128u * p.G * p.tpt);
+        for (int h = 0; h < 2; ++h)
+          tma_load_4d(s_q + t * kTile + h * kHalf, &tm_q, &sh.q_full[t], h * 64, 0, head, tok0 + t * p.tpt);
+      }
   } else if (id == 0) {                   // the tables themselves: ascending, inside the tensors
     bool bad = false;
-    for (int i = threadIdx.x - 256; i <= p.n_seqs; i += 128) {
+    for (int i = threadIdx.x - 288; i <= p.n_seqs; i += kThreads - 288) {
       const int a = p.cu_q[i], b = p.cu_k[i];
       bad = bad || a < (i ? p.cu_q[i - 1] : 0) || b < (i ? p.cu_k[i - 1] : 0) || a > p.Tq || b > p.Tk;
     }
     if (bad) set_status(p.status, SSA_ST_BAD_POS);
   }
-  tc5_fence_before();
   __syncthreads();
-  tc5_fence_after();
 
   // blocks of this CTA, and of each tile in it
   const int x0 = sh.lo_min;
@@ -217,13 +243,6 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
 
   if (warp == kTma && lane == 0) {
     // ---- loads ----
-    const uint32_t q_bytes = 2u * 128u * p.G * p.tpt;
-    for (int t = 0; t < 2; ++t)
-      if (tb0[t] < tb1[t]) {
-        mbar_arrive_expect_tx(&sh.q_full[t], q_bytes);
-        for (int h = 0; h < 2; ++h)
-          tma_load_4d(s_q + t * kTile + h * kHalf, &tm_q, &sh.q_full[t], h * 64, 0, head, tok0 + t * p.tpt);
-      }
     int it = 0;
     bool ok = true;
     for (int i = b0; ok && i < b1; ++i)
@@ -235,9 +254,10 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
           tma_load_3d(s_kv + st * kTile + h * kHalf, v ? (const void*)&tm_v : (const void*)&tm_k, &sh.full[st],
                       h * 64, head, x0 + i * kBlk);
       }
-    if (*abort) {                         // copies in flight land before the CTA goes
-      for (int t = 0; t < 2; ++t)
-        if (tb0[t] < tb1[t]) mbar_wait(&sh.q_full[t], 0, nullptr);
+    // copies in flight land before the CTA goes: q's of rows without keys, and all if it gives up
+    for (int t = 0; t < 2; ++t)
+      if (tok0 + t * p.tpt < p.Tq) mbar_wait(&sh.q_full[t], 0, nullptr);
+    if (*abort) {
       for (int j = max(0, it - kStages); j < it; ++j)
         mbar_wait(&sh.full[j % kStages], (j / kStages) & 1, nullptr);
     }
@@ -311,7 +331,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
         const uint32_t v = a_v + vs * (kTile >> 4) + (j & 1) * (kSub * 128 >> 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k) tc5_mma_ta(O, S + (j & 1) * kSub + k * 8, v + k * 128, id_pv, j > first || k > 0);
-        tc5_commit(&sh.o_full[t]);
+        tc5_commit(&sh.o_full[t][j & 1]);
         if (j + 2 < last) scores(j + 2);
         if ((j & 1) || j == last - 1) next_v(true);
       }
@@ -319,7 +339,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
     skip(b1 - max(i1, i0));
     release(&sh.drain, i0 < i1);          // no MMA is in flight when the CTA goes
     mbar_wait(&sh.drain, 0, nullptr);
-  } else if (warp == kLook) {
+  } else if (warp >= kLook) {
     // ---- V of the blocks that some row does not see all of: what is not finite becomes zero ----
     const int lo_max = sh.lo_max, hi_min = sh.hi_min;
     int vs = 1;
@@ -330,7 +350,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
         uint4* v = reinterpret_cast<uint4*>(s_kv + vs * kTile);
         bool found = false;
 #pragma unroll 8
-        for (int j = lane; j < kTile / 16; j += 32) {
+        for (int j = threadIdx.x - kLook * 32; j < kTile / 16; j += kLooks * 32) {
           const uint4 w = v[j];
           if (any_odd<T>(w)) {
             v[j] = make_uint4(finite_part<T>(w.x), finite_part<T>(w.y), finite_part<T>(w.z), finite_part<T>(w.w));
@@ -358,6 +378,10 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
       if (!ok) give_up(SSA_ST_TIMEOUT);
       return ok;
     };
+    // The first n products P V are done.  Each of the two barriers is at most one
+    // phase short: the scores of half block n - 1 came behind the product n - 3,
+    // which used the barrier of n - 1 before it.
+    const auto o_done = [&](int n) { return mbar_wait(&sh.o_full[tile][(n - 1) & 1], ((n - 1) >> 1) & 1, abort); };
     float m = -INFINITY, l = 0.0f;
     int n = 0;
     bool ok = true;
@@ -392,7 +416,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
         if (move) m = top;
         l *= a;
         if (n > 0) {
-          if (!all(mbar_wait(&sh.o_full[tile], (n - 1) & 1, abort))) { ok = false; break; }
+          if (!all(o_done(n))) { ok = false; break; }
           tc5_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
@@ -428,14 +452,13 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
       if (lane == 0) mbar_arrive(&sh.p_full[tile][j & 1]);
     }
     // ---- epilogue ----
-    // (the last scores came behind the last product but two: one phase after the other)
-    if (ok && n > 1) ok = all(mbar_wait(&sh.o_full[tile], n & 1, abort));
-    if (ok && n > 0) ok = all(mbar_wait(&sh.o_full[tile], (n - 1) & 1, abort));
+    if (ok && n > 0) ok = all(o_done(n));
+    // (without a product nobody has waited for the queries, whose place is used below)
+    if (ok && n == 0 && tok0 + tile * p.tpt < p.Tq) ok = all(mbar_wait(&sh.q_full[tile], 0, abort));
     if (ok) {
       tc5_fence_after();
       const bool seen = live && n > 0;
       if (!live) { m = -INFINITY; l = 0.0f; }          // (a row without keys ran along)
-      const float inv = 1.0f / l;
       const size_t row = (((size_t)pair * p.Hkv + head) * p.n_split + split) * (2 * kRows) + threadIdx.x;
       const int hq = head * p.G + r % p.G;
       if (p.n_split > 1) {
@@ -444,46 +467,65 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
       } else if (in_seq && p.lse) {
         p.lse[(size_t)tok * p.Hq + hq] = l != 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
       }
+      // The warp's 32 rows go through the shared memory of its tile's queries, whose
+      // products are done, so that a row is written by neighbouring lanes: 32 lanes
+      // on 32 rows took 6,000 clocks.  256 bytes of a row at a time (all of it, or
+      // half of the fp32 row of a split), 16-byte pieces turned by the row.
+      uint8_t* const mine = s_q + tile * kTile + (warp & 3) * 32 * 256;
+      const int64_t place = p.n_split > 1 ? (int64_t)row * kD : tok * p.o_tok + hq * p.o_head;
+      const uint32_t rows = __ballot_sync(~0u, in_seq);
+      const float f = p.n_split > 1 ? 1.0f : seen && l != 0.0f ? 1.0f / l : 0.0f;
+      for (int part = 0; part < (p.n_split > 1 ? 2 : 1); ++part) {
+        const int n_c = p.n_split > 1 ? 2 : 4;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
-        if (n > 0) {
-          tmem_ld32(o, O + 32 * c);
-          tmem_wait_ld(o);
-        }
-        if (in_seq) {
+        for (int c = 0; c < n_c; ++c) {
+          uint32_t o[32];
+          const int col = 64 * part + 32 * c;
+          if (n > 0) {
+            tmem_ld32(o, O + col);
+            tmem_wait_ld(o);
+          }
           if (!seen) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0;
+            for (int e = 0; e < 32; ++e) o[e] = 0;
           }
           if (seen && sh.dirty) {         // what was set to zero, for the rows that see it
-            const T* v = static_cast<const T*>(p.v) + head * p.v_head + 32 * c;
+            const T* v = static_cast<const T*>(p.v) + head * p.v_head + col;
             for (int x = max(lo, x0 + b0 * kBlk); x < min(hi, x0 + b1 * kBlk); ++x) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float e = to_f32<T>(v[(int64_t)x * p.v_tok + j]);
-                if (!isfinite(e)) o[j] = __float_as_uint(__uint_as_float(o[j]) + e);
+              for (int e = 0; e < 32; ++e) {
+                const float y = to_f32<T>(v[(int64_t)x * p.v_tok + e]);
+                if (!isfinite(y)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
               }
             }
           }
           if (p.n_split > 1) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + row * kD + 32 * c);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              dst[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
-                                   __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(mine + lane * 256 + (((8 * c + e) ^ (lane & 15)) << 4)) =
+                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           } else {
-            const float f = seen && l != 0.0f ? inv : 0.0f;
-            T* dst = static_cast<T*>(p.out) + tok * p.o_tok + hq * p.o_head + 32 * c;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int e = 0; e < 4; ++e) {
               uint32_t w[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack16<T>(__uint_as_float(o[8 * j + 2 * e]) * f, __uint_as_float(o[8 * j + 2 * e + 1]) * f);
-              reinterpret_cast<uint4*>(dst)[j] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int i = 0; i < 4; ++i)
+                w[i] = pack16<T>(__uint_as_float(o[8 * e + 2 * i]) * f, __uint_as_float(o[8 * e + 2 * i + 1]) * f);
+              *reinterpret_cast<uint4*>(mine + lane * 256 + (((4 * c + e) ^ (lane & 15)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
+        }
+        __syncwarp();
+        char* const dst = p.n_split > 1 ? reinterpret_cast<char*>(p.part_o + 64 * part) : static_cast<char*>(p.out);
+        const int size = p.n_split > 1 ? 4 : 2, piece = lane & 15;
+#pragma unroll 4
+        for (int e = 0; e < 16; ++e) {
+          const int rr = 2 * e + (lane >> 4);
+          const int64_t at = __shfl_sync(~0u, place, rr);
+          if (rows >> rr & 1)
+            *reinterpret_cast<uint4*>(dst + at * size + 16 * piece) =
+                *reinterpret_cast<const uint4*>(mine + rr * 256 + ((piece ^ (rr & 15)) << 4));
         }
         __syncwarp();
       }
