@@ -61,9 +61,7 @@ struct Shared {                           // behind the tiles
   uint64_t drain;
   uint32_t tmem;
   int abort, dirty;
-  int lo_min, hi_max;                     // keys that any row sees
-  int lo_max, hi_min;                     // keys that every row sees
-  int t_lo[2], t_hi[2];                   // keys that any row of a tile sees
+  int4 seen[8];                           // of each 32 rows: least lo, greatest hi, greatest lo, least hi
   int cu_q[kTable], cu_k[kTable];
 };
 constexpr size_t kSmem = (size_t)(2 + kStages) * kTile + sizeof(Shared);
@@ -105,6 +103,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 template <typename T> __device__ __forceinline__ float to_f32(T x) {
   if constexpr (std::is_same_v<T, __half>) return __half2float(x);
   else return __bfloat162float(x);
+}
+
+template <typename T> __device__ __forceinline__ T from_f32(float x) {
+  if constexpr (std::is_same_v<T, __half>) return __float2half_rn(x);
+  else return __float2bfloat16_rn(x);
 }
 
 // The range of packed keys that query token `tok` sees.  False where no
@@ -160,19 +163,22 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
   const int head = rest % p.Hkv, pair = p.n_pairs - 1 - rest / p.Hkv;   // the longest rows first
   const int tok0 = pair * 2 * p.tpt;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 2); mbar_init(&sh.clean[i], kLooks); }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.q_full[i], 1);
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(&sh.s_full[i][b], 1); mbar_init(&sh.p_full[i][b], 4); mbar_init(&sh.o_full[i][b], 1);
-      }
-      sh.t_lo[i] = INT_MAX; sh.t_hi[i] = 0;
-    }
+  if (threadIdx.x < kStages) {
+    mbar_init(&sh.full[threadIdx.x], 1);
+    mbar_init(&sh.empty[threadIdx.x], 2);
+    mbar_init(&sh.clean[threadIdx.x], kLooks);
+    fence_barrier_init();
+  } else if (threadIdx.x >= 8 && threadIdx.x < 12) {
+    const int t = threadIdx.x & 1, b = threadIdx.x >> 1 & 1;
+    mbar_init(&sh.s_full[t][b], 1);
+    mbar_init(&sh.p_full[t][b], 4);
+    mbar_init(&sh.o_full[t][b], 1);
+    fence_barrier_init();
+  } else if (threadIdx.x == 12) {
+    mbar_init(&sh.q_full[0], 1);
+    mbar_init(&sh.q_full[1], 1);
     mbar_init(&sh.drain, 2);
     sh.abort = sh.dirty = 0;
-    sh.lo_min = sh.hi_min = INT_MAX;
-    sh.hi_max = sh.lo_max = 0;
     fence_barrier_init();
   }
   if (warp == kMma) tmem_alloc_all(&sh.tmem);
@@ -199,11 +205,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
     const bool any = lo < hi;
     const int least = __reduce_min_sync(~0u, any ? lo : INT_MAX), most = __reduce_max_sync(~0u, any ? hi : 0);
     const int lo_max = __reduce_max_sync(~0u, any ? lo : 0), hi_min = __reduce_min_sync(~0u, any ? hi : INT_MAX);
-    if (lane == 0 && most > 0) {
-      atomicMin(&sh.lo_min, least); atomicMax(&sh.hi_max, most);
-      atomicMax(&sh.lo_max, lo_max); atomicMin(&sh.hi_min, hi_min);
-      atomicMin(&sh.t_lo[tile], least); atomicMax(&sh.t_hi[tile], most);
-    }
+    if (lane == 0) sh.seen[warp] = make_int4(least, most, lo_max, hi_min);
   } else if (warp == kTma) {
     // q needs no range
     for (int t = 0; lane == 0 && t < 2; ++t)
@@ -223,19 +225,34 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
   __syncthreads();
 
   // blocks of this CTA, and of each tile in it
-  const int x0 = sh.lo_min;
-  const int nb = sh.hi_max > 0 ? (sh.hi_max - x0 + kBlk - 1) / kBlk : 0;
+  int x0 = INT_MAX, end = 0, lo_max = 0, hi_min = INT_MAX, t_lo[2], t_hi[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    t_lo[t] = INT_MAX;
+    t_hi[t] = 0;
+#pragma unroll
+    for (int w = 4 * t; w < 4 * t + 4; ++w) {
+      const int4 u = sh.seen[w];
+      t_lo[t] = min(t_lo[t], u.x);
+      t_hi[t] = max(t_hi[t], u.y);
+      lo_max = max(lo_max, u.z);          // what every row sees begins here
+      hi_min = min(hi_min, u.w);          // and ends here
+    }
+    x0 = min(x0, t_lo[t]);
+    end = max(end, t_hi[t]);
+  }
+  const int nb = end > 0 ? (end - x0 + kBlk - 1) / kBlk : 0;
   const int b0 = (int)((long long)nb * split / p.n_split), b1 = (int)((long long)nb * (split + 1) / p.n_split);
   int tb0[2], tb1[2], j1[2];              // j1: the first half block that a tile does not need
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     tb0[t] = tb1[t] = b1;
-    if (sh.t_hi[t] > 0) {
-      tb0[t] = max(b0, (sh.t_lo[t] - x0) / kBlk);
-      tb1[t] = min(b1, (sh.t_hi[t] - x0 + kBlk - 1) / kBlk);
+    if (t_hi[t] > 0) {
+      tb0[t] = max(b0, (t_lo[t] - x0) / kBlk);
+      tb1[t] = min(b1, (t_hi[t] - x0 + kBlk - 1) / kBlk);
       if (tb1[t] <= tb0[t]) tb0[t] = tb1[t] = b1;         // none in this part
     }
-    j1[t] = tb0[t] < tb1[t] ? min(2 * tb1[t], (sh.t_hi[t] - x0 + kSub - 1) / kSub) : 2 * tb0[t];
+    j1[t] = tb0[t] < tb1[t] ? min(2 * tb1[t], (t_hi[t] - x0 + kSub - 1) / kSub) : 2 * tb0[t];
   }
   const uint32_t tmem = sh.tmem;
   volatile int* abort = &sh.abort;
@@ -271,7 +288,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
     const uint32_t q = tc5_desc(smem_u32(s_q + t * kTile), 16), a_k = tc5_desc(smem_u32(s_kv), 16),
                    a_v = tc5_desc(smem_u32(s_kv), kHalf);
     const uint32_t S = tmem + t * 128, O = tmem + 256 + t * 128;
-    const int i0 = tb0[t], i1 = tb1[t], first = 2 * i0, last = j1[t];
+    const int i0 = t ? tb0[1] : tb0[0], i1 = t ? tb1[1] : tb1[0], first = 2 * i0, last = t ? j1[1] : j1[0];
     bool ok = true;
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
       ok = ok && __all_sync(~0u, mbar_wait(bar, parity, abort));
@@ -341,7 +358,6 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
     mbar_wait(&sh.drain, 0, nullptr);
   } else if (warp >= kLook) {
     // ---- V of the blocks that some row does not see all of: what is not finite becomes zero ----
-    const int lo_max = sh.lo_max, hi_min = sh.hi_min;
     int vs = 1;
     uint32_t vp = 0;
     for (int i = b0; i < b1; ++i) {
@@ -385,8 +401,8 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
     float m = -INFINITY, l = 0.0f;
     int n = 0;
     bool ok = true;
-    const int first = 2 * tb0[tile];
-    for (int j = first; j < j1[tile]; ++j, ++n) {
+    const int first = 2 * (tile ? tb0[1] : tb0[0]), last = tile ? j1[1] : j1[0];
+    for (int j = first; j < last; ++j, ++n) {
       const uint32_t Sj = S + (j & 1) * kSub;
       if (!all(mbar_wait(&sh.s_full[tile][j & 1], (n >> 1) & 1, abort))) { ok = false; break; }
       tc5_fence_after();
@@ -475,51 +491,10 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
       const int64_t place = p.n_split > 1 ? (int64_t)row * kD : tok * p.o_tok + hq * p.o_head;
       const uint32_t rows = __ballot_sync(~0u, in_seq);
       const float f = p.n_split > 1 ? 1.0f : seen && l != 0.0f ? 1.0f / l : 0.0f;
-      for (int part = 0; part < (p.n_split > 1 ? 2 : 1); ++part) {
-        const int n_c = p.n_split > 1 ? 2 : 4;
-#pragma unroll 1
-        for (int c = 0; c < n_c; ++c) {
-          uint32_t o[32];
-          const int col = 64 * part + 32 * c;
-          if (n > 0) {
-            tmem_ld32(o, O + col);
-            tmem_wait_ld(o);
-          }
-          if (!seen) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0;
-          }
-          if (seen && sh.dirty) {         // what was set to zero, for the rows that see it
-            const T* v = static_cast<const T*>(p.v) + head * p.v_head + col;
-            for (int x = max(lo, x0 + b0 * kBlk); x < min(hi, x0 + b1 * kBlk); ++x) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float y = to_f32<T>(v[(int64_t)x * p.v_tok + e]);
-                if (!isfinite(y)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
-              }
-            }
-          }
-          if (p.n_split > 1) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4*>(mine + lane * 256 + (((8 * c + e) ^ (lane & 15)) << 4)) =
-                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                w[i] = pack16<T>(__uint_as_float(o[8 * e + 2 * i]) * f, __uint_as_float(o[8 * e + 2 * i + 1]) * f);
-              *reinterpret_cast<uint4*>(mine + lane * 256 + (((4 * c + e) ^ (lane & 15)) << 4)) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-        }
+      const auto write = [&](char* dst, int size) {
         __syncwarp();
-        char* const dst = p.n_split > 1 ? reinterpret_cast<char*>(p.part_o + 64 * part) : static_cast<char*>(p.out);
-        const int size = p.n_split > 1 ? 4 : 2, piece = lane & 15;
-#pragma unroll 4
+        const int piece = lane & 15;
+#pragma unroll 8
         for (int e = 0; e < 16; ++e) {
           const int rr = 2 * e + (lane >> 4);
           const int64_t at = __shfl_sync(~0u, place, rr);
@@ -528,6 +503,61 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
                 *reinterpret_cast<const uint4*>(mine + rr * 256 + ((piece ^ (rr & 15)) << 4));
         }
         __syncwarp();
+      };
+      // What was set to zero, for the rows that see it: added to the staged row, elements
+      // of type E, dimensions from `col` on.
+      const bool dirty = seen && sh.dirty;
+      const auto restore = [&](auto* type, int col, int dims) {
+        using E = std::remove_const_t<std::remove_pointer_t<decltype(type)>>;
+        if (!dirty) return;
+        const T* v = static_cast<const T*>(p.v) + head * p.v_head + col;
+        for (int x = max(lo, x0 + b0 * kBlk); x < min(hi, x0 + b1 * kBlk); ++x)
+#pragma unroll 4
+          for (int e = 0; e < dims; ++e) {
+            const float y = to_f32<T>(v[(int64_t)x * p.v_tok + e]);
+            if (isfinite(y)) continue;
+            const int at = e * (int)sizeof(E);
+            E* z = reinterpret_cast<E*>(mine + lane * 256 + ((at >> 4 ^ (lane & 15)) << 4) + (at & 15));
+            if constexpr (sizeof(E) == 4) *z += y;
+            else *z = from_f32<T>(to_f32<T>(*z) + y);
+          }
+      };
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {       // 64 of the 128 dimensions
+        uint32_t o[2][32];
+        if (n > 0) {
+          tmem_ld32(o[0], O + 64 * h);
+          tmem_ld32(o[1], O + 64 * h + 32);
+          tmem_wait_ld(o[0]);
+          tmem_wait_ld(o[1]);
+        }
+        if (!seen) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e) o[e >> 5][e & 31] = 0;
+        }
+        if (p.n_split > 1) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            *reinterpret_cast<uint4*>(mine + lane * 256 + ((e ^ (lane & 15)) << 4)) =
+                *reinterpret_cast<uint4*>(&o[e >> 3][4 * (e & 7)]);
+          restore(static_cast<const float*>(nullptr), 64 * h, 64);
+          write(reinterpret_cast<char*>(p.part_o + 64 * h), 4);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t* x = &o[e >> 2][8 * (e & 3)];
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack16<T>(__uint_as_float(x[2 * i]) * f, __uint_as_float(x[2 * i + 1]) * f);
+            *reinterpret_cast<uint4*>(mine + lane * 256 + (((8 * h + e) ^ (lane & 15)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (p.n_split == 1) {
+        restore(static_cast<const T*>(nullptr), 0, kD);
+        write(static_cast<char*>(p.out), 2);
       }
     }
     tc5_fence_before();
@@ -540,36 +570,72 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
   }
 }
 
-// out = sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - max m): a warp per row,
-// four dimensions a lane, the splits in order.
+// out = sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - max m): `warps` warps a row, four
+// dimensions a lane, eight splits of a warp in flight (each read is a round trip to
+// L2: with one warp a row 76 splits took 25 us).  Always in the same order.
 template <typename T>
-__global__ void __launch_bounds__(256) prompt_join_kernel(const Params p) {
+__global__ void __launch_bounds__(256) prompt_join_kernel(const Params p, int warps) {
+  __shared__ float4 s_o[8][32];
+  __shared__ float s_m[8], s_l[8];
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp & (warps - 1);
+  const long long i = (long long)blockIdx.x * (8 / warps) + warp / warps;
   const int tok = (int)(i / p.Hq), hq = (int)(i % p.Hq);
-  if (tok >= p.Tq) return;
-  const int head = hq / p.G, pair = tok / (2 * p.tpt), in = tok % (2 * p.tpt);
-  const int r = in / p.tpt * kRows + in % p.tpt * p.G + hq % p.G;
-  const size_t row0 = ((size_t)pair * p.Hkv + head) * p.n_split * (2 * kRows) + r;
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-  if (ml[row0].y < 0.0f) return;          // not a token of any sequence
-  float m = -INFINITY;
-  for (int s = lane; s < p.n_split; s += 32) m = fmaxf(m, ml[row0 + (size_t)s * 2 * kRows].x);
-  m = warp_max(m);
-  float l = 0.0f;
+  bool mine = tok < p.Tq;
+  float m = -INFINITY, l = 0.0f;
   float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-  for (int s = 0; s < p.n_split; ++s) {
-    const size_t row = row0 + (size_t)s * 2 * kRows;
-    const float2 x = ml[row];
-    const float4 y = reinterpret_cast<const float4*>(p.part_o + row * kD)[lane];
-    if (x.y == 0.0f) continue;            // saw no key
-    const float w = fast_exp2(x.x - m);
-    l += w * x.y;
-    o.x += w * y.x; o.y += w * y.y; o.z += w * y.z; o.w += w * y.w;
+  if (mine) {
+    const int head = hq / p.G, pair = tok / (2 * p.tpt), in = tok % (2 * p.tpt);
+    const int r = in / p.tpt * kRows + in % p.tpt * p.G + hq % p.G;
+    const size_t row0 = ((size_t)pair * p.Hkv + head) * p.n_split * (2 * kRows) + r;
+    for (int s0 = w; s0 < p.n_split; s0 += 8 * warps) {
+      float2 ml[8];
+      float4 y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const size_t row = row0 + (size_t)min(s0 + e * warps, p.n_split - 1) * 2 * kRows;
+        ml[e] = reinterpret_cast<const float2*>(p.part_ml)[row];
+        y[e] = reinterpret_cast<const float4*>(p.part_o + row * kD)[lane];
+        if (s0 + e * warps >= p.n_split) ml[e] = make_float2(-INFINITY, 0.0f);
+      }
+      if (ml[0].y < 0.0f) mine = false;   // not a token of any sequence: every split says so
+      float top = m;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, ml[e].x);
+      const float old = m == -INFINITY ? 0.0f : fast_exp2(m - top);
+      m = top;
+      l *= old;
+      o.x *= old; o.y *= old; o.z *= old; o.w *= old;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (ml[e].y == 0.0f) continue;    // saw no key
+        const float f = fast_exp2(ml[e].x - m);
+        l += f * ml[e].y;
+        o.x += f * y[e].x; o.y += f * y[e].y; o.z += f * y[e].z; o.w += f * y[e].w;
+      }
+    }
   }
+  if (warps > 1) {
+    s_o[warp][lane] = o;
+    if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
+    __syncthreads();
+    if (w != 0) return;
+    float top = m;
+    for (int e = 1; e < warps; ++e) top = fmaxf(top, s_m[warp + e]);
+    const float f0 = m == -INFINITY ? 0.0f : fast_exp2(m - top);
+    l *= f0;
+    o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+    for (int e = 1; e < warps; ++e) {
+      if (s_l[warp + e] == 0.0f) continue;
+      const float f = fast_exp2(s_m[warp + e] - top);
+      const float4 y = s_o[warp + e][lane];
+      l += f * s_l[warp + e];
+      o.x += f * y.x; o.y += f * y.y; o.z += f * y.z; o.w += f * y.w;
+    }
+    m = top;
+  }
+  if (!mine) return;
   const float f = l != 0.0f ? 1.0f / l : 0.0f;
   T* dst = static_cast<T*>(p.out) + tok * p.o_tok + hq * p.o_head + 4 * lane;
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<T>(o.x * f, o.y * f), pack16<T>(o.z * f, o.w * f));
@@ -612,7 +678,9 @@ cudaError_t launch_prompt(const Params& p, const CUtensorMap& q, const CUtensorM
   count_launch();
   if (e != cudaSuccess || p.n_split == 1) return e;
   const long long rows = (long long)p.Tq * p.Hq;
-  e = launch_pdl(prompt_join_kernel<T>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, p);
+  int warps = 1;                          // of a row: no more than eight splits to each
+  while (warps < 8 && 8 * warps < p.n_split) warps *= 2;
+  e = launch_pdl(prompt_join_kernel<T>, dim3((unsigned)((rows * warps + 7) / 8)), dim3(256), 0, s, p, warps);
   count_launch();
   return e;
 }
