@@ -10,14 +10,13 @@
 // cos and sin once, and walks over its (layer, head) rows.  A row lies in the
 // registers of 2^n lanes, 16 bytes of each half of the rotated part (or of the
 // interleaved pairs, or of the rest) to a lane, so that the sum of squares is n
-// shuffles and the row is read once.  A lane's weights stay in registers while
-// the layer does.
+// shuffles and the row is read once.
 #include "rope.cuh"
 
 namespace ssa {
 namespace {
 
-constexpr int kCtas = 3;                 // per SM
+constexpr int kCtas = 4;                 // per SM
 constexpr int kInFlight = 4;             // 16-byte loads of a lane
 
 struct NormParams {
@@ -46,145 +45,186 @@ __device__ __forceinline__ void fill_table(const NormParams& p, long long tok, i
   __syncwarp();
 }
 
-// 16 bytes as floats, and back.
-template <typename T, int V> __device__ __forceinline__ void widen(uint4 u, float* x) {
+// The token of a warp (more than one warp a token only where they fit 32 bits).
+__device__ __forceinline__ long long token_of(const NormParams& p, long long gw) {
+  return p.split == 1 ? gw : (long long)((uint32_t)gw / (uint32_t)p.split);
+}
+
+// 16 bytes as pairs of floats, and back.
+template <typename T, int V> __device__ __forceinline__ void widen(uint4 u, uint64_t* x) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < V / 2; ++i) {
     if constexpr (sizeof(T) == 4) {
-      x[i] = __uint_as_float(w[i]);
+      x[i] = pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     } else {
       const float2 f = unpack<T>(w[i]);
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
+      x[i] = pack2(f.x, f.y);
     }
   }
 }
-template <typename T, int V> __device__ __forceinline__ uint4 narrow(const float* x) {
+template <typename T, int V> __device__ __forceinline__ uint4 narrow(const uint64_t* x) {
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(x[i]);
-    else w[i] = pack<T>(x[2 * i], x[2 * i + 1]);
+  for (int i = 0; i < V / 2; ++i) {
+    const float2 f = unpack2(x[i]);
+    if constexpr (sizeof(T) == 4) {
+      w[2 * i] = __float_as_uint(f.x);
+      w[2 * i + 1] = __float_as_uint(f.y);
+    } else {
+      w[i] = pack<T>(f.x, f.y);
+    }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Rows in registers: D and rd / 2 (INTER: rd) multiples of V = 16 bytes, at
-// most 32 units to a row.
+// most 32 units to a row.  Weights, cosines and sines are multiplied once a token
+// (and layer) into a table of the warp's own in shared memory: a turned pair is
+//   a' = (f a) (wa c) - (f b) (wb s),  b' = (f b) (wb c) + (f a) (wa s),
+// f the row's norm, four factors a pair (elements that do not turn: one factor).
+// (32,768 tokens of 36 heads of 128 in bf16: 106 us, the bytes at the copy rate take
+// 89.  The factors in registers took 120: 80 registers, 24 warps per SM.)
 template <typename T, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, kCtas) norm_rope_kernel(const __grid_constant__ NormParams p) {
-  extern __shared__ float2 s_cs[];       // [warps][rd / 2]
+  extern __shared__ __align__(16) float4 s_f[];          // [warps][units * NF], then cos and sin [warps][rd / 2]
   constexpr int V = 16 / sizeof(T);
   constexpr int NA = INTER ? 1 : 2;      // accesses of a unit that turns
-  constexpr int NP = INTER ? V / 2 : V;  // its pairs
+  constexpr int H = V / 2;               // pairs of floats of an access
+  constexpr int NF = INTER ? H : V;      // entries of a unit
   constexpr int NR = kInFlight / NA;     // rows in flight
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long gw = (long long)blockIdx.x * (kRopeThreads / 32) + warp;
-  const long long tok = gw / p.split;
+  const long long tok = token_of(p, gw);
   if (tok >= p.T) return;
   const int part = (int)(gw - tok * p.split);
-  float2* cs_w = s_cs + warp * (p.rd / 2);
+  float4* fac = s_f + warp * p.units * NF;
+  float2* cs_w = reinterpret_cast<float2*>(s_f + (kRopeThreads / 32) * p.units * NF) + warp * (p.rd / 2);
   const int col = lane & (p.lanes_row - 1), first = lane / p.lanes_row;
   const bool on = col < p.units, turns = col < p.u_rot, two = NA == 2 && turns;
-  const int e = turns ? col * NP * (INTER ? 2 : 1) : p.rd + (col - p.u_rot) * V;
+  const int e = turns ? col * V : p.rd + (col - p.u_rot) * V;
   const int step = p.rd / 2;
   const float inv_d = 1.0f / (float)p.D;
+  const float4* my = fac + (on ? col : 0);               // entry c of unit u at [c * units + u]: no bank twice
 
   bool have = false;
-  float2 cs[NP];
   for (int xi = 0; xi < p.n_x; ++xi) {
     const RopeRows& x = p.x[xi];
-    const int heads = x.x.heads, rows = p.L * heads;
-    const int base = part * x.per_warp, r1 = min(base + x.per_warp, rows);
-    int left = r1 - base - first;                               // rows from this lane's on
-    int l = (base + first) / heads, h = base + first - l * heads;
-    const int dl = p.rows_pass / heads;
-    const T* in = static_cast<const T*>(x.x.in) + l * x.x.is[0] + tok * x.x.is[1] + h * x.x.is[2] + e;
-    T* out = static_cast<T*>(x.x.out) + l * x.x.os[0] + tok * x.x.os[1] + h * x.x.os[2] + e;
-    int w_of = -1;                                              // the layer of wa, wb
-    __align__(16) float wa[V], wb[V];
+    const int heads = x.x.heads, base = part * x.per_warp, r1 = min(base + x.per_warp, p.L * heads);
+    const float* weights = p.w[xi];
+    int w_of = -1;                                              // the layer of the factors
+    for (int r = base; r < r1;) {                               // a layer's rows together
+      const int l = r / heads, h0 = r - l * heads, n = min(heads - h0, r1 - r);
+      const T* in = static_cast<const T*>(x.x.in) + l * x.x.is[0] + tok * x.x.is[1] + (h0 + first) * x.x.is[2] + e;
+      T* out = static_cast<T*>(x.x.out) + l * x.x.os[0] + tok * x.x.os[1] + (h0 + first) * x.x.os[2] + e;
+      for (int k = 0; k < n; k += p.rows_pass * NR) {
+        uint4 a[NR], b[NR];
+        const int left = on ? n - k - first : 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) wa[i] = wb[i] = 1.0f;
-    for (int r = base; r < r1; r += p.rows_pass * NR) {
-      uint4 a[NR], b[NR];
-      int layer[NR];
-      uint32_t wraps = 0;
-#pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        a[i] = b[i] = make_uint4(0, 0, 0, 0);
-        layer[i] = l;
-        if (on && left > i * p.rows_pass) {
-          a[i] = *reinterpret_cast<const uint4*>(in);
-          if (two) b[i] = *reinterpret_cast<const uint4*>(in + step);
+        for (int i = 0; i < NR; ++i) {
+          a[i] = b[i] = make_uint4(0, 0, 0, 0);
+          if (left > i * p.rows_pass) {
+            a[i] = *reinterpret_cast<const uint4*>(in);
+            if (two) b[i] = *reinterpret_cast<const uint4*>(in + step);
+          }
+          in += x.in_step;
         }
-        in += x.in_step;
-        h += x.dh;
-        l += dl;
-        if (h >= heads) {
-          h -= heads;
-          ++l;
-          in += x.in_wrap;
-          wraps |= 1u << i;
-        }
-      }
-      if (!have) {                        // while the first loads are in flight
-        fill_table(p, tok, lane, cs_w);
+        const float* w = weights ? weights + l * p.w_step[xi] : nullptr;
+        float2 early[2];                  // the first factors' weights, on their way with the rows
+        if (!have) {
 #pragma unroll
-        for (int k = 0; k < NP; ++k) cs[k] = turns ? cs_w[col * NP + k] : make_float2(1.0f, 0.0f);
+          for (int j = 0; j < 2; ++j) {
+            early[j] = make_float2(1.0f, 1.0f);
+            const int at = lane + 32 * j;
+            if (w && at < p.u_rot * NF)
+              early[j] = INTER ? make_float2(w[2 * at], w[2 * at + 1]) : make_float2(w[at], w[at + step]);
+          }
+          fill_table(p, tok, lane, cs_w);
+        }
+        if (w_of < 0 || (p.w_step[xi] && w_of != l)) {
+          w_of = l;
+          __syncwarp();
+#pragma unroll 2
+          for (int j = lane; j < p.units * NF; j += 32) {
+            float4 f = make_float4(1, 0, 0, 0);
+            if (j < p.u_rot * NF) {
+              const int i0 = INTER ? 2 * j : j, i1 = INTER ? 2 * j + 1 : j + step;
+              float wa, wb;
+              if (!have && j < 64) {
+                wa = j < 32 ? early[0].x : early[1].x;
+                wb = j < 32 ? early[0].y : early[1].y;
+              } else {
+                wa = w ? w[i0] : 1.0f;
+                wb = w ? w[i1] : 1.0f;
+              }
+              const float2 c = cs_w[j];
+              // NA == 2: wa c, wa s, wb c, -wb s; INTER: wa c, wb c, -wb s, wa s
+              f = INTER ? make_float4(wa * c.x, wb * c.x, -wb * c.y, wa * c.y)
+                        : make_float4(wa * c.x, wa * c.y, wb * c.x, -wb * c.y);
+            } else if (INTER) {
+              const int i0 = p.rd + 2 * (j - p.u_rot * NF);
+              f = make_float4(w ? w[i0] : 1.0f, w ? w[i0 + 1] : 1.0f, 0, 0);
+            } else if (w) {
+              f.x = w[p.rd + j - p.u_rot * NF];
+            }
+            float* at = reinterpret_cast<float*>(fac + (INTER ? j % NF : j % NF & ~1) * p.units + j / NF);
+            if (INTER) {
+              *reinterpret_cast<float4*>(at) = f;
+            } else {                      // two pairs' factors side by side, as they are multiplied
+              at += j & 1;
+              at[0] = f.x;
+              at[2] = f.y;
+              at[4 * p.units] = f.z;
+              at[4 * p.units + 2] = f.w;
+            }
+          }
+          __syncwarp();
+        }
         have = true;
-      }
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        const bool mine = on && left > i * p.rows_pass;
-        if (mine && p.w[xi] && layer[i] != w_of) {
-          w_of = layer[i];
-          const float* w = p.w[xi] + w_of * p.w_step[xi] + e;
+        for (int i = 0; i < NR; ++i) {
+          uint64_t u[H], v[H], s2 = 0;
+          widen<T, V>(a[i], u);
 #pragma unroll
-          for (int k = 0; k < V; k += 4) *reinterpret_cast<float4*>(wa + k) = *reinterpret_cast<const float4*>(w + k);
-          if (two) {
-#pragma unroll
-            for (int k = 0; k < V; k += 4)
-              *reinterpret_cast<float4*>(wb + k) = *reinterpret_cast<const float4*>(w + step + k);
-          }
-        }
-        float u[V], v[V];
-        widen<T, V>(a[i], u);
-        if constexpr (NA == 2) widen<T, V>(b[i], v);
-        float ss = 0.0f;
-#pragma unroll
-        for (int k = 0; k < V; ++k) ss = fmaf(u[k], u[k], ss);
-        if constexpr (NA == 2) {
-#pragma unroll
-          for (int k = 0; k < V; ++k) ss = fmaf(v[k], v[k], ss);
-        }
-        for (int o = 1; o < p.lanes_row; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float f = rsqrtf(fmaf(ss, inv_d, p.eps));
-#pragma unroll
-        for (int k = 0; k < V; ++k) u[k] *= f * wa[k];
-        if constexpr (NA == 2) {
-#pragma unroll
-          for (int k = 0; k < V; ++k) v[k] *= f * wb[k];
-          if (turns) {
-#pragma unroll
-            for (int k = 0; k < V; ++k) rotate(u[k], v[k], cs[k]);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < NP; ++k) rotate(u[2 * k], u[2 * k + 1], cs[k]);
-        }
-        if (mine) {
-          *reinterpret_cast<uint4*>(out) = narrow<T, V>(u);
+          for (int c = 0; c < H; ++c) s2 = fma2(u[c], u[c], s2);
           if constexpr (NA == 2) {
-            if (two) *reinterpret_cast<uint4*>(out + step) = narrow<T, V>(v);
+            widen<T, V>(b[i], v);
+#pragma unroll
+            for (int c = 0; c < H; ++c) s2 = fma2(v[c], v[c], s2);
           }
+          const float2 s1 = unpack2(s2);
+          float ss = s1.x + s1.y;
+          for (int o = 1; o < p.lanes_row; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float f = rsqrtf(fmaf(ss, inv_d, p.eps));
+          if (left > i * p.rows_pass) {
+            const uint64_t f2 = pack2(f, f);
+#pragma unroll
+            for (int c = 0; c < H; ++c) {
+              u[c] = mul2(u[c], f2);
+              if constexpr (NA == 2) {
+                v[c] = mul2(v[c], f2);
+                const ulonglong2 ga = *reinterpret_cast<const ulonglong2*>(my + 2 * c * p.units);
+                const ulonglong2 gb = *reinterpret_cast<const ulonglong2*>(my + (2 * c + 1) * p.units);
+                const uint64_t z = fma2(v[c], gb.y, mul2(u[c], ga.x));
+                v[c] = fma2(u[c], ga.y, mul2(v[c], gb.x));
+                u[c] = z;
+              } else {
+                const ulonglong2 g = *reinterpret_cast<const ulonglong2*>(my + c * p.units);
+                const float2 t = unpack2(u[c]);
+                u[c] = fma2(pack2(t.y, t.x), g.y, mul2(u[c], g.x));
+              }
+            }
+            *reinterpret_cast<uint4*>(out) = narrow<T, V>(u);
+            if constexpr (NA == 2) {
+              if (two) *reinterpret_cast<uint4*>(out + step) = narrow<T, V>(v);
+            }
+          }
+          out += x.out_step;
         }
-        out += x.out_step;
-        if (wraps >> i & 1) out += x.out_wrap;
       }
-      left -= NR * p.rows_pass;
+      r += n;
     }
   }
 }
@@ -198,7 +238,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_any_kernel(const __gri
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = p.rd / 2;
   const long long gw = (long long)blockIdx.x * (kRopeThreads / 32) + warp;
-  const long long tok = gw / p.split;
+  const long long tok = token_of(p, gw);
   if (tok >= p.T) return;
   const int part = (int)(gw - tok * p.split);
   float2* cs = s_cs + warp * half;
@@ -246,30 +286,31 @@ cudaError_t launch_t(NormParams p, int num_sms, cudaStream_t s) {
   while (p.lanes_row < p.units && p.lanes_row < 32) p.lanes_row *= 2;
   if (!vec) p.lanes_row = 32;
   p.rows_pass = 32 / p.lanes_row;
-  // a warp per token where the tokens fill the machine (32 warps per SM), else
-  // a token's rows over several warps, down to one pass each
+  // a warp per token where the tokens fill the machine, else a token's rows over
+  // several warps, down to one pass each (rounded down: 4,099 tokens x 48 rows in one
+  // wave of a warp each 36 us, in 1.7 waves of half a token 48)
   long long rows = 0;
   for (int i = 0; i < p.n_x; ++i) rows += (long long)p.L * p.x[i].x.heads;
   const long long most = (rows + p.rows_pass - 1) / p.rows_pass;
-  long long split = (32LL * num_sms + p.T - 1) / p.T;
+  long long split = (long long)kCtas * (kRopeThreads / 32) * num_sms / p.T;
   if (split > most) split = most;
+  if (split < 1) split = 1;
   p.split = (int)split;
   for (int i = 0; i < p.n_x; ++i) {
     RopeRows& x = p.x[i];
     const long long n = (long long)p.L * x.x.heads, per = (n + split - 1) / split;
     x.per_warp = (int)((per + p.rows_pass - 1) / p.rows_pass * p.rows_pass);
-    const int dl = p.rows_pass / x.x.heads;
-    x.dh = p.rows_pass % x.x.heads;
-    x.in_step = dl * x.x.is[0] + x.dh * x.x.is[2];
-    x.out_step = dl * x.x.os[0] + x.dh * x.x.os[2];
-    x.in_wrap = x.x.is[0] - x.x.heads * x.x.is[2];
-    x.out_wrap = x.x.os[0] - x.x.heads * x.x.os[2];
+    x.in_step = p.rows_pass * x.x.is[2];
+    x.out_step = p.rows_pass * x.x.os[2];
   }
   const long long ctas = ((long long)p.T * p.split + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  const cudaError_t e = launch_pdl(vec ? norm_rope_kernel<T, INTER> : norm_rope_any_kernel<T, INTER>,
-                                   dim3((unsigned)ctas), dim3(kRopeThreads),
-                                   (size_t)(kRopeThreads / 32) * p.rd / 2 * sizeof(float2), s, p);
+  size_t smem = (size_t)(kRopeThreads / 32) * p.rd / 2 * sizeof(float2);
+  if (vec) smem += (size_t)(kRopeThreads / 32) * p.units * (INTER ? V / 2 : V) * sizeof(float4);
+  const auto kernel = vec ? norm_rope_kernel<T, INTER> : norm_rope_any_kernel<T, INTER>;
+  if (smem > 48 * 1024)
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
+  const cudaError_t e = launch_pdl(kernel, dim3((unsigned)ctas), dim3(kRopeThreads), smem, s, p);
   count_launch();
   return e;
 }
