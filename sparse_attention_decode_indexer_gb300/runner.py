@@ -28,7 +28,12 @@ while the next indexer writes the other.
 With ``rope`` (a RopePlan), queries and keys come without their positions:
 ``store`` rotates the keys by the ``positions`` it is given, ``step`` the
 queries by each request's last position (seq_lens - 1), both into buffers of
-the runner's own, in front of the calls that read them.
+the runner's own, in front of the calls that read them.  With ``norm`` (a
+HeadNorm) their heads are normed in the same pass.
+
+``prefill`` is a prompt's way in, layer by layer: norms and positions, the
+prompts' attention over themselves, the store.  ``beam_step`` is the way on:
+the next tokens of beams, and the pages that follow them.
 """
 from __future__ import annotations
 
@@ -36,9 +41,11 @@ import math
 
 import torch
 
-from . import (KVCache, Layout, RequestTable, ssa_compact_pages, ssa_ensure_remap, ssa_ensure_remap_bind,
+from . import (BeamState, HeadNorm, KVCache, Layout, RequestTable, ssa_beam_select,
+               ssa_beam_workspace_size, ssa_compact_pages, ssa_ensure_remap, ssa_ensure_remap_bind,
                ssa_ensure_remap_deferred, ssa_ensure_remap_shared, ssa_ensure_resident,
-               ssa_fetch_misses, ssa_fork_requests, ssa_index_topk, ssa_lru_init, ssa_prefetch_pages,
+               ssa_fetch_misses, ssa_fork_requests, ssa_index_topk, ssa_lru_init, ssa_norm_rope,
+               ssa_prefetch_pages, ssa_prompt_attention, ssa_prompt_workspace_size,
                ssa_remap_block_table, ssa_rope, ssa_sparse_paged_decode,
                ssa_sparse_paged_decode_fetch, ssa_store_kv_mirror, ssa_workspace_size)
 
@@ -56,7 +63,7 @@ class DecodeRunner:
     def __init__(self, layout: Layout, host_tier: bool, identity: bool, block_table, seq_lens,
                  device="cuda", preload_width: int = 0, shared_residency: bool = False,
                  fetch_in_attention: bool = False, graphs: bool = False,
-                 overlap_groups: int = 0, rope=None):
+                 overlap_groups: int = 0, rope=None, norm: HeadNorm | None = None):
         self.layout = layout
         self.cache = KVCache(layout, host_tier, device)
         L, B, W = layout.n_layers, layout.batch, layout.max_sel
@@ -95,7 +102,13 @@ class DecodeRunner:
         self.overlap_groups = int(overlap_groups)
         if rope is not None and rope.head_dim != layout.head_dim:
             raise ValueError(f"rope: head_dim {rope.head_dim}, the cache's is {layout.head_dim}")
-        self.rope = rope
+        if norm is not None:
+            if rope is None:
+                raise ValueError("norm: with rope, in front of which it stands")
+            if norm.head_dim not in (None, layout.head_dim) or norm.layers not in (None, L):
+                raise ValueError(f"norm: {norm.layers} layers of {norm.head_dim}, the cache has "
+                                 f"{L} of {layout.head_dim}")
+        self.rope, self.norm = rope, norm
         if rope is not None:
             self.q_rot = torch.zeros_like(self.out)
 
@@ -117,6 +130,15 @@ class DecodeRunner:
         self.ev_preload = torch.cuda.Event()
         self.n_steps = 0
 
+    # positions ------------------------------------------------------------------
+    def _place(self, positions, layer0: int, **kw):
+        """q and k (in and out, as for ssa_rope) at their positions, normed first
+        where the runner has norms."""
+        if self.norm is None:
+            ssa_rope(self.rope, positions, **kw)
+        else:
+            ssa_norm_rope(self.rope, self.norm, positions, layer0=layer0, **kw)
+
     # write path ---------------------------------------------------------------
     def store(self, layer0: int, n_layers: int, k, v, pos, positions=None):
         """k, v: bf16 [n_layers][T][Hkv][D] on the device, strided views (of a
@@ -129,8 +151,11 @@ class DecodeRunner:
             if positions is None:
                 raise ValueError("store with rope: positions of the tokens")
             k_rot = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-            ssa_rope(self.rope, positions, k=k, k_out=k_rot)
+            self._place(positions, layer0, k=k, k_out=k_rot)
             k = k_rot
+        self._store(layer0, n_layers, k, v, pos)
+
+    def _store(self, layer0: int, n_layers: int, k, v, pos):
         # with shared residency a page's slot is that of layer 0 in every layer:
         # the other layers' rows say so while the store reads them
         rows = None
@@ -141,6 +166,57 @@ class DecodeRunner:
                             self.status)
         if rows is not None:
             rows.fill_(-1)
+
+    def prefill(self, layer: int, q, k, v, pos, cu_seqlens, positions=None, causal: bool = True):
+        """One layer of whole prompts, packed one behind the other: q [T][Hq][D],
+        k and v [T][Hkv][D] bf16, strided views among them; prompt i has the
+        tokens cu_seqlens[i] .. cu_seqlens[i + 1] (int32 on the device); pos
+        and positions [T] as for ``store`` (so the prompts come in the order of
+        their pages).  Norms and positions, attention of the prompts over
+        themselves, store; returns the attention [T][Hq][D].  (8-bit caches: the
+        prompts attend over K and V as they come, the cache holds them rounded.)"""
+        if self.rope is not None:
+            if positions is None:
+                raise ValueError("prefill with rope: positions of the tokens")
+            q_rot, k_rot = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
+            self._place(positions, layer, q=q, k=k, q_out=q_rot, k_out=k_rot)
+            q, k = q_rot, k_rot
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        ssa_prompt_attention(q, k, v, cu_seqlens, out, self.status,
+                             self._scratch("_prompt_ws", ssa_prompt_workspace_size()),
+                             causal=causal, sm_scale=self.sm_scale)
+        self._wait_preload()
+        self._store(layer, 1, k.contiguous()[None], v.contiguous()[None], pos)
+        return out
+
+    def _scratch(self, name: str, size: int):
+        """A zeroed workspace of the runner's own, made on first use (outside a
+        capture, whose memory would go with its graph)."""
+        ws = getattr(self, name, None)
+        if ws is None or ws.nbytes < size:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("make this call once before a capture")
+            ws = torch.zeros((size,), dtype=torch.uint8, device=self.out.device)
+            setattr(self, name, ws)
+        return ws
+
+    # the next tokens ----------------------------------------------------------------
+    def beam_step(self, logits, state: BeamState, eos: int = -1):
+        """The next tokens of beams: logits [batch][V], the runner's rows in groups
+        of state.beams.  The best of each group become its rows: state in place,
+        and the rows of the table continue the pages of their parents, a token
+        longer (``fork``).  Returns parent and token, int32 [batch], buffers of
+        the runner's own that the next call overwrites."""
+        B = self.layout.batch
+        if state.groups * state.beams != B:
+            raise ValueError(f"state: {state.groups} groups of {state.beams}, the runner has {B} rows")
+        ws = self._scratch(f"_beam_ws_{state.beams}", ssa_beam_workspace_size(state.groups, state.beams))
+        ints = self._scratch("_beam_out", 3 * 4 * B).view(torch.int32).view(3, B)
+        table = self.table
+        ssa_beam_select(logits, state, ints[0], ints[1], self.status, ws, eos=eos,
+                        seq_lens=table.seq_lens, new_lens=ints[2])
+        self.fork(ints[0], ints[2])
+        return ints[0], ints[1]
 
     # owners of the pages ----------------------------------------------------------
     @property
@@ -188,7 +264,7 @@ class DecodeRunner:
         """The queries of the layers `sl` at their requests' last positions."""
         if self.rope is None:
             return q
-        ssa_rope(self.rope, self.seq_lens, q=q, q_out=self.q_rot[sl], offset=-1)
+        self._place(self.seq_lens, sl.start or 0, q=q, q_out=self.q_rot[sl], offset=-1)
         return self.q_rot[sl]
 
     def _calls(self, q, layer0: int, n_layers: int, keep_scores: bool, fused: bool):
