@@ -633,7 +633,9 @@ def _rope_tensor(plan, name, x, out, shape):
     if out is None:
         out = x
     got, lead = x.shape, len(shape) == 4
-    if len(got) != len(shape) or got[:-2] != shape[:-2] or got[-1] != shape[-1]:
+    # (entry by entry: slices of sizes cost more than the rest of a small call)
+    if len(got) != len(shape) or got[0] != shape[0] or got[-1] != shape[-1] or \
+            (lead and got[1] != shape[1]):
         raise ValueError(f"{name}: [n_layers][T][heads][D] or [T][heads][D] with (T, D) of the "
                          f"positions and the plan and the same layers for q and k, got "
                          f"{tuple(got)}")
@@ -754,13 +756,13 @@ def ssa_prompt_workspace_size() -> int:
 def _prompt_tensor(name, x, n, dtype, dev):
     """The C view of q, k, v or out: [n][heads][D], any strides but the last."""
     got = x.shape
-    if len(got) != 3 or (n is not None and got[0] != n) or x.dtype != dtype or x.get_device() != dev:
+    if len(got) != 3 or (n is not None and got[0] != n) or x.dtype is not dtype or x.get_device() != dev:
         raise ValueError(f"{name}: [tokens][heads][D] of q's type and device, k's tokens as v's and "
                          f"q's as out's, got {tuple(got)} {x.dtype} on {x.device}")
-    st = x.stride()
-    if st[2] != 1 and x.numel():
+    t, h, one = x.stride()
+    if one != 1 and x.numel():
         raise ValueError(f"{name}: the elements of a head must be contiguous")
-    return _pack_prompt(x.data_ptr(), got[1], st[0], st[1])
+    return _pack_prompt(x.data_ptr(), got[1], t, h)
 
 
 def ssa_prompt_attention(q, k, v, cu_q, out, status, ws, cu_k=None, causal: bool = True,
@@ -772,34 +774,35 @@ def ssa_prompt_attention(q, k, v, cu_q, out, status, ws, cu_k=None, causal: bool
     tokens are the last ones of its keys.  sm_scale: default 1 / sqrt(D).  lse:
     fp32 [Tq][Hq], the logarithm of each row's sum.  ws: at least
     ssa_prompt_workspace_size() bytes."""
-    dtype, dev = _PROMPT_DTYPES.get(q.dtype), q.get_device()
+    dt, dev, size = q.dtype, q.get_device(), q.shape
+    dtype = _PROMPT_DTYPES.get(dt)
     if dtype is None:
-        raise ValueError(f"q, k, v: bfloat16 or float16, got {q.dtype}")
-    tq = _prompt_tensor("q", q, None, q.dtype, dev)
-    tk = _prompt_tensor("k", k, None, q.dtype, dev)
-    tv = _prompt_tensor("v", v, k.shape[0], q.dtype, dev)
-    to = _prompt_tensor("out", out, q.shape[0], q.dtype, dev)
-    n_q, heads, D = q.shape
-    if k.shape[2] != D or v.shape[1:] != k.shape[1:] or out.shape != q.shape:
-        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, out "
+        raise ValueError(f"q, k, v: bfloat16 or float16, got {dt}")
+    tq = _prompt_tensor("q", q, None, dt, dev)
+    tk = _prompt_tensor("k", k, None, dt, dev)
+    tv = _prompt_tensor("v", v, k.shape[0], dt, dev)
+    to = _prompt_tensor("out", out, size[0], dt, dev)
+    n_q, heads, D = size
+    if k.shape[2] != D or v.shape != k.shape or out.shape != size:
+        raise ValueError(f"q {tuple(size)}, k {tuple(k.shape)}, v {tuple(v.shape)}, out "
                          f"{tuple(out.shape)}: one head size, k and v alike, q and out alike")
-    if cu_k is None:
-        cu_k = cu_q
-    n = cu_q.numel()
-    pq, pk = _ints("cu_q", cu_q, n, dev), _ints("cu_k", cu_k, n, dev)
+    n = cu_q.shape[0] if cu_q.dim() == 1 else 0
+    pq = _ints("cu_q", cu_q, n, dev)
+    pk = pq if cu_k is None or cu_k is cu_q else _ints("cu_k", cu_k, n, dev)
     if n < 1:
         raise ValueError("cu_q: the first token of each sequence, and the end of the last")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n_q, heads) or
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != size[:2] or
                             not lse.is_contiguous() or lse.get_device() != dev):
         raise ValueError(f"lse: contiguous float32 [{n_q}][{heads}] on q's device")
     if status is not None:
         _ints("status", status, 1, dev)
-    if ws.get_device() != dev or ws.nbytes < lib().ssa_prompt_workspace_size() or not ws.is_contiguous():
+    L = lib()
+    if ws.get_device() != dev or ws.nbytes < L.ssa_prompt_workspace_size() or not ws.is_contiguous():
         raise ValueError("ws: ssa_prompt_workspace_size() contiguous bytes on q's device")
     _on_current_device(dev)
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(D)
-    _check(lib().ssa_prompt_attention(dtype, D, n - 1, n_q, k.shape[0], tq, tk, tv, to, pq, pk,
+    _check(L.ssa_prompt_attention(dtype, D, n - 1, n_q, k.shape[0], tq, tk, tv, to, pq, pk,
                                       causal, sm_scale, _ptr(lse), _ptr(status), ws.data_ptr(),
                                       _stream(stream)))
 
