@@ -336,8 +336,8 @@ template <int N> __device__ __forceinline__ uint32_t kth(const uint32_t (&x)[N],
 
 // The group's choice and the new states, by the group's last CTA.  What it takes
 // is round trips to L2, one after another, so loads go out together: the parts,
-// the lists' first candidates and the old states; then the K lists whose first
-// candidates are the best, among which the K best are.
+// the candidates and the old states.  (Of very many candidates the lists' first;
+// then the K lists whose first are the best, among which the K best are.)
 __device__ __noinline__ void choose(const Params& p, int g, Scratch& sc) {
   constexpr int kPerThread = kMaxLists / kThreads;
   const int K = p.K, lists = K * p.parts, tid = threadIdx.x, lane = tid & 31;
@@ -350,20 +350,25 @@ __device__ __noinline__ void choose(const Params& p, int g, Scratch& sc) {
   __shared__ float s_score[kMaxBeams];
   const int row0 = g * K;
   const int2* cand = reinterpret_cast<const int2*>(p.cand + (size_t)row0 * p.parts * K);
-  int2 head[kPerThread];                  // a list is sorted: its first is its best
+  // all candidates where a thread can hold its share of them, else the lists' first,
+  // which are their best
+  const bool every = lists * K <= kMaxLists;
+  const int held = every ? lists * K : lists, of_row = every ? p.parts * K : p.parts;
+  int2 head[kPerThread];
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
     const int i = tid + j * kThreads;
-    head[j] = i < lists ? __ldcg(cand + (size_t)i * K) : make_int2(0, -1);
+    head[j] = i < held ? __ldcg(cand + (size_t)i * (every ? 1 : K)) : make_int2(0, -1);
   }
-  if (tid < K) {                          // everything old: in and out may be the same
-    s_add[tid] = p.scores[row0 + tid];
-    s_old[tid] = p.ended ? p.ended[row0 + tid] : 0;
-    s_lens[tid] = p.seq_lens ? p.seq_lens[row0 + tid] : 0;
-    s_parent[tid] = s_token[tid] = -1;
-    s_score[tid] = -INFINITY;
+  // everything old: in and out may be the same
+  float add = 0.0f;
+  uint8_t old = 0;
+  int lens = 0, len = 0;
+  if (tid < K) {
+    add = p.scores[row0 + tid];
+    if (p.ended) old = p.ended[row0 + tid];
+    if (p.seq_lens) lens = p.seq_lens[row0 + tid];
   }
-  int len = 0;
   if (p.history) len = p.hist_len[g];
   for (int r = tid >> 5; r < K; r += kThreads / 32) {
     const uint4* part = reinterpret_cast<const uint4*>(p.part + (size_t)(row0 + r) * p.parts);
@@ -387,6 +392,13 @@ __device__ __noinline__ void choose(const Params& p, int g, Scratch& sc) {
     z = warp_sum(c > -INFINITY ? z >> (int)fminf(top - c, 63.0f) : 0);
     if (lane == 0) { s_z[r] = z; s_c[r] = top; s_far[r] = far; }
   }
+  if (tid < K) {
+    s_add[tid] = add;
+    s_old[tid] = old;
+    s_lens[tid] = lens;
+    s_parent[tid] = s_token[tid] = -1;
+    s_score[tid] = -INFINITY;
+  }
   if (tid == 0) s_n = s_lists = 0;
   __syncthreads();
   if (tid < K) {
@@ -406,58 +418,57 @@ __device__ __noinline__ void choose(const Params& p, int g, Scratch& sc) {
     return s;
   };
   // (the upper half of a score's rank is in its order)
+  Score mine[kPerThread];
   uint32_t most[kPerThread];
-#pragma unroll
-  for (int j = 0; j < kPerThread; ++j) {
-    const int i = tid + j * kThreads;
-    most[j] = i < lists ? (uint32_t)(score_of(i / p.parts, head[j]).s >> 32) : 0u;
-  }
-  uint32_t bound;
-  if (lists <= kThreads) {
-    const uint32_t one[1] = {most[0]};
-    bound = kth(one, K);
-  } else {
-    bound = kth(most, K);
-  }
-#pragma unroll
-  for (int j = 0; j < kPerThread; ++j)
-    if (most[j] && most[j] >= bound) s_list[atomicAdd(&s_lists, 1)] = (uint16_t)(tid + j * kThreads);
-  __syncthreads();
-  const int some = s_lists * K;           // candidates of those lists
-  const auto place = [&](const Score& s, int r) {
-    s_parent[r] = (int)(s.at >> 32);
-    s_token[r] = (int)(uint32_t)s.at;
-    s_score[r] = (float)unrank64(s.s);
-  };
-  if (some <= kMaxLists) {
-    Score mine[kPerThread];
-#pragma unroll
-    for (int j = 0; j < kPerThread; ++j) {
-      const int i = tid + j * kThreads;
-      mine[j] = Score{0, ~0ull};
-      if (i < some) {
-        const int list = s_list[i / K];
-        mine[j] = score_of(list / p.parts, __ldcg(cand + (size_t)list * K + i % K));
-      }
-      most[j] = (uint32_t)(mine[j].s >> 32);
-    }
-    if (some <= kThreads) {
-      const uint32_t one[1] = {most[0]};
-      bound = kth(one, K);
-    } else {
-      bound = kth(most, K);
-    }
+  const auto listed = [&](int n) {        // of the first n candidates, those among the K best, or equal to them
+    const uint32_t bound = n <= kThreads ? kth<1>({most[0]}, K) : kth<kPerThread>(most, K);
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j)
       if (most[j] && most[j] >= bound) {
         const int at = atomicAdd(&s_n, 1);
         if (at < kFinal) sc.score[at] = mine[j];
       }
-  } else if (tid == 0) {
-    s_n = kFinal + 1;
+  };
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    const int i = tid + j * kThreads;
+    mine[j] = Score{0, ~0ull};
+    if (i < held) mine[j] = score_of(i / of_row, head[j]);
+    most[j] = (uint32_t)(mine[j].s >> 32);
+  }
+  if (every) {
+    listed(held);
+  } else {
+    // the K lists that begin best, and of theirs the K best
+    const uint32_t bound = lists <= kThreads ? kth<1>({most[0]}, K) : kth<kPerThread>(most, K);
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j)
+      if (most[j] && most[j] >= bound) s_list[atomicAdd(&s_lists, 1)] = (uint16_t)(tid + j * kThreads);
+    __syncthreads();
+    const int some = s_lists * K;
+    if (some <= kMaxLists) {
+#pragma unroll
+      for (int j = 0; j < kPerThread; ++j) {
+        const int i = tid + j * kThreads;
+        mine[j] = Score{0, ~0ull};
+        if (i < some) {
+          const int list = s_list[i / K];
+          mine[j] = score_of(list / p.parts, __ldcg(cand + (size_t)list * K + i % K));
+        }
+        most[j] = (uint32_t)(mine[j].s >> 32);
+      }
+      listed(some);
+    } else if (tid == 0) {
+      s_n = kFinal + 1;
+    }
   }
   __syncthreads();
   const int n = s_n;
+  const auto place = [&](const Score& s, int r) {
+    s_parent[r] = (int)(s.at >> 32);
+    s_token[r] = (int)(uint32_t)s.at;
+    s_score[r] = (float)unrank64(s.s);
+  };
   if (n <= kFinal) {
     for (int i = tid; i < n; i += kThreads) {
       const Score s = sc.score[i];
