@@ -19,7 +19,10 @@
  *
  * and what a serving loop does around them:
  *
- *   ssa_rope                rotary positions of queries and new keys
+ *   ssa_rope, ssa_norm_rope rotary positions of queries and new keys, and the
+ *                           norms of their heads in front
+ *   ssa_prompt_attention    attention over whole prompts, on their way in
+ *   ssa_beam_select         the next tokens of beams
  *   ssa_copy_pages, ssa_fork_requests, ssa_compact_pages
  *                           who owns the pages: copies, forks, growth, freed
  *                           requests, a compact page space
@@ -593,8 +596,8 @@ int ssa_rope(int dtype, int head_dim, int rotary_dim, int interleaved, int inver
  * Norms of queries and keys, head by head, and their rotary positions in one
  * pass (models that norm q and k do so right before the rotation):
  *   y = x / sqrt(mean(x^2) + eps) * w,  then ssa_rope's rotation of y
- * over the head_dim elements of every (layer, token, head); in fp32, rounded
- * once.  Arguments as for ssa_rope (no inverse), and
+ * over the head_dim elements of every (layer, token, head); in fp32 (in whose
+ * range the sum of squares must stay), rounded once.  Arguments as for ssa_rope (no inverse), and
  *   q_weight, k_weight  [n_layers][head_dim] fp32, device, weight_step floats
  *             from one layer's to the next's (0: all layers share them); NULL:
  *             ones

@@ -99,16 +99,6 @@ __device__ __forceinline__ double unrank64(uint64_t b) {
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t t) { return (uint64_t)rank32(x) << 32 | (uint32_t)~t; }
 __device__ __forceinline__ float key_x(uint64_t k) { return unrank32((uint32_t)(k >> 32)); }
 
-__device__ __forceinline__ uint32_t redux_add(uint32_t v) {
-  uint32_t r;
-  asm("redux.sync.add.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(v));
-  return r;
-}
-// The sum of 32 numbers below 2^47, in halves of 21 and 26 bits.
-__device__ __forceinline__ uint64_t warp_sum47(uint64_t v) {
-  const uint32_t lo = redux_add((uint32_t)v & 0x3FFFFFFu), hi = redux_add((uint32_t)(v >> 26));
-  return ((uint64_t)hi << 26) + lo;
-}
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);

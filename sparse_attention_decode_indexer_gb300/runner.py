@@ -210,6 +210,7 @@ class DecodeRunner:
         B = self.layout.batch
         if state.groups * state.beams != B:
             raise ValueError(f"state: {state.groups} groups of {state.beams}, the runner has {B} rows")
+        self._wait_preload_or_refuse()          # as the fork would, before anything changes
         ws = self._scratch(f"_beam_ws_{state.beams}", ssa_beam_workspace_size(state.groups, state.beams))
         ints = self._scratch("_beam_out", 3 * 4 * B).view(torch.int32).view(3, B)
         table = self.table

@@ -150,6 +150,18 @@ def test_beam_step_in_a_graph():
         assert torch.equal(run.block_table, eager.block_table) and torch.equal(a.history, b.history)
 
 
+def test_no_beam_step_is_captured_beside_a_preload():
+    lens = [30, 30]
+    run, _ = make("bf16", lens, n=6, host_tier=True)
+    state = ssa.BeamState(1, 2)
+    x = torch.randn((2, 90), device="cuda")
+    run.beam_step(x, state)
+    run.enable_preload(2)
+    with pytest.raises(RuntimeError, match="preload"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            run.beam_step(x, state)
+
+
 def test_refusals():
     run, hn = make()
     with pytest.raises(ValueError, match="positions"):

@@ -177,9 +177,10 @@ def test_many_rows_and_a_long_sequence():
 
 @gpu
 @pytest.mark.parametrize("lq,lk", [([300, 200], [300, 200]), ([4, 3], [900, 2500])])
-def test_not_finite_where_nothing_is_seen(lq, lk):
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_not_finite_where_nothing_is_seen(lq, lk, dtype):
     """Infinities and NaN in keys and values behind a row's last key, and in other sequences'."""
-    q, k, v = inputs(lq, lk, 16, 2, BF16)
+    q, k, v = inputs(lq, lk, 16, 2, dtype)
     k, v, b = k.clone(), v.clone(), lk[0]
     for i, bad in enumerate((math.nan, math.inf, -math.inf)):
         v[b - 1 - i, :, 5 + i] = bad          # the first sequence's last keys
@@ -225,6 +226,30 @@ def test_rows_outside_the_sequences_stay():
     compare((out[10:90], lse[10:90]), reference(q[10:90], k[10:90], v[10:90], [30, 0, 50], [30, 0, 50], True))
     for x in (out, lse):
         assert (x[:10] == 3.0).all() and (x[90:] == 3.0).all()
+
+
+@gpu
+def test_rows_outside_the_sequences_stay_in_a_split():
+    q, k, v = inputs([12], [6000], 8, 2, BF16)
+    out, lse = torch.full_like(q, 3.0), torch.full((12, 8), 3.0, device="cuda")
+    cq, ck = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([2, 7, 7, 10], [100, 3000, 3500, 5900]))
+    ssa.ssa_prompt_attention(q, k, v, cq, out, None, workspace(), cu_k=ck, lse=lse)
+    want = reference(q[2:10], k[100:5900], v[100:5900], [5, 0, 3], [2900, 500, 2400], True)
+    compare((out[2:10], lse[2:10]), want)
+    for x in (out, lse):
+        assert (x[:2] == 3.0).all() and (x[10:] == 3.0).all()
+
+
+@gpu
+def test_no_keys_at_all():
+    check([5, 200], [0, 0], 8, 2)
+
+
+@gpu
+def test_many_sequences():
+    """More sequences than the kernel holds on chip."""
+    lens = [(7 * i) % 23 for i in range(700)]
+    check(lens, lens, 4, 2)
 
 
 @gpu
@@ -316,4 +341,5 @@ def test_c_refusals():
     assert go(Hq=5) == -3 and go(Hq=258, Hk=2) == -3
     assert go(data=None) == -1 and go(data=p + 2) == -1
     assert go(st=516) == -1 and go(st=0) == -1 and go(st=-512) == -1
-    assert go(nq=0) == 0 and go(n=0) == 0          # nothing to do, nothing launched
+    assert go() == -1                               # out over its inputs
+    assert go(nq=0) == 0                            # nothing to do, nothing launched
