@@ -753,16 +753,16 @@ def ssa_prompt_workspace_size() -> int:
     return int(lib().ssa_prompt_workspace_size())
 
 
-def _prompt_tensor(name, x, n, dtype, dev):
-    """The C view of q, k, v or out: [n][heads][D], any strides but the last."""
-    got = x.shape
-    if len(got) != 3 or (n is not None and got[0] != n) or x.dtype is not dtype or x.get_device() != dev:
-        raise ValueError(f"{name}: [tokens][heads][D] of q's type and device, k's tokens as v's and "
-                         f"q's as out's, got {tuple(got)} {x.dtype} on {x.device}")
-    t, h, one = x.stride()
-    if one != 1 and x.numel():
-        raise ValueError(f"{name}: the elements of a head must be contiguous")
-    return _pack_prompt(x.data_ptr(), got[1], t, h)
+def _refuse_prompt(q, k, v, out):
+    """Why ssa_prompt_attention does not take these tensors."""
+    for name, x in (("q", q), ("k", k), ("v", v), ("out", out)):
+        if x.dim() != 3 or x.dtype != q.dtype or x.get_device() != q.get_device():
+            raise ValueError(f"{name}: [tokens][heads][D] of q's type and device, got "
+                             f"{tuple(x.shape)} {x.dtype} on {x.device}")
+        if x.numel() and x.stride(2) != 1:
+            raise ValueError(f"{name}: the elements of a head must be contiguous")
+    raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, out "
+                     f"{tuple(out.shape)}: one head size, k and v alike, q and out alike")
 
 
 def ssa_prompt_attention(q, k, v, cu_q, out, status, ws, cu_k=None, causal: bool = True,
@@ -774,18 +774,23 @@ def ssa_prompt_attention(q, k, v, cu_q, out, status, ws, cu_k=None, causal: bool
     tokens are the last ones of its keys.  sm_scale: default 1 / sqrt(D).  lse:
     fp32 [Tq][Hq], the logarithm of each row's sum.  ws: at least
     ssa_prompt_workspace_size() bytes."""
-    dt, dev, size = q.dtype, q.get_device(), q.shape
+    # (a small call's time is this function's: each property is read once)
+    dt, dev, size, sk = q.dtype, q.get_device(), q.shape, k.shape
     dtype = _PROMPT_DTYPES.get(dt)
     if dtype is None:
         raise ValueError(f"q, k, v: bfloat16 or float16, got {dt}")
-    tq = _prompt_tensor("q", q, None, dt, dev)
-    tk = _prompt_tensor("k", k, None, dt, dev)
-    tv = _prompt_tensor("v", v, k.shape[0], dt, dev)
-    to = _prompt_tensor("out", out, size[0], dt, dev)
+    if len(size) != 3 or len(sk) != 3 or size[2] != sk[2] or v.shape != sk or out.shape != size or \
+            k.dtype is not dt or v.dtype is not dt or out.dtype is not dt or \
+            k.get_device() != dev or v.get_device() != dev or out.get_device() != dev:
+        _refuse_prompt(q, k, v, out)
     n_q, heads, D = size
-    if k.shape[2] != D or v.shape != k.shape or out.shape != size:
-        raise ValueError(f"q {tuple(size)}, k {tuple(k.shape)}, v {tuple(v.shape)}, out "
-                         f"{tuple(out.shape)}: one head size, k and v alike, q and out alike")
+    n_k, heads_k, _ = sk
+    q0, q1, q2 = q.stride()
+    k0, k1, k2 = k.stride()
+    v0, v1, v2 = v.stride()
+    o0, o1, o2 = out.stride()
+    if (q2 != 1 or o2 != 1) and n_q or (k2 != 1 or v2 != 1) and n_k:
+        _refuse_prompt(q, k, v, out)
     n = cu_q.shape[0] if cu_q.dim() == 1 else 0
     pq = _ints("cu_q", cu_q, n, dev)
     pk = pq if cu_k is None or cu_k is cu_q else _ints("cu_k", cu_k, n, dev)
@@ -794,17 +799,17 @@ def ssa_prompt_attention(q, k, v, cu_q, out, status, ws, cu_k=None, causal: bool
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != size[:2] or
                             not lse.is_contiguous() or lse.get_device() != dev):
         raise ValueError(f"lse: contiguous float32 [{n_q}][{heads}] on q's device")
-    if status is not None:
-        _ints("status", status, 1, dev)
     L = lib()
-    if ws.get_device() != dev or ws.nbytes < L.ssa_prompt_workspace_size() or not ws.is_contiguous():
-        raise ValueError("ws: ssa_prompt_workspace_size() contiguous bytes on q's device")
+    if ws.get_device() != dev or ws.nbytes < L.ssa_prompt_workspace_size():
+        raise ValueError("ws: ssa_prompt_workspace_size() bytes on q's device")
     _on_current_device(dev)
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(D)
-    _check(L.ssa_prompt_attention(dtype, D, n - 1, n_q, k.shape[0], tq, tk, tv, to, pq, pk,
-                                      causal, sm_scale, _ptr(lse), _ptr(status), ws.data_ptr(),
-                                      _stream(stream)))
+    _check(L.ssa_prompt_attention(
+        dtype, D, n - 1, n_q, n_k, _pack_prompt(q.data_ptr(), heads, q0, q1),
+        _pack_prompt(k.data_ptr(), heads_k, k0, k1), _pack_prompt(v.data_ptr(), heads_k, v0, v1),
+        _pack_prompt(out.data_ptr(), heads, o0, o1), pq, pk, causal, sm_scale, _ptr(lse),
+        _ptr(status), ws.data_ptr(), _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

@@ -43,6 +43,7 @@
 // 32/4 heads, 368 us (924: a third of a CTA's time is its start and its end);
 // 8 tokens behind 65,528 25 us (2.7 TB/s), 17 tokens 6.7 us.
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <climits>
 #include <type_traits>
@@ -681,8 +682,15 @@ bool map_q(CUtensorMap* tm, const ssa_prompt_tensor& x, int n, int Hkv, int tpt,
 template <typename T>
 cudaError_t launch_prompt(const Params& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                           cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-  if (e != cudaSuccess) return e;
+  // once a device: the attribute stays, and asking for it is a tenth of a small call
+  static std::atomic<bool> asked[kMaxDevices];
+  std::atomic<bool>& done = asked[current_device_ordinal()];
+  cudaError_t e;
+  if (!done.load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    done.store(true, std::memory_order_relaxed);
+  }
   const long long n = (long long)p.n_pairs * p.Hkv * p.n_split;
   if (n > INT_MAX) return cudaErrorInvalidValue;
   e = launch_pdl(prompt_kernel<T>, dim3((unsigned)n), dim3(kThreads), kSmem, s, p, q, k, v);

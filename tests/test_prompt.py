@@ -303,16 +303,17 @@ def _call_cpu(**kw):
 @pytest.mark.parametrize("kw,match", [
     (dict(q=torch.zeros((6, 4, D))), "bfloat16 or float16"),
     (dict(k=torch.zeros((6, 2, D), dtype=F16)), "k: "),
-    (dict(v=torch.zeros((5, 2, D), dtype=BF16)), "v: "),
+    (dict(v=torch.zeros((6, 2, D))), "v: "),
+    (dict(v=torch.zeros((5, 2, D), dtype=BF16)), "alike"),
     (dict(v=torch.zeros((6, 1, D), dtype=BF16)), "alike"),
     (dict(out=torch.zeros((6, 2, D), dtype=BF16)), "alike"),
-    (dict(out=torch.zeros((5, 4, D), dtype=BF16)), "out: "),
+    (dict(out=torch.zeros((5, 4, D), dtype=BF16)), "alike"),
+    (dict(out=torch.zeros((6, 4, D), dtype=F16)), "out: "),
     (dict(q=torch.zeros((6, 4, 2 * D), dtype=BF16)[..., ::2]), "contiguous"),
     (dict(cu_q=torch.tensor([0, 6])), "cu_q"),
     (dict(cu_q=torch.zeros((0,), dtype=torch.int32)), "cu_q"),
     (dict(cu_k=torch.tensor([0, 3, 6], dtype=torch.int32)), "cu_k"),
     (dict(lse=torch.zeros((6, 2))), "lse"),
-    (dict(status=torch.zeros((1,), dtype=torch.int64)), "status"),
     (dict(ws=torch.zeros((16,), dtype=torch.uint8)), "ws"),
     (dict(), "current CUDA device"),
 ])
