@@ -46,6 +46,7 @@
 #include <atomic>
 #include <cfloat>
 #include <climits>
+#include <cmath>
 #include <type_traits>
 
 #include "internal.h"
@@ -707,6 +708,26 @@ cudaError_t launch_prompt(const Params& p, const CUtensorMap& q, const CUtensorM
 // Partial rows of one launch: a split launch has no more CTAs than SMs.
 size_t part_rows(int sms) { return (size_t)sms * 2 * kRows; }
 
+// Parts that the keys of a CTA's rows are split into, where CTAs would not fill the
+// machine.  How many keys a CTA walks over stands in the tables on the device; the
+// host goes by the average sequence, and by the keys of all the sequences that
+// share a CTA's tokens.  A CTA takes about 1 us for 80 keys; a part more costs 520
+// bytes of every row written and read, 0.26 ns a row, and the second kernel 5 us.
+// (1,000 tokens, 16/2 heads: 18.8 us whole, 24.1 in two; 2,000 tokens, 8/1: 31.3 and
+// 30.8; 64 tokens behind 8,000, 16/2: 109 whole, 18.0 in 15, 18.9 in 19; one token each
+// of 8 sequences of 4,000: 370 whole, 19.6 in 62; one behind 30,000: 13.9 in 58,
+// 16.9 in 152, so four blocks at least to a part.)
+int splits(const Params& p, int n_seqs, int sms) {
+  const long long units = (long long)p.n_pairs * p.Hkv;
+  const double rows = (double)p.Tq * p.Hq;
+  const double walk = std::min((double)p.Tk, std::max((double)p.Tk / n_seqs, (double)p.Tk / p.Tq * 2 * p.tpt));
+  const double whole = walk / 80, row_cost = rows * 2.6e-4;                      // us
+  const double best = std::min({(double)(sms / units), walk / (4 * kBlk), std::sqrt(whole / row_cost)});
+  const int n = best > 2 ? (int)best : best >= 1.5 ? 2 : 1;
+  if (n < 2 || n * units > sms) return 1;
+  return whole * (1.0 - 1.0 / n) > 5 + row_cost * n ? n : 1;
+}
+
 int check_tensor(const ssa_prompt_tensor* x, int n) {
   if (!x || x->heads < 1) return SSA_ERR_INVALID_ARG;
   if (n > 0 && (!x->data || ((uintptr_t)x->data & 15))) return SSA_ERR_INVALID_ARG;
@@ -759,10 +780,7 @@ int ssa_prompt_attention(int dtype, int head_dim, int n_seqs, int n_q, int n_kv,
   p.lse = lse_opt;
   p.status = status;
   const int sms = current_device_info().sms;
-  const long long units = (long long)p.n_pairs * p.Hkv;
-  // at least four blocks of keys to a split
-  const long long most = std::max(1, (n_kv + 4 * kBlk - 1) / (4 * kBlk));
-  p.n_split = (int)std::max(1ll, std::min(sms / units, most));
+  p.n_split = splits(p, n_seqs, sms);
   p.part_o = static_cast<float*>(ws);
   p.part_ml = p.part_o + part_rows(sms) * kD;
 
