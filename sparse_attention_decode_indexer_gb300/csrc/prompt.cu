@@ -83,13 +83,13 @@ static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 struct Params {
   const int32_t *cu_q, *cu_k;
   int n_seqs, Tq, Tk, Hq, Hkv, G, tpt;    // tpt: tokens of a tile
-  int n_pairs, n_split, causal;
+  int tiles, n_ctas, n_split, causal;     // tiles of a CTA, CTAs of a head and part
   float scale_log2;
   int64_t v_tok, v_head, o_tok, o_head;   // strides in elements
   const void* v;
   void* out;
   float* lse;
-  float *part_o, *part_ml;                // [pair][head][split][2 * kRows][kD], [..][2]
+  float *part_o, *part_ml;                // [CTA][head][split][2 * kRows][kD], [..][2]
   int32_t* status;
 };
 
@@ -173,8 +173,8 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
   constexpr bool BF = !std::is_same_v<T, __half>;
 
   const int id = blockIdx.x, split = id % p.n_split, rest = id / p.n_split;
-  const int head = rest % p.Hkv, pair = p.n_pairs - 1 - rest / p.Hkv;   // the longest rows first
-  const int tok0 = pair * 2 * p.tpt;
+  const int head = rest % p.Hkv, place = p.n_ctas - 1 - rest / p.Hkv;   // the longest rows first
+  const int tok0 = place * p.tiles * p.tpt;
 
   if (threadIdx.x < kStages) {
     mbar_init(&sh.full[threadIdx.x], 1);
@@ -213,7 +213,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
   int lo = 0, hi = 0;
   bool in_seq = false;
   if (threadIdx.x < 256) {
-    if (r < p.tpt * p.G && tok < p.Tq)
+    if (tile < p.tiles && r < p.tpt * p.G && tok < p.Tq)
       in_seq = on_chip ? row_keys(p, sh.cu_q, sh.cu_k, tok, lo, hi) : row_keys(p, p.cu_q, p.cu_k, tok, lo, hi);
     const bool any = lo < hi;
     const int least = __reduce_min_sync(~0u, any ? lo : INT_MAX), most = __reduce_max_sync(~0u, any ? hi : 0);
@@ -222,7 +222,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
   } else if (warp == kTma) {
     // q needs no range
     for (int t = 0; lane == 0 && t < 2; ++t)
-      if (tok0 + t * p.tpt < p.Tq) {
+      if (t < p.tiles && tok0 + t * p.tpt < p.Tq) {
         mbar_arrive_expect_tx(&sh.q_full[t], 2u * 128u * p.G * p.tpt);
         for (int h = 0; h < 2; ++h)
           tma_load_4d(s_q + t * kTile + h * kHalf, &tm_q, &sh.q_full[t], h * 64, 0, head, tok0 + t * p.tpt);
@@ -286,7 +286,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
       }
     // copies in flight land before the CTA goes: q's of rows without keys, and all if it gives up
     for (int t = 0; t < 2; ++t)
-      if (tok0 + t * p.tpt < p.Tq) mbar_wait(&sh.q_full[t], 0, nullptr);
+      if (t < p.tiles && tok0 + t * p.tpt < p.Tq) mbar_wait(&sh.q_full[t], 0, nullptr);
     if (*abort) {
       for (int j = max(0, it - kStages); j < it; ++j)
         mbar_wait(&sh.full[j % kStages], (j / kStages) & 1, nullptr);
@@ -483,15 +483,15 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
     // ---- epilogue ----
     if (ok && n > 0) ok = all(o_done(n));
     // (without a product nobody has waited for the queries, whose place is used below)
-    if (ok && n == 0 && tok0 + tile * p.tpt < p.Tq) ok = all(mbar_wait(&sh.q_full[tile], 0, abort));
+    if (ok && n == 0 && tile < p.tiles && tok0 + tile * p.tpt < p.Tq) ok = all(mbar_wait(&sh.q_full[tile], 0, abort));
     if (ok) {
       tc5_fence_after();
       const bool seen = live && n > 0;
       if (!live) { m = -INFINITY; l = 0.0f; }          // (a row without keys ran along)
-      const size_t row = (((size_t)pair * p.Hkv + head) * p.n_split + split) * (2 * kRows) + threadIdx.x;
+      const size_t row = (((size_t)place * p.Hkv + head) * p.n_split + split) * (2 * kRows) + threadIdx.x;
       const int hq = head * p.G + r % p.G;
       if (p.n_split > 1) {
-        if (r < p.tpt * p.G && tok < p.Tq)
+        if (tile < p.tiles && r < p.tpt * p.G && tok < p.Tq)
           *reinterpret_cast<float2*>(p.part_ml + 2 * row) = make_float2(m, in_seq ? l : -1.0f);
       } else if (in_seq && p.lse) {
         p.lse[(size_t)tok * p.Hq + hq] = l != 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
@@ -501,7 +501,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
       // on 32 rows took 6,000 clocks.  256 bytes of a row at a time (all of it, or
       // half of the fp32 row of a split), 16-byte pieces turned by the row.
       uint8_t* const mine = s_q + tile * kTile + (warp & 3) * 32 * 256;
-      const int64_t place = p.n_split > 1 ? (int64_t)row * kD : tok * p.o_tok + hq * p.o_head;
+      const int64_t at_row = p.n_split > 1 ? (int64_t)row * kD : tok * p.o_tok + hq * p.o_head;
       const uint32_t rows = __ballot_sync(~0u, in_seq);
       const float f = p.n_split > 1 ? 1.0f : seen && l != 0.0f ? 1.0f / l : 0.0f;
       const auto write = [&](char* dst, int size) {
@@ -510,7 +510,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
 #pragma unroll 8
         for (int e = 0; e < 16; ++e) {
           const int rr = 2 * e + (lane >> 4);
-          const int64_t at = __shfl_sync(~0u, place, rr);
+          const int64_t at = __shfl_sync(~0u, at_row, rr);
           if (rows >> rr & 1)
             *reinterpret_cast<uint4*>(dst + at * size + 16 * piece) =
                 *reinterpret_cast<const uint4*>(mine + rr * 256 + ((piece ^ (rr & 15)) << 4));
@@ -599,9 +599,9 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const Params p, int wa
   float m = -INFINITY, l = 0.0f;
   float4 o = make_float4(0, 0, 0, 0);
   if (mine) {
-    const int head = hq / p.G, pair = tok / (2 * p.tpt), in = tok % (2 * p.tpt);
+    const int head = hq / p.G, of_cta = p.tiles * p.tpt, in = tok % of_cta;
     const int r = in / p.tpt * kRows + in % p.tpt * p.G + hq % p.G;
-    const size_t row0 = ((size_t)pair * p.Hkv + head) * p.n_split * (2 * kRows) + r;
+    const size_t row0 = ((size_t)(tok / of_cta) * p.Hkv + head) * p.n_split * (2 * kRows) + r;
     for (int s0 = w; s0 < p.n_split; s0 += 8 * warps) {
       float2 ml[8];
       float4 y[8];
@@ -692,7 +692,7 @@ cudaError_t launch_prompt(const Params& p, const CUtensorMap& q, const CUtensorM
     if (e != cudaSuccess) return e;
     done.store(true, std::memory_order_relaxed);
   }
-  const long long n = (long long)p.n_pairs * p.Hkv * p.n_split;
+  const long long n = (long long)p.n_ctas * p.Hkv * p.n_split;
   if (n > INT_MAX) return cudaErrorInvalidValue;
   e = launch_pdl(prompt_kernel<T>, dim3((unsigned)n), dim3(kThreads), kSmem, s, p, q, k, v);
   count_launch();
@@ -711,17 +711,17 @@ size_t part_rows(int sms) { return (size_t)sms * 2 * kRows; }
 // Parts that the keys of a CTA's rows are split into, where CTAs would not fill the
 // machine.  How many keys a CTA walks over stands in the tables on the device; the
 // host goes by the average sequence, and by the keys of all the sequences that
-// share a CTA's tokens.  A CTA takes about 1 us for 80 keys; a part more costs 520
+// share a CTA's tokens.  A CTA takes about 1 us for 80 keys (one tile: 140); a part more costs 520
 // bytes of every row written and read, 0.26 ns a row, and the second kernel 5 us.
 // (1,000 tokens, 16/2 heads: 18.8 us whole, 24.1 in two; 2,000 tokens, 8/1: 31.3 and
 // 30.8; 64 tokens behind 8,000, 16/2: 109 whole, 18.0 in 15, 18.9 in 19; one token each
 // of 8 sequences of 4,000: 370 whole, 19.6 in 62; one behind 30,000: 13.9 in 58,
 // 16.9 in 152, so four blocks at least to a part.)
 int splits(const Params& p, int n_seqs, int sms) {
-  const long long units = (long long)p.n_pairs * p.Hkv;
+  const long long units = (long long)p.n_ctas * p.Hkv;
   const double rows = (double)p.Tq * p.Hq;
-  const double walk = std::min((double)p.Tk, std::max((double)p.Tk / n_seqs, (double)p.Tk / p.Tq * 2 * p.tpt));
-  const double whole = walk / 80, row_cost = rows * 2.6e-4;                      // us
+  const double walk = std::min((double)p.Tk, std::max((double)p.Tk / n_seqs, (double)p.Tk / p.Tq * p.tiles * p.tpt));
+  const double whole = walk / (p.tiles == 1 ? 140 : 80), row_cost = rows * 2.6e-4;                      // us
   const double best = std::min({(double)(sms / units), walk / (4 * kBlk), std::sqrt(whole / row_cost)});
   const int n = best > 2 ? (int)best : best >= 1.5 ? 2 : 1;
   if (n < 2 || n * units > sms) return 1;
@@ -771,7 +771,12 @@ int ssa_prompt_attention(int dtype, int head_dim, int n_seqs, int n_q, int n_kv,
   p.n_seqs = n_seqs; p.Tq = n_q; p.Tk = n_kv;
   p.Hq = q->heads; p.Hkv = k->heads; p.G = p.Hq / p.Hkv;
   p.tpt = kRows / p.G;
-  p.n_pairs = (n_q + 2 * p.tpt - 1) / (2 * p.tpt);
+  // two tiles a CTA share its K and V; where one tile each fits the machine at once
+  // the CTAs are twice as many and each is done sooner (2,000 tokens x 8/1 heads:
+  // two tiles 31.5 us, one 25.5)
+  const int sms = current_device_info().sms, n_tiles = (n_q + p.tpt - 1) / p.tpt;
+  p.tiles = (long long)n_tiles * p.Hkv <= sms ? 1 : 2;
+  p.n_ctas = (n_tiles + p.tiles - 1) / p.tiles;
   p.causal = causal ? 1 : 0;
   // not zero: masked scores are -inf, and stay so when scaled
   p.scale_log2 = std::max(sm_scale * 1.4426950408889634f, FLT_MIN);
@@ -779,7 +784,6 @@ int ssa_prompt_attention(int dtype, int head_dim, int n_seqs, int n_q, int n_kv,
   p.out = out->data; p.o_tok = out->stride[0]; p.o_head = out->stride[1];
   p.lse = lse_opt;
   p.status = status;
-  const int sms = current_device_info().sms;
   p.n_split = splits(p, n_seqs, sms);
   p.part_o = static_cast<float*>(ws);
   p.part_ml = p.part_o + part_rows(sms) * kD;
