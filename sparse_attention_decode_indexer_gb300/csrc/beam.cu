@@ -18,17 +18,24 @@
 // is the K-th best of the chunks before.  The values that reach it, few more
 // than K, go to a list, in which each finds its rank by counting; values are
 // compared together with their index, so no two are equal and the order of the
-// list does not matter.  Where many values
-// equal the bound (a mask of one finite value) the list would overflow: then the
-// bound is taken over (value, index) of each thread, which at most K threads'
-// values reach.
+// list does not matter.  Where many values equal the bound (a mask of one finite
+// value) the list would overflow: then the bound is taken over (value, index) of
+// each thread, which at most K threads' values reach.
 //
 // Sums are 64-bit integers in units of 2^-40 beside a largest term above 1/2 (so at
-// most 2^23 terms), which do not depend on any order.  Double arithmetic (two operations a clock
-// and SM here) makes the logarithms and adds the scores, so that candidates of
-// different beams are ordered by what they are and not by a rounding to fp32:
-// an exponential is off by about 2^-22, an average over many by less.  2^(x L),
-// L = log2e rounded to fp32, in place of e^x is off by 2e-8 of the row's entropy.
+// most 2^23 terms), which do not depend on any order.  Double arithmetic (two
+// operations a clock and SM here) makes the logarithms and adds the scores, so that
+// candidates of different beams are ordered by what they are and not by a rounding
+// to fp32: an exponential is off by about 2^-22, an average over many by less.
+// 2^(x L), L = log2e rounded to fp32, in place of e^x is off by 2e-8 of the row's
+// entropy.
+//
+// Measured: 32 x 8 beams of 160,000 bf16 logits, histories of 4,096: 38 us (82 MB, 12
+// at the copy rate; 300 instructions a warp and chunk at 0.42 of the issue rate);
+// 64 x 1 of 131,072: 13 us; 1 x 4 of 32,000: 10.7 us, of which the last CTA's choice
+// is 5 (64 us for the first of these before loads went out together and double
+// comparisons became integers, 231 at first).  Chunks of 64 bytes a thread: two more
+// in flight through shared memory measured the same (39).
 // Beyond 2^20 (masks of some large number) c, an fp32 product, would no longer be
 // the logit it stands for: there sums are taken against the logit itself.
 #include <algorithm>

@@ -38,10 +38,10 @@
 //     then adds it for the rows that do see it.
 //   * Few rows and many keys: the key blocks of a tile are split over several
 //     CTAs; their unnormalised outputs are joined by a second kernel.
-// Measured: 24,576 tokens x 16/2 heads causal 1.55 to 1.7 ms (1,450 to 1,600
-// TFLOP/s, by how far the power limit lets the clock); 24 prompts of 1 to 4K tokens,
-// 32/4 heads, 368 us (924: a third of a CTA's time is its start and its end);
-// 8 tokens behind 65,528 25 us (2.7 TB/s), 17 tokens 6.7 us.
+// Measured: 24,576 tokens x 16/2 heads causal 1.63 to 1.73 ms (1,430 to 1,520
+// TFLOP/s, by how far the power limit lets the clock); 24 prompts of 69 to 3,712
+// tokens, 32/4 heads, 368 us (924: a third of a CTA's time is its start and its end);
+// 8 tokens behind 65,528 25 us (2.7 TB/s), 17 tokens 6.3 us.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
