@@ -166,6 +166,14 @@ def test_full_and_bad_histories_are_flagged():
 
 
 @gpu
+def test_rows_beyond_4_gib():
+    x, st = make(1, 3, 9000, BF16, seed=6)
+    far = torch.empty((3, 1_200_000_000), dtype=BF16, device="cuda")[:, :9000]
+    far.copy_(x)
+    check(far, st)
+
+
+@gpu
 def test_ties_go_to_the_lowest_row_and_token():
     G, K, V = 3, 4, 20000
     x = torch.zeros((G * K, V), device="cuda")

@@ -106,6 +106,20 @@ def test_views_and_in_place(dtype, shift, in_place, inter):
 
 
 @gpu
+@pytest.mark.parametrize("shift", [0, 1])
+def test_tokens_beyond_4_gib(shift):
+    T, far = 5, 600_000_000
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q = torch.randn((1, T, 4, 128), generator=g, device="cuda").to(BF16)
+    x = torch.empty((T * far + 8,), dtype=BF16, device="cuda")[shift:].as_strided((T, 4, 128), (far, 128, 1))
+    x.copy_(q[0])
+    plan, norm, pos = ssa.RopePlan(128), ssa.HeadNorm(eps=1e-6), torch.arange(T, device="cuda")
+    theta = 10000.0 ** (-2.0 * torch.arange(64, dtype=torch.float64, device="cuda") / 128)
+    ssa.ssa_norm_rope(plan, norm, pos, x)
+    check(x[None], reference(q, None, 1e-6, theta, pos, 128, False))
+
+
+@gpu
 @pytest.mark.parametrize("scale,eps", [(1e-4, 1e-5), (300.0, 1e-6), (1.0, 0.0), (1e-3, 1e3)])
 def test_magnitudes(scale, eps):
     run(1, 40, 4, 2, 128, 128, False, BF16, scale=scale, eps=eps)

@@ -241,6 +241,20 @@ def test_rows_outside_the_sequences_stay_in_a_split():
 
 
 @gpu
+def test_keys_by_head_and_tokens_far_apart():
+    """K and V laid out head by head; query and result rows more than 4 GiB from the first."""
+    n, far = 50, 100_000_000
+    q, k, v = inputs([n], [n], 8, 2, BF16)
+    k, v = (x.transpose(0, 1).contiguous().transpose(0, 1) for x in (k, v))
+    store = [torch.empty((n * far,), dtype=BF16, device="cuda") for _ in range(2)]
+    qf, out = (x.as_strided((n, 8, D), (far, D, 1)) for x in store)
+    qf.copy_(q)
+    lse = torch.empty((n, 8), device="cuda")
+    ssa.ssa_prompt_attention(qf, k, v, offsets([n]), out, None, workspace(), lse=lse)
+    compare((out, lse), reference(q, k, v, [n], [n], True))
+
+
+@gpu
 def test_no_keys_at_all():
     check([5, 200], [0, 0], 8, 2)
 
