@@ -178,7 +178,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
 
   if (threadIdx.x < kStages) {
     mbar_init(&sh.full[threadIdx.x], 1);
-    mbar_init(&sh.empty[threadIdx.x], 2);
+    mbar_init(&sh.empty[threadIdx.x], 2 + kLooks);   // two MMA warps, and those that look through V
     mbar_init(&sh.clean[threadIdx.x], kLooks);
     fence_barrier_init();
   } else if (threadIdx.x >= 8 && threadIdx.x < 12) {
@@ -371,12 +371,24 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
     mbar_wait(&sh.drain, 0, nullptr);
   } else if (warp >= kLook) {
     // ---- V of the blocks that some row does not see all of: what is not finite becomes zero ----
-    int vs = 1;
-    uint32_t vp = 0;
+    // They wait for K too, and a stage is free only when they have seen what it held:
+    // copies land in any order, and the phase before the one waited for reads as a
+    // phase that is done, so that a use that a waiter leaves out lets it pass too early.
+    int st = 0;
+    uint32_t ph = 0;
+    const auto seen = [&](uint64_t* clean) {
+      if (lane == 0) {
+        if (clean) mbar_arrive(clean);
+        mbar_arrive(&sh.empty[st]);
+      }
+      if (++st == kStages) { st = 0; ph ^= 1; }
+    };
     for (int i = b0; i < b1; ++i) {
-      if (!__all_sync(~0u, mbar_wait(&sh.full[vs], vp, abort))) { give_up(SSA_ST_TIMEOUT); break; }
+      if (!__all_sync(~0u, mbar_wait(&sh.full[st], ph, abort))) { give_up(SSA_ST_TIMEOUT); break; }
+      seen(nullptr);
+      if (!__all_sync(~0u, mbar_wait(&sh.full[st], ph, abort))) { give_up(SSA_ST_TIMEOUT); break; }
       if (x0 + i * kBlk < lo_max || x0 + (i + 1) * kBlk > hi_min) {
-        uint4* v = reinterpret_cast<uint4*>(s_kv + vs * kTile);
+        uint4* v = reinterpret_cast<uint4*>(s_kv + st * kTile);
         bool found = false;
 #pragma unroll 8
         for (int j = threadIdx.x - kLook * 32; j < kTile / 16; j += kLooks * 32) {
@@ -392,9 +404,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
         }
         __syncwarp();
       }
-      if (lane == 0) mbar_arrive(&sh.clean[vs]);
-      vs += 2;
-      if (vs >= kStages) { vs -= kStages; vp ^= 1; }
+      seen(&sh.clean[st]);
     }
   } else if (warp < 8) {
     // ---- softmax: a thread per row ----

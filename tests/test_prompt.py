@@ -314,6 +314,27 @@ def _call_cpu(**kw):
     ssa.ssa_prompt_attention(**z)
 
 
+@gpu
+@pytest.mark.parametrize("n,ctx", [(8, 16376), (8, 65528), (700, 3000)])
+def test_keys_and_values_from_cold_memory(n, ctx):
+    """Copies that come from memory and not from the cache land out of order: a V before the K that had
+    its stage.  Every call finds the cache full of something else, and gives the bits of the first."""
+    gen = torch.Generator(device="cuda").manual_seed(n + ctx)
+    q, k, v = (torch.randn((t, h, D), generator=gen, device="cuda").to(BF16)
+               for t, h in ((n, 16), (n + ctx, 2), (n + ctx, 2)))
+    other = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu_q, cu_k = offsets([n]), offsets([n + ctx])
+    outs, ws = [torch.zeros_like(q) for _ in range(30)], workspace()
+    for i, out in enumerate(outs):
+        other.fill_(i)
+        ssa.ssa_prompt_attention(q, k, v, cu_q, out, status, ws, cu_k=cu_k)
+    assert status.item() == 0
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    ref, _, tol, _ = reference(q, k, v, [n], [n + ctx], True)
+    assert ((outs[0].double() - ref).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("kw,match", [
     (dict(q=torch.zeros((6, 4, D))), "bfloat16 or float16"),
     (dict(k=torch.zeros((6, 2, D), dtype=F16)), "k: "),
