@@ -634,18 +634,25 @@ __global__ void __launch_bounds__(kThreads, kCtas) beam_kernel(const __grid_cons
       if (c > -INFINITY) sum = far < INFINITY ? x.sum_from(far) : x.sum(c);
       // above: a NaN, or logits far above the reference of the chunks before
       if (!(sum <= 64.0f) || (c == -INFINITY && m > -INFINITY)) flags |= 2;
-      const bool some = __syncthreads_or(flags != 0);
-      if (some && __syncthreads_or((flags & 2) != 0)) {
-        const float q = warp_max(m);
-        if (lane == 0) s_max[warp] = q;
-        __syncthreads();
-        refer(block_top());
-        sum = 0.0f;
-        if (c > -INFINITY) sum = far < INFINITY ? x.sum_from(far) : x.sum_clean(c);
+      // The size of the list is read between two barriers: a warp that is done with a
+      // chunk which lists nothing (a NaN alone brought it here) may add to the next
+      // one's while another still decides, and they would part ways.
+      int found = 0;
+      if (__syncthreads_or(flags != 0)) {
+        found = s_n;
+        if (__syncthreads_or((flags & 2) != 0)) {
+          const float q = warp_max(m);
+          if (lane == 0) s_max[warp] = q;
+          __syncthreads();
+          refer(block_top());
+          sum = 0.0f;
+          if (c > -INFINITY) sum = far < INFINITY ? x.sum_from(far) : x.sum_clean(c);
+          __syncthreads();                // s_max is the next chunk's from here on
+        }
       }
       z += (uint64_t)(sum * kUnit);
-      if (some && s_n > 0) {
-        int n = kept + s_n;
+      if (found > 0) {
+        int n = kept + found;
         if (n > kList) {
           // many equal ones: bounded over (value, token) instead
           uint64_t best = 0;
