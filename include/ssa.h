@@ -706,8 +706,9 @@ int ssa_prompt_attention(int dtype, int head_dim, int n_seqs, int n_q, int n_kv,
  *   seq_lens_opt, new_lens_opt  [groups * beams] int32, both or none:
  *             new_lens[row] = seq_lens[parent] + 1, 0 for parent -1, as
  *             ssa_fork_requests takes them (may be the same array)
- *   ws        ssa_beam_workspace_size(groups, beams) bytes, 256-byte aligned,
- *             zeroed once, not used by another call at the same time
+ *   ws        ssa_beam_workspace_size(groups, beams) bytes or more, 256-byte
+ *             aligned, zeroed once, not used by another call at the same time;
+ *             calls of any sizes that it is large enough for may take turns
  */
 typedef struct ssa_beams {
   float *scores;

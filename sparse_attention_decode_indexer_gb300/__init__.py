@@ -846,7 +846,8 @@ class BeamState:
 
 
 def ssa_beam_workspace_size(groups: int, beams: int) -> int:
-    """Bytes of scratch of ssa_beam_select (zeroed once), for any vocabulary."""
+    """Bytes of scratch of ssa_beam_select (zeroed once), for any vocabulary and
+    for fewer groups or beams too."""
     return int(lib().ssa_beam_workspace_size(groups, beams))
 
 

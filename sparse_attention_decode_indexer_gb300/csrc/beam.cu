@@ -51,6 +51,7 @@ constexpr int kThreads = 256;
 constexpr int kCtas = 4;                  // per SM
 constexpr int kBytes = 64;                // of a chunk of logits, a thread
 constexpr int kMaxBeams = 32;
+constexpr int kMaxGroups = 65535;
 constexpr int kMaxLists = 1024;           // (row, part) lists of a group
 constexpr int kList = kMaxBeams * 33;     // values in a CTA's list: K threads' 32, and K kept
 constexpr int kFinal = 512;               // candidates in a group's list
@@ -744,6 +745,10 @@ __global__ void __launch_bounds__(kMoveThreads) beam_move_kernel(const __grid_co
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// A workspace begins with a ticket for every group that a call may have: what a call
+// of any size leaves behind them is never another's ticket.
+constexpr size_t kTickets = ((size_t)kMaxGroups * sizeof(int32_t) + 255) & ~(size_t)255;
+
 template <typename T>
 cudaError_t launch(Params p, int groups, cudaStream_t s) {
   constexpr int N = 16 / sizeof(T);
@@ -771,7 +776,7 @@ size_t ssa_beam_workspace_size(int groups, int beams) {
   using namespace ssa;
   if (groups < 1 || beams < 1 || beams > kMaxBeams) return 0;
   const size_t lists = std::max((size_t)groups * beams, (size_t)kMaxLists);
-  return 2 * align256((size_t)groups * 4) + align256(lists * sizeof(Part)) + align256(lists * beams * sizeof(Cand));
+  return kTickets + align256((size_t)groups * 4) + align256(lists * sizeof(Part)) + align256(lists * beams * sizeof(Cand));
 }
 
 int ssa_beam_select(int dtype, int groups, int beams, int vocab, const void* logits, int64_t row_stride,
@@ -781,7 +786,7 @@ int ssa_beam_select(int dtype, int groups, int beams, int vocab, const void* log
   using namespace ssa;
   if (dtype < SSA_BF16 || dtype > SSA_F32) return SSA_ERR_UNSUPPORTED;
   if (groups < 1 || beams < 1 || vocab < 1 || max_len < 0 || eos < -1 || eos >= vocab) return SSA_ERR_INVALID_ARG;
-  if (beams > kMaxBeams || groups > 65535 || vocab > 1 << 23) return SSA_ERR_UNSUPPORTED;
+  if (beams > kMaxBeams || groups > kMaxGroups || vocab > 1 << 23) return SSA_ERR_UNSUPPORTED;
   if (!logits || !in || !out || !in->scores || !out->scores || !parent || !token || !ws) return SSA_ERR_INVALID_ARG;
   if ((uintptr_t)logits & (dtype == SSA_F32 ? 3 : 1)) return SSA_ERR_INVALID_ARG;
   if (row_stride < vocab && (long long)groups * beams > 1) return SSA_ERR_INVALID_ARG;
@@ -803,7 +808,7 @@ int ssa_beam_select(int dtype, int groups, int beams, int vocab, const void* log
   p.move_here = (long long)beams * max_len <= (long long)(sizeof(Scratch::move) / 4);
   char* w = static_cast<char*>(ws);
   p.ticket = reinterpret_cast<int32_t*>(w);
-  w += align256((size_t)groups * 4);
+  w += kTickets;
   p.old_len = reinterpret_cast<int32_t*>(w);
   w += align256((size_t)groups * 4);
   p.part = reinterpret_cast<Part*>(w);
