@@ -260,6 +260,22 @@ template <typename T> struct Logits {
   }
 };
 
+// A reference of a sum in octaves: whole ones, or a far logit's.
+__device__ __forceinline__ double octaves(float c, float far) {
+  return far < INFINITY ? (double)far * (double)kLog2e : (double)c;
+}
+// A sum beside the reference (c, far) as one beside (c1, far1), which is not below it
+// but for the rounding of a far c.  Whole octaves are a shift; between far references a
+// part of an octave is left.
+__device__ __forceinline__ uint64_t beside(uint64_t z, float c, float far, float c1, float far1) {
+  if (!(far < INFINITY) && !(far1 < INFINITY)) return z >> (int)fminf(c1 - c, 63.0f);
+  const double d = octaves(c1, far1) - octaves(c, far);
+  if (!(d < 63.0)) return 0;
+  const int n = max((int)d, 0);
+  const uint64_t f = (uint64_t)(exp2f((float)((double)n - d)) * 0x1p31f);     // at most a little above 2^31
+  return __umul64hi(z >> n, f << 32) << 1;
+}
+
 struct Score {                            // of a candidate, and its place in the group
   uint64_t s;                             // rank64 of the score; 0: none
   uint64_t at;                            // row << 32 | token
@@ -376,19 +392,18 @@ __device__ __noinline__ void choose(const Params& p, int g, Scratch& sc) {
       const uint4 u = __ldcg(part + i);
       const uint64_t s = (uint64_t)u.y << 32 | u.x;
       const float pc = __uint_as_float(u.z);
-      if (pc > c) {
-        z = (c > -INFINITY ? z >> (int)fminf(pc - c, 63.0f) : 0) + s;
+      const float pf = __uint_as_float(u.w);
+      if (pc > c || (pc == c && pf > far)) {
+        z = (c > -INFINITY ? beside(z, c, far, pc, pf) : 0) + s;
         c = pc;
-        far = __uint_as_float(u.w);
+        far = pf;
       } else if (pc > -INFINITY) {
-        z += s >> (int)fminf(c - pc, 63.0f);
-        if (pc == c) far = fmaxf(far, __uint_as_float(u.w));
+        z += beside(s, pc, pf, c, far);
       }
     }
-    const float top = warp_max(c);
-    far = warp_max(c == top ? far : -INFINITY);
-    z = warp_sum(c > -INFINITY ? z >> (int)fminf(top - c, 63.0f) : 0);
-    if (lane == 0) { s_z[r] = z; s_c[r] = top; s_far[r] = far; }
+    const float top = warp_max(c), top_far = warp_max(c == top ? far : -INFINITY);
+    z = warp_sum(c > -INFINITY ? beside(z, c, far, top, top_far) : 0);
+    if (lane == 0) { s_z[r] = z; s_c[r] = top; s_far[r] = top_far; }
   }
   if (tid < K) {
     s_add[tid] = add;
@@ -576,9 +591,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) beam_kernel(const __grid_cons
         const bool is_far = fabsf(top) >= kFar;
         const float tc = is_far ? fmaxf(top, -kGreatest) * kLog2e : ceilf(top * kLog2e);
         if (tc > c || (tc == c && is_far && top > far)) {
-          if (c > -INFINITY) z >>= (int)fminf(is_far && far < INFINITY ? (top - far) * kLog2e : tc - c, 63.0f);
+          const float tf = is_far ? top : INFINITY;
+          if (c > -INFINITY) z = beside(z, c, far, tc, tf);
           c = tc;
-          far = is_far ? top : INFINITY;
+          far = tf;
         }
       }
     };
