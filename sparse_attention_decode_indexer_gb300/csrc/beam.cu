@@ -22,8 +22,9 @@
 // value) the list would overflow: then the bound is taken over (value, index) of
 // each thread, which at most K threads' values reach.
 //
-// Sums are 64-bit integers in units of 2^-40 beside a largest term above 1/2 (so at
-// most 2^23 terms), which do not depend on any order.  Double arithmetic (two
+// Sums are 64-bit integers in units of 2^-40, which do not depend on any order.  The
+// reference moves when a thread's sum of a chunk passes its number of logits, so the
+// terms average at most one and 2^23 of them come to 2^63.  Double arithmetic (two
 // operations a clock and SM here) makes the logarithms and adds the scores, so that
 // candidates of different beams are ordered by what they are and not by a rounding
 // to fp32: an exponential is off by about 2^-22, an average over many by less.
@@ -649,8 +650,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) beam_kernel(const __grid_cons
       }
       float sum = 0.0f;
       if (c > -INFINITY) sum = far < INFINITY ? x.sum_from(far) : x.sum(c);
-      // above: a NaN, or logits far above the reference of the chunks before
-      if (!(sum <= 64.0f) || (c == -INFINITY && m > -INFINITY)) flags |= 2;
+      // above: a NaN, or logits above the reference of the chunks before
+      if (!(sum <= (float)X::M) || (c == -INFINITY && m > -INFINITY)) flags |= 2;
       // The size of the list is read between two barriers: a warp that is done with a
       // chunk which lists nothing (a NaN alone brought it here) may add to the next
       // one's while another still decides, and they would part ways.

@@ -34,3 +34,18 @@ def test_spread_over_chunks_and_parts(base, sign, dtype):
         # a row's parts far from one another and next to one another
         far = torch.randint(0, 4, (4 * G, 15), device="cuda").repeat_interleave(4000, 1)
         check((sign * base + x + 5e5 * far).to(dtype), st)
+
+
+@pytest.mark.parametrize("rows", [1, 2])
+def test_sums_of_the_largest_vocabulary(rows):
+    """2^23 logits, all but each part's first chunk two octaves above it."""
+    V, chunk = 1 << 23, 4096
+    room = 4 * torch.cuda.get_device_properties(0).multi_processor_count // rows
+    per_part = -(-(V // chunk) // room)
+    st = ssa.BeamState(1, rows)
+    st.scores.zero_()
+    for low in (-1.4, -0.7):
+        x = torch.zeros((rows, V // chunk, chunk), device="cuda")
+        x[:, ::per_part] = low
+        x = x.view(rows, V)
+        check(x, st)
