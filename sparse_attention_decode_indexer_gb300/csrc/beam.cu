@@ -105,7 +105,10 @@ __device__ __forceinline__ double unrank64(uint64_t b) {
   return __longlong_as_double((int64_t)(b ^ ((int64_t)b < 0 ? 1ull << 63 : ~0ull)));
 }
 // A logit and its token (or another index): the greater logit, then the lower index.
-__device__ __forceinline__ uint64_t key_of(float x, uint32_t t) { return (uint64_t)rank32(x) << 32 | (uint32_t)~t; }
+// (The sum makes both zeros one.)
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t t) {
+  return (uint64_t)rank32(x + 0.0f) << 32 | (uint32_t)~t;
+}
 __device__ __forceinline__ float key_x(uint64_t k) { return unrank32((uint32_t)(k >> 32)); }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
