@@ -31,7 +31,10 @@
 //   * Softmax in one pass against a lazy reference: the maximum that p is taken
 //     against moves only when a score exceeds it by 8 octaves; then the row's O
 //     is rescaled in tensor memory.  Sums and references are fp32; P in 16 bits
-//     is off by half a step of its type, as the inputs are.
+//     is off by half a step of its type, as the inputs are.  For fp16 the reference
+//     lies 7 octaves below the maximum (p up to 2^15 of 65,504): weights keep their
+//     bits down to 2^-21 of the greatest, where 2^-14 would cut the many small ones
+//     of a long context.
 //   * Masked scores give p = 0, and 0 times an infinite or NaN v would still
 //     be NaN.  Four spare warps look through the V of those blocks that some
 //     row does not see all of, and set what is not finite to zero; the epilogue
@@ -67,6 +70,7 @@ constexpr int kStages = 5;                // K and V blocks in flight
 constexpr int kHalf = kRows * 128;        // bytes of 64 of the 128 dimensions
 constexpr int kTile = 2 * kHalf;
 constexpr float kLazy = 8.0f;             // octaves
+template <typename T> constexpr float kBelow = std::is_same_v<T, __half> ? 7.0f : 0.0f;     // reference below the maximum
 
 struct Shared {                           // behind the tiles
   uint64_t full[kStages], empty[kStages], clean[kStages];
@@ -449,10 +453,10 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
           mx[e & 3] = max3(mx[e & 3], __uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1]));
       }
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-      const bool move = live && top > m + kLazy;
+      const bool move = live && top > m + (kLazy + kBelow<T>);
       if (__any_sync(~0u, move)) {
-        const float a = move ? fast_exp2(m - top) : 1.0f;
-        if (move) m = top;
+        const float to = top - kBelow<T>, a = move ? fast_exp2(m - to) : 1.0f;
+        if (move) m = to;
         l *= a;
         if (n > 0) {
           if (!all(o_done(n))) { ok = false; break; }
