@@ -647,8 +647,9 @@ int ssa_rope_frequencies(int rotary_dim, double base, int scaling, double factor
  * sequence are left as they were.  What a row does not see has no part in it,
  * infinities and NaN among it.
  *   dtype     SSA_BF16 or SSA_F16, of q, k, v and out; scores, softmax and sums
- *             in fp32, weights rounded to dtype before they meet v (fp16 weights
- *             lose bits below 2^-21 of a row's greatest, and those below 2^-32 go)
+ *             in fp32, weights rounded to dtype before they meet v and divided by
+ *             the sum of the rounded ones (fp16 weights lose bits below 2^-21 of a
+ *             row's greatest, and those below 2^-32 go)
  *   head_dim  128;  G at most 128
  *   q, out    [n_q][Hq][128];  k, v [n_kv][Hkv][128], 16-byte aligned; element
  *             strides of token and head, positive multiples of 8, so that

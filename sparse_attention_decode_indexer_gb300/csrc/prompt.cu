@@ -31,7 +31,10 @@
 //   * Softmax in one pass against a lazy reference: the maximum that p is taken
 //     against moves only when a score exceeds it by 8 octaves; then the row's O
 //     is rescaled in tensor memory.  Sums and references are fp32; P in 16 bits
-//     is off by half a step of its type, as the inputs are.  For fp16 the reference
+//     is off by half a step of its type, as the inputs are, and divided by the sum
+//     of the rounded weights: a row's error is sum_j w_j d_j (v_j - out), d_j the
+//     roundings, so that of a weight near one cancels.  (The logarithm is that of the
+//     sum before rounding.  The second sum costs packed prompts 2.5 %.)  For fp16 the reference
 //     lies 7 octaves below the maximum (p up to 2^15 of 65,504): weights keep their
 //     bits down to 2^-21 of the greatest, where 2^-14 would cut the many small ones
 //     of a long context.
@@ -93,7 +96,7 @@ struct Params {
   const void* v;
   void* out;
   float* lse;
-  float *part_o, *part_ml;                // [CTA][head][split][2 * kRows][kD], [..][2]
+  float *part_o, *part_ml;                // [CTA][head][split][2 * kRows][kD], [..][4]: reference, two sums
   int32_t* status;
 };
 
@@ -111,6 +114,15 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tm, uint64_t*
 template <typename T> __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   if constexpr (std::is_same_v<T, __half>) return pack_f16(lo, hi);
   else return pack_bf16(lo, hi);
+}
+// a and b and the two elements of a word.
+template <typename T> __device__ __forceinline__ void add16(uint32_t w, float& a, float& b) {
+  if constexpr (std::is_same_v<T, __half>)
+    asm("{\n.reg .b16 x, y;\nmov.b32 {x, y}, %2;\nadd.f32.f16 %0, x, %0;\nadd.f32.f16 %1, y, %1;\n}"
+        : "+f"(a), "+f"(b) : "r"(w));
+  else
+    asm("{\n.reg .b16 x, y;\nmov.b32 {x, y}, %2;\nadd.f32.bf16 %0, x, %0;\nadd.f32.bf16 %1, y, %1;\n}"
+        : "+f"(a), "+f"(b) : "r"(w));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -425,7 +437,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
     // phase short: the scores of half block n - 1 came behind the product n - 3,
     // which used the barrier of n - 1 before it.
     const auto o_done = [&](int n) { return mbar_wait(&sh.o_full[tile][(n - 1) & 1], ((n - 1) >> 1) & 1, abort); };
-    float m = -INFINITY, l = 0.0f;
+    float m = -INFINITY, l = 0.0f, z = 0.0f;              // reference, sum, sum of the rounded
     int n = 0;
     bool ok = true;
     const int first = 2 * (tile ? tb0[1] : tb0[0]), last = tile ? j1[1] : j1[0];
@@ -458,6 +470,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
         const float to = top - kBelow<T>, a = move ? fast_exp2(m - to) : 1.0f;
         if (move) m = to;
         l *= a;
+        z *= a;
         if (n > 0) {
           if (!all(o_done(n))) { ok = false; break; }
           tc5_fence_after();
@@ -475,6 +488,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
       const float ref = m == -INFINITY ? 0.0f : m;
       const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), ref2 = pack2(-ref, -ref);
       uint64_t sum[4] = {0, 0, 0, 0};
+      float rounded[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t w[16];
@@ -484,11 +498,13 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
           const float e0 = fast_exp2(t.x), e1 = fast_exp2(t.y);
           sum[e & 3] = add2(sum[e & 3], pack2(e0, e1));
           w[e] = pack16<T>(e0, e1);
+          add16<T>(w[e], rounded[2 * (e & 1)], rounded[2 * (e & 1) + 1]);
         }
         tmem_st16(Sj + 16 * c, w);        // over the scores
       }
       const float2 total = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
       l += total.x + total.y;
+      z += (rounded[0] + rounded[1]) + (rounded[2] + rounded[3]);
       tmem_wait_st();
       tc5_fence_before();
       __syncwarp();
@@ -501,12 +517,12 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
     if (ok) {
       tc5_fence_after();
       const bool seen = live && n > 0;
-      if (!live) { m = -INFINITY; l = 0.0f; }          // (a row without keys ran along)
+      if (!live) { m = -INFINITY; l = z = 0.0f; }      // (a row without keys ran along)
       const size_t row = (((size_t)place * p.Hkv + head) * p.n_split + split) * (2 * kRows) + threadIdx.x;
       const int hq = head * p.G + r % p.G;
       if (p.n_split > 1) {
         if (tile < p.tiles && r < p.tpt * p.G && tok < p.Tq)
-          *reinterpret_cast<float2*>(p.part_ml + 2 * row) = make_float2(m, in_seq ? l : -1.0f);
+          reinterpret_cast<float4*>(p.part_ml)[row] = make_float4(m, in_seq ? l : -1.0f, z, 0.0f);
       } else if (in_seq && p.lse) {
         p.lse[(size_t)tok * p.Hq + hq] = l != 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
       }
@@ -517,7 +533,7 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
       uint8_t* const mine = s_q + tile * kTile + (warp & 3) * 32 * 256;
       const int64_t at_row = p.n_split > 1 ? (int64_t)row * kD : tok * p.o_tok + hq * p.o_head;
       const uint32_t rows = __ballot_sync(~0u, in_seq);
-      const float f = p.n_split > 1 ? 1.0f : seen && l != 0.0f ? 1.0f / l : 0.0f;
+      const float f = p.n_split > 1 ? 1.0f : seen && z != 0.0f ? 1.0f / z : 0.0f;
       const auto write = [&](char* dst, int size) {
         __syncwarp();
         const int piece = lane & 15;
@@ -597,34 +613,34 @@ prompt_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __
   }
 }
 
-// out = sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - max m): `warps` warps a row, four
+// out = sum_s w_s O_s / sum_s w_s z_s, w_s = 2^(m_s - max m): `warps` warps a row, four
 // dimensions a lane, eight splits of a warp in flight (each read is a round trip to
 // L2: with one warp a row 76 splits took 25 us).  Always in the same order.
 template <typename T>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const Params p, int warps) {
   __shared__ float4 s_o[8][32];
-  __shared__ float s_m[8], s_l[8];
+  __shared__ float s_m[8], s_l[8], s_z[8];
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp & (warps - 1);
   const long long i = (long long)blockIdx.x * (8 / warps) + warp / warps;
   const int tok = (int)(i / p.Hq), hq = (int)(i % p.Hq);
   bool mine = tok < p.Tq;
-  float m = -INFINITY, l = 0.0f;
+  float m = -INFINITY, l = 0.0f, z = 0.0f;
   float4 o = make_float4(0, 0, 0, 0);
   if (mine) {
     const int head = hq / p.G, of_cta = p.tiles * p.tpt, in = tok % of_cta;
     const int r = in / p.tpt * kRows + in % p.tpt * p.G + hq % p.G;
     const size_t row0 = ((size_t)(tok / of_cta) * p.Hkv + head) * p.n_split * (2 * kRows) + r;
     for (int s0 = w; s0 < p.n_split; s0 += 8 * warps) {
-      float2 ml[8];
+      float4 ml[8];
       float4 y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const size_t row = row0 + (size_t)min(s0 + e * warps, p.n_split - 1) * 2 * kRows;
-        ml[e] = reinterpret_cast<const float2*>(p.part_ml)[row];
+        ml[e] = reinterpret_cast<const float4*>(p.part_ml)[row];
         y[e] = reinterpret_cast<const float4*>(p.part_o + row * kD)[lane];
-        if (s0 + e * warps >= p.n_split) ml[e] = make_float2(-INFINITY, 0.0f);
+        if (s0 + e * warps >= p.n_split) ml[e] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
       }
       if (ml[0].y < 0.0f) mine = false;   // not a token of any sequence: every split says so
       float top = m;
@@ -633,37 +649,41 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const Params p, int wa
       const float old = m == -INFINITY ? 0.0f : fast_exp2(m - top);
       m = top;
       l *= old;
+      z *= old;
       o.x *= old; o.y *= old; o.z *= old; o.w *= old;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         if (ml[e].y == 0.0f) continue;    // saw no key
         const float f = fast_exp2(ml[e].x - m);
         l += f * ml[e].y;
+        z += f * ml[e].z;
         o.x += f * y[e].x; o.y += f * y[e].y; o.z += f * y[e].z; o.w += f * y[e].w;
       }
     }
   }
   if (warps > 1) {
     s_o[warp][lane] = o;
-    if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
+    if (lane == 0) { s_m[warp] = m; s_l[warp] = l; s_z[warp] = z; }
     __syncthreads();
     if (w != 0) return;
     float top = m;
     for (int e = 1; e < warps; ++e) top = fmaxf(top, s_m[warp + e]);
     const float f0 = m == -INFINITY ? 0.0f : fast_exp2(m - top);
     l *= f0;
+    z *= f0;
     o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
     for (int e = 1; e < warps; ++e) {
       if (s_l[warp + e] == 0.0f) continue;
       const float f = fast_exp2(s_m[warp + e] - top);
       const float4 y = s_o[warp + e][lane];
       l += f * s_l[warp + e];
+      z += f * s_z[warp + e];
       o.x += f * y.x; o.y += f * y.y; o.z += f * y.z; o.w += f * y.w;
     }
     m = top;
   }
   if (!mine) return;
-  const float f = l != 0.0f ? 1.0f / l : 0.0f;
+  const float f = z != 0.0f ? 1.0f / z : 0.0f;
   T* dst = static_cast<T*>(p.out) + tok * p.o_tok + hq * p.o_head + 4 * lane;
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<T>(o.x * f, o.y * f), pack16<T>(o.z * f, o.w * f));
   if (p.lse && lane == 0)
@@ -725,7 +745,7 @@ size_t part_rows(int sms) { return (size_t)sms * 2 * kRows; }
 // Parts that the keys of a CTA's rows are split into, where CTAs would not fill the
 // machine.  How many keys a CTA walks over stands in the tables on the device; the
 // host goes by the average sequence, and by the keys of all the sequences that
-// share a CTA's tokens.  A CTA takes about 1 us for 80 keys (one tile: 140); a part more costs 520
+// share a CTA's tokens.  A CTA takes about 1 us for 80 keys (one tile: 140); a part more costs 528
 // bytes of every row written and read, 0.26 ns a row, and the second kernel 5 us.
 // (1,000 tokens, 16/2 heads: 18.8 us whole, 24.1 in two; 2,000 tokens, 8/1: 31.3 and
 // 30.8; 64 tokens behind 8,000, 16/2: 109 whole, 18.0 in 15, 18.9 in 19; one token each
@@ -757,7 +777,7 @@ int check_tensor(const ssa_prompt_tensor* x, int n) {
 extern "C" {
 
 size_t ssa_prompt_workspace_size(void) {
-  return ssa::part_rows(ssa::current_device_info().sms) * (ssa::kD + 2) * sizeof(float);
+  return ssa::part_rows(ssa::current_device_info().sms) * (ssa::kD + 4) * sizeof(float);
 }
 
 int ssa_prompt_attention(int dtype, int head_dim, int n_seqs, int n_q, int n_kv, const ssa_prompt_tensor* q,
