@@ -653,8 +653,9 @@ int ssa_rope_frequencies(int rotary_dim, double base, int scaling, double factor
  *   head_dim  128;  G at most 128
  *   q, out    [n_q][Hq][128];  k, v [n_kv][Hkv][128], 16-byte aligned; element
  *             strides of token and head, positive multiples of 8, so that
- *             slices of a fused projection need no copy.  out must not overlap
- *             the others.
+ *             slices of a fused projection need no copy.  No element of out is
+ *             another's or twice in out; where it lies between the rows of an
+ *             input, both have the same token stride (SSA_ERR_INVALID_ARG)
  *   cu_q, cu_kv  [n_seqs + 1] int32, device, ascending, within the tensors
  *             (SSA_ST_BAD_POS otherwise; nothing outside the tensors is read
  *             or written).  The same array where queries and keys are the same

@@ -768,7 +768,54 @@ int check_tensor(const ssa_prompt_tensor* x, int n) {
   const int size[2] = {n, x->heads};
   for (int i = 0; i < 2; ++i)
     if (size[i] > 1 && (x->stride[i] <= 0 || x->stride[i] % 8 || x->stride[i] >= 1ll << 38)) return SSA_ERR_INVALID_ARG;
+  // (no address space has more; what follows stays within 64 bits)
+  if (n > 0 && (double)(n - 1) * (n > 1 ? x->stride[0] : 0) + (double)(x->heads - 1) * (x->heads > 1 ? x->stride[1] : 0) > 0x1p56)
+    return SSA_ERR_INVALID_ARG;
   return SSA_OK;
+}
+
+// Rows of kD elements, n tokens by heads.
+struct Rows {
+  int64_t at;                             // the first's address in elements
+  int64_t n, heads, tok, head;            // counts and strides
+  int64_t end() const { return at + (n - 1) * tok + (heads - 1) * head + kD; }
+};
+Rows rows_of(const ssa_prompt_tensor& x, int n) {
+  return Rows{(int64_t)((uintptr_t)x.data / 2), n, x.heads, n > 1 ? x.stride[0] : 0, x.heads > 1 ? x.stride[1] : 0};
+}
+// Whether |c + k * step| < kD for some k in [k0, k1]: the one nearest to -c / step.
+bool meets(int64_t c, int64_t step, int64_t k0, int64_t k1) {
+  int64_t k = step ? -c / step : 0;
+  for (int64_t i = k - 1; i <= k + 1; ++i) {
+    const int64_t d = c + std::min(std::max(i, k0), k1) * step;
+    if (d > -kD && d < kD) return true;
+  }
+  return false;
+}
+// Whether a row of a and a row of b share an element.  Slices of one buffer lie between
+// each other's rows; token strides that differ there are taken for an overlap.
+bool overlap(const Rows& a, const Rows& b) {
+  if (a.at >= b.end() || b.at >= a.end()) return false;
+  if (a.n > 1 && b.n > 1 && a.tok != b.tok) return true;
+  const int64_t step = std::max(a.tok, b.tok);
+  const bool alike = a.head == b.head || a.heads == 1 || b.heads == 1;
+  const int64_t head = std::max(a.head, b.head);
+  for (int64_t h = 0; h < a.heads; ++h)
+    for (int64_t i = 0; i < b.heads; ++i) {
+      // heads alike: only their difference counts, -(b.heads - 1) .. a.heads - 1
+      if (alike && h > 0 && i > 0) break;
+      if (meets(a.at - b.at + (alike ? (h - i) * head : h * a.head - i * b.head), step, 1 - b.n, a.n - 1)) return true;
+    }
+  return false;
+}
+// Whether two rows of x share an element.
+bool overlaps_itself(const Rows& x) {
+  if (x.heads > 1 && x.head < kD) return true;
+  if (x.n == 1) return false;
+  if (x.tok >= (x.heads - 1) * x.head + kD) return false;
+  for (int64_t h = 0; h < x.heads; ++h)   // another token's, h heads on
+    if (meets(h * x.head, x.tok, 1 - x.n, -1)) return true;
+  return false;
 }
 
 }  // namespace
@@ -795,8 +842,11 @@ int ssa_prompt_attention(int dtype, int head_dim, int n_seqs, int n_q, int n_kv,
   if (q->heads % k->heads || q->heads / k->heads > kRows) return SSA_ERR_UNSUPPORTED;
   if ((uintptr_t)ws & 15) return SSA_ERR_INVALID_ARG;
   // (a tile's result may come before another's reads)
-  if (n_q > 0 && (out->data == q->data || (n_kv > 0 && (out->data == k->data || out->data == v->data))))
-    return SSA_ERR_INVALID_ARG;
+  if (n_q > 0) {
+    const Rows o = rows_of(*out, n_q);
+    if (overlaps_itself(o) || overlap(o, rows_of(*q, n_q))) return SSA_ERR_INVALID_ARG;
+    if (n_kv > 0 && (overlap(o, rows_of(*k, n_kv)) || overlap(o, rows_of(*v, n_kv)))) return SSA_ERR_INVALID_ARG;
+  }
   if (n_q > INT_MAX / 2 || n_kv > INT_MAX / 2) return SSA_ERR_UNSUPPORTED;
   if (n_q == 0 || n_seqs == 0) return SSA_OK;
 
