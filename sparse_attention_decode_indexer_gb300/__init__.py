@@ -772,8 +772,8 @@ def ssa_prompt_attention(q, k, v, cu_q, out, status, ws, cu_k=None, causal: bool
     has the query tokens cu_q[s] .. cu_q[s + 1] and the keys cu_k[s] ..
     cu_k[s + 1] (default: cu_q), int32 on the device; with ``causal`` its query
     tokens are the last ones of its keys.  sm_scale: default 1 / sqrt(D).  lse:
-    fp32 [Tq][Hq], the logarithm of each row's sum.  ws: at least
-    ssa_prompt_workspace_size() bytes."""
+    fp32 [Tq][Hq], the logarithm of each row's sum.  status: one int32, or None.
+    ws: at least ssa_prompt_workspace_size() contiguous bytes."""
     # (a small call's time is this function's: each property is read once)
     dt, dev, size, sk = q.dtype, q.get_device(), q.shape, k.shape
     dtype = _PROMPT_DTYPES.get(dt)
@@ -799,9 +799,11 @@ def ssa_prompt_attention(q, k, v, cu_q, out, status, ws, cu_k=None, causal: bool
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != size[:2] or
                             not lse.is_contiguous() or lse.get_device() != dev):
         raise ValueError(f"lse: contiguous float32 [{n_q}][{heads}] on q's device")
+    ps = None if status is None else _ints("status", status, 1, dev)
     L = lib()
-    if ws.get_device() != dev or ws.nbytes < L.ssa_prompt_workspace_size():
-        raise ValueError("ws: ssa_prompt_workspace_size() bytes on q's device")
+    if ws.get_device() != dev or not ws.is_contiguous() or \
+            ws.nbytes < L.ssa_prompt_workspace_size():
+        raise ValueError("ws: ssa_prompt_workspace_size() contiguous bytes on q's device")
     _on_current_device(dev)
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(D)
@@ -809,7 +811,7 @@ def ssa_prompt_attention(q, k, v, cu_q, out, status, ws, cu_k=None, causal: bool
         dtype, D, n - 1, n_q, n_k, _pack_prompt(q.data_ptr(), heads, q0, q1),
         _pack_prompt(k.data_ptr(), heads_k, k0, k1), _pack_prompt(v.data_ptr(), heads_k, v0, v1),
         _pack_prompt(out.data_ptr(), heads, o0, o1), pq, pk, causal, sm_scale, _ptr(lse),
-        _ptr(status), ws.data_ptr(), _stream(stream)))
+        ps, ws.data_ptr(), _stream(stream)))
 
 
 # ---------------------------------------------------------------------------
