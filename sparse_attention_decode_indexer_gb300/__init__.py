@@ -716,6 +716,12 @@ class HeadNorm:
         self._ptr = [0 if w is None else w.data_ptr() for w in ws]
         self._dev = next((w.get_device() for w in ws if w is not None), None)
 
+    def __setattr__(self, name, value):
+        # calls go by the addresses of the weights made above
+        if name in ("q_weight", "k_weight") and "_ptr" in self.__dict__:
+            raise AttributeError(f"{name}: change the tensor in place (copy_, fill_)")
+        object.__setattr__(self, name, value)
+
 
 def ssa_norm_rope(plan: RopePlan, norm: HeadNorm, positions, q=None, k=None, q_out=None,
                   k_out=None, offset: int = 0, layer0: int = 0, stream=None):
