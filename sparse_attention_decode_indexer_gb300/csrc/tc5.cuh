@@ -73,12 +73,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t* x, uint32_t addr) {
                "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
                : SSA_R8(x, 0), SSA_R8(x, 8), SSA_R8(x, 16), SSA_R8(x, 24) : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* x) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-               "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
-               ::SSA_W8(x, 0), SSA_W8(x, 8), SSA_W8(x, 16), SSA_W8(x, 24), "r"(addr) : "memory");
-}
 // Waits for the loads so far; x, loaded by the last of them, has its values only now.
 #define SSA_RW8(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3]), "+r"(x[i + 4]), \
                       "+r"(x[i + 5]), "+r"(x[i + 6]), "+r"(x[i + 7])
