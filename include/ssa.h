@@ -689,7 +689,8 @@ int ssa_prompt_attention(int dtype, int head_dim, int n_seqs, int n_q, int n_kv,
  *   row whose score is -infinity or NaN; logits above 2^126 count as 2^126
  * The `beams` best of each group, best first, equal scores by the lower row and
  * then the lower token, become the group's rows; the best of several rows may
- * be of one parent.  Sums and scores in double, one rounding to fp32 at the end.
+ * be of one parent.  Sums in 64-bit integers (each exponential is off by about
+ * 2^-22 of itself), scores in double, one rounding to fp32 at the end.
  *   dtype     SSA_BF16, SSA_F16 or SSA_F32, of the logits
  *   logits    [groups * beams] rows, row_stride elements apart
  *   groups at most 65,535, beams at most 32, vocab at most 2^23 (SSA_ERR_UNSUPPORTED)
@@ -708,7 +709,8 @@ int ssa_prompt_attention(int dtype, int head_dim, int n_seqs, int n_q, int n_kv,
  *   token     [groups * beams] int32 out
  *   seq_lens_opt, new_lens_opt  [groups * beams] int32, both or none:
  *             new_lens[row] = seq_lens[parent] + 1, 0 for parent -1, as
- *             ssa_fork_requests takes them (may be the same array)
+ *             ssa_fork_requests takes them (may be the same array).  That of a
+ *             beam that has ended grows too, a token a call, as its history does
  *   ws        ssa_beam_workspace_size(groups, beams) bytes or more, 256-byte
  *             aligned, zeroed once, not used by another call at the same time;
  *             calls of any sizes that it is large enough for may take turns

@@ -36,7 +36,8 @@
 // 64 x 1 of 131,072: 13 us; 1 x 4 of 32,000: 10.7 us, of which the last CTA's choice
 // is 5 (64 us for the first of these before loads went out together and double
 // comparisons became integers, 231 at first).  Chunks of 64 bytes a thread: two more
-// in flight through shared memory measured the same (39).
+// in flight through shared memory measured the same (39).  64 registers allow four
+// CTAs; the 16-bit kernels spill 32 bytes for it.
 // Beyond 2^20 (masks of some large number) c, an fp32 product, would no longer be
 // the logit it stands for: there sums are taken against the logit itself.
 #include <algorithm>

@@ -34,7 +34,8 @@
 //     is off by half a step of its type, as the inputs are, and divided by the sum
 //     of the rounded weights: a row's error is sum_j w_j d_j (v_j - out), d_j the
 //     roundings, so that of a weight near one cancels.  (The logarithm is that of the
-//     sum before rounding.  The second sum costs packed prompts 2.5 %.)  For fp16 the reference
+//     sum before rounding.  The second sum costs packed prompts 3 %, prompts of some
+//     hundred tokens 3 to 6 %, 24,576 tokens 1 %.)  For fp16 the reference
 //     lies 7 octaves below the maximum (p up to 2^15 of 65,504): weights keep their
 //     bits down to 2^-21 of the greatest, where 2^-14 would cut the many small ones
 //     of a long context.
@@ -44,10 +45,10 @@
 //     then adds it for the rows that do see it, which read these blocks again.
 //   * Few rows and many keys: the key blocks of a tile are split over several
 //     CTAs; their unnormalised outputs are joined by a second kernel.
-// Measured: 24,576 tokens x 16/2 heads causal 1.63 to 1.73 ms (1,430 to 1,520
+// Measured: 24,576 tokens x 16/2 heads causal 1.70 to 1.83 ms (1,350 to 1,455
 // TFLOP/s, by how far the power limit lets the clock); 24 prompts of 69 to 3,712
-// tokens, 32/4 heads, 368 us (924: a third of a CTA's time is its start and its end);
-// 8 tokens behind 65,528 25 us (2.7 TB/s), 17 tokens 6.3 us.
+// tokens, 32/4 heads, 384 us (885: a third of a CTA's time is its start and its end);
+// 8 tokens behind 65,528 24 us (2.8 TB/s), 17 tokens 6.3 us.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -751,7 +752,7 @@ size_t part_rows(int sms) { return (size_t)sms * 2 * kRows; }
 // host goes by the average sequence, and by the keys of all the sequences that
 // share a CTA's tokens.  A CTA takes about 1 us for 80 keys (one tile: 140); a part more costs 528
 // bytes of every row written and read, 0.26 ns a row, and the second kernel 5 us.
-// (1,000 tokens, 16/2 heads: 18.8 us whole, 24.1 in two; 2,000 tokens, 8/1: 31.3 and
+// (Before the second sum: 1,000 tokens, 16/2 heads: 18.8 us whole, 24.1 in two; 2,000 tokens, 8/1: 31.3 and
 // 30.8; 64 tokens behind 8,000, 16/2: 109 whole, 18.0 in 15, 18.9 in 19; one token each
 // of 8 sequences of 4,000: 370 whole, 19.6 in 62; one behind 30,000: 13.9 in 58,
 // 16.9 in 152, so four blocks at least to a part.)
@@ -861,7 +862,7 @@ int ssa_prompt_attention(int dtype, int head_dim, int n_seqs, int n_q, int n_kv,
   p.tpt = kRows / p.G;
   // two tiles a CTA share its K and V; where one tile each fits the machine at once
   // the CTAs are twice as many and each is done sooner (2,000 tokens x 8/1 heads:
-  // two tiles 31.5 us, one 25.5)
+  // two tiles 31.5 us, one 25.5 before the second sum and 27.4 with it)
   const int sms = current_device_info().sms, n_tiles = (n_q + p.tpt - 1) / p.tpt;
   p.tiles = (long long)n_tiles * p.Hkv <= sms ? 1 : 2;
   p.n_ctas = (n_tiles + p.tiles - 1) / p.tiles;

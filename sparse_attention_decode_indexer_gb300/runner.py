@@ -173,8 +173,10 @@ class DecodeRunner:
         tokens cu_seqlens[i] .. cu_seqlens[i + 1] (int32 on the device); pos
         and positions [T] as for ``store`` (so the prompts come in the order of
         their pages).  Norms and positions, attention of the prompts over
-        themselves, store; returns the attention [T][Hq][D].  (8-bit caches: the
-        prompts attend over K and V as they come, the cache holds them rounded.)"""
+        themselves, store; returns the attention [T][Hq][D], in which rows of no
+        prompt (padding behind the last) hold nothing in particular.  (8-bit
+        caches: the prompts attend over K and V as they come, the cache holds them
+        rounded.)"""
         if self.rope is not None:
             if positions is None:
                 raise ValueError("prefill with rope: positions of the tokens")
@@ -205,7 +207,8 @@ class DecodeRunner:
         """The next tokens of beams: logits [batch][V], the runner's rows in groups
         of state.beams.  The best of each group become its rows: state in place,
         and the rows of the table continue the pages of their parents, a token
-        longer (``fork``).  Returns parent and token, int32 [batch], buffers of
+        longer (``fork``); those of ended beams too, so a group whose beams have
+        all ended is best freed.  Returns parent and token, int32 [batch], buffers of
         the runner's own that the next call overwrites."""
         B = self.layout.batch
         if state.groups * state.beams != B:
